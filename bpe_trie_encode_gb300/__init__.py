@@ -13,6 +13,14 @@ PyTorch is used only for device memory and streams.
     ids, id_off = ctx.encode(trie, data_u8_cuda, doc_off_i64_cuda)
     uni = ctx.unigram(trie, scores_f64, unk_id, unk_score)       # Viterbi model
     ids, id_off = ctx.unigram_encode(uni, data_u8_cuda, doc_off_i64_cuda)
+
+The output head of a model over the same vocabulary (``examples/generate.py``):
+
+    w8, ws = ctx.head_quantize(weight)                           # once
+    x8, xs, stream = ctx.head_norm(hidden, norm_weight, residual)
+    logits = ctx.head_logits(x8, xs, w8, ws)
+    ids, logprob = ctx.head_sample(logits, u, temperature=0.8, top_p=0.95)
+    text = ctx.decode(merges, ids)
 """
 from __future__ import annotations
 
@@ -43,6 +51,52 @@ def _need_cuda(t: torch.Tensor, dtype: torch.dtype, name: str, device: torch.dev
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     return t.contiguous()
+
+
+_HEAD_TYPES = {torch.float32: _capi.BPE_F32, torch.bfloat16: _capi.BPE_BF16, torch.float16: _capi.BPE_F16}
+_E4M3 = torch.float8_e4m3fn
+
+
+def _head_matrix(t: torch.Tensor, name: str, device: torch.device, dtypes, shape=None, out: bool = False) -> torch.Tensor:
+    """A CUDA matrix whose rows are contiguous (an input is copied where they are not)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the context is on {device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be {'a matrix' if shape is None else tuple(shape)}, got {tuple(t.shape)}")
+    rows, cols = t.shape
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        if out:
+            raise ValueError(f"{name}: the rows of an output must be contiguous and apart")
+        t = t.contiguous()
+    return t
+
+
+def _head_scales(t: torch.Tensor, name: str, device: torch.device, rows: int, blocks: int, out: bool = False) -> None:
+    """Scales may lie in any order; those of an output may not share a place."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32:
+        raise TypeError(f"{name} must be a float32 CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the context is on {device}")
+    if t.shape != (rows, blocks):
+        raise ValueError(f"{name} must be {(rows, blocks)}, got {tuple(t.shape)}")
+    if out:
+        (s0, n0), (s1, n1) = sorted(((t.stride(0), rows), (t.stride(1), blocks)))
+        if (n0 > 1 and s0 == 0) or (n1 > 1 and s1 < (n0 - 1) * s0 + 1):
+            raise ValueError(f"{name}: the scales of an output must lie apart")
+
+
+def _head_vector(t: torch.Tensor, name: str, device: torch.device, dtype: torch.dtype, rows: int,
+                 out: bool = False) -> torch.Tensor:
+    if out and isinstance(t, torch.Tensor) and not t.is_contiguous():
+        raise ValueError(f"{name}: an output must be contiguous")
+    t = _need_cuda(t, dtype, name, device)
+    if t.shape != (rows,):
+        raise ValueError(f"{name} must be ({rows},), got {tuple(t.shape)}")
+    return t
 
 
 class Trie:
@@ -246,6 +300,141 @@ class Context:
             raise BpeError(rc, f"{n_ids.value} ids needed, capacity {cap}")
         _capi.check(self._h, rc)
         return ids_out[: n_ids.value], id_off[: n_docs + 1]
+
+    # -- the output head ------------------------------------------------------
+    def head_norm(self, x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                  eps: float = 1e-6, out: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                  residual_out: torch.Tensor | None = None):
+        """Root-mean-square norm of x + residual, in 8 bits with one scale per
+        128 columns.  x, residual: [rows, dim] f32, bf16 or f16; weight: [dim]
+        of any of the three.  Returns (x8 float8_e4m3fn [rows, dim], scales f32
+        [rows, ceil(dim / 128)], the sum in x's type [rows, dim] or None).  The
+        sum is written when a residual is given or residual_out is; it may be x
+        or the residual itself.  Asynchronous on the current stream."""
+        dev = self.device
+        x = _head_matrix(x, "x", dev, _HEAD_TYPES)
+        rows, dim = x.shape
+        if not isinstance(weight, torch.Tensor) or weight.dtype not in _HEAD_TYPES:
+            raise TypeError("weight must be a float32, bfloat16 or float16 tensor")
+        weight = _need_cuda(weight, weight.dtype, "weight", dev)
+        if weight.shape != (dim,):
+            raise ValueError(f"weight must be ({dim},), got {tuple(weight.shape)}")
+        if residual is not None:
+            residual = _head_matrix(residual, "residual", dev, (x.dtype,), x.shape)
+            if residual_out is None:
+                residual_out = torch.empty(rows, dim, dtype=x.dtype, device=dev)
+        if residual_out is not None:
+            residual_out = _head_matrix(residual_out, "residual_out", dev, (x.dtype,), x.shape, out=True)
+        if out is None:   # rows start on 16 bytes, which the product reads without a copy
+            out = torch.empty(rows, -(-dim // 16) * 16, dtype=_E4M3, device=dev)[:, :dim]
+        else:
+            out = _head_matrix(out, "out", dev, (_E4M3,), x.shape, out=True)
+        blocks = -(-dim // _capi.BPE_HEAD_BLOCK)
+        if scales is None:
+            scales = torch.empty(blocks, rows, dtype=torch.float32, device=dev).t()
+        else:
+            _head_scales(scales, "scales", dev, rows, blocks, out=True)
+        self._sync_stream()
+        rc = self.lib.head_norm(self._h, x.data_ptr(), x.stride(0), _HEAD_TYPES[x.dtype], weight.data_ptr(),
+                                _HEAD_TYPES[weight.dtype], residual.data_ptr() if residual is not None else None,
+                                residual.stride(0) if residual is not None else 0, rows, dim, eps,
+                                residual_out.data_ptr() if residual_out is not None else None,
+                                residual_out.stride(0) if residual_out is not None else 0, out.data_ptr(),
+                                out.stride(0), scales.data_ptr(), scales.stride(0), scales.stride(1))
+        if rc:
+            _capi.check(self._h, rc)
+        return out, scales, residual_out
+
+    def head_quantize(self, weight: torch.Tensor):
+        """A weight matrix [n_tok, dim] (f32, bf16 or f16) in 8 bits with one
+        scale per 128 x 128 block: (w8 float8_e4m3fn [n_tok, dim], its rows
+        starting on 16 bytes, ws f32 [ceil(n_tok / 128), ceil(dim / 128)])."""
+        weight = _head_matrix(weight, "weight", self.device, _HEAD_TYPES)
+        n_tok, dim = weight.shape
+        w8 = torch.empty(n_tok, -(-dim // 16) * 16, dtype=_E4M3, device=self.device)[:, :dim]
+        ws = torch.empty(-(-n_tok // _capi.BPE_HEAD_BLOCK), -(-dim // _capi.BPE_HEAD_BLOCK), dtype=torch.float32,
+                         device=self.device)
+        self._sync_stream()
+        _capi.check(self._h, self.lib.head_quantize(self._h, weight.data_ptr(), weight.stride(0),
+                                                    _HEAD_TYPES[weight.dtype], n_tok, dim, w8.data_ptr(),
+                                                    w8.stride(0), ws.data_ptr(), ws.stride(0)))
+        return w8, ws
+
+    def head_logits(self, x8: torch.Tensor, xs: torch.Tensor, w8: torch.Tensor, ws: torch.Tensor,
+                    out: torch.Tensor | None = None, dtype: torch.dtype = torch.float32) -> torch.Tensor:
+        """Logits [rows, n_tok] of 8-bit hidden states x8 [rows, dim] (scales
+        xs [rows, ceil(dim / 128)]) and weights w8 [n_tok, dim] (scales ws
+        [ceil(n_tok / 128), ceil(dim / 128)]), accumulated in 32 bits and
+        rounded once to ``dtype`` (f32, bf16 or f16; ``out``'s when it is
+        given).  Scales may have any strides.  Asynchronous on the current
+        stream."""
+        dev = self.device
+        x8 = _head_matrix(x8, "x8", dev, (_E4M3,))
+        w8 = _head_matrix(w8, "w8", dev, (_E4M3,))
+        rows, dim = x8.shape
+        n_tok = w8.shape[0]
+        if w8.shape[1] != dim:
+            raise ValueError(f"w8 has {w8.shape[1]} columns, x8 {dim}")
+        blocks = -(-dim // _capi.BPE_HEAD_BLOCK)
+        _head_scales(xs, "xs", dev, rows, blocks)
+        _head_scales(ws, "ws", dev, -(-n_tok // _capi.BPE_HEAD_BLOCK), blocks)
+        if out is None:
+            if dtype not in _HEAD_TYPES:
+                raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+            out = torch.empty(rows, n_tok, dtype=dtype, device=dev)
+        else:
+            out = _head_matrix(out, "out", dev, _HEAD_TYPES, (rows, n_tok), out=True)
+        self._sync_stream()
+        rc = self.lib.head_logits(self._h, x8.data_ptr(), x8.stride(0), xs.data_ptr(), xs.stride(0), xs.stride(1),
+                                  w8.data_ptr(), w8.stride(0), ws.data_ptr(), ws.stride(0), ws.stride(1), rows, n_tok,
+                                  dim, out.data_ptr(), out.stride(0), _HEAD_TYPES[out.dtype])
+        if rc:
+            _capi.check(self._h, rc)
+        return out
+
+    def head_sample(self, logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=None, top_p=None, min_p=None,
+                    ids: torch.Tensor | None = None, logprob: torch.Tensor | None = None):
+        """One id per row of logits [rows, n_tok] (f32, bf16 or f16), drawn by
+        the random numbers u [rows] (f32 in [0, 1)).  temperature, top_p and
+        min_p are numbers or f32 [rows] tensors, top_k a number or an int32
+        [rows] tensor (None: off; temperature 0: the largest logit).  Returns
+        (ids int32 [rows], logprob f32 [rows], the id's log-probability under
+        the filtered distribution); a row without a logit above -infinity
+        gives -1 and -infinity.  Asynchronous on the current stream."""
+        dev = self.device
+        logits = _head_matrix(logits, "logits", dev, _HEAD_TYPES)
+        rows, n_tok = logits.shape
+        u = _head_vector(u, "u", dev, torch.float32, rows)
+        if ids is None:
+            ids = torch.empty(rows, dtype=torch.int32, device=dev)
+        else:
+            ids = _head_vector(ids, "ids", dev, torch.int32, rows, out=True)
+        if logprob is None:
+            logprob = torch.empty(rows, dtype=torch.float32, device=dev)
+        else:
+            logprob = _head_vector(logprob, "logprob", dev, torch.float32, rows, out=True)
+        keep = []   # vectors that had to be copied live until the kernel is queued
+
+        def one(v, name, dtype, off):
+            if v is None:
+                return off, None
+            if not isinstance(v, torch.Tensor):
+                return v, None
+            v = _head_vector(v, name, dev, dtype, rows)
+            keep.append(v)
+            return off, v.data_ptr()
+
+        t, d_t = one(temperature, "temperature", torch.float32, 1.0)
+        k, d_k = one(top_k, "top_k", torch.int32, 0)
+        p, d_p = one(top_p, "top_p", torch.float32, 1.0)
+        q, d_q = one(min_p, "min_p", torch.float32, 0.0)
+        filters = _capi.head_filters(t, k, p, q, d_t, d_k, d_p, d_q)
+        self._sync_stream()
+        rc = self.lib.head_sample(self._h, logits.data_ptr(), logits.stride(0), _HEAD_TYPES[logits.dtype], rows, n_tok,
+                                  u.data_ptr(), ctypes.byref(filters), ids.data_ptr(), logprob.data_ptr())
+        if rc:
+            _capi.check(self._h, rc)
+        return ids, logprob
 
 
 class Unigram:

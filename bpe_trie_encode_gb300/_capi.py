@@ -25,6 +25,8 @@ BPE_OPT_MERGE, BPE_OPT_PERSISTENT, BPE_OPT_TRIE_LAYOUT, BPE_OPT_UNI_CHUNK = 6, 7
 BPE_OPT_TEST_STALL_TILE, BPE_OPT_SPARSE_MERGE, BPE_OPT_LIST_FRONTIER, BPE_OPT_LIST_TAIL = 10, 11, 12, 13
 BPE_TRIE_DOUBLE_ARRAY, BPE_TRIE_BITMAP = 0, 1
 BPE_MERGE_TWO_PASS, BPE_MERGE_LOOKBACK, BPE_MERGE_TILES, BPE_MERGE_LISTS = 0, 1, 2, 3
+BPE_F32, BPE_BF16, BPE_F16 = 0, 1, 2
+BPE_HEAD_BLOCK, BPE_HEAD_MAX_DIM, BPE_HEAD_MAX_TOKENS = 128, 32768, 1 << 22
 
 # every symbol the header declares (checked by the tests)
 EXPORTS = [
@@ -34,6 +36,7 @@ EXPORTS = [
     "trie_encode_noalloc", "trie_stream_open", "trie_stream_push", "trie_stream_close",
     "trie_encode_host", "unigram_create", "unigram_encode", "unigram_free",
     "bpe_vocab_from_merges", "bpe_decode",
+    "head_norm", "head_quantize", "head_logits", "head_sample",
 ]
 
 
@@ -56,6 +59,12 @@ class bpe_kernel_stat(ctypes.Structure):
 
 class bpe_stats(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int), ("kernel_launches", ctypes.c_uint64), ("k", bpe_kernel_stat * 8)]
+
+
+class head_filters(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_float), ("top_k", ctypes.c_int32), ("top_p", ctypes.c_float),
+                ("min_p", ctypes.c_float), ("d_temperature", ctypes.c_void_p), ("d_top_k", ctypes.c_void_p),
+                ("d_top_p", ctypes.c_void_p), ("d_min_p", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -98,6 +107,11 @@ def load() -> ctypes.CDLL:
             "unigram_free": (None, [vp]),
             "bpe_vocab_from_merges": (i32, [vp, u32, vp, u64, vp, P(u64)]),
             "bpe_decode": (i32, [vp, vp, u32, vp, u64, vp, u64, P(u64)]),
+            "head_norm": (i32, [vp, vp, u64, i32, vp, i32, vp, u64, u32, u32, ctypes.c_float, vp, u64, vp, u64,
+                                vp, u64, u64]),
+            "head_quantize": (i32, [vp, vp, u64, i32, u32, u32, vp, u64, vp, u64]),
+            "head_logits": (i32, [vp, vp, u64, vp, u64, u64, vp, u64, vp, u64, u64, u32, u32, u32, vp, u64, i32]),
+            "head_sample": (i32, [vp, vp, u64, i32, u32, u32, vp, P(head_filters), vp, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)

@@ -1,6 +1,7 @@
 /*
- * bpetrie.h -- byte-level BPE training, greedy trie encoding and Unigram
- * (Viterbi) encoding on one GPU.
+ * bpetrie.h -- byte-level BPE training, greedy trie encoding, Unigram
+ * (Viterbi) encoding, and the 8-bit output head that draws token ids, on one
+ * GPU.
  *
  * C ABI of libbpetrie.so (sm_103a).  Plain pointers and sizes only.
  *
@@ -14,7 +15,8 @@
  *     library owns the context, its scratch pool and tries.
  *   - Work is ordered on the context's stream.  A call returns only after its
  *     work is complete when it returns a host-side result (n_done, n_ids...);
- *     bpe_pretokenize returns as soon as its kernel is queued.
+ *     bpe_pretokenize and the head_ calls return as soon as their kernels are
+ *     queued.
  *   - Return value: BPE_OK (0) or a negative BPE_ERR_* code; the message of
  *     the last failure is available from bpe_last_error().  On failure no
  *     output beyond what the code describes is meaningful.
@@ -403,6 +405,99 @@ int unigram_encode(bpe_ctx *ctx, const bpe_unigram *model, const uint8_t *d_byte
                    uint32_t n_docs, int32_t *d_ids_out, uint64_t ids_capacity, uint64_t *d_id_off_out,
                    uint64_t *n_ids);
 void unigram_free(bpe_unigram *model);
+
+/* ----------------------------------------------------- output head ------ */
+
+/* The last step of a language model over a vocabulary of this library: from
+ * the hidden state of each position (a row) to the id that follows it.
+ * head_norm -> head_logits -> head_sample, then bpe_decode for the bytes.
+ * The pages have no counterpart.  All four calls are asynchronous on the
+ * context's stream; strides count elements; n_rows == 0 is a no-op. */
+enum { BPE_F32 = 0, BPE_BF16 = 1, BPE_F16 = 2 };
+#define BPE_HEAD_BLOCK 128u            /* columns (and vocabulary rows) that share a scale */
+#define BPE_HEAD_MAX_DIM 32768u
+#define BPE_HEAD_MAX_TOKENS (1u << 22)
+
+/* Root-mean-square norm of x + residual, in 8 bits.  Per row, in 32 bits:
+ *   s = x + residual (s = x when d_residual is NULL)
+ *   y = s * rsqrt(mean(s^2) + eps) * weight
+ *   per block b of 128 columns: scale[b] = max(max|y| / 448, 2^-126) and
+ *   y8 = e4m3(y * (1 / scale[b])), rounded to nearest even.
+ * A block that holds an infinity or a NaN gets that as its scale, so its
+ * values stand for NaN.
+ *
+ * d_x, d_residual, d_residual_out: n_rows x dim of `type`, rows `*_stride`
+ * elements apart.  d_residual_out (nullable) receives s rounded to `type`; it
+ * may be d_x or d_residual itself, with the same stride.  d_weight: dim of
+ * `weight_type`.  d_y8: n_rows x dim e4m3 bytes, rows y8_stride apart
+ * (head_logits reads rows that start on 16 bytes fastest).  d_scales:
+ * scale[row, b] at row * scale_row_stride + b * scale_block_stride.
+ * 1 <= dim <= BPE_HEAD_MAX_DIM.  Errors: INVALID_ARG, CUDA. */
+int head_norm(bpe_ctx *ctx, const void *d_x, uint64_t x_stride, int type, const void *d_weight, int weight_type,
+              const void *d_residual, uint64_t residual_stride, uint32_t n_rows, uint32_t dim, float eps,
+              void *d_residual_out, uint64_t residual_out_stride, uint8_t *d_y8, uint64_t y8_stride,
+              float *d_scales, uint64_t scale_row_stride, uint64_t scale_block_stride);
+
+/* A weight matrix in 8 bits, once, for head_logits: per block of 128 rows and
+ * 128 columns scale = max(max|w| / 448, 2^-126), w8 = e4m3(w * (1 / scale)).
+ * d_w: n_tok x dim of `type`, rows w_stride apart; d_w8: n_tok x dim, rows
+ * w8_stride apart; d_ws: ceil(n_tok/128) x ceil(dim/128), rows ws_stride
+ * apart.  Infinities and NaN as in head_norm.  Errors: INVALID_ARG, CUDA. */
+int head_quantize(bpe_ctx *ctx, const void *d_w, uint64_t w_stride, int type, uint32_t n_tok, uint32_t dim,
+                  uint8_t *d_w8, uint64_t w8_stride, float *d_ws, uint64_t ws_stride);
+
+/* Logits: out[r, t] = sum over blocks b of xs[r, b] * ws[t / 128, b] *
+ * (sum over the block's columns of x8[r, k] * w8[t, k]), accumulated in 32
+ * bits and rounded once to out_type.
+ *
+ * d_x8: n_rows x dim e4m3, rows x8_stride apart; d_xs: scale of row r, block
+ * b at r * xs_row_stride + b * xs_block_stride.  d_w8: n_tok x dim e4m3, rows
+ * w8_stride apart; d_ws: block (t, b) at t * ws_row_stride + b *
+ * ws_block_stride.  d_out: n_rows x n_tok of out_type, rows out_stride apart.
+ * Matrices whose rows do not all start on 16 bytes are first copied to the
+ * context's scratch.  1 <= dim <= BPE_HEAD_MAX_DIM, 1 <= n_tok <=
+ * BPE_HEAD_MAX_TOKENS.  Errors: INVALID_ARG, OOM, TIMEOUT, CUDA. */
+int head_logits(bpe_ctx *ctx, const uint8_t *d_x8, uint64_t x8_stride, const float *d_xs, uint64_t xs_row_stride,
+                uint64_t xs_block_stride, const uint8_t *d_w8, uint64_t w8_stride, const float *d_ws,
+                uint64_t ws_row_stride, uint64_t ws_block_stride, uint32_t n_rows, uint32_t n_tok, uint32_t dim,
+                void *d_out, uint64_t out_stride, int out_type);
+
+/* How head_sample filters and scales; each d_ pointer (nullable, n_rows
+ * values on the device) replaces the single value before it. */
+typedef struct {
+    float temperature;             /* below 2^-126 (0, negative, NaN): the largest logit is taken */
+    int32_t top_k;                 /* < 1: off */
+    float top_p;                   /* >= 1 or NaN: off */
+    float min_p;                   /* <= 0 or NaN: off; above 1 counts as 1 */
+    const float *d_temperature;
+    const int32_t *d_top_k;
+    const float *d_top_p;
+    const float *d_min_p;
+} head_filters;
+
+/* One id per row, drawn from its logits by a given random number.  A NaN
+ * counts as -infinity.  With m the row's largest logit, z = (logit - m) *
+ * (1 / temperature) in 32 bits (0 where logit == m) and the whole numbers w =
+ * floor(exp(z) * 2^40), so that every sum is exact and no result depends on
+ * an order of addition:
+ *   - tokens are ordered by logit, largest first, equal ones by lowest id;
+ *   - top-k keeps the first top_k of them, W_k being their mass (sum of w);
+ *   - top-p keeps those of the rest before which less mass than floor(top_p *
+ *     W_k) lies, and always the first;
+ *   - min-p keeps those of the rest with w >= floor(min_p * 2^40);
+ *   - with W the mass kept, the id drawn is the lowest whose running mass, in
+ *     order of ids, exceeds min(floor(u * W), W - 1) (products of u, top_p
+ *     and a mass in f64).
+ * The log-probability of the id under the distribution drawn from is z -
+ * log(W * 2^-40) (0 where the largest logit is taken).  A row with no logit
+ * above -infinity gives id -1 and -infinity.
+ *
+ * d_logits: n_rows x n_tok of `type`, rows `stride` apart; d_u: n_rows f32 in
+ * [0, 1) (taken as 0 when below or NaN); filters: host struct (NULL: temperature 1,
+ * no filter); d_ids_out: n_rows int32; d_logprob_out (nullable): n_rows f32.
+ * 1 <= n_tok <= BPE_HEAD_MAX_TOKENS.  Errors: INVALID_ARG, OOM, CUDA. */
+int head_sample(bpe_ctx *ctx, const void *d_logits, uint64_t stride, int type, uint32_t n_rows, uint32_t n_tok,
+                const float *d_u, const head_filters *filters, int32_t *d_ids_out, float *d_logprob_out);
 
 #ifdef __cplusplus
 }
