@@ -82,6 +82,23 @@ int ensure_events(bpe_ctx *ctx, size_t n) {
     return BPE_OK;
 }
 
+int head_status(bpe_ctx *ctx, uint32_t **out) {
+    if (!ctx->head_flag) {
+        void *p = nullptr;
+        BPE_CUDA(ctx, cudaHostAlloc(&p, sizeof(uint32_t), cudaHostAllocMapped), "cudaHostAlloc");
+        *(uint32_t *)p = 0;
+        ctx->head_flag = (uint32_t *)p;
+    }
+    if (*ctx->head_flag) {
+        *ctx->head_flag = 0;
+        return fail(ctx, BPE_ERR_TIMEOUT, "an earlier head_logits gave up a wait: its logits are not valid");
+    }
+    void *d = nullptr;
+    BPE_CUDA(ctx, cudaHostGetDevicePointer(&d, (void *)ctx->head_flag, 0), "cudaHostGetDevicePointer");
+    *out = (uint32_t *)d;
+    return BPE_OK;
+}
+
 void stats_reset(bpe_ctx *ctx) { memset(&ctx->stats, 0, sizeof ctx->stats); }
 
 int stats_slot(bpe_ctx *ctx, const char *name) {
@@ -144,6 +161,7 @@ extern "C" void bpe_ctx_destroy(bpe_ctx *ctx) {
         if (s.p) cudaFree(s.p);
     for (auto ev : ctx->events) cudaEventDestroy(ev);
     if (ctx->pinned) cudaFreeHost(ctx->pinned);
+    if (ctx->head_flag) cudaFreeHost((void *)ctx->head_flag);
     if (ctx->capture_stream) cudaStreamDestroy(ctx->capture_stream);
     delete ctx;
 }

@@ -1,72 +1,464 @@
 // head_logits.cu -- 8-bit matrix product with a scale per block of 128.
+//
+//   out[r, t] = sum_b xs[r, b] ws[t / 128, b] (sum_{k in b} x8[r, k] w8[t, k])
+//
+// The inner sums run on the tensor cores (tcgen05, e4m3 x e4m3, 32-bit
+// accumulators in tensor memory), one block of 128 columns at a time; because
+// every block has scales of its own, each block's 32-bit sums are read back
+// and added, times their scales, to accumulators that stay in registers.  TMA
+// fills a ring of shared-memory stages, one thread issues the products, the
+// other warps scale and add; tensor memory holds several blocks' sums, so that
+// the products of the next blocks run meanwhile.
 #include "head.cuh"
+
+#include <cudaTypedefs.h>
 
 #include "device.cuh"
 #include "internal.h"
+#include "tc.cuh"
 
 namespace bpe {
 namespace {
 
-constexpr int kBlock = (int)BPE_HEAD_BLOCK;
-constexpr int kTile = 64, kDepth = 32;   // output tile, columns staged at a time
+constexpr int kBlock = (int)BPE_HEAD_BLOCK;   // columns per scale = bytes per stage row
 
 struct LogitsParams {
-    const uint8_t *x8, *w8;
     const float *xs, *ws;
     void *out;
-    uint64_t x_stride, xs_row, xs_blk, w_stride, ws_row, ws_blk, out_stride;
-    uint32_t n_rows, n_tok, dim;
+    uint64_t xs_row, xs_blk, ws_row, ws_blk, out_stride;
+    uint32_t n_rows, n_tok, blocks;
+    uint32_t *status;
 };
 
-// One CTA per 64 x 64 tile of the output, 4 x 4 per thread.
-template <typename O>
-__global__ void __launch_bounds__(256) k_head_logits(LogitsParams P) {
-    __shared__ float sx[kDepth][kTile + 1], sw[kDepth][kTile + 1];
-    const uint32_t row0 = blockIdx.y * kTile, tok0 = blockIdx.x * kTile;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {}, part[4][4] = {};
-    for (uint32_t k0 = 0; k0 < P.dim; k0 += kDepth) {
-        for (int i = threadIdx.x; i < kTile * kDepth; i += 256) {
-            const uint32_t r = i / kDepth, c = i % kDepth, k = k0 + c;
-            __nv_fp8_e4m3 a, b;
-            a.__x = row0 + r < P.n_rows && k < P.dim ? P.x8[(row0 + r) * P.x_stride + k] : 0;
-            b.__x = tok0 + r < P.n_tok && k < P.dim ? P.w8[(uint64_t)(tok0 + r) * P.w_stride + k] : 0;
-            sx[c][r] = (float)a;
-            sw[c][r] = (float)b;
+// ------------------------------------------------------------- few rows ----
+// Up to 64 rows: the bound is reading the weights once.  The weights are the
+// product's 128-row side, so that a tile is 128 tokens by kN rows of x, and
+// each lane of tensor memory is a token: its scale is the same for the whole
+// tile, and row r's scale comes from lane r by a shuffle.  Several CTAs share
+// an SM, each with a few stages; a cluster splits the columns of one tile when
+// there are too few tiles to fill the GPU, and joins the parts through
+// distributed shared memory in a fixed order.
+constexpr int kFewThreads = 192;   // 4 warps scale and add, 1 loads, 1 multiplies
+constexpr int kFewStages = 3;
+
+template <int kN> struct Few {
+    static constexpr int kBufs = kN == 64 ? 2 : 4;
+    static constexpr int kCols = kN * kBufs;                    // 64, 128 or 128 of tensor memory
+    static constexpr int kStage = (128 + kN) * kBlock;
+    static constexpr int kSmem = kFewStages * kStage + 1024 + 256;
+    static constexpr int kPerSm = kN == 16 ? 4 : 3;
+};
+
+template <int kN, typename O>
+__global__ void __launch_bounds__(kFewThreads, Few<kN>::kPerSm)
+k_logits_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, LogitsParams P,
+             uint32_t split) {
+    using F = Few<kN>;
+    extern __shared__ uint8_t raw[];
+    uint8_t *base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    const uint32_t tiles = smem_u32(base);
+    const uint32_t bars = tiles + kFewStages * F::kStage;
+    uint32_t *extra = (uint32_t *)(base + kFewStages * F::kStage + 128);   // [0] tensor memory, [1] gave up
+    auto full = [&](int s) { return bars + 8 * s; };
+    auto empty = [&](int s) { return bars + 8 * (kFewStages + s); };
+    auto done = [&](int b) { return bars + 8 * (2 * kFewStages + b); };
+    auto taken = [&](int b) { return bars + 8 * (2 * kFewStages + F::kBufs + b); };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t part = blockIdx.x % split, tile = blockIdx.x / split;
+    const uint32_t b0 = (uint32_t)((uint64_t)P.blocks * part / split), b1 = (uint32_t)((uint64_t)P.blocks * (part + 1) / split);
+    const uint32_t tok0 = tile * 128, row0 = blockIdx.y * kN;
+    volatile uint32_t *gave_up = extra + 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kFewStages; s++) mbar_init(full(s), 1), mbar_init(empty(s), 1);
+        for (int b = 0; b < F::kBufs; b++) mbar_init(done(b), 1), mbar_init(taken(b), 4);
+        extra[1] = 0;
+        mbar_init_fence();
+    }
+    if (warp == 5) tmem_alloc(smem_u32(extra), F::kCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = extra[0];
+
+    float acc[kN];
+#pragma unroll
+    for (int c = 0; c < kN; c++) acc[c] = 0.0f;
+
+    if (warp == 4) {
+        if (lane == 0) {
+            tma_prefetch_map(&map_w);
+            tma_prefetch_map(&map_x);
+            int s = 0;
+            uint32_t phase = 1, issued = 0;
+            for (uint32_t b = b0; b < b1; b++) {
+                if (!mbar_wait(empty(s), phase)) { *gave_up = 1; break; }
+                mbar_expect(full(s), F::kStage);
+                tma_load(tiles + s * F::kStage, &map_w, (int)(b * kBlock), (int)tok0, full(s));
+                tma_load(tiles + s * F::kStage + 128 * kBlock, &map_x, (int)(b * kBlock), (int)row0, full(s));
+                issued++;
+                if (++s == kFewStages) s = 0, phase ^= 1;
+            }
+            if (*gave_up)   // no copy may be in flight when the CTA ends
+                for (uint32_t i = issued > kFewStages ? issued - kFewStages : 0; i < issued; i++)
+                    mbar_wait(full(i % kFewStages), (i / kFewStages) & 1);
         }
-        __syncthreads();
-#pragma unroll 8
-        for (int c = 0; c < kDepth; c++) {
-            float a[4], b[4];
+    } else if (warp == 5) {
+        if (lane == 0) {
+            int s = 0, buf = 0;
+            uint32_t phase = 0, bphase = 1;
+            for (uint32_t b = b0; b < b1; b++) {
+                if (!mbar_wait(taken(buf), bphase) || !mbar_wait(full(s), phase)) { *gave_up = 1; break; }
+                tc_fence_after();
+                const uint64_t dw = operand_desc(tiles + s * F::kStage);
+                const uint64_t dx = operand_desc(tiles + s * F::kStage + 128 * kBlock);
 #pragma unroll
-            for (int j = 0; j < 4; j++) a[j] = sx[c][ty + 16 * j], b[j] = sw[c][tx + 16 * j];
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-#pragma unroll
-                for (int j = 0; j < 4; j++) part[i][j] = fmaf(a[i], b[j], part[i][j]);
+                for (int k = 0; k < 4; k++)
+                    mma_e4m3(tmem + buf * kN, dw + 2 * k, dx + 2 * k, e4m3_instr(128, kN), k > 0);
+                mma_commit(empty(s));
+                mma_commit(done(buf));
+                if (++s == kFewStages) s = 0, phase ^= 1;
+                if (++buf == F::kBufs) buf = 0, bphase ^= 1;
+            }
         }
-        __syncthreads();
-        if ((k0 + kDepth) % kBlock == 0 || k0 + kDepth >= P.dim) {
-            const uint32_t blk = k0 / kBlock;
+    } else {
+        constexpr int kPer = (kN + 31) / 32;   // row scales that a lane holds
+        const float *ws = P.ws + tile * P.ws_row;
+        float sx[kPer];
+        auto scales = [&](uint32_t b) {
+            const float sw = b < b1 ? ws[b * P.ws_blk] : 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; i++)
+            for (int i = 0; i < kPer; i++) {
+                const uint32_t r = row0 + i * 32 + lane;
+                sx[i] = b < b1 && r < P.n_rows && i * 32 + lane < kN ? P.xs[r * P.xs_row + b * P.xs_blk] * sw : 0.0f;
+            }
+        };
+        scales(b0);
+        int buf = 0;
+        uint32_t bphase = 0;
+        for (uint32_t b = b0; b < b1; b++) {
+            float s[kPer];
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const uint32_t r = row0 + ty + 16 * i, t = tok0 + tx + 16 * j;
-                    const float s = r < P.n_rows && t < P.n_tok
-                        ? P.xs[r * P.xs_row + blk * P.xs_blk] * P.ws[t / kBlock * P.ws_row + blk * P.ws_blk] : 0.0f;
-                    acc[i][j] = fmaf(part[i][j], s, acc[i][j]);
-                    part[i][j] = 0.0f;
+            for (int i = 0; i < kPer; i++) s[i] = sx[i];
+            scales(b + 1);
+            if (!__all_sync(kFull, mbar_wait(done(buf), bphase))) { *gave_up = 1; break; }
+            tc_fence_after();
+            constexpr int kStep = kN < 32 ? kN : 32;
+#pragma unroll
+            for (int c0 = 0; c0 < kN; c0 += kStep) {
+                float d[kStep];
+                tmem_load(d, tmem + ((uint32_t)warp << 21) + buf * kN + c0);
+                tmem_wait(d);
+                if (c0 + kStep == kN) {
+                    tc_fence_before();
+                    if (lane == 0) mbar_arrive(taken(buf));
                 }
+#pragma unroll
+                for (int c = 0; c < kStep; c++)
+                    acc[c0 + c] = fmaf(d[c], __shfl_sync(kFull, s[c0 / 32], c), acc[c0 + c]);
+            }
+            if (++buf == F::kBufs) buf = 0, bphase ^= 1;
         }
     }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 5) tmem_free(tmem, F::kCols);
+    const bool failed = *gave_up != 0;
+    if (failed && threadIdx.x == 0) *P.status = DERR_TIMEOUT;
+    O *out = (O *)P.out;
+    const uint32_t t = tok0 + warp * 32 + lane;
+    if (split == 1) {
+        if (warp < 4 && t < P.n_tok && !failed) {
 #pragma unroll
-    for (int i = 0; i < 4; i++)
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const uint32_t r = row0 + ty + 16 * i, t = tok0 + tx + 16 * j;
-            if (r < P.n_rows && t < P.n_tok) ((O *)P.out)[r * P.out_stride + t] = from_f32<O>(acc[i][j]);
+            for (int c = 0; c < kN; c++)
+                if (row0 + c < P.n_rows) out[(row0 + c) * P.out_stride + t] = from_f32<O>(acc[c]);
         }
+        return;
+    }
+    // join: every CTA's stages are idle now and hold its part; CTA i adds up rows i, i + split, ...
+    float *mine = (float *)base;
+    if (warp < 4) {
+#pragma unroll
+        for (int c = 0; c < kN; c++) mine[c * 128 + warp * 32 + lane] = acc[c];
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (warp < 4) {
+        for (uint32_t c = part; c < kN && row0 + c < P.n_rows; c += split) {
+            const uint32_t at = smem_u32(mine + c * 128 + warp * 32 + lane);
+            float v[8];
+#pragma unroll
+            for (uint32_t p = 0; p < 8; p++) {
+                v[p] = 0.0f;
+                if (p < split) {
+                    uint32_t far;
+                    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(at), "r"(p));
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[p]) : "r"(far) : "memory");
+                }
+            }
+            const float sum = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+            if (t < P.n_tok && !failed) out[(row0 + c) * P.out_stride + t] = from_f32<O>(sum);
+        }
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ------------------------------------------------------------ many rows ----
+// The rows of x are the product's 128-row side, 256 tokens the other; one
+// persistent CTA per SM takes tiles in turn, rows of tiles fastest, so that the
+// CTAs that run together read the same weights from L2.  Two sets of sums fill
+// the 512 columns of tensor memory.  A thread that adds holds one row and 128
+// tokens, which is one weight scale: its factor is one number per block.
+constexpr int kManyThreads = 320;   // 8 warps scale and add, 1 loads, 1 multiplies
+constexpr int kManyStages = 4, kManyToks = 256;
+constexpr int kManyStage = (128 + kManyToks) * kBlock;
+constexpr int kStageOut = 33 * 32 * 4;   // a warp's 32 x 32 tile on its way out
+constexpr int kManySmem = kManyStages * kManyStage + 8 * kStageOut + 1024 + 256;
+static_assert(kManySmem <= 232448, "shared memory of a CTA");
+
+template <typename O>
+__global__ void __launch_bounds__(kManyThreads, 1)
+k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, LogitsParams P) {
+    extern __shared__ uint8_t raw[];
+    uint8_t *base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    const uint32_t tiles = smem_u32(base);
+    float *stage_out = (float *)(base + kManyStages * kManyStage);
+    uint8_t *after = base + kManyStages * kManyStage + 8 * kStageOut;
+    const uint32_t bars = smem_u32(after);
+    uint32_t *extra = (uint32_t *)(after + 128);
+    auto full = [&](int s) { return bars + 8 * s; };
+    auto empty = [&](int s) { return bars + 8 * (kManyStages + s); };
+    auto done = [&](int b) { return bars + 8 * (2 * kManyStages + b); };
+    auto taken = [&](int b) { return bars + 8 * (2 * kManyStages + 2 + b); };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t row_tiles = (P.n_rows + 127) / 128, tok_tiles = (P.n_tok + kManyToks - 1) / kManyToks;
+    const uint32_t n_tiles = row_tiles * tok_tiles;
+    volatile uint32_t *gave_up = extra + 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kManyStages; s++) mbar_init(full(s), 1), mbar_init(empty(s), 1);
+        for (int b = 0; b < 2; b++) mbar_init(done(b), 1), mbar_init(taken(b), 8);
+        extra[1] = 0;
+        mbar_init_fence();
+    }
+    if (warp == 9) tmem_alloc(smem_u32(extra), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = extra[0];
+
+    if (warp == 8) {
+        if (lane == 0) {
+            tma_prefetch_map(&map_w);
+            tma_prefetch_map(&map_x);
+            int s = 0;
+            uint32_t phase = 1, issued = 0;
+            for (uint32_t i = blockIdx.x; i < n_tiles && !*gave_up; i += gridDim.x) {
+                const int row0 = (int)(i % row_tiles * 128), tok0 = (int)(i / row_tiles * kManyToks);
+                for (uint32_t b = 0; b < P.blocks; b++) {
+                    if (!mbar_wait(empty(s), phase)) { *gave_up = 1; break; }
+                    mbar_expect(full(s), kManyStage);
+                    tma_load(tiles + s * kManyStage, &map_x, (int)(b * kBlock), row0, full(s));
+                    tma_load(tiles + s * kManyStage + 128 * kBlock, &map_w, (int)(b * kBlock), tok0, full(s));
+                    issued++;
+                    if (++s == kManyStages) s = 0, phase ^= 1;
+                }
+            }
+            if (*gave_up)   // no copy may be in flight when the CTA ends
+                for (uint32_t i = issued > kManyStages ? issued - kManyStages : 0; i < issued; i++)
+                    mbar_wait(full(i % kManyStages), (i / kManyStages) & 1);
+        }
+    } else if (warp == 9) {
+        if (lane == 0) {
+            int s = 0, buf = 0;
+            uint32_t phase = 0, bphase = 1;
+            for (uint32_t i = blockIdx.x; i < n_tiles && !*gave_up; i += gridDim.x) {
+                for (uint32_t b = 0; b < P.blocks; b++) {
+                    if (!mbar_wait(taken(buf), bphase) || !mbar_wait(full(s), phase)) { *gave_up = 1; break; }
+                    tc_fence_after();
+                    const uint64_t dx = operand_desc(tiles + s * kManyStage);
+                    const uint64_t dw = operand_desc(tiles + s * kManyStage + 128 * kBlock);
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        mma_e4m3(tmem + buf * kManyToks, dx + 2 * k, dw + 2 * k, e4m3_instr(128, kManyToks), k > 0);
+                    mma_commit(empty(s));
+                    mma_commit(done(buf));
+                    if (++s == kManyStages) s = 0, phase ^= 1;
+                    if (++buf == 2) buf = 0, bphase ^= 1;
+                }
+            }
+        }
+    } else {
+        const int quarter = warp & 3, half = warp >> 2;
+        float *mine = stage_out + warp * (33 * 32);
+        O *out = (O *)P.out;
+        int buf = 0;
+        uint32_t bphase = 0;
+        for (uint32_t i = blockIdx.x; i < n_tiles; i += gridDim.x) {
+            const uint32_t row0 = i % row_tiles * 128 + quarter * 32, tok0 = i / row_tiles * kManyToks + half * 128;
+            const uint32_t row = row0 + lane;
+            const float *xs = P.xs + (uint64_t)min(row, P.n_rows - 1) * P.xs_row;
+            const float *ws = P.ws + (uint64_t)min(tok0 / kBlock, (P.n_tok - 1) / kBlock) * P.ws_row;
+            float acc[128];
+#pragma unroll
+            for (int c = 0; c < 128; c++) acc[c] = 0.0f;
+            float sx = xs[0], sw = ws[0];
+            bool ok = true;
+            for (uint32_t b = 0; b < P.blocks; b++) {
+                const float s = sx * sw;
+                const uint32_t nb = min(b + 1, P.blocks - 1);
+                sx = xs[nb * P.xs_blk];
+                sw = ws[nb * P.ws_blk];
+                if (!__all_sync(kFull, mbar_wait(done(buf), bphase))) { ok = false; break; }
+                tc_fence_after();
+#pragma unroll
+                for (int c0 = 0; c0 < 128; c0 += 32) {
+                    float d[32];
+                    tmem_load(d, tmem + ((uint32_t)quarter << 21) + buf * kManyToks + half * 128 + c0);
+                    tmem_wait(d);
+                    if (c0 == 96) {
+                        tc_fence_before();
+                        if (lane == 0) mbar_arrive(taken(buf));
+                    }
+#pragma unroll
+                    for (int c = 0; c < 32; c++) acc[c0 + c] = fmaf(d[c], s, acc[c0 + c]);
+                }
+                if (++buf == 2) buf = 0, bphase ^= 1;
+            }
+            if (!ok) { *gave_up = 1; break; }
+            // rows to lines: 32 x 32 at a time through shared memory, so that a store is 32 tokens of one row
+#pragma unroll
+            for (int c0 = 0; c0 < 128; c0 += 32) {
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 32; c++) mine[lane * 33 + c] = acc[c0 + c];
+                __syncwarp();
+                const uint32_t t = tok0 + c0 + lane;
+                if (t < P.n_tok) {
+#pragma unroll 8
+                    for (uint32_t r = 0; r < 32; r++)
+                        if (row0 + r < P.n_rows) out[(row0 + r) * P.out_stride + t] = from_f32<O>(mine[r * 33 + lane]);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_free(tmem, 512);
+    if (threadIdx.x == 0 && *gave_up) *P.status = DERR_TIMEOUT;
+}
+
+// -------------------------------------------------------------- the host ---
+// Rows that do not start on 16 bytes, copied to rows that do.
+__global__ void __launch_bounds__(256) k_head_align(const uint8_t *__restrict__ src, uint64_t stride, uint32_t rows,
+                                                    uint32_t dim, uint8_t *__restrict__ dst, uint32_t dst_stride) {
+    const uint64_t words = (uint64_t)rows * (dst_stride / 4);
+    for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < words; i += gridDim.x * 256ull) {
+        const uint64_t r = i / (dst_stride / 4);
+        const uint32_t c = (uint32_t)(i % (dst_stride / 4)) * 4;
+        uint32_t v = 0;
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (c + j < dim) v |= (uint32_t)src[r * stride + c + j] << (8 * j);
+        *(uint32_t *)(dst + r * dst_stride + c) = v;
+    }
+}
+
+typedef PFN_cuTensorMapEncodeTiled_v12000 EncodeFn;
+
+EncodeFn encode_fn() {
+    static const EncodeFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return (EncodeFn) nullptr;
+        }
+        return (EncodeFn)p;
+    }();
+    return fn;
+}
+
+// The tile map of an 8-bit matrix, box_rows x 128 columns; columns past dim read as 0.
+int encode_map(bpe_ctx *ctx, CUtensorMap *map, const uint8_t *p, uint64_t stride, uint32_t rows, uint32_t dim, uint32_t box_rows) {
+    EncodeFn fn = encode_fn();
+    if (!fn) return fail(ctx, BPE_ERR_CUDA, "head_logits: the driver has no cuTensorMapEncodeTiled");
+    const cuuint64_t size[2] = {dim, rows}, strides[1] = {stride};
+    const cuuint32_t box[2] = {(cuuint32_t)kBlock, box_rows}, step[2] = {1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void *)p, size, strides, box, step,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(ctx, BPE_ERR_CUDA, "head_logits: cuTensorMapEncodeTiled returned %d", (int)r);
+    return BPE_OK;
+}
+
+// `p` itself where TMA can read it, else a copy in scratch.
+int aligned_rows(bpe_ctx *ctx, Slot slot, const uint8_t *&p, uint64_t &stride, uint32_t rows, uint32_t dim) {
+    if (rows == 1 && stride % 16) stride = ((uint64_t)dim + 15) & ~15ull;
+    if ((uintptr_t)p % 16 == 0 && stride % 16 == 0 && stride < (1ull << 40)) return BPE_OK;
+    const uint32_t to = (dim + 15) & ~15u;
+    void *q;
+    int rc = ensure(ctx, slot, (size_t)rows * to, &q);
+    if (rc) return rc;
+    const uint64_t want = ((uint64_t)rows * (to / 4) + 255) / 256;
+    const uint32_t grid = (uint32_t)(want < (uint64_t)ctx->sm_count * 16 ? want : (uint64_t)ctx->sm_count * 16);
+    k_head_align<<<grid, 256, 0, ctx->stream>>>(p, stride, rows, dim, (uint8_t *)q, to);
+    BPE_CUDA(ctx, cudaGetLastError(), "head_logits align");
+    p = (const uint8_t *)q;
+    stride = to;
+    return BPE_OK;
+}
+
+template <int kN, typename O>
+int launch_few(bpe_ctx *ctx, const CUtensorMap &mw, const CUtensorMap &mx, const LogitsParams &P) {
+    using F = Few<kN>;
+    const uint32_t tiles = (P.n_tok + 127) / 128, rows = (P.n_rows + kN - 1) / kN;
+    // split the columns while all parts still run at once and a part has four blocks
+    uint32_t split = 1;
+    while (split < 8 && tiles * rows * split * 2 <= (uint32_t)(ctx->sm_count * F::kPerSm) && P.blocks >= split * 8) split *= 2;
+    auto k = k_logits_few<kN, O>;
+    BPE_CUDA(ctx, cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem), "head_logits");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(tiles * split, rows);
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = F::kSmem;
+    cfg.stream = ctx->stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {split, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 1 : 0;
+    BPE_CUDA(ctx, cudaLaunchKernelEx(&cfg, k, mw, mx, P, split), "head_logits launch");
+    return BPE_OK;
+}
+
+template <typename O>
+int launch_many(bpe_ctx *ctx, const CUtensorMap &mw, const CUtensorMap &mx, const LogitsParams &P) {
+    auto k = k_logits_many<O>;
+    BPE_CUDA(ctx, cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kManySmem), "head_logits");
+    const uint64_t n_tiles = (uint64_t)((P.n_rows + 127) / 128) * ((P.n_tok + kManyToks - 1) / kManyToks);
+    const uint32_t grid = (uint32_t)(n_tiles < (uint64_t)ctx->sm_count ? n_tiles : (uint64_t)ctx->sm_count);
+    k<<<grid, kManyThreads, kManySmem, ctx->stream>>>(mw, mx, P);
+    BPE_CUDA(ctx, cudaGetLastError(), "head_logits launch");
+    return BPE_OK;
+}
+
+template <typename O>
+int launch(bpe_ctx *ctx, const uint8_t *x8, uint64_t x_stride, const uint8_t *w8, uint64_t w_stride, uint32_t dim, const LogitsParams &P) {
+    const int n = P.n_rows <= 16 ? 16 : P.n_rows <= 32 ? 32 : P.n_rows <= 64 ? 64 : 0;
+    CUtensorMap mw, mx;
+    int rc;
+    if ((rc = encode_map(ctx, &mw, w8, w_stride, P.n_tok, dim, n ? 128 : kManyToks)) ||
+        (rc = encode_map(ctx, &mx, x8, x_stride, P.n_rows, dim, n ? n : 128)))
+        return rc;
+    if (n == 16) return launch_few<16, O>(ctx, mw, mx, P);
+    if (n == 32) return launch_few<32, O>(ctx, mw, mx, P);
+    if (n == 64) return launch_few<64, O>(ctx, mw, mx, P);
+    return launch_many<O>(ctx, mw, mx, P);
 }
 
 }  // namespace
@@ -83,21 +475,19 @@ extern "C" int head_logits(bpe_ctx *ctx, const uint8_t *d_x8, uint64_t x8_stride
     if (dim == 0 || dim > BPE_HEAD_MAX_DIM || n_tok == 0 || n_tok > BPE_HEAD_MAX_TOKENS)
         return fail(ctx, BPE_ERR_INVALID_ARG, "head_logits: %u tokens of %u columns", n_tok, dim);
     if (n_rows == 0) return BPE_OK;
-    if (n_rows > (1u << 22)) return fail(ctx, BPE_ERR_INVALID_ARG, "head_logits: %u rows", n_rows);
+    if (n_rows > BPE_HEAD_MAX_TOKENS) return fail(ctx, BPE_ERR_INVALID_ARG, "head_logits: %u rows", n_rows);
     if (!d_x8 || !d_xs || !d_w8 || !d_ws || !d_out) return fail(ctx, BPE_ERR_INVALID_ARG, "head_logits: null pointer");
     if ((n_rows > 1 && (x8_stride < dim || out_stride < n_tok)) || (n_tok > 1 && w8_stride < dim))
         return fail(ctx, BPE_ERR_INVALID_ARG, "head_logits: a row stride is below its row's length");
     BPE_CUDA(ctx, cudaSetDevice(ctx->device), "cudaSetDevice");
-    LogitsParams P{d_x8, d_w8, d_xs, d_ws, d_out, x8_stride, xs_row_stride, xs_block_stride, w8_stride,
-                   ws_row_stride, ws_block_stride, out_stride, n_rows, n_tok, dim};
-    const dim3 grid((n_tok + kTile - 1) / kTile, (n_rows + kTile - 1) / kTile);
-    if (grid.y > 65535) return fail(ctx, BPE_ERR_INVALID_ARG, "head_logits: %u rows", n_rows);
-    if (out_type == BPE_F32)
-        k_head_logits<float><<<grid, 256, 0, ctx->stream>>>(P);
-    else if (out_type == BPE_BF16)
-        k_head_logits<__nv_bfloat16><<<grid, 256, 0, ctx->stream>>>(P);
-    else
-        k_head_logits<__half><<<grid, 256, 0, ctx->stream>>>(P);
-    BPE_CUDA(ctx, cudaGetLastError(), "head_logits launch");
-    return BPE_OK;
+    int rc;
+    uint32_t *status;
+    if ((rc = head_status(ctx, &status)) || (rc = aligned_rows(ctx, S_HEAD_X, d_x8, x8_stride, n_rows, dim)) ||
+        (rc = aligned_rows(ctx, S_HEAD_W, d_w8, w8_stride, n_tok, dim)))
+        return rc;
+    const LogitsParams P{d_xs, d_ws, d_out, xs_row_stride, xs_block_stride, ws_row_stride, ws_block_stride, out_stride,
+                         n_rows, n_tok, (dim + kBlock - 1) / kBlock, status};
+    if (out_type == BPE_F32) return launch<float>(ctx, d_x8, x8_stride, d_w8, w8_stride, dim, P);
+    if (out_type == BPE_BF16) return launch<__nv_bfloat16>(ctx, d_x8, x8_stride, d_w8, w8_stride, dim, P);
+    return launch<__half>(ctx, d_x8, x8_stride, d_w8, w8_stride, dim, P);
 }

@@ -27,6 +27,7 @@ enum Slot {
     S_DEC_TOK, S_DEC_OFF, S_DEC_BSUM, S_DEC_STATE,
     S_L_STATE, S_L_OCC, S_L_EKEY, S_L_ECNT, S_L_ELEN, S_L_EOFF, S_L_VLEN, S_L_BFILL, S_L_EBEST, S_L_FRONT,
     S_L_HSLOT, S_L_HCNT, S_L_HENT, S_L_NS, S_L_CAND, S_L_APP, S_L_REC, S_L_CSTAT, S_L_KMODE, S_L_CBAR, S_L_CTILE,
+    S_HEAD_X, S_HEAD_W,
     S_NUM
 };
 
@@ -86,6 +87,7 @@ struct bpe_ctx {
     bpe_stream *pipe_stream = nullptr;
     const bpe_trie *pipe_trie = nullptr;
     uint32_t pipe_max_len = 0;
+    volatile uint32_t *head_flag = nullptr;   // host word (mapped) that a head kernel sets when a wait gives up
 };
 
 namespace bpe {
@@ -105,6 +107,11 @@ int ensure_pinned(bpe_ctx *ctx, size_t bytes, void **out);
 
 // Make sure ctx->events holds at least n timing events.
 int ensure_events(bpe_ctx *ctx, size_t n);
+
+// The device address of the word that a head kernel sets when a bounded wait
+// gives up (made on first use).  Fails with BPE_ERR_TIMEOUT when an earlier
+// call on this context has set it.
+int head_status(bpe_ctx *ctx, uint32_t **out);
 
 // Stats helpers.
 void stats_reset(bpe_ctx *ctx);
