@@ -1,5 +1,17 @@
 // head_sample.cu -- temperature, top-k, top-p, min-p and the draw of one id
 // per row from a given random number.
+//
+// With m the row's largest logit, e = exp((l - m) / T) and the whole numbers
+// w = floor(e 2^40): sums of w are exact, so neither the split of a row over
+// threads and CTAs nor the order of atomics changes an answer.  The three
+// filters keep a prefix of the tokens ordered by logit (then by id), so that
+// one cut -- a last kept token -- describes what is kept, and the draw is a
+// search for a running sum in order of ids.
+//
+// A row is read once: a cluster of 1 to 8 CTAs keeps its e in shared memory.  The
+// cut is found by histograms over the bits of e, which are ordered as e is: 4
+// buckets an octave, then 128 of the bucket that holds the cut, and so on until
+// at most 128 tokens are left, which are ranked by comparing all pairs.
 #include "head.cuh"
 
 #include "device.cuh"
@@ -17,6 +29,7 @@ struct SampleParams {
     const void *logits;
     uint64_t stride;
     uint32_t n_tok;
+    int type;
     const float *u;
     head_filters f;
     int32_t *ids;
@@ -24,7 +37,7 @@ struct SampleParams {
 };
 
 // Logits as whole numbers of the same order (a NaN as -infinity, -0 as 0).
-constexpr uint32_t kKeyNegInf = 0x007FFFFFu, kKeyPosInf = 0xFF800000u;
+constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
 __device__ __forceinline__ uint32_t key_of(float v) {
     const uint32_t b = __float_as_uint(v + 0.0f);
     const uint32_t k = b & 0x80000000u ? ~b : b | 0x80000000u;
@@ -34,7 +47,9 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
-__device__ __forceinline__ float z_of(float v, float top, float inv_t) { return v == top ? 0.0f : (v - top) * inv_t; }
+__device__ __forceinline__ float z_of(float v, float top, float inv_t) {
+    return v == top ? 0.0f : __fmul_rn(v - top, inv_t);
+}
 __device__ __forceinline__ u64 weight_of(float v, float top, float inv_t) {
     return v > -INFINITY ? (u64)(expf(z_of(v, top, inv_t)) * kOne) : 0;   // 0 for -infinity and NaN
 }
@@ -50,10 +65,468 @@ __device__ __forceinline__ u64 sum_all(u64 v, u64 *red) {
     return t;
 }
 
-// One CTA per row.  The kept tokens are those with a key above `cut`, and the
+// ------------------------------------------------- rows in shared memory ---
+constexpr int kBuckets = 161;              // 4 per octave from 2^-40 to 1
+constexpr int kList = 128;                 // tokens that are ranked pair by pair
+constexpr uint32_t kLeast = 0x2B800000u;   // the bits of 2^-40: below it a weight is 0
+constexpr int kMaxTeam = 8;
+
+// w = floor(e 2^40) for 2^-40 <= e <= 1, given e's bits.
+__device__ __forceinline__ u64 weight_bits(uint32_t b) {
+    return (u64)((b & 0x7FFFFFu) | 0x800000u) << ((b >> 23) - 87) >> 23;
+}
+
+struct __align__(16) Entry { uint32_t key, idx; u64 w; };
+
+template <int kThreads> struct SampleShared {
+    static constexpr int kCopies = kThreads / 32;   // of a histogram, by thread
+    uint32_t lo[kBuckets * kCopies], hi[kBuckets * kCopies];
+    u64 sum[2][kBuckets];                  // this CTA's histogram, read by the whole cluster
+    u64 slot[2][kMaxTeam];                 // a value from each CTA of the cluster
+    u64 red[32];
+    Entry list[kList];
+    uint32_t list_n;
+    u64 pick[3];                           // bucket found, sums above and in it
+    u64 goal[2];                           // whole sum, target
+    uint32_t cut[3];                       // bits, key, id of the last kept token
+    float4 e[1];                           // the CTA's tokens, four at a time
+};
+
+__device__ __forceinline__ uint32_t far_addr(const void *p, uint32_t rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void far_store(void *p, uint32_t rank, u64 v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(far_addr(p, rank)), "l"(v) : "memory");
+}
+__device__ __forceinline__ void far_store(uint32_t *p, uint32_t rank, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(far_addr(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ u64 far_load(const u64 *p, uint32_t rank) {
+    u64 v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(far_addr(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t far_count(uint32_t *p, uint32_t rank) {
+    uint32_t v;
+    asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(v) : "r"(far_addr(p, rank)) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ u64 warp_sum(u64 v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+    return v;
+}
+__device__ __forceinline__ u64 warp_scan(u64 v, int lane) {   // inclusive
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const u64 o = __shfl_up_sync(kFull, v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+template <int kThreads>
+struct Sampler {
+    static constexpr int kWarps = kThreads / 32, kCopies = SampleShared<kThreads>::kCopies;
+    SampleShared<kThreads> &S;
+    const SampleParams &P;
+    const uint8_t *l;       // the row
+    uint32_t rank, size;    // this CTA among the row's
+    uint32_t first, quads;  // its tokens begin here; groups of four
+    uint32_t q0, q1;        // the groups of this warp, contiguous
+    int lane, warp, turn;
+    float top, inv_t;
+    uint32_t cut_bits, cut_key, cut_idx;
+
+    __device__ __forceinline__ void sync() const {
+        if (size == 1)
+            __syncthreads();
+        else
+            asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+    __device__ __forceinline__ float logit(uint32_t idx) const {
+        if (P.type == BPE_F32) return ((const float *)l)[idx];
+        if (P.type == BPE_BF16) return to_f32(((const __nv_bfloat16 *)l)[idx]);
+        return to_f32(((const __half *)l)[idx]);
+    }
+    __device__ __forceinline__ uint32_t key(uint32_t i) const { return key_of(logit(first + i)); }   // of the CTA's token i
+    __device__ __forceinline__ float exp_of(float v) const {
+        return v == top ? 1.0f : fmaxf(expf(__fmul_rn(v - top, inv_t)), 0.0f);   // NaN, of inf * 0, as 0
+    }
+    // f(i, bits of e) for the CTA's tokens, this warp's share
+    template <typename F> __device__ __forceinline__ void each(F f) const {
+#pragma unroll 2
+        for (uint32_t q = q0 + lane; q < q1; q += 32) {
+            const float4 v = S.e[q];
+            f(q * 4, __float_as_uint(v.x));
+            f(q * 4 + 1, __float_as_uint(v.y));
+            f(q * 4 + 2, __float_as_uint(v.z));
+            f(q * 4 + 3, __float_as_uint(v.w));
+        }
+    }
+
+    // One value per CTA to every CTA of the row; all threads of the CTA hold `v`.
+    __device__ __forceinline__ void exchange(u64 v) {
+        turn ^= 1;
+        if (threadIdx.x < size) far_store(&S.slot[turn][rank], threadIdx.x, v);
+        sync();
+    }
+    __device__ __forceinline__ u64 max_row(u64 v) {
+        v = warp_max_u64(v);
+        __syncthreads();
+        if (lane == 0) S.red[warp] = v;
+        __syncthreads();
+        exchange(warp_max_u64(lane < kWarps ? S.red[lane] : 0));
+        v = 0;
+        for (uint32_t r = 0; r < size; r++) v = max(v, S.slot[turn][r]);
+        return v;
+    }
+    // The row's sum; `before`, `mine`: the sums of the CTAs before this one, and this one's.  The warps' stay in S.red.
+    __device__ __forceinline__ u64 sum_row(u64 v, u64 &before, u64 &mine) {
+        v = warp_sum(v);
+        __syncthreads();
+        if (lane == 0) S.red[warp] = v;
+        __syncthreads();
+        mine = warp_sum(lane < kWarps ? S.red[lane] : 0);
+        exchange(mine);
+        u64 total = 0;
+        before = 0;
+        for (uint32_t r = 0; r < size; r++) {
+            const u64 x = S.slot[turn][r];
+            before += r < rank ? x : 0;
+            total += x;
+        }
+        return total;
+    }
+    __device__ __forceinline__ u64 sum_row(u64 v) {
+        u64 a, b;
+        return sum_row(v, a, b);
+    }
+
+    // The token, in order of ids, at which the running sum of value(i, bits) passes t; the lane that holds it calls
+    // found(i).  Follows sum_row over the same values.
+    template <typename V, typename F>
+    __device__ __forceinline__ void locate(V value, u64 t, u64 before, u64 mine, F found) {
+        if (t < before || t - before >= mine) return;
+        t -= before;
+        const u64 own = lane < kWarps ? S.red[lane] : 0, run = warp_scan(own, lane);
+        if (__ffs(__ballot_sync(kFull, run > t)) - 1 != warp) return;
+        t -= __shfl_sync(kFull, run - own, warp);
+        for (uint32_t q = q0; q < q1; q += 32) {
+            const float4 v = q + lane < q1 ? S.e[q + lane] : make_float4(0, 0, 0, 0);
+            const uint32_t i = (q + lane) * 4;
+            const u64 a = value(i, __float_as_uint(v.x)), b = value(i + 1, __float_as_uint(v.y));
+            const u64 c = value(i + 2, __float_as_uint(v.z)), d = value(i + 3, __float_as_uint(v.w));
+            const u64 s = a + b + c + d, upto = warp_scan(s, lane);
+            const unsigned past = __ballot_sync(kFull, upto > t);
+            if (past) {
+                if (lane == __ffs(past) - 1) {
+                    const u64 r = t - (upto - s);
+                    found(r < a ? i : r < a + b ? i + 1 : r < a + b + c ? i + 2 : i + 3);
+                }
+                return;
+            }
+            t -= __shfl_sync(kFull, upto, 31);
+        }
+    }
+
+    // The weight of token i if it is kept under the cut.
+    __device__ __forceinline__ u64 kept(uint32_t i, uint32_t b) const {
+        if (b < cut_bits) return 0;
+        if (b == cut_bits && cut_idx != ~0u) {
+            const uint32_t x = key(i);
+            if (x < cut_key || (x == cut_key && first + i > cut_idx)) return 0;
+        }
+        return weight_bits(b);
+    }
+    __device__ __forceinline__ u64 mass() const {
+        u64 m = 0;
+        each([&](uint32_t i, uint32_t b) { m += kept(i, b); });
+        return m;
+    }
+    __device__ __forceinline__ void read_cut() { cut_bits = S.cut[0], cut_key = S.cut[1], cut_idx = S.cut[2]; }
+
+    // The last token kept when tokens are taken in order (largest logit, then lowest id) until the sum of their
+    // values -- 1, or the weight -- reaches the target: `target`, or with share >= 0 that share of the whole sum, and
+    // at least 1.  Where the whole sum is below the target, everything is kept and the cut stays.
+    template <bool kMass>
+    __device__ __forceinline__ void select(u64 target, double share) {
+        u64 above = 0;
+        uint32_t low = kLeast;
+        int shift = 21, buckets = kBuckets;
+        for (int level = 0;; level++) {
+            // histogram of [low, low + (buckets << shift))
+            for (int i = threadIdx.x; i < buckets * kCopies; i += kThreads) {
+                S.lo[i] = 0;
+                if (kMass) S.hi[i] = 0;
+            }
+            if (threadIdx.x == 0) S.list_n = 0, S.pick[0] = ~0ull;
+            __syncthreads();
+            const int copy = threadIdx.x & (kCopies - 1);
+            each([&](uint32_t, uint32_t b) {
+                const uint32_t k = (b - low) >> shift;
+                if (b < low || k >= (uint32_t)buckets) return;
+                if (kMass) {   // at most 2,048 tokens a copy: neither half passes 32 bits
+                    const u64 w = weight_bits(b);
+                    atomicAdd(&S.lo[k * kCopies + copy], (uint32_t)w & 0xFFFFFu);
+                    const uint32_t h = (uint32_t)(w >> 20);
+                    if (h) atomicAdd(&S.hi[k * kCopies + copy], h);
+                } else {
+                    atomicAdd(&S.lo[k * kCopies + copy], 1u);
+                }
+            });
+            __syncthreads();
+            u64 *sum = S.sum[level & 1];
+            for (int b = threadIdx.x; b < buckets; b += kThreads) {
+                u64 lo = 0, hi = 0;
+#pragma unroll
+                for (int c = 0; c < kCopies; c++) {
+                    const int a = b * kCopies + ((c + b) & (kCopies - 1));
+                    lo += S.lo[a];
+                    if (kMass) hi += S.hi[a];
+                }
+                sum[b] = lo + (hi << 20);
+            }
+            sync();
+            // the row's histogram, largest first, and the bucket at which the running sum reaches the target
+            if (warp == 0) {
+                constexpr int kPer = (kBuckets + 31) / 32;
+                u64 v[kPer], s = 0;
+#pragma unroll
+                for (int j = 0; j < kPer; j++) {
+                    const int b = buckets - 1 - (lane * kPer + j);
+                    v[j] = 0;
+                    if (b >= 0)
+                        for (uint32_t r = 0; r < size; r++) v[j] += far_load(sum + b, r);
+                    s += v[j];
+                }
+                u64 run = warp_scan(s, lane);
+                if (level == 0 && share >= 0.0) {
+                    const double x = share * (double)__shfl_sync(kFull, run, 31);
+                    target = x > 1.0 ? (u64)x : 1;
+                }
+                run = above + run - s;
+#pragma unroll
+                for (int j = 0; j < kPer; j++) {
+                    if (run < target && target <= run + v[j]) {
+                        S.pick[0] = buckets - 1 - (lane * kPer + j);
+                        S.pick[1] = run;
+                        S.pick[2] = v[j];
+                    }
+                    run += v[j];
+                }
+                if (lane == 0) S.goal[0] = target;
+            }
+            __syncthreads();
+            if (S.pick[0] == ~0ull) return;   // at level 0: less than the target in all
+            target = S.goal[0];
+            low += (uint32_t)S.pick[0] << shift;
+            above = S.pick[1];
+            const uint32_t high = low + (1u << shift) - 1;
+            // at most this many tokens are in the bucket
+            const u64 most = kMass ? S.pick[2] / weight_bits(low) : S.pick[2];
+            if (most <= kList) {
+                each([&](uint32_t i, uint32_t b) {
+                    if (b < low || b > high) return;
+                    const uint32_t k = key(i);
+                    const u64 w = weight_bits(b);
+                    for (uint32_t r = 0; r < size; r++) {
+                        const uint32_t n = far_count(&S.list_n, r);
+                        asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(far_addr(&S.list[n], r)),
+                                     "r"(k), "r"(first + i), "r"((uint32_t)w), "r"((uint32_t)(w >> 32)) : "memory");
+                    }
+                });
+                sync();
+                const uint32_t n = S.list_n;
+                // four lanes a token add up what comes before it
+                for (uint32_t i0 = 0; i0 < n; i0 += kThreads / 4) {
+                    const uint32_t i = min(i0 + threadIdx.x / 4, n - 1);
+                    const Entry x = S.list[i];
+                    u64 run = 0;
+                    for (uint32_t j = lane & 3; j < n; j += 4) {
+                        const Entry y = S.list[j];
+                        if (y.key > x.key || (y.key == x.key && y.idx < x.idx)) run += kMass ? y.w : 1;
+                    }
+                    run += __shfl_xor_sync(kFull, run, 1);
+                    run += __shfl_xor_sync(kFull, run, 2);
+                    run += above;
+                    if (run < target && target <= run + (kMass ? x.w : 1)) {
+                        S.cut[0] = __float_as_uint(exp_of(key_value(x.key)));
+                        S.cut[1] = x.key;
+                        S.cut[2] = x.idx;
+                    }
+                }
+                __syncthreads();
+                return;
+            }
+            if (shift == 0) break;   // over kList tokens with the same e
+            buckets = 128;
+            shift -= 7;
+            sync();                  // the row's sums are read before they are written again
+        }
+        // tokens of one e: `need` of them, by logit, then by id
+        const u64 w = kMass ? weight_bits(low) : 1;
+        u64 need = (target - above + w - 1) / w, big = 0, small = 0;
+        each([&](uint32_t i, uint32_t b) {
+            if (b != low) return;
+            const uint32_t k = key(i);
+            big = max(big, (u64)k);
+            small = max(small, (u64)(uint32_t)~k);
+        });
+        big = max_row(big);
+        small = (uint32_t)~(uint32_t)max_row(small);
+        uint32_t at = (uint32_t)small;
+        if (big != small) {          // logits that differ by less than e can tell
+            at = 0;
+            for (int bit = 31; bit >= 0; bit--) {
+                const uint32_t c = at | 1u << bit;
+                u64 m = 0;
+                each([&](uint32_t i, uint32_t b) { m += b == low && key(i) >= c; });
+                if (sum_row(m) >= need) at = c;
+            }
+            u64 m = 0;
+            each([&](uint32_t i, uint32_t b) { m += b == low && key(i) > at; });
+            need -= sum_row(m);
+        }
+        auto one = [&](uint32_t i, uint32_t b) -> u64 { return b == low && key(i) == at; };
+        u64 m = 0, before, mine;
+        each([&](uint32_t i, uint32_t b) { m += one(i, b); });
+        sum_row(m, before, mine);
+        locate(one, need - 1, before, mine, [&](uint32_t i) {
+            for (uint32_t r = 0; r < size; r++) far_store(&S.cut[2], r, first + i);
+        });
+        if (threadIdx.x == 0) S.cut[0] = low, S.cut[1] = at;
+        sync();
+    }
+};
+
+// Four tokens of a row as f32.
+template <typename T> __device__ __forceinline__ float4 load_quad(const T *p);
+template <> __device__ __forceinline__ float4 load_quad<float>(const float *p) { return __ldcs((const float4 *)p); }
+template <> __device__ __forceinline__ float4 load_quad<__nv_bfloat16>(const __nv_bfloat16 *p) {
+    const uint2 v = __ldcs((const uint2 *)p);
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xFFFF0000u));
+}
+template <> __device__ __forceinline__ float4 load_quad<__half>(const __half *p) {
+    const uint2 v = __ldcs((const uint2 *)p);
+    const float2 a = __half22float2(*(const __half2 *)&v.x), b = __half22float2(*(const __half2 *)&v.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// The CTA's tokens to shared memory; the largest of this thread's, NaN aside.
+template <typename T, int kThreads>
+__device__ __forceinline__ float load_row(const T *l, uint32_t count, bool wide, float4 *e) {
+    float big = -INFINITY;
+    const uint32_t whole = wide ? count / 4 : 0;
+#pragma unroll 8
+    for (uint32_t q = threadIdx.x; q < whole; q += kThreads) {
+        const float4 v = load_quad(l + q * 4);
+        big = fmaxf(fmaxf(big, fmaxf(v.x, v.y)), fmaxf(v.z, v.w));
+        e[q] = v;
+    }
+    const uint32_t end = (count + 3) & ~3u;
+#pragma unroll 4
+    for (uint32_t i = whole * 4 + threadIdx.x; i < end; i += kThreads) {
+        const float v = i < count ? to_f32(l[i]) : -INFINITY;
+        big = fmaxf(big, v);
+        ((float *)e)[i] = v;
+    }
+    return big;
+}
+
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    SampleShared<kThreads> &S = *reinterpret_cast<SampleShared<kThreads> *>(raw);
+    const uint32_t row = blockIdx.x / team, rank = blockIdx.x % team;
+    const uint32_t first = min(P.n_tok, rank * slice), count = min(P.n_tok, first + slice) - first;
+    const uint64_t at = row * P.stride + first;
+    // every CTA of the row has begun before another writes to its shared memory
+    if (team > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    float big = P.type == BPE_F32    ? load_row<float, kThreads>((const float *)P.logits + at, count, wide, S.e)
+                : P.type == BPE_BF16 ? load_row<__nv_bfloat16, kThreads>((const __nv_bfloat16 *)P.logits + at, count, wide, S.e)
+                                     : load_row<__half, kThreads>((const __half *)P.logits + at, count, wide, S.e);
+    const uint32_t quads = (count + 3) / 4, seg = (quads + kThreads / 32 - 1) / (kThreads / 32);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Sampler<kThreads> A{S, P, (const uint8_t *)P.logits + row * P.stride * (P.type == BPE_F32 ? 4 : 2), rank, team, first,
+                        quads, min(quads, warp * seg), min(quads, (warp + 1) * seg), lane, warp, 0};
+    if (team > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const uint32_t kmax = (uint32_t)A.max_row(key_of(big));
+    if (kmax == kKeyNegInf) {
+        if (rank == 0 && threadIdx.x == 0) {
+            P.ids[row] = -1;
+            if (P.logprob) P.logprob[row] = -INFINITY;
+        }
+        A.sync();
+        return;
+    }
+    A.top = key_value(kmax);
+    const float temp = P.f.d_temperature ? P.f.d_temperature[row] : P.f.temperature;
+    if (!(temp >= kMinScale)) {   // the lowest id of the largest logit
+        u64 low = 0;
+        A.each([&](uint32_t i, uint32_t b) {
+            if (__uint_as_float(b) == A.top && i < count) low = max(low, (u64)(uint32_t)~(first + i));
+        });
+        low = A.max_row(low);
+        if (rank == 0 && threadIdx.x == 0) {
+            P.ids[row] = (int32_t)~(uint32_t)low;
+            if (P.logprob) P.logprob[row] = 0.0f;
+        }
+        A.sync();
+        return;
+    }
+    const int32_t k = P.f.d_top_k ? P.f.d_top_k[row] : P.f.top_k;
+    const float p = P.f.d_top_p ? P.f.d_top_p[row] : P.f.top_p;
+    const float q = P.f.d_min_p ? P.f.d_min_p[row] : P.f.min_p;
+    A.inv_t = 1.0f / temp;
+#pragma unroll 2
+    for (uint32_t i = A.q0 + lane; i < A.q1; i += 32) {
+        float4 v = S.e[i];
+        v.x = A.exp_of(v.x), v.y = A.exp_of(v.y), v.z = A.exp_of(v.z), v.w = A.exp_of(v.w);
+        S.e[i] = v;
+    }
+    if (threadIdx.x == 0) S.cut[0] = kLeast, S.cut[1] = 0, S.cut[2] = ~0u;   // keep every weight above 0
+    __syncthreads();
+    const bool by_count = k >= 1 && (uint32_t)k < P.n_tok;
+    if (by_count) A.template select<false>((u64)k, -1.0);
+    if (p < 1.0f) {
+        u64 target = 0;
+        if (by_count) {
+            A.read_cut();
+            const double x = (double)p * (double)A.sum_row(A.mass());
+            target = x > 1.0 ? (u64)x : 1;
+        }
+        A.template select<true>(target, by_count ? -1.0 : p > 0.0f ? (double)p : 0.0);
+    }
+    A.read_cut();
+    if (q > 0.0f) {
+        // w >= floor(q 2^40), a multiple of 2^-40 with at most 24 digits: compare e's bits
+        const uint32_t least = __float_as_uint((float)(u64)(fminf(q, 1.0f) * kOne) * 0x1p-40f);
+        if (least > A.cut_bits) A.cut_bits = least, A.cut_idx = ~0u;
+    }
+    u64 before, mine;
+    const u64 total = A.sum_row(A.mass(), before, mine);
+    const double x = (double)P.u[row] * (double)total;
+    u64 t = x > 0.0 ? (u64)x : 0;
+    if (t > total - 1) t = total - 1;
+    A.locate([&](uint32_t i, uint32_t b) { return A.kept(i, b); }, t, before, mine, [&](uint32_t i) {
+        P.ids[row] = (int32_t)(first + i);
+        if (P.logprob)
+            P.logprob[row] = (float)((double)z_of(A.logit(first + i), A.top, A.inv_t) - log((double)total * 0x1p-40));
+    });
+    A.sync();   // no CTA ends while another may read its shared memory
+}
+
+// Vocabularies beyond a cluster's shared memory (over 262,144 tokens): one CTA per
+// row reads it from L2 again in each step.  The kept tokens are those with a key above `cut`, and the
 // first `ties` with the key `cut`; the cut is found bit by bit.
 template <typename T>
-__global__ void __launch_bounds__(kSampThreads) k_head_sample(SampleParams P) {
+__global__ void __launch_bounds__(kSampThreads) k_sample_stream(SampleParams P) {
     __shared__ u64 red[kSampThreads / 32];
     __shared__ u64 seg_mass[kSampThreads / 32];
     __shared__ uint32_t seg_ties[kSampThreads / 32];
@@ -194,6 +667,46 @@ __global__ void __launch_bounds__(kSampThreads) k_head_sample(SampleParams P) {
     }
 }
 
+template <int kThreads>
+int launch_team(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows, uint32_t team, bool wide) {
+    auto k = k_sample<kThreads>;
+    const uint32_t slice = ((P.n_tok + team - 1) / team + 3) & ~3u;
+    const size_t smem = sizeof(SampleShared<kThreads>) + (size_t)slice * 4;
+    BPE_CUDA(ctx, cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem), "head_sample");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n_rows * team);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = ctx->stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {team, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = team > 1 ? 1 : 0;
+    BPE_CUDA(ctx, cudaLaunchKernelEx(&cfg, k, P, team, slice, wide), "head_sample launch");
+    return BPE_OK;
+}
+
+int launch(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows) {
+    if (P.n_tok > kMaxTeam * 32768u || n_rows > 0x0FFFFFFFu) {
+        auto k = P.type == BPE_F32 ? k_sample_stream<float>
+                 : P.type == BPE_BF16 ? k_sample_stream<__nv_bfloat16> : k_sample_stream<__half>;
+        k<<<n_rows, kSampThreads, 0, ctx->stream>>>(P);
+        BPE_CUDA(ctx, cudaGetLastError(), "head_sample launch");
+        return BPE_OK;
+    }
+    const uintptr_t quad = 4 * head_type_size(P.type);
+    const bool wide = (uintptr_t)P.logits % quad == 0 && (n_rows == 1 || P.stride % 4 == 0);
+    // the smallest team whose shared memory holds the row, two CTAs an SM; more CTAs a row while the GPU has room
+    uint32_t team = 1;
+    while (team < kMaxTeam && P.n_tok > team * 16384) team *= 2;
+    while (team < kMaxTeam && (uint64_t)n_rows * team * 2 <= (uint64_t)ctx->sm_count * 2 && P.n_tok >= team * 2 * 2048) team *= 2;
+    const uint32_t each = (P.n_tok + team - 1) / team;
+    if (each <= 8192) return launch_team<256>(ctx, P, n_rows, team, wide);
+    if (each <= 16384) return launch_team<512>(ctx, P, n_rows, team, wide);
+    return launch_team<1024>(ctx, P, n_rows, team, wide);
+}
+
 }  // namespace
 }  // namespace bpe
 
@@ -211,13 +724,6 @@ extern "C" int head_sample(bpe_ctx *ctx, const void *d_logits, uint64_t stride, 
     if (n_rows > 1 && stride < n_tok) return fail(ctx, BPE_ERR_INVALID_ARG, "head_sample: the row stride is below n_tok");
     BPE_CUDA(ctx, cudaSetDevice(ctx->device), "cudaSetDevice");
     const head_filters none{1.0f, 0, 1.0f, 0.0f, nullptr, nullptr, nullptr, nullptr};
-    SampleParams P{d_logits, stride, n_tok, d_u, filters ? *filters : none, d_ids_out, d_logprob_out};
-    if (type == BPE_F32)
-        k_head_sample<float><<<n_rows, kSampThreads, 0, ctx->stream>>>(P);
-    else if (type == BPE_BF16)
-        k_head_sample<__nv_bfloat16><<<n_rows, kSampThreads, 0, ctx->stream>>>(P);
-    else
-        k_head_sample<__half><<<n_rows, kSampThreads, 0, ctx->stream>>>(P);
-    BPE_CUDA(ctx, cudaGetLastError(), "head_sample launch");
-    return BPE_OK;
+    SampleParams P{d_logits, stride, n_tok, type, d_u, filters ? *filters : none, d_ids_out, d_logprob_out};
+    return launch(ctx, P, n_rows);
 }
