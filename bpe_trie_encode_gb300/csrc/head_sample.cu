@@ -71,23 +71,43 @@ constexpr int kList = 128;                 // tokens that are ranked pair by pai
 constexpr uint32_t kLeast = 0x2B800000u;   // the bits of 2^-40: below it a weight is 0
 constexpr int kMaxTeam = 8;
 
-// w = floor(e 2^40) for 2^-40 <= e <= 1, given e's bits.
-__device__ __forceinline__ u64 weight_bits(uint32_t b) {
-    return (u64)((b & 0x7FFFFFu) | 0x800000u) << ((b >> 23) - 87) >> 23;
+constexpr int kSmallK = 256, kSmall = 512; // top-k up to kSmallK works on a list of up to kSmall tokens
+constexpr int kNear = 128;                 // buckets of 1/8 below the largest logit, for that list
+
+// w = floor(e 2^40) in two parts of 20 bits, for 0 <= e <= 1: additions that round towards zero leave the whole part
+// of e 2^20, then of its rest times 2^20, in the low bits of a float between 2^23 and 2^24.
+constexpr uint32_t kWhole = 0x4B000000u;   // 2^23
+struct Parts { uint32_t hi, lo; };
+__device__ __forceinline__ Parts parts_of(float e) {
+    const float t = __fmaf_rz(e, 0x1p20f, 0x1p23f);
+    const float l = __fmaf_rz(fmaf(e, 0x1p20f, 0x1p23f - t), 0x1p20f, 0x1p23f);
+    return {__float_as_uint(t) - kWhole, __float_as_uint(l) - kWhole};
+}
+__device__ __forceinline__ u64 join(uint32_t hi, uint32_t lo) { return ((u64)hi << 20) + lo; }
+__device__ __forceinline__ u64 weight(float e) {
+    const Parts p = parts_of(e);
+    return join(p.hi, p.lo);
 }
 
 struct __align__(16) Entry { uint32_t key, idx; u64 w; };
 
 template <int kThreads> struct SampleShared {
     static constexpr int kCopies = kThreads / 32;   // of a histogram, by thread
-    uint32_t lo[kBuckets * kCopies], hi[kBuckets * kCopies];
+    union {
+        struct { uint32_t lo[kBuckets * kCopies], hi[kBuckets * kCopies]; };
+        struct { u64 order[kSmall], heavy[kSmall]; };   // the small list, sorted: logit and id, weight
+    };
     u64 sum[2][kBuckets];                  // this CTA's histogram, read by the whole cluster
+    __align__(16) uint32_t near_n[kNear];              // threads by their largest logit
     u64 slot[2][kMaxTeam];                 // a value from each CTA of the cluster
     u64 red[32];
-    Entry list[kList];
+    union {
+        Entry list[kList];
+        u64 small[kSmall];                 // logit and id of the largest tokens
+    };
     uint32_t list_n;
     u64 pick[3];                           // bucket found, sums above and in it
-    u64 goal[2];                           // whole sum, target
+    u64 goal[2];                           // target, this CTA's sum above the bucket
     uint32_t cut[3];                       // bits, key, id of the last kept token
     float4 e[1];                           // the CTA's tokens, four at a time
 };
@@ -114,10 +134,11 @@ __device__ __forceinline__ uint32_t far_count(uint32_t *p, uint32_t rank) {
     return v;
 }
 
-__device__ __forceinline__ u64 warp_sum(u64 v) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
-    return v;
+__device__ __forceinline__ u64 warp_sum(u64 v) {   // of values below 2^63, by parts of 22 bits
+    const uint32_t a = __reduce_add_sync(kFull, (uint32_t)v & 0x3FFFFFu);
+    const uint32_t b = __reduce_add_sync(kFull, (uint32_t)(v >> 22) & 0x3FFFFFu);
+    const uint32_t c = __reduce_add_sync(kFull, (uint32_t)(v >> 44));
+    return a + ((u64)b << 22) + ((u64)c << 44);
 }
 __device__ __forceinline__ u64 warp_scan(u64 v, int lane) {   // inclusive
 #pragma unroll
@@ -142,6 +163,7 @@ struct Sampler {
     uint32_t cut_bits, cut_key, cut_idx;
 
     __device__ __forceinline__ void sync() const {
+        __syncwarp();
         if (size == 1)
             __syncthreads();
         else
@@ -154,8 +176,9 @@ struct Sampler {
     }
     __device__ __forceinline__ uint32_t key(uint32_t i) const { return key_of(logit(first + i)); }   // of the CTA's token i
     __device__ __forceinline__ float exp_of(float v) const {
-        return v == top ? 1.0f : fmaxf(expf(__fmul_rn(v - top, inv_t)), 0.0f);   // NaN, of inf * 0, as 0
+        return fmaxf(expf(__fmul_rn(v - top, inv_t)), 0.0f);   // NaN as 0; row_exp is for a largest logit of infinity
     }
+    __device__ __forceinline__ float row_exp(float v) const { return v == top ? 1.0f : exp_of(v); }
     // f(i, bits of e) for the CTA's tokens, this warp's share
     template <typename F> __device__ __forceinline__ void each(F f) const {
 #pragma unroll 2
@@ -174,23 +197,29 @@ struct Sampler {
         if (threadIdx.x < size) far_store(&S.slot[turn][rank], threadIdx.x, v);
         sync();
     }
-    __device__ __forceinline__ u64 max_row(u64 v) {
-        v = warp_max_u64(v);
+    __device__ __forceinline__ uint32_t max_row(uint32_t v) {
+        v = __reduce_max_sync(kFull, v);
         __syncthreads();
         if (lane == 0) S.red[warp] = v;
         __syncthreads();
-        exchange(warp_max_u64(lane < kWarps ? S.red[lane] : 0));
+        exchange(__reduce_max_sync(kFull, lane < kWarps ? (uint32_t)S.red[lane] : 0));
         v = 0;
-        for (uint32_t r = 0; r < size; r++) v = max(v, S.slot[turn][r]);
+        for (uint32_t r = 0; r < size; r++) v = max(v, (uint32_t)S.slot[turn][r]);
         return v;
     }
     // The row's sum; `before`, `mine`: the sums of the CTAs before this one, and this one's.  The warps' stay in S.red.
-    __device__ __forceinline__ u64 sum_row(u64 v, u64 &before, u64 &mine) {
+    __device__ __forceinline__ u64 sum_cta(u64 v) {
         v = warp_sum(v);
         __syncthreads();
         if (lane == 0) S.red[warp] = v;
         __syncthreads();
-        mine = warp_sum(lane < kWarps ? S.red[lane] : 0);
+        return warp_sum(lane < kWarps ? S.red[lane] : 0);
+    }
+    __device__ __forceinline__ u64 sum_row(u64 v, u64 &before, u64 &mine) {
+        mine = sum_cta(v);
+        return sum_ctas(mine, before);
+    }
+    __device__ __forceinline__ u64 sum_ctas(u64 mine, u64 &before) {
         exchange(mine);
         u64 total = 0;
         before = 0;
@@ -240,21 +269,53 @@ struct Sampler {
             const uint32_t x = key(i);
             if (x < cut_key || (x == cut_key && first + i > cut_idx)) return 0;
         }
-        return weight_bits(b);
+        return weight(__uint_as_float(b));
     }
-    __device__ __forceinline__ u64 mass() const {
-        u64 m = 0;
-        each([&](uint32_t i, uint32_t b) { m += kept(i, b); });
-        return m;
+    __device__ __forceinline__ u64 mass() const {   // at most 64 tokens a thread: the parts stay below 2^32
+        uint32_t hi = 0, lo = 0;
+        each([&](uint32_t i, uint32_t b) {
+            bool in = b >= cut_bits;
+            if (b == cut_bits && cut_idx != ~0u) {
+                const uint32_t x = key(i);
+                in = x > cut_key || (x == cut_key && first + i <= cut_idx);
+            }
+            if (__any_sync(__activemask(), in)) {
+                const Parts p = parts_of(in ? __uint_as_float(b) : 0.0f);
+                hi += p.hi;
+                lo += p.lo;
+            }
+        });
+        return join(hi, 0) + lo;
     }
     __device__ __forceinline__ void read_cut() { cut_bits = S.cut[0], cut_key = S.cut[1], cut_idx = S.cut[2]; }
 
+    // e of the CTA's tokens in place of their logits, f(bits) for each.
+    template <typename F> __device__ __forceinline__ void to_exp(F f) {
+        const bool inf = top == INFINITY;
+#pragma unroll 2
+        for (uint32_t q = q0 + lane; q < q1; q += 32) {
+            float4 v = S.e[q];
+            if (inf) {
+                v.x = row_exp(v.x), v.y = row_exp(v.y), v.z = row_exp(v.z), v.w = row_exp(v.w);
+            } else {
+                v.x = exp_of(v.x), v.y = exp_of(v.y), v.z = exp_of(v.z), v.w = exp_of(v.w);
+            }
+            S.e[q] = v;
+            f(__float_as_uint(v.x));
+            f(__float_as_uint(v.y));
+            f(__float_as_uint(v.z));
+            f(__float_as_uint(v.w));
+        }
+    }
+
     // The last token kept when tokens are taken in order (largest logit, then lowest id) until the sum of their
     // values -- 1, or the weight -- reaches the target: `target`, or with share >= 0 that share of the whole sum, and
-    // at least 1.  Where the whole sum is below the target, everything is kept and the cut stays.
-    template <bool kMass>
-    __device__ __forceinline__ void select(u64 target, double share) {
-        u64 above = 0;
+    // at least 1.  Where the whole sum is below the target, everything is kept and the cut stays.  kFirst: the
+    // CTA's tokens are still logits.  With kMass, *total and *mine become the row's kept sum and this CTA's, unless
+    // false is returned.
+    template <bool kMass, bool kFirst>
+    __device__ __forceinline__ bool select(u64 target, double share, u64 *total = nullptr, u64 *mine = nullptr) {
+        u64 above = 0, own = 0;
         uint32_t low = kLeast;
         int shift = 21, buckets = kBuckets;
         for (int level = 0;; level++) {
@@ -266,18 +327,21 @@ struct Sampler {
             if (threadIdx.x == 0) S.list_n = 0, S.pick[0] = ~0ull;
             __syncthreads();
             const int copy = threadIdx.x & (kCopies - 1);
-            each([&](uint32_t, uint32_t b) {
-                const uint32_t k = (b - low) >> shift;
-                if (b < low || k >= (uint32_t)buckets) return;
-                if (kMass) {   // at most 2,048 tokens a copy: neither half passes 32 bits
-                    const u64 w = weight_bits(b);
-                    atomicAdd(&S.lo[k * kCopies + copy], (uint32_t)w & 0xFFFFFu);
-                    const uint32_t h = (uint32_t)(w >> 20);
-                    if (h) atomicAdd(&S.hi[k * kCopies + copy], h);
+            auto file = [&](uint32_t b) {
+                const uint32_t k = (b - low) >> shift;   // wraps to a large number below `low`
+                if (k >= (uint32_t)buckets) return;
+                if (kMass) {   // at most 2,047 tokens a copy: neither part's sum passes 32 bits
+                    const Parts p = parts_of(__uint_as_float(b));
+                    atomicAdd(&S.lo[k * kCopies + copy], p.lo);
+                    if (p.hi) atomicAdd(&S.hi[k * kCopies + copy], p.hi);
                 } else {
                     atomicAdd(&S.lo[k * kCopies + copy], 1u);
                 }
-            });
+            };
+            if (kFirst && level == 0)
+                to_exp(file);
+            else
+                each([&](uint32_t, uint32_t b) { file(b); });
             __syncthreads();
             u64 *sum = S.sum[level & 1];
             for (int b = threadIdx.x; b < buckets; b += kThreads) {
@@ -296,13 +360,16 @@ struct Sampler {
                 constexpr int kPer = (kBuckets + 31) / 32;
                 u64 v[kPer], s = 0;
 #pragma unroll
-                for (int j = 0; j < kPer; j++) {
-                    const int b = buckets - 1 - (lane * kPer + j);
-                    v[j] = 0;
-                    if (b >= 0)
-                        for (uint32_t r = 0; r < size; r++) v[j] += far_load(sum + b, r);
-                    s += v[j];
+                for (int j = 0; j < kPer; j++) v[j] = 0;
+                for (uint32_t r = 0; r < size; r++) {
+#pragma unroll
+                    for (int j = 0; j < kPer; j++) {
+                        const int b = buckets - 1 - (lane * kPer + j);
+                        if (b >= 0) v[j] += far_load(sum + b, r);
+                    }
                 }
+#pragma unroll
+                for (int j = 0; j < kPer; j++) s += v[j];
                 u64 run = warp_scan(s, lane);
                 if (level == 0 && share >= 0.0) {
                     const double x = share * (double)__shfl_sync(kFull, run, 31);
@@ -319,20 +386,29 @@ struct Sampler {
                     run += v[j];
                 }
                 if (lane == 0) S.goal[0] = target;
+                if (kMass) {   // this CTA's part of what lies above the bucket
+                    __syncwarp();
+                    const int found = (int)S.pick[0];
+                    u64 m = 0;
+                    for (int b = found + 1 + lane; found >= 0 && b < buckets; b += 32) m += sum[b];
+                    m = warp_sum(m);
+                    if (lane == 0) S.goal[1] = m;
+                }
             }
             __syncthreads();
-            if (S.pick[0] == ~0ull) return;   // at level 0: less than the target in all
+            if (S.pick[0] == ~0ull) return false;   // at level 0: less than the target in all
             target = S.goal[0];
+            if (kMass) own += S.goal[1];
             low += (uint32_t)S.pick[0] << shift;
             above = S.pick[1];
             const uint32_t high = low + (1u << shift) - 1;
             // at most this many tokens are in the bucket
-            const u64 most = kMass ? S.pick[2] / weight_bits(low) : S.pick[2];
+            const u64 most = kMass ? S.pick[2] / weight(__uint_as_float(low)) : S.pick[2];
             if (most <= kList) {
                 each([&](uint32_t i, uint32_t b) {
                     if (b < low || b > high) return;
                     const uint32_t k = key(i);
-                    const u64 w = weight_bits(b);
+                    const u64 w = weight(__uint_as_float(b));
                     for (uint32_t r = 0; r < size; r++) {
                         const uint32_t n = far_count(&S.list_n, r);
                         asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(far_addr(&S.list[n], r)),
@@ -345,40 +421,51 @@ struct Sampler {
                 for (uint32_t i0 = 0; i0 < n; i0 += kThreads / 4) {
                     const uint32_t i = min(i0 + threadIdx.x / 4, n - 1);
                     const Entry x = S.list[i];
-                    u64 run = 0;
+                    u64 run = 0, here = 0;
                     for (uint32_t j = lane & 3; j < n; j += 4) {
                         const Entry y = S.list[j];
-                        if (y.key > x.key || (y.key == x.key && y.idx < x.idx)) run += kMass ? y.w : 1;
+                        const bool before = y.key > x.key || (y.key == x.key && y.idx < x.idx);
+                        if (before) run += kMass ? y.w : 1;
+                        if (kMass && (before || j == i) && y.idx - first < quads * 4) here += y.w;
                     }
                     run += __shfl_xor_sync(kFull, run, 1);
                     run += __shfl_xor_sync(kFull, run, 2);
                     run += above;
-                    if (run < target && target <= run + (kMass ? x.w : 1)) {
-                        S.cut[0] = __float_as_uint(exp_of(key_value(x.key)));
+                    if (kMass) {
+                        here += __shfl_xor_sync(kFull, here, 1);
+                        here += __shfl_xor_sync(kFull, here, 2);
+                    }
+                    const u64 upto = run + (kMass ? x.w : 1);
+                    if (run < target && target <= upto) {
+                        S.cut[0] = __float_as_uint(row_exp(key_value(x.key)));
                         S.cut[1] = x.key;
                         S.cut[2] = x.idx;
+                        S.pick[0] = upto;
+                        S.pick[1] = own + here;
                     }
                 }
                 __syncthreads();
-                return;
+                if (kMass && total) *total = S.pick[0], *mine = S.pick[1];
+                return true;
             }
             if (shift == 0) break;   // over kList tokens with the same e
+            __syncthreads();         // what was found has been read by all
             buckets = 128;
             shift -= 7;
-            sync();                  // the row's sums are read before they are written again
         }
         // tokens of one e: `need` of them, by logit, then by id
-        const u64 w = kMass ? weight_bits(low) : 1;
-        u64 need = (target - above + w - 1) / w, big = 0, small = 0;
+        const u64 w = kMass ? weight(__uint_as_float(low)) : 1;
+        u64 need = (target - above + w - 1) / w;
+        uint32_t big = 0, small = 0;
         each([&](uint32_t i, uint32_t b) {
             if (b != low) return;
             const uint32_t k = key(i);
-            big = max(big, (u64)k);
-            small = max(small, (u64)(uint32_t)~k);
+            big = max(big, k);
+            small = max(small, ~k);
         });
         big = max_row(big);
-        small = (uint32_t)~(uint32_t)max_row(small);
-        uint32_t at = (uint32_t)small;
+        small = ~max_row(small);
+        uint32_t at = small;
         if (big != small) {          // logits that differ by less than e can tell
             at = 0;
             for (int bit = 31; bit >= 0; bit--) {
@@ -392,14 +479,130 @@ struct Sampler {
             need -= sum_row(m);
         }
         auto one = [&](uint32_t i, uint32_t b) -> u64 { return b == low && key(i) == at; };
-        u64 m = 0, before, mine;
+        u64 m = 0, before, part;
         each([&](uint32_t i, uint32_t b) { m += one(i, b); });
-        sum_row(m, before, mine);
-        locate(one, need - 1, before, mine, [&](uint32_t i) {
+        sum_row(m, before, part);
+        locate(one, need - 1, before, part, [&](uint32_t i) {
             for (uint32_t r = 0; r < size; r++) far_store(&S.cut[2], r, first + i);
         });
         if (threadIdx.x == 0) S.cut[0] = low, S.cut[1] = at;
         sync();
+        return false;
+    }
+
+    // top-k up to kSmallK, with what follows it, on a list: the k-th largest of the threads' largest logits is a
+    // lower bound of the k-th largest logit, and few tokens lie above it.  Only they need an exponential.  Returns
+    // false, with nothing done, where the list would not do.
+    __device__ __forceinline__ bool small_list(float big, uint32_t k, float p, u64 least, uint32_t row) {
+        const float scale = inv_t * 8.0f;
+        auto near = [&](float v) { return __fmul_rn(top - v, scale); };   // grows as v falls
+        for (int i = threadIdx.x; i < kNear; i += kThreads) S.near_n[i] = 0;
+        if (threadIdx.x == 0) S.list_n = 0;
+        __syncthreads();
+        const float x = near(big);
+        if (x < (float)kNear) atomicAdd(&S.near_n[(int)x], 1u);
+        sync();
+        if (warp == 0) {
+            uint32_t v[kNear / 32], s = 0;
+#pragma unroll
+            for (int j = 0; j < kNear / 32; j++) v[j] = 0;
+            for (uint32_t r = 0; r < size; r++) {
+                uint4 c;
+                asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(c.x), "=r"(c.y), "=r"(c.z), "=r"(c.w)
+                             : "r"(far_addr(S.near_n + lane * 4, r)) : "memory");
+                v[0] += c.x, v[1] += c.y, v[2] += c.z, v[3] += c.w;
+            }
+            s = v[0] + v[1] + v[2] + v[3];
+            uint32_t run = warp_incl_sum(s, lane) - s, edge = ~0u;
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                if (run < k && k <= run + v[j]) edge = lane * 4 + j + 1;
+                run += v[j];
+            }
+            edge = __reduce_min_sync(kFull, edge);
+            if (lane == 0) S.pick[0] = edge;
+        }
+        __syncthreads();
+        if ((uint32_t)S.pick[0] == ~0u) return false;
+        const float edge = (float)(uint32_t)S.pick[0];
+        each([&](uint32_t i, uint32_t b) {
+            if (near(__uint_as_float(b)) < edge) {
+                const uint32_t n = far_count(&S.list_n, 0);
+                if (n < kSmall)
+                    far_store(&S.small[n], 0, (u64)key_of(__uint_as_float(b)) << 32 | (uint32_t)~(first + i));
+            }
+        });
+        sync();
+        uint32_t n = S.list_n;
+        if (size > 1) {
+            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(n) : "r"(far_addr(&S.list_n, 0)) : "memory");
+        }
+        if (n > kSmall) {
+            sync();   // before list_n is cleared
+            return false;
+        }
+        if (size > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        if (rank == 0) {
+            // sorted: a token's place is the number of larger ones
+            for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+                const u64 x = S.small[i];
+                uint32_t place = 0;
+#pragma unroll 4
+                for (uint32_t j = 0; j < n; j++) place += S.small[j] > x;
+                if (place < k) {
+                    S.order[place] = x;
+                    S.heavy[place] = weight(row_exp(key_value((uint32_t)(x >> 32))));
+                }
+            }
+            __syncthreads();
+            n = min(n, k);
+            if (warp == 0) {   // 8 tokens a lane
+                constexpr int kPer = kSmallK / 32;
+                u64 w[kPer], s = 0;
+#pragma unroll
+                for (int j = 0; j < kPer; j++) {
+                    w[j] = (uint32_t)(lane * kPer + j) < n ? S.heavy[lane * kPer + j] : 0;
+                    s += w[j];
+                }
+                const u64 upto = warp_scan(s, lane);
+                u64 edge = ~0ull;
+                if (p < 1.0f) {
+                    const double x = (double)p * (double)__shfl_sync(kFull, upto, 31);
+                    edge = x > 1.0 ? (u64)x : 1;
+                }
+                u64 run = upto - s, total = 0;
+                uint32_t keep = 0;
+#pragma unroll
+                for (int j = 0; j < kPer; j++) {
+                    if (w[j] > 0 && run < edge && w[j] >= least) keep++, total += w[j];
+                    run += w[j];
+                }
+                keep = __reduce_add_sync(kFull, keep);
+                total = warp_sum(total);
+                if (lane == 0) S.pick[1] = keep, S.pick[2] = total;
+            }
+            __syncthreads();
+            const uint32_t keep = (uint32_t)S.pick[1];
+            const u64 total = S.pick[2];
+            const double y = (double)P.u[row] * (double)total;
+            u64 t = y > 0.0 ? (u64)y : 0;
+            if (t > total - 1) t = total - 1;
+            for (uint32_t i = threadIdx.x; i < keep; i += kThreads) {
+                const uint32_t mine = (uint32_t)S.order[i];   // ~id
+                u64 run = 0;
+#pragma unroll 4
+                for (uint32_t j = 0; j < keep; j++) run += (uint32_t)S.order[j] > mine ? S.heavy[j] : 0;
+                if (run <= t && t < run + S.heavy[i]) answer(row, ~mine, total);
+            }
+        }
+        __syncwarp();
+        if (size > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        return true;
+    }
+
+    __device__ __forceinline__ void answer(uint32_t row, uint32_t id, u64 total) const {
+        P.ids[row] = (int32_t)id;
+        if (P.logprob) P.logprob[row] = (float)((double)z_of(logit(id), top, inv_t) - log((double)total * 0x1p-40));
     }
 };
 
@@ -438,6 +641,17 @@ __device__ __forceinline__ float load_row(const T *l, uint32_t count, bool wide,
     return big;
 }
 
+// The draw: the token at which the kept running mass passes floor(u W).
+template <int kThreads>
+__device__ __forceinline__ void draw(Sampler<kThreads> &A, uint32_t row, u64 total, u64 before, u64 mine) {
+    const double x = (double)A.P.u[row] * (double)total;
+    u64 t = x > 0.0 ? (u64)x : 0;
+    if (t > total - 1) t = total - 1;
+    A.locate([&](uint32_t i, uint32_t b) { return A.kept(i, b); }, t, before, mine,
+             [&](uint32_t i) { A.answer(row, A.first + i, total); });
+    A.sync();   // no CTA ends while another may read its shared memory
+}
+
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
@@ -456,7 +670,7 @@ k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
     Sampler<kThreads> A{S, P, (const uint8_t *)P.logits + row * P.stride * (P.type == BPE_F32 ? 4 : 2), rank, team, first,
                         quads, min(quads, warp * seg), min(quads, (warp + 1) * seg), lane, warp, 0};
     if (team > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    const uint32_t kmax = (uint32_t)A.max_row(key_of(big));
+    const uint32_t kmax = A.max_row(key_of(big));
     if (kmax == kKeyNegInf) {
         if (rank == 0 && threadIdx.x == 0) {
             P.ids[row] = -1;
@@ -468,13 +682,13 @@ k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
     A.top = key_value(kmax);
     const float temp = P.f.d_temperature ? P.f.d_temperature[row] : P.f.temperature;
     if (!(temp >= kMinScale)) {   // the lowest id of the largest logit
-        u64 low = 0;
+        uint32_t low = 0;
         A.each([&](uint32_t i, uint32_t b) {
-            if (__uint_as_float(b) == A.top && i < count) low = max(low, (u64)(uint32_t)~(first + i));
+            if (__uint_as_float(b) == A.top && i < count) low = max(low, ~(first + i));
         });
         low = A.max_row(low);
         if (rank == 0 && threadIdx.x == 0) {
-            P.ids[row] = (int32_t)~(uint32_t)low;
+            P.ids[row] = (int32_t)~low;
             if (P.logprob) P.logprob[row] = 0.0f;
         }
         A.sync();
@@ -483,43 +697,53 @@ k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
     const int32_t k = P.f.d_top_k ? P.f.d_top_k[row] : P.f.top_k;
     const float p = P.f.d_top_p ? P.f.d_top_p[row] : P.f.top_p;
     const float q = P.f.d_min_p ? P.f.d_min_p[row] : P.f.min_p;
+    const u64 least = q > 0.0f ? (u64)(fminf(q, 1.0f) * kOne) : 0;
     A.inv_t = 1.0f / temp;
-#pragma unroll 2
-    for (uint32_t i = A.q0 + lane; i < A.q1; i += 32) {
-        float4 v = S.e[i];
-        v.x = A.exp_of(v.x), v.y = A.exp_of(v.y), v.z = A.exp_of(v.z), v.w = A.exp_of(v.w);
-        S.e[i] = v;
-    }
-    if (threadIdx.x == 0) S.cut[0] = kLeast, S.cut[1] = 0, S.cut[2] = ~0u;   // keep every weight above 0
-    __syncthreads();
     const bool by_count = k >= 1 && (uint32_t)k < P.n_tok;
-    if (by_count) A.template select<false>((u64)k, -1.0);
-    if (p < 1.0f) {
-        u64 target = 0;
-        if (by_count) {
+    if (by_count && k <= kSmallK && A.top < INFINITY && A.small_list(big, (uint32_t)k, p, least, row)) return;
+    if (threadIdx.x == 0) S.cut[0] = kLeast, S.cut[1] = 0, S.cut[2] = ~0u;   // keep every weight above 0
+    u64 total = 0, mine = 0, before;
+    bool summed = false;
+    if (by_count) {
+        A.template select<false, true>((u64)k, -1.0);
+        if (p < 1.0f) {
             A.read_cut();
-            const double x = (double)p * (double)A.sum_row(A.mass());
-            target = x > 1.0 ? (u64)x : 1;
+            const double x = (double)p * (double)A.sum_row(A.mass(), before, mine);
+            A.template select<true, false>(x > 1.0 ? (u64)x : 1, -1.0);
         }
-        A.template select<true>(target, by_count ? -1.0 : p > 0.0f ? (double)p : 0.0);
+    } else if (p < 1.0f) {
+        summed = A.template select<true, true>(0, p > 0.0f ? (double)p : 0.0, &total, &mine);
+    } else {
+        uint32_t hi = 0, lo = 0;
+        A.to_exp([&](uint32_t b) {
+            const Parts w = parts_of(__uint_as_float(b));
+            hi += w.hi;
+            lo += w.lo;
+        });
+        if (!least) {
+            total = A.sum_row(join(hi, 0) + lo, before, mine);
+            A.read_cut();
+            draw(A, row, total, before, mine);
+            return;
+        }
+        __syncthreads();
     }
     A.read_cut();
-    if (q > 0.0f) {
+    if (least) {
         // w >= floor(q 2^40), a multiple of 2^-40 with at most 24 digits: compare e's bits
-        const uint32_t least = __float_as_uint((float)(u64)(fminf(q, 1.0f) * kOne) * 0x1p-40f);
-        if (least > A.cut_bits) A.cut_bits = least, A.cut_idx = ~0u;
+        const uint32_t bits = __float_as_uint((float)least * 0x1p-40f);
+        if (bits > A.cut_bits) A.cut_bits = bits, A.cut_idx = ~0u, summed = false;
     }
-    u64 before, mine;
-    const u64 total = A.sum_row(A.mass(), before, mine);
-    const double x = (double)P.u[row] * (double)total;
-    u64 t = x > 0.0 ? (u64)x : 0;
-    if (t > total - 1) t = total - 1;
-    A.locate([&](uint32_t i, uint32_t b) { return A.kept(i, b); }, t, before, mine, [&](uint32_t i) {
-        P.ids[row] = (int32_t)(first + i);
-        if (P.logprob)
-            P.logprob[row] = (float)((double)z_of(A.logit(first + i), A.top, A.inv_t) - log((double)total * 0x1p-40));
-    });
-    A.sync();   // no CTA ends while another may read its shared memory
+    if (summed) {
+        A.sum_ctas(mine, before);
+        const double x = (double)P.u[row] * (double)total;
+        u64 t = x > 0.0 ? (u64)x : 0;
+        if (t > total - 1) t = total - 1;
+        if (t >= before && t - before < mine) A.sum_cta(A.mass());   // the warps' sums, where the draw needs them
+    } else {
+        total = A.sum_row(A.mass(), before, mine);
+    }
+    draw(A, row, total, before, mine);
 }
 
 // Vocabularies beyond a cluster's shared memory (over 262,144 tokens): one CTA per
@@ -699,11 +923,12 @@ int launch(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows) {
     const bool wide = (uintptr_t)P.logits % quad == 0 && (n_rows == 1 || P.stride % 4 == 0);
     // the smallest team whose shared memory holds the row, two CTAs an SM; more CTAs a row while the GPU has room
     uint32_t team = 1;
-    while (team < kMaxTeam && P.n_tok > team * 16384) team *= 2;
+    while (team < kMaxTeam && P.n_tok > team * 20480) team *= 2;
     while (team < kMaxTeam && (uint64_t)n_rows * team * 2 <= (uint64_t)ctx->sm_count * 2 && P.n_tok >= team * 2 * 2048) team *= 2;
     const uint32_t each = (P.n_tok + team - 1) / team;
-    if (each <= 8192) return launch_team<256>(ctx, P, n_rows, team, wide);
-    if (each <= 16384) return launch_team<512>(ctx, P, n_rows, team, wide);
+    if (each <= 5120) return launch_team<128>(ctx, P, n_rows, team, wide);
+    if (each <= 10240) return launch_team<256>(ctx, P, n_rows, team, wide);
+    if (each <= 20480) return launch_team<512>(ctx, P, n_rows, team, wide);
     return launch_team<1024>(ctx, P, n_rows, team, wide);
 }
 
