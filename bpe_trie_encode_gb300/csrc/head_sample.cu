@@ -70,7 +70,6 @@ constexpr int kBuckets = 161;              // 4 per octave from 2^-40 to 1
 constexpr int kList = 128;                 // tokens that are ranked pair by pair
 constexpr uint32_t kLeast = 0x2B800000u;   // the bits of 2^-40: below it a weight is 0
 constexpr int kMaxTeam = 8;
-
 constexpr int kSmallK = 256, kSmall = 512; // top-k up to kSmallK works on a list of up to kSmall tokens
 constexpr int kNear = 128;                 // buckets of 1/8 below the largest logit, for that list
 
@@ -92,22 +91,19 @@ __device__ __forceinline__ u64 weight(float e) {
 struct __align__(16) Entry { uint32_t key, idx; u64 w; };
 
 template <int kThreads> struct SampleShared {
-    static constexpr int kCopies = kThreads / 32;   // of a histogram, by thread
-    union {
-        struct { uint32_t lo[kBuckets * kCopies], hi[kBuckets * kCopies]; };
-        struct { u64 order[kSmall], heavy[kSmall]; };   // the small list, sorted: logit and id, weight
-    };
-    u64 sum[2][kBuckets];                  // this CTA's histogram, read by the whole cluster
-    __align__(16) uint32_t near_n[kNear];              // threads by their largest logit
+    static constexpr int kCopies = kThreads < 512 ? kThreads / 32 : 16;   // of a histogram, by thread
+    uint32_t lo[kBuckets * kCopies], hi[kBuckets * kCopies];
+    u64 sum[2][kBuckets + 1];              // this CTA's histogram, read by the whole cluster
+    u64 all[kBuckets + 1];                 // the row's
+    uint32_t near_n[kNear];                // threads by their largest logit
     u64 slot[2][kMaxTeam];                 // a value from each CTA of the cluster
     u64 red[32];
-    union {
-        Entry list[kList];
-        u64 small[kSmall];                 // logit and id of the largest tokens
-    };
-    uint32_t list_n;
-    u64 pick[3];                           // bucket found, sums above and in it
-    u64 goal[2];                           // target, this CTA's sum above the bucket
+    Entry mine[kList];                     // tokens of the last bucket: this CTA's, read by the whole cluster
+    Entry list[kList];                     // and the row's
+    u64 small[kSmall];                     // logit and id of the largest tokens: this CTA's, read by the first CTA
+    uint32_t list_n, small_n;
+    u64 pick[4];                           // bucket found, sums above and in it, this CTA's sum above it
+    u64 goal;
     uint32_t cut[3];                       // bits, key, id of the last kept token
     float4 e[1];                           // the CTA's tokens, four at a time
 };
@@ -128,9 +124,15 @@ __device__ __forceinline__ u64 far_load(const u64 *p, uint32_t rank) {
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(far_addr(p, rank)) : "memory");
     return v;
 }
-__device__ __forceinline__ uint32_t far_count(uint32_t *p, uint32_t rank) {
+__device__ __forceinline__ uint32_t far_load(const uint32_t *p, uint32_t rank) {
     uint32_t v;
-    asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(v) : "r"(far_addr(p, rank)) : "memory");
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(far_addr(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 far_load(const Entry *p, uint32_t rank) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(far_addr(p, rank)) : "memory");
     return v;
 }
 
@@ -157,7 +159,7 @@ struct Sampler {
     const uint8_t *l;       // the row
     uint32_t rank, size;    // this CTA among the row's
     uint32_t first, quads;  // its tokens begin here; groups of four
-    uint32_t q0, q1;        // the groups of this warp, contiguous
+    uint32_t span, q0, q1;  // a thread's groups: contiguous, an odd number, so that a warp's loads meet no bank twice
     int lane, warp, turn;
     float top, inv_t;
     uint32_t cut_bits, cut_key, cut_idx;
@@ -179,15 +181,33 @@ struct Sampler {
         return fmaxf(expf(__fmul_rn(v - top, inv_t)), 0.0f);   // NaN as 0; row_exp is for a largest logit of infinity
     }
     __device__ __forceinline__ float row_exp(float v) const { return v == top ? 1.0f : exp_of(v); }
-    // f(i, bits of e) for the CTA's tokens, this warp's share
+    // f(i, bits of e) for this thread's tokens
     template <typename F> __device__ __forceinline__ void each(F f) const {
 #pragma unroll 2
-        for (uint32_t q = q0 + lane; q < q1; q += 32) {
+        for (uint32_t q = q0; q < q1; q++) {
             const float4 v = S.e[q];
             f(q * 4, __float_as_uint(v.x));
             f(q * 4 + 1, __float_as_uint(v.y));
             f(q * 4 + 2, __float_as_uint(v.z));
             f(q * 4 + 3, __float_as_uint(v.w));
+        }
+    }
+    // e of this thread's tokens in place of their logits, f(bits) for each
+    template <typename F> __device__ __forceinline__ void to_exp(F f) {
+        const bool inf = top == INFINITY;
+#pragma unroll 2
+        for (uint32_t q = q0; q < q1; q++) {
+            float4 v = S.e[q];
+            if (inf) {
+                v.x = row_exp(v.x), v.y = row_exp(v.y), v.z = row_exp(v.z), v.w = row_exp(v.w);
+            } else {
+                v.x = exp_of(v.x), v.y = exp_of(v.y), v.z = exp_of(v.z), v.w = exp_of(v.w);
+            }
+            S.e[q] = v;
+            f(__float_as_uint(v.x));
+            f(__float_as_uint(v.y));
+            f(__float_as_uint(v.z));
+            f(__float_as_uint(v.w));
         }
     }
 
@@ -207,7 +227,7 @@ struct Sampler {
         for (uint32_t r = 0; r < size; r++) v = max(v, (uint32_t)S.slot[turn][r]);
         return v;
     }
-    // The row's sum; `before`, `mine`: the sums of the CTAs before this one, and this one's.  The warps' stay in S.red.
+    // The CTA's sum; the warps' stay in S.red.
     __device__ __forceinline__ u64 sum_cta(u64 v) {
         v = warp_sum(v);
         __syncthreads();
@@ -215,10 +235,7 @@ struct Sampler {
         __syncthreads();
         return warp_sum(lane < kWarps ? S.red[lane] : 0);
     }
-    __device__ __forceinline__ u64 sum_row(u64 v, u64 &before, u64 &mine) {
-        mine = sum_cta(v);
-        return sum_ctas(mine, before);
-    }
+    // The row's sum of the CTAs' sums; `before`: of the CTAs before this one.
     __device__ __forceinline__ u64 sum_ctas(u64 mine, u64 &before) {
         exchange(mine);
         u64 total = 0;
@@ -231,56 +248,47 @@ struct Sampler {
         return total;
     }
     __device__ __forceinline__ u64 sum_row(u64 v) {
-        u64 a, b;
-        return sum_row(v, a, b);
+        u64 before;
+        return sum_ctas(sum_cta(v), before);
     }
 
     // The token, in order of ids, at which the running sum of value(i, bits) passes t; the lane that holds it calls
-    // found(i).  Follows sum_row over the same values.
+    // found(i).  own: this thread's sum; S.red holds the warps', `mine` is the CTA's, `before` the CTAs' before it.
     template <typename V, typename F>
-    __device__ __forceinline__ void locate(V value, u64 t, u64 before, u64 mine, F found) {
+    __device__ __forceinline__ void locate(V value, u64 own, u64 t, u64 before, u64 mine, F found) {
         if (t < before || t - before >= mine) return;
         t -= before;
-        const u64 own = lane < kWarps ? S.red[lane] : 0, run = warp_scan(own, lane);
+        const u64 w = lane < kWarps ? S.red[lane] : 0, run = warp_scan(w, lane);
         if (__ffs(__ballot_sync(kFull, run > t)) - 1 != warp) return;
-        t -= __shfl_sync(kFull, run - own, warp);
-        for (uint32_t q = q0; q < q1; q += 32) {
-            const float4 v = q + lane < q1 ? S.e[q + lane] : make_float4(0, 0, 0, 0);
-            const uint32_t i = (q + lane) * 4;
-            const u64 a = value(i, __float_as_uint(v.x)), b = value(i + 1, __float_as_uint(v.y));
-            const u64 c = value(i + 2, __float_as_uint(v.z)), d = value(i + 3, __float_as_uint(v.w));
-            const u64 s = a + b + c + d, upto = warp_scan(s, lane);
-            const unsigned past = __ballot_sync(kFull, upto > t);
+        t -= __shfl_sync(kFull, run - w, warp);
+        const u64 upto = warp_scan(own, lane);
+        const int who = __ffs(__ballot_sync(kFull, upto > t)) - 1;
+        t -= __shfl_sync(kFull, upto - own, who);
+        const uint32_t i0 = __shfl_sync(kFull, q0, who) * 4, i1 = __shfl_sync(kFull, q1, who) * 4;
+        for (uint32_t i = i0 + lane; i - lane < i1; i += 32) {   // the thread's tokens, a lane each
+            const u64 v = i < i1 ? value(i, __float_as_uint(((const float *)S.e)[i])) : 0, s = warp_scan(v, lane);
+            const unsigned past = __ballot_sync(kFull, s > t);
             if (past) {
-                if (lane == __ffs(past) - 1) {
-                    const u64 r = t - (upto - s);
-                    found(r < a ? i : r < a + b ? i + 1 : r < a + b + c ? i + 2 : i + 3);
-                }
+                if (lane == __ffs(past) - 1) found(i);
                 return;
             }
-            t -= __shfl_sync(kFull, upto, 31);
+            t -= __shfl_sync(kFull, s, 31);
         }
     }
 
-    // The weight of token i if it is kept under the cut.
-    __device__ __forceinline__ u64 kept(uint32_t i, uint32_t b) const {
-        if (b < cut_bits) return 0;
+    // Whether token i is kept under the cut.
+    __device__ __forceinline__ bool in_cut(uint32_t i, uint32_t b) const {
         if (b == cut_bits && cut_idx != ~0u) {
             const uint32_t x = key(i);
-            if (x < cut_key || (x == cut_key && first + i > cut_idx)) return 0;
+            return x > cut_key || (x == cut_key && first + i <= cut_idx);
         }
-        return weight(__uint_as_float(b));
+        return b >= cut_bits;
     }
-    __device__ __forceinline__ u64 mass() const {   // at most 64 tokens a thread: the parts stay below 2^32
+    __device__ __forceinline__ u64 mass() const {   // at most 68 tokens a thread: the parts stay below 2^32
         uint32_t hi = 0, lo = 0;
         each([&](uint32_t i, uint32_t b) {
-            bool in = b >= cut_bits;
-            if (b == cut_bits && cut_idx != ~0u) {
-                const uint32_t x = key(i);
-                in = x > cut_key || (x == cut_key && first + i <= cut_idx);
-            }
-            if (__any_sync(__activemask(), in)) {
-                const Parts p = parts_of(in ? __uint_as_float(b) : 0.0f);
+            if (in_cut(i, b)) {
+                const Parts p = parts_of(__uint_as_float(b));
                 hi += p.hi;
                 lo += p.lo;
             }
@@ -289,30 +297,11 @@ struct Sampler {
     }
     __device__ __forceinline__ void read_cut() { cut_bits = S.cut[0], cut_key = S.cut[1], cut_idx = S.cut[2]; }
 
-    // e of the CTA's tokens in place of their logits, f(bits) for each.
-    template <typename F> __device__ __forceinline__ void to_exp(F f) {
-        const bool inf = top == INFINITY;
-#pragma unroll 2
-        for (uint32_t q = q0 + lane; q < q1; q += 32) {
-            float4 v = S.e[q];
-            if (inf) {
-                v.x = row_exp(v.x), v.y = row_exp(v.y), v.z = row_exp(v.z), v.w = row_exp(v.w);
-            } else {
-                v.x = exp_of(v.x), v.y = exp_of(v.y), v.z = exp_of(v.z), v.w = exp_of(v.w);
-            }
-            S.e[q] = v;
-            f(__float_as_uint(v.x));
-            f(__float_as_uint(v.y));
-            f(__float_as_uint(v.z));
-            f(__float_as_uint(v.w));
-        }
-    }
-
     // The last token kept when tokens are taken in order (largest logit, then lowest id) until the sum of their
     // values -- 1, or the weight -- reaches the target: `target`, or with share >= 0 that share of the whole sum, and
     // at least 1.  Where the whole sum is below the target, everything is kept and the cut stays.  kFirst: the
-    // CTA's tokens are still logits.  With kMass, *total and *mine become the row's kept sum and this CTA's, unless
-    // false is returned.
+    // CTA's tokens are still logits, and the histogram is clear.  With kMass, *total and *mine become the row's
+    // kept sum and this CTA's, unless false is returned.
     template <bool kMass, bool kFirst>
     __device__ __forceinline__ bool select(u64 target, double share, u64 *total = nullptr, u64 *mine = nullptr) {
         u64 above = 0, own = 0;
@@ -320,22 +309,25 @@ struct Sampler {
         int shift = 21, buckets = kBuckets;
         for (int level = 0;; level++) {
             // histogram of [low, low + (buckets << shift))
-            for (int i = threadIdx.x; i < buckets * kCopies; i += kThreads) {
-                S.lo[i] = 0;
-                if (kMass) S.hi[i] = 0;
+            if (!kFirst || level > 0) {
+                for (int i = threadIdx.x; i < buckets * kCopies; i += kThreads) {
+                    S.lo[i] = 0;
+                    if (kMass) S.hi[i] = 0;
+                }
             }
             if (threadIdx.x == 0) S.list_n = 0, S.pick[0] = ~0ull;
             __syncthreads();
             const int copy = threadIdx.x & (kCopies - 1);
             auto file = [&](uint32_t b) {
                 const uint32_t k = (b - low) >> shift;   // wraps to a large number below `low`
-                if (k >= (uint32_t)buckets) return;
-                if (kMass) {   // at most 2,047 tokens a copy: neither part's sum passes 32 bits
-                    const Parts p = parts_of(__uint_as_float(b));
-                    atomicAdd(&S.lo[k * kCopies + copy], p.lo);
-                    if (p.hi) atomicAdd(&S.hi[k * kCopies + copy], p.hi);
-                } else {
-                    atomicAdd(&S.lo[k * kCopies + copy], 1u);
+                if (k < (uint32_t)buckets) {
+                    if (kMass) {   // at most 4,095 tokens a copy: neither part's sum passes 32 bits
+                        const Parts p = parts_of(__uint_as_float(b));
+                        atomicAdd(&S.lo[k * kCopies + copy], p.lo);
+                        if (p.hi) atomicAdd(&S.hi[k * kCopies + copy], p.hi);
+                    } else {
+                        atomicAdd(&S.lo[k * kCopies + copy], 1u);
+                    }
                 }
             };
             if (kFirst && level == 0)
@@ -344,33 +336,41 @@ struct Sampler {
                 each([&](uint32_t, uint32_t b) { file(b); });
             __syncthreads();
             u64 *sum = S.sum[level & 1];
-            for (int b = threadIdx.x; b < buckets; b += kThreads) {
-                u64 lo = 0, hi = 0;
+            for (int i = threadIdx.x; i < buckets * 4; i += kThreads) {   // four lanes a bucket
+                const int b = i >> 2;
+                uint32_t lo0 = 0, hi0 = 0;
+                u64 v = 0;
 #pragma unroll
-                for (int c = 0; c < kCopies; c++) {
-                    const int a = b * kCopies + ((c + b) & (kCopies - 1));
-                    lo += S.lo[a];
-                    if (kMass) hi += S.hi[a];
+                for (int c = 0; c < kCopies / 4; c++) {
+                    const int a = b * kCopies + (((i & 3) + c * 4 + b * 4) & (kCopies - 1));
+                    lo0 = S.lo[a];
+                    if (kMass) hi0 = S.hi[a];
+                    v += join(hi0, lo0);
                 }
-                sum[b] = lo + (hi << 20);
+                const unsigned with = __activemask();
+                v += __shfl_xor_sync(with, v, 1);
+                v += __shfl_xor_sync(with, v, 2);
+                if ((i & 3) == 0) sum[b] = v;
             }
             sync();
-            // the row's histogram, largest first, and the bucket at which the running sum reaches the target
+            for (int b = threadIdx.x; b < buckets; b += kThreads) {
+                u64 v = 0;
+                for (uint32_t r = 0; r < size; r++) v += far_load(sum + b, r);
+                S.all[b] = v;
+            }
+            __syncthreads();
+            // largest first, the bucket at which the running sum reaches the target
             if (warp == 0) {
                 constexpr int kPer = (kBuckets + 31) / 32;
-                u64 v[kPer], s = 0;
+                u64 v[kPer], s = 0, m = 0;
 #pragma unroll
-                for (int j = 0; j < kPer; j++) v[j] = 0;
-                for (uint32_t r = 0; r < size; r++) {
-#pragma unroll
-                    for (int j = 0; j < kPer; j++) {
-                        const int b = buckets - 1 - (lane * kPer + j);
-                        if (b >= 0) v[j] += far_load(sum + b, r);
-                    }
+                for (int j = 0; j < kPer; j++) {
+                    const int b = buckets - 1 - (lane * kPer + j);
+                    v[j] = b >= 0 ? S.all[b] : 0;
+                    s += v[j];
+                    if (kMass && b >= 0) m += sum[b];
                 }
-#pragma unroll
-                for (int j = 0; j < kPer; j++) s += v[j];
-                u64 run = warp_scan(s, lane);
+                u64 run = warp_scan(s, lane), part = kMass ? warp_scan(m, lane) - m : 0;
                 if (level == 0 && share >= 0.0) {
                     const double x = share * (double)__shfl_sync(kFull, run, 31);
                     target = x > 1.0 ? (u64)x : 1;
@@ -378,49 +378,46 @@ struct Sampler {
                 run = above + run - s;
 #pragma unroll
                 for (int j = 0; j < kPer; j++) {
+                    const int b = buckets - 1 - (lane * kPer + j);
                     if (run < target && target <= run + v[j]) {
-                        S.pick[0] = buckets - 1 - (lane * kPer + j);
+                        S.pick[0] = b;
                         S.pick[1] = run;
                         S.pick[2] = v[j];
+                        S.pick[3] = part;
                     }
                     run += v[j];
+                    if (kMass && b >= 0) part += sum[b];
                 }
-                if (lane == 0) S.goal[0] = target;
-                if (kMass) {   // this CTA's part of what lies above the bucket
-                    __syncwarp();
-                    const int found = (int)S.pick[0];
-                    u64 m = 0;
-                    for (int b = found + 1 + lane; found >= 0 && b < buckets; b += 32) m += sum[b];
-                    m = warp_sum(m);
-                    if (lane == 0) S.goal[1] = m;
-                }
+                if (lane == 0) S.goal = target;
             }
             __syncthreads();
             if (S.pick[0] == ~0ull) return false;   // at level 0: less than the target in all
-            target = S.goal[0];
-            if (kMass) own += S.goal[1];
+            target = S.goal;
             low += (uint32_t)S.pick[0] << shift;
             above = S.pick[1];
+            own += S.pick[3];
             const uint32_t high = low + (1u << shift) - 1;
-            // at most this many tokens are in the bucket
-            const u64 most = kMass ? S.pick[2] / weight(__uint_as_float(low)) : S.pick[2];
-            if (most <= kList) {
+            // the bucket's tokens are few when even its smallest weight, kList times, makes more than its sum
+            if (S.pick[2] <= kList * (kMass ? weight(__uint_as_float(low)) : 1)) {
                 each([&](uint32_t i, uint32_t b) {
-                    if (b < low || b > high) return;
-                    const uint32_t k = key(i);
-                    const u64 w = weight(__uint_as_float(b));
-                    for (uint32_t r = 0; r < size; r++) {
-                        const uint32_t n = far_count(&S.list_n, r);
-                        asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(far_addr(&S.list[n], r)),
-                                     "r"(k), "r"(first + i), "r"((uint32_t)w), "r"((uint32_t)(w >> 32)) : "memory");
+                    if (b >= low && b <= high) {
+                        const uint32_t n = atomicAdd(&S.list_n, 1u);
+                        S.mine[n] = Entry{key(i), first + i, weight(__uint_as_float(b))};
                     }
                 });
                 sync();
-                const uint32_t n = S.list_n;
+                // every CTA's to one list
+                uint32_t n = 0;
+                for (uint32_t r = 0; r < size; r++) {
+                    const uint32_t c = size == 1 ? S.list_n : far_load(&S.list_n, r);
+                    for (uint32_t i = threadIdx.x; i < c; i += kThreads)
+                        *reinterpret_cast<uint4 *>(&S.list[n + i]) = far_load(&S.mine[i], r);
+                    n += c;
+                }
+                __syncthreads();
                 // four lanes a token add up what comes before it
-                for (uint32_t i0 = 0; i0 < n; i0 += kThreads / 4) {
-                    const uint32_t i = min(i0 + threadIdx.x / 4, n - 1);
-                    const Entry x = S.list[i];
+                for (uint32_t i = threadIdx.x / 4; i < ((n + 7) & ~7u); i += kThreads / 4) {
+                    const Entry x = S.list[min(i, n - 1)];
                     u64 run = 0, here = 0;
                     for (uint32_t j = lane & 3; j < n; j += 4) {
                         const Entry y = S.list[j];
@@ -430,22 +427,22 @@ struct Sampler {
                     }
                     run += __shfl_xor_sync(kFull, run, 1);
                     run += __shfl_xor_sync(kFull, run, 2);
-                    run += above;
                     if (kMass) {
                         here += __shfl_xor_sync(kFull, here, 1);
                         here += __shfl_xor_sync(kFull, here, 2);
                     }
+                    run += above;
                     const u64 upto = run + (kMass ? x.w : 1);
-                    if (run < target && target <= upto) {
+                    if (i < n && run < target && target <= upto) {
                         S.cut[0] = __float_as_uint(row_exp(key_value(x.key)));
                         S.cut[1] = x.key;
                         S.cut[2] = x.idx;
-                        S.pick[0] = upto;
-                        S.pick[1] = own + here;
+                        S.pick[1] = upto;
+                        S.pick[3] = own + here;
                     }
                 }
                 __syncthreads();
-                if (kMass && total) *total = S.pick[0], *mine = S.pick[1];
+                if (kMass && total) *total = S.pick[1], *mine = S.pick[3];
                 return true;
             }
             if (shift == 0) break;   // over kList tokens with the same e
@@ -458,10 +455,11 @@ struct Sampler {
         u64 need = (target - above + w - 1) / w;
         uint32_t big = 0, small = 0;
         each([&](uint32_t i, uint32_t b) {
-            if (b != low) return;
-            const uint32_t k = key(i);
-            big = max(big, k);
-            small = max(small, ~k);
+            if (b == low) {
+                const uint32_t k = key(i);
+                big = max(big, k);
+                small = max(small, ~k);
+            }
         });
         big = max_row(big);
         small = ~max_row(small);
@@ -479,10 +477,11 @@ struct Sampler {
             need -= sum_row(m);
         }
         auto one = [&](uint32_t i, uint32_t b) -> u64 { return b == low && key(i) == at; };
-        u64 m = 0, before, part;
+        u64 m = 0, before;
         each([&](uint32_t i, uint32_t b) { m += one(i, b); });
-        sum_row(m, before, part);
-        locate(one, need - 1, before, part, [&](uint32_t i) {
+        const u64 part = sum_cta(m);
+        sum_ctas(part, before);
+        locate(one, m, need - 1, before, part, [&](uint32_t i) {
             for (uint32_t r = 0; r < size; r++) far_store(&S.cut[2], r, first + i);
         });
         if (threadIdx.x == 0) S.cut[0] = low, S.cut[1] = at;
@@ -496,27 +495,24 @@ struct Sampler {
     __device__ __forceinline__ bool small_list(float big, uint32_t k, float p, u64 least, uint32_t row) {
         const float scale = inv_t * 8.0f;
         auto near = [&](float v) { return __fmul_rn(top - v, scale); };   // grows as v falls
-        for (int i = threadIdx.x; i < kNear; i += kThreads) S.near_n[i] = 0;
-        if (threadIdx.x == 0) S.list_n = 0;
-        __syncthreads();
         const float x = near(big);
         if (x < (float)kNear) atomicAdd(&S.near_n[(int)x], 1u);
         sync();
+        for (int b = threadIdx.x; b < kNear; b += kThreads) {
+            uint32_t v = 0;
+            for (uint32_t r = 0; r < size; r++) v += far_load(S.near_n + b, r);
+            S.all[b] = v;
+        }
+        __syncthreads();
         if (warp == 0) {
-            uint32_t v[kNear / 32], s = 0;
+            constexpr int kPer = kNear / 32;
+            uint32_t v[kPer], s = 0, edge = ~0u;
 #pragma unroll
-            for (int j = 0; j < kNear / 32; j++) v[j] = 0;
-            for (uint32_t r = 0; r < size; r++) {
-                uint4 c;
-                asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(c.x), "=r"(c.y), "=r"(c.z), "=r"(c.w)
-                             : "r"(far_addr(S.near_n + lane * 4, r)) : "memory");
-                v[0] += c.x, v[1] += c.y, v[2] += c.z, v[3] += c.w;
-            }
-            s = v[0] + v[1] + v[2] + v[3];
-            uint32_t run = warp_incl_sum(s, lane) - s, edge = ~0u;
+            for (int j = 0; j < kPer; j++) s += v[j] = (uint32_t)S.all[lane * kPer + j];
+            uint32_t run = warp_incl_sum(s, lane) - s;
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                if (run < k && k <= run + v[j]) edge = lane * 4 + j + 1;
+            for (int j = 0; j < kPer; j++) {
+                if (run < k && k <= run + v[j]) edge = lane * kPer + j + 1;
                 run += v[j];
             }
             edge = __reduce_min_sync(kFull, edge);
@@ -527,82 +523,96 @@ struct Sampler {
         const float edge = (float)(uint32_t)S.pick[0];
         each([&](uint32_t i, uint32_t b) {
             if (near(__uint_as_float(b)) < edge) {
-                const uint32_t n = far_count(&S.list_n, 0);
-                if (n < kSmall)
-                    far_store(&S.small[n], 0, (u64)key_of(__uint_as_float(b)) << 32 | (uint32_t)~(first + i));
+                const uint32_t n = atomicAdd(&S.small_n, 1u);
+                if (n < kSmall) S.small[n] = (u64)key_of(__uint_as_float(b)) << 32 | (uint32_t)~(first + i);
             }
         });
         sync();
-        uint32_t n = S.list_n;
-        if (size > 1) {
-            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(n) : "r"(far_addr(&S.list_n, 0)) : "memory");
-        }
-        if (n > kSmall) {
-            sync();   // before list_n is cleared
-            return false;
-        }
-        if (size > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        uint32_t n = 0;
+        for (uint32_t r = 0; r < size; r++) n += far_load(&S.small_n, r);
+        if (n > kSmall) return false;
+        u64 *order = (u64 *)S.lo, *heavy = order + kSmallK;   // in the histogram's place
+        static_assert(sizeof(S.lo) + sizeof(S.hi) >= 2 * kSmallK * sizeof(u64), "room for the sorted list");
         if (rank == 0) {
-            // sorted: a token's place is the number of larger ones
-            for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-                const u64 x = S.small[i];
-                uint32_t place = 0;
-#pragma unroll 4
-                for (uint32_t j = 0; j < n; j++) place += S.small[j] > x;
-                if (place < k) {
-                    S.order[place] = x;
-                    S.heavy[place] = weight(row_exp(key_value((uint32_t)(x >> 32))));
+            if (size > 1) {   // the other CTAs' behind this one's
+                uint32_t at = S.small_n;
+                for (uint32_t r = 1; r < size; r++) {
+                    const uint32_t c = far_load(&S.small_n, r);
+                    for (uint32_t i = threadIdx.x; i < c; i += kThreads) S.small[at + i] = far_load(S.small + i, r);
+                    at += c;
                 }
             }
             __syncthreads();
-            n = min(n, k);
-            if (warp == 0) {   // 8 tokens a lane
-                constexpr int kPer = kSmallK / 32;
-                u64 w[kPer], s = 0;
-#pragma unroll
-                for (int j = 0; j < kPer; j++) {
-                    w[j] = (uint32_t)(lane * kPer + j) < n ? S.heavy[lane * kPer + j] : 0;
-                    s += w[j];
-                }
-                const u64 upto = warp_scan(s, lane);
-                u64 edge = ~0ull;
-                if (p < 1.0f) {
-                    const double x = (double)p * (double)__shfl_sync(kFull, upto, 31);
-                    edge = x > 1.0 ? (u64)x : 1;
-                }
-                u64 run = upto - s, total = 0;
-                uint32_t keep = 0;
-#pragma unroll
-                for (int j = 0; j < kPer; j++) {
-                    if (w[j] > 0 && run < edge && w[j] >= least) keep++, total += w[j];
-                    run += w[j];
-                }
-                keep = __reduce_add_sync(kFull, keep);
-                total = warp_sum(total);
-                if (lane == 0) S.pick[1] = keep, S.pick[2] = total;
-            }
-            __syncthreads();
-            const uint32_t keep = (uint32_t)S.pick[1];
-            const u64 total = S.pick[2];
-            const double y = (double)P.u[row] * (double)total;
-            u64 t = y > 0.0 ? (u64)y : 0;
-            if (t > total - 1) t = total - 1;
-            for (uint32_t i = threadIdx.x; i < keep; i += kThreads) {
-                const uint32_t mine = (uint32_t)S.order[i];   // ~id
-                u64 run = 0;
+        }
+        sync();               // the other CTAs end here
+        if (rank != 0) return true;
+        // sorted: a token's place is the number of larger ones
+        for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+            const u64 y = S.small[i];
+            uint32_t place = 0;
 #pragma unroll 4
-                for (uint32_t j = 0; j < keep; j++) run += (uint32_t)S.order[j] > mine ? S.heavy[j] : 0;
-                if (run <= t && t < run + S.heavy[i]) answer(row, ~mine, total);
+            for (uint32_t j = 0; j < n; j++) place += S.small[j] > y;
+            if (place < k) {
+                order[place] = y;
+                heavy[place] = weight(row_exp(key_value((uint32_t)(y >> 32))));
             }
         }
-        __syncwarp();
-        if (size > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        __syncthreads();
+        n = min(n, k);
+        if (warp == 0) {   // 8 tokens a lane
+            constexpr int kPer = kSmallK / 32;
+            u64 w[kPer], s = 0;
+#pragma unroll
+            for (int j = 0; j < kPer; j++) {
+                w[j] = (uint32_t)(lane * kPer + j) < n ? heavy[lane * kPer + j] : 0;
+                s += w[j];
+            }
+            const u64 upto = warp_scan(s, lane);
+            u64 edge = ~0ull;
+            if (p < 1.0f) {
+                const double y = (double)p * (double)__shfl_sync(kFull, upto, 31);
+                edge = y > 1.0 ? (u64)y : 1;
+            }
+            u64 run = upto - s, total = 0;
+            uint32_t keep = 0;
+#pragma unroll
+            for (int j = 0; j < kPer; j++) {
+                if (w[j] > 0 && run < edge && w[j] >= least) keep++, total += w[j];
+                run += w[j];
+            }
+            keep = __reduce_add_sync(kFull, keep);
+            total = warp_sum(total);
+            if (lane == 0) S.pick[1] = keep, S.pick[2] = total;
+        }
+        __syncthreads();
+        const uint32_t keep = (uint32_t)S.pick[1];
+        const u64 total = S.pick[2], t = goal_of(row, total);
+        for (uint32_t i = threadIdx.x; i < keep; i += kThreads) {
+            const uint32_t mine = (uint32_t)order[i];   // ~id
+            u64 run = 0;
+#pragma unroll 4
+            for (uint32_t j = 0; j < keep; j++) run += (uint32_t)order[j] > mine ? heavy[j] : 0;
+            if (run <= t && t < run + heavy[i]) answer(row, ~mine, total);
+        }
         return true;
     }
 
+    // The running mass that the id drawn passes.
+    __device__ __forceinline__ u64 goal_of(uint32_t row, u64 total) const {
+        const double x = (double)P.u[row] * (double)total;
+        const u64 t = x > 0.0 ? (u64)x : 0;
+        return t < total ? t : total - 1;
+    }
     __device__ __forceinline__ void answer(uint32_t row, uint32_t id, u64 total) const {
         P.ids[row] = (int32_t)id;
-        if (P.logprob) P.logprob[row] = (float)((double)z_of(logit(id), top, inv_t) - log((double)total * 0x1p-40));
+        if (P.logprob) P.logprob[row] = z_of(logit(id), top, inv_t) - logf((float)total * 0x1p-40f);
+    }
+    // own: this thread's kept mass.
+    __device__ __forceinline__ void draw(uint32_t row, u64 own, u64 total, u64 before, u64 mine) const {
+        auto value = [&](uint32_t i, uint32_t b) { return in_cut(i, b) ? weight(__uint_as_float(b)) : 0; };
+        const_cast<Sampler *>(this)->locate(value, own, goal_of(row, total), before, mine,
+                                            [&](uint32_t i) { answer(row, first + i, total); });
+        sync();   // no CTA ends while another may read its shared memory
     }
 };
 
@@ -641,17 +651,6 @@ __device__ __forceinline__ float load_row(const T *l, uint32_t count, bool wide,
     return big;
 }
 
-// The draw: the token at which the kept running mass passes floor(u W).
-template <int kThreads>
-__device__ __forceinline__ void draw(Sampler<kThreads> &A, uint32_t row, u64 total, u64 before, u64 mine) {
-    const double x = (double)A.P.u[row] * (double)total;
-    u64 t = x > 0.0 ? (u64)x : 0;
-    if (t > total - 1) t = total - 1;
-    A.locate([&](uint32_t i, uint32_t b) { return A.kept(i, b); }, t, before, mine,
-             [&](uint32_t i) { A.answer(row, A.first + i, total); });
-    A.sync();   // no CTA ends while another may read its shared memory
-}
-
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
@@ -662,13 +661,16 @@ k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
     const uint64_t at = row * P.stride + first;
     // every CTA of the row has begun before another writes to its shared memory
     if (team > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    float big = P.type == BPE_F32    ? load_row<float, kThreads>((const float *)P.logits + at, count, wide, S.e)
-                : P.type == BPE_BF16 ? load_row<__nv_bfloat16, kThreads>((const __nv_bfloat16 *)P.logits + at, count, wide, S.e)
-                                     : load_row<__half, kThreads>((const __half *)P.logits + at, count, wide, S.e);
-    const uint32_t quads = (count + 3) / 4, seg = (quads + kThreads / 32 - 1) / (kThreads / 32);
+    for (int i = threadIdx.x; i < kBuckets * S.kCopies; i += kThreads) S.lo[i] = S.hi[i] = 0;
+    for (int i = threadIdx.x; i < kNear; i += kThreads) S.near_n[i] = 0;
+    if (threadIdx.x == 0) S.small_n = 0;
+    const float big = P.type == BPE_F32    ? load_row<float, kThreads>((const float *)P.logits + at, count, wide, S.e)
+                      : P.type == BPE_BF16 ? load_row<__nv_bfloat16, kThreads>((const __nv_bfloat16 *)P.logits + at, count, wide, S.e)
+                                           : load_row<__half, kThreads>((const __half *)P.logits + at, count, wide, S.e);
+    const uint32_t quads = (count + 3) / 4, span = ((quads + kThreads - 1) / kThreads) | 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     Sampler<kThreads> A{S, P, (const uint8_t *)P.logits + row * P.stride * (P.type == BPE_F32 ? 4 : 2), rank, team, first,
-                        quads, min(quads, warp * seg), min(quads, (warp + 1) * seg), lane, warp, 0};
+                        quads, span, min(quads, threadIdx.x * span), min(quads, (threadIdx.x + 1) * span), lane, warp, 0};
     if (team > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     const uint32_t kmax = A.max_row(key_of(big));
     if (kmax == kKeyNegInf) {
@@ -702,13 +704,13 @@ k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
     const bool by_count = k >= 1 && (uint32_t)k < P.n_tok;
     if (by_count && k <= kSmallK && A.top < INFINITY && A.small_list(big, (uint32_t)k, p, least, row)) return;
     if (threadIdx.x == 0) S.cut[0] = kLeast, S.cut[1] = 0, S.cut[2] = ~0u;   // keep every weight above 0
-    u64 total = 0, mine = 0, before;
+    u64 total = 0, mine = 0, before, own;
     bool summed = false;
     if (by_count) {
         A.template select<false, true>((u64)k, -1.0);
         if (p < 1.0f) {
             A.read_cut();
-            const double x = (double)p * (double)A.sum_row(A.mass(), before, mine);
+            const double x = (double)p * (double)A.sum_row(A.mass());
             A.template select<true, false>(x > 1.0 ? (u64)x : 1, -1.0);
         }
     } else if (p < 1.0f) {
@@ -720,13 +722,15 @@ k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
             hi += w.hi;
             lo += w.lo;
         });
+        __syncthreads();
         if (!least) {
-            total = A.sum_row(join(hi, 0) + lo, before, mine);
             A.read_cut();
-            draw(A, row, total, before, mine);
+            own = join(hi, 0) + lo;
+            mine = A.sum_cta(own);
+            total = A.sum_ctas(mine, before);
+            A.draw(row, own, total, before, mine);
             return;
         }
-        __syncthreads();
     }
     A.read_cut();
     if (least) {
@@ -734,16 +738,16 @@ k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
         const uint32_t bits = __float_as_uint((float)least * 0x1p-40f);
         if (bits > A.cut_bits) A.cut_bits = bits, A.cut_idx = ~0u, summed = false;
     }
-    if (summed) {
+    if (summed) {   // the mass is known; only the CTA that holds the draw adds up its threads'
         A.sum_ctas(mine, before);
-        const double x = (double)P.u[row] * (double)total;
-        u64 t = x > 0.0 ? (u64)x : 0;
-        if (t > total - 1) t = total - 1;
-        if (t >= before && t - before < mine) A.sum_cta(A.mass());   // the warps' sums, where the draw needs them
+        const u64 t = A.goal_of(row, total);
+        if (t >= before && t - before < mine) A.sum_cta(own = A.mass());
     } else {
-        total = A.sum_row(A.mass(), before, mine);
+        own = A.mass();
+        mine = A.sum_cta(own);
+        total = A.sum_ctas(mine, before);
     }
-    draw(A, row, total, before, mine);
+    A.draw(row, own, total, before, mine);
 }
 
 // Vocabularies beyond a cluster's shared memory (over 262,144 tokens): one CTA per
@@ -926,8 +930,9 @@ int launch(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows) {
     while (team < kMaxTeam && P.n_tok > team * 20480) team *= 2;
     while (team < kMaxTeam && (uint64_t)n_rows * team * 2 <= (uint64_t)ctx->sm_count * 2 && P.n_tok >= team * 2 * 2048) team *= 2;
     const uint32_t each = (P.n_tok + team - 1) / team;
-    if (each <= 5120) return launch_team<128>(ctx, P, n_rows, team, wide);
-    if (each <= 10240) return launch_team<256>(ctx, P, n_rows, team, wide);
+    const bool room = (uint64_t)n_rows * team <= (uint64_t)ctx->sm_count * 2;   // all at once: threads cut the latency
+    if (each <= 5120 && !room) return launch_team<128>(ctx, P, n_rows, team, wide);
+    if (each <= 10240 && !room) return launch_team<256>(ctx, P, n_rows, team, wide);
     if (each <= 20480) return launch_team<512>(ctx, P, n_rows, team, wide);
     return launch_team<1024>(ctx, P, n_rows, team, wide);
 }
