@@ -27,6 +27,7 @@ struct LogitsParams {
     void *out;
     uint64_t xs_row, xs_blk, ws_row, ws_blk, out_stride;
     uint32_t n_rows, n_tok, blocks;
+    bool tma_out;                // the output's rows start on 16 bytes
     uint32_t *status;
 };
 
@@ -205,149 +206,225 @@ k_logits_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
 }
 
 // ------------------------------------------------------------ many rows ----
-// The rows of x are the product's 128-row side, 256 tokens the other; one
-// persistent CTA per SM takes tiles in turn, rows of tiles fastest, so that the
-// CTAs that run together read the same weights from L2.  Two sets of sums fill
-// the 512 columns of tensor memory.  A thread that adds holds one row and 128
-// tokens, which is one weight scale: its factor is one number per block.
-constexpr int kManyThreads = 320;   // 8 warps scale and add, 1 loads, 1 multiplies
-constexpr int kManyStages = 4, kManyToks = 256;
-constexpr int kManyStage = (128 + kManyToks) * kBlock;
-constexpr int kStageOut = 33 * 32 * 4;   // a warp's 32 x 32 tile on its way out
-constexpr int kManySmem = kManyStages * kManyStage + 8 * kStageOut + 1024 + 256;
-static_assert(kManySmem <= 232448, "shared memory of a CTA");
+// The rows of x are the product's row side, 256 tokens the other.  A tile is
+// 128 rows by one CTA, or 256 by a pair of CTAs that share the tokens' side (a
+// pair reads a third less from L2 than two CTAs would).  Persistent CTAs take
+// tiles in turn, rows fastest, so that those that run together read the same
+// weights from L2.  Two sets of sums fill the 512 columns of tensor memory.  A
+// thread that adds holds one row and 64 tokens, which are of one weight scale:
+// its factor is one number per block.  16 such warps, 4 per scheduler, cover
+// the latency of reading tensor memory.  The tile leaves through shared memory
+// by TMA while the next one is under way.
+constexpr int kManyThreads = 576;   // 16 warps scale and add, 1 loads, 1 multiplies
+constexpr int kManyToks = 256;
+constexpr int kOutBytes = 128 * 128;   // of one group of 4 warps: 128 rows of 128 bytes
 
-template <typename O>
+template <int kCtas> struct Many {
+    static constexpr int kRows = 128 * kCtas;
+    static constexpr int kStages = kCtas == 1 ? 3 : 5;
+    static constexpr int kToks = kManyToks / kCtas;                 // weights that a CTA loads
+    static constexpr int kStage = (128 + kToks) * kBlock;
+    static constexpr int kSmem = kStages * kStage + 4 * kOutBytes + 1024 + 256;
+    static_assert(kSmem <= 232448, "shared memory of a CTA");
+};
+
+// 16 bytes of the tile's way out: 4 or 8 columns of a row.
+__device__ __forceinline__ uint4 pack(const float *v, float) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+__device__ __forceinline__ uint4 pack(const float *v, __nv_bfloat16) {
+    __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    __nv_bfloat162 c = __floats2bfloat162_rn(v[4], v[5]), d = __floats2bfloat162_rn(v[6], v[7]);
+    return make_uint4(*(uint32_t *)&a, *(uint32_t *)&b, *(uint32_t *)&c, *(uint32_t *)&d);
+}
+__device__ __forceinline__ uint4 pack(const float *v, __half) {
+    __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
+    __half2 c = __floats2half2_rn(v[4], v[5]), d = __floats2half2_rn(v[6], v[7]);
+    return make_uint4(*(uint32_t *)&a, *(uint32_t *)&b, *(uint32_t *)&c, *(uint32_t *)&d);
+}
+
+template <typename O, int kCtas>
 __global__ void __launch_bounds__(kManyThreads, 1)
-k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, LogitsParams P) {
+k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+              const __grid_constant__ CUtensorMap map_out, LogitsParams P) {
+    using M = Many<kCtas>;
+    constexpr int kStages = M::kStages;
     extern __shared__ uint8_t raw[];
     uint8_t *base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     const uint32_t tiles = smem_u32(base);
-    float *stage_out = (float *)(base + kManyStages * kManyStage);
-    uint8_t *after = base + kManyStages * kManyStage + 8 * kStageOut;
+    uint8_t *outs = base + kStages * M::kStage;
+    uint8_t *after = outs + 4 * kOutBytes;
     const uint32_t bars = smem_u32(after);
-    uint32_t *extra = (uint32_t *)(after + 128);
-    auto full = [&](int s) { return bars + 8 * s; };
-    auto empty = [&](int s) { return bars + 8 * (kManyStages + s); };
-    auto done = [&](int b) { return bars + 8 * (2 * kManyStages + b); };
-    auto taken = [&](int b) { return bars + 8 * (2 * kManyStages + 2 + b); };
+    uint32_t *extra = (uint32_t *)(after + 128);   // [0] tensor memory, [1] gave up
+    auto full = [&](int s) { return bars + 8 * s; };               // a pair's: rank 0's
+    auto empty = [&](int s) { return bars + 8 * (kStages + s); };
+    auto done = [&](int b) { return bars + 8 * (2 * kStages + b); };
+    auto taken = [&](int b) { return bars + 8 * (2 * kStages + 2 + b); };   // a pair's: rank 0's
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t row_tiles = (P.n_rows + 127) / 128, tok_tiles = (P.n_tok + kManyToks - 1) / kManyToks;
+    const uint32_t rank = blockIdx.x % kCtas, team = blockIdx.x / kCtas, teams = gridDim.x / kCtas;
+    const uint32_t row_tiles = (P.n_rows + M::kRows - 1) / M::kRows, tok_tiles = (P.n_tok + kManyToks - 1) / kManyToks;
     const uint32_t n_tiles = row_tiles * tok_tiles;
     volatile uint32_t *gave_up = extra + 1;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kManyStages; s++) mbar_init(full(s), 1), mbar_init(empty(s), 1);
-        for (int b = 0; b < 2; b++) mbar_init(done(b), 1), mbar_init(taken(b), 8);
+        for (int s = 0; s < kStages; s++) mbar_init(full(s), 1), mbar_init(empty(s), 1);
+        for (int b = 0; b < 2; b++) mbar_init(done(b), 1), mbar_init(taken(b), 16 * kCtas);
         extra[1] = 0;
         mbar_init_fence();
     }
-    if (warp == 9) tmem_alloc(smem_u32(extra), 512);
+    if (warp == 17) {
+        if (kCtas == 1)
+            tmem_alloc(smem_u32(extra), 512);
+        else
+            tmem_alloc_pair(smem_u32(extra), 512);
+    }
     tc_fence_before();
-    __syncthreads();
+    if (kCtas == 1)
+        __syncthreads();
+    else
+        asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     tc_fence_after();
     const uint32_t tmem = extra[0];
 
-    if (warp == 8) {
+    if (warp == 16) {
         if (lane == 0) {
             tma_prefetch_map(&map_w);
             tma_prefetch_map(&map_x);
             int s = 0;
             uint32_t phase = 1, issued = 0;
-            for (uint32_t i = blockIdx.x; i < n_tiles && !*gave_up; i += gridDim.x) {
-                const int row0 = (int)(i % row_tiles * 128), tok0 = (int)(i / row_tiles * kManyToks);
+            for (uint32_t i = team; i < n_tiles && !*gave_up; i += teams) {
+                const int row0 = (int)(i % row_tiles * M::kRows + rank * 128);
+                const int tok0 = (int)(i / row_tiles * kManyToks + rank * M::kToks);
                 for (uint32_t b = 0; b < P.blocks; b++) {
                     if (!mbar_wait(empty(s), phase)) { *gave_up = 1; break; }
-                    mbar_expect(full(s), kManyStage);
-                    tma_load(tiles + s * kManyStage, &map_x, (int)(b * kBlock), row0, full(s));
-                    tma_load(tiles + s * kManyStage + 128 * kBlock, &map_w, (int)(b * kBlock), tok0, full(s));
+                    const uint32_t at = tiles + s * M::kStage;
+                    if (rank == 0) mbar_expect(full(s), M::kStage * kCtas);
+                    if (kCtas == 1) {
+                        tma_load(at, &map_x, (int)(b * kBlock), row0, full(s));
+                        tma_load(at + 128 * kBlock, &map_w, (int)(b * kBlock), tok0, full(s));
+                    } else {
+                        tma_load_pair(at, &map_x, (int)(b * kBlock), row0, full(s));
+                        tma_load_pair(at + 128 * kBlock, &map_w, (int)(b * kBlock), tok0, full(s));
+                    }
                     issued++;
-                    if (++s == kManyStages) s = 0, phase ^= 1;
+                    if (++s == kStages) s = 0, phase ^= 1;
                 }
             }
-            if (*gave_up)   // no copy may be in flight when the CTA ends
-                for (uint32_t i = issued > kManyStages ? issued - kManyStages : 0; i < issued; i++)
-                    mbar_wait(full(i % kManyStages), (i / kManyStages) & 1);
+            if (*gave_up && rank == 0)   // no copy may be in flight when the CTA ends
+                for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; i++)
+                    mbar_wait(full(i % kStages), (i / kStages) & 1);
         }
-    } else if (warp == 9) {
-        if (lane == 0) {
+    } else if (warp == 17) {
+        if (lane == 0 && rank == 0) {
             int s = 0, buf = 0;
             uint32_t phase = 0, bphase = 1;
-            for (uint32_t i = blockIdx.x; i < n_tiles && !*gave_up; i += gridDim.x) {
+            for (uint32_t i = team; i < n_tiles && !*gave_up; i += teams) {
                 for (uint32_t b = 0; b < P.blocks; b++) {
                     if (!mbar_wait(taken(buf), bphase) || !mbar_wait(full(s), phase)) { *gave_up = 1; break; }
                     tc_fence_after();
-                    const uint64_t dx = operand_desc(tiles + s * kManyStage);
-                    const uint64_t dw = operand_desc(tiles + s * kManyStage + 128 * kBlock);
+                    const uint64_t dx = operand_desc(tiles + s * M::kStage);
+                    const uint64_t dw = operand_desc(tiles + s * M::kStage + 128 * kBlock);
 #pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        mma_e4m3(tmem + buf * kManyToks, dx + 2 * k, dw + 2 * k, e4m3_instr(128, kManyToks), k > 0);
-                    mma_commit(empty(s));
-                    mma_commit(done(buf));
-                    if (++s == kManyStages) s = 0, phase ^= 1;
+                    for (int k = 0; k < 4; k++) {
+                        if (kCtas == 1)
+                            mma_e4m3(tmem + buf * kManyToks, dx + 2 * k, dw + 2 * k, e4m3_instr(128, kManyToks), k > 0);
+                        else
+                            mma_e4m3_pair(tmem + buf * kManyToks, dx + 2 * k, dw + 2 * k, e4m3_instr(256, kManyToks), k > 0);
+                    }
+                    if (kCtas == 1) {
+                        mma_commit(empty(s));
+                        mma_commit(done(buf));
+                    } else {
+                        mma_commit_pair(empty(s));
+                        mma_commit_pair(done(buf));
+                    }
+                    if (++s == kStages) s = 0, phase ^= 1;
                     if (++buf == 2) buf = 0, bphase ^= 1;
                 }
             }
         }
     } else {
-        const int quarter = warp & 3, half = warp >> 2;
-        float *mine = stage_out + warp * (33 * 32);
-        O *out = (O *)P.out;
+        const int quarter = warp & 3, group = warp >> 2;
+        uint8_t *mine = outs + group * kOutBytes;   // the group's 128 rows of 128 bytes, swizzled as TMA reads them
+        const uint32_t r = quarter * 32 + lane;
+        constexpr int kPer = 128 / sizeof(O);       // tokens in 128 bytes
+        constexpr int kVec = 16 / sizeof(O);
         int buf = 0;
         uint32_t bphase = 0;
-        for (uint32_t i = blockIdx.x; i < n_tiles; i += gridDim.x) {
-            const uint32_t row0 = i % row_tiles * 128 + quarter * 32, tok0 = i / row_tiles * kManyToks + half * 128;
-            const uint32_t row = row0 + lane;
-            const float *xs = P.xs + (uint64_t)min(row, P.n_rows - 1) * P.xs_row;
+        for (uint32_t i = team; i < n_tiles; i += teams) {
+            const uint32_t row0 = i % row_tiles * M::kRows + rank * 128, tok0 = i / row_tiles * kManyToks + group * 64;
+            const float *xs = P.xs + (uint64_t)min(row0 + r, P.n_rows - 1) * P.xs_row;
             const float *ws = P.ws + (uint64_t)min(tok0 / kBlock, (P.n_tok - 1) / kBlock) * P.ws_row;
-            float acc[128];
+            float acc[64];
 #pragma unroll
-            for (int c = 0; c < 128; c++) acc[c] = 0.0f;
-            float sx = xs[0], sw = ws[0];
+            for (int c = 0; c < 64; c++) acc[c] = 0.0f;
+            const uint32_t last = P.blocks - 1;
+            float sx0 = xs[0], sw0 = ws[0], sx1 = xs[min(1u, last) * P.xs_blk], sw1 = ws[min(1u, last) * P.ws_blk];
             bool ok = true;
             for (uint32_t b = 0; b < P.blocks; b++) {
-                const float s = sx * sw;
-                const uint32_t nb = min(b + 1, P.blocks - 1);
-                sx = xs[nb * P.xs_blk];
-                sw = ws[nb * P.ws_blk];
+                const float s = sx0 * sw0;
+                sx0 = sx1, sw0 = sw1;
+                sx1 = xs[min(b + 2, last) * P.xs_blk];
+                sw1 = ws[min(b + 2, last) * P.ws_blk];
                 if (!__all_sync(kFull, mbar_wait(done(buf), bphase))) { ok = false; break; }
                 tc_fence_after();
+                const uint32_t at = tmem + ((uint32_t)quarter << 21) + buf * kManyToks + group * 64;
 #pragma unroll
-                for (int c0 = 0; c0 < 128; c0 += 32) {
-                    float d[32];
-                    tmem_load(d, tmem + ((uint32_t)quarter << 21) + buf * kManyToks + half * 128 + c0);
+                for (int c0 = 0; c0 < 64; c0 += 16) {   // 16 at a time: 96 registers is what 18 warps have
+                    float d[16];
+                    tmem_load(d, at + c0);
                     tmem_wait(d);
-                    if (c0 == 96) {
+                    if (c0 == 48) {
                         tc_fence_before();
-                        if (lane == 0) mbar_arrive(taken(buf));
+                        if (lane == 0) {
+                            if (kCtas == 1)
+                                mbar_arrive(taken(buf));
+                            else
+                                mbar_arrive_far(taken(buf), 0);
+                        }
                     }
 #pragma unroll
-                    for (int c = 0; c < 32; c++) acc[c0 + c] = fmaf(d[c], s, acc[c0 + c]);
+                    for (int c = 0; c < 16; c++) acc[c0 + c] = fmaf(d[c], s, acc[c0 + c]);
                 }
                 if (++buf == 2) buf = 0, bphase ^= 1;
             }
             if (!ok) { *gave_up = 1; break; }
-            // rows to lines: 32 x 32 at a time through shared memory, so that a store is 32 tokens of one row
 #pragma unroll
-            for (int c0 = 0; c0 < 128; c0 += 32) {
-                __syncwarp();
+            for (int c0 = 0; c0 < 64; c0 += kPer) {
+                if (P.tma_out && quarter == 0 && lane == 0) tma_store_wait();
+                asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
 #pragma unroll
-                for (int c = 0; c < 32; c++) mine[lane * 33 + c] = acc[c0 + c];
-                __syncwarp();
-                const uint32_t t = tok0 + c0 + lane;
-                if (t < P.n_tok) {
-#pragma unroll 8
-                    for (uint32_t r = 0; r < 32; r++)
-                        if (row0 + r < P.n_rows) out[(row0 + r) * P.out_stride + t] = from_f32<O>(mine[r * 33 + lane]);
+                for (int j = 0; j < 8; j++)
+                    *reinterpret_cast<uint4 *>(mine + r * 128 + ((j ^ (r & 7)) << 4)) = pack(acc + c0 + j * kVec, O());
+                if (P.tma_out) fence_for_tma();
+                asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+                if (P.tma_out) {
+                    if (quarter == 0 && lane == 0 && row0 < P.n_rows && tok0 + c0 < P.n_tok)
+                        tma_store(&map_out, (int)(tok0 + c0), (int)row0, smem_u32(mine));
+                } else {
+                    const uint32_t c = threadIdx.x & (kPer - 1), t = tok0 + c0 + c;
+                    for (uint32_t q = (threadIdx.x & 127) / kPer; q < 128 && row0 + q < P.n_rows; q += 128 / kPer)
+                        if (t < P.n_tok)
+                            ((O *)P.out)[(row0 + q) * P.out_stride + t] =
+                                *reinterpret_cast<O *>(mine + q * 128 + (((c / kVec) ^ (q & 7)) << 4) + c % kVec * sizeof(O));
                 }
             }
         }
+        if (P.tma_out && quarter == 0 && lane == 0) tma_store_wait();
     }
     __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    if (kCtas == 1)
+        __syncthreads();
+    else
+        asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     tc_fence_after();
-    if (warp == 9) tmem_free(tmem, 512);
+    if (warp == 17) {
+        if (kCtas == 1)
+            tmem_free(tmem, 512);
+        else
+            tmem_free_pair(tmem, 512);
+    }
     if (threadIdx.x == 0 && *gave_up) *P.status = DERR_TIMEOUT;
 }
 
@@ -396,6 +473,20 @@ int encode_map(bpe_ctx *ctx, CUtensorMap *map, const uint8_t *p, uint64_t stride
     return BPE_OK;
 }
 
+// The output's map, for tiles of 128 rows and 128 bytes.
+template <typename O>
+int encode_out(bpe_ctx *ctx, CUtensorMap *map, const LogitsParams &P) {
+    EncodeFn fn = encode_fn();
+    if (!fn) return fail(ctx, BPE_ERR_CUDA, "head_logits: the driver has no cuTensorMapEncodeTiled");
+    const CUtensorMapDataType type = sizeof(O) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+    const cuuint64_t size[2] = {P.n_tok, P.n_rows}, strides[1] = {P.out_stride * sizeof(O)};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / sizeof(O)), 128}, step[2] = {1, 1};
+    const CUresult r = fn(map, type, 2, P.out, size, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(ctx, BPE_ERR_CUDA, "head_logits: cuTensorMapEncodeTiled returned %d", (int)r);
+    return BPE_OK;
+}
+
 // `p` itself where TMA can read it, else a copy in scratch.
 int aligned_rows(bpe_ctx *ctx, Slot slot, const uint8_t *&p, uint64_t &stride, uint32_t rows, uint32_t dim) {
     if (rows == 1 && stride % 16) stride = ((uint64_t)dim + 15) & ~15ull;
@@ -436,29 +527,52 @@ int launch_few(bpe_ctx *ctx, const CUtensorMap &mw, const CUtensorMap &mx, const
     return BPE_OK;
 }
 
-template <typename O>
-int launch_many(bpe_ctx *ctx, const CUtensorMap &mw, const CUtensorMap &mx, const LogitsParams &P) {
-    auto k = k_logits_many<O>;
-    BPE_CUDA(ctx, cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kManySmem), "head_logits");
-    const uint64_t n_tiles = (uint64_t)((P.n_rows + 127) / 128) * ((P.n_tok + kManyToks - 1) / kManyToks);
-    const uint32_t grid = (uint32_t)(n_tiles < (uint64_t)ctx->sm_count ? n_tiles : (uint64_t)ctx->sm_count);
-    k<<<grid, kManyThreads, kManySmem, ctx->stream>>>(mw, mx, P);
-    BPE_CUDA(ctx, cudaGetLastError(), "head_logits launch");
+template <typename O, int kCtas>
+int launch_many(bpe_ctx *ctx, const CUtensorMap &mw, const CUtensorMap &mx, const CUtensorMap &mo, const LogitsParams &P) {
+    using M = Many<kCtas>;
+    auto k = k_logits_many<O, kCtas>;
+    BPE_CUDA(ctx, cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, M::kSmem), "head_logits");
+    const uint64_t n_tiles = (uint64_t)((P.n_rows + M::kRows - 1) / M::kRows) * ((P.n_tok + kManyToks - 1) / kManyToks);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctx->sm_count / kCtas * kCtas);
+    cfg.blockDim = dim3(kManyThreads);
+    cfg.dynamicSmemBytes = M::kSmem;
+    cfg.stream = ctx->stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {kCtas, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = kCtas > 1 ? 1 : 0;
+    // as many as run at once: a pair needs two free SMs of one GPC
+    int &teams = ctx->head_teams[kCtas - 1];
+    if (teams == 0) {
+        if (kCtas == 1)
+            teams = ctx->sm_count;
+        else
+            BPE_CUDA(ctx, cudaOccupancyMaxActiveClusters(&teams, k, &cfg), "head_logits");
+        if (teams < 1) return fail(ctx, BPE_ERR_CUDA, "head_logits: no pair of CTAs fits");
+    }
+    cfg.gridDim = dim3((uint32_t)(n_tiles < (uint64_t)teams ? n_tiles : (uint64_t)teams) * kCtas);
+    BPE_CUDA(ctx, cudaLaunchKernelEx(&cfg, k, mw, mx, mo, P), "head_logits launch");
     return BPE_OK;
 }
 
 template <typename O>
-int launch(bpe_ctx *ctx, const uint8_t *x8, uint64_t x_stride, const uint8_t *w8, uint64_t w_stride, uint32_t dim, const LogitsParams &P) {
+int launch(bpe_ctx *ctx, const uint8_t *x8, uint64_t x_stride, const uint8_t *w8, uint64_t w_stride, uint32_t dim, LogitsParams P) {
     const int n = P.n_rows <= 16 ? 16 : P.n_rows <= 32 ? 32 : P.n_rows <= 64 ? 64 : 0;
-    CUtensorMap mw, mx;
+    // a pair's 256 rows where they waste no more than 128-row tiles would
+    const bool pair = !n && (P.n_rows + 127) / 128 % 2 == 0;
+    CUtensorMap mw, mx, mo = {};
     int rc;
-    if ((rc = encode_map(ctx, &mw, w8, w_stride, P.n_tok, dim, n ? 128 : kManyToks)) ||
+    if ((rc = encode_map(ctx, &mw, w8, w_stride, P.n_tok, dim, n || pair ? 128 : kManyToks)) ||
         (rc = encode_map(ctx, &mx, x8, x_stride, P.n_rows, dim, n ? n : 128)))
         return rc;
     if (n == 16) return launch_few<16, O>(ctx, mw, mx, P);
     if (n == 32) return launch_few<32, O>(ctx, mw, mx, P);
     if (n == 64) return launch_few<64, O>(ctx, mw, mx, P);
-    return launch_many<O>(ctx, mw, mx, P);
+    P.tma_out = (uintptr_t)P.out % 16 == 0 && P.out_stride * sizeof(O) % 16 == 0 && P.out_stride * sizeof(O) < (1ull << 40);
+    if (P.tma_out && (rc = encode_out<O>(ctx, &mo, P))) return rc;
+    return pair ? launch_many<O, 2>(ctx, mw, mx, mo, P) : launch_many<O, 1>(ctx, mw, mx, mo, P);
 }
 
 }  // namespace
@@ -486,7 +600,7 @@ extern "C" int head_logits(bpe_ctx *ctx, const uint8_t *d_x8, uint64_t x8_stride
         (rc = aligned_rows(ctx, S_HEAD_W, d_w8, w8_stride, n_tok, dim)))
         return rc;
     const LogitsParams P{d_xs, d_ws, d_out, xs_row_stride, xs_block_stride, ws_row_stride, ws_block_stride, out_stride,
-                         n_rows, n_tok, (dim + kBlock - 1) / kBlock, status};
+                         n_rows, n_tok, (dim + kBlock - 1) / kBlock, false, status};
     if (out_type == BPE_F32) return launch<float>(ctx, d_x8, x8_stride, d_w8, w8_stride, dim, P);
     if (out_type == BPE_BF16) return launch<__nv_bfloat16>(ctx, d_x8, x8_stride, d_w8, w8_stride, dim, P);
     return launch<__half>(ctx, d_x8, x8_stride, d_w8, w8_stride, dim, P);

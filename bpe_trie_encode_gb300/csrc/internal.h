@@ -87,6 +87,7 @@ struct bpe_ctx {
     bpe_stream *pipe_stream = nullptr;
     const bpe_trie *pipe_trie = nullptr;
     uint32_t pipe_max_len = 0;
+    int head_teams[2] = {0, 0};   // persistent CTAs, and pairs of them, that this device runs at once
     volatile uint32_t *head_flag = nullptr;   // host word (mapped) that a head kernel sets when a wait gives up
 };
 
