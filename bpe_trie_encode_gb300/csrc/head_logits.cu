@@ -64,7 +64,7 @@ k_logits_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
     auto empty = [&](int s) { return bars + 8 * (kFewStages + s); };
     auto done = [&](int b) { return bars + 8 * (2 * kFewStages + b); };
     auto taken = [&](int b) { return bars + 8 * (2 * kFewStages + F::kBufs + b); };
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(kFull, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t part = blockIdx.x % split, tile = blockIdx.x / split;
     const uint32_t b0 = (uint32_t)((uint64_t)P.blocks * part / split), b1 = (uint32_t)((uint64_t)P.blocks * (part + 1) / split);
     const uint32_t tok0 = tile * 128, row0 = blockIdx.y * kN;
@@ -87,40 +87,42 @@ k_logits_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
     for (int c = 0; c < kN; c++) acc[c] = 0.0f;
 
     if (warp == 4) {
-        if (lane == 0) {
-            tma_prefetch_map(&map_w);
-            tma_prefetch_map(&map_x);
-            int s = 0;
-            uint32_t phase = 1, issued = 0;
-            for (uint32_t b = b0; b < b1; b++) {
-                if (!mbar_wait(empty(s), phase)) { *gave_up = 1; break; }
+        tma_prefetch_map(&map_w);
+        tma_prefetch_map(&map_x);
+        int s = 0;
+        uint32_t phase = 1, issued = 0;
+        for (uint32_t b = b0; b < b1; b++) {
+            if (!__all_sync(kFull, mbar_wait(empty(s), phase))) { *gave_up = 1; break; }
+            if (elect_one()) {
                 mbar_expect(full(s), F::kStage);
                 tma_load(tiles + s * F::kStage, &map_w, (int)(b * kBlock), (int)tok0, full(s));
                 tma_load(tiles + s * F::kStage + 128 * kBlock, &map_x, (int)(b * kBlock), (int)row0, full(s));
-                issued++;
-                if (++s == kFewStages) s = 0, phase ^= 1;
             }
-            if (*gave_up)   // no copy may be in flight when the CTA ends
-                for (uint32_t i = issued > kFewStages ? issued - kFewStages : 0; i < issued; i++)
-                    mbar_wait(full(i % kFewStages), (i / kFewStages) & 1);
+            issued++;
+            if (++s == kFewStages) s = 0, phase ^= 1;
         }
+        if (*gave_up)   // no copy may be in flight when the CTA ends
+            for (uint32_t i = issued > kFewStages ? issued - kFewStages : 0; i < issued; i++)
+                mbar_wait(full(i % kFewStages), (i / kFewStages) & 1);
     } else if (warp == 5) {
-        if (lane == 0) {
-            int s = 0, buf = 0;
-            uint32_t phase = 0, bphase = 1;
-            for (uint32_t b = b0; b < b1; b++) {
-                if (!mbar_wait(taken(buf), bphase) || !mbar_wait(full(s), phase)) { *gave_up = 1; break; }
-                tc_fence_after();
-                const uint64_t dw = operand_desc(tiles + s * F::kStage);
-                const uint64_t dx = operand_desc(tiles + s * F::kStage + 128 * kBlock);
-#pragma unroll
-                for (int k = 0; k < 4; k++)
-                    mma_e4m3(tmem + buf * kN, dw + 2 * k, dx + 2 * k, e4m3_instr(128, kN), k > 0);
-                mma_commit(empty(s));
+        int s = 0, buf = 0;
+        uint32_t phase = 0, bphase = 1;
+        const uint32_t w0 = operand_lo(tiles), x0 = operand_lo(tiles + 128 * kBlock);
+        for (uint32_t b = b0; b < b1; b++) {
+            if (!__all_sync(kFull, mbar_wait(taken(buf), bphase) && mbar_wait(full(s), phase))) { *gave_up = 1; break; }
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t w = w0 + s * (F::kStage >> 4), x = x0 + s * (F::kStage >> 4), d = tmem + buf * kN;
+                constexpr uint32_t kInstr = e4m3_instr(128, kN);
+                mma_e4m3<false>(d, w, x, kInstr);
+                mma_e4m3<true>(d, w + 2, x + 2, kInstr);
+                mma_e4m3<true>(d, w + 4, x + 4, kInstr);
+                mma_e4m3<true>(d, w + 6, x + 6, kInstr);
                 mma_commit(done(buf));
-                if (++s == kFewStages) s = 0, phase ^= 1;
-                if (++buf == F::kBufs) buf = 0, bphase ^= 1;
+                mma_commit(empty(s));
             }
+            if (++s == kFewStages) s = 0, phase ^= 1;
+            if (++buf == F::kBufs) buf = 0, bphase ^= 1;
         }
     } else {
         constexpr int kPer = (kN + 31) / 32;   // row scales that a lane holds
@@ -260,7 +262,7 @@ k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     auto empty = [&](int s) { return bars + 8 * (kStages + s); };
     auto done = [&](int b) { return bars + 8 * (2 * kStages + b); };
     auto taken = [&](int b) { return bars + 8 * (2 * kStages + 2 + b); };   // a pair's: rank 0's
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(kFull, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = blockIdx.x % kCtas, team = blockIdx.x / kCtas, teams = gridDim.x / kCtas;
     const uint32_t row_tiles = (P.n_rows + M::kRows - 1) / M::kRows, tok_tiles = (P.n_tok + kManyToks - 1) / kManyToks;
     const uint32_t n_tiles = row_tiles * tok_tiles;
@@ -287,17 +289,17 @@ k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     const uint32_t tmem = extra[0];
 
     if (warp == 16) {
-        if (lane == 0) {
-            tma_prefetch_map(&map_w);
-            tma_prefetch_map(&map_x);
-            int s = 0;
-            uint32_t phase = 1, issued = 0;
-            for (uint32_t i = team; i < n_tiles && !*gave_up; i += teams) {
-                const int row0 = (int)(i % row_tiles * M::kRows + rank * 128);
-                const int tok0 = (int)(i / row_tiles * kManyToks + rank * M::kToks);
-                for (uint32_t b = 0; b < P.blocks; b++) {
-                    if (!mbar_wait(empty(s), phase)) { *gave_up = 1; break; }
-                    const uint32_t at = tiles + s * M::kStage;
+        tma_prefetch_map(&map_w);
+        tma_prefetch_map(&map_x);
+        int s = 0;
+        uint32_t phase = 1, issued = 0;
+        for (uint32_t i = team; i < n_tiles && !__any_sync(kFull, *gave_up); i += teams) {
+            const int row0 = (int)(i % row_tiles * M::kRows + rank * 128);
+            const int tok0 = (int)(i / row_tiles * kManyToks + rank * M::kToks);
+            for (uint32_t b = 0; b < P.blocks; b++) {
+                if (!__all_sync(kFull, mbar_wait(empty(s), phase))) { *gave_up = 1; break; }
+                const uint32_t at = tiles + s * M::kStage;
+                if (elect_one()) {
                     if (rank == 0) mbar_expect(full(s), M::kStage * kCtas);
                     if (kCtas == 1) {
                         tma_load(at, &map_x, (int)(b * kBlock), row0, full(s));
@@ -306,37 +308,41 @@ k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                         tma_load_pair(at, &map_x, (int)(b * kBlock), row0, full(s));
                         tma_load_pair(at + 128 * kBlock, &map_w, (int)(b * kBlock), tok0, full(s));
                     }
-                    issued++;
-                    if (++s == kStages) s = 0, phase ^= 1;
                 }
+                issued++;
+                if (++s == kStages) s = 0, phase ^= 1;
             }
-            if (*gave_up && rank == 0)   // no copy may be in flight when the CTA ends
-                for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; i++)
-                    mbar_wait(full(i % kStages), (i / kStages) & 1);
         }
+        if (*gave_up && rank == 0)   // no copy may be in flight when the CTA ends
+            for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; i++)
+                mbar_wait(full(i % kStages), (i / kStages) & 1);
     } else if (warp == 17) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             int s = 0, buf = 0;
             uint32_t phase = 0, bphase = 1;
-            for (uint32_t i = team; i < n_tiles && !*gave_up; i += teams) {
+            const uint32_t x0 = operand_lo(tiles), w0 = operand_lo(tiles + 128 * kBlock);
+            for (uint32_t i = team; i < n_tiles && !__any_sync(kFull, *gave_up); i += teams) {
                 for (uint32_t b = 0; b < P.blocks; b++) {
-                    if (!mbar_wait(taken(buf), bphase) || !mbar_wait(full(s), phase)) { *gave_up = 1; break; }
+                    if (!__all_sync(kFull, mbar_wait(taken(buf), bphase) && mbar_wait(full(s), phase))) { *gave_up = 1; break; }
                     tc_fence_after();
-                    const uint64_t dx = operand_desc(tiles + s * M::kStage);
-                    const uint64_t dw = operand_desc(tiles + s * M::kStage + 128 * kBlock);
-#pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        if (kCtas == 1)
-                            mma_e4m3(tmem + buf * kManyToks, dx + 2 * k, dw + 2 * k, e4m3_instr(128, kManyToks), k > 0);
-                        else
-                            mma_e4m3_pair(tmem + buf * kManyToks, dx + 2 * k, dw + 2 * k, e4m3_instr(256, kManyToks), k > 0);
-                    }
-                    if (kCtas == 1) {
-                        mma_commit(empty(s));
-                        mma_commit(done(buf));
-                    } else {
-                        mma_commit_pair(empty(s));
-                        mma_commit_pair(done(buf));
+                    if (elect_one()) {
+                        const uint32_t x = x0 + s * (M::kStage >> 4), w = w0 + s * (M::kStage >> 4), d = tmem + buf * kManyToks;
+                        constexpr uint32_t kInstr = e4m3_instr(M::kRows, kManyToks);
+                        if (kCtas == 1) {
+                            mma_e4m3<false>(d, x, w, kInstr);
+                            mma_e4m3<true>(d, x + 2, w + 2, kInstr);
+                            mma_e4m3<true>(d, x + 4, w + 4, kInstr);
+                            mma_e4m3<true>(d, x + 6, w + 6, kInstr);
+                            mma_commit(done(buf));
+                            mma_commit(empty(s));
+                        } else {
+                            mma_e4m3_pair<false>(d, x, w, kInstr);
+                            mma_e4m3_pair<true>(d, x + 2, w + 2, kInstr);
+                            mma_e4m3_pair<true>(d, x + 4, w + 4, kInstr);
+                            mma_e4m3_pair<true>(d, x + 6, w + 6, kInstr);
+                            mma_commit_pair(done(buf));
+                            mma_commit_pair(empty(s));
+                        }
                     }
                     if (++s == kStages) s = 0, phase ^= 1;
                     if (++buf == 2) buf = 0, bphase ^= 1;
@@ -350,16 +356,21 @@ k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         constexpr int kPer = 128 / sizeof(O);       // tokens in 128 bytes
         constexpr int kVec = 16 / sizeof(O);
         int buf = 0;
-        uint32_t bphase = 0;
+        uint32_t bphase = 0, row0, tok0;
+        const uint32_t last = P.blocks - 1;
+        const float *xs, *ws;
+        float sx0, sw0, sx1, sw1;   // the scales of the next two blocks
+        auto begin = [&](uint32_t i) {
+            row0 = i % row_tiles * M::kRows + rank * 128, tok0 = i / row_tiles * kManyToks + group * 64;
+            xs = P.xs + (uint64_t)min(row0 + r, P.n_rows - 1) * P.xs_row;
+            ws = P.ws + (uint64_t)min(tok0 / kBlock, (P.n_tok - 1) / kBlock) * P.ws_row;
+            sx0 = xs[0], sw0 = ws[0], sx1 = xs[min(1u, last) * P.xs_blk], sw1 = ws[min(1u, last) * P.ws_blk];
+        };
+        if (team < n_tiles) begin(team);
         for (uint32_t i = team; i < n_tiles; i += teams) {
-            const uint32_t row0 = i % row_tiles * M::kRows + rank * 128, tok0 = i / row_tiles * kManyToks + group * 64;
-            const float *xs = P.xs + (uint64_t)min(row0 + r, P.n_rows - 1) * P.xs_row;
-            const float *ws = P.ws + (uint64_t)min(tok0 / kBlock, (P.n_tok - 1) / kBlock) * P.ws_row;
             float acc[64];
 #pragma unroll
             for (int c = 0; c < 64; c++) acc[c] = 0.0f;
-            const uint32_t last = P.blocks - 1;
-            float sx0 = xs[0], sw0 = ws[0], sx1 = xs[min(1u, last) * P.xs_blk], sw1 = ws[min(1u, last) * P.ws_blk];
             bool ok = true;
             for (uint32_t b = 0; b < P.blocks; b++) {
                 const float s = sx0 * sw0;
@@ -389,6 +400,8 @@ k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 if (++buf == 2) buf = 0, bphase ^= 1;
             }
             if (!ok) { *gave_up = 1; break; }
+            const uint32_t out_row = row0, out_tok = tok0;
+            if (i + teams < n_tiles) begin(i + teams);   // the next tile's first scales arrive while this one leaves
 #pragma unroll
             for (int c0 = 0; c0 < 64; c0 += kPer) {
                 if (P.tma_out && quarter == 0 && lane == 0) tma_store_wait();
@@ -399,13 +412,13 @@ k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 if (P.tma_out) fence_for_tma();
                 asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
                 if (P.tma_out) {
-                    if (quarter == 0 && lane == 0 && row0 < P.n_rows && tok0 + c0 < P.n_tok)
-                        tma_store(&map_out, (int)(tok0 + c0), (int)row0, smem_u32(mine));
+                    if (quarter == 0 && lane == 0 && out_row < P.n_rows && out_tok + c0 < P.n_tok)
+                        tma_store(&map_out, (int)(out_tok + c0), (int)out_row, smem_u32(mine));
                 } else {
-                    const uint32_t c = threadIdx.x & (kPer - 1), t = tok0 + c0 + c;
-                    for (uint32_t q = (threadIdx.x & 127) / kPer; q < 128 && row0 + q < P.n_rows; q += 128 / kPer)
+                    const uint32_t c = threadIdx.x & (kPer - 1), t = out_tok + c0 + c;
+                    for (uint32_t q = (threadIdx.x & 127) / kPer; q < 128 && out_row + q < P.n_rows; q += 128 / kPer)
                         if (t < P.n_tok)
-                            ((O *)P.out)[(row0 + q) * P.out_stride + t] =
+                            ((O *)P.out)[(out_row + q) * P.out_stride + t] =
                                 *reinterpret_cast<O *>(mine + q * 128 + (((c / kVec) ^ (q & 7)) << 4) + c % kVec * sizeof(O));
                 }
             }

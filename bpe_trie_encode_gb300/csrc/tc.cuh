@@ -26,24 +26,27 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive_far(uint32_t bar, uint32_t rank) {
     asm volatile(
         "{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %0, %1;\n"
-        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(bar), "r"(rank) : "memory");
+        "mbarrier.arrive.shared::cluster.b64 _, [a];\n}" ::"r"(bar), "r"(rank) : "memory");
 }
 
-// Waits until the phase with this parity has ended.  A try sleeps for about a
-// microsecond at most, so the wait gives up (false) after about two seconds,
-// far beyond any copy or product that it could be for.
-constexpr uint32_t kWaitTries = 1u << 21;
+// Waits until the phase with this parity has ended; gives up (false) after
+// about two seconds, far beyond any copy or product that it could be for.
+constexpr long long kWaitCycles = 4000000000ll;
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.b32 %0, 1, 0, p;\n}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-    for (uint32_t i = 0; i < kWaitTries; i++) {
-        uint32_t ok;
-        asm volatile(
-            "{\n.reg .pred p;\n"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n"
-            "selp.b32 %0, 1, 0, p;\n}"
-            : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-        if (ok) return true;
-    }
-    return false;
+    if (mbar_try(bar, parity)) return true;
+    const long long begin = clock64();
+    while (!mbar_try(bar, parity))
+        if (clock64() - begin > kWaitCycles) return false;
+    return true;
 }
 
 // ------------------------------------------------------------------- TMA ---
@@ -120,29 +123,39 @@ __device__ __forceinline__ void tmem_wait(float (&r)[N]) {
 }
 
 // --------------------------------------------------------------- product ---
-// A K-major operand in shared memory as TMA writes it with the 128-byte
-// swizzle: rows of 128 bytes, groups of 8 rows 1024 bytes apart.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t smem) {
-    return (uint64_t)((smem & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
-           (uint64_t)2 << 61;
+// One lane of a converged warp.  What it alone executes has operands that the
+// compiler knows to be the same for the warp, which tcgen05 wants: behind a
+// test of the lane number each product took over 100 cycles to issue.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.b32 %0, 1, 0, p;\n}" : "=r"(ok));
+    return ok != 0;
 }
+
+// A K-major operand in shared memory as TMA writes it with the 128-byte
+// swizzle: rows of 128 bytes, groups of 8 rows 1024 bytes apart.  The low word
+// of its descriptor holds the address in units of 16 bytes.
+__device__ __forceinline__ uint32_t operand_lo(uint32_t smem) { return (smem & 0x3FFFFu) >> 4 | 1u << 16; }
+constexpr uint32_t kOperandHi = 1024 >> 4 | 1u << 14 | 2u << 29;
 // Instruction word: f32 accumulators, both operands e4m3 and K-major.
 __host__ __device__ constexpr uint32_t e4m3_instr(int m, int n) { return 1u << 4 | (uint32_t)(n / 8) << 17 | (uint32_t)(m / 16) << 24; }
 
 // 32 columns (bytes) of K: D (+)= A B^T.
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, bool add) {
+template <bool kAdd>
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t instr) {
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
-        ::"r"(d), "l"(a), "l"(b), "r"(instr), "r"((uint32_t)add) : "memory");
+        "{\n.reg .pred p;\n.reg .b64 a, b;\nsetp.ne.b32 p, %4, 0;\nmov.b64 a, {%1, %5};\nmov.b64 b, {%2, %5};\n"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n}"
+        ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(instr), "n"(kAdd ? 1 : 0), "n"(kOperandHi) : "memory");
 }
 // The same by a pair of CTAs (cluster ranks 0 and 1): each holds half of A's rows, half of B's, and the sums of its
 // own rows of A.  Issued by rank 0.
-__device__ __forceinline__ void mma_e4m3_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, bool add) {
+template <bool kAdd>
+__device__ __forceinline__ void mma_e4m3_pair(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t instr) {
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
-        ::"r"(d), "l"(a), "l"(b), "r"(instr), "r"((uint32_t)add) : "memory");
+        "{\n.reg .pred p;\n.reg .b64 a, b;\nsetp.ne.b32 p, %4, 0;\nmov.b64 a, {%1, %5};\nmov.b64 b, {%2, %5};\n"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, p;\n}"
+        ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(instr), "n"(kAdd ? 1 : 0), "n"(kOperandHi) : "memory");
 }
 // The barrier is arrived on when the products issued so far are done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
