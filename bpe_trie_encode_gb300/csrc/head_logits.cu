@@ -13,6 +13,8 @@
 
 #include <cudaTypedefs.h>
 
+#include <type_traits>
+
 #include "device.cuh"
 #include "internal.h"
 #include "tc.cuh"
@@ -356,28 +358,30 @@ k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         constexpr int kPer = 128 / sizeof(O);       // tokens in 128 bytes
         constexpr int kVec = 16 / sizeof(O);
         int buf = 0;
-        uint32_t bphase = 0, row0, tok0;
+        uint32_t bphase = 0;
         const uint32_t last = P.blocks - 1;
+        // tile i + teams is row_step tiles of rows and tok_step of tokens further
+        const uint32_t row_step = teams % row_tiles, tok_step = teams / row_tiles;
+        uint32_t row_tile = team % row_tiles, tok_tile = team / row_tiles;
         const float *xs, *ws;
-        float sx0, sw0, sx1, sw1;   // the scales of the next two blocks
-        auto begin = [&](uint32_t i) {
-            row0 = i % row_tiles * M::kRows + rank * 128, tok0 = i / row_tiles * kManyToks + group * 64;
-            xs = P.xs + (uint64_t)min(row0 + r, P.n_rows - 1) * P.xs_row;
-            ws = P.ws + (uint64_t)min(tok0 / kBlock, (P.n_tok - 1) / kBlock) * P.ws_row;
+        float sx0, sw0, sx1, sw1;   // the scales of a tile's first two blocks
+        auto begin = [&] {
+            xs = P.xs + (uint64_t)min(row_tile * M::kRows + rank * 128 + r, P.n_rows - 1) * P.xs_row;
+            ws = P.ws + (uint64_t)min((tok_tile * kManyToks + group * 64) / kBlock, (P.n_tok - 1) / kBlock) * P.ws_row;
             sx0 = xs[0], sw0 = ws[0], sx1 = xs[min(1u, last) * P.xs_blk], sw1 = ws[min(1u, last) * P.ws_blk];
         };
-        if (team < n_tiles) begin(team);
+        if (team < n_tiles) begin();
         for (uint32_t i = team; i < n_tiles; i += teams) {
             float acc[64];
-#pragma unroll
-            for (int c = 0; c < 64; c++) acc[c] = 0.0f;
             bool ok = true;
-            for (uint32_t b = 0; b < P.blocks; b++) {
-                const float s = sx0 * sw0;
-                sx0 = sx1, sw0 = sw1;
-                sx1 = xs[min(b + 2, last) * P.xs_blk];
-                sw1 = ws[min(b + 2, last) * P.ws_blk];
-                if (!__all_sync(kFull, mbar_wait(done(buf), bphase))) { ok = false; break; }
+            const float *const tx = xs, *const tw = ws;
+            float ax = sx0, aw = sw0, bx = sx1, bw = sw1;
+            auto add = [&](uint32_t b, auto first) {
+                const float s = ax * aw;
+                ax = bx, aw = bw;
+                bx = tx[min(b + 2, last) * P.xs_blk];
+                bw = tw[min(b + 2, last) * P.ws_blk];
+                if (!__all_sync(kFull, mbar_wait(done(buf), bphase))) { ok = false; return; }
                 tc_fence_after();
                 const uint32_t at = tmem + ((uint32_t)quarter << 21) + buf * kManyToks + group * 64;
 #pragma unroll
@@ -395,13 +399,17 @@ k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                         }
                     }
 #pragma unroll
-                    for (int c = 0; c < 16; c++) acc[c0 + c] = fmaf(d[c], s, acc[c0 + c]);
+                    for (int c = 0; c < 16; c++) acc[c0 + c] = decltype(first)::value ? d[c] * s : fmaf(d[c], s, acc[c0 + c]);
                 }
                 if (++buf == 2) buf = 0, bphase ^= 1;
-            }
+            };
+            add(0, std::true_type());
+            for (uint32_t b = 1; b < P.blocks && ok; b++) add(b, std::false_type());
             if (!ok) { *gave_up = 1; break; }
-            const uint32_t out_row = row0, out_tok = tok0;
-            if (i + teams < n_tiles) begin(i + teams);   // the next tile's first scales arrive while this one leaves
+            const uint32_t row0 = row_tile * M::kRows + rank * 128, tok0 = tok_tile * kManyToks + group * 64;
+            row_tile += row_step, tok_tile += tok_step;
+            if (row_tile >= row_tiles) row_tile -= row_tiles, tok_tile++;
+            if (i + teams < n_tiles) begin();   // the next tile's first scales arrive while this one leaves
 #pragma unroll
             for (int c0 = 0; c0 < 64; c0 += kPer) {
                 if (P.tma_out && quarter == 0 && lane == 0) tma_store_wait();
@@ -412,13 +420,13 @@ k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 if (P.tma_out) fence_for_tma();
                 asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
                 if (P.tma_out) {
-                    if (quarter == 0 && lane == 0 && out_row < P.n_rows && out_tok + c0 < P.n_tok)
-                        tma_store(&map_out, (int)(out_tok + c0), (int)out_row, smem_u32(mine));
+                    if (quarter == 0 && lane == 0 && row0 < P.n_rows && tok0 + c0 < P.n_tok)
+                        tma_store(&map_out, (int)(tok0 + c0), (int)row0, smem_u32(mine));
                 } else {
-                    const uint32_t c = threadIdx.x & (kPer - 1), t = out_tok + c0 + c;
-                    for (uint32_t q = (threadIdx.x & 127) / kPer; q < 128 && out_row + q < P.n_rows; q += 128 / kPer)
+                    const uint32_t c = threadIdx.x & (kPer - 1), t = tok0 + c0 + c;
+                    for (uint32_t q = (threadIdx.x & 127) / kPer; q < 128 && row0 + q < P.n_rows; q += 128 / kPer)
                         if (t < P.n_tok)
-                            ((O *)P.out)[(out_row + q) * P.out_stride + t] =
+                            ((O *)P.out)[(row0 + q) * P.out_stride + t] =
                                 *reinterpret_cast<O *>(mine + q * 128 + (((c / kVec) ^ (q & 7)) << 4) + c % kVec * sizeof(O));
                 }
             }
