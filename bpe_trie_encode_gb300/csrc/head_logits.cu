@@ -34,179 +34,169 @@ struct LogitsParams {
 };
 
 // ------------------------------------------------------------- few rows ----
-// Up to 64 rows: the bound is reading the weights once.  The weights are the
-// product's 128-row side, so that a tile is 128 tokens by kN rows of x, and
-// each lane of tensor memory is a token: its scale is the same for the whole
-// tile, and row r's scale comes from lane r by a shuffle.  Several CTAs share
-// an SM, each with a few stages; a cluster splits the columns of one tile when
-// there are too few tiles to fill the GPU, and joins the parts through
-// distributed shared memory in a fixed order.
-constexpr int kFewThreads = 192;   // 4 warps scale and add, 1 loads, 1 multiplies
-constexpr int kFewStages = 3;
+// Up to 128 rows: the bound is reading the weights once.  The weights are the
+// product's 128-row side, the kN rows of x the other.  Each SM streams its own
+// contiguous share of the vocabulary, in steps of 16 tokens, through one
+// CTA's ring of stages: shares are equal to within a step, so that all SMs end
+// together, and a vocabulary of a few thousand tokens still spreads over all of
+// them.  A lane of tensor memory is a token; row r's scale comes from lane r by
+// a shuffle, the token's own is the lane's.
+constexpr int kFewThreads = 320;   // 8 warps scale and add, 1 loads, 1 multiplies
+constexpr int kStep = 16;          // tokens per load
 
 template <int kN> struct Few {
-    static constexpr int kBufs = kN == 64 ? 2 : 4;
-    static constexpr int kCols = kN * kBufs;                    // 64, 128 or 128 of tensor memory
+    static constexpr int kBufs = 4;
+    static constexpr int kCols = kN * kBufs;                    // of tensor memory
     static constexpr int kStage = (128 + kN) * kBlock;
-    static constexpr int kSmem = kFewStages * kStage + 1024 + 256;
-    static constexpr int kPerSm = kN == 16 ? 4 : 3;
+    static constexpr int kStages = kN == 16 ? 12 : kN == 32 ? 11 : kN == 64 ? 9 : 7;
+    static constexpr int kSmem = kStages * kStage + 1024 + 512;
+    static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
 
 template <int kN, typename O>
-__global__ void __launch_bounds__(kFewThreads, Few<kN>::kPerSm)
+__global__ void __launch_bounds__(kFewThreads, 1)
 k_logits_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, LogitsParams P,
-             uint32_t split) {
+             uint32_t share) {
     using F = Few<kN>;
+    constexpr int kStages = F::kStages, kHalf = kN / 2;   // a warp adds half of the rows
     extern __shared__ uint8_t raw[];
     uint8_t *base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     const uint32_t tiles = smem_u32(base);
-    const uint32_t bars = tiles + kFewStages * F::kStage;
-    uint32_t *extra = (uint32_t *)(base + kFewStages * F::kStage + 128);   // [0] tensor memory, [1] gave up
+    const uint32_t bars = tiles + kStages * F::kStage;
+    uint32_t *extra = (uint32_t *)(base + kStages * F::kStage + 448);   // [0] tensor memory, [1] gave up
     auto full = [&](int s) { return bars + 8 * s; };
-    auto empty = [&](int s) { return bars + 8 * (kFewStages + s); };
-    auto done = [&](int b) { return bars + 8 * (2 * kFewStages + b); };
-    auto taken = [&](int b) { return bars + 8 * (2 * kFewStages + F::kBufs + b); };
+    auto empty = [&](int s) { return bars + 8 * (kStages + s); };
+    auto done = [&](int b) { return bars + 8 * (2 * kStages + b); };
+    auto taken = [&](int b) { return bars + 8 * (2 * kStages + F::kBufs + b); };
     const int warp = __shfl_sync(kFull, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const uint32_t part = blockIdx.x % split, tile = blockIdx.x / split;
-    const uint32_t b0 = (uint32_t)((uint64_t)P.blocks * part / split), b1 = (uint32_t)((uint64_t)P.blocks * (part + 1) / split);
-    const uint32_t tok0 = tile * 128, row0 = blockIdx.y * kN;
+    const uint32_t begin = min(P.n_tok, blockIdx.x * share), end = min(P.n_tok, begin + share);
     volatile uint32_t *gave_up = extra + 1;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kFewStages; s++) mbar_init(full(s), 1), mbar_init(empty(s), 1);
-        for (int b = 0; b < F::kBufs; b++) mbar_init(done(b), 1), mbar_init(taken(b), 4);
+        for (int s = 0; s < kStages; s++) mbar_init(full(s), 1), mbar_init(empty(s), 1);
+        for (int b = 0; b < F::kBufs; b++) mbar_init(done(b), 1), mbar_init(taken(b), 8);
         extra[1] = 0;
         mbar_init_fence();
     }
-    if (warp == 5) tmem_alloc(smem_u32(extra), F::kCols);
+    if (warp == 9) tmem_alloc(smem_u32(extra), F::kCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = extra[0];
 
-    float acc[kN];
-#pragma unroll
-    for (int c = 0; c < kN; c++) acc[c] = 0.0f;
-
-    if (warp == 4) {
+    if (warp == 8) {
         tma_prefetch_map(&map_w);
         tma_prefetch_map(&map_x);
         int s = 0;
         uint32_t phase = 1, issued = 0;
-        for (uint32_t b = b0; b < b1; b++) {
-            if (!__all_sync(kFull, mbar_wait(empty(s), phase))) { *gave_up = 1; break; }
-            if (elect_one()) {
-                mbar_expect(full(s), F::kStage);
-                tma_load(tiles + s * F::kStage, &map_w, (int)(b * kBlock), (int)tok0, full(s));
-                tma_load(tiles + s * F::kStage + 128 * kBlock, &map_x, (int)(b * kBlock), (int)row0, full(s));
+        for (uint32_t tok = begin; tok < end && !__any_sync(kFull, *gave_up); tok += 128) {
+            const uint32_t steps = (min(128u, end - tok) + kStep - 1) / kStep;
+            for (uint32_t b = 0; b < P.blocks; b++) {
+                if (!__all_sync(kFull, mbar_wait(empty(s), phase))) { *gave_up = 1; break; }
+                if (elect_one()) {
+                    const uint32_t at = tiles + s * F::kStage;
+                    mbar_expect(full(s), (steps * kStep + kN) * kBlock);
+                    tma_load(at + 128 * kBlock, &map_x, (int)(b * kBlock), 0, full(s));
+                    for (uint32_t i = 0; i < steps; i++)   // what a short tile leaves of the stage keeps old weights, whose sums go nowhere
+                        tma_load(at + i * kStep * kBlock, &map_w, (int)(b * kBlock), (int)(tok + i * kStep), full(s));
+                }
+                issued++;
+                if (++s == kStages) s = 0, phase ^= 1;
             }
-            issued++;
-            if (++s == kFewStages) s = 0, phase ^= 1;
         }
         if (*gave_up)   // no copy may be in flight when the CTA ends
-            for (uint32_t i = issued > kFewStages ? issued - kFewStages : 0; i < issued; i++)
-                mbar_wait(full(i % kFewStages), (i / kFewStages) & 1);
-    } else if (warp == 5) {
+            for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; i++)
+                mbar_wait(full(i % kStages), (i / kStages) & 1);
+    } else if (warp == 9) {
         int s = 0, buf = 0;
         uint32_t phase = 0, bphase = 1;
         const uint32_t w0 = operand_lo(tiles), x0 = operand_lo(tiles + 128 * kBlock);
-        for (uint32_t b = b0; b < b1; b++) {
-            if (!__all_sync(kFull, mbar_wait(taken(buf), bphase) && mbar_wait(full(s), phase))) { *gave_up = 1; break; }
-            tc_fence_after();
-            if (elect_one()) {
-                const uint32_t w = w0 + s * (F::kStage >> 4), x = x0 + s * (F::kStage >> 4), d = tmem + buf * kN;
-                constexpr uint32_t kInstr = e4m3_instr(128, kN);
-                mma_e4m3<false>(d, w, x, kInstr);
-                mma_e4m3<true>(d, w + 2, x + 2, kInstr);
-                mma_e4m3<true>(d, w + 4, x + 4, kInstr);
-                mma_e4m3<true>(d, w + 6, x + 6, kInstr);
-                mma_commit(done(buf));
-                mma_commit(empty(s));
+        for (uint32_t tok = begin; tok < end && !__any_sync(kFull, *gave_up); tok += 128) {
+            for (uint32_t b = 0; b < P.blocks; b++) {
+                if (!__all_sync(kFull, mbar_wait(taken(buf), bphase) && mbar_wait(full(s), phase))) { *gave_up = 1; break; }
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t w = w0 + s * (F::kStage >> 4), x = x0 + s * (F::kStage >> 4), d = tmem + buf * kN;
+                    constexpr uint32_t kInstr = e4m3_instr(128, kN);
+                    mma_e4m3<false>(d, w, x, kInstr);
+                    mma_e4m3<true>(d, w + 2, x + 2, kInstr);
+                    mma_e4m3<true>(d, w + 4, x + 4, kInstr);
+                    mma_e4m3<true>(d, w + 6, x + 6, kInstr);
+                    mma_commit(done(buf));
+                    mma_commit(empty(s));
+                }
+                if (++s == kStages) s = 0, phase ^= 1;
+                if (++buf == F::kBufs) buf = 0, bphase ^= 1;
             }
-            if (++s == kFewStages) s = 0, phase ^= 1;
-            if (++buf == F::kBufs) buf = 0, bphase ^= 1;
         }
     } else {
-        constexpr int kPer = (kN + 31) / 32;   // row scales that a lane holds
-        const float *ws = P.ws + tile * P.ws_row;
-        float sx[kPer];
-        auto scales = [&](uint32_t b) {
-            const float sw = b < b1 ? ws[b * P.ws_blk] : 0.0f;
-#pragma unroll
-            for (int i = 0; i < kPer; i++) {
-                const uint32_t r = row0 + i * 32 + lane;
-                sx[i] = b < b1 && r < P.n_rows && i * 32 + lane < kN ? P.xs[r * P.xs_row + b * P.xs_blk] * sw : 0.0f;
-            }
-        };
-        scales(b0);
+        constexpr int kPer = (kHalf + 31) / 32;   // row scales that a lane holds
+        const int quarter = warp & 3, col0 = (warp >> 2) * kHalf;
+        const uint32_t last = P.blocks - 1;
         int buf = 0;
         uint32_t bphase = 0;
-        for (uint32_t b = b0; b < b1; b++) {
-            float s[kPer];
+        struct Scales { float w, x[kPer]; };
+        const float *xs[kPer];
 #pragma unroll
-            for (int i = 0; i < kPer; i++) s[i] = sx[i];
-            scales(b + 1);
-            if (!__all_sync(kFull, mbar_wait(done(buf), bphase))) { *gave_up = 1; break; }
-            tc_fence_after();
-            constexpr int kStep = kN < 32 ? kN : 32;
+        for (int i = 0; i < kPer; i++)   // lanes past the rows read a scale that nothing uses
+            xs[i] = P.xs + min((uint32_t)(col0 + i * 32 + lane), P.n_rows - 1) * P.xs_row;
+        bool ok = true;
+        for (uint32_t tok = begin; tok < end && ok; tok += 128) {
+            const uint32_t t = tok + quarter * 32 + lane;
+            const float *ws = P.ws + (uint64_t)(min(t, P.n_tok - 1) / kBlock) * P.ws_row;
+            auto load = [&](uint32_t b) {
+                Scales s;
+                b = min(b, last);
+                s.w = ws[b * P.ws_blk];
 #pragma unroll
-            for (int c0 = 0; c0 < kN; c0 += kStep) {
-                float d[kStep];
-                tmem_load(d, tmem + ((uint32_t)warp << 21) + buf * kN + c0);
-                tmem_wait(d);
-                if (c0 + kStep == kN) {
-                    tc_fence_before();
-                    if (lane == 0) mbar_arrive(taken(buf));
+                for (int i = 0; i < kPer; i++) s.x[i] = xs[i][b * P.xs_blk];
+                return s;
+            };
+            float acc[kHalf];
+#pragma unroll
+            for (int c = 0; c < kHalf; c++) acc[c] = 0.0f;
+            auto add = [&](const Scales &s) {
+                if (!__all_sync(kFull, mbar_wait(done(buf), bphase))) { ok = false; return; }
+                tc_fence_after();
+                constexpr int kLoad = kHalf < 32 ? kHalf : 32;
+#pragma unroll
+                for (int c0 = 0; c0 < kHalf; c0 += kLoad) {
+                    float d[kLoad];
+                    tmem_load(d, tmem + ((uint32_t)quarter << 21) + buf * kN + col0 + c0);
+                    tmem_wait(d);
+                    if (c0 + kLoad == kHalf) {
+                        tc_fence_before();
+                        if (lane == 0) mbar_arrive(taken(buf));
+                    }
+#pragma unroll
+                    for (int c = 0; c < kLoad; c++)
+                        acc[c0 + c] = fmaf(d[c], s.w * __shfl_sync(kFull, s.x[c0 / 32], c), acc[c0 + c]);
                 }
-#pragma unroll
-                for (int c = 0; c < kStep; c++)
-                    acc[c0 + c] = fmaf(d[c], __shfl_sync(kFull, s[c0 / 32], c), acc[c0 + c]);
+                if (++buf == F::kBufs) buf = 0, bphase ^= 1;
+            };
+            // two blocks in turn, so that a block's scales have two blocks' time to arrive
+            Scales s0 = load(0), s1 = load(1);
+            for (uint32_t b = 0; b < P.blocks && ok; b += 2) {
+                add(s0);
+                s0 = load(b + 2);
+                if (b + 1 < P.blocks && ok) add(s1);
+                s1 = load(b + 3);
             }
-            if (++buf == F::kBufs) buf = 0, bphase ^= 1;
+            if (ok && t < end) {
+                O *out = (O *)P.out + t;
+#pragma unroll
+                for (int c = 0; c < kHalf; c++)
+                    if (col0 + c < P.n_rows) out[(uint64_t)(col0 + c) * P.out_stride] = from_f32<O>(acc[c]);
+            }
         }
+        if (!ok) *gave_up = 1;
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 5) tmem_free(tmem, F::kCols);
-    const bool failed = *gave_up != 0;
-    if (failed && threadIdx.x == 0) *P.status = DERR_TIMEOUT;
-    O *out = (O *)P.out;
-    const uint32_t t = tok0 + warp * 32 + lane;
-    if (split == 1) {
-        if (warp < 4 && t < P.n_tok && !failed) {
-#pragma unroll
-            for (int c = 0; c < kN; c++)
-                if (row0 + c < P.n_rows) out[(row0 + c) * P.out_stride + t] = from_f32<O>(acc[c]);
-        }
-        return;
-    }
-    // join: every CTA's stages are idle now and hold its part; CTA i adds up rows i, i + split, ...
-    float *mine = (float *)base;
-    if (warp < 4) {
-#pragma unroll
-        for (int c = 0; c < kN; c++) mine[c * 128 + warp * 32 + lane] = acc[c];
-    }
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (warp < 4) {
-        for (uint32_t c = part; c < kN && row0 + c < P.n_rows; c += split) {
-            const uint32_t at = smem_u32(mine + c * 128 + warp * 32 + lane);
-            float v[8];
-#pragma unroll
-            for (uint32_t p = 0; p < 8; p++) {
-                v[p] = 0.0f;
-                if (p < split) {
-                    uint32_t far;
-                    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(at), "r"(p));
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[p]) : "r"(far) : "memory");
-                }
-            }
-            const float sum = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
-            if (t < P.n_tok && !failed) out[(row0 + c) * P.out_stride + t] = from_f32<O>(sum);
-        }
-    }
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (warp == 9) tmem_free(tmem, F::kCols);
+    if (threadIdx.x == 0 && *gave_up) *P.status = DERR_TIMEOUT;
 }
 
 // ------------------------------------------------------------ many rows ----
@@ -528,23 +518,11 @@ int aligned_rows(bpe_ctx *ctx, Slot slot, const uint8_t *&p, uint64_t &stride, u
 template <int kN, typename O>
 int launch_few(bpe_ctx *ctx, const CUtensorMap &mw, const CUtensorMap &mx, const LogitsParams &P) {
     using F = Few<kN>;
-    const uint32_t tiles = (P.n_tok + 127) / 128, rows = (P.n_rows + kN - 1) / kN;
-    // split the columns while all parts still run at once and a part has four blocks
-    uint32_t split = 1;
-    while (split < 8 && tiles * rows * split * 2 <= (uint32_t)(ctx->sm_count * F::kPerSm) && P.blocks >= split * 8) split *= 2;
+    const uint32_t steps = (P.n_tok + kStep - 1) / kStep, each = (steps + ctx->sm_count - 1) / ctx->sm_count;
     auto k = k_logits_few<kN, O>;
     BPE_CUDA(ctx, cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem), "head_logits");
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(tiles * split, rows);
-    cfg.blockDim = dim3(kFewThreads);
-    cfg.dynamicSmemBytes = F::kSmem;
-    cfg.stream = ctx->stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {split, 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = split > 1 ? 1 : 0;
-    BPE_CUDA(ctx, cudaLaunchKernelEx(&cfg, k, mw, mx, P, split), "head_logits launch");
+    k<<<(steps + each - 1) / each, kFewThreads, F::kSmem, ctx->stream>>>(mw, mx, P, each * kStep);
+    BPE_CUDA(ctx, cudaGetLastError(), "head_logits launch");
     return BPE_OK;
 }
 
@@ -580,17 +558,18 @@ int launch_many(bpe_ctx *ctx, const CUtensorMap &mw, const CUtensorMap &mx, cons
 
 template <typename O>
 int launch(bpe_ctx *ctx, const uint8_t *x8, uint64_t x_stride, const uint8_t *w8, uint64_t w_stride, uint32_t dim, LogitsParams P) {
-    const int n = P.n_rows <= 16 ? 16 : P.n_rows <= 32 ? 32 : P.n_rows <= 64 ? 64 : 0;
+    const int n = P.n_rows <= 16 ? 16 : P.n_rows <= 32 ? 32 : P.n_rows <= 64 ? 64 : P.n_rows <= 128 ? 128 : 0;
     // a pair's 256 rows where they waste no more than 128-row tiles would
     const bool pair = !n && (P.n_rows + 127) / 128 % 2 == 0;
     CUtensorMap mw, mx, mo = {};
     int rc;
-    if ((rc = encode_map(ctx, &mw, w8, w_stride, P.n_tok, dim, n || pair ? 128 : kManyToks)) ||
+    if ((rc = encode_map(ctx, &mw, w8, w_stride, P.n_tok, dim, n ? kStep : pair ? 128 : kManyToks)) ||
         (rc = encode_map(ctx, &mx, x8, x_stride, P.n_rows, dim, n ? n : 128)))
         return rc;
     if (n == 16) return launch_few<16, O>(ctx, mw, mx, P);
     if (n == 32) return launch_few<32, O>(ctx, mw, mx, P);
     if (n == 64) return launch_few<64, O>(ctx, mw, mx, P);
+    if (n == 128) return launch_few<128, O>(ctx, mw, mx, P);
     P.tma_out = (uintptr_t)P.out % 16 == 0 && P.out_stride * sizeof(O) % 16 == 0 && P.out_stride * sizeof(O) < (1ull << 40);
     if (P.tma_out && (rc = encode_out<O>(ctx, &mo, P))) return rc;
     return pair ? launch_many<O, 2>(ctx, mw, mx, mo, P) : launch_many<O, 1>(ctx, mw, mx, mo, P);

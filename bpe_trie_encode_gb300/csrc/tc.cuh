@@ -93,7 +93,7 @@ __device__ __forceinline__ void tmem_free_pair(uint32_t base, uint32_t cols) {
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// 16 or 32 columns of the warp's 32 lanes: column c of lane l to r[c] of thread l.
+// 8, 16 or 32 columns of the warp's 32 lanes: column c of lane l to r[c] of thread l.
 __device__ __forceinline__ void tmem_load(float (&r)[32], uint32_t addr) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -112,6 +112,11 @@ __device__ __forceinline__ void tmem_load(float (&r)[16], uint32_t addr) {
         : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
           "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
         : "r"(addr));
+}
+__device__ __forceinline__ void tmem_load(float (&r)[8], uint32_t addr) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+                 : "r"(addr));
 }
 // The loads issued so far have arrived.  The registers pass through, so that
 // nothing that reads them is moved above the wait.
