@@ -39,7 +39,13 @@ from ._capi import (BPE_MAX_MERGES, BPE_MERGE_LISTS, BPE_MERGE_LOOKBACK, BPE_MER
 __all__ = ["Context", "Trie", "Unigram", "BpeError", "vocab_from_merges", "BPE_WORD_START", "BPE_MAX_MERGES"]
 
 
+# the current stream's handle without a Stream object around it, where torch has that (2 us of a call's 10)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_ptr(device: torch.device) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
@@ -57,45 +63,54 @@ _HEAD_TYPES = {torch.float32: _capi.BPE_F32, torch.bfloat16: _capi.BPE_BF16, tor
 _E4M3 = torch.float8_e4m3fn
 
 
-def _head_matrix(t: torch.Tensor, name: str, device: torch.device, dtypes, shape=None, out: bool = False) -> torch.Tensor:
-    """A CUDA matrix whose rows are contiguous (an input is copied where they are not)."""
+def _head_place(t, name: str, device: torch.device, dtypes) -> None:
+    """The error of a tensor that is not a CUDA tensor of the context's device and of one of the types."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the context is on {device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must be {'a matrix' if shape is None else tuple(shape)}, got {tuple(t.shape)}")
-    rows, cols = t.shape
-    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+    raise ValueError(f"{name} is on {t.device}, the context is on {device}")
+
+
+def _head_matrix(t: torch.Tensor, name: str, device: torch.device, dtypes, shape=None, out: bool = False):
+    """(matrix, distance of its rows): a CUDA matrix whose rows are contiguous; an input is copied where they are not."""
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype not in dtypes:
+        _head_place(t, name, device, dtypes)
+    size, stride = t.shape, t.stride()
+    if len(stride) != 2 or (shape is not None and size != shape):
+        raise ValueError(f"{name} must be {'a matrix' if shape is None else tuple(shape)}, got {tuple(size)}")
+    if (stride[1] != 1 and size[1] > 1) or (stride[0] < size[1] and size[0] > 1):
         if out:
             raise ValueError(f"{name}: the rows of an output must be contiguous and apart")
         t = t.contiguous()
-    return t
+        return t, t.stride(0)
+    return t, stride[0]
 
 
-def _head_scales(t: torch.Tensor, name: str, device: torch.device, rows: int, blocks: int, out: bool = False) -> None:
-    """Scales may lie in any order; those of an output may not share a place."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32:
-        raise TypeError(f"{name} must be a float32 CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the context is on {device}")
+def _head_scales(t: torch.Tensor, name: str, device: torch.device, rows: int, blocks: int, out: bool = False):
+    """The distances of rows and of blocks.  Scales may lie in any order; those of an output may not share a place."""
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype is not torch.float32:
+        _head_place(t, name, device, (torch.float32,))
     if t.shape != (rows, blocks):
         raise ValueError(f"{name} must be {(rows, blocks)}, got {tuple(t.shape)}")
-    if out:
-        (s0, n0), (s1, n1) = sorted(((t.stride(0), rows), (t.stride(1), blocks)))
-        if (n0 > 1 and s0 == 0) or (n1 > 1 and s1 < (n0 - 1) * s0 + 1):
+    s0, s1 = t.stride()
+    if out and not (0 < s1 * blocks <= s0 or 0 < s0 * rows <= s1):
+        (a, n), (b, m) = sorted(((s0, rows), (s1, blocks)))
+        if (n > 1 and a == 0) or (m > 1 and b < (n - 1) * a + 1):
             raise ValueError(f"{name}: the scales of an output must lie apart")
+    return s0, s1
 
 
 def _head_vector(t: torch.Tensor, name: str, device: torch.device, dtype: torch.dtype, rows: int,
                  out: bool = False) -> torch.Tensor:
-    if out and isinstance(t, torch.Tensor) and not t.is_contiguous():
-        raise ValueError(f"{name}: an output must be contiguous")
-    t = _need_cuda(t, dtype, name, device)
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype is not dtype:
+        _head_place(t, name, device, (dtype,))
     if t.shape != (rows,):
         raise ValueError(f"{name} must be ({rows},), got {tuple(t.shape)}")
+    if rows > 1 and t.stride(0) != 1:
+        if out:
+            raise ValueError(f"{name}: an output must be contiguous")
+        t = t.contiguous()
     return t
 
 
@@ -312,35 +327,32 @@ class Context:
         sum is written when a residual is given or residual_out is; it may be x
         or the residual itself.  Asynchronous on the current stream."""
         dev = self.device
-        x = _head_matrix(x, "x", dev, _HEAD_TYPES)
-        rows, dim = x.shape
+        x, x_stride = _head_matrix(x, "x", dev, _HEAD_TYPES)
+        size, dtype = x.shape, x.dtype
+        rows, dim = size
         if not isinstance(weight, torch.Tensor) or weight.dtype not in _HEAD_TYPES:
             raise TypeError("weight must be a float32, bfloat16 or float16 tensor")
-        weight = _need_cuda(weight, weight.dtype, "weight", dev)
-        if weight.shape != (dim,):
-            raise ValueError(f"weight must be ({dim},), got {tuple(weight.shape)}")
+        weight = _head_vector(weight, "weight", dev, weight.dtype, dim)
+        r_ptr, r_stride, ro_ptr, ro_stride = None, 0, None, 0
         if residual is not None:
-            residual = _head_matrix(residual, "residual", dev, (x.dtype,), x.shape)
+            residual, r_stride = _head_matrix(residual, "residual", dev, (dtype,), size)
+            r_ptr = residual.data_ptr()
             if residual_out is None:
-                residual_out = torch.empty(rows, dim, dtype=x.dtype, device=dev)
+                residual_out = torch.empty(rows, dim, dtype=dtype, device=dev)
         if residual_out is not None:
-            residual_out = _head_matrix(residual_out, "residual_out", dev, (x.dtype,), x.shape, out=True)
+            residual_out, ro_stride = _head_matrix(residual_out, "residual_out", dev, (dtype,), size, out=True)
+            ro_ptr = residual_out.data_ptr()
         if out is None:   # rows start on 16 bytes, which the product reads without a copy
             out = torch.empty(rows, -(-dim // 16) * 16, dtype=_E4M3, device=dev)[:, :dim]
-        else:
-            out = _head_matrix(out, "out", dev, (_E4M3,), x.shape, out=True)
+        out, y_stride = _head_matrix(out, "out", dev, (_E4M3,), size, out=True)
         blocks = -(-dim // _capi.BPE_HEAD_BLOCK)
         if scales is None:
             scales = torch.empty(blocks, rows, dtype=torch.float32, device=dev).t()
-        else:
-            _head_scales(scales, "scales", dev, rows, blocks, out=True)
+        s_row, s_block = _head_scales(scales, "scales", dev, rows, blocks, out=True)
         self._sync_stream()
-        rc = self.lib.head_norm(self._h, x.data_ptr(), x.stride(0), _HEAD_TYPES[x.dtype], weight.data_ptr(),
-                                _HEAD_TYPES[weight.dtype], residual.data_ptr() if residual is not None else None,
-                                residual.stride(0) if residual is not None else 0, rows, dim, eps,
-                                residual_out.data_ptr() if residual_out is not None else None,
-                                residual_out.stride(0) if residual_out is not None else 0, out.data_ptr(),
-                                out.stride(0), scales.data_ptr(), scales.stride(0), scales.stride(1))
+        rc = self.lib.head_norm(self._h, x.data_ptr(), x_stride, _HEAD_TYPES[dtype], weight.data_ptr(),
+                                _HEAD_TYPES[weight.dtype], r_ptr, r_stride, rows, dim, eps, ro_ptr, ro_stride,
+                                out.data_ptr(), y_stride, scales.data_ptr(), s_row, s_block)
         if rc:
             _capi.check(self._h, rc)
         return out, scales, residual_out
@@ -349,13 +361,13 @@ class Context:
         """A weight matrix [n_tok, dim] (f32, bf16 or f16) in 8 bits with one
         scale per 128 x 128 block: (w8 float8_e4m3fn [n_tok, dim], its rows
         starting on 16 bytes, ws f32 [ceil(n_tok / 128), ceil(dim / 128)])."""
-        weight = _head_matrix(weight, "weight", self.device, _HEAD_TYPES)
+        weight, stride = _head_matrix(weight, "weight", self.device, _HEAD_TYPES)
         n_tok, dim = weight.shape
         w8 = torch.empty(n_tok, -(-dim // 16) * 16, dtype=_E4M3, device=self.device)[:, :dim]
         ws = torch.empty(-(-n_tok // _capi.BPE_HEAD_BLOCK), -(-dim // _capi.BPE_HEAD_BLOCK), dtype=torch.float32,
                          device=self.device)
         self._sync_stream()
-        _capi.check(self._h, self.lib.head_quantize(self._h, weight.data_ptr(), weight.stride(0),
+        _capi.check(self._h, self.lib.head_quantize(self._h, weight.data_ptr(), stride,
                                                     _HEAD_TYPES[weight.dtype], n_tok, dim, w8.data_ptr(),
                                                     w8.stride(0), ws.data_ptr(), ws.stride(0)))
         return w8, ws
@@ -369,25 +381,24 @@ class Context:
         given).  Scales may have any strides.  Asynchronous on the current
         stream."""
         dev = self.device
-        x8 = _head_matrix(x8, "x8", dev, (_E4M3,))
-        w8 = _head_matrix(w8, "w8", dev, (_E4M3,))
+        x8, x_stride = _head_matrix(x8, "x8", dev, (_E4M3,))
+        w8, w_stride = _head_matrix(w8, "w8", dev, (_E4M3,))
         rows, dim = x8.shape
-        n_tok = w8.shape[0]
-        if w8.shape[1] != dim:
-            raise ValueError(f"w8 has {w8.shape[1]} columns, x8 {dim}")
+        n_tok, w_dim = w8.shape
+        if w_dim != dim:
+            raise ValueError(f"w8 has {w_dim} columns, x8 {dim}")
         blocks = -(-dim // _capi.BPE_HEAD_BLOCK)
-        _head_scales(xs, "xs", dev, rows, blocks)
-        _head_scales(ws, "ws", dev, -(-n_tok // _capi.BPE_HEAD_BLOCK), blocks)
+        xs_row, xs_block = _head_scales(xs, "xs", dev, rows, blocks)
+        ws_row, ws_block = _head_scales(ws, "ws", dev, -(-n_tok // _capi.BPE_HEAD_BLOCK), blocks)
         if out is None:
             if dtype not in _HEAD_TYPES:
                 raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
             out = torch.empty(rows, n_tok, dtype=dtype, device=dev)
-        else:
-            out = _head_matrix(out, "out", dev, _HEAD_TYPES, (rows, n_tok), out=True)
+        out, out_stride = _head_matrix(out, "out", dev, _HEAD_TYPES, (rows, n_tok), out=True)
         self._sync_stream()
-        rc = self.lib.head_logits(self._h, x8.data_ptr(), x8.stride(0), xs.data_ptr(), xs.stride(0), xs.stride(1),
-                                  w8.data_ptr(), w8.stride(0), ws.data_ptr(), ws.stride(0), ws.stride(1), rows, n_tok,
-                                  dim, out.data_ptr(), out.stride(0), _HEAD_TYPES[out.dtype])
+        rc = self.lib.head_logits(self._h, x8.data_ptr(), x_stride, xs.data_ptr(), xs_row, xs_block, w8.data_ptr(),
+                                  w_stride, ws.data_ptr(), ws_row, ws_block, rows, n_tok, dim, out.data_ptr(),
+                                  out_stride, _HEAD_TYPES[out.dtype])
         if rc:
             _capi.check(self._h, rc)
         return out
@@ -402,7 +413,7 @@ class Context:
         the filtered distribution); a row without a logit above -infinity
         gives -1 and -infinity.  Asynchronous on the current stream."""
         dev = self.device
-        logits = _head_matrix(logits, "logits", dev, _HEAD_TYPES)
+        logits, stride = _head_matrix(logits, "logits", dev, _HEAD_TYPES)
         rows, n_tok = logits.shape
         u = _head_vector(u, "u", dev, torch.float32, rows)
         if ids is None:
@@ -430,7 +441,7 @@ class Context:
         q, d_q = one(min_p, "min_p", torch.float32, 0.0)
         filters = _capi.head_filters(t, k, p, q, d_t, d_k, d_p, d_q)
         self._sync_stream()
-        rc = self.lib.head_sample(self._h, logits.data_ptr(), logits.stride(0), _HEAD_TYPES[logits.dtype], rows, n_tok,
+        rc = self.lib.head_sample(self._h, logits.data_ptr(), stride, _HEAD_TYPES[logits.dtype], rows, n_tok,
                                   u.data_ptr(), ctypes.byref(filters), ids.data_ptr(), logprob.data_ptr())
         if rc:
             _capi.check(self._h, rc)

@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "bpetrie.h"
@@ -36,6 +37,16 @@ __device__ __forceinline__ float block_scale(uint32_t amax) {
 
 __device__ __forceinline__ uint8_t to_e4m3(float v) {
     return (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+}
+
+// Lets a kernel have `bytes` of shared memory on this device; asked of the runtime once per device.
+template <typename K>
+inline cudaError_t allow_shared(K kernel, int device, size_t bytes, std::atomic<uint64_t> &devices) {
+    const uint64_t bit = 1ull << (device & 63);
+    if (device < 64 && (devices.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && device < 64) devices.fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 inline bool head_type_ok(int t) { return t == BPE_F32 || t == BPE_BF16 || t == BPE_F16; }

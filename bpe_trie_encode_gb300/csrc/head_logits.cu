@@ -34,57 +34,60 @@ struct LogitsParams {
 };
 
 // ------------------------------------------------------------- few rows ----
-// Up to 128 rows: the bound is reading the weights once.  The weights are the
+// Up to 64 rows: the bound is reading the weights once.  The weights are the
 // product's 128-row side, the kN rows of x the other.  Each SM streams its own
 // contiguous share of the vocabulary, in steps of 16 tokens, through one
 // CTA's ring of stages: shares are equal to within a step, so that all SMs end
 // together, and a vocabulary of a few thousand tokens still spreads over all of
 // them.  A lane of tensor memory is a token; row r's scale comes from lane r by
-// a shuffle, the token's own is the lane's.
-constexpr int kFewThreads = 320;   // 8 warps scale and add, 1 loads, 1 multiplies
+// a shuffle, the token's own is the lane's.  A stage has its own columns of
+// tensor memory, and is loaded again when its sums have been read: the warp
+// that multiplies, whose loop of about 300 cycles a block must stay below the
+// 700 that 16 KB take to arrive, waits on one barrier and signals one.
 constexpr int kStep = 16;          // tokens per load
 
 template <int kN> struct Few {
-    static constexpr int kBufs = 4;
-    static constexpr int kCols = kN * kBufs;                    // of tensor memory
+    static constexpr int kGroups = kN == 16 ? 2 : 4;            // of 4 warps that scale and add, each a part of the rows
+    static constexpr int kThreads = kGroups * 128 + 64;         // and 1 warp loads, 1 multiplies
     static constexpr int kStage = (128 + kN) * kBlock;
-    static constexpr int kStages = kN == 16 ? 12 : kN == 32 ? 11 : kN == 64 ? 9 : 7;
+    static constexpr int kStages = kN == 16 ? 12 : kN == 32 ? 11 : 8;
+    static constexpr int kCols = kN * kStages <= 256 ? 256 : 512;   // of tensor memory, kN for each stage
+    static_assert(kN * kStages <= kCols, "tensor memory");
     static constexpr int kSmem = kStages * kStage + 1024 + 512;
     static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
 
 template <int kN, typename O>
-__global__ void __launch_bounds__(kFewThreads, 1)
+__global__ void __launch_bounds__(Few<kN>::kThreads, 1)
 k_logits_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, LogitsParams P,
              uint32_t share) {
     using F = Few<kN>;
-    constexpr int kStages = F::kStages, kHalf = kN / 2;   // a warp adds half of the rows
+    constexpr int kStages = F::kStages, kLoader = F::kGroups * 4;
+    constexpr int kPart = kN / F::kGroups;   // rows that a warp adds
     extern __shared__ uint8_t raw[];
     uint8_t *base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     const uint32_t tiles = smem_u32(base);
     const uint32_t bars = tiles + kStages * F::kStage;
     uint32_t *extra = (uint32_t *)(base + kStages * F::kStage + 448);   // [0] tensor memory, [1] gave up
     auto full = [&](int s) { return bars + 8 * s; };
-    auto empty = [&](int s) { return bars + 8 * (kStages + s); };
-    auto done = [&](int b) { return bars + 8 * (2 * kStages + b); };
-    auto taken = [&](int b) { return bars + 8 * (2 * kStages + F::kBufs + b); };
+    auto done = [&](int s) { return bars + 8 * (kStages + s); };
+    auto taken = [&](int s) { return bars + 8 * (2 * kStages + s); };
     const int warp = __shfl_sync(kFull, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t begin = min(P.n_tok, blockIdx.x * share), end = min(P.n_tok, begin + share);
     volatile uint32_t *gave_up = extra + 1;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; s++) mbar_init(full(s), 1), mbar_init(empty(s), 1);
-        for (int b = 0; b < F::kBufs; b++) mbar_init(done(b), 1), mbar_init(taken(b), 8);
+        for (int s = 0; s < kStages; s++) mbar_init(full(s), 1), mbar_init(done(s), 1), mbar_init(taken(s), kLoader);
         extra[1] = 0;
         mbar_init_fence();
     }
-    if (warp == 9) tmem_alloc(smem_u32(extra), F::kCols);
+    if (warp == kLoader + 1) tmem_alloc(smem_u32(extra), F::kCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = extra[0];
 
-    if (warp == 8) {
+    if (warp == kLoader) {
         tma_prefetch_map(&map_w);
         tma_prefetch_map(&map_x);
         int s = 0;
@@ -92,13 +95,14 @@ k_logits_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
         for (uint32_t tok = begin; tok < end && !__any_sync(kFull, *gave_up); tok += 128) {
             const uint32_t steps = (min(128u, end - tok) + kStep - 1) / kStep;
             for (uint32_t b = 0; b < P.blocks; b++) {
-                if (!__all_sync(kFull, mbar_wait(empty(s), phase))) { *gave_up = 1; break; }
+                if (!__all_sync(kFull, mbar_wait(taken(s), phase))) { *gave_up = 1; break; }
                 if (elect_one()) {
                     const uint32_t at = tiles + s * F::kStage;
                     mbar_expect(full(s), (steps * kStep + kN) * kBlock);
-                    tma_load(at + 128 * kBlock, &map_x, (int)(b * kBlock), 0, full(s));
+                    const int x = (int)(b * kBlock);
+                    tma_load(at + 128 * kBlock, &map_x, x, 0, full(s));
                     for (uint32_t i = 0; i < steps; i++)   // what a short tile leaves of the stage keeps old weights, whose sums go nowhere
-                        tma_load(at + i * kStep * kBlock, &map_w, (int)(b * kBlock), (int)(tok + i * kStep), full(s));
+                        tma_load(at + i * kStep * kBlock, &map_w, x, (int)(tok + i * kStep), full(s));
                 }
                 issued++;
                 if (++s == kStages) s = 0, phase ^= 1;
@@ -107,85 +111,88 @@ k_logits_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
         if (*gave_up)   // no copy may be in flight when the CTA ends
             for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; i++)
                 mbar_wait(full(i % kStages), (i / kStages) & 1);
-    } else if (warp == 9) {
-        int s = 0, buf = 0;
-        uint32_t phase = 0, bphase = 1;
+    } else if (warp == kLoader + 1) {
+        int s = 0;
+        uint32_t phase = 0;
         const uint32_t w0 = operand_lo(tiles), x0 = operand_lo(tiles + 128 * kBlock);
         for (uint32_t tok = begin; tok < end && !__any_sync(kFull, *gave_up); tok += 128) {
             for (uint32_t b = 0; b < P.blocks; b++) {
-                if (!__all_sync(kFull, mbar_wait(taken(buf), bphase) && mbar_wait(full(s), phase))) { *gave_up = 1; break; }
+                if (!__all_sync(kFull, mbar_wait(full(s), phase))) { *gave_up = 1; break; }
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t w = w0 + s * (F::kStage >> 4), x = x0 + s * (F::kStage >> 4), d = tmem + buf * kN;
+                    const uint32_t w = w0 + s * (F::kStage >> 4), x = x0 + s * (F::kStage >> 4), d = tmem + s * kN;
                     constexpr uint32_t kInstr = e4m3_instr(128, kN);
                     mma_e4m3<false>(d, w, x, kInstr);
                     mma_e4m3<true>(d, w + 2, x + 2, kInstr);
                     mma_e4m3<true>(d, w + 4, x + 4, kInstr);
                     mma_e4m3<true>(d, w + 6, x + 6, kInstr);
-                    mma_commit(done(buf));
-                    mma_commit(empty(s));
+                    mma_commit(done(s));
                 }
                 if (++s == kStages) s = 0, phase ^= 1;
-                if (++buf == F::kBufs) buf = 0, bphase ^= 1;
             }
         }
     } else {
-        constexpr int kPer = (kHalf + 31) / 32;   // row scales that a lane holds
-        const int quarter = warp & 3, col0 = (warp >> 2) * kHalf;
+        constexpr int kPer = (kPart + 31) / 32;   // row scales that a lane holds
+        const int quarter = warp & 3, col0 = (warp >> 2) * kPart;
         const uint32_t last = P.blocks - 1;
-        int buf = 0;
-        uint32_t bphase = 0;
+        int s = 0;
+        uint32_t phase = 0;
         struct Scales { float w, x[kPer]; };
         const float *xs[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; i++)   // lanes past the rows read a scale that nothing uses
             xs[i] = P.xs + min((uint32_t)(col0 + i * 32 + lane), P.n_rows - 1) * P.xs_row;
+        const uint32_t mine = tmem + ((uint32_t)quarter << 21) + col0;
         bool ok = true;
         for (uint32_t tok = begin; tok < end && ok; tok += 128) {
             const uint32_t t = tok + quarter * 32 + lane;
             const float *ws = P.ws + (uint64_t)(min(t, P.n_tok - 1) / kBlock) * P.ws_row;
             auto load = [&](uint32_t b) {
-                Scales s;
+                Scales v;
                 b = min(b, last);
-                s.w = ws[b * P.ws_blk];
+                v.w = ws[b * P.ws_blk];
 #pragma unroll
-                for (int i = 0; i < kPer; i++) s.x[i] = xs[i][b * P.xs_blk];
-                return s;
+                for (int i = 0; i < kPer; i++) v.x[i] = xs[i][b * P.xs_blk];
+                return v;
             };
-            float acc[kHalf];
+            float acc[kPart];
 #pragma unroll
-            for (int c = 0; c < kHalf; c++) acc[c] = 0.0f;
-            auto add = [&](const Scales &s) {
-                if (!__all_sync(kFull, mbar_wait(done(buf), bphase))) { ok = false; return; }
+            for (int c = 0; c < kPart; c++) acc[c] = 0.0f;
+            auto add = [&](const float (&d)[kPart], const Scales &by) {
+#pragma unroll
+                for (int c = 0; c < kPart; c++)
+                    acc[c] = fmaf(d[c], by.w * __shfl_sync(kFull, by.x[c / 32], c), acc[c]);
+            };
+            // two blocks at a time: half the waits, and a block's scales have two blocks' time to arrive
+            Scales a = load(0), b2 = load(1);
+            for (uint32_t b = 0; b < P.blocks; b += 2) {
+                const bool two = b + 1 < P.blocks;
+                const int s1 = s + 1 == kStages ? 0 : s + 1;
+                const uint32_t phase1 = s1 ? phase : phase ^ 1;
+                const bool second = two && lane >= 16;   // half of the lanes watch each barrier
+                if (!__all_sync(kFull, mbar_wait(second ? done(s1) : done(s), second ? phase1 : phase))) { ok = false; break; }
                 tc_fence_after();
-                constexpr int kLoad = kHalf < 32 ? kHalf : 32;
-#pragma unroll
-                for (int c0 = 0; c0 < kHalf; c0 += kLoad) {
-                    float d[kLoad];
-                    tmem_load(d, tmem + ((uint32_t)quarter << 21) + buf * kN + col0 + c0);
-                    tmem_wait(d);
-                    if (c0 + kLoad == kHalf) {
-                        tc_fence_before();
-                        if (lane == 0) mbar_arrive(taken(buf));
-                    }
-#pragma unroll
-                    for (int c = 0; c < kLoad; c++)
-                        acc[c0 + c] = fmaf(d[c], s.w * __shfl_sync(kFull, s.x[c0 / 32], c), acc[c0 + c]);
+                float d[kPart], d1[kPart];
+                tmem_load(d, mine + s * kN);
+                tmem_load(d1, mine + (two ? s1 : s) * kN);
+                tmem_wait(d);
+                tmem_wait(d1);
+                tc_fence_before();
+                if (lane == 0) {
+                    mbar_arrive(taken(s));
+                    if (two) mbar_arrive(taken(s1));
                 }
-                if (++buf == F::kBufs) buf = 0, bphase ^= 1;
-            };
-            // two blocks in turn, so that a block's scales have two blocks' time to arrive
-            Scales s0 = load(0), s1 = load(1);
-            for (uint32_t b = 0; b < P.blocks && ok; b += 2) {
-                add(s0);
-                s0 = load(b + 2);
-                if (b + 1 < P.blocks && ok) add(s1);
-                s1 = load(b + 3);
+                add(d, a);
+                a = load(b + 2);
+                if (two) add(d1, b2);
+                b2 = load(b + 3);
+                s = s1, phase = phase1;
+                if (two && ++s == kStages) s = 0, phase ^= 1;
             }
             if (ok && t < end) {
                 O *out = (O *)P.out + t;
 #pragma unroll
-                for (int c = 0; c < kHalf; c++)
+                for (int c = 0; c < kPart; c++)
                     if (col0 + c < P.n_rows) out[(uint64_t)(col0 + c) * P.out_stride] = from_f32<O>(acc[c]);
             }
         }
@@ -195,7 +202,7 @@ k_logits_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) tmem_free(tmem, F::kCols);
+    if (warp == kLoader + 1) tmem_free(tmem, F::kCols);
     if (threadIdx.x == 0 && *gave_up) *P.status = DERR_TIMEOUT;
 }
 
@@ -520,8 +527,9 @@ int launch_few(bpe_ctx *ctx, const CUtensorMap &mw, const CUtensorMap &mx, const
     using F = Few<kN>;
     const uint32_t steps = (P.n_tok + kStep - 1) / kStep, each = (steps + ctx->sm_count - 1) / ctx->sm_count;
     auto k = k_logits_few<kN, O>;
-    BPE_CUDA(ctx, cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem), "head_logits");
-    k<<<(steps + each - 1) / each, kFewThreads, F::kSmem, ctx->stream>>>(mw, mx, P, each * kStep);
+    static std::atomic<uint64_t> devices{0};
+    BPE_CUDA(ctx, allow_shared(k, ctx->device, F::kSmem, devices), "head_logits");
+    k<<<(steps + each - 1) / each, F::kThreads, F::kSmem, ctx->stream>>>(mw, mx, P, each * kStep);
     BPE_CUDA(ctx, cudaGetLastError(), "head_logits launch");
     return BPE_OK;
 }
@@ -530,7 +538,8 @@ template <typename O, int kCtas>
 int launch_many(bpe_ctx *ctx, const CUtensorMap &mw, const CUtensorMap &mx, const CUtensorMap &mo, const LogitsParams &P) {
     using M = Many<kCtas>;
     auto k = k_logits_many<O, kCtas>;
-    BPE_CUDA(ctx, cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, M::kSmem), "head_logits");
+    static std::atomic<uint64_t> devices{0};
+    BPE_CUDA(ctx, allow_shared(k, ctx->device, M::kSmem, devices), "head_logits");
     const uint64_t n_tiles = (uint64_t)((P.n_rows + M::kRows - 1) / M::kRows) * ((P.n_tok + kManyToks - 1) / kManyToks);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctx->sm_count / kCtas * kCtas);
@@ -558,7 +567,7 @@ int launch_many(bpe_ctx *ctx, const CUtensorMap &mw, const CUtensorMap &mx, cons
 
 template <typename O>
 int launch(bpe_ctx *ctx, const uint8_t *x8, uint64_t x_stride, const uint8_t *w8, uint64_t w_stride, uint32_t dim, LogitsParams P) {
-    const int n = P.n_rows <= 16 ? 16 : P.n_rows <= 32 ? 32 : P.n_rows <= 64 ? 64 : P.n_rows <= 128 ? 128 : 0;
+    const int n = P.n_rows <= 16 ? 16 : P.n_rows <= 32 ? 32 : P.n_rows <= 64 ? 64 : 0;
     // a pair's 256 rows where they waste no more than 128-row tiles would
     const bool pair = !n && (P.n_rows + 127) / 128 % 2 == 0;
     CUtensorMap mw, mx, mo = {};
@@ -569,7 +578,6 @@ int launch(bpe_ctx *ctx, const uint8_t *x8, uint64_t x_stride, const uint8_t *w8
     if (n == 16) return launch_few<16, O>(ctx, mw, mx, P);
     if (n == 32) return launch_few<32, O>(ctx, mw, mx, P);
     if (n == 64) return launch_few<64, O>(ctx, mw, mx, P);
-    if (n == 128) return launch_few<128, O>(ctx, mw, mx, P);
     P.tma_out = (uintptr_t)P.out % 16 == 0 && P.out_stride * sizeof(O) % 16 == 0 && P.out_stride * sizeof(O) < (1ull << 40);
     if (P.tma_out && (rc = encode_out<O>(ctx, &mo, P))) return rc;
     return pair ? launch_many<O, 2>(ctx, mw, mx, mo, P) : launch_many<O, 1>(ctx, mw, mx, mo, P);

@@ -70,6 +70,7 @@ constexpr int kBuckets = 161;              // 4 per octave from 2^-40 to 1
 constexpr int kList = 128;                 // tokens that are ranked pair by pair
 constexpr uint32_t kLeast = 0x2B800000u;   // the bits of 2^-40: below it a weight is 0
 constexpr int kMaxTeam = 8;
+constexpr size_t kMaxShared = 232448;
 constexpr int kSmallK = 256, kSmall = 512; // top-k up to kSmallK works on a list of up to kSmall tokens
 constexpr int kNear = 128;                 // buckets of 1/8 below the largest logit, for that list
 
@@ -900,7 +901,8 @@ int launch_team(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows, uint32_t t
     auto k = k_sample<kThreads>;
     const uint32_t slice = ((P.n_tok + team - 1) / team + 3) & ~3u;
     const size_t smem = sizeof(SampleShared<kThreads>) + (size_t)slice * 4;
-    BPE_CUDA(ctx, cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem), "head_sample");
+    static std::atomic<uint64_t> devices{0};
+    BPE_CUDA(ctx, allow_shared(k, ctx->device, kMaxShared, devices), "head_sample");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(n_rows * team);
     cfg.blockDim = dim3(kThreads);
