@@ -25,14 +25,31 @@ template <> __device__ __forceinline__ float from_f32<float>(float v) { return v
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// |v| as an ordered whole number: the order of magnitudes, with infinity above
-// every finite value and NaN above infinity, so that a maximum keeps them.
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// The larger of two, a NaN if either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 
-// Scale of a block whose largest magnitude has the bits `amax`.
-__device__ __forceinline__ float block_scale(uint32_t amax) {
-    const float s = __uint_as_float(amax) / kE4m3Max;
-    return s < kMinScale ? kMinScale : s;   // NaN stays
+// Scale of a block whose largest magnitude is `amax`; NaN stays.
+__device__ __forceinline__ float block_scale(float amax) {
+    return max_nan(amax * (1.0f / kE4m3Max), kMinScale);
+}
+
+// 16 bytes of a type from 32-bit values.
+__device__ __forceinline__ uint4 pack16(const float *v, float) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+__device__ __forceinline__ uint4 pack16(const float *v, __nv_bfloat16) {
+    __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    __nv_bfloat162 c = __floats2bfloat162_rn(v[4], v[5]), d = __floats2bfloat162_rn(v[6], v[7]);
+    return make_uint4(*(uint32_t *)&a, *(uint32_t *)&b, *(uint32_t *)&c, *(uint32_t *)&d);
+}
+__device__ __forceinline__ uint4 pack16(const float *v, __half) {
+    __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
+    __half2 c = __floats2half2_rn(v[4], v[5]), d = __floats2half2_rn(v[6], v[7]);
+    return make_uint4(*(uint32_t *)&a, *(uint32_t *)&b, *(uint32_t *)&c, *(uint32_t *)&d);
 }
 
 __device__ __forceinline__ uint8_t to_e4m3(float v) {

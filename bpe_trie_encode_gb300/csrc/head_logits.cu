@@ -229,21 +229,6 @@ template <int kCtas> struct Many {
     static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
 
-// 16 bytes of the tile's way out: 4 or 8 columns of a row.
-__device__ __forceinline__ uint4 pack(const float *v, float) {
-    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-}
-__device__ __forceinline__ uint4 pack(const float *v, __nv_bfloat16) {
-    __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-    __nv_bfloat162 c = __floats2bfloat162_rn(v[4], v[5]), d = __floats2bfloat162_rn(v[6], v[7]);
-    return make_uint4(*(uint32_t *)&a, *(uint32_t *)&b, *(uint32_t *)&c, *(uint32_t *)&d);
-}
-__device__ __forceinline__ uint4 pack(const float *v, __half) {
-    __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
-    __half2 c = __floats2half2_rn(v[4], v[5]), d = __floats2half2_rn(v[6], v[7]);
-    return make_uint4(*(uint32_t *)&a, *(uint32_t *)&b, *(uint32_t *)&c, *(uint32_t *)&d);
-}
-
 template <typename O, int kCtas>
 __global__ void __launch_bounds__(kManyThreads, 1)
 k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
@@ -413,7 +398,7 @@ k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
 #pragma unroll
                 for (int j = 0; j < 8; j++)
-                    *reinterpret_cast<uint4 *>(mine + r * 128 + ((j ^ (r & 7)) << 4)) = pack(acc + c0 + j * kVec, O());
+                    *reinterpret_cast<uint4 *>(mine + r * 128 + ((j ^ (r & 7)) << 4)) = pack16(acc + c0 + j * kVec, O());
                 if (P.tma_out) fence_for_tma();
                 asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
                 if (P.tma_out) {
