@@ -1,17 +1,19 @@
 // head_sample.cu -- temperature, top-k, top-p, min-p and the draw of one id
 // per row from a given random number.
 //
-// With m the row's largest logit, e = exp((l - m) / T) and the whole numbers
-// w = floor(e 2^40): sums of w are exact, so neither the split of a row over
-// threads and CTAs nor the order of atomics changes an answer.  The three
+// With m the row's largest logit, z = (l - m) / T and the whole numbers
+// w = floor(exp(z) 2^40): sums of w are exact, so neither the split of a row
+// over threads and CTAs nor the order of atomics changes an answer.  The three
 // filters keep a prefix of the tokens ordered by logit (then by id), so that
 // one cut -- a last kept token -- describes what is kept, and the draw is a
 // search for a running sum in order of ids.
 //
-// A row is read once: a cluster of 1 to 8 CTAs keeps its e in shared memory.  The
-// cut is found by histograms over the bits of e, which are ordered as e is: 4
-// buckets an octave, then 128 of the bucket that holds the cut, and so on until
-// at most 128 tokens are left, which are ranked by comparing all pairs.
+// A row is read once, into the shared memory of one CTA (up to 46,000 tokens of
+// 32 bits, 92,000 of 16), or of a cluster of up to 8 where it does not fit: a
+// barrier of a cluster costs over 1,000 cycles and a row needs six, so a row
+// is split for its size only.  The cut is found by histograms over -z in fixed
+// point: 4 buckets per unit, then 128 of the bucket that holds the cut, and so
+// on until at most 128 tokens are left, which are ranked by comparing all pairs.
 #include "head.cuh"
 
 #include "device.cuh"
@@ -50,29 +52,6 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 __device__ __forceinline__ float z_of(float v, float top, float inv_t) {
     return v == top ? 0.0f : __fmul_rn(v - top, inv_t);
 }
-__device__ __forceinline__ u64 weight_of(float v, float top, float inv_t) {
-    return v > -INFINITY ? (u64)(expf(z_of(v, top, inv_t)) * kOne) : 0;   // 0 for -infinity and NaN
-}
-
-__device__ __forceinline__ u64 sum_all(u64 v, u64 *red) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    u64 t = 0;
-    for (int i = 0; i < kSampThreads / 32; i++) t += red[i];
-    return t;
-}
-
-// ------------------------------------------------- rows in shared memory ---
-constexpr int kBuckets = 161;              // 4 per octave from 2^-40 to 1
-constexpr int kList = 128;                 // tokens that are ranked pair by pair
-constexpr uint32_t kLeast = 0x2B800000u;   // the bits of 2^-40: below it a weight is 0
-constexpr int kMaxTeam = 8;
-constexpr size_t kMaxShared = 232448;
-constexpr int kSmallK = 256, kSmall = 512; // top-k up to kSmallK works on a list of up to kSmall tokens
-constexpr int kNear = 128;                 // buckets of 1/8 below the largest logit, for that list
 
 // w = floor(e 2^40) in two parts of 20 bits, for 0 <= e <= 1: additions that round towards zero leave the whole part
 // of e 2^20, then of its rest times 2^20, in the low bits of a float between 2^23 and 2^24.
@@ -89,13 +68,23 @@ __device__ __forceinline__ u64 weight(float e) {
     return join(p.hi, p.lo);
 }
 
+// ------------------------------------------------- rows in shared memory ---
+constexpr int kBuckets = 128;
+constexpr float kCodeScale = -0x1p27f;     // -z as a whole number
+constexpr uint32_t kCodes = 28u << 27;      // from here on a weight is 0
+constexpr int kList = 128;                 // tokens that are ranked pair by pair
+constexpr int kMaxTeam = 8;
+constexpr size_t kMaxShared = 232448;
+constexpr int kSmallK = 256, kSmall = 512; // top-k up to kSmallK works on a list of up to kSmall tokens
+constexpr int kNear = 128;                 // buckets of 1/8 below the largest logit, for that list
+
 struct __align__(16) Entry { uint32_t key, idx; u64 w; };
 
 template <int kThreads> struct SampleShared {
-    static constexpr int kCopies = kThreads < 512 ? kThreads / 32 : 16;   // of a histogram, by thread
+    static constexpr int kCopies = kThreads / 32;   // of a histogram, by thread: no more than 4,095 tokens meet in one
     uint32_t lo[kBuckets * kCopies], hi[kBuckets * kCopies];
-    u64 sum[2][kBuckets + 1];              // this CTA's histogram, read by the whole cluster
-    u64 all[kBuckets + 1];                 // the row's
+    u64 sum[2][kBuckets];                  // this CTA's histogram, read by the whole cluster
+    u64 all[kBuckets];                     // the row's
     uint32_t near_n[kNear];                // threads by their largest logit
     u64 slot[2][kMaxTeam];                 // a value from each CTA of the cluster
     u64 red[32];
@@ -105,8 +94,9 @@ template <int kThreads> struct SampleShared {
     uint32_t list_n, small_n;
     u64 pick[4];                           // bucket found, sums above and in it, this CTA's sum above it
     u64 goal;
-    uint32_t cut[3];                       // bits, key, id of the last kept token
-    float4 e[1];                           // the CTA's tokens, four at a time
+    float cut_v;                           // the last kept token
+    uint32_t cut_idx;
+    uint4 row[1];                          // the CTA's logits as they are, 16 bytes at a time
 };
 
 __device__ __forceinline__ uint32_t far_addr(const void *p, uint32_t rank) {
@@ -136,6 +126,11 @@ __device__ __forceinline__ uint4 far_load(const Entry *p, uint32_t rank) {
                  : "r"(far_addr(p, rank)) : "memory");
     return v;
 }
+// counter += v where v is not 0, without a branch around it
+__device__ __forceinline__ void count_up(uint32_t *counter, uint32_t v) {
+    asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %1, 0;\n@p red.shared.add.u32 [%0], %1;\n}"
+                 ::"r"((uint32_t)__cvta_generic_to_shared(counter)), "r"(v) : "memory");
+}
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {   // of values below 2^63, by parts of 22 bits
     const uint32_t a = __reduce_add_sync(kFull, (uint32_t)v & 0x3FFFFFu);
@@ -152,18 +147,20 @@ __device__ __forceinline__ u64 warp_scan(u64 v, int lane) {   // inclusive
     return v;
 }
 
-template <int kThreads>
+// kHalf: logits of 16 bits.
+template <bool kHalf, int kThreads>
 struct Sampler {
     static constexpr int kWarps = kThreads / 32, kCopies = SampleShared<kThreads>::kCopies;
+    static constexpr int kVec = kHalf ? 8 : 4;   // logits in 16 bytes
     SampleShared<kThreads> &S;
     const SampleParams &P;
-    const uint8_t *l;       // the row
     uint32_t rank, size;    // this CTA among the row's
-    uint32_t first, quads;  // its tokens begin here; groups of four
-    uint32_t span, q0, q1;  // a thread's groups: contiguous, an odd number, so that a warp's loads meet no bank twice
+    uint32_t first, count;  // its tokens
+    uint32_t g0, g1;        // a thread's groups of 16 bytes: contiguous, an odd number, so that no two lanes' meet in a bank
     int lane, warp, turn;
     float top, inv_t;
-    uint32_t cut_bits, cut_key, cut_idx;
+    float cut_v;
+    uint32_t cut_idx;
 
     __device__ __forceinline__ void sync() const {
         __syncwarp();
@@ -172,45 +169,47 @@ struct Sampler {
         else
             asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
-    __device__ __forceinline__ float logit(uint32_t idx) const {
-        if (P.type == BPE_F32) return ((const float *)l)[idx];
-        if (P.type == BPE_BF16) return to_f32(((const __nv_bfloat16 *)l)[idx]);
-        return to_f32(((const __half *)l)[idx]);
+    __device__ __forceinline__ float decode(uint32_t half) const {   // 16 bits of either type
+        return P.type == BPE_BF16 ? __uint_as_float(half << 16) : __half2float(__ushort_as_half((unsigned short)half));
     }
-    __device__ __forceinline__ uint32_t key(uint32_t i) const { return key_of(logit(first + i)); }   // of the CTA's token i
-    __device__ __forceinline__ float exp_of(float v) const {
-        return fmaxf(expf(__fmul_rn(v - top, inv_t)), 0.0f);   // NaN as 0; row_exp is for a largest logit of infinity
+    __device__ __forceinline__ float logit(uint32_t i) const {       // of the CTA's token i
+        if (kHalf) return decode(((const unsigned short *)S.row)[i]);
+        return ((const float *)S.row)[i];
     }
-    __device__ __forceinline__ float row_exp(float v) const { return v == top ? 1.0f : exp_of(v); }
-    // f(i, bits of e) for this thread's tokens
-    template <typename F> __device__ __forceinline__ void each(F f) const {
-#pragma unroll 2
-        for (uint32_t q = q0; q < q1; q++) {
-            const float4 v = S.e[q];
-            f(q * 4, __float_as_uint(v.x));
-            f(q * 4 + 1, __float_as_uint(v.y));
-            f(q * 4 + 2, __float_as_uint(v.z));
-            f(q * 4 + 3, __float_as_uint(v.w));
-        }
-    }
-    // e of this thread's tokens in place of their logits, f(bits) for each
-    template <typename F> __device__ __forceinline__ void to_exp(F f) {
-        const bool inf = top == INFINITY;
-#pragma unroll 2
-        for (uint32_t q = q0; q < q1; q++) {
-            float4 v = S.e[q];
-            if (inf) {
-                v.x = row_exp(v.x), v.y = row_exp(v.y), v.z = row_exp(v.z), v.w = row_exp(v.w);
+    __device__ __forceinline__ void unpack(const uint4 &q, float (&v)[kVec]) const {
+        if (!kHalf) {
+            v[0] = __uint_as_float(q.x), v[1] = __uint_as_float(q.y), v[2] = __uint_as_float(q.z), v[3] = __uint_as_float(q.w);
+        } else {
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+            if (P.type == BPE_BF16) {
+#pragma unroll
+                for (int i = 0; i < 4; i++) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
             } else {
-                v.x = exp_of(v.x), v.y = exp_of(v.y), v.z = exp_of(v.z), v.w = exp_of(v.w);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const float2 f = __half22float2(*(const __half2 *)&w[i]);
+                    v[2 * i] = f.x, v[2 * i + 1] = f.y;
+                }
             }
-            S.e[q] = v;
-            f(__float_as_uint(v.x));
-            f(__float_as_uint(v.y));
-            f(__float_as_uint(v.z));
-            f(__float_as_uint(v.w));
         }
     }
+    // f(i, logit) for this thread's tokens; those past the end are -infinity
+    template <typename F> __device__ __forceinline__ void each(F f) const {
+#pragma unroll 1
+        for (uint32_t g = g0; g < g1; g++) {
+            float v[kVec];
+            unpack(S.row[g], v);
+#pragma unroll
+            for (int j = 0; j < kVec; j++) f(g * kVec + j, v[j]);
+        }
+    }
+    // z, or -100 where nothing can be drawn (infinities' differences, NaN)
+    __device__ __forceinline__ float z_at(float v) const {
+        if (top == INFINITY) return v == top ? 0.0f : -100.0f;
+        return fmaxf(__fmul_rn(v - top, inv_t), -100.0f);
+    }
+    __device__ __forceinline__ uint32_t code_at(float z) const { return __float2uint_rz(z * kCodeScale); }
+    __device__ __forceinline__ u64 weight_at(float v) const { return weight(expf(z_at(v))); }
 
     // One value per CTA to every CTA of the row; all threads of the CTA hold `v`.
     __device__ __forceinline__ void exchange(u64 v) {
@@ -223,7 +222,9 @@ struct Sampler {
         __syncthreads();
         if (lane == 0) S.red[warp] = v;
         __syncthreads();
-        exchange(__reduce_max_sync(kFull, lane < kWarps ? (uint32_t)S.red[lane] : 0));
+        v = __reduce_max_sync(kFull, lane < kWarps ? (uint32_t)S.red[lane] : 0);
+        if (size == 1) return v;
+        exchange(v);
         v = 0;
         for (uint32_t r = 0; r < size; r++) v = max(v, (uint32_t)S.slot[turn][r]);
         return v;
@@ -238,9 +239,10 @@ struct Sampler {
     }
     // The row's sum of the CTAs' sums; `before`: of the CTAs before this one.
     __device__ __forceinline__ u64 sum_ctas(u64 mine, u64 &before) {
+        before = 0;
+        if (size == 1) return mine;
         exchange(mine);
         u64 total = 0;
-        before = 0;
         for (uint32_t r = 0; r < size; r++) {
             const u64 x = S.slot[turn][r];
             before += r < rank ? x : 0;
@@ -253,10 +255,10 @@ struct Sampler {
         return sum_ctas(sum_cta(v), before);
     }
 
-    // The token, in order of ids, at which the running sum of value(i, bits) passes t; the lane that holds it calls
+    // The token, in order of ids, at which the running sum of value(i, logit) passes t; the lane that holds it calls
     // found(i).  own: this thread's sum; S.red holds the warps', `mine` is the CTA's, `before` the CTAs' before it.
     template <typename V, typename F>
-    __device__ __forceinline__ void locate(V value, u64 own, u64 t, u64 before, u64 mine, F found) {
+    __device__ __forceinline__ void locate(V value, u64 own, u64 t, u64 before, u64 mine, F found) const {
         if (t < before || t - before >= mine) return;
         t -= before;
         const u64 w = lane < kWarps ? S.red[lane] : 0, run = warp_scan(w, lane);
@@ -265,9 +267,9 @@ struct Sampler {
         const u64 upto = warp_scan(own, lane);
         const int who = __ffs(__ballot_sync(kFull, upto > t)) - 1;
         t -= __shfl_sync(kFull, upto - own, who);
-        const uint32_t i0 = __shfl_sync(kFull, q0, who) * 4, i1 = __shfl_sync(kFull, q1, who) * 4;
+        const uint32_t i0 = __shfl_sync(kFull, g0, who) * kVec, i1 = __shfl_sync(kFull, g1, who) * kVec;
         for (uint32_t i = i0 + lane; i - lane < i1; i += 32) {   // the thread's tokens, a lane each
-            const u64 v = i < i1 ? value(i, __float_as_uint(((const float *)S.e)[i])) : 0, s = warp_scan(v, lane);
+            const u64 v = i < i1 ? value(i, logit(i)) : 0, s = warp_scan(v, lane);
             const unsigned past = __ballot_sync(kFull, s > t);
             if (past) {
                 if (lane == __ffs(past) - 1) found(i);
@@ -277,39 +279,40 @@ struct Sampler {
         }
     }
 
-    // Whether token i is kept under the cut.
-    __device__ __forceinline__ bool in_cut(uint32_t i, uint32_t b) const {
-        if (b == cut_bits && cut_idx != ~0u) {
-            const uint32_t x = key(i);
-            return x > cut_key || (x == cut_key && first + i <= cut_idx);
-        }
-        return b >= cut_bits;
+    __device__ __forceinline__ bool in_cut(uint32_t i, float v) const {
+        return v > cut_v || (v == cut_v && first + i <= cut_idx);
     }
-    __device__ __forceinline__ u64 mass() const {   // at most 68 tokens a thread: the parts stay below 2^32
+    __device__ __forceinline__ u64 kept(uint32_t i, float v, u64 least) const {
+        const u64 w = in_cut(i, v) ? weight_at(v) : 0;
+        return w >= least ? w : 0;
+    }
+    // This thread's kept mass: at most 104 tokens, so the parts stay below 2^32.
+    __device__ __forceinline__ u64 mass(u64 least) const {
         uint32_t hi = 0, lo = 0;
-        each([&](uint32_t i, uint32_t b) {
-            if (in_cut(i, b)) {
-                const Parts p = parts_of(__uint_as_float(b));
+        each([&](uint32_t i, float v) {
+            if (in_cut(i, v)) {
+                Parts p = parts_of(expf(z_at(v)));
+                if (least && join(p.hi, p.lo) < least) p = {0, 0};
                 hi += p.hi;
                 lo += p.lo;
             }
         });
         return join(hi, 0) + lo;
     }
-    __device__ __forceinline__ void read_cut() { cut_bits = S.cut[0], cut_key = S.cut[1], cut_idx = S.cut[2]; }
+    __device__ __forceinline__ void read_cut() { cut_v = S.cut_v, cut_idx = S.cut_idx; }
 
     // The last token kept when tokens are taken in order (largest logit, then lowest id) until the sum of their
     // values -- 1, or the weight -- reaches the target: `target`, or with share >= 0 that share of the whole sum, and
     // at least 1.  Where the whole sum is below the target, everything is kept and the cut stays.  kFirst: the
-    // CTA's tokens are still logits, and the histogram is clear.  With kMass, *total and *mine become the row's
-    // kept sum and this CTA's, unless false is returned.
+    // histogram is clear.  With kMass, *total and *mine become the row's kept sum and this CTA's, unless false is
+    // returned.
     template <bool kMass, bool kFirst>
     __device__ __forceinline__ bool select(u64 target, double share, u64 *total = nullptr, u64 *mine = nullptr) {
         u64 above = 0, own = 0;
-        uint32_t low = kLeast;
-        int shift = 21, buckets = kBuckets;
+        uint32_t low = 0;
+        int shift = 25, buckets = kBuckets;
         for (int level = 0;; level++) {
-            // histogram of [low, low + (buckets << shift))
+            // histogram of the codes in [low, low + (buckets << shift))
             if (!kFirst || level > 0) {
                 for (int i = threadIdx.x; i < buckets * kCopies; i += kThreads) {
                     S.lo[i] = 0;
@@ -319,34 +322,38 @@ struct Sampler {
             if (threadIdx.x == 0) S.list_n = 0, S.pick[0] = ~0ull;
             __syncthreads();
             const int copy = threadIdx.x & (kCopies - 1);
-            auto file = [&](uint32_t b) {
-                const uint32_t k = (b - low) >> shift;   // wraps to a large number below `low`
-                if (k < (uint32_t)buckets) {
-                    if (kMass) {   // at most 4,095 tokens a copy: neither part's sum passes 32 bits
-                        const Parts p = parts_of(__uint_as_float(b));
-                        atomicAdd(&S.lo[k * kCopies + copy], p.lo);
-                        if (p.hi) atomicAdd(&S.hi[k * kCopies + copy], p.hi);
+            if (level == 0) {
+                each([&](uint32_t, float v) {
+                    const float z = z_at(v);
+                    const uint32_t k = code_at(z) >> 25;   // 112 and above: no weight
+                    if (kMass) {
+                        const Parts p = parts_of(expf(z));
+                        count_up(&S.lo[k * kCopies + copy], p.lo);
+                        count_up(&S.hi[k * kCopies + copy], p.hi);
                     } else {
-                        atomicAdd(&S.lo[k * kCopies + copy], 1u);
+                        count_up(&S.lo[k * kCopies + copy], k < (kCodes >> 25));
                     }
-                }
-            };
-            if (kFirst && level == 0)
-                to_exp(file);
-            else
-                each([&](uint32_t, uint32_t b) { file(b); });
+                });
+            } else {
+                each([&](uint32_t, float v) {
+                    const float z = z_at(v);
+                    const uint32_t k = (code_at(z) - low) >> shift;   // wraps to a large number below `low`
+                    if (k < (uint32_t)buckets) {
+                        const Parts p = kMass ? parts_of(expf(z)) : Parts{0, 1};
+                        count_up(&S.lo[k * kCopies + copy], p.lo);
+                        if (kMass) count_up(&S.hi[k * kCopies + copy], p.hi);
+                    }
+                });
+            }
             __syncthreads();
-            u64 *sum = S.sum[level & 1];
+            u64 *sum = size == 1 ? S.all : S.sum[level & 1];
             for (int i = threadIdx.x; i < buckets * 4; i += kThreads) {   // four lanes a bucket
                 const int b = i >> 2;
-                uint32_t lo0 = 0, hi0 = 0;
                 u64 v = 0;
 #pragma unroll
                 for (int c = 0; c < kCopies / 4; c++) {
                     const int a = b * kCopies + (((i & 3) + c * 4 + b * 4) & (kCopies - 1));
-                    lo0 = S.lo[a];
-                    if (kMass) hi0 = S.hi[a];
-                    v += join(hi0, lo0);
+                    v += join(kMass ? S.hi[a] : 0, S.lo[a]);
                 }
                 const unsigned with = __activemask();
                 v += __shfl_xor_sync(with, v, 1);
@@ -354,24 +361,29 @@ struct Sampler {
                 if ((i & 3) == 0) sum[b] = v;
             }
             sync();
-            for (int b = threadIdx.x; b < buckets; b += kThreads) {
-                u64 v = 0;
-                for (uint32_t r = 0; r < size; r++) v += far_load(sum + b, r);
-                S.all[b] = v;
+            if (size > 1) {
+                for (int b = threadIdx.x; b < buckets; b += kThreads) {
+                    u64 v[kMaxTeam], s = 0;
+#pragma unroll
+                    for (int r = 0; r < kMaxTeam; r++) v[r] = (uint32_t)r < size ? far_load(sum + b, r) : 0;
+#pragma unroll
+                    for (int r = 0; r < kMaxTeam; r++) s += v[r];
+                    S.all[b] = s;
+                }
+                __syncthreads();
             }
-            __syncthreads();
-            // largest first, the bucket at which the running sum reaches the target
+            // largest logits first, the bucket at which the running sum reaches the target
             if (warp == 0) {
-                constexpr int kPer = (kBuckets + 31) / 32;
+                constexpr int kPer = kBuckets / 32;
                 u64 v[kPer], s = 0, m = 0;
 #pragma unroll
                 for (int j = 0; j < kPer; j++) {
-                    const int b = buckets - 1 - (lane * kPer + j);
-                    v[j] = b >= 0 ? S.all[b] : 0;
+                    const int b = lane * kPer + j;
+                    v[j] = b < buckets ? S.all[b] : 0;
                     s += v[j];
-                    if (kMass && b >= 0) m += sum[b];
+                    if (kMass && size > 1 && b < buckets) m += sum[b];
                 }
-                u64 run = warp_scan(s, lane), part = kMass ? warp_scan(m, lane) - m : 0;
+                u64 run = warp_scan(s, lane), part = kMass && size > 1 ? warp_scan(m, lane) - m : 0;
                 if (level == 0 && share >= 0.0) {
                     const double x = share * (double)__shfl_sync(kFull, run, 31);
                     target = x > 1.0 ? (u64)x : 1;
@@ -379,15 +391,15 @@ struct Sampler {
                 run = above + run - s;
 #pragma unroll
                 for (int j = 0; j < kPer; j++) {
-                    const int b = buckets - 1 - (lane * kPer + j);
+                    const int b = lane * kPer + j;
                     if (run < target && target <= run + v[j]) {
                         S.pick[0] = b;
                         S.pick[1] = run;
                         S.pick[2] = v[j];
-                        S.pick[3] = part;
+                        S.pick[3] = size > 1 ? part : run;
                     }
                     run += v[j];
-                    if (kMass && b >= 0) part += sum[b];
+                    if (kMass && size > 1 && b < buckets) part += sum[b];
                 }
                 if (lane == 0) S.goal = target;
             }
@@ -396,96 +408,115 @@ struct Sampler {
             target = S.goal;
             low += (uint32_t)S.pick[0] << shift;
             above = S.pick[1];
-            own += S.pick[3];
-            const uint32_t high = low + (1u << shift) - 1;
-            // the bucket's tokens are few when even its smallest weight, kList times, makes more than its sum
-            if (S.pick[2] <= kList * (kMass ? weight(__uint_as_float(low)) : 1)) {
-                each([&](uint32_t i, uint32_t b) {
-                    if (b >= low && b <= high) {
+            own = size > 1 ? own + S.pick[3] : above;
+            // are the bucket's tokens few?  By weight: an estimate, and the list says when it was wrong.
+            u64 about = S.pick[2];
+            if (kMass) {
+                const float e = expf((float)low * (1.0f / kCodeScale));
+                about = e > 0x1p-38f ? (u64)((float)about / (e * kOne)) : 0;
+            }
+            if (about <= kList || shift == 0) {
+                const uint32_t width = (1u << shift) - 1;
+                Entry *to = size == 1 ? S.list : S.mine;
+                each([&](uint32_t i, float v) {
+                    const float z = z_at(v);
+                    if (code_at(z) - low <= width) {
                         const uint32_t n = atomicAdd(&S.list_n, 1u);
-                        S.mine[n] = Entry{key(i), first + i, weight(__uint_as_float(b))};
+                        if (n < kList) to[n] = Entry{key_of(v), first + i, weight(expf(z))};
                     }
                 });
                 sync();
-                // every CTA's to one list
-                uint32_t n = 0;
-                for (uint32_t r = 0; r < size; r++) {
-                    const uint32_t c = size == 1 ? S.list_n : far_load(&S.list_n, r);
-                    for (uint32_t i = threadIdx.x; i < c; i += kThreads)
-                        *reinterpret_cast<uint4 *>(&S.list[n + i]) = far_load(&S.mine[i], r);
-                    n += c;
+                uint32_t n = S.list_n;
+                if (size > 1) {   // every CTA's to one list
+                    uint32_t c = (uint32_t)lane < size ? far_load(&S.list_n, lane) : 0;
+                    const uint32_t end = warp_incl_sum(c, lane);
+                    n = __shfl_sync(kFull, end, 31);
+                    for (uint32_t i = threadIdx.x; i < ((n + 31) & ~31u) && n <= kList; i += kThreads) {
+                        uint32_t from = 0, begin = 0;   // the CTA whose part holds place i
+#pragma unroll
+                        for (int r = 0; r < kMaxTeam - 1; r++) {
+                            const uint32_t e = __shfl_sync(kFull, end, r);
+                            if ((uint32_t)r < size && i >= e) from = r + 1, begin = e;
+                        }
+                        if (i < n) *reinterpret_cast<uint4 *>(&S.list[i]) = far_load(&S.mine[i - begin], from);
+                    }
+                    __syncthreads();
                 }
-                __syncthreads();
-                // four lanes a token add up what comes before it
-                for (uint32_t i = threadIdx.x / 4; i < ((n + 7) & ~7u); i += kThreads / 4) {
-                    const Entry x = S.list[min(i, n - 1)];
-                    u64 run = 0, here = 0;
-                    for (uint32_t j = lane & 3; j < n; j += 4) {
-                        const Entry y = S.list[j];
-                        const bool before = y.key > x.key || (y.key == x.key && y.idx < x.idx);
-                        if (before) run += kMass ? y.w : 1;
-                        if (kMass && (before || j == i) && y.idx - first < quads * 4) here += y.w;
+                if (n <= kList) {
+                    // four lanes a token add up what comes before it
+                    for (uint32_t i = threadIdx.x / 4; i < ((n + 7) & ~7u); i += kThreads / 4) {
+                        const Entry x = S.list[min(i, n - 1)];
+                        u64 run = 0, here = 0;
+                        for (uint32_t j = lane & 3; j < n; j += 4) {
+                            const Entry y = S.list[j];
+                            const bool before = y.key > x.key || (y.key == x.key && y.idx < x.idx);
+                            if (before) run += kMass ? y.w : 1;
+                            if (kMass && size > 1 && (before || j == i) && y.idx - first < count) here += y.w;
+                        }
+                        run += __shfl_xor_sync(kFull, run, 1);
+                        run += __shfl_xor_sync(kFull, run, 2);
+                        if (kMass && size > 1) {
+                            here += __shfl_xor_sync(kFull, here, 1);
+                            here += __shfl_xor_sync(kFull, here, 2);
+                        }
+                        run += above;
+                        const u64 upto = run + (kMass ? x.w : 1);
+                        if (i < n && run < target && target <= upto) {
+                            S.cut_v = key_value(x.key);
+                            S.cut_idx = x.idx;
+                            S.pick[1] = upto;
+                            S.pick[3] = size > 1 ? own + here : upto;
+                        }
                     }
-                    run += __shfl_xor_sync(kFull, run, 1);
-                    run += __shfl_xor_sync(kFull, run, 2);
-                    if (kMass) {
-                        here += __shfl_xor_sync(kFull, here, 1);
-                        here += __shfl_xor_sync(kFull, here, 2);
-                    }
-                    run += above;
-                    const u64 upto = run + (kMass ? x.w : 1);
-                    if (i < n && run < target && target <= upto) {
-                        S.cut[0] = __float_as_uint(row_exp(key_value(x.key)));
-                        S.cut[1] = x.key;
-                        S.cut[2] = x.idx;
-                        S.pick[1] = upto;
-                        S.pick[3] = own + here;
-                    }
+                    __syncthreads();
+                    if (kMass && total) *total = S.pick[1], *mine = S.pick[3];
+                    return true;
                 }
-                __syncthreads();
-                if (kMass && total) *total = S.pick[1], *mine = S.pick[3];
-                return true;
+                if (shift == 0) break;   // over kList tokens of one code
+                sync();                  // list_n has been read by all
             }
-            if (shift == 0) break;   // over kList tokens with the same e
-            __syncthreads();         // what was found has been read by all
-            buckets = 128;
-            shift -= 7;
+            __syncthreads();             // what was found has been read by all
+            buckets = shift >= 7 ? 128 : 1 << shift;
+            shift = shift >= 7 ? shift - 7 : 0;
         }
-        // tokens of one e: `need` of them, by logit, then by id
-        const u64 w = kMass ? weight(__uint_as_float(low)) : 1;
-        u64 need = (target - above + w - 1) / w;
+        // tokens of one code: by logit, then by id
+        auto in = [&](float v) { return code_at(z_at(v)) == low; };
+        auto value = [&](float v) -> u64 { return kMass ? weight_at(v) : 1; };
         uint32_t big = 0, small = 0;
-        each([&](uint32_t i, uint32_t b) {
-            if (b == low) {
-                const uint32_t k = key(i);
-                big = max(big, k);
-                small = max(small, ~k);
+        each([&](uint32_t, float v) {
+            if (in(v)) {
+                big = max(big, key_of(v));
+                small = max(small, ~key_of(v));
             }
         });
         big = max_row(big);
         small = ~max_row(small);
         uint32_t at = small;
-        if (big != small) {          // logits that differ by less than e can tell
+        u64 need = target - above;
+        if (big != small) {          // logits that differ by less than a code
             at = 0;
             for (int bit = 31; bit >= 0; bit--) {
                 const uint32_t c = at | 1u << bit;
                 u64 m = 0;
-                each([&](uint32_t i, uint32_t b) { m += b == low && key(i) >= c; });
+                each([&](uint32_t, float v) { m += in(v) && key_of(v) >= c ? value(v) : 0; });
                 if (sum_row(m) >= need) at = c;
             }
             u64 m = 0;
-            each([&](uint32_t i, uint32_t b) { m += b == low && key(i) > at; });
+            each([&](uint32_t, float v) { m += in(v) && key_of(v) > at ? value(v) : 0; });
             need -= sum_row(m);
         }
-        auto one = [&](uint32_t i, uint32_t b) -> u64 { return b == low && key(i) == at; };
+        const float last = key_value(at);
+        const u64 w = value(last);
+        need = (need + w - 1) / w;   // that many of the logit `last`
+        auto one = [&](uint32_t, float v) -> u64 { return v == last; };
         u64 m = 0, before;
-        each([&](uint32_t i, uint32_t b) { m += one(i, b); });
+        each([&](uint32_t i, float v) { m += one(i, v); });
         const u64 part = sum_cta(m);
         sum_ctas(part, before);
         locate(one, m, need - 1, before, part, [&](uint32_t i) {
-            for (uint32_t r = 0; r < size; r++) far_store(&S.cut[2], r, first + i);
+            for (uint32_t r = 0; r < size; r++) far_store(&S.cut_idx, r, first + i);
         });
-        if (threadIdx.x == 0) S.cut[0] = low, S.cut[1] = at;
+        if (threadIdx.x == 0) S.cut_v = last;
         sync();
         return false;
     }
@@ -499,17 +530,20 @@ struct Sampler {
         const float x = near(big);
         if (x < (float)kNear) atomicAdd(&S.near_n[(int)x], 1u);
         sync();
-        for (int b = threadIdx.x; b < kNear; b += kThreads) {
-            uint32_t v = 0;
-            for (uint32_t r = 0; r < size; r++) v += far_load(S.near_n + b, r);
-            S.all[b] = v;
+        if (size > 1) {
+            for (int b = threadIdx.x; b < kNear; b += kThreads) {
+                uint32_t v = 0;
+                for (uint32_t r = 0; r < size; r++) v += far_load(S.near_n + b, r);
+                S.all[b] = v;
+            }
+            __syncthreads();
         }
-        __syncthreads();
         if (warp == 0) {
             constexpr int kPer = kNear / 32;
             uint32_t v[kPer], s = 0, edge = ~0u;
 #pragma unroll
-            for (int j = 0; j < kPer; j++) s += v[j] = (uint32_t)S.all[lane * kPer + j];
+            for (int j = 0; j < kPer; j++)
+                s += v[j] = size > 1 ? (uint32_t)S.all[lane * kPer + j] : S.near_n[lane * kPer + j];
             uint32_t run = warp_incl_sum(s, lane) - s;
 #pragma unroll
             for (int j = 0; j < kPer; j++) {
@@ -522,40 +556,40 @@ struct Sampler {
         __syncthreads();
         if ((uint32_t)S.pick[0] == ~0u) return false;
         const float edge = (float)(uint32_t)S.pick[0];
-        each([&](uint32_t i, uint32_t b) {
-            if (near(__uint_as_float(b)) < edge) {
+        each([&](uint32_t i, float v) {
+            if (near(v) < edge) {
                 const uint32_t n = atomicAdd(&S.small_n, 1u);
-                if (n < kSmall) S.small[n] = (u64)key_of(__uint_as_float(b)) << 32 | (uint32_t)~(first + i);
+                if (n < kSmall) S.small[n] = (u64)key_of(v) << 32 | (uint32_t)~(first + i);
             }
         });
         sync();
-        uint32_t n = 0;
-        for (uint32_t r = 0; r < size; r++) n += far_load(&S.small_n, r);
-        if (n > kSmall) return false;
-        u64 *order = (u64 *)S.lo, *heavy = order + kSmallK;   // in the histogram's place
-        static_assert(sizeof(S.lo) + sizeof(S.hi) >= 2 * kSmallK * sizeof(u64), "room for the sorted list");
-        if (rank == 0) {
-            if (size > 1) {   // the other CTAs' behind this one's
+        uint32_t n = S.small_n;
+        if (size > 1) {
+            uint32_t c = (uint32_t)lane < size ? far_load(&S.small_n, lane) : 0;
+            n = __reduce_add_sync(kFull, c);
+            if (n <= kSmall && rank == 0) {   // the other CTAs' behind this one's
                 uint32_t at = S.small_n;
                 for (uint32_t r = 1; r < size; r++) {
-                    const uint32_t c = far_load(&S.small_n, r);
-                    for (uint32_t i = threadIdx.x; i < c; i += kThreads) S.small[at + i] = far_load(S.small + i, r);
-                    at += c;
+                    const uint32_t m = __shfl_sync(kFull, c, r);
+                    for (uint32_t i = threadIdx.x; i < m; i += kThreads) S.small[at + i] = far_load(S.small + i, r);
+                    at += m;
                 }
             }
-            __syncthreads();
+            sync();           // the other CTAs end here
         }
-        sync();               // the other CTAs end here
+        if (n > kSmall) return false;
         if (rank != 0) return true;
+        u64 *order = (u64 *)S.lo, *heavy = order + kSmallK;   // in the histogram's place
+        static_assert(sizeof(S.lo) + sizeof(S.hi) >= 2 * kSmallK * sizeof(u64), "room for the sorted list");
         // sorted: a token's place is the number of larger ones
         for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
             const u64 y = S.small[i];
             uint32_t place = 0;
-#pragma unroll 4
+#pragma unroll 8
             for (uint32_t j = 0; j < n; j++) place += S.small[j] > y;
             if (place < k) {
                 order[place] = y;
-                heavy[place] = weight(row_exp(key_value((uint32_t)(y >> 32))));
+                heavy[place] = weight_at(key_value((uint32_t)(y >> 32)));
             }
         }
         __syncthreads();
@@ -578,8 +612,12 @@ struct Sampler {
             uint32_t keep = 0;
 #pragma unroll
             for (int j = 0; j < kPer; j++) {
-                if (w[j] > 0 && run < edge && w[j] >= least) keep++, total += w[j];
+                const bool in = w[j] > 0 && run < edge;
                 run += w[j];
+                if (!(in && w[j] >= least)) w[j] = 0;
+                if (in) keep++;
+                total += w[j];
+                if ((uint32_t)(lane * kPer + j) < n) heavy[lane * kPer + j] = w[j];
             }
             keep = __reduce_add_sync(kFull, keep);
             total = warp_sum(total);
@@ -591,9 +629,9 @@ struct Sampler {
         for (uint32_t i = threadIdx.x; i < keep; i += kThreads) {
             const uint32_t mine = (uint32_t)order[i];   // ~id
             u64 run = 0;
-#pragma unroll 4
+#pragma unroll 8
             for (uint32_t j = 0; j < keep; j++) run += (uint32_t)order[j] > mine ? heavy[j] : 0;
-            if (run <= t && t < run + heavy[i]) answer(row, ~mine, total);
+            if (run <= t && t < run + heavy[i]) answer(row, ~mine, key_value((uint32_t)(order[i] >> 32)), total);
         }
         return true;
     }
@@ -604,74 +642,66 @@ struct Sampler {
         const u64 t = x > 0.0 ? (u64)x : 0;
         return t < total ? t : total - 1;
     }
-    __device__ __forceinline__ void answer(uint32_t row, uint32_t id, u64 total) const {
+    __device__ __forceinline__ void answer(uint32_t row, uint32_t id, float v, u64 total) const {
         P.ids[row] = (int32_t)id;
-        if (P.logprob) P.logprob[row] = z_of(logit(id), top, inv_t) - logf((float)total * 0x1p-40f);
+        if (P.logprob) P.logprob[row] = z_of(v, top, inv_t) - logf((float)total * 0x1p-40f);
     }
     // own: this thread's kept mass.
-    __device__ __forceinline__ void draw(uint32_t row, u64 own, u64 total, u64 before, u64 mine) const {
-        auto value = [&](uint32_t i, uint32_t b) { return in_cut(i, b) ? weight(__uint_as_float(b)) : 0; };
-        const_cast<Sampler *>(this)->locate(value, own, goal_of(row, total), before, mine,
-                                            [&](uint32_t i) { answer(row, first + i, total); });
+    __device__ __forceinline__ void draw(uint32_t row, u64 own, u64 total, u64 before, u64 mine, u64 least) const {
+        locate([&](uint32_t i, float v) { return kept(i, v, least); }, own, goal_of(row, total), before, mine,
+               [&](uint32_t i) { answer(row, first + i, logit(i), total); });
         sync();   // no CTA ends while another may read its shared memory
     }
 };
 
-// Four tokens of a row as f32.
-template <typename T> __device__ __forceinline__ float4 load_quad(const T *p);
-template <> __device__ __forceinline__ float4 load_quad<float>(const float *p) { return __ldcs((const float4 *)p); }
-template <> __device__ __forceinline__ float4 load_quad<__nv_bfloat16>(const __nv_bfloat16 *p) {
-    const uint2 v = __ldcs((const uint2 *)p);
-    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
-                       __uint_as_float(v.y & 0xFFFF0000u));
-}
-template <> __device__ __forceinline__ float4 load_quad<__half>(const __half *p) {
-    const uint2 v = __ldcs((const uint2 *)p);
-    const float2 a = __half22float2(*(const __half2 *)&v.x), b = __half22float2(*(const __half2 *)&v.y);
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-
-// The CTA's tokens to shared memory; the largest of this thread's, NaN aside.
-template <typename T, int kThreads>
-__device__ __forceinline__ float load_row(const T *l, uint32_t count, bool wide, float4 *e) {
+// The CTA's logits to shared memory as they are; the largest of this thread's, NaN aside.
+template <bool kHalf, int kThreads>
+__device__ __forceinline__ float load_row(Sampler<kHalf, kThreads> &A, const uint8_t *l, bool wide) {
+    constexpr int kVec = kHalf ? 8 : 4, kSize = kHalf ? 2 : 4;
     float big = -INFINITY;
-    const uint32_t whole = wide ? count / 4 : 0;
+    const uint32_t whole = wide ? A.count / kVec : 0;
 #pragma unroll 8
-    for (uint32_t q = threadIdx.x; q < whole; q += kThreads) {
-        const float4 v = load_quad(l + q * 4);
-        big = fmaxf(fmaxf(big, fmaxf(v.x, v.y)), fmaxf(v.z, v.w));
-        e[q] = v;
+    for (uint32_t g = threadIdx.x; g < whole; g += kThreads) {
+        const uint4 q = __ldcs((const uint4 *)l + g);
+        float v[kVec];
+        A.unpack(q, v);
+#pragma unroll
+        for (int j = 0; j < kVec; j++) big = fmaxf(big, v[j]);
+        A.S.row[g] = q;
     }
-    const uint32_t end = (count + 3) & ~3u;
+    const uint32_t end = (A.count + kVec - 1) / kVec * kVec;
 #pragma unroll 4
-    for (uint32_t i = whole * 4 + threadIdx.x; i < end; i += kThreads) {
-        const float v = i < count ? to_f32(l[i]) : -INFINITY;
-        big = fmaxf(big, v);
-        ((float *)e)[i] = v;
+    for (uint32_t i = whole * kVec + threadIdx.x; i < end; i += kThreads) {
+        uint32_t b = kSize == 4 || A.P.type == BPE_BF16 ? 0xFF800000u : 0xFC00FC00u;   // -infinity
+        if (kSize == 2 && A.P.type == BPE_BF16) b >>= 16;
+        if (i < A.count) b = kHalf ? ((const unsigned short *)l)[i] : ((const uint32_t *)l)[i];
+        if (kHalf)
+            ((unsigned short *)A.S.row)[i] = (unsigned short)b;
+        else
+            ((uint32_t *)A.S.row)[i] = b;
+        big = fmaxf(big, kHalf ? A.decode(b & 0xFFFFu) : __uint_as_float(b));
     }
     return big;
 }
 
-template <int kThreads>
+template <bool kHalf, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
     extern __shared__ __align__(16) uint8_t raw[];
     SampleShared<kThreads> &S = *reinterpret_cast<SampleShared<kThreads> *>(raw);
     const uint32_t row = blockIdx.x / team, rank = blockIdx.x % team;
     const uint32_t first = min(P.n_tok, rank * slice), count = min(P.n_tok, first + slice) - first;
-    const uint64_t at = row * P.stride + first;
     // every CTA of the row has begun before another writes to its shared memory
     if (team > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     for (int i = threadIdx.x; i < kBuckets * S.kCopies; i += kThreads) S.lo[i] = S.hi[i] = 0;
     for (int i = threadIdx.x; i < kNear; i += kThreads) S.near_n[i] = 0;
     if (threadIdx.x == 0) S.small_n = 0;
-    const float big = P.type == BPE_F32    ? load_row<float, kThreads>((const float *)P.logits + at, count, wide, S.e)
-                      : P.type == BPE_BF16 ? load_row<__nv_bfloat16, kThreads>((const __nv_bfloat16 *)P.logits + at, count, wide, S.e)
-                                           : load_row<__half, kThreads>((const __half *)P.logits + at, count, wide, S.e);
-    const uint32_t quads = (count + 3) / 4, span = ((quads + kThreads - 1) / kThreads) | 1;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Sampler<kThreads> A{S, P, (const uint8_t *)P.logits + row * P.stride * (P.type == BPE_F32 ? 4 : 2), rank, team, first,
-                        quads, span, min(quads, threadIdx.x * span), min(quads, (threadIdx.x + 1) * span), lane, warp, 0};
+    Sampler<kHalf, kThreads> A{S, P, rank, team, first, count};
+    constexpr int kVec = kHalf ? 8 : 4;
+    const uint32_t groups = (count + kVec - 1) / kVec, span = ((groups + kThreads - 1) / kThreads) | 1;
+    A.g0 = min(groups, threadIdx.x * span), A.g1 = min(groups, (threadIdx.x + 1) * span);
+    A.lane = threadIdx.x & 31, A.warp = threadIdx.x >> 5, A.turn = 0;
+    const float big = load_row(A, (const uint8_t *)P.logits + (row * P.stride + first) * (kHalf ? 2 : 4), wide);
     if (team > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     const uint32_t kmax = A.max_row(key_of(big));
     if (kmax == kKeyNegInf) {
@@ -686,8 +716,8 @@ k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
     const float temp = P.f.d_temperature ? P.f.d_temperature[row] : P.f.temperature;
     if (!(temp >= kMinScale)) {   // the lowest id of the largest logit
         uint32_t low = 0;
-        A.each([&](uint32_t i, uint32_t b) {
-            if (__uint_as_float(b) == A.top && i < count) low = max(low, ~(first + i));
+        A.each([&](uint32_t i, float v) {
+            if (v == A.top && i < count) low = max(low, ~(first + i));
         });
         low = A.max_row(low);
         if (rank == 0 && threadIdx.x == 0) {
@@ -704,54 +734,51 @@ k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
     A.inv_t = 1.0f / temp;
     const bool by_count = k >= 1 && (uint32_t)k < P.n_tok;
     if (by_count && k <= kSmallK && A.top < INFINITY && A.small_list(big, (uint32_t)k, p, least, row)) return;
-    if (threadIdx.x == 0) S.cut[0] = kLeast, S.cut[1] = 0, S.cut[2] = ~0u;   // keep every weight above 0
+    if (threadIdx.x == 0) S.cut_v = -INFINITY, S.cut_idx = ~0u;   // keep all
     u64 total = 0, mine = 0, before, own;
     bool summed = false;
     if (by_count) {
         A.template select<false, true>((u64)k, -1.0);
         if (p < 1.0f) {
+            __syncthreads();
             A.read_cut();
-            const double x = (double)p * (double)A.sum_row(A.mass());
+            const double x = (double)p * (double)A.sum_row(A.mass(0));
+            A.sync();   // the lists have been read by all
             A.template select<true, false>(x > 1.0 ? (u64)x : 1, -1.0);
         }
     } else if (p < 1.0f) {
-        summed = A.template select<true, true>(0, p > 0.0f ? (double)p : 0.0, &total, &mine);
-    } else {
-        uint32_t hi = 0, lo = 0;
-        A.to_exp([&](uint32_t b) {
-            const Parts w = parts_of(__uint_as_float(b));
-            hi += w.hi;
-            lo += w.lo;
-        });
-        __syncthreads();
-        if (!least) {
-            A.read_cut();
-            own = join(hi, 0) + lo;
-            mine = A.sum_cta(own);
-            total = A.sum_ctas(mine, before);
-            A.draw(row, own, total, before, mine);
-            return;
-        }
+        summed = A.template select<true, true>(0, p > 0.0f ? (double)p : 0.0, &total, &mine) && !least;
     }
+    __syncthreads();
     A.read_cut();
-    if (least) {
-        // w >= floor(q 2^40), a multiple of 2^-40 with at most 24 digits: compare e's bits
-        const uint32_t bits = __float_as_uint((float)least * 0x1p-40f);
-        if (bits > A.cut_bits) A.cut_bits = bits, A.cut_idx = ~0u, summed = false;
-    }
-    if (summed) {   // the mass is known; only the CTA that holds the draw adds up its threads'
+    if (summed && team > 1) {   // the mass is known; only the CTA that holds the draw adds up its threads'
         A.sum_ctas(mine, before);
         const u64 t = A.goal_of(row, total);
-        if (t >= before && t - before < mine) A.sum_cta(own = A.mass());
+        if (t >= before && t - before < mine) A.sum_cta(own = A.mass(0));
     } else {
-        own = A.mass();
+        own = A.mass(least);
         mine = A.sum_cta(own);
         total = A.sum_ctas(mine, before);
     }
-    A.draw(row, own, total, before, mine);
+    A.draw(row, own, total, before, mine, least);
 }
 
-// Vocabularies beyond a cluster's shared memory (over 262,144 tokens): one CTA per
+__device__ __forceinline__ u64 weight_of(float v, float top, float inv_t) {
+    return v > -INFINITY ? weight(expf(z_of(v, top, inv_t))) : 0;   // 0 for -infinity and NaN
+}
+
+__device__ __forceinline__ u64 sum_all(u64 v, u64 *red) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    u64 t = 0;
+    for (int i = 0; i < kSampThreads / 32; i++) t += red[i];
+    return t;
+}
+
+// Vocabularies beyond a cluster's shared memory: one CTA per
 // row reads it from L2 again in each step.  The kept tokens are those with a key above `cut`, and the
 // first `ties` with the key `cut`; the cut is found bit by bit.
 template <typename T>
@@ -896,17 +923,15 @@ __global__ void __launch_bounds__(kSampThreads) k_sample_stream(SampleParams P) 
     }
 }
 
-template <int kThreads>
-int launch_team(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows, uint32_t team, bool wide) {
-    auto k = k_sample<kThreads>;
-    const uint32_t slice = ((P.n_tok + team - 1) / team + 3) & ~3u;
-    const size_t smem = sizeof(SampleShared<kThreads>) + (size_t)slice * 4;
+template <bool kHalf, int kThreads>
+int launch_team(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows, uint32_t team, uint32_t slice, bool wide) {
+    auto k = k_sample<kHalf, kThreads>;
     static std::atomic<uint64_t> devices{0};
     BPE_CUDA(ctx, allow_shared(k, ctx->device, kMaxShared, devices), "head_sample");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(n_rows * team);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = sizeof(SampleShared<kThreads>) + (size_t)slice * (kHalf ? 2 : 4);
     cfg.stream = ctx->stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -917,26 +942,27 @@ int launch_team(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows, uint32_t t
     return BPE_OK;
 }
 
+template <bool kHalf>
 int launch(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows) {
-    if (P.n_tok > kMaxTeam * 32768u || n_rows > 0x0FFFFFFFu) {
+    constexpr uint32_t kSize = kHalf ? 2 : 4, kVec = 16 / kSize;
+    constexpr uint32_t kMost = (uint32_t)((kMaxShared - sizeof(SampleShared<1024>)) / 16) * kVec;   // tokens of a CTA
+    static_assert(kMost <= 1024 * 104, "tokens of a thread");
+    if (P.n_tok > kMaxTeam * kMost || n_rows > 0x0FFFFFFFu) {
         auto k = P.type == BPE_F32 ? k_sample_stream<float>
                  : P.type == BPE_BF16 ? k_sample_stream<__nv_bfloat16> : k_sample_stream<__half>;
         k<<<n_rows, kSampThreads, 0, ctx->stream>>>(P);
         BPE_CUDA(ctx, cudaGetLastError(), "head_sample launch");
         return BPE_OK;
     }
-    const uintptr_t quad = 4 * head_type_size(P.type);
-    const bool wide = (uintptr_t)P.logits % quad == 0 && (n_rows == 1 || P.stride % 4 == 0);
-    // the smallest team whose shared memory holds the row, two CTAs an SM; more CTAs a row while the GPU has room
-    uint32_t team = 1;
-    while (team < kMaxTeam && P.n_tok > team * 20480) team *= 2;
-    while (team < kMaxTeam && (uint64_t)n_rows * team * 2 <= (uint64_t)ctx->sm_count * 2 && P.n_tok >= team * 2 * 2048) team *= 2;
-    const uint32_t each = (P.n_tok + team - 1) / team;
-    const bool room = (uint64_t)n_rows * team <= (uint64_t)ctx->sm_count * 2;   // all at once: threads cut the latency
-    if (each <= 5120 && !room) return launch_team<128>(ctx, P, n_rows, team, wide);
-    if (each <= 10240 && !room) return launch_team<256>(ctx, P, n_rows, team, wide);
-    if (each <= 20480) return launch_team<512>(ctx, P, n_rows, team, wide);
-    return launch_team<1024>(ctx, P, n_rows, team, wide);
+    const bool wide = (uintptr_t)P.logits % 16 == 0 && (n_rows == 1 || P.stride % kVec == 0);
+    const uint32_t team = (P.n_tok + kMost - 1) / kMost;
+    const uint32_t slice = ((P.n_tok + team - 1) / team + kVec - 1) / kVec * kVec;
+    // where rows wait for an SM, small CTAs, so that several share one and cover each other's latency; else the
+    // threads that finish a row soonest
+    const bool many = (uint64_t)n_rows * team > (uint64_t)ctx->sm_count;
+    if (slice <= 5120 && many) return launch_team<kHalf, 128>(ctx, P, n_rows, team, slice, wide);
+    if (slice <= 8192 || (many && slice * kSize <= 80 * 1024)) return launch_team<kHalf, 512>(ctx, P, n_rows, team, slice, wide);
+    return launch_team<kHalf, 1024>(ctx, P, n_rows, team, slice, wide);
 }
 
 }  // namespace
@@ -957,5 +983,5 @@ extern "C" int head_sample(bpe_ctx *ctx, const void *d_logits, uint64_t stride, 
     BPE_CUDA(ctx, cudaSetDevice(ctx->device), "cudaSetDevice");
     const head_filters none{1.0f, 0, 1.0f, 0.0f, nullptr, nullptr, nullptr, nullptr};
     SampleParams P{d_logits, stride, n_tok, type, d_u, filters ? *filters : none, d_ids_out, d_logprob_out};
-    return launch(ctx, P, n_rows);
+    return type == BPE_F32 ? launch<false>(ctx, P, n_rows) : launch<true>(ctx, P, n_rows);
 }
