@@ -62,6 +62,16 @@ __device__ __forceinline__ Parts parts_of(float e) {
     const float l = __fmaf_rz(fmaf(e, 0x1p20f, 0x1p23f - t), 0x1p20f, 0x1p23f);
     return {__float_as_uint(t) - kWhole, __float_as_uint(l) - kWhole};
 }
+// Sums of both parts; what the 2^23 of each addition adds is taken off at the end.
+struct PartSum {
+    uint32_t hi = 0, lo = 0;
+    __device__ __forceinline__ void add(float e) {
+        const float t = __fmaf_rz(e, 0x1p20f, 0x1p23f);
+        hi += __float_as_uint(t);
+        lo += __float_as_uint(__fmaf_rz(fmaf(e, 0x1p20f, 0x1p23f - t), 0x1p20f, 0x1p23f));
+    }
+    __device__ __forceinline__ u64 value(uint32_t n) const { return ((u64)(hi - n * kWhole) << 20) + (lo - n * kWhole); }
+};
 __device__ __forceinline__ u64 join(uint32_t hi, uint32_t lo) { return ((u64)hi << 20) + lo; }
 __device__ __forceinline__ u64 weight(float e) {
     const Parts p = parts_of(e);
@@ -76,7 +86,7 @@ constexpr int kList = 128;                 // tokens that are ranked pair by pai
 constexpr int kMaxTeam = 8;
 constexpr size_t kMaxShared = 232448;
 constexpr int kSmallK = 256, kSmall = 512; // top-k up to kSmallK works on a list of up to kSmall tokens
-constexpr int kNear = 128;                 // buckets of 1/8 below the largest logit, for that list
+constexpr int kNear = 256;                 // buckets of 1/8 below the largest logit, for that list
 
 struct __align__(16) Entry { uint32_t key, idx; u64 w; };
 
@@ -84,7 +94,7 @@ template <int kThreads> struct SampleShared {
     static constexpr int kCopies = kThreads / 32;   // of a histogram, by thread: no more than 4,095 tokens meet in one
     uint32_t lo[kBuckets * kCopies], hi[kBuckets * kCopies];
     u64 sum[2][kBuckets];                  // this CTA's histogram, read by the whole cluster
-    u64 all[kBuckets];                     // the row's
+    u64 all[kNear];                        // the row's
     uint32_t near_n[kNear];                // threads by their largest logit
     u64 slot[2][kMaxTeam];                 // a value from each CTA of the cluster
     u64 red[32];
@@ -158,7 +168,7 @@ struct Sampler {
     uint32_t first, count;  // its tokens
     uint32_t g0, g1;        // a thread's groups of 16 bytes: contiguous, an odd number, so that no two lanes' meet in a bank
     int lane, warp, turn;
-    float top, inv_t;
+    float top, temp, inv_t;
     float cut_v;
     uint32_t cut_idx;
 
@@ -193,7 +203,50 @@ struct Sampler {
             }
         }
     }
-    // f(i, logit) for this thread's tokens; those past the end are -infinity
+    // f(first of the tokens, logits) for this thread's groups; those past the end are -infinity
+    template <typename F> __device__ __forceinline__ void groups(F f) const {
+#pragma unroll (kHalf ? 1 : 2)
+        for (uint32_t g = g0; g < g1; g++) {
+            float v[kVec];
+            unpack(S.row[g], v);
+            f(g * kVec, v);
+        }
+    }
+    // the largest of a group, NaN aside
+    __device__ __forceinline__ float most(const uint4 &q) const {
+        if (!kHalf)
+            return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)), fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
+        if (P.type == BPE_BF16) {
+            const __nv_bfloat162 *h = (const __nv_bfloat162 *)&q;
+            const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+            return __bfloat162float(__hmax(m.x, m.y));
+        }
+        const __half2 *h = (const __half2 *)&q;
+        const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        return __half2float(__hmax(m.x, m.y));
+    }
+    // f(i, logit) for this thread's tokens with logits in [low, high]: few, so that most groups end with their largest
+    template <typename F> __device__ __forceinline__ void few(float low, float high, F f) const {
+#pragma unroll 2
+        for (uint32_t g = g0; g < g1; g++) {
+            const uint4 q = S.row[g];
+            if (most(q) >= low) {
+                float v[kVec];
+                unpack(q, v);
+#pragma unroll
+                for (int j = 0; j < kVec; j++)
+                    if (v[j] >= low && v[j] <= high) f(g * kVec + j, v[j]);
+            }
+        }
+    }
+    // Bounds of the logits whose z is in [z0, z1]: wider by more than all rounding (z is above -33).
+    __device__ __forceinline__ float least_logit(float z0) const {
+        return top + (z0 - 1e-3f) * temp - 1e-6f * (fabsf(top) + 40.0f * temp);
+    }
+    __device__ __forceinline__ float most_logit(float z1) const {
+        return z1 > -2e-3f ? INFINITY : top + (z1 + 1e-3f) * temp + 1e-6f * (fabsf(top) + 40.0f * temp);
+    }
+    // f(i, logit) for this thread's tokens
     template <typename F> __device__ __forceinline__ void each(F f) const {
 #pragma unroll 1
         for (uint32_t g = g0; g < g1; g++) {
@@ -203,11 +256,8 @@ struct Sampler {
             for (int j = 0; j < kVec; j++) f(g * kVec + j, v[j]);
         }
     }
-    // z, or -100 where nothing can be drawn (infinities' differences, NaN)
-    __device__ __forceinline__ float z_at(float v) const {
-        if (top == INFINITY) return v == top ? 0.0f : -100.0f;
-        return fmaxf(__fmul_rn(v - top, inv_t), -100.0f);
-    }
+    // z, or -31.75 where nothing can be drawn; NaN too
+    __device__ __forceinline__ float z_at(float v) const { return fmaxf(__fmul_rn(v - top, inv_t), -31.75f); }
     __device__ __forceinline__ uint32_t code_at(float z) const { return __float2uint_rz(z * kCodeScale); }
     __device__ __forceinline__ u64 weight_at(float v) const { return weight(expf(z_at(v))); }
 
@@ -280,24 +330,37 @@ struct Sampler {
     }
 
     __device__ __forceinline__ bool in_cut(uint32_t i, float v) const {
-        return v > cut_v || (v == cut_v && first + i <= cut_idx);
+        return (v > cut_v) | ((v == cut_v) & (first + i <= cut_idx));
     }
     __device__ __forceinline__ u64 kept(uint32_t i, float v, u64 least) const {
         const u64 w = in_cut(i, v) ? weight_at(v) : 0;
         return w >= least ? w : 0;
     }
-    // This thread's kept mass: at most 104 tokens, so the parts stay below 2^32.
+    // This thread's kept mass: at most 104 tokens, so the parts' sums stay below 2^32.
     __device__ __forceinline__ u64 mass(u64 least) const {
-        uint32_t hi = 0, lo = 0;
-        each([&](uint32_t i, float v) {
-            if (in_cut(i, v)) {
-                Parts p = parts_of(expf(z_at(v)));
-                if (least && join(p.hi, p.lo) < least) p = {0, 0};
-                hi += p.hi;
-                lo += p.lo;
+        PartSum sum;
+        if (cut_v == -INFINITY && !least) {   // everything
+            each([&](uint32_t, float v) { sum.add(expf(z_at(v))); });
+            return sum.value((g1 - g0) * kVec);
+        }
+        const float floor_v = least ? fmaxf(cut_v, least_logit(logf((float)least * 0x1p-40f))) : cut_v;
+        uint32_t n = 0;
+#pragma unroll 1
+        for (uint32_t g = g0; g < g1; g++) {
+            const uint4 q = S.row[g];
+            if (most(q) >= floor_v) {
+                float v[kVec];
+                unpack(q, v);
+#pragma unroll
+                for (int j = 0; j < kVec; j++) {
+                    float e = in_cut(g * kVec + j, v[j]) ? expf(z_at(v[j])) : 0.0f;
+                    if (least) e = weight(e) < least ? 0.0f : e;
+                    sum.add(e);
+                }
+                n += kVec;
             }
-        });
-        return join(hi, 0) + lo;
+        }
+        return sum.value(n);
     }
     __device__ __forceinline__ void read_cut() { cut_v = S.cut_v, cut_idx = S.cut_idx; }
 
@@ -325,7 +388,8 @@ struct Sampler {
             if (level == 0) {
                 each([&](uint32_t, float v) {
                     const float z = z_at(v);
-                    const uint32_t k = code_at(z) >> 25;   // 112 and above: no weight
+                    // floor(-4 z), the code's upper bits, in the low bits of a sum that rounds towards zero
+                    const uint32_t k = __float_as_uint(__fmaf_rz(z, -4.0f, 0x1p23f)) - kWhole;
                     if (kMass) {
                         const Parts p = parts_of(expf(z));
                         count_up(&S.lo[k * kCopies + copy], p.lo);
@@ -335,13 +399,14 @@ struct Sampler {
                     }
                 });
             } else {
-                each([&](uint32_t, float v) {
+                const uint32_t width = ((uint32_t)buckets << shift) - 1;
+                few(least_logit((float)(low + width) / kCodeScale), most_logit((float)low / kCodeScale), [&](uint32_t, float v) {
                     const float z = z_at(v);
-                    const uint32_t k = (code_at(z) - low) >> shift;   // wraps to a large number below `low`
-                    if (k < (uint32_t)buckets) {
+                    const uint32_t c = code_at(z) - low;
+                    if (c <= width) {
                         const Parts p = kMass ? parts_of(expf(z)) : Parts{0, 1};
-                        count_up(&S.lo[k * kCopies + copy], p.lo);
-                        if (kMass) count_up(&S.hi[k * kCopies + copy], p.hi);
+                        count_up(&S.lo[(c >> shift) * kCopies + copy], p.lo);
+                        if (kMass) count_up(&S.hi[(c >> shift) * kCopies + copy], p.hi);
                     }
                 });
             }
@@ -418,11 +483,10 @@ struct Sampler {
             if (about <= kList || shift == 0) {
                 const uint32_t width = (1u << shift) - 1;
                 Entry *to = size == 1 ? S.list : S.mine;
-                each([&](uint32_t i, float v) {
-                    const float z = z_at(v);
-                    if (code_at(z) - low <= width) {
+                few(least_logit((float)(low + width) / kCodeScale), most_logit((float)low / kCodeScale), [&](uint32_t i, float v) {
+                    if (code_at(z_at(v)) - low <= width) {
                         const uint32_t n = atomicAdd(&S.list_n, 1u);
-                        if (n < kList) to[n] = Entry{key_of(v), first + i, weight(expf(z))};
+                        if (n < kList) to[n] = Entry{key_of(v), first + i, weight_at(v)};
                     }
                 });
                 sync();
@@ -555,12 +619,10 @@ struct Sampler {
         }
         __syncthreads();
         if ((uint32_t)S.pick[0] == ~0u) return false;
-        const float edge = (float)(uint32_t)S.pick[0];
-        each([&](uint32_t i, float v) {
-            if (near(v) < edge) {
-                const uint32_t n = atomicAdd(&S.small_n, 1u);
-                if (n < kSmall) S.small[n] = (u64)key_of(v) << 32 | (uint32_t)~(first + i);
-            }
+        const float edge = least_logit((float)(uint32_t)S.pick[0] * -0.125f);
+        few(edge, INFINITY, [&](uint32_t i, float v) {
+            const uint32_t n = atomicAdd(&S.small_n, 1u);
+            if (n < kSmall) S.small[n] = (u64)key_of(v) << 32 | (uint32_t)~(first + i);
         });
         sync();
         uint32_t n = S.small_n;
@@ -581,13 +643,15 @@ struct Sampler {
         if (rank != 0) return true;
         u64 *order = (u64 *)S.lo, *heavy = order + kSmallK;   // in the histogram's place
         static_assert(sizeof(S.lo) + sizeof(S.hi) >= 2 * kSmallK * sizeof(u64), "room for the sorted list");
-        // sorted: a token's place is the number of larger ones
-        for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-            const u64 y = S.small[i];
+        // sorted: a token's place is the number of larger ones, counted by four lanes
+        for (uint32_t i = threadIdx.x / 4; i < ((n + 7) & ~7u); i += kThreads / 4) {
+            const u64 y = S.small[min(i, n - 1)];
             uint32_t place = 0;
-#pragma unroll 8
-            for (uint32_t j = 0; j < n; j++) place += S.small[j] > y;
-            if (place < k) {
+#pragma unroll 4
+            for (uint32_t j = lane & 3; j < n; j += 4) place += S.small[j] > y;
+            place += __shfl_xor_sync(kFull, place, 1);
+            place += __shfl_xor_sync(kFull, place, 2);
+            if (i < n && place < k && (lane & 3) == 0) {
                 order[place] = y;
                 heavy[place] = weight_at(key_value((uint32_t)(y >> 32)));
             }
@@ -621,22 +685,24 @@ struct Sampler {
             }
             keep = __reduce_add_sync(kFull, keep);
             total = warp_sum(total);
-            if (lane == 0) S.pick[1] = keep, S.pick[2] = total;
+            if (lane == 0) S.pick[1] = keep, S.pick[2] = total, S.goal = goal_of(row, total);
         }
         __syncthreads();
         const uint32_t keep = (uint32_t)S.pick[1];
-        const u64 total = S.pick[2], t = goal_of(row, total);
-        for (uint32_t i = threadIdx.x; i < keep; i += kThreads) {
-            const uint32_t mine = (uint32_t)order[i];   // ~id
+        const u64 total = S.pick[2], t = S.goal;
+        for (uint32_t i = threadIdx.x / 4; i < ((keep + 7) & ~7u); i += kThreads / 4) {
+            const uint32_t mine = (uint32_t)order[min(i, keep - 1)];   // ~id
             u64 run = 0;
-#pragma unroll 8
-            for (uint32_t j = 0; j < keep; j++) run += (uint32_t)order[j] > mine ? heavy[j] : 0;
-            if (run <= t && t < run + heavy[i]) answer(row, ~mine, key_value((uint32_t)(order[i] >> 32)), total);
+#pragma unroll 4
+            for (uint32_t j = lane & 3; j < keep; j += 4) run += (uint32_t)order[j] > mine ? heavy[j] : 0;
+            run += __shfl_xor_sync(kFull, run, 1);
+            run += __shfl_xor_sync(kFull, run, 2);
+            if (i < keep && (lane & 3) == 0 && run <= t && t < run + heavy[i])
+                answer(row, ~mine, key_value((uint32_t)(order[i] >> 32)), total);
         }
         return true;
     }
 
-    // The running mass that the id drawn passes.
     __device__ __forceinline__ u64 goal_of(uint32_t row, u64 total) const {
         const double x = (double)P.u[row] * (double)total;
         const u64 t = x > 0.0 ? (u64)x : 0;
@@ -646,9 +712,15 @@ struct Sampler {
         P.ids[row] = (int32_t)id;
         if (P.logprob) P.logprob[row] = z_of(v, top, inv_t) - logf((float)total * 0x1p-40f);
     }
+    // The running mass that the id drawn passes, worked out by one thread: 64-bit floating point is slow here.
+    __device__ __forceinline__ u64 goal_for_all(uint32_t row, u64 total) const {
+        if (threadIdx.x == 0) S.goal = goal_of(row, total);
+        __syncthreads();
+        return S.goal;
+    }
     // own: this thread's kept mass.
-    __device__ __forceinline__ void draw(uint32_t row, u64 own, u64 total, u64 before, u64 mine, u64 least) const {
-        locate([&](uint32_t i, float v) { return kept(i, v, least); }, own, goal_of(row, total), before, mine,
+    __device__ __forceinline__ void draw(uint32_t row, u64 own, u64 t, u64 total, u64 before, u64 mine, u64 least) const {
+        locate([&](uint32_t i, float v) { return kept(i, v, least); }, own, t, before, mine,
                [&](uint32_t i) { answer(row, first + i, logit(i), total); });
         sync();   // no CTA ends while another may read its shared memory
     }
@@ -701,7 +773,7 @@ k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
     const uint32_t groups = (count + kVec - 1) / kVec, span = ((groups + kThreads - 1) / kThreads) | 1;
     A.g0 = min(groups, threadIdx.x * span), A.g1 = min(groups, (threadIdx.x + 1) * span);
     A.lane = threadIdx.x & 31, A.warp = threadIdx.x >> 5, A.turn = 0;
-    const float big = load_row(A, (const uint8_t *)P.logits + (row * P.stride + first) * (kHalf ? 2 : 4), wide);
+    float big = load_row(A, (const uint8_t *)P.logits + (row * P.stride + first) * (kHalf ? 2 : 4), wide);
     if (team > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     const uint32_t kmax = A.max_row(key_of(big));
     if (kmax == kKeyNegInf) {
@@ -713,7 +785,19 @@ k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
         return;
     }
     A.top = key_value(kmax);
-    const float temp = P.f.d_temperature ? P.f.d_temperature[row] : P.f.temperature;
+    if (A.top == INFINITY) {   // only infinities can be drawn: 0 in their place, -infinity elsewhere
+        A.each([&](uint32_t i, float v) {
+            const bool in = v == INFINITY;
+            if (kHalf)
+                ((unsigned short *)S.row)[i] = in ? 0 : P.type == BPE_BF16 ? 0xFF80 : 0xFC00;
+            else
+                ((float *)S.row)[i] = in ? 0.0f : -INFINITY;
+        });
+        __syncthreads();
+        A.top = 0.0f;
+        big = -INFINITY;       // small_list's bounds do not hold
+    }
+    const float temp = A.temp = P.f.d_temperature ? P.f.d_temperature[row] : P.f.temperature;
     if (!(temp >= kMinScale)) {   // the lowest id of the largest logit
         uint32_t low = 0;
         A.each([&](uint32_t i, float v) {
@@ -733,7 +817,7 @@ k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
     const u64 least = q > 0.0f ? (u64)(fminf(q, 1.0f) * kOne) : 0;
     A.inv_t = 1.0f / temp;
     const bool by_count = k >= 1 && (uint32_t)k < P.n_tok;
-    if (by_count && k <= kSmallK && A.top < INFINITY && A.small_list(big, (uint32_t)k, p, least, row)) return;
+    if (by_count && k <= kSmallK && A.small_list(big, (uint32_t)k, p, least, row)) return;
     if (threadIdx.x == 0) S.cut_v = -INFINITY, S.cut_idx = ~0u;   // keep all
     u64 total = 0, mine = 0, before, own;
     bool summed = false;
@@ -742,25 +826,31 @@ k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
         if (p < 1.0f) {
             __syncthreads();
             A.read_cut();
-            const double x = (double)p * (double)A.sum_row(A.mass(0));
-            A.sync();   // the lists have been read by all
-            A.template select<true, false>(x > 1.0 ? (u64)x : 1, -1.0);
+            const u64 kept = A.sum_row(A.mass(0));
+            if (threadIdx.x == 0) {
+                const double x = (double)p * (double)kept;
+                S.goal = x > 1.0 ? (u64)x : 1;
+            }
+            A.sync();   // the lists have been read by all, too
+            A.template select<true, false>(S.goal, -1.0);
         }
     } else if (p < 1.0f) {
         summed = A.template select<true, true>(0, p > 0.0f ? (double)p : 0.0, &total, &mine) && !least;
     }
     __syncthreads();
     A.read_cut();
+    u64 t;
     if (summed && team > 1) {   // the mass is known; only the CTA that holds the draw adds up its threads'
         A.sum_ctas(mine, before);
-        const u64 t = A.goal_of(row, total);
+        t = A.goal_for_all(row, total);
         if (t >= before && t - before < mine) A.sum_cta(own = A.mass(0));
     } else {
         own = A.mass(least);
         mine = A.sum_cta(own);
         total = A.sum_ctas(mine, before);
+        t = A.goal_for_all(row, total);
     }
-    A.draw(row, own, total, before, mine, least);
+    A.draw(row, own, t, total, before, mine, least);
 }
 
 __device__ __forceinline__ u64 weight_of(float v, float top, float inv_t) {
@@ -955,7 +1045,11 @@ int launch(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows) {
         return BPE_OK;
     }
     const bool wide = (uintptr_t)P.logits % 16 == 0 && (n_rows == 1 || P.stride % kVec == 0);
-    const uint32_t team = (P.n_tok + kMost - 1) / kMost;
+    uint32_t team = (P.n_tok + kMost - 1) / kMost;
+    // A few rows without a small top-k, whose every logit needs an exponential: while SMs are idle, more CTAs a row
+    // (1 x 32,256: 16 us with 8, 22 with 1); with a small top-k the barriers cost more (33 x 32,256: 18 us with 8, 14 with 1).
+    const bool small_k = P.f.d_top_k || (P.f.top_k >= 1 && P.f.top_k <= kSmallK);
+    while (!small_k && team * 2 <= kMaxTeam && (uint64_t)n_rows * team * 2 <= (uint64_t)ctx->sm_count && P.n_tok >= team * 2 * 4096) team *= 2;
     const uint32_t slice = ((P.n_tok + team - 1) / team + kVec - 1) / kVec * kVec;
     // where rows wait for an SM, small CTAs, so that several share one and cover each other's latency; else the
     // threads that finish a row soonest
