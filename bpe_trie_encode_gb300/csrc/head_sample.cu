@@ -239,6 +239,19 @@ struct Sampler {
             }
         }
     }
+    // f(i, logit) for this thread's groups whose largest is `low` at least
+    template <typename F> __device__ __forceinline__ void some(float low, F f) const {
+#pragma unroll (kHalf ? 1 : 2)
+        for (uint32_t g = g0; g < g1; g++) {
+            const uint4 q = S.row[g];
+            if (most(q) >= low) {
+                float v[kVec];
+                unpack(q, v);
+#pragma unroll
+                for (int j = 0; j < kVec; j++) f(g * kVec + j, v[j]);
+            }
+        }
+    }
     // Bounds of the logits whose z is in [z0, z1]: wider by more than all rounding (z is above -33).
     __device__ __forceinline__ float least_logit(float z0) const {
         return top + (z0 - 1e-3f) * temp - 1e-6f * (fabsf(top) + 40.0f * temp);
@@ -343,9 +356,13 @@ struct Sampler {
             each([&](uint32_t, float v) { sum.add(expf(z_at(v))); });
             return sum.value((g1 - g0) * kVec);
         }
-        const float floor_v = least ? fmaxf(cut_v, least_logit(logf((float)least * 0x1p-40f))) : cut_v;
+        return least ? mass_above<true>(least) : mass_above<false>(0);
+    }
+    template <bool kLeastOn> __device__ __forceinline__ u64 mass_above(u64 least) const {
+        PartSum sum;
+        const float floor_v = kLeastOn ? fmaxf(cut_v, least_logit(logf((float)least * 0x1p-40f))) : cut_v;
         uint32_t n = 0;
-#pragma unroll 1
+#pragma unroll (kHalf ? 1 : 2)
         for (uint32_t g = g0; g < g1; g++) {
             const uint4 q = S.row[g];
             if (most(q) >= floor_v) {
@@ -353,8 +370,9 @@ struct Sampler {
                 unpack(q, v);
 #pragma unroll
                 for (int j = 0; j < kVec; j++) {
-                    float e = in_cut(g * kVec + j, v[j]) ? expf(z_at(v[j])) : 0.0f;
-                    if (least) e = weight(e) < least ? 0.0f : e;
+                    float e = expf(z_at(v[j]));
+                    e = in_cut(g * kVec + j, v[j]) ? e : 0.0f;
+                    if (kLeastOn) e = weight(e) < least ? 0.0f : e;
                     sum.add(e);
                 }
                 n += kVec;
@@ -373,18 +391,30 @@ struct Sampler {
     __device__ __forceinline__ bool select(u64 target, double share, u64 *total = nullptr, u64 *mine = nullptr) {
         u64 above = 0, own = 0;
         uint32_t low = 0;
-        int shift = 25, buckets = kBuckets;
+        int shift = 25, buckets = kBuckets, copies = kCopies;
+        // After the first level the bucket's tokens, where they fit, are listed in the upper half of the histogram's
+        // place, and the levels that follow (4 copies, in the lower half) read only them.
+        constexpr bool kPick = kThreads >= 512;
+        uint32_t *const picked = S.hi, *upper = S.hi;
+        uint32_t n_pick = ~0u;
+        auto in_range = [&](uint32_t width, auto f) {
+            if (n_pick != ~0u) {
+                for (uint32_t j = threadIdx.x; j < n_pick; j += kThreads) f(picked[j], logit(picked[j]));
+            } else {
+                few(least_logit((float)(low + width) / kCodeScale), most_logit((float)low / kCodeScale), f);
+            }
+        };
         for (int level = 0;; level++) {
             // histogram of the codes in [low, low + (buckets << shift))
             if (!kFirst || level > 0) {
-                for (int i = threadIdx.x; i < buckets * kCopies; i += kThreads) {
+                for (int i = threadIdx.x; i < buckets * copies; i += kThreads) {
                     S.lo[i] = 0;
-                    if (kMass) S.hi[i] = 0;
+                    if (kMass) upper[i] = 0;
                 }
             }
             if (threadIdx.x == 0) S.list_n = 0, S.pick[0] = ~0ull;
             __syncthreads();
-            const int copy = threadIdx.x & (kCopies - 1);
+            const int copy = threadIdx.x & (copies - 1);
             if (level == 0) {
                 each([&](uint32_t, float v) {
                     const float z = z_at(v);
@@ -400,13 +430,13 @@ struct Sampler {
                 });
             } else {
                 const uint32_t width = ((uint32_t)buckets << shift) - 1;
-                few(least_logit((float)(low + width) / kCodeScale), most_logit((float)low / kCodeScale), [&](uint32_t, float v) {
+                in_range(width, [&](uint32_t, float v) {
                     const float z = z_at(v);
                     const uint32_t c = code_at(z) - low;
                     if (c <= width) {
                         const Parts p = kMass ? parts_of(expf(z)) : Parts{0, 1};
-                        count_up(&S.lo[(c >> shift) * kCopies + copy], p.lo);
-                        if (kMass) count_up(&S.hi[(c >> shift) * kCopies + copy], p.hi);
+                        count_up(&S.lo[(c >> shift) * copies + copy], p.lo);
+                        if (kMass) count_up(&upper[(c >> shift) * copies + copy], p.hi);
                     }
                 });
             }
@@ -415,10 +445,9 @@ struct Sampler {
             for (int i = threadIdx.x; i < buckets * 4; i += kThreads) {   // four lanes a bucket
                 const int b = i >> 2;
                 u64 v = 0;
-#pragma unroll
-                for (int c = 0; c < kCopies / 4; c++) {
-                    const int a = b * kCopies + (((i & 3) + c * 4 + b * 4) & (kCopies - 1));
-                    v += join(kMass ? S.hi[a] : 0, S.lo[a]);
+                for (int c = 0; c < copies; c += 4) {
+                    const int a = b * copies + (((i & 3) + c + b * 4) & (copies - 1));
+                    v += join(kMass ? upper[a] : 0, S.lo[a]);
                 }
                 const unsigned with = __activemask();
                 v += __shfl_xor_sync(with, v, 1);
@@ -483,7 +512,7 @@ struct Sampler {
             if (about <= kList || shift == 0) {
                 const uint32_t width = (1u << shift) - 1;
                 Entry *to = size == 1 ? S.list : S.mine;
-                few(least_logit((float)(low + width) / kCodeScale), most_logit((float)low / kCodeScale), [&](uint32_t i, float v) {
+                in_range(width, [&](uint32_t i, float v) {
                     if (code_at(z_at(v)) - low <= width) {
                         const uint32_t n = atomicAdd(&S.list_n, 1u);
                         if (n < kList) to[n] = Entry{key_of(v), first + i, weight_at(v)};
@@ -540,6 +569,28 @@ struct Sampler {
                 sync();                  // list_n has been read by all
             }
             __syncthreads();             // what was found has been read by all
+            if (kPick && level == 0) {   // z in (z0, z1] is the bucket
+                const float z0 = (float)(low + (1u << shift)) / kCodeScale, z1 = (float)low / kCodeScale;
+                const float v0 = least_logit(z0);
+                uint32_t mine_n = 0;
+                auto in = [&](float v) { const float z = __fmul_rn(v - top, inv_t); return (z > z0) & (z <= z1); };
+                some(v0, [&](uint32_t, float v) { mine_n += in(v); });
+                const uint32_t upto = warp_incl_sum(mine_n, lane);
+                if (lane == 31) S.red[warp] = upto;
+                __syncthreads();
+                const uint32_t w = lane < kWarps ? (uint32_t)S.red[lane] : 0, run = warp_incl_sum(w, lane);
+                const uint32_t n = __shfl_sync(kFull, run, 31);
+                if (n <= kBuckets * kCopies) {
+                    uint32_t at = __shfl_sync(kFull, run - w, warp) + upto - mine_n;
+                    some(v0, [&](uint32_t i, float v) {
+                        if (in(v)) picked[at++] = i;
+                    });
+                    n_pick = n;
+                    copies = 4;
+                    upper = S.lo + kBuckets * 4;
+                }
+                __syncthreads();
+            }
             buckets = shift >= 7 ? 128 : 1 << shift;
             shift = shift >= 7 ? shift - 7 : 0;
         }
