@@ -501,6 +501,22 @@ def test_other_streams_and_graphs(ctx):
         assert torch.equal(got[0], want[i][0]) and torch.equal(got[1], want[i][1])
 
 
+def test_example_generates_the_same_text_again(ctx):
+    """examples/generate.py: train, encode, norm, logits, draw and decode in one run; each id had its chance."""
+    import importlib.util
+    import os
+    at = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "generate.py")
+    spec = importlib.util.spec_from_file_location("generate", at)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    out, logprob, texts, merges = example.main(["--rows", "3", "--tokens", "20", "--merges", "64"])
+    again = example.main(["--rows", "3", "--tokens", "20", "--merges", "64"])
+    assert torch.equal(out, again[0]) and torch.equal(logprob, again[1]) and texts == again[2]
+    assert out.shape == (3, 20) and (out >= 0).all() and (out < 256 + len(merges)).all()
+    assert (logprob <= 0).all() and torch.isfinite(logprob).all()
+    assert all(len(t) >= 20 for t in texts)
+
+
 def test_refusals(ctx):
     import bpe_trie_encode_gb300 as bt
     x, w = torch.zeros(2, 256, device="cuda"), torch.ones(256, device="cuda")
