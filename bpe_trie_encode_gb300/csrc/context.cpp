@@ -85,7 +85,11 @@ int ensure_events(bpe_ctx *ctx, size_t n) {
 int head_status(bpe_ctx *ctx, uint32_t **out) {
     if (!ctx->head_flag) {
         void *p = nullptr;
-        BPE_CUDA(ctx, cudaHostAlloc(&p, sizeof(uint32_t), cudaHostAllocMapped), "cudaHostAlloc");
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;   // the first call may be a captured one
+        cudaThreadExchangeStreamCaptureMode(&mode);
+        const cudaError_t e = cudaHostAlloc(&p, sizeof(uint32_t), cudaHostAllocMapped);
+        cudaThreadExchangeStreamCaptureMode(&mode);
+        if (e != cudaSuccess) return cuda_fail(ctx, e, "cudaHostAlloc");
         *(uint32_t *)p = 0;
         ctx->head_flag = (uint32_t *)p;
     }
@@ -96,6 +100,30 @@ int head_status(bpe_ctx *ctx, uint32_t **out) {
     void *d = nullptr;
     BPE_CUDA(ctx, cudaHostGetDevicePointer(&d, (void *)ctx->head_flag, 0), "cudaHostGetDevicePointer");
     *out = (uint32_t *)d;
+    return BPE_OK;
+}
+
+int head_scratch(bpe_ctx *ctx, size_t bytes, void **out) {
+    if (!ctx->head_pool) {
+        cudaMemPoolProps props = {};
+        props.allocType = cudaMemAllocationTypePinned;
+        props.location.type = cudaMemLocationTypeDevice;
+        props.location.id = ctx->device;
+        BPE_CUDA(ctx, cudaMemPoolCreate(&ctx->head_pool, &props), "cudaMemPoolCreate");
+        uint64_t keep = ~0ull;   // freed memory stays with the pool for the next call
+        BPE_CUDA(ctx, cudaMemPoolSetAttribute(ctx->head_pool, cudaMemPoolAttrReleaseThreshold, &keep), "cudaMemPoolSetAttribute");
+    }
+    const cudaError_t e = cudaMallocFromPoolAsync(out, bytes, ctx->head_pool, ctx->stream);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(ctx, e == cudaErrorMemoryAllocation ? BPE_ERR_OOM : BPE_ERR_CUDA, "scratch of %zu bytes: %s", bytes,
+                    cudaGetErrorString(e));
+    }
+    return BPE_OK;
+}
+
+int head_scratch_free(bpe_ctx *ctx, void *p) {
+    if (p) BPE_CUDA(ctx, cudaFreeAsync(p, ctx->stream), "cudaFreeAsync");
     return BPE_OK;
 }
 
@@ -162,6 +190,7 @@ extern "C" void bpe_ctx_destroy(bpe_ctx *ctx) {
     for (auto ev : ctx->events) cudaEventDestroy(ev);
     if (ctx->pinned) cudaFreeHost(ctx->pinned);
     if (ctx->head_flag) cudaFreeHost((void *)ctx->head_flag);
+    if (ctx->head_pool) cudaMemPoolDestroy(ctx->head_pool);   // once its last memory is given back
     if (ctx->capture_stream) cudaStreamDestroy(ctx->capture_stream);
     delete ctx;
 }

@@ -490,14 +490,15 @@ int encode_out(bpe_ctx *ctx, CUtensorMap *map, const LogitsParams &P) {
     return BPE_OK;
 }
 
-// `p` itself where TMA can read it, else a copy in scratch.
-int aligned_rows(bpe_ctx *ctx, Slot slot, const uint8_t *&p, uint64_t &stride, uint32_t rows, uint32_t dim) {
-    if (rows == 1 && stride % 16) stride = ((uint64_t)dim + 15) & ~15ull;
+// `p` itself where TMA can read it, else a copy in scratch (*copy, to be given back).
+int aligned_rows(bpe_ctx *ctx, void **copy, const uint8_t *&p, uint64_t &stride, uint32_t rows, uint32_t dim) {
+    if (rows == 1) stride = ((uint64_t)dim + 15) & ~15ull;
     if ((uintptr_t)p % 16 == 0 && stride % 16 == 0 && stride < (1ull << 40)) return BPE_OK;
     const uint32_t to = (dim + 15) & ~15u;
     void *q;
-    int rc = ensure(ctx, slot, (size_t)rows * to, &q);
+    int rc = head_scratch(ctx, (size_t)rows * to, &q);
     if (rc) return rc;
+    *copy = q;
     const uint64_t want = ((uint64_t)rows * (to / 4) + 255) / 256;
     const uint32_t grid = (uint32_t)(want < (uint64_t)ctx->sm_count * 16 ? want : (uint64_t)ctx->sm_count * 16);
     k_head_align<<<grid, 256, 0, ctx->stream>>>(p, stride, rows, dim, (uint8_t *)q, to);
@@ -589,12 +590,17 @@ extern "C" int head_logits(bpe_ctx *ctx, const uint8_t *d_x8, uint64_t x8_stride
     BPE_CUDA(ctx, cudaSetDevice(ctx->device), "cudaSetDevice");
     int rc;
     uint32_t *status;
-    if ((rc = head_status(ctx, &status)) || (rc = aligned_rows(ctx, S_HEAD_X, d_x8, x8_stride, n_rows, dim)) ||
-        (rc = aligned_rows(ctx, S_HEAD_W, d_w8, w8_stride, n_tok, dim)))
-        return rc;
+    if ((rc = head_status(ctx, &status))) return rc;
+    void *copy_x = nullptr, *copy_w = nullptr;
+    rc = aligned_rows(ctx, &copy_x, d_x8, x8_stride, n_rows, dim);
+    if (!rc) rc = aligned_rows(ctx, &copy_w, d_w8, w8_stride, n_tok, dim);
     const LogitsParams P{d_xs, d_ws, d_out, xs_row_stride, xs_block_stride, ws_row_stride, ws_block_stride, out_stride,
                          n_rows, n_tok, (dim + kBlock - 1) / kBlock, false, status};
-    if (out_type == BPE_F32) return launch<float>(ctx, d_x8, x8_stride, d_w8, w8_stride, dim, P);
-    if (out_type == BPE_BF16) return launch<__nv_bfloat16>(ctx, d_x8, x8_stride, d_w8, w8_stride, dim, P);
-    return launch<__half>(ctx, d_x8, x8_stride, d_w8, w8_stride, dim, P);
+    if (!rc)
+        rc = out_type == BPE_F32    ? launch<float>(ctx, d_x8, x8_stride, d_w8, w8_stride, dim, P)
+             : out_type == BPE_BF16 ? launch<__nv_bfloat16>(ctx, d_x8, x8_stride, d_w8, w8_stride, dim, P)
+                                    : launch<__half>(ctx, d_x8, x8_stride, d_w8, w8_stride, dim, P);
+    int freed = head_scratch_free(ctx, copy_x);
+    if (!freed) freed = head_scratch_free(ctx, copy_w);
+    return rc ? rc : freed;
 }

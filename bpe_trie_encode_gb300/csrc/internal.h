@@ -27,7 +27,6 @@ enum Slot {
     S_DEC_TOK, S_DEC_OFF, S_DEC_BSUM, S_DEC_STATE,
     S_L_STATE, S_L_OCC, S_L_EKEY, S_L_ECNT, S_L_ELEN, S_L_EOFF, S_L_VLEN, S_L_BFILL, S_L_EBEST, S_L_FRONT,
     S_L_HSLOT, S_L_HCNT, S_L_HENT, S_L_NS, S_L_CAND, S_L_APP, S_L_REC, S_L_CSTAT, S_L_KMODE, S_L_CBAR, S_L_CTILE,
-    S_HEAD_X, S_HEAD_W,
     S_NUM
 };
 
@@ -88,6 +87,7 @@ struct bpe_ctx {
     const bpe_trie *pipe_trie = nullptr;
     uint32_t pipe_max_len = 0;
     int head_teams[2] = {0, 0};   // persistent CTAs, and pairs of them, that this device runs at once
+    cudaMemPool_t head_pool = nullptr;   // stream-ordered scratch of the head calls (they do not wait for their work)
     volatile uint32_t *head_flag = nullptr;   // host word (mapped) that a head kernel sets when a wait gives up
 };
 
@@ -113,6 +113,11 @@ int ensure_events(bpe_ctx *ctx, size_t n);
 // gives up (made on first use).  Fails with BPE_ERR_TIMEOUT when an earlier
 // call on this context has set it.
 int head_status(bpe_ctx *ctx, uint32_t **out);
+
+// Stream-ordered scratch: made and given back in the order of the context's
+// stream, so that calls on other streams and captured graphs have their own.
+int head_scratch(bpe_ctx *ctx, size_t bytes, void **out);
+int head_scratch_free(bpe_ctx *ctx, void *p);
 
 // Stats helpers.
 void stats_reset(bpe_ctx *ctx);

@@ -412,7 +412,9 @@ void unigram_free(bpe_unigram *model);
  * the hidden state of each position (a row) to the id that follows it.
  * head_norm -> head_logits -> head_sample, then bpe_decode for the bytes.
  * The pages have no counterpart.  All four calls are asynchronous on the
- * context's stream; strides count elements; n_rows == 0 is a no-op. */
+ * context's stream, may be captured in a CUDA graph, and share nothing between
+ * calls, so that streams may take turns freely; strides count elements; n_rows
+ * == 0 is a no-op. */
 enum { BPE_F32 = 0, BPE_BF16 = 1, BPE_F16 = 2 };
 #define BPE_HEAD_BLOCK 128u            /* columns (and vocabulary rows) that share a scale */
 #define BPE_HEAD_MAX_DIM 32768u
@@ -454,8 +456,10 @@ int head_quantize(bpe_ctx *ctx, const void *d_w, uint64_t w_stride, int type, ui
  * b at r * xs_row_stride + b * xs_block_stride.  d_w8: n_tok x dim e4m3, rows
  * w8_stride apart; d_ws: block (t, b) at t * ws_row_stride + b *
  * ws_block_stride.  d_out: n_rows x n_tok of out_type, rows out_stride apart.
- * Matrices whose rows do not all start on 16 bytes are first copied to the
- * context's scratch.  1 <= dim <= BPE_HEAD_MAX_DIM, 1 <= n_tok <=
+ * Matrices whose rows do not all start on 16 bytes are first copied to
+ * stream-ordered scratch.  The kernels' waits are bounded: if one gives up, the
+ * logits are not valid and the next head_logits on the context returns TIMEOUT
+ * (once).  1 <= dim <= BPE_HEAD_MAX_DIM, 1 <= n_tok <=
  * BPE_HEAD_MAX_TOKENS.  Errors: INVALID_ARG, OOM, TIMEOUT, CUDA. */
 int head_logits(bpe_ctx *ctx, const uint8_t *d_x8, uint64_t x8_stride, const float *d_xs, uint64_t xs_row_stride,
                 uint64_t xs_block_stride, const uint8_t *d_w8, uint64_t w8_stride, const float *d_ws,

@@ -227,6 +227,29 @@ def test_logits_strides(ctx, rows, dim, x_pad, w_pad):
     assert (wide[:, :5] == 7).all() and (wide[:, 5 + n:] == 7).all()
 
 
+def test_logits_copies_on_two_streams_and_in_a_graph(ctx):
+    """Rows that have to be copied first: each stream and each captured graph has its own copy."""
+    sets = [logits_inputs(5, 4000, 1001, seed=40 + i) for i in range(2)]
+    want = [ctx.head_logits(*s) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(ctx.head_logits(*sets[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, want[i]) for g in got[i])
+    graph, out = torch.cuda.CUDAGraph(), torch.empty_like(want[0])
+    with torch.cuda.graph(graph):
+        ctx.head_logits(*sets[0], out=out)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want[0])
+
+
 def test_logits_nan_stays_in_its_row(ctx):
     for rows in (4, 140):
         x, xs, w, ws = logits_inputs(rows, 300, 512, seed=11)
@@ -341,7 +364,8 @@ def test_sample(ctx, dtype, n):
         check_sample(ctx, some_logits(6, n, dtype, seed=n + i), uniforms(6, i), temperature=0.5 + 0.2 * i, **kw)
 
 
-@pytest.mark.parametrize("dtype,n,rows", [(F32, 32256, 3), (BF16, 65536, 2), (F32, 250000, 2), (F16, 100001, 2), (BF16, 32256, 5)])
+@pytest.mark.parametrize("dtype,n,rows", [(F32, 32256, 3), (BF16, 65536, 2), (F32, 250000, 2), (F16, 100001, 2), (BF16, 32256, 5),
+                                          (F32, 400001, 1), (BF16, 800003, 1)])
 @pytest.mark.parametrize("spread", [0.01, 0.7, 4.0])
 def test_sample_large_vocabularies(ctx, dtype, n, rows, spread):
     """Flat rows, whose nuclei hold most of the vocabulary and whose 16-bit values tie, and peaked ones."""
