@@ -432,18 +432,28 @@ k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
 }
 
 // -------------------------------------------------------------- the host ---
-// Rows that do not start on 16 bytes, copied to rows that do.
+// Rows that do not start on 16 bytes, copied to rows that do: 16 bytes a thread, from the five aligned words that hold
+// them.  A word is read only if a byte of the row lies in it.
 __global__ void __launch_bounds__(256) k_head_align(const uint8_t *__restrict__ src, uint64_t stride, uint32_t rows,
                                                     uint32_t dim, uint8_t *__restrict__ dst, uint32_t dst_stride) {
-    const uint64_t words = (uint64_t)rows * (dst_stride / 4);
-    for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < words; i += gridDim.x * 256ull) {
-        const uint64_t r = i / (dst_stride / 4);
-        const uint32_t c = (uint32_t)(i % (dst_stride / 4)) * 4;
-        uint32_t v = 0;
+    const uint32_t each = dst_stride / 16;
+    const uint64_t parts = (uint64_t)rows * each;
+    for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < parts; i += gridDim.x * 256ull) {
+        const uint64_t r = i / each;
+        const uint32_t c = (uint32_t)(i % each) * 16;
+        const uintptr_t from = (uintptr_t)(src + r * stride + c), end = (uintptr_t)(src + r * stride + dim);
+        const uint32_t *word = (const uint32_t *)(from & ~(uintptr_t)3);
+        const uint32_t shift = (uint32_t)(from & 3) * 8;
+        uint32_t w[5], v[4];
 #pragma unroll
-        for (int j = 0; j < 4; j++)
-            if (c + j < dim) v |= (uint32_t)src[r * stride + c + j] << (8 * j);
-        *(uint32_t *)(dst + r * dst_stride + c) = v;
+        for (int j = 0; j < 5; j++) w[j] = (uintptr_t)(word + j) < end ? __ldg(word + j) : 0;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            v[j] = __funnelshift_r(w[j], w[j + 1], shift);
+            const int left = (int)dim - (int)(c + 4 * j);   // bytes of the row from here on
+            if (left < 4) v[j] = left <= 0 ? 0 : v[j] & ((1u << 8 * left) - 1);
+        }
+        *(uint4 *)(dst + r * dst_stride + c) = make_uint4(v[0], v[1], v[2], v[3]);
     }
 }
 
@@ -499,7 +509,7 @@ int aligned_rows(bpe_ctx *ctx, void **copy, const uint8_t *&p, uint64_t &stride,
     int rc = head_scratch(ctx, (size_t)rows * to, &q);
     if (rc) return rc;
     *copy = q;
-    const uint64_t want = ((uint64_t)rows * (to / 4) + 255) / 256;
+    const uint64_t want = ((uint64_t)rows * (to / 16) + 255) / 256;
     const uint32_t grid = (uint32_t)(want < (uint64_t)ctx->sm_count * 16 ? want : (uint64_t)ctx->sm_count * 16);
     k_head_align<<<grid, 256, 0, ctx->stream>>>(p, stride, rows, dim, (uint8_t *)q, to);
     BPE_CUDA(ctx, cudaGetLastError(), "head_logits align");
