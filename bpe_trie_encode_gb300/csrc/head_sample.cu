@@ -19,7 +19,7 @@
 // for an exponential and an exact weight, 26 more with two shared-memory
 // atomics for the first histogram; a small top-k needs neither (2 instructions)
 // and is bound by the latency of its steps.  Measured: 4,096 rows of 4,352 bf16
-// without filters 32 us (1.1 TB/s, 54% of issue slots); 256 x 65,536 bf16 with
+// without filters 27 us (1.3 TB/s); 256 x 65,536 bf16 with
 // all filters 25 us (1.4 TB/s); 61 x 250,000 f32, top-p over flat rows, 110 us;
 // 1 x 32,256 f32, top-p, 14 us.
 #include "head.cuh"
@@ -92,23 +92,26 @@ constexpr float kCodeScale = -0x1p27f;     // -z as a whole number
 constexpr uint32_t kCodes = 28u << 27;      // from here on a weight is 0
 constexpr int kList = 128;                 // tokens that are ranked pair by pair
 constexpr int kMaxTeam = 8;
-constexpr size_t kMaxShared = 232448;
+constexpr size_t kMaxShared = 232448, kSmShared = 233472;   // of a CTA, of an SM
 constexpr int kSmallK = 256, kSmall = 512; // top-k up to kSmallK works on a list of up to kSmall tokens
 constexpr int kNear = 256;                 // buckets of 1/8 below the largest logit, for that list
 
 struct __align__(16) Entry { uint32_t key, idx; u64 w; };
 
-template <int kThreads> struct SampleShared {
+// kTeam: the row's CTAs are several.
+template <int kThreads, bool kTeam> struct SampleShared {
     static constexpr int kCopies = kThreads / 32;   // of a histogram, by thread: no more than 4,095 tokens meet in one
     uint32_t lo[kBuckets * kCopies], hi[kBuckets * kCopies];
-    u64 sum[2][kBuckets];                  // this CTA's histogram, read by the whole cluster
-    u64 all[kNear];                        // the row's
+    u64 sum[2][kTeam ? kBuckets : 1];      // this CTA's histogram, read by the whole cluster
+    u64 all[kTeam ? kNear : kBuckets];     // the row's
     uint32_t near_n[kNear];                // threads by their largest logit
     u64 slot[2][kMaxTeam];                 // a value from each CTA of the cluster
     u64 red[32];
-    Entry mine[kList];                     // tokens of the last bucket: this CTA's, read by the whole cluster
-    Entry list[kList];                     // and the row's
-    u64 small[kSmall];                     // logit and id of the largest tokens: this CTA's, read by the first CTA
+    Entry mine[kTeam ? kList : 1];         // tokens of the last bucket: this CTA's, read by the whole cluster
+    union {
+        Entry list[kList];                 // and the row's
+        u64 small[kSmall];                 // logit and id of the largest tokens: this CTA's, read by the first CTA
+    };
     uint32_t list_n, small_n;
     u64 pick[4];                           // bucket found, sums above and in it, this CTA's sum above it
     u64 goal;
@@ -166,13 +169,15 @@ __device__ __forceinline__ u64 warp_scan(u64 v, int lane) {   // inclusive
 }
 
 // kHalf: logits of 16 bits.
-template <bool kHalf, int kThreads>
+template <bool kHalf, int kThreads, bool kTeam>
 struct Sampler {
-    static constexpr int kWarps = kThreads / 32, kCopies = SampleShared<kThreads>::kCopies;
+    using Shared = SampleShared<kThreads, kTeam>;
+    static constexpr int kWarps = kThreads / 32, kCopies = Shared::kCopies;
     static constexpr int kVec = kHalf ? 8 : 4;   // logits in 16 bytes
-    SampleShared<kThreads> &S;
+    Shared &S;
     const SampleParams &P;
-    uint32_t rank, size;    // this CTA among the row's
+    const uint4 *data;      // the CTA's logits
+    uint32_t rank, team;    // this CTA among the row's
     uint32_t first, count;  // its tokens
     uint32_t g0, g1;        // a thread's groups of 16 bytes: contiguous, an odd number, so that no two lanes' meet in a bank
     int lane, warp, turn;
@@ -180,9 +185,10 @@ struct Sampler {
     float cut_v;
     uint32_t cut_idx;
 
+    __device__ __forceinline__ uint32_t members() const { return kTeam ? team : 1; }
     __device__ __forceinline__ void sync() const {
         __syncwarp();
-        if (size == 1)
+        if (members() == 1)
             __syncthreads();
         else
             asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -191,8 +197,8 @@ struct Sampler {
         return P.type == BPE_BF16 ? __uint_as_float(half << 16) : __half2float(__ushort_as_half((unsigned short)half));
     }
     __device__ __forceinline__ float logit(uint32_t i) const {       // of the CTA's token i
-        if (kHalf) return decode(((const unsigned short *)S.row)[i]);
-        return ((const float *)S.row)[i];
+        if (kHalf) return decode(((const unsigned short *)data)[i]);
+        return ((const float *)data)[i];
     }
     __device__ __forceinline__ void unpack(const uint4 &q, float (&v)[kVec]) const {
         if (!kHalf) {
@@ -216,7 +222,7 @@ struct Sampler {
 #pragma unroll (kHalf ? 1 : 2)
         for (uint32_t g = g0; g < g1; g++) {
             float v[kVec];
-            unpack(S.row[g], v);
+            unpack(data[g], v);
             f(g * kVec, v);
         }
     }
@@ -237,7 +243,7 @@ struct Sampler {
     template <typename F> __device__ __forceinline__ void few(float low, float high, F f) const {
 #pragma unroll 2
         for (uint32_t g = g0; g < g1; g++) {
-            const uint4 q = S.row[g];
+            const uint4 q = data[g];
             if (most(q) >= low) {
                 float v[kVec];
                 unpack(q, v);
@@ -251,7 +257,7 @@ struct Sampler {
     template <typename F> __device__ __forceinline__ void some(float low, F f) const {
 #pragma unroll (kHalf ? 1 : 2)
         for (uint32_t g = g0; g < g1; g++) {
-            const uint4 q = S.row[g];
+            const uint4 q = data[g];
             if (most(q) >= low) {
                 float v[kVec];
                 unpack(q, v);
@@ -272,7 +278,7 @@ struct Sampler {
 #pragma unroll 1
         for (uint32_t g = g0; g < g1; g++) {
             float v[kVec];
-            unpack(S.row[g], v);
+            unpack(data[g], v);
 #pragma unroll
             for (int j = 0; j < kVec; j++) f(g * kVec + j, v[j]);
         }
@@ -282,10 +288,20 @@ struct Sampler {
     __device__ __forceinline__ uint32_t code_at(float z) const { return __float2uint_rz(z * kCodeScale); }
     __device__ __forceinline__ u64 weight_at(float v) const { return weight(expf(z_at(v))); }
 
+    // Before a row: a thread's share of it, and clear counters.
+    __device__ __forceinline__ void begin_row() {
+        const uint32_t n = (count + kVec - 1) / kVec, span = ((n + kThreads - 1) / kThreads) | 1;
+        g0 = min(n, threadIdx.x * span), g1 = min(n, (threadIdx.x + 1) * span);
+        lane = threadIdx.x & 31, warp = threadIdx.x >> 5, turn = 0;
+        for (int i = threadIdx.x; i < kBuckets * kCopies; i += kThreads) S.lo[i] = S.hi[i] = 0;
+        for (int i = threadIdx.x; i < kNear; i += kThreads) S.near_n[i] = 0;
+        if (threadIdx.x == 0) S.small_n = 0;
+    }
+
     // One value per CTA to every CTA of the row; all threads of the CTA hold `v`.
     __device__ __forceinline__ void exchange(u64 v) {
         turn ^= 1;
-        if (threadIdx.x < size) far_store(&S.slot[turn][rank], threadIdx.x, v);
+        if (threadIdx.x < members()) far_store(&S.slot[turn][rank], threadIdx.x, v);
         sync();
     }
     __device__ __forceinline__ uint32_t max_row(uint32_t v) {
@@ -294,10 +310,10 @@ struct Sampler {
         if (lane == 0) S.red[warp] = v;
         __syncthreads();
         v = __reduce_max_sync(kFull, lane < kWarps ? (uint32_t)S.red[lane] : 0);
-        if (size == 1) return v;
+        if (members() == 1) return v;
         exchange(v);
         v = 0;
-        for (uint32_t r = 0; r < size; r++) v = max(v, (uint32_t)S.slot[turn][r]);
+        for (uint32_t r = 0; r < members(); r++) v = max(v, (uint32_t)S.slot[turn][r]);
         return v;
     }
     // The CTA's sum; the warps' stay in S.red.
@@ -311,10 +327,10 @@ struct Sampler {
     // The row's sum of the CTAs' sums; `before`: of the CTAs before this one.
     __device__ __forceinline__ u64 sum_ctas(u64 mine, u64 &before) {
         before = 0;
-        if (size == 1) return mine;
+        if (members() == 1) return mine;
         exchange(mine);
         u64 total = 0;
-        for (uint32_t r = 0; r < size; r++) {
+        for (uint32_t r = 0; r < members(); r++) {
             const u64 x = S.slot[turn][r];
             before += r < rank ? x : 0;
             total += x;
@@ -372,7 +388,7 @@ struct Sampler {
         uint32_t n = 0;
 #pragma unroll (kHalf ? 1 : 2)
         for (uint32_t g = g0; g < g1; g++) {
-            const uint4 q = S.row[g];
+            const uint4 q = data[g];
             if (most(q) >= floor_v) {
                 float v[kVec];
                 unpack(q, v);
@@ -449,7 +465,7 @@ struct Sampler {
                 });
             }
             __syncthreads();
-            u64 *sum = size == 1 ? S.all : S.sum[level & 1];
+            u64 *sum = members() == 1 ? S.all : S.sum[level & 1];
             for (int i = threadIdx.x; i < buckets * 4; i += kThreads) {   // four lanes a bucket
                 const int b = i >> 2;
                 u64 v = 0;
@@ -463,11 +479,11 @@ struct Sampler {
                 if ((i & 3) == 0) sum[b] = v;
             }
             sync();
-            if (size > 1) {
+            if (members() > 1) {
                 for (int b = threadIdx.x; b < buckets; b += kThreads) {
                     u64 v[kMaxTeam], s = 0;
 #pragma unroll
-                    for (int r = 0; r < kMaxTeam; r++) v[r] = (uint32_t)r < size ? far_load(sum + b, r) : 0;
+                    for (int r = 0; r < kMaxTeam; r++) v[r] = (uint32_t)r < members() ? far_load(sum + b, r) : 0;
 #pragma unroll
                     for (int r = 0; r < kMaxTeam; r++) s += v[r];
                     S.all[b] = s;
@@ -483,9 +499,9 @@ struct Sampler {
                     const int b = lane * kPer + j;
                     v[j] = b < buckets ? S.all[b] : 0;
                     s += v[j];
-                    if (kMass && size > 1 && b < buckets) m += sum[b];
+                    if (kMass && members() > 1 && b < buckets) m += sum[b];
                 }
-                u64 run = warp_scan(s, lane), part = kMass && size > 1 ? warp_scan(m, lane) - m : 0;
+                u64 run = warp_scan(s, lane), part = kMass && members() > 1 ? warp_scan(m, lane) - m : 0;
                 if (level == 0 && share >= 0.0) {
                     const double x = share * (double)__shfl_sync(kFull, run, 31);
                     target = x > 1.0 ? (u64)x : 1;
@@ -498,10 +514,10 @@ struct Sampler {
                         S.pick[0] = b;
                         S.pick[1] = run;
                         S.pick[2] = v[j];
-                        S.pick[3] = size > 1 ? part : run;
+                        S.pick[3] = members() > 1 ? part : run;
                     }
                     run += v[j];
-                    if (kMass && size > 1 && b < buckets) part += sum[b];
+                    if (kMass && members() > 1 && b < buckets) part += sum[b];
                 }
                 if (lane == 0) S.goal = target;
             }
@@ -510,7 +526,7 @@ struct Sampler {
             target = S.goal;
             low += (uint32_t)S.pick[0] << shift;
             above = S.pick[1];
-            own = size > 1 ? own + S.pick[3] : above;
+            own = members() > 1 ? own + S.pick[3] : above;
             // are the bucket's tokens few?  By weight: an estimate, and the list says when it was wrong.
             u64 about = S.pick[2];
             if (kMass) {
@@ -519,7 +535,7 @@ struct Sampler {
             }
             if (about <= kList || shift == 0) {
                 const uint32_t width = (1u << shift) - 1;
-                Entry *to = size == 1 ? S.list : S.mine;
+                Entry *to = members() == 1 ? S.list : S.mine;
                 in_range(width, [&](uint32_t i, float v) {
                     if (code_at(z_at(v)) - low <= width) {
                         const uint32_t n = atomicAdd(&S.list_n, 1u);
@@ -528,8 +544,8 @@ struct Sampler {
                 });
                 sync();
                 uint32_t n = S.list_n;
-                if (size > 1) {   // every CTA's to one list
-                    uint32_t c = (uint32_t)lane < size ? far_load(&S.list_n, lane) : 0;
+                if (members() > 1) {   // every CTA's to one list
+                    uint32_t c = (uint32_t)lane < members() ? far_load(&S.list_n, lane) : 0;
                     const uint32_t end = warp_incl_sum(c, lane);
                     n = __shfl_sync(kFull, end, 31);
                     for (uint32_t i = threadIdx.x; i < ((n + 31) & ~31u) && n <= kList; i += kThreads) {
@@ -537,7 +553,7 @@ struct Sampler {
 #pragma unroll
                         for (int r = 0; r < kMaxTeam - 1; r++) {
                             const uint32_t e = __shfl_sync(kFull, end, r);
-                            if ((uint32_t)r < size && i >= e) from = r + 1, begin = e;
+                            if ((uint32_t)r < members() && i >= e) from = r + 1, begin = e;
                         }
                         if (i < n) *reinterpret_cast<uint4 *>(&S.list[i]) = far_load(&S.mine[i - begin], from);
                     }
@@ -552,11 +568,11 @@ struct Sampler {
                             const Entry y = S.list[j];
                             const bool before = y.key > x.key || (y.key == x.key && y.idx < x.idx);
                             if (before) run += kMass ? y.w : 1;
-                            if (kMass && size > 1 && (before || j == i) && y.idx - first < count) here += y.w;
+                            if (kMass && members() > 1 && (before || j == i) && y.idx - first < count) here += y.w;
                         }
                         run += __shfl_xor_sync(kFull, run, 1);
                         run += __shfl_xor_sync(kFull, run, 2);
-                        if (kMass && size > 1) {
+                        if (kMass && members() > 1) {
                             here += __shfl_xor_sync(kFull, here, 1);
                             here += __shfl_xor_sync(kFull, here, 2);
                         }
@@ -566,7 +582,7 @@ struct Sampler {
                             S.cut_v = key_value(x.key);
                             S.cut_idx = x.idx;
                             S.pick[1] = upto;
-                            S.pick[3] = size > 1 ? own + here : upto;
+                            S.pick[3] = members() > 1 ? own + here : upto;
                         }
                     }
                     __syncthreads();
@@ -637,7 +653,7 @@ struct Sampler {
         const u64 part = sum_cta(m);
         sum_ctas(part, before);
         locate(one, m, need - 1, before, part, [&](uint32_t i) {
-            for (uint32_t r = 0; r < size; r++) far_store(&S.cut_idx, r, first + i);
+            for (uint32_t r = 0; r < members(); r++) far_store(&S.cut_idx, r, first + i);
         });
         if (threadIdx.x == 0) S.cut_v = last;
         sync();
@@ -653,10 +669,10 @@ struct Sampler {
         const float x = near(big);
         if (x < (float)kNear) atomicAdd(&S.near_n[(int)x], 1u);
         sync();
-        if (size > 1) {
+        if (members() > 1) {
             for (int b = threadIdx.x; b < kNear; b += kThreads) {
                 uint32_t v = 0;
-                for (uint32_t r = 0; r < size; r++) v += far_load(S.near_n + b, r);
+                for (uint32_t r = 0; r < members(); r++) v += far_load(S.near_n + b, r);
                 S.all[b] = v;
             }
             __syncthreads();
@@ -666,7 +682,7 @@ struct Sampler {
             uint32_t v[kPer], s = 0, edge = ~0u;
 #pragma unroll
             for (int j = 0; j < kPer; j++)
-                s += v[j] = size > 1 ? (uint32_t)S.all[lane * kPer + j] : S.near_n[lane * kPer + j];
+                s += v[j] = members() > 1 ? (uint32_t)S.all[lane * kPer + j] : S.near_n[lane * kPer + j];
             uint32_t run = warp_incl_sum(s, lane) - s;
 #pragma unroll
             for (int j = 0; j < kPer; j++) {
@@ -685,12 +701,12 @@ struct Sampler {
         });
         sync();
         uint32_t n = S.small_n;
-        if (size > 1) {
-            uint32_t c = (uint32_t)lane < size ? far_load(&S.small_n, lane) : 0;
+        if (members() > 1) {
+            uint32_t c = (uint32_t)lane < members() ? far_load(&S.small_n, lane) : 0;
             n = __reduce_add_sync(kFull, c);
             if (n <= kSmall && rank == 0) {   // the other CTAs' behind this one's
                 uint32_t at = S.small_n;
-                for (uint32_t r = 1; r < size; r++) {
+                for (uint32_t r = 1; r < members(); r++) {
                     const uint32_t m = __shfl_sync(kFull, c, r);
                     for (uint32_t i = threadIdx.x; i < m; i += kThreads) S.small[at + i] = far_load(S.small + i, r);
                     at += m;
@@ -785,10 +801,31 @@ struct Sampler {
     }
 };
 
-// The CTA's logits to shared memory as they are; the largest of this thread's, NaN aside.
-template <bool kHalf, int kThreads>
-__device__ __forceinline__ float load_row(Sampler<kHalf, kThreads> &A, const uint8_t *l, bool wide) {
+// The CTA's logits to shared memory one at a time, from group `whole` on, and -infinity to the last group's end; the
+// largest of this thread's, NaN aside.
+template <bool kHalf, int kThreads, bool kTeam>
+__device__ __forceinline__ float load_tail(Sampler<kHalf, kThreads, kTeam> &A, uint4 *to, const uint8_t *l, uint32_t whole) {
     constexpr int kVec = kHalf ? 8 : 4, kSize = kHalf ? 2 : 4;
+    float big = -INFINITY;
+    const uint32_t end = (A.count + kVec - 1) / kVec * kVec;
+#pragma unroll 4
+    for (uint32_t i = whole * kVec + threadIdx.x; i < end; i += kThreads) {
+        uint32_t b = kSize == 4 || A.P.type == BPE_BF16 ? 0xFF800000u : 0xFC00FC00u;   // -infinity
+        if (kSize == 2 && A.P.type == BPE_BF16) b >>= 16;
+        if (i < A.count) b = kHalf ? ((const unsigned short *)l)[i] : ((const uint32_t *)l)[i];
+        if (kHalf)
+            ((unsigned short *)to)[i] = (unsigned short)b;
+        else
+            ((uint32_t *)to)[i] = b;
+        big = fmaxf(big, kHalf ? A.decode(b & 0xFFFFu) : __uint_as_float(b));
+    }
+    return big;
+}
+
+// The same, 16 bytes at a time where rows start on 16 bytes.
+template <bool kHalf, int kThreads, bool kTeam>
+__device__ __forceinline__ float load_row(Sampler<kHalf, kThreads, kTeam> &A, uint4 *to, const uint8_t *l, bool wide) {
+    constexpr int kVec = kHalf ? 8 : 4;
     float big = -INFINITY;
     const uint32_t whole = wide ? A.count / kVec : 0;
 #pragma unroll 8
@@ -798,42 +835,16 @@ __device__ __forceinline__ float load_row(Sampler<kHalf, kThreads> &A, const uin
         A.unpack(q, v);
 #pragma unroll
         for (int j = 0; j < kVec; j++) big = fmaxf(big, v[j]);
-        A.S.row[g] = q;
+        to[g] = q;
     }
-    const uint32_t end = (A.count + kVec - 1) / kVec * kVec;
-#pragma unroll 4
-    for (uint32_t i = whole * kVec + threadIdx.x; i < end; i += kThreads) {
-        uint32_t b = kSize == 4 || A.P.type == BPE_BF16 ? 0xFF800000u : 0xFC00FC00u;   // -infinity
-        if (kSize == 2 && A.P.type == BPE_BF16) b >>= 16;
-        if (i < A.count) b = kHalf ? ((const unsigned short *)l)[i] : ((const uint32_t *)l)[i];
-        if (kHalf)
-            ((unsigned short *)A.S.row)[i] = (unsigned short)b;
-        else
-            ((uint32_t *)A.S.row)[i] = b;
-        big = fmaxf(big, kHalf ? A.decode(b & 0xFFFFu) : __uint_as_float(b));
-    }
-    return big;
+    return fmaxf(big, load_tail(A, to, l, whole));
 }
-
-template <bool kHalf, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
-k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
-    extern __shared__ __align__(16) uint8_t raw[];
-    SampleShared<kThreads> &S = *reinterpret_cast<SampleShared<kThreads> *>(raw);
-    const uint32_t row = blockIdx.x / team, rank = blockIdx.x % team;
-    const uint32_t first = min(P.n_tok, rank * slice), count = min(P.n_tok, first + slice) - first;
-    // every CTA of the row has begun before another writes to its shared memory
-    if (team > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    for (int i = threadIdx.x; i < kBuckets * S.kCopies; i += kThreads) S.lo[i] = S.hi[i] = 0;
-    for (int i = threadIdx.x; i < kNear; i += kThreads) S.near_n[i] = 0;
-    if (threadIdx.x == 0) S.small_n = 0;
-    Sampler<kHalf, kThreads> A{S, P, rank, team, first, count};
-    constexpr int kVec = kHalf ? 8 : 4;
-    const uint32_t groups = (count + kVec - 1) / kVec, span = ((groups + kThreads - 1) / kThreads) | 1;
-    A.g0 = min(groups, threadIdx.x * span), A.g1 = min(groups, (threadIdx.x + 1) * span);
-    A.lane = threadIdx.x & 31, A.warp = threadIdx.x >> 5, A.turn = 0;
-    float big = load_row(A, (const uint8_t *)P.logits + (row * P.stride + first) * (kHalf ? 2 : 4), wide);
-    if (team > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+// One row, whose logits are in place; big: the largest of those that this thread has seen.
+template <bool kHalf, int kThreads, bool kTeam>
+__device__ __forceinline__ void sample_row(Sampler<kHalf, kThreads, kTeam> &A, uint32_t row, float big, uint4 *to) {
+    auto &S = A.S;
+    const SampleParams &P = A.P;
+    const uint32_t rank = A.rank, first = A.first, count = A.count;
     const uint32_t kmax = A.max_row(key_of(big));
     if (kmax == kKeyNegInf) {
         if (rank == 0 && threadIdx.x == 0) {
@@ -848,9 +859,9 @@ k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
         A.each([&](uint32_t i, float v) {
             const bool in = v == INFINITY;
             if (kHalf)
-                ((unsigned short *)S.row)[i] = in ? 0 : P.type == BPE_BF16 ? 0xFF80 : 0xFC00;
+                ((unsigned short *)to)[i] = in ? 0 : P.type == BPE_BF16 ? 0xFF80 : 0xFC00;
             else
-                ((float *)S.row)[i] = in ? 0.0f : -INFINITY;
+                ((float *)to)[i] = in ? 0.0f : -INFINITY;
         });
         __syncthreads();
         A.top = 0.0f;
@@ -899,7 +910,7 @@ k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
     __syncthreads();
     A.read_cut();
     u64 t;
-    if (summed && team > 1) {   // the mass is known; only the CTA that holds the draw adds up its threads'
+    if (summed && A.members() > 1) {   // the mass is known; only the CTA that holds the draw adds up its threads'
         A.sum_ctas(mine, before);
         t = A.goal_for_all(row, total);
         if (t >= before && t - before < mine) A.sum_cta(own = A.mass(0));
@@ -910,6 +921,60 @@ k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
         t = A.goal_for_all(row, total);
     }
     A.draw(row, own, t, total, before, mine, least);
+}
+
+template <bool kHalf, int kThreads, bool kTeam>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    auto &S = *reinterpret_cast<SampleShared<kThreads, kTeam> *>(raw);
+    const uint32_t row = kTeam ? blockIdx.x / team : blockIdx.x, rank = kTeam ? blockIdx.x % team : 0;
+    const uint32_t first = min(P.n_tok, rank * slice), count = min(P.n_tok, first + slice) - first;
+    // every CTA of the row has begun before another writes to its shared memory
+    if (kTeam) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    Sampler<kHalf, kThreads, kTeam> A{S, P, S.row, rank, team, first, count};
+    A.begin_row();
+    const float big = load_row(A, S.row, (const uint8_t *)P.logits + (row * P.stride + first) * (kHalf ? 2 : 4), wide);
+    if (kTeam) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    sample_row(A, row, big, S.row);
+}
+
+// Many rows of a small vocabulary: each CTA takes rows in turn, and the next one's logits arrive while it draws from
+// this one's.
+template <bool kHalf, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+k_sample_rows(SampleParams P, uint32_t n_rows, uint32_t slice, bool wide) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    auto &S = *reinterpret_cast<SampleShared<kThreads, false> *>(raw);
+    constexpr int kVec = kHalf ? 8 : 4;
+    const uint32_t groups = (P.n_tok + kVec - 1) / kVec, whole = wide ? P.n_tok / kVec : 0;
+    Sampler<kHalf, kThreads, false> A{S, P, S.row, 0, 1, 0, P.n_tok};
+    auto fetch = [&](uint32_t row, uint4 *to) {
+        const uint8_t *l = (const uint8_t *)P.logits + row * P.stride * (kHalf ? 2 : 4);
+        for (uint32_t g = threadIdx.x; g < whole; g += kThreads)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                         ::"r"((uint32_t)__cvta_generic_to_shared(to + g)), "l"(l + (uint64_t)g * 16) : "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (whole < groups) load_tail(A, to, l, whole);
+    };
+    uint4 *now = S.row, *next = S.row + slice / kVec;
+    if (blockIdx.x < n_rows) fetch(blockIdx.x, now);
+    for (uint32_t row = blockIdx.x; row < n_rows; row += gridDim.x) {
+        if (row + gridDim.x < n_rows) fetch(row + gridDim.x, next);
+        A.data = now;
+        A.begin_row();
+        if (row + gridDim.x < n_rows)
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        float big = -INFINITY;
+        for (uint32_t g = A.g0; g < A.g1; g++) big = fmaxf(big, A.most(now[g]));
+        sample_row(A, row, big, now);
+        __syncthreads();
+        uint4 *t = now;
+        now = next, next = t;
+    }
 }
 
 __device__ __forceinline__ u64 weight_of(float v, float top, float inv_t) {
@@ -1072,29 +1137,43 @@ __global__ void __launch_bounds__(kSampThreads) k_sample_stream(SampleParams P) 
     }
 }
 
-template <bool kHalf, int kThreads>
+template <bool kHalf, int kThreads, bool kTeam>
 int launch_team(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows, uint32_t team, uint32_t slice, bool wide) {
-    auto k = k_sample<kHalf, kThreads>;
+    auto k = k_sample<kHalf, kThreads, kTeam>;
     static std::atomic<uint64_t> devices{0};
     BPE_CUDA(ctx, allow_shared(k, ctx->device, kMaxShared, devices), "head_sample");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(n_rows * team);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = sizeof(SampleShared<kThreads>) + (size_t)slice * (kHalf ? 2 : 4);
+    cfg.dynamicSmemBytes = sizeof(SampleShared<kThreads, kTeam>) + (size_t)slice * (kHalf ? 2 : 4);
     cfg.stream = ctx->stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim = {team, 1, 1};
     cfg.attrs = attr;
-    cfg.numAttrs = team > 1 ? 1 : 0;
+    cfg.numAttrs = kTeam ? 1 : 0;
     BPE_CUDA(ctx, cudaLaunchKernelEx(&cfg, k, P, team, slice, wide), "head_sample launch");
+    return BPE_OK;
+}
+
+template <bool kHalf>
+int launch_rows(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows, uint32_t slice, bool wide) {
+    constexpr int kThreads = 128;
+    auto k = k_sample_rows<kHalf, kThreads>;
+    static std::atomic<uint64_t> devices{0};
+    BPE_CUDA(ctx, allow_shared(k, ctx->device, kMaxShared, devices), "head_sample");
+    const size_t smem = sizeof(SampleShared<kThreads, false>) + 2 * (size_t)slice * (kHalf ? 2 : 4);
+    const uint32_t fit = (uint32_t)(kSmShared / (smem + 1024)), per_sm = fit < 8 ? fit : 8;
+    const uint32_t grid = per_sm * (uint32_t)ctx->sm_count;
+    k<<<n_rows < grid ? n_rows : grid, kThreads, smem, ctx->stream>>>(P, n_rows, slice, wide);
+    BPE_CUDA(ctx, cudaGetLastError(), "head_sample launch");
     return BPE_OK;
 }
 
 template <bool kHalf>
 int launch(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows) {
     constexpr uint32_t kSize = kHalf ? 2 : 4, kVec = 16 / kSize;
-    constexpr uint32_t kMost = (uint32_t)((kMaxShared - sizeof(SampleShared<1024>)) / 16) * kVec;   // tokens of a CTA
+    constexpr uint32_t kMost = (uint32_t)((kMaxShared - sizeof(SampleShared<1024, true>)) / 16) * kVec;   // tokens of a CTA
     static_assert(kMost <= 1024 * 104, "tokens of a thread");
     if (P.n_tok > kMaxTeam * kMost || n_rows > 0x0FFFFFFFu) {
         auto k = P.type == BPE_F32 ? k_sample_stream<float>
@@ -1113,9 +1192,13 @@ int launch(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows) {
     // where rows wait for an SM, small CTAs, so that several share one and cover each other's latency; else the
     // threads that finish a row soonest
     const bool many = (uint64_t)n_rows * team > (uint64_t)ctx->sm_count;
-    if (slice <= 5120 && many) return launch_team<kHalf, 128>(ctx, P, n_rows, team, slice, wide);
-    if (slice <= 8192 || (many && slice * kSize <= 80 * 1024)) return launch_team<kHalf, 512>(ctx, P, n_rows, team, slice, wide);
-    return launch_team<kHalf, 1024>(ctx, P, n_rows, team, slice, wide);
+    if (team > 1)
+        return slice <= 8192 ? launch_team<kHalf, 512, true>(ctx, P, n_rows, team, slice, wide)
+                             : launch_team<kHalf, 1024, true>(ctx, P, n_rows, team, slice, wide);
+    if (slice <= 5120 && many) return launch_rows<kHalf>(ctx, P, n_rows, slice, wide);
+    if (slice <= 8192 || (many && slice * kSize <= 80 * 1024))
+        return launch_team<kHalf, 512, false>(ctx, P, n_rows, 1, slice, wide);
+    return launch_team<kHalf, 1024, false>(ctx, P, n_rows, 1, slice, wide);
 }
 
 }  // namespace

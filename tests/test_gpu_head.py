@@ -373,6 +373,32 @@ def test_sample_large_vocabularies(ctx, dtype, n, rows, spread):
         check_sample(ctx, some_logits(rows, n, dtype, seed=i, spread=spread), uniforms(rows, 50 + i), **kw)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("n,pad", [(1000, 0), (999, 2), (5120, 0), (5121, 7), (20000, 0)])
+def test_sample_more_rows_than_multiprocessors(ctx, dtype, n, pad):
+    """CTAs that take several rows in turn; rows with every kind of filter, masks and infinities among them."""
+    rows = 2500 if n <= 1000 else 400
+    x = some_logits(rows, n + pad, dtype, seed=n)[:, :n]
+    x[5::97] = -INF
+    x[7::101, n // 2] = INF
+    x[11::103, 1:] = NAN
+    g = torch.Generator().manual_seed(n)
+    kw = {"temperature": torch.rand(rows, generator=g).cuda() + 0.1,
+          "top_k": torch.randint(-20, 300, (rows,), generator=g, dtype=torch.int32).cuda(),
+          "top_p": (torch.rand(rows, generator=g) * 1.3).cuda(), "min_p": (torch.rand(rows, generator=g) * 0.1 - 0.03).cuda()}
+    kw["temperature"][::50] = 0.0
+    u = uniforms(rows, n + 1)
+    some = torch.arange(0, rows, 7)   # the reference goes row by row
+    ids, lp = ctx.head_sample(x, u, **kw)
+    want, want_lp = sample_reference(x[some], u[some], **{a: v[some] for a, v in kw.items()})
+    assert ids[some].cpu().tolist() == want
+    for a, b in zip(lp[some].cpu().tolist(), want_lp):
+        assert a == b if not math.isfinite(b) else abs(a - b) <= 2.0 ** -22 * (2 + abs(b))
+    plain = {"temperature": 0.7}
+    ids, _ = ctx.head_sample(x, u, **plain)
+    assert ids[some].cpu().tolist() == sample_reference(x[some], u[some], **plain)[0]
+
+
 def test_sample_settings_of_each_row(ctx):
     rows, n = 12, 4352
     g = torch.Generator().manual_seed(3)
