@@ -89,7 +89,6 @@ __device__ __forceinline__ u64 weight(float e) {
 // ------------------------------------------------- rows in shared memory ---
 constexpr int kBuckets = 128;
 constexpr float kCodeScale = -0x1p27f;     // -z as a whole number
-constexpr uint32_t kCodes = 28u << 27;      // from here on a weight is 0
 constexpr int kList = 128;                 // tokens that are ranked pair by pair
 constexpr int kMaxTeam = 8;
 constexpr size_t kMaxShared = 232448, kSmShared = 233472;   // of a CTA, of an SM
@@ -104,7 +103,7 @@ template <int kThreads, bool kTeam> struct SampleShared {
     uint32_t lo[kBuckets * kCopies], hi[kBuckets * kCopies];
     u64 sum[2][kTeam ? kBuckets : 1];      // this CTA's histogram, read by the whole cluster
     u64 all[kTeam ? kNear : kBuckets];     // the row's
-    uint32_t near_n[kNear];                // threads by their largest logit
+    uint32_t near_n[kNear];                // groups of logits by their largest
     u64 slot[2][kMaxTeam];                 // a value from each CTA of the cluster
     u64 red[32];
     Entry mine[kTeam ? kList : 1];         // tokens of the last bucket: this CTA's, read by the whole cluster
@@ -147,10 +146,9 @@ __device__ __forceinline__ uint4 far_load(const Entry *p, uint32_t rank) {
                  : "r"(far_addr(p, rank)) : "memory");
     return v;
 }
-// counter += v where v is not 0, without a branch around it
-__device__ __forceinline__ void count_up(uint32_t *counter, uint32_t v) {
-    asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %1, 0;\n@p red.shared.add.u32 [%0], %1;\n}"
-                 ::"r"((uint32_t)__cvta_generic_to_shared(counter)), "r"(v) : "memory");
+// The counter at this shared address += v, where v is not 0; without a branch around it.
+__device__ __forceinline__ void count_up(uint32_t at, uint32_t v) {
+    asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %1, 0;\n@p red.shared.add.u32 [%0], %1;\n}" ::"r"(at), "r"(v) : "memory");
 }
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {   // of values below 2^63, by parts of 22 bits
@@ -439,17 +437,20 @@ struct Sampler {
             if (threadIdx.x == 0) S.list_n = 0, S.pick[0] = ~0ull;
             __syncthreads();
             const int copy = threadIdx.x & (copies - 1);
+            const uint32_t lo_at = (uint32_t)__cvta_generic_to_shared(S.lo + copy), hi_at = (uint32_t)__cvta_generic_to_shared(upper + copy);
             if (level == 0) {
+                // floor(-4 z), the code's upper bits, lies in the low bits of a sum that rounds towards zero; times the
+                // size of a bucket, the 2^23 above it is taken off the addresses
+                constexpr uint32_t kSize = kCopies * 4, kOff = kWhole * kSize;
                 each([&](uint32_t, float v) {
                     const float z = z_at(v);
-                    // floor(-4 z), the code's upper bits, in the low bits of a sum that rounds towards zero
-                    const uint32_t k = __float_as_uint(__fmaf_rz(z, -4.0f, 0x1p23f)) - kWhole;
+                    const uint32_t at = __float_as_uint(__fmaf_rz(z, -4.0f, 0x1p23f)) * kSize - kOff;
                     if (kMass) {
                         const Parts p = parts_of(expf(z));
-                        count_up(&S.lo[k * kCopies + copy], p.lo);
-                        count_up(&S.hi[k * kCopies + copy], p.hi);
+                        count_up(lo_at + at, p.lo);
+                        count_up(hi_at + at, p.hi);
                     } else {
-                        count_up(&S.lo[k * kCopies + copy], k < (kCodes >> 25));
+                        count_up(lo_at + at, z > -28.0f);
                     }
                 });
             } else {
@@ -459,8 +460,9 @@ struct Sampler {
                     const uint32_t c = code_at(z) - low;
                     if (c <= width) {
                         const Parts p = kMass ? parts_of(expf(z)) : Parts{0, 1};
-                        count_up(&S.lo[(c >> shift) * copies + copy], p.lo);
-                        if (kMass) count_up(&upper[(c >> shift) * copies + copy], p.hi);
+                        const uint32_t at = (c >> shift) * copies * 4;
+                        count_up(lo_at + at, p.lo);
+                        if (kMass) count_up(hi_at + at, p.hi);
                     }
                 });
             }
@@ -660,14 +662,21 @@ struct Sampler {
         return false;
     }
 
-    // top-k up to kSmallK, with what follows it, on a list: the k-th largest of the threads' largest logits is a
-    // lower bound of the k-th largest logit, and few tokens lie above it.  Only they need an exponential.  Returns
-    // false, with nothing done, where the list would not do.
-    __device__ __forceinline__ bool small_list(float big, uint32_t k, float p, u64 least, uint32_t row) {
+    // top-k up to kSmallK, with what follows it, on a list: the k-th largest of the groups' largest logits (in short
+    // rows, of all logits) is a lower bound of the k-th largest logit, and few tokens lie above it.  Only they need an
+    // exponential.  Returns false, with nothing done, where the list would not do.
+    __device__ __forceinline__ bool small_list(uint32_t k, float p, u64 least, uint32_t row) {
         const float scale = inv_t * 8.0f;
         auto near = [&](float v) { return __fmul_rn(top - v, scale); };   // grows as v falls
-        const float x = near(big);
-        if (x < (float)kNear) atomicAdd(&S.near_n[(int)x], 1u);
+        auto file = [&](float v) {
+            const float x = near(v);
+            if (x < (float)kNear) atomicAdd(&S.near_n[(int)x], 1u);
+        };
+        if (kThreads >= 512) {
+            for (uint32_t g = g0; g < g1; g++) file(most(data[g]));   // over 600 groups
+        } else {
+            each([&](uint32_t, float v) { file(v); });
+        }
         sync();
         if (members() > 1) {
             for (int b = threadIdx.x; b < kNear; b += kThreads) {
@@ -865,7 +874,6 @@ __device__ __forceinline__ void sample_row(Sampler<kHalf, kThreads, kTeam> &A, u
         });
         __syncthreads();
         A.top = 0.0f;
-        big = -INFINITY;       // small_list's bounds do not hold
     }
     const float temp = A.temp = P.f.d_temperature ? P.f.d_temperature[row] : P.f.temperature;
     if (!(temp >= kMinScale)) {   // the lowest id of the largest logit
@@ -887,7 +895,7 @@ __device__ __forceinline__ void sample_row(Sampler<kHalf, kThreads, kTeam> &A, u
     const u64 least = q > 0.0f ? (u64)(fminf(q, 1.0f) * kOne) : 0;
     A.inv_t = 1.0f / temp;
     const bool by_count = k >= 1 && (uint32_t)k < P.n_tok;
-    if (by_count && k <= kSmallK && A.small_list(big, (uint32_t)k, p, least, row)) return;
+    if (by_count && k <= kSmallK && A.small_list((uint32_t)k, p, least, row)) return;
     if (threadIdx.x == 0) S.cut_v = -INFINITY, S.cut_idx = ~0u;   // keep all
     u64 total = 0, mine = 0, before, own;
     bool summed = false;
@@ -1156,14 +1164,13 @@ int launch_team(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows, uint32_t t
     return BPE_OK;
 }
 
-template <bool kHalf>
+template <bool kHalf, int kThreads>
 int launch_rows(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows, uint32_t slice, bool wide) {
-    constexpr int kThreads = 128;
     auto k = k_sample_rows<kHalf, kThreads>;
     static std::atomic<uint64_t> devices{0};
     BPE_CUDA(ctx, allow_shared(k, ctx->device, kMaxShared, devices), "head_sample");
     const size_t smem = sizeof(SampleShared<kThreads, false>) + 2 * (size_t)slice * (kHalf ? 2 : 4);
-    const uint32_t fit = (uint32_t)(kSmShared / (smem + 1024)), per_sm = fit < 8 ? fit : 8;
+    const uint32_t fit = (uint32_t)(kSmShared / (smem + 1024)), most = 1024 / kThreads, per_sm = fit < most ? fit : most;
     const uint32_t grid = per_sm * (uint32_t)ctx->sm_count;
     k<<<n_rows < grid ? n_rows : grid, kThreads, smem, ctx->stream>>>(P, n_rows, slice, wide);
     BPE_CUDA(ctx, cudaGetLastError(), "head_sample launch");
@@ -1190,12 +1197,12 @@ int launch(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows) {
     while (!small_k && team * 2 <= kMaxTeam && (uint64_t)n_rows * team * 2 <= (uint64_t)ctx->sm_count && P.n_tok >= team * 2 * 4096) team *= 2;
     const uint32_t slice = ((P.n_tok + team - 1) / team + kVec - 1) / kVec * kVec;
     // where rows wait for an SM, small CTAs, so that several share one and cover each other's latency; else the
-    // threads that finish a row soonest
+    // threads that finish a row soonest (168 x 580, top-k: 19 us with 128 threads a row)
     const bool many = (uint64_t)n_rows * team > (uint64_t)ctx->sm_count;
     if (team > 1)
         return slice <= 8192 ? launch_team<kHalf, 512, true>(ctx, P, n_rows, team, slice, wide)
                              : launch_team<kHalf, 1024, true>(ctx, P, n_rows, team, slice, wide);
-    if (slice <= 5120 && many) return launch_rows<kHalf>(ctx, P, n_rows, slice, wide);
+    if (slice <= 5120 && n_rows > 4 * (uint32_t)ctx->sm_count) return launch_rows<kHalf, 128>(ctx, P, n_rows, slice, wide);
     if (slice <= 8192 || (many && slice * kSize <= 80 * 1024))
         return launch_team<kHalf, 512, false>(ctx, P, n_rows, 1, slice, wide);
     return launch_team<kHalf, 1024, false>(ctx, P, n_rows, 1, slice, wide);
