@@ -19,7 +19,7 @@
 // for an exponential and an exact weight, 26 more with two shared-memory
 // atomics for the first histogram; a small top-k needs neither (2 instructions)
 // and is bound by the latency of its steps.  Measured: 4,096 rows of 4,352 bf16
-// without filters 27 us (1.3 TB/s); 256 x 65,536 bf16 with
+// without filters 25 us (1.4 TB/s); 256 x 65,536 bf16 with
 // all filters 25 us (1.4 TB/s); 61 x 250,000 f32, top-p over flat rows, 110 us;
 // 1 x 32,256 f32, top-p, 14 us.
 #include "head.cuh"
@@ -93,23 +93,24 @@ constexpr int kList = 128;                 // tokens that are ranked pair by pai
 constexpr int kMaxTeam = 8;
 constexpr size_t kMaxShared = 232448, kSmShared = 233472;   // of a CTA, of an SM
 constexpr int kSmallK = 256, kSmall = 512; // top-k up to kSmallK works on a list of up to kSmall tokens
+constexpr int kRowCtas = 12;               // of 128 threads, an SM
 constexpr int kNear = 256;                 // buckets of 1/8 below the largest logit, for that list
 
 struct __align__(16) Entry { uint32_t key, idx; u64 w; };
 
-// kTeam: the row's CTAs are several.
-template <int kThreads, bool kTeam> struct SampleShared {
+// kTeam: the row's CTAs are several.  kCut: with top-k or top-p.
+template <int kThreads, bool kTeam, bool kCut> struct SampleShared {
     static constexpr int kCopies = kThreads / 32;   // of a histogram, by thread: no more than 4,095 tokens meet in one
-    uint32_t lo[kBuckets * kCopies], hi[kBuckets * kCopies];
+    uint32_t lo[kCut ? kBuckets * kCopies : 4], hi[kCut ? kBuckets * kCopies : 4];
     u64 sum[2][kTeam ? kBuckets : 1];      // this CTA's histogram, read by the whole cluster
-    u64 all[kTeam ? kNear : kBuckets];     // the row's
-    uint32_t near_n[kNear];                // groups of logits by their largest
+    u64 all[!kCut ? 2 : kTeam ? kNear : kBuckets];     // the row's
+    uint32_t near_n[kCut ? kNear : 4];                // groups of logits by their largest
     u64 slot[2][kMaxTeam];                 // a value from each CTA of the cluster
     u64 red[32];
     Entry mine[kTeam ? kList : 1];         // tokens of the last bucket: this CTA's, read by the whole cluster
     union {
-        Entry list[kList];                 // and the row's
-        u64 small[kSmall];                 // logit and id of the largest tokens: this CTA's, read by the first CTA
+        Entry list[kCut ? kList : 1];      // and the row's
+        u64 small[kCut ? kSmall : 2];                 // logit and id of the largest tokens: this CTA's, read by the first CTA
     };
     uint32_t list_n, small_n;
     u64 pick[4];                           // bucket found, sums above and in it, this CTA's sum above it
@@ -167,9 +168,9 @@ __device__ __forceinline__ u64 warp_scan(u64 v, int lane) {   // inclusive
 }
 
 // kHalf: logits of 16 bits.
-template <bool kHalf, int kThreads, bool kTeam>
+template <bool kHalf, int kThreads, bool kTeam, bool kCut>
 struct Sampler {
-    using Shared = SampleShared<kThreads, kTeam>;
+    using Shared = SampleShared<kThreads, kTeam, kCut>;
     static constexpr int kWarps = kThreads / 32, kCopies = Shared::kCopies;
     static constexpr int kVec = kHalf ? 8 : 4;   // logits in 16 bytes
     Shared &S;
@@ -291,9 +292,11 @@ struct Sampler {
         const uint32_t n = (count + kVec - 1) / kVec, span = ((n + kThreads - 1) / kThreads) | 1;
         g0 = min(n, threadIdx.x * span), g1 = min(n, (threadIdx.x + 1) * span);
         lane = threadIdx.x & 31, warp = threadIdx.x >> 5, turn = 0;
-        for (int i = threadIdx.x; i < kBuckets * kCopies; i += kThreads) S.lo[i] = S.hi[i] = 0;
-        for (int i = threadIdx.x; i < kNear; i += kThreads) S.near_n[i] = 0;
-        if (threadIdx.x == 0) S.small_n = 0;
+        if (kCut) {
+            for (int i = threadIdx.x; i < kBuckets * kCopies; i += kThreads) S.lo[i] = S.hi[i] = 0;
+            for (int i = threadIdx.x; i < kNear; i += kThreads) S.near_n[i] = 0;
+            if (threadIdx.x == 0) S.small_n = 0;
+        }
     }
 
     // One value per CTA to every CTA of the row; all threads of the CTA hold `v`.
@@ -416,7 +419,7 @@ struct Sampler {
         int shift = 25, buckets = kBuckets, copies = kCopies;
         // After the first level the bucket's tokens, where they fit, are listed in the upper half of the histogram's
         // place, and the levels that follow (4 copies, in the lower half) read only them.
-        constexpr bool kPick = kThreads >= 512;
+        constexpr bool kPick = kThreads >= 256;
         uint32_t *const picked = S.hi, *upper = S.hi;
         uint32_t n_pick = ~0u;
         auto in_range = [&](uint32_t width, auto f) {
@@ -812,8 +815,8 @@ struct Sampler {
 
 // The CTA's logits to shared memory one at a time, from group `whole` on, and -infinity to the last group's end; the
 // largest of this thread's, NaN aside.
-template <bool kHalf, int kThreads, bool kTeam>
-__device__ __forceinline__ float load_tail(Sampler<kHalf, kThreads, kTeam> &A, uint4 *to, const uint8_t *l, uint32_t whole) {
+template <bool kHalf, int kThreads, bool kTeam, bool kCut>
+__device__ __forceinline__ float load_tail(Sampler<kHalf, kThreads, kTeam, kCut> &A, uint4 *to, const uint8_t *l, uint32_t whole) {
     constexpr int kVec = kHalf ? 8 : 4, kSize = kHalf ? 2 : 4;
     float big = -INFINITY;
     const uint32_t end = (A.count + kVec - 1) / kVec * kVec;
@@ -832,8 +835,8 @@ __device__ __forceinline__ float load_tail(Sampler<kHalf, kThreads, kTeam> &A, u
 }
 
 // The same, 16 bytes at a time where rows start on 16 bytes.
-template <bool kHalf, int kThreads, bool kTeam>
-__device__ __forceinline__ float load_row(Sampler<kHalf, kThreads, kTeam> &A, uint4 *to, const uint8_t *l, bool wide) {
+template <bool kHalf, int kThreads, bool kTeam, bool kCut>
+__device__ __forceinline__ float load_row(Sampler<kHalf, kThreads, kTeam, kCut> &A, uint4 *to, const uint8_t *l, bool wide) {
     constexpr int kVec = kHalf ? 8 : 4;
     float big = -INFINITY;
     const uint32_t whole = wide ? A.count / kVec : 0;
@@ -849,8 +852,8 @@ __device__ __forceinline__ float load_row(Sampler<kHalf, kThreads, kTeam> &A, ui
     return fmaxf(big, load_tail(A, to, l, whole));
 }
 // One row, whose logits are in place; big: the largest of those that this thread has seen.
-template <bool kHalf, int kThreads, bool kTeam>
-__device__ __forceinline__ void sample_row(Sampler<kHalf, kThreads, kTeam> &A, uint32_t row, float big, uint4 *to) {
+template <bool kHalf, int kThreads, bool kTeam, bool kCut>
+__device__ __forceinline__ void sample_row(Sampler<kHalf, kThreads, kTeam, kCut> &A, uint32_t row, float big, uint4 *to) {
     auto &S = A.S;
     const SampleParams &P = A.P;
     const uint32_t rank = A.rank, first = A.first, count = A.count;
@@ -894,26 +897,30 @@ __device__ __forceinline__ void sample_row(Sampler<kHalf, kThreads, kTeam> &A, u
     const float q = P.f.d_min_p ? P.f.d_min_p[row] : P.f.min_p;
     const u64 least = q > 0.0f ? (u64)(fminf(q, 1.0f) * kOne) : 0;
     A.inv_t = 1.0f / temp;
-    const bool by_count = k >= 1 && (uint32_t)k < P.n_tok;
-    if (by_count && k <= kSmallK && A.small_list((uint32_t)k, p, least, row)) return;
+    const bool by_count = kCut && k >= 1 && (uint32_t)k < P.n_tok;
+    if constexpr (kCut) {
+        if (by_count && k <= kSmallK && A.small_list((uint32_t)k, p, least, row)) return;
+    }
     if (threadIdx.x == 0) S.cut_v = -INFINITY, S.cut_idx = ~0u;   // keep all
     u64 total = 0, mine = 0, before, own;
     bool summed = false;
-    if (by_count) {
-        A.template select<false, true>((u64)k, -1.0);
-        if (p < 1.0f) {
-            __syncthreads();
-            A.read_cut();
-            const u64 kept = A.sum_row(A.mass(0));
-            if (threadIdx.x == 0) {
-                const double x = (double)p * (double)kept;
-                S.goal = x > 1.0 ? (u64)x : 1;
+    if constexpr (kCut) {
+        if (by_count) {
+            A.template select<false, true>((u64)k, -1.0);
+            if (p < 1.0f) {
+                __syncthreads();
+                A.read_cut();
+                const u64 kept = A.sum_row(A.mass(0));
+                if (threadIdx.x == 0) {
+                    const double x = (double)p * (double)kept;
+                    S.goal = x > 1.0 ? (u64)x : 1;
+                }
+                A.sync();   // the lists have been read by all, too
+                A.template select<true, false>(S.goal, -1.0);
             }
-            A.sync();   // the lists have been read by all, too
-            A.template select<true, false>(S.goal, -1.0);
+        } else if (p < 1.0f) {
+            summed = A.template select<true, true>(0, p > 0.0f ? (double)p : 0.0, &total, &mine) && !least;
         }
-    } else if (p < 1.0f) {
-        summed = A.template select<true, true>(0, p > 0.0f ? (double)p : 0.0, &total, &mine) && !least;
     }
     __syncthreads();
     A.read_cut();
@@ -935,28 +942,28 @@ template <bool kHalf, int kThreads, bool kTeam>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 k_sample(SampleParams P, uint32_t team, uint32_t slice, bool wide) {
     extern __shared__ __align__(16) uint8_t raw[];
-    auto &S = *reinterpret_cast<SampleShared<kThreads, kTeam> *>(raw);
+    auto &S = *reinterpret_cast<SampleShared<kThreads, kTeam, true> *>(raw);
     const uint32_t row = kTeam ? blockIdx.x / team : blockIdx.x, rank = kTeam ? blockIdx.x % team : 0;
     const uint32_t first = min(P.n_tok, rank * slice), count = min(P.n_tok, first + slice) - first;
     // every CTA of the row has begun before another writes to its shared memory
     if (kTeam) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    Sampler<kHalf, kThreads, kTeam> A{S, P, S.row, rank, team, first, count};
+    Sampler<kHalf, kThreads, kTeam, true> A{S, P, S.row, rank, team, first, count};
     A.begin_row();
     const float big = load_row(A, S.row, (const uint8_t *)P.logits + (row * P.stride + first) * (kHalf ? 2 : 4), wide);
     if (kTeam) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     sample_row(A, row, big, S.row);
 }
 
-// Many rows of a small vocabulary: each CTA takes rows in turn, and the next one's logits arrive while it draws from
-// this one's.
+// Many rows of a small vocabulary, without top-k and top-p: each CTA takes rows in turn, and the next one's logits
+// arrive while it draws from this one's.
 template <bool kHalf, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+__global__ void __launch_bounds__(kThreads, kRowCtas)
 k_sample_rows(SampleParams P, uint32_t n_rows, uint32_t slice, bool wide) {
     extern __shared__ __align__(16) uint8_t raw[];
-    auto &S = *reinterpret_cast<SampleShared<kThreads, false> *>(raw);
+    auto &S = *reinterpret_cast<SampleShared<kThreads, false, false> *>(raw);
     constexpr int kVec = kHalf ? 8 : 4;
     const uint32_t groups = (P.n_tok + kVec - 1) / kVec, whole = wide ? P.n_tok / kVec : 0;
-    Sampler<kHalf, kThreads, false> A{S, P, S.row, 0, 1, 0, P.n_tok};
+    Sampler<kHalf, kThreads, false, false> A{S, P, S.row, 0, 1, 0, P.n_tok};
     auto fetch = [&](uint32_t row, uint4 *to) {
         const uint8_t *l = (const uint8_t *)P.logits + row * P.stride * (kHalf ? 2 : 4);
         for (uint32_t g = threadIdx.x; g < whole; g += kThreads)
@@ -1153,7 +1160,7 @@ int launch_team(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows, uint32_t t
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(n_rows * team);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = sizeof(SampleShared<kThreads, kTeam>) + (size_t)slice * (kHalf ? 2 : 4);
+    cfg.dynamicSmemBytes = sizeof(SampleShared<kThreads, kTeam, true>) + (size_t)slice * (kHalf ? 2 : 4);
     cfg.stream = ctx->stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1169,8 +1176,8 @@ int launch_rows(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows, uint32_t s
     auto k = k_sample_rows<kHalf, kThreads>;
     static std::atomic<uint64_t> devices{0};
     BPE_CUDA(ctx, allow_shared(k, ctx->device, kMaxShared, devices), "head_sample");
-    const size_t smem = sizeof(SampleShared<kThreads, false>) + 2 * (size_t)slice * (kHalf ? 2 : 4);
-    const uint32_t fit = (uint32_t)(kSmShared / (smem + 1024)), most = 1024 / kThreads, per_sm = fit < most ? fit : most;
+    const size_t smem = sizeof(SampleShared<kThreads, false, false>) + 2 * (size_t)slice * (kHalf ? 2 : 4);
+    const uint32_t fit = (uint32_t)(kSmShared / (smem + 1024)), most = kRowCtas, per_sm = fit < most ? fit : most;
     const uint32_t grid = per_sm * (uint32_t)ctx->sm_count;
     k<<<n_rows < grid ? n_rows : grid, kThreads, smem, ctx->stream>>>(P, n_rows, slice, wide);
     BPE_CUDA(ctx, cudaGetLastError(), "head_sample launch");
@@ -1180,7 +1187,7 @@ int launch_rows(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows, uint32_t s
 template <bool kHalf>
 int launch(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows) {
     constexpr uint32_t kSize = kHalf ? 2 : 4, kVec = 16 / kSize;
-    constexpr uint32_t kMost = (uint32_t)((kMaxShared - sizeof(SampleShared<1024, true>)) / 16) * kVec;   // tokens of a CTA
+    constexpr uint32_t kMost = (uint32_t)((kMaxShared - sizeof(SampleShared<1024, true, true>)) / 16) * kVec;   // tokens of a CTA
     static_assert(kMost <= 1024 * 104, "tokens of a thread");
     if (P.n_tok > kMaxTeam * kMost || n_rows > 0x0FFFFFFFu) {
         auto k = P.type == BPE_F32 ? k_sample_stream<float>
@@ -1196,13 +1203,16 @@ int launch(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows) {
     const bool small_k = P.f.d_top_k || (P.f.top_k >= 1 && P.f.top_k <= kSmallK);
     while (!small_k && team * 2 <= kMaxTeam && (uint64_t)n_rows * team * 2 <= (uint64_t)ctx->sm_count && P.n_tok >= team * 2 * 4096) team *= 2;
     const uint32_t slice = ((P.n_tok + team - 1) / team + kVec - 1) / kVec * kVec;
+    const bool by_cut = P.f.d_top_k || P.f.top_k >= 1 || P.f.d_top_p || P.f.top_p < 1.0f;   // many short steps
     // where rows wait for an SM, small CTAs, so that several share one and cover each other's latency; else the
     // threads that finish a row soonest (168 x 580, top-k: 19 us with 128 threads a row)
     const bool many = (uint64_t)n_rows * team > (uint64_t)ctx->sm_count;
     if (team > 1)
         return slice <= 8192 ? launch_team<kHalf, 512, true>(ctx, P, n_rows, team, slice, wide)
                              : launch_team<kHalf, 1024, true>(ctx, P, n_rows, team, slice, wide);
-    if (slice <= 5120 && n_rows > 4 * (uint32_t)ctx->sm_count) return launch_rows<kHalf, 128>(ctx, P, n_rows, slice, wide);
+    if (slice <= 5120 && n_rows > 4 * (uint32_t)ctx->sm_count && !by_cut) return launch_rows<kHalf, 128>(ctx, P, n_rows, slice, wide);
+    if (n_rows > 2 * (uint32_t)ctx->sm_count && slice * kSize <= 39 * 1024)
+        return launch_team<kHalf, 256, false>(ctx, P, n_rows, 1, slice, wide);
     if (slice <= 8192 || (many && slice * kSize <= 80 * 1024))
         return launch_team<kHalf, 512, false>(ctx, P, n_rows, 1, slice, wide);
     return launch_team<kHalf, 1024, false>(ctx, P, n_rows, 1, slice, wide);
