@@ -9,9 +9,9 @@
 // search for a running sum in order of ids.
 //
 // A row is read once, into the shared memory of one CTA (up to 46,000 tokens of
-// 32 bits, 92,000 of 16), or of a cluster of up to 8 where it does not fit: a
-// barrier of a cluster costs over 1,000 cycles and a row needs six, so a row
-// is split for its size only.  The cut is found by histograms over -z in fixed
+// 32 bits, 92,000 of 16), or of a cluster of up to 8 where it does not fit or
+// where SMs are idle: a barrier of a cluster costs over 1,000 cycles and a row
+// needs six, so a split never takes an SM from another row.  The cut is found by histograms over -z in fixed
 // point: 4 buckets per unit, then 128 of the bucket that holds the cut, and so
 // on until at most 128 tokens are left, which are ranked by comparing all pairs.
 //
@@ -1204,12 +1204,17 @@ int launch(bpe_ctx *ctx, const SampleParams &P, uint32_t n_rows) {
     while (!small_k && team * 2 <= kMaxTeam && (uint64_t)n_rows * team * 2 <= (uint64_t)ctx->sm_count && P.n_tok >= team * 2 * 4096) team *= 2;
     const uint32_t slice = ((P.n_tok + team - 1) / team + kVec - 1) / kVec * kVec;
     const bool by_cut = P.f.d_top_k || P.f.top_k >= 1 || P.f.d_top_p || P.f.top_p < 1.0f;   // many short steps
-    // where rows wait for an SM, small CTAs, so that several share one and cover each other's latency; else the
-    // threads that finish a row soonest (168 x 580, top-k: 19 us with 128 threads a row)
+    // Where rows wait for an SM, small CTAs, so that several share one and cover each other's latency; else the
+    // threads that finish a row soonest.  In us, with CTAs of 256 / 512 / 1024 threads: 1,548 x 15,500 bf16 top-p
+    // 99 / 116 / 165; 256 x 32,256 bf16 top-p 47 / 41 / 46; 152 x 16,000 bf16 top-p 23 / 18 / 17.  Rows without a cut of
+    // their own by k_sample_rows: 4,096 x 4,352 bf16 25 against 39 with 256 threads a row; with one, its steps of few
+    // threads take longer (2,060 x 2,902 f32 top-k: 64 against 47).  In clusters, 512 threads where two CTAs fit an SM,
+    // since clusters of whole SMs do not fill the GPU: 38 x 65,536 f32 top-p 25 / 36 with 512 / 1024, and 4 x 100,000
+    // 21 / 23; longer slices want the threads (152 x 70,000 f32 top-p 65 / 62).
     const bool many = (uint64_t)n_rows * team > (uint64_t)ctx->sm_count;
     if (team > 1)
-        return slice <= 8192 ? launch_team<kHalf, 512, true>(ctx, P, n_rows, team, slice, wide)
-                             : launch_team<kHalf, 1024, true>(ctx, P, n_rows, team, slice, wide);
+        return slice * kSize <= 80 * 1024 ? launch_team<kHalf, 512, true>(ctx, P, n_rows, team, slice, wide)
+                                          : launch_team<kHalf, 1024, true>(ctx, P, n_rows, team, slice, wide);
     if (slice <= 5120 && n_rows > 4 * (uint32_t)ctx->sm_count && !by_cut) return launch_rows<kHalf, 128>(ctx, P, n_rows, slice, wide);
     if (n_rows > 2 * (uint32_t)ctx->sm_count && slice * kSize <= 39 * 1024)
         return launch_team<kHalf, 256, false>(ctx, P, n_rows, 1, slice, wide);
