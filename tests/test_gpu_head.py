@@ -227,6 +227,21 @@ def test_logits_strides(ctx, rows, dim, x_pad, w_pad):
     assert (wide[:, :5] == 7).all() and (wide[:, 5 + n:] == 7).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("rows", [70, 200])
+@pytest.mark.parametrize("n", [1, 6, 64, 259, 520])
+def test_logits_output_place(ctx, dtype, rows, n):
+    """An output whose rows start at any element gets the same values, and nothing around them is written."""
+    x, xs, w, ws = logits_inputs(rows, n, 256, seed=rows + n)
+    plain = torch.empty(rows, -(-n // 8) * 8, dtype=dtype, device="cuda")[:, :n]
+    want = ctx.head_logits(x, xs, w, ws.mul_(0.05), out=plain)
+    for before in range(9):
+        wide = torch.full((rows, n + 11 + before % 2), 7.0, dtype=dtype, device="cuda")
+        ctx.head_logits(x, xs, w, ws, out=wide[:, before:before + n])
+        assert torch.equal(wide[:, before:before + n], want)
+        assert (wide[:, :before] == 7).all() and (wide[:, before + n:] == 7).all()
+
+
 def test_logits_copies_on_two_streams_and_in_a_graph(ctx):
     """Rows that have to be copied first: each stream and each captured graph has its own copy."""
     sets = [logits_inputs(5, 4000, 1001, seed=40 + i) for i in range(2)]
