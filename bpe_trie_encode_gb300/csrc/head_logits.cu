@@ -604,10 +604,18 @@ int launch_many(bpe_ctx *ctx, const CUtensorMap &mw, const CUtensorMap &mx, cons
 template <typename O>
 int launch(bpe_ctx *ctx, const uint8_t *x8, uint64_t x_stride, const uint8_t *w8, uint64_t w_stride, uint32_t dim, LogitsParams P) {
     const int n = P.n_rows <= 16 ? 16 : P.n_rows <= 32 ? 32 : P.n_rows <= 64 ? 64 : 0;
-    // A pair's 256 rows where they waste no more than 128-row tiles would: 512 x 250,000 x 1,040 takes 138 us by pairs
-    // and 171 by single CTAs, 128 x 65,536 x 4,096 74 and 60.  Up to 64 rows the few-row kernel (64 x 65,536 x 4,096:
-    // 56 us against 53 by 128-row tiles, but 1,000 tokens fill 63 SMs instead of 4).
-    const bool pair = !n && (P.n_rows + 127) / 128 % 2 == 0;
+    P.tma_out = (uintptr_t)P.out % 16 == 0 && P.out_stride * sizeof(O) % 16 == 0 && P.out_stride * sizeof(O) < (1ull << 40);
+    const uint64_t sms = (uint64_t)ctx->sm_count, row_tiles = (P.n_rows + 127) / 128, tok_tiles = (P.n_tok + kManyToks - 1) / kManyToks;
+    const uint64_t singles = (row_tiles * tok_tiles + sms - 1) / sms, pairs = ((row_tiles + 1) / 2 * tok_tiles + sms / 2 - 1) / (sms / 2);
+    // Pairs or single CTAs, by the rounds that each needs and what a round of pairs takes of one of single CTAs: 0.91 to
+    // 0.94 measured over several rounds, more than all of it where there are few (2,000 x 4,352 x 1,024 f32: 19.1 us
+    // against 17.3), 0.75 to 0.83 where rows start between lines of 128 bytes: loads cost more, and pairs load less.
+    // In us, pairs / single CTAs: 512 x 250,000 x 1,024 120 / 129, x 1,040 147 / 175; 779 x 142,608 x 2,896 318 / 368;
+    // 640 x 65,536 x 4,096 156 / 138; 384 x 65,536 x 4,096 103 / 98; 128 x 65,536 x 4,096 74 / 58.  An output that TMA
+    // cannot write makes a tile's end longer than its loads (1,547 x 53,514 x 433: 120 / 108).  Up to 64 rows the few-row
+    // kernel (64 x 65,536 x 4,096: 56 us against 53 by 128-row tiles, but 1,000 tokens fill 63 SMs instead of 4).
+    const float share = P.tma_out && w_stride % kBlock ? 0.8f : singles >= 4 ? 0.95f : 1.05f;
+    const bool pair = !n && (float)pairs * share < (float)singles;
     CUtensorMap mw, mx, mo = {};
     int rc;
     if ((rc = encode_map(ctx, &mw, w8, w_stride, P.n_tok, dim, n ? kStep : pair ? 128 : kManyToks)) ||
@@ -616,7 +624,6 @@ int launch(bpe_ctx *ctx, const uint8_t *x8, uint64_t x_stride, const uint8_t *w8
     if (n == 16) return launch_few<16, O>(ctx, mw, mx, P);
     if (n == 32) return launch_few<32, O>(ctx, mw, mx, P);
     if (n == 64) return launch_few<64, O>(ctx, mw, mx, P);
-    P.tma_out = (uintptr_t)P.out % 16 == 0 && P.out_stride * sizeof(O) % 16 == 0 && P.out_stride * sizeof(O) < (1ull << 40);
     if (P.tma_out && (rc = encode_out<O>(ctx, &mo, P))) return rc;
     return pair ? launch_many<O, 2>(ctx, mw, mx, mo, P) : launch_many<O, 1>(ctx, mw, mx, mo, P);
 }
