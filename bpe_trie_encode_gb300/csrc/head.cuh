@@ -32,10 +32,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// Scale of a block whose largest magnitude is `amax`; NaN stays.
+// Scale of a block whose largest magnitude is `amax`, and what its values are multiplied by; NaN stays.  Both are
+// correctly rounded: 1 / 448 is no 32-bit number, and a product with it put one scale in six a unit in the last place
+// from the quotient.
 __device__ __forceinline__ float block_scale(float amax) {
-    return max_nan(amax * (1.0f / kE4m3Max), kMinScale);
+    return max_nan(__fdiv_rn(amax, kE4m3Max), kMinScale);
 }
+__device__ __forceinline__ float block_back(float scale) { return __frcp_rn(scale); }
 
 // 16 bytes of a type from 32-bit values.
 __device__ __forceinline__ uint4 pack16(const float *v, float) {

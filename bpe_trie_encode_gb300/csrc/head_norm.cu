@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(1024) k_head_norm_vec(NormParams P) {
         }
 #pragma unroll
         for (int d = kLanes / 2; d > 0; d >>= 1) amax = max_nan(amax, __shfl_xor_sync(kFull, amax, d));
-        const float scale = block_scale(amax), back = __fdividef(1.0f, scale);
+        const float scale = block_scale(amax), back = block_back(scale);
         if (i < n) {
             struct alignas(kVec) Bytes { __nv_fp8x2_storage_t v[kVec / 2]; } b;
 #pragma unroll
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kNormThreads) k_head_norm(NormParams P) {
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) amax = max_nan(amax, __shfl_xor_sync(kFull, amax, d));
-        const float scale = block_scale(amax), back = __fdividef(1.0f, scale);
+        const float scale = block_scale(amax), back = block_back(scale);
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             const uint32_t i = b * kBlock + j * 32 + lane;
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kNormThreads) k_head_quantize(const T *__restr
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kWarps; i++) amax = max_nan(amax, red[i]);
-    const float scale = block_scale(amax), back = __fdividef(1.0f, scale);
+    const float scale = block_scale(amax), back = block_back(scale);
 #pragma unroll
     for (int i = 0; i < kRows; i++) {
         const uint64_t row = row0 + warp + i * kWarps;

@@ -1,0 +1,69 @@
+"""The output head on the GPU at its edges: exact roundings, sizes between launch limits, waits that give up, captures."""
+import os
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+E4M3 = torch.float8_e4m3fn
+INF, NAN = float("inf"), float("nan")
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    import bpe_trie_encode_gb300 as bt
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    c = bt.Context(0)
+    yield c
+    c.close()
+
+
+def randn(*shape, seed=0):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed))
+
+
+# ------------------------------------------------------- exact roundings ---
+
+def blocks_exactly(v):
+    """Scales and 8-bit values of the rows of v [rows, dim] (f32), each step one 32-bit operation rounded to nearest even."""
+    rows, dim = v.shape
+    q, scales = torch.empty(rows, dim), []
+    for c in range(0, dim, 128):
+        part = v[:, c:c + 128].numpy()
+        scale = np.maximum(np.abs(part).max(1) / np.float32(448), np.float32(2.0 ** -126))
+        back = np.float32(1) / scale
+        q[:, c:c + 128] = torch.from_numpy(part * back[:, None]).clamp(-448, 448).to(E4M3).float()
+        scales.append(torch.from_numpy(scale))
+    return q, torch.stack(scales, 1)
+
+
+@pytest.mark.parametrize("dim,off", [(4096, 0), (1024, 3), (128, 0)])
+def test_norm_scales_and_values_are_the_formulas(ctx, dim, off):
+    """A state of +-1 has the root mean square 1, so that y is the weight: max|y| / 448 and e4m3(y * (1 / scale)) bit for bit."""
+    sign = randn(64, dim, seed=1).sign()
+    for seed in range(8):
+        w = randn(dim, seed=10 + seed) * 10.0 ** (seed - 4)
+        x = torch.empty(64, dim + off)
+        x[:, off:] = sign
+        y8, scales, _ = ctx.head_norm(x.cuda()[:, off:], w.cuda(), eps=0.0)
+        q, want = blocks_exactly(sign * w)
+        assert torch.equal(scales.cpu(), want)
+        assert torch.equal(y8.cpu().float(), q)
+
+
+def test_quantize_scales_and_values_are_the_formulas(ctx):
+    for seed in range(4):
+        w = randn(128 * 40, 128, seed=20 + seed)
+        w8, ws = ctx.head_quantize(w.cuda())
+        part = w.view(40, -1).numpy()
+        scale = np.abs(part).max(1) / np.float32(448)
+        assert np.array_equal(ws.cpu().numpy()[:, 0], scale)
+        back = (np.float32(1) / scale)[:, None]
+        assert torch.equal(w8.cpu().float().view(40, -1), torch.from_numpy(part * back).to(E4M3).float())
