@@ -31,6 +31,7 @@ struct LogitsParams {
     uint32_t n_rows, n_tok, blocks;
     bool tma_out;                // the output's rows start on 16 bytes
     uint32_t *status;
+    long long stall;             // BPE_OPT_TEST_STALL_HEAD
 };
 
 // ------------------------------------------------------------- few rows ----
@@ -96,7 +97,7 @@ k_logits_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
         tma_prefetch_map(&map_x);
         int s = 0;
         uint32_t phase = 1, issued = 0;
-        for (uint32_t tok = begin; tok < end && !__any_sync(kFull, *gave_up); tok += 128) {
+        for (uint32_t tok = P.stall == blockIdx.x ? end : begin; tok < end && !__any_sync(kFull, *gave_up); tok += 128) {
             const uint32_t steps = (min(128u, end - tok) + kStep - 1) / kStep;
             for (uint32_t b = 0; b < P.blocks; b++) {
                 if (!__all_sync(kFull, mbar_wait(taken(s), phase))) { *gave_up = 1; break; }
@@ -267,6 +268,15 @@ __device__ __forceinline__ void store_part(O *to, const uint8_t *row, uint32_t s
     }
 }
 
+// A barrier of a group's four warps: whether all of them have their sums.  They leave a tile, and the loop, together:
+// a warp whose wait gave up by itself would be missed at the barriers that follow, which have no limit.
+__device__ __forceinline__ bool group_all(uint32_t bar, bool ok) {
+    uint32_t all;
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %2, 0;\nbar.red.and.pred q, %1, 128, p;\nselp.u32 %0, 1, 0, q;\n}"
+                 : "=r"(all) : "r"(bar), "r"((uint32_t)ok) : "memory");
+    return all != 0;
+}
+
 template <typename O, int kCtas>
 __global__ void __launch_bounds__(kManyThreads, 1)
 k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
@@ -315,7 +325,7 @@ k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         tma_prefetch_map(&map_x);
         int s = 0;
         uint32_t phase = 1, issued = 0;
-        for (uint32_t i = team; i < n_tiles && !__any_sync(kFull, *gave_up); i += teams) {
+        for (uint32_t i = P.stall == blockIdx.x ? n_tiles : team; i < n_tiles && !__any_sync(kFull, *gave_up); i += teams) {
             const int row0 = (int)(i % row_tiles * M::kRows + rank * 128);
             const int tok0 = (int)(i / row_tiles * kManyToks + rank * M::kToks);
             for (uint32_t b = 0; b < P.blocks; b++) {
@@ -425,18 +435,21 @@ k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             };
             add(0, std::true_type());
             for (uint32_t b = 1; b < P.blocks && ok; b++) add(b, std::false_type());
-            if (!ok) { *gave_up = 1; break; }
             const uint32_t row0 = row_tile * M::kRows + rank * 128, tok0 = tok_tile * kManyToks + group * 64;
             row_tile += row_step, tok_tile += tok_step;
             if (row_tile >= row_tiles) row_tile -= row_tiles, tok_tile++;
             if (i + teams < n_tiles) begin();   // the next tile's first scales arrive while this one leaves
+            if (P.tma_out && quarter == 0 && lane == 0) tma_store_wait();
+            if (!group_all(1 + group, ok)) { *gave_up = 1; break; }
 #pragma unroll
             for (int c0 = 0; c0 < 64; c0 += kPer) {
                 // TMA ends a row at a whole 16 bytes: a last part that does not is stored by threads
                 const uint32_t t = tok0 + c0;
                 const bool by_tma = P.tma_out && (t + kPer <= P.n_tok || P.n_tok % kVec == 0);
-                if (P.tma_out && quarter == 0 && lane == 0) tma_store_wait();
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+                if (c0 > 0) {
+                    if (P.tma_out && quarter == 0 && lane == 0) tma_store_wait();
+                    asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+                }
 #pragma unroll
                 for (int j = 0; j < 8; j++)
                     *reinterpret_cast<uint4 *>(mine + r * 128 + ((j ^ (r & 7)) << 4)) = pack16(acc + c0 + j * kVec, O());
@@ -654,7 +667,7 @@ extern "C" int head_logits(bpe_ctx *ctx, const uint8_t *d_x8, uint64_t x8_stride
     rc = aligned_rows(ctx, &copy_x, d_x8, x8_stride, n_rows, dim);
     if (!rc) rc = aligned_rows(ctx, &copy_w, d_w8, w8_stride, n_tok, dim);
     const LogitsParams P{d_xs, d_ws, d_out, xs_row_stride, xs_block_stride, ws_row_stride, ws_block_stride, out_stride,
-                         n_rows, n_tok, (dim + kBlock - 1) / kBlock, false, status};
+                         n_rows, n_tok, (dim + kBlock - 1) / kBlock, false, status, ctx->test_stall_head};
     if (!rc)
         rc = out_type == BPE_F32    ? launch<float>(ctx, d_x8, x8_stride, d_w8, w8_stride, dim, P)
              : out_type == BPE_BF16 ? launch<__nv_bfloat16>(ctx, d_x8, x8_stride, d_w8, w8_stride, dim, P)

@@ -68,6 +68,7 @@ struct bpe_ctx {
     int trie_layout = 0;   // BPE_TRIE_*
     int uni_chunk = 0;     // unigram_encode chunk bytes (0: default)
     long long test_stall_tile = -1;   // BPE_OPT_TEST_STALL_TILE
+    long long test_stall_head = -1;   // BPE_OPT_TEST_STALL_HEAD
     // cached graph of merge iterations
     bpe::TrainGraph graph;
     bpe::TrainGraph graph_sparse;   // the same for occurrence-driven merge windows

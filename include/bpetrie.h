@@ -129,6 +129,9 @@ const char *bpe_last_error(const bpe_ctx *ctx);
  *                        tiles after it wait until their bounded wait gives up
  *                        and the call returns BPE_ERR_TIMEOUT (the context
  *                        stays usable); -1 = off (default)
+ *   BPE_OPT_TEST_STALL_HEAD  testing only: in head_logits the CTA of this
+ *                        number loads nothing, so that its waits run out
+ *                        (about two seconds); -1 = off (default)
  *   BPE_OPT_PERSISTENT   1 = with BPE_MERGE_TWO_PASS, the merge loop runs as one cooperative
  *                        launch per window of merges (all CTAs resident,
  *                        phases separated by grid barriers) instead of a CUDA
@@ -162,7 +165,8 @@ enum {
     BPE_OPT_TEST_STALL_TILE = 10,
     BPE_OPT_SPARSE_MERGE = 11,
     BPE_OPT_LIST_FRONTIER = 12,
-    BPE_OPT_LIST_TAIL = 13
+    BPE_OPT_LIST_TAIL = 13,
+    BPE_OPT_TEST_STALL_HEAD = 14
 };
 enum { BPE_TRIE_DOUBLE_ARRAY = 0, BPE_TRIE_BITMAP = 1 };
 enum { BPE_MERGE_TWO_PASS = 0, BPE_MERGE_LOOKBACK = 1, BPE_MERGE_TILES = 2, BPE_MERGE_LISTS = 3 };

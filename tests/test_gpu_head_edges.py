@@ -67,3 +67,42 @@ def test_quantize_scales_and_values_are_the_formulas(ctx):
         assert np.array_equal(ws.cpu().numpy()[:, 0], scale)
         back = (np.float32(1) / scale)[:, None]
         assert torch.equal(w8.cpu().float().view(40, -1), torch.from_numpy(part * back).to(E4M3).float())
+
+
+# --------------------------------------------------- waits that give up ---
+
+def logits_inputs(rows, n, dim, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, dim, generator=g).mul_(60).clamp_(-448, 448).to(E4M3).cuda()
+    w = torch.randn(n, dim, generator=g).mul_(90).clamp_(-448, 448).to(E4M3).cuda()
+    kb = -(-dim // 128)
+    xs = (torch.rand(rows, kb, generator=g) + 0.01).cuda()
+    ws = (torch.rand(-(-n // 128), kb, generator=g) * 0.001 + 1e-5).cuda()
+    return x, xs, w, ws
+
+
+# few rows; single CTAs with an output that TMA and that threads write; pairs of CTAs with both
+STALLS = [(5, 4096, 256), (50, 4096, 256), (140, 1024, 384), (140, 1023, 384), (512, 60000, 256), (512, 60001, 256)]
+
+
+@pytest.mark.parametrize("rows,n,dim", STALLS)
+def test_logits_wait_that_runs_out(ctx, rows, n, dim):
+    """A CTA whose tiles never arrive gives up its waits, all its warps together; the others finish, the failure is
+    reported once, and the context stays usable."""
+    import bpe_trie_encode_gb300 as bt
+    from bpe_trie_encode_gb300 import _capi
+    args = logits_inputs(rows, n, dim, seed=rows)
+    want = ctx.head_logits(*args)
+    out = torch.full_like(want, 5.0)
+    ctx.set_option(_capi.BPE_OPT_TEST_STALL_HEAD, 2)
+    try:
+        ctx.head_logits(*args, out=out)
+        torch.cuda.synchronize()
+    finally:
+        ctx.set_option(_capi.BPE_OPT_TEST_STALL_HEAD, -1)
+    done = out == want
+    assert not done.all() and done.float().mean() > 0.7
+    with pytest.raises(bt.BpeError) as e:
+        ctx.head_logits(*args)
+    assert e.value.name == "TIMEOUT"
+    assert torch.equal(ctx.head_logits(*args), want)
