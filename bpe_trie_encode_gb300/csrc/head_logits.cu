@@ -148,8 +148,8 @@ k_logits_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
         for (int i = 0; i < kPer; i++)   // lanes past the rows read a scale that nothing uses
             xs[i] = P.xs + min((uint32_t)(col0 + i * 32 + lane), P.n_rows - 1) * P.xs_row;
         const uint32_t mine = tmem + ((uint32_t)quarter << 21) + col0;
-        bool ok = true;
-        for (uint32_t tok = begin; tok < end && ok; tok += 128) {
+        bool ok = true;   // once a wait has given up: NaN for what is left
+        for (uint32_t tok = begin; tok < end; tok += 128) {
             const uint32_t t = tok + quarter * 32 + lane;
             const float *ws = P.ws + (uint64_t)(min(t, P.n_tok - 1) / kBlock) * P.ws_row;
             auto load = [&](uint32_t b) {
@@ -170,12 +170,12 @@ k_logits_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
             };
             // two blocks at a time: half the waits, and a block's scales have two blocks' time to arrive
             Scales a = load(0), b2 = load(1);
-            for (uint32_t b = 0; b < P.blocks; b += 2) {
+            for (uint32_t b = 0; b < P.blocks && ok; b += 2) {
                 const bool two = b + 1 < P.blocks;
                 const int s1 = s + 1 == kStages ? 0 : s + 1;
                 const uint32_t phase1 = s1 ? phase : phase ^ 1;
                 const bool second = two && lane >= 16;   // half of the lanes watch each barrier
-                if (!__all_sync(kFull, mbar_wait(second ? done(s1) : done(s), second ? phase1 : phase))) { ok = false; break; }
+                if (!__all_sync(kFull, mbar_wait(second ? done(s1) : done(s), second ? phase1 : phase))) { ok = false, *gave_up = 1; break; }
                 tc_fence_after();
                 float d[kPart], d1[kPart];
                 tmem_load(d, mine + s * kN);
@@ -194,14 +194,17 @@ k_logits_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
                 s = s1, phase = phase1;
                 if (two && ++s == kStages) s = 0, phase ^= 1;
             }
-            if (ok && t < end) {
+            if (!ok) {
+#pragma unroll
+                for (int c = 0; c < kPart; c++) acc[c] = NAN;
+            }
+            if (t < end) {
                 O *out = (O *)P.out + t;
 #pragma unroll
                 for (int c = 0; c < kPart; c++)
                     if (col0 + c < P.n_rows) out[(uint64_t)(col0 + c) * P.out_stride] = from_f32<O>(acc[c]);
             }
         }
-        if (!ok) *gave_up = 1;
     }
     __syncwarp();
     tc_fence_before();
@@ -390,7 +393,7 @@ k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         int buf = 0;
         uint32_t bphase = 0;
         const uint32_t last = P.blocks - 1;
-        // tile i + teams is row_step tiles of rows and tok_step of tokens further
+        // the team's next tile is row_step tiles of rows and tok_step of tokens further
         const uint32_t row_step = teams % row_tiles, tok_step = teams / row_tiles;
         uint32_t row_tile = team % row_tiles, tok_tile = team / row_tiles;
         const float *xs, *ws;
@@ -400,8 +403,12 @@ k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             ws = P.ws + (uint64_t)min((tok_tile * kManyToks + group * 64) / kBlock, (P.n_tok - 1) / kBlock) * P.ws_row;
             sx0 = xs[0], sw0 = ws[0], sx1 = xs[min(1u, last) * P.xs_blk], sw1 = ws[min(1u, last) * P.ws_blk];
         };
-        if (team < n_tiles) begin();
-        for (uint32_t i = team; i < n_tiles; i += teams) {
+        auto advance = [&] {
+            row_tile += row_step, tok_tile += tok_step;
+            if (row_tile >= row_tiles) row_tile -= row_tiles, tok_tile++;
+        };
+        if (tok_tile < tok_tiles) begin();
+        while (tok_tile < tok_tiles) {
             float acc[64];
             bool ok = true;
             const float *const tx = xs, *const tw = ws;
@@ -436,11 +443,10 @@ k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             add(0, std::true_type());
             for (uint32_t b = 1; b < P.blocks && ok; b++) add(b, std::false_type());
             const uint32_t row0 = row_tile * M::kRows + rank * 128, tok0 = tok_tile * kManyToks + group * 64;
-            row_tile += row_step, tok_tile += tok_step;
-            if (row_tile >= row_tiles) row_tile -= row_tiles, tok_tile++;
-            if (i + teams < n_tiles) begin();   // the next tile's first scales arrive while this one leaves
             if (P.tma_out && quarter == 0 && lane == 0) tma_store_wait();
             if (!group_all(1 + group, ok)) { *gave_up = 1; break; }
+            advance();
+            if (tok_tile < tok_tiles) begin();   // the next tile's first scales arrive while this one leaves
 #pragma unroll
             for (int c0 = 0; c0 < 64; c0 += kPer) {
                 // TMA ends a row at a whole 16 bytes: a last part that does not is stored by threads
@@ -467,6 +473,12 @@ k_logits_many(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             }
         }
         if (P.tma_out && quarter == 0 && lane == 0) tma_store_wait();
+        for (; tok_tile < tok_tiles; advance()) {   // a wait gave up: NaN for what is left
+            const uint32_t row = row_tile * M::kRows + rank * 128 + r, tok0 = tok_tile * kManyToks + group * 64;
+            if (row < P.n_rows)
+                for (uint32_t t = tok0; t < tok0 + 64 && t < P.n_tok; t++)
+                    ((O *)P.out)[row * P.out_stride + t] = from_f32<O>(NAN);
+        }
     }
     __syncwarp();
     tc_fence_before();

@@ -462,8 +462,8 @@ int head_quantize(bpe_ctx *ctx, const void *d_w, uint64_t w_stride, int type, ui
  * ws_block_stride.  d_out: n_rows x n_tok of out_type, rows out_stride apart.
  * Matrices whose rows do not all start on 16 bytes are first copied to
  * stream-ordered scratch.  The kernels' waits are bounded: if one gives up, the
- * logits are not valid and the next head_logits on the context returns TIMEOUT
- * (once).  1 <= dim <= BPE_HEAD_MAX_DIM, 1 <= n_tok <=
+ * logits that it was for are NaN and the next head_logits on the context returns
+ * TIMEOUT (once).  1 <= dim <= BPE_HEAD_MAX_DIM, 1 <= n_tok <=
  * BPE_HEAD_MAX_TOKENS.  Errors: INVALID_ARG, OOM, TIMEOUT, CUDA. */
 int head_logits(bpe_ctx *ctx, const uint8_t *d_x8, uint64_t x8_stride, const float *d_xs, uint64_t xs_row_stride,
                 uint64_t xs_block_stride, const uint8_t *d_w8, uint64_t w8_stride, const float *d_ws,

@@ -106,3 +106,43 @@ def test_logits_wait_that_runs_out(ctx, rows, n, dim):
         ctx.head_logits(*args)
     assert e.value.name == "TIMEOUT"
     assert torch.equal(ctx.head_logits(*args), want)
+
+
+@pytest.mark.parametrize("rows,n,dim,dtype", [s + (F32,) for s in STALLS] + [s + (t,) for s in STALLS[2:4] for t in (BF16, F16)])
+def test_logits_that_were_given_up_are_nan(ctx, rows, n, dim, dtype):
+    """Nothing of an earlier step is left where a wait gave up."""
+    import bpe_trie_encode_gb300 as bt
+    from bpe_trie_encode_gb300 import _capi
+    args = logits_inputs(rows, n, dim, seed=rows + 1)
+    want = ctx.head_logits(*args, dtype=dtype)
+    out = torch.full_like(want, 5.0)
+    ctx.set_option(_capi.BPE_OPT_TEST_STALL_HEAD, 2)
+    try:
+        ctx.head_logits(*args, out=out)
+        torch.cuda.synchronize()
+    finally:
+        ctx.set_option(_capi.BPE_OPT_TEST_STALL_HEAD, -1)
+    done = out == want
+    assert not done.all() and out[~done].isnan().all()
+    with pytest.raises(bt.BpeError):
+        ctx.head_logits(*args)
+
+
+def test_draw_from_logits_that_were_given_up(ctx):
+    """The draw that is already queued behind them has no token to draw."""
+    import bpe_trie_encode_gb300 as bt
+    from bpe_trie_encode_gb300 import _capi
+    args = logits_inputs(3, 16, 128, seed=1)
+    u, out = torch.full((3,), 0.5, device="cuda"), torch.ones(3, 16, device="cuda")
+    want = ctx.head_sample(ctx.head_logits(*args), u)   # what a first call sets up is set up
+    torch.cuda.synchronize()
+    ctx.set_option(_capi.BPE_OPT_TEST_STALL_HEAD, 0)
+    try:
+        ids, logprob = ctx.head_sample(ctx.head_logits(*args, out=out), u)
+        torch.cuda.synchronize()
+    finally:
+        ctx.set_option(_capi.BPE_OPT_TEST_STALL_HEAD, -1)
+    assert (ids == -1).all() and (logprob == -INF).all()
+    with pytest.raises(bt.BpeError):
+        ctx.head_logits(*args)
+    assert torch.equal(ctx.head_sample(ctx.head_logits(*args), u)[0], want[0])
