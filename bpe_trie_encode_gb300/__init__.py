@@ -447,6 +447,15 @@ class Context:
             _capi.check(self._h, rc)
         return ids, logprob
 
+    def head_check(self) -> None:
+        """Raises BpeError (TIMEOUT), once, when a head_logits of this context
+        has given up a wait: some of its logits are NaN.  head_logits and
+        head_sample ask the same before they start; a replayed CUDA graph does
+        not.  Does not wait: call it after a synchronization."""
+        rc = self.lib.head_check(self._h)
+        if rc:
+            _capi.check(self._h, rc)
+
 
 class Unigram:
     """A Unigram model on the GPU (see ``Context.unigram``); keeps its trie alive."""

@@ -37,7 +37,7 @@ EXPORTS = [
     "trie_encode_noalloc", "trie_stream_open", "trie_stream_push", "trie_stream_close",
     "trie_encode_host", "unigram_create", "unigram_encode", "unigram_free",
     "bpe_vocab_from_merges", "bpe_decode",
-    "head_norm", "head_quantize", "head_logits", "head_sample",
+    "head_norm", "head_quantize", "head_logits", "head_sample", "head_check",
 ]
 
 
@@ -112,6 +112,7 @@ def load() -> ctypes.CDLL:
                                 vp, u64, u64]),
             "head_quantize": (i32, [vp, vp, u64, i32, u32, u32, vp, u64, vp, u64]),
             "head_logits": (i32, [vp, vp, u64, vp, u64, u64, vp, u64, vp, u64, u64, u32, u32, u32, vp, u64, i32]),
+            "head_check": (i32, [vp]),
             "head_sample": (i32, [vp, vp, u64, i32, u32, u32, vp, P(head_filters), vp, vp]),
         }
         for name, (res, args) in sig.items():

@@ -82,6 +82,12 @@ int ensure_events(bpe_ctx *ctx, size_t n) {
     return BPE_OK;
 }
 
+int head_report(bpe_ctx *ctx) {
+    if (!ctx->head_flag || !*ctx->head_flag) return BPE_OK;
+    *ctx->head_flag = 0;
+    return fail(ctx, BPE_ERR_TIMEOUT, "an earlier head_logits gave up a wait: logits that it was for are NaN");
+}
+
 int head_status(bpe_ctx *ctx, uint32_t **out) {
     if (!ctx->head_flag) {
         void *p = nullptr;
@@ -93,10 +99,7 @@ int head_status(bpe_ctx *ctx, uint32_t **out) {
         *(uint32_t *)p = 0;
         ctx->head_flag = (uint32_t *)p;
     }
-    if (*ctx->head_flag) {
-        *ctx->head_flag = 0;
-        return fail(ctx, BPE_ERR_TIMEOUT, "an earlier head_logits gave up a wait: its logits are not valid");
-    }
+    if (const int rc = head_report(ctx)) return rc;
     void *d = nullptr;
     BPE_CUDA(ctx, cudaHostGetDevicePointer(&d, (void *)ctx->head_flag, 0), "cudaHostGetDevicePointer");
     *out = (uint32_t *)d;
@@ -265,6 +268,8 @@ extern "C" int bpe_ctx_set_option(bpe_ctx *ctx, int option, int64_t value) {
         return fail(ctx, BPE_ERR_INVALID_ARG, "unknown option %d", option);
     }
 }
+
+extern "C" int head_check(bpe_ctx *ctx) { return ctx ? head_report(ctx) : BPE_ERR_INVALID_ARG; }
 
 extern "C" int bpe_last_stats(const bpe_ctx *ctx, bpe_stats *out) {
     if (!ctx || !out) return BPE_ERR_INVALID_ARG;

@@ -1238,6 +1238,7 @@ extern "C" int head_sample(bpe_ctx *ctx, const void *d_logits, uint64_t stride, 
     if (n_rows > 0x7FFFFFFFu) return fail(ctx, BPE_ERR_INVALID_ARG, "head_sample: %u rows", n_rows);
     if (!d_logits || !d_u || !d_ids_out) return fail(ctx, BPE_ERR_INVALID_ARG, "head_sample: null pointer");
     if (n_rows > 1 && stride < n_tok) return fail(ctx, BPE_ERR_INVALID_ARG, "head_sample: the row stride is below n_tok");
+    if (const int rc = head_report(ctx)) return rc;
     BPE_CUDA(ctx, cudaSetDevice(ctx->device), "cudaSetDevice");
     const head_filters none{1.0f, 0, 1.0f, 0.0f, nullptr, nullptr, nullptr, nullptr};
     SampleParams P{d_logits, stride, n_tok, type, d_u, filters ? *filters : none, d_ids_out, d_logprob_out};

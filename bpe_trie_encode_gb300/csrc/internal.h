@@ -115,6 +115,9 @@ int ensure_events(bpe_ctx *ctx, size_t n);
 // call on this context has set it.
 int head_status(bpe_ctx *ctx, uint32_t **out);
 
+// BPE_ERR_TIMEOUT, once, when that word has been set.
+int head_report(bpe_ctx *ctx);
+
 // Stream-ordered scratch: made and given back in the order of the context's
 // stream, so that calls on other streams and captured graphs have their own.
 int head_scratch(bpe_ctx *ctx, size_t bytes, void **out);

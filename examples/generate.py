@@ -61,6 +61,8 @@ def generate(ctx: bt.Context, model: Bigrams, first: torch.Tensor, n_tokens: int
         graph.replay()
         out.append(ids.clone())
         logprobs.append(logprob.clone())
+    torch.cuda.synchronize()
+    ctx.head_check()   # a replayed product reports nothing by itself
     return torch.stack(out, 1), torch.stack(logprobs, 1)
 
 

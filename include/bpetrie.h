@@ -415,10 +415,10 @@ void unigram_free(bpe_unigram *model);
 /* The last step of a language model over a vocabulary of this library: from
  * the hidden state of each position (a row) to the id that follows it.
  * head_norm -> head_logits -> head_sample, then bpe_decode for the bytes.
- * The pages have no counterpart.  All four calls are asynchronous on the
- * context's stream, may be captured in a CUDA graph, and share nothing between
- * calls, so that streams may take turns freely; strides count elements; n_rows
- * == 0 is a no-op. */
+ * The pages have no counterpart.  The calls are asynchronous on the context's
+ * stream, may be captured in a CUDA graph, and share nothing between calls but
+ * the report of a wait that gave up (head_check), so that streams may take turns
+ * freely; strides count elements; n_rows == 0 is a no-op. */
 enum { BPE_F32 = 0, BPE_BF16 = 1, BPE_F16 = 2 };
 #define BPE_HEAD_BLOCK 128u            /* columns (and vocabulary rows) that share a scale */
 #define BPE_HEAD_MAX_DIM 32768u
@@ -462,8 +462,9 @@ int head_quantize(bpe_ctx *ctx, const void *d_w, uint64_t w_stride, int type, ui
  * ws_block_stride.  d_out: n_rows x n_tok of out_type, rows out_stride apart.
  * Matrices whose rows do not all start on 16 bytes are first copied to
  * stream-ordered scratch.  The kernels' waits are bounded: if one gives up, the
- * logits that it was for are NaN and the next head_logits on the context returns
- * TIMEOUT (once).  1 <= dim <= BPE_HEAD_MAX_DIM, 1 <= n_tok <=
+ * logits that it was for are NaN, and head_check or the next head_logits or
+ * head_sample on the context, on any stream, returns TIMEOUT (once) and does
+ * nothing else.  1 <= dim <= BPE_HEAD_MAX_DIM, 1 <= n_tok <=
  * BPE_HEAD_MAX_TOKENS.  Errors: INVALID_ARG, OOM, TIMEOUT, CUDA. */
 int head_logits(bpe_ctx *ctx, const uint8_t *d_x8, uint64_t x8_stride, const float *d_xs, uint64_t xs_row_stride,
                 uint64_t xs_block_stride, const uint8_t *d_w8, uint64_t w8_stride, const float *d_ws,
@@ -503,9 +504,15 @@ typedef struct {
  * d_logits: n_rows x n_tok of `type`, rows `stride` apart; d_u: n_rows f32 in
  * [0, 1) (taken as 0 when below or NaN); filters: host struct (NULL: temperature 1,
  * no filter); d_ids_out: n_rows int32; d_logprob_out (nullable): n_rows f32.
- * 1 <= n_tok <= BPE_HEAD_MAX_TOKENS.  Errors: INVALID_ARG, OOM, CUDA. */
+ * 1 <= n_tok <= BPE_HEAD_MAX_TOKENS.  Errors: INVALID_ARG, OOM, TIMEOUT (of an
+ * earlier head_logits), CUDA. */
 int head_sample(bpe_ctx *ctx, const void *d_logits, uint64_t stride, int type, uint32_t n_rows, uint32_t n_tok,
                 const float *d_u, const head_filters *filters, int32_t *d_ids_out, float *d_logprob_out);
+
+/* TIMEOUT, once, when a head_logits of this context, one in a replayed graph
+ * included, has given up a wait.  Reads a word of host memory and does not
+ * wait: call it once the work in question is complete. */
+int head_check(bpe_ctx *ctx);
 
 #ifdef __cplusplus
 }

@@ -146,3 +146,29 @@ def test_draw_from_logits_that_were_given_up(ctx):
     with pytest.raises(bt.BpeError):
         ctx.head_logits(*args)
     assert torch.equal(ctx.head_sample(ctx.head_logits(*args), u)[0], want[0])
+
+
+def test_given_up_waits_are_reported(ctx):
+    """By a check after a replayed graph, and by the next draw; once each."""
+    import bpe_trie_encode_gb300 as bt
+    from bpe_trie_encode_gb300 import _capi
+    args = logits_inputs(3, 16, 128, seed=2)
+    u, out = torch.full((3,), 0.5, device="cuda"), torch.empty(3, 16, device="cuda")
+    want = ctx.head_sample(ctx.head_logits(*args, out=out), u)
+    torch.cuda.synchronize()
+    ctx.head_check()
+    graph = torch.cuda.CUDAGraph()
+    ctx.set_option(_capi.BPE_OPT_TEST_STALL_HEAD, 0)
+    try:
+        with torch.cuda.graph(graph):
+            ctx.head_logits(*args, out=out)
+    finally:
+        ctx.set_option(_capi.BPE_OPT_TEST_STALL_HEAD, -1)
+    for report in (ctx.head_check, lambda: ctx.head_sample(out, u), lambda: ctx.head_logits(*args)):
+        graph.replay()
+        torch.cuda.synchronize()
+        with pytest.raises(bt.BpeError) as e:
+            report()
+        assert e.value.name == "TIMEOUT"
+        ctx.head_check()
+        assert torch.equal(ctx.head_sample(ctx.head_logits(*args), u)[0], want[0])
