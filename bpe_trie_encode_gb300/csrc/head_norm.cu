@@ -268,8 +268,11 @@ int launch_norm(bpe_ctx *ctx, const NormParams &P, uint32_t n_rows, int weight_t
     auto k = weight_type == BPE_F32 ? k_head_norm<T, float>
              : weight_type == BPE_BF16 ? k_head_norm<T, __nv_bfloat16> : k_head_norm<T, __half>;
     const size_t smem = (size_t)P.dim * sizeof(float);
-    if (smem > 48 * 1024)
-        BPE_CUDA(ctx, cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem), "head_norm");
+    // Beyond what any kernel has, 48 KB together with its static arrays.  The limit is the device's, for all contexts and
+    // threads: always raised to the largest row's, never lowered.
+    static std::atomic<uint64_t> devices[3];   // of each weight type's kernel
+    if (smem > 32 * 1024)
+        BPE_CUDA(ctx, allow_shared(k, ctx->device, BPE_HEAD_MAX_DIM * sizeof(float), devices[weight_type]), "head_norm");
     k<<<n_rows, kNormThreads, smem, ctx->stream>>>(P);
     BPE_CUDA(ctx, cudaGetLastError(), "head_norm launch");
     return BPE_OK;

@@ -172,3 +172,46 @@ def test_given_up_waits_are_reported(ctx):
         assert e.value.name == "TIMEOUT"
         ctx.head_check()
         assert torch.equal(ctx.head_sample(ctx.head_logits(*args), u)[0], want[0])
+
+
+# ------------------------------------------------- launches of odd widths ---
+
+# f32 rows of 12,281 to 12,288 take less than 48 KB by themselves, but not with the kernel's static arrays
+@pytest.mark.parametrize("dim,off", [(8191, 0), (12280, 1), (12281, 0), (12287, 0), (12288, 1), (12289, 0), (32767, 0), (32768, 1)])
+def test_norm_widths_in_a_fresh_process(dim, off):
+    """The first call of a process, so that no wider one has raised the kernel's limits."""
+    code = f"""
+import torch, bpe_trie_encode_gb300 as bt
+ctx = bt.Context(0)
+x = torch.randn(3, {dim} + {off}, device="cuda")[:, {off}:]
+w = torch.ones({dim}, device="cuda", dtype=torch.bfloat16)
+y8, scales, _ = ctx.head_norm(x, w)
+y = x.double() / (x.double().square().mean(1, keepdim=True) + 1e-6).sqrt()
+got = y8.double() * scales.double().repeat_interleave(128, 1)[:, :{dim}]
+assert ((got - y).abs() <= y.abs() / 15 + 1e-3).all()   # half a step of e4m3 is 2^-4 of the value, 2^-10 of a scale below
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_norm_widths_from_two_threads(ctx):
+    """Two contexts of one device: a narrower row's call never takes room from a wider one's."""
+    import threading
+
+    import bpe_trie_encode_gb300 as bt
+    failed = []
+
+    def run(dim):
+        try:
+            c = bt.Context(0)
+            x, w = torch.randn(2, dim, device="cuda"), torch.ones(dim, device="cuda")
+            first = c.head_norm(x, w)[0]
+            for _ in range(300):
+                assert torch.equal(c.head_norm(x, w)[0].float(), first.float())
+        except Exception as e:
+            failed.append(repr(e))
+
+    threads = [threading.Thread(target=run, args=(dim,)) for dim in (13001, 32767)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not failed
