@@ -61,6 +61,7 @@ def _need_cuda(t: torch.Tensor, dtype: torch.dtype, name: str, device: torch.dev
 
 _HEAD_TYPES = {torch.float32: _capi.BPE_F32, torch.bfloat16: _capi.BPE_BF16, torch.float16: _capi.BPE_F16}
 _E4M3 = torch.float8_e4m3fn
+_HEAD_MOST = 0x7FFFFFFF   # ctypes cuts what does not fit the library's 32 bits without a word
 
 
 def _head_place(t, name: str, device: torch.device, dtypes) -> None:
@@ -79,6 +80,8 @@ def _head_matrix(t: torch.Tensor, name: str, device: torch.device, dtypes, shape
     size, stride = t.shape, t.stride()
     if len(stride) != 2 or (shape is not None and size != shape):
         raise ValueError(f"{name} must be {'a matrix' if shape is None else tuple(shape)}, got {tuple(size)}")
+    if size[0] > _HEAD_MOST or size[1] > _HEAD_MOST:
+        raise ValueError(f"{name}: {tuple(size)} has a size above {_HEAD_MOST}")
     if (stride[1] != 1 and size[1] > 1) or (stride[0] < size[1] and size[0] > 1):
         if out:
             raise ValueError(f"{name}: the rows of an output must be contiguous and apart")
@@ -112,6 +115,11 @@ def _head_vector(t: torch.Tensor, name: str, device: torch.device, dtype: torch.
             raise ValueError(f"{name}: an output must be contiguous")
         t = t.contiguous()
     return t
+
+
+def _head_count(k):
+    """A number of tokens as the library's 32 bits hold it: none of its vocabularies has as many as the largest."""
+    return max(-1, min(k, _HEAD_MOST))
 
 
 class Trie:
@@ -430,7 +438,7 @@ class Context:
             if v is None:
                 return off, None
             if not isinstance(v, torch.Tensor):
-                return v, None
+                return (_head_count(v) if dtype is torch.int32 else v), None
             v = _head_vector(v, name, dev, dtype, rows)
             keep.append(v)
             return off, v.data_ptr()

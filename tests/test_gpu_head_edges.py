@@ -215,3 +215,25 @@ def test_norm_widths_from_two_threads(ctx):
     [t.start() for t in threads]
     [t.join() for t in threads]
     assert not failed
+
+
+# ------------------------------------------------------------------ sizes ---
+
+def test_sizes_and_top_k_beyond_32_bits(ctx):
+    one = torch.zeros(1, 1, device="cuda")
+    rows = 2 ** 32 + 5
+    u = torch.zeros(1, device="cuda").expand(rows)
+    with pytest.raises(ValueError, match="above"):
+        ctx.head_sample(one.expand(rows, 1), u)
+    with pytest.raises(ValueError, match="above"):
+        ctx.head_norm(one.expand(rows, 1), torch.ones(1, device="cuda"))
+    with pytest.raises(ValueError, match="above"):
+        ctx.head_logits(one.to(E4M3).expand(rows, 1), one.expand(rows, 1), one.to(E4M3), one)
+    with pytest.raises(ValueError, match="above"):
+        ctx.head_quantize(one.expand(rows, 1))
+    x = randn(64, 500, seed=3).cuda()
+    u = torch.rand(64, generator=torch.Generator().manual_seed(4)).cuda()
+    off = ctx.head_sample(x, u)[0]
+    assert torch.equal(ctx.head_sample(x, u, top_k=2 ** 32 + 1)[0], off)
+    assert torch.equal(ctx.head_sample(x, u, top_k=-2 ** 33 + 1)[0], off)
+    assert not torch.equal(ctx.head_sample(x, u, top_k=1)[0], off)
