@@ -82,6 +82,13 @@ int ensure_events(bpe_ctx *ctx, size_t n) {
     return BPE_OK;
 }
 
+// A context's first head call may be one that a stream captures: what is set up then is allowed in this thread.
+struct RelaxedCapture {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+    ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
 int head_report(bpe_ctx *ctx) {
     if (!ctx->head_flag || !*ctx->head_flag) return BPE_OK;
     *ctx->head_flag = 0;
@@ -91,11 +98,8 @@ int head_report(bpe_ctx *ctx) {
 int head_status(bpe_ctx *ctx, uint32_t **out) {
     if (!ctx->head_flag) {
         void *p = nullptr;
-        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;   // the first call may be a captured one
-        cudaThreadExchangeStreamCaptureMode(&mode);
-        const cudaError_t e = cudaHostAlloc(&p, sizeof(uint32_t), cudaHostAllocMapped);
-        cudaThreadExchangeStreamCaptureMode(&mode);
-        if (e != cudaSuccess) return cuda_fail(ctx, e, "cudaHostAlloc");
+        const RelaxedCapture relaxed;
+        BPE_CUDA(ctx, cudaHostAlloc(&p, sizeof(uint32_t), cudaHostAllocMapped), "cudaHostAlloc");
         *(uint32_t *)p = 0;
         ctx->head_flag = (uint32_t *)p;
     }
@@ -108,6 +112,7 @@ int head_status(bpe_ctx *ctx, uint32_t **out) {
 
 int head_scratch(bpe_ctx *ctx, size_t bytes, void **out) {
     if (!ctx->head_pool) {
+        const RelaxedCapture relaxed;
         cudaMemPoolProps props = {};
         props.allocType = cudaMemAllocationTypePinned;
         props.location.type = cudaMemLocationTypeDevice;

@@ -237,3 +237,35 @@ def test_sizes_and_top_k_beyond_32_bits(ctx):
     assert torch.equal(ctx.head_sample(x, u, top_k=2 ** 32 + 1)[0], off)
     assert torch.equal(ctx.head_sample(x, u, top_k=-2 ** 33 + 1)[0], off)
     assert not torch.equal(ctx.head_sample(x, u, top_k=1)[0], off)
+
+
+# --------------------------------------------------------------- captures ---
+
+@pytest.mark.parametrize("rows,off", [(3, 0), (3, 1), (200, 0), (200, 1)])
+def test_first_calls_of_a_process_are_captured(rows, off):
+    """Nothing has been called before the capture; with off the weights' rows have to be copied to scratch."""
+    code = f"""
+import torch, bpe_trie_encode_gb300 as bt
+rows, dim, n = {rows}, 640, 1000
+ctx = bt.Context(0)
+g = torch.Generator().manual_seed(1)
+h, w = torch.randn(rows, dim, generator=g).cuda(), torch.randn(n, dim, generator=g).cuda()
+gain, u = torch.ones(dim, device="cuda"), torch.rand(rows, generator=g).cuda()
+w8 = torch.randn(n, dim + {off}, generator=g).mul_(90).clamp_(-448, 448).to(torch.float8_e4m3fn).cuda()[:, {off}:]
+torch.cuda.synchronize()
+
+def step():
+    x8, xs, _ = ctx.head_norm(h, gain)
+    _, ws = ctx.head_quantize(w)
+    logits = ctx.head_logits(x8, xs, w8, ws)
+    return logits, *ctx.head_sample(logits, u, temperature=30.0, top_p=0.9)
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, step()))
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
