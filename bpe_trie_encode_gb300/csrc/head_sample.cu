@@ -992,8 +992,9 @@ k_sample_rows(SampleParams P, uint32_t n_rows, uint32_t slice, bool wide) {
     }
 }
 
+// 0 for -infinity and NaN, and where z is none: an infinite distance times the 0 of an infinite temperature.
 __device__ __forceinline__ u64 weight_of(float v, float top, float inv_t) {
-    return v > -INFINITY ? weight(expf(z_of(v, top, inv_t))) : 0;   // 0 for -infinity and NaN
+    return v > -INFINITY ? weight(expf(fmaxf(z_of(v, top, inv_t), -31.75f))) : 0;
 }
 
 __device__ __forceinline__ u64 sum_all(u64 v, u64 *red) {

@@ -269,3 +269,27 @@ assert all(torch.equal(a, b) for a, b in zip(got, step()))
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+# ----------------------------------------------------- infinite distances ---
+
+@pytest.mark.parametrize("dtype,n", [(F32, 1000), (BF16, 4352), (F32, 65536), (F32, 250000), (F32, 400001), (BF16, 800003)])
+@pytest.mark.parametrize("temperature", [INF, 3e38])
+def test_infinite_distances(ctx, dtype, n, temperature):
+    """A distance of infinity leaves nothing at any temperature: neither below an infinite logit nor across the type's range.
+    The last two vocabularies are beyond a cluster's shared memory."""
+    big = torch.finfo(dtype).max
+    x = torch.zeros(4, n, dtype=dtype, device="cuda")
+    x[0, 7] = x[0, n - 2] = INF
+    x[1] = -big
+    x[1, 5] = x[1, 900] = big
+    x[2, 100:] = -INF
+    x[2, :100] = NAN
+    x[2, 40] = -big
+    u = torch.tensor([0.25, 0.75, 0.5, 0.999], device="cuda")
+    for kw in ({}, {"top_k": 3}, {"top_p": 0.999}, {"top_k": 400, "top_p": 0.99, "min_p": 0.5}):
+        ids, logprob = ctx.head_sample(x, u, temperature=temperature, **kw)
+        assert ids[:3].tolist() == [7, 900, 40], kw
+        half = torch.tensor(0.5).log()
+        assert (logprob[:2].cpu() - half).abs().max() < 1e-6 and logprob[2] == 0
+        assert ids[3] >= 0 and torch.isfinite(logprob[3])
