@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(1024) k_head_norm_vec(NormParams P) {
             s[j][c] = s[j][c] * inv * w[c];
             amax = max_nan(amax, fabsf(s[j][c]));
         }
+        if (i >= n) amax = 0.0f;   // 0 times an infinite 1 / rms is no element of the row
 #pragma unroll
         for (int d = kLanes / 2; d > 0; d >>= 1) amax = max_nan(amax, __shfl_xor_sync(kFull, amax, d));
         const float scale = block_scale(amax), back = block_back(scale);

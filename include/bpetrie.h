@@ -487,8 +487,9 @@ typedef struct {
 /* One id per row, drawn from its logits by a given random number.  A NaN
  * counts as -infinity.  With m the row's largest logit, z = (logit - m) *
  * (1 / temperature) in 32 bits (0 where logit == m, -infinity where logit - m
- * is, whatever the temperature) and the whole numbers w = floor(exp(z) * 2^40), so that every sum is exact and no result depends on
- * an order of addition:
+ * is, whatever the temperature) and the whole numbers w = floor(exp(z) *
+ * 2^40), so that every sum is exact and no result depends on an order of
+ * addition:
  *   - tokens are ordered by logit, largest first, equal ones by lowest id;
  *   - top-k keeps the first top_k of them, W_k being their mass (sum of w);
  *   - top-p keeps those of the rest before which less mass than floor(top_p *

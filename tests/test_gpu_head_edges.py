@@ -293,3 +293,17 @@ def test_infinite_distances(ctx, dtype, n, temperature):
         half = torch.tensor(0.5).log()
         assert (logprob[:2].cpu() - half).abs().max() < 1e-6 and logprob[2] == 0
         assert ids[3] >= 0 and torch.isfinite(logprob[3])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dim", [8, 72, 128, 136, 1000, 4104])
+def test_norm_of_a_state_whose_squares_vanish(ctx, dtype, dim):
+    """Without eps 1 / rms is infinite: a block holds infinities, not NaN, also where the row ends inside it; the same by
+    either kernel (rows one element off take the general one)."""
+    x = torch.full((3, dim + 1), 1e-30, dtype=dtype, device="cuda")
+    w = torch.ones(dim, dtype=dtype, device="cuda")
+    for rows in (x[:, 1:], x[:, 1:].contiguous()):
+        y8, scales, _ = ctx.head_norm(rows, w, eps=0.0)
+        assert (scales == INF).all()
+        zero = ctx.head_norm(torch.zeros_like(rows), w, eps=0.0)   # 0 * infinity
+        assert zero[1].isnan().all()
