@@ -471,16 +471,15 @@ struct Sampler {
             }
             __syncthreads();
             u64 *sum = members() == 1 ? S.all : S.sum[level & 1];
-            for (int i = threadIdx.x; i < buckets * 4; i += kThreads) {   // four lanes a bucket
+            for (int i = threadIdx.x; i < buckets * 4; i += kThreads) {   // four lanes a bucket; whole warps: 16 buckets at least
                 const int b = i >> 2;
                 u64 v = 0;
                 for (int c = 0; c < copies; c += 4) {
                     const int a = b * copies + (((i & 3) + c + b * 4) & (copies - 1));
                     v += join(kMass ? upper[a] : 0, S.lo[a]);
                 }
-                const unsigned with = __activemask();
-                v += __shfl_xor_sync(with, v, 1);
-                v += __shfl_xor_sync(with, v, 2);
+                v += __shfl_xor_sync(kFull, v, 1);
+                v += __shfl_xor_sync(kFull, v, 2);
                 if ((i & 3) == 0) sum[b] = v;
             }
             sync();
