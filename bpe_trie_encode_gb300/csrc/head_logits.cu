@@ -538,7 +538,8 @@ EncodeFn encode_fn() {
     return fn;
 }
 
-// The tile map of an 8-bit matrix, box_rows x 128 columns; columns past dim read as 0.
+// The tile map of an 8-bit matrix, box_rows x 128 columns; columns past dim read as 0.  A load ends a row at the byte
+// (rows padded with NaN to 16 bytes give the same bits), where a store ends it at whole 16 bytes.
 int encode_map(bpe_ctx *ctx, CUtensorMap *map, const uint8_t *p, uint64_t stride, uint32_t rows, uint32_t dim, uint32_t box_rows) {
     EncodeFn fn = encode_fn();
     if (!fn) return fail(ctx, BPE_ERR_CUDA, "head_logits: the driver has no cuTensorMapEncodeTiled");

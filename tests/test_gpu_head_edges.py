@@ -307,3 +307,63 @@ def test_norm_of_a_state_whose_squares_vanish(ctx, dtype, dim):
         assert (scales == INF).all()
         zero = ctx.head_norm(torch.zeros_like(rows), w, eps=0.0)   # 0 * infinity
         assert zero[1].isnan().all()
+
+
+# ------------------------------------------- several tiles a CTA or a pair ---
+
+def logits_bounds(x, xs, w, ws):
+    """The product in 64 bits, and how far 32-bit sums may be from it (2^-23 of the magnitudes for each addition)."""
+    rows, dim = x.shape
+    n = w.shape[0]
+    want = torch.zeros(rows, n, dtype=torch.float64, device="cuda")
+    size = torch.zeros_like(want)
+    X, W = x.float().double(), w.float().double()
+    for i, c in enumerate(range(0, dim, 128)):
+        s = xs[:, i].double()[:, None] * ws[:, i].double().repeat_interleave(128)[:n][None]
+        want += s * (X[:, c:c + 128] @ W[:, c:c + 128].t())
+        size += s * (X[:, c:c + 128].abs() @ W[:, c:c + 128].abs().t())
+    return want, (min(dim, 128) + -(-dim // 128) + 4) * 2.0 ** -23 * size
+
+
+def check_bounds(out, want, tol):
+    lo, hi = want - tol, want + tol
+    if out.dtype != F32:   # rounding to the output's type keeps order
+        lo, hi = lo.float().to(out.dtype).double(), hi.float().to(out.dtype).double()
+    bad = ~((out.double() >= lo) & (out.double() <= hi))
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:4].tolist())
+
+
+# on 152 SMs: pairs of CTAs with 6 to 7 tiles each of 5, 4, 1 and 9 blocks, then single CTAs with 4 to 5 of 9, 4 and 3
+@pytest.mark.parametrize("rows,n,dim", [(512, 60000, 640), (512, 60001, 512), (500, 60004, 100), (400, 60004, 1040),
+                                        (300, 60000, 1040), (300, 60001, 512), (290, 60004, 384)])
+def test_logits_of_many_tiles(ctx, rows, n, dim):
+    """Stages, sums and scales carried from tile to tile, with outputs that TMA writes whole, up to the last 16 bytes of a
+    row, or not at all."""
+    x, xs, w, ws = logits_inputs(rows, n, dim, seed=dim)
+    want, tol = logits_bounds(x, xs, w, ws)
+    for dtype in (F32, BF16, F16):
+        check_bounds(ctx.head_logits(x, xs, w, ws, dtype=dtype), want, tol)
+        for before, wide in ((0, -(-n // 8) * 8), (1, n + 3)):
+            out = torch.full((rows, wide), 7.0, dtype=dtype, device="cuda")
+            ctx.head_logits(x, xs, w, ws, out=out[:, before:before + n])
+            check_bounds(out[:, before:before + n], want, tol)
+            assert (out[:, :before] == 7).all() and (out[:, before + n:] == 7).all()
+
+
+# ------------------------------------------------------ what pads the rows ---
+
+@pytest.mark.parametrize("dim", [127, 1000, 1039])
+@pytest.mark.parametrize("rows", [1, 2, 40, 150, 600])
+def test_logits_do_not_read_past_a_row(ctx, dim, rows):
+    """Rows that start on 16 bytes and end inside them go to TMA as they are: whatever pads them, NaN included."""
+    n = 300
+    x, xs, w, ws = logits_inputs(rows, n, dim, seed=dim + rows)
+    got = []
+    for pad in (0x00, 0x70, 0x7F):   # 0, 256, NaN
+        def padded(t):
+            full = torch.full((t.shape[0], -(-dim // 16) * 16), pad, dtype=torch.uint8, device="cuda")
+            full[:, :dim] = t.view(torch.uint8)
+            return full.view(E4M3)[:, :dim]
+        got.append(ctx.head_logits(padded(x), xs, padded(w), ws))
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+    check_bounds(got[0], *logits_bounds(x, xs, w, ws))
