@@ -4,6 +4,8 @@
 // architecture", 2.: buffers are made once and reused by later calls; a call
 // that needs more grows the buffer to 1.5x the request.
 #include <cstring>
+#include <mutex>
+#include <vector>
 
 #include "internal.h"
 
@@ -89,6 +91,11 @@ struct RelaxedCapture {
     ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
 };
 
+// The words of contexts that have ended, for later ones.  None is freed: a captured graph that outlives its context
+// still holds the address.
+static std::mutex spare_mutex;
+static std::vector<void *> &spare_words = *new std::vector<void *>;   // contexts may end after the library's destructors
+
 int head_report(bpe_ctx *ctx) {
     if (!ctx->head_flag || !*ctx->head_flag) return BPE_OK;
     *ctx->head_flag = 0;
@@ -98,8 +105,14 @@ int head_report(bpe_ctx *ctx) {
 int head_status(bpe_ctx *ctx, uint32_t **out) {
     if (!ctx->head_flag) {
         void *p = nullptr;
-        const RelaxedCapture relaxed;
-        BPE_CUDA(ctx, cudaHostAlloc(&p, sizeof(uint32_t), cudaHostAllocMapped), "cudaHostAlloc");
+        {
+            const std::lock_guard<std::mutex> hold(spare_mutex);
+            if (!spare_words.empty()) p = spare_words.back(), spare_words.pop_back();
+        }
+        if (!p) {
+            const RelaxedCapture relaxed;
+            BPE_CUDA(ctx, cudaHostAlloc(&p, sizeof(uint32_t), cudaHostAllocMapped | cudaHostAllocPortable), "cudaHostAlloc");
+        }
         *(uint32_t *)p = 0;
         ctx->head_flag = (uint32_t *)p;
     }
@@ -197,7 +210,10 @@ extern "C" void bpe_ctx_destroy(bpe_ctx *ctx) {
         if (s.p) cudaFree(s.p);
     for (auto ev : ctx->events) cudaEventDestroy(ev);
     if (ctx->pinned) cudaFreeHost(ctx->pinned);
-    if (ctx->head_flag) cudaFreeHost((void *)ctx->head_flag);
+    if (ctx->head_flag) {
+        const std::lock_guard<std::mutex> hold(spare_mutex);
+        spare_words.push_back((void *)ctx->head_flag);
+    }
     if (ctx->head_pool) cudaMemPoolDestroy(ctx->head_pool);   // once its last memory is given back
     if (ctx->capture_stream) cudaStreamDestroy(ctx->capture_stream);
     delete ctx;

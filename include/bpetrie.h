@@ -418,7 +418,7 @@ void unigram_free(bpe_unigram *model);
  * The pages have no counterpart.  The calls are asynchronous on the context's
  * stream, may be captured in a CUDA graph, and share nothing between calls but
  * the report of a wait that gave up (head_check), so that streams may take turns
- * freely; strides count elements; n_rows == 0 is a no-op. */
+ * freely, and a captured graph may outlive its context; strides count elements; n_rows == 0 is a no-op. */
 enum { BPE_F32 = 0, BPE_BF16 = 1, BPE_F16 = 2 };
 #define BPE_HEAD_BLOCK 128u            /* columns (and vocabulary rows) that share a scale */
 #define BPE_HEAD_MAX_DIM 32768u

@@ -367,3 +367,36 @@ def test_logits_do_not_read_past_a_row(ctx, dim, rows):
         got.append(ctx.head_logits(padded(x), xs, padded(w), ws))
     assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
     check_bounds(got[0], *logits_bounds(x, xs, w, ws))
+
+
+@pytest.mark.parametrize("off", [0, 1])
+def test_graph_that_outlives_its_context(off):
+    """Nothing that a captured product uses ends with the context, the word that a given-up wait sets included."""
+    import bpe_trie_encode_gb300 as bt
+    from bpe_trie_encode_gb300 import _capi
+    x, xs, w, ws = logits_inputs(4, 4096, 256, seed=5)
+    w = torch.cat([w[:, :off].view(torch.uint8), w.view(torch.uint8)], 1).view(E4M3)[:, off:]
+    graphs, outs = [], []
+    c = bt.Context(0)
+    want = c.head_logits(x, xs, w, ws)
+    torch.cuda.synchronize()
+    for stall in (-1, 2):
+        outs.append(torch.zeros_like(want))
+        graphs.append(torch.cuda.CUDAGraph())
+        c.set_option(_capi.BPE_OPT_TEST_STALL_HEAD, stall)
+        with torch.cuda.graph(graphs[-1]):
+            c.head_logits(x, xs, w, ws, out=outs[-1])
+    c.close()
+    for _ in range(2):
+        outs[0].zero_()
+        graphs[0].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want)
+    graphs[1].replay()
+    torch.cuda.synchronize()
+    assert outs[1].isnan().any()
+    other = bt.Context(0)   # has the word now, and begins without a report
+    assert torch.equal(other.head_logits(x, xs, w, ws), want)
+    torch.cuda.synchronize()
+    other.head_check()
+    other.close()
