@@ -400,3 +400,17 @@ def test_graph_that_outlives_its_context(off):
     torch.cuda.synchronize()
     other.head_check()
     other.close()
+
+
+def test_quantize_scales_over_the_whole_range(ctx):
+    """A column of weights has a scale per 128: magnitudes from the smallest scale's to near the type's largest."""
+    blocks = 16384
+    g = torch.Generator().manual_seed(30)
+    size = 2.0 ** torch.randint(-117, 127, (blocks, 1), generator=g).float()
+    w = (torch.rand(blocks, 128, generator=g) * 2 - 1) * size
+    w8, ws = ctx.head_quantize(w.view(-1, 1).cuda())
+    part = w.numpy()
+    scale = np.maximum(np.abs(part).max(1) / np.float32(448), np.float32(2.0 ** -126))
+    assert np.array_equal(ws.cpu().numpy()[:, 0], scale)
+    back = (np.float32(1) / scale)[:, None]
+    assert torch.equal(w8.cpu().float().view(blocks, 128), torch.from_numpy(part * back).to(E4M3).float())
