@@ -333,7 +333,9 @@ class Context:
         of any of the three.  Returns (x8 float8_e4m3fn [rows, dim], scales f32
         [rows, ceil(dim / 128)], the sum in x's type [rows, dim] or None).  The
         sum is written when a residual is given or residual_out is; it may be x
-        or the residual itself.  Asynchronous on the current stream."""
+        or the residual itself.  Asynchronous on the current stream.  Not
+        differentiable, like all head_ calls: what they return has no gradient,
+        whether the inputs want one or not."""
         dev = self.device
         x, x_stride = _head_matrix(x, "x", dev, _HEAD_TYPES)
         size, dtype = x.shape, x.dtype
@@ -368,7 +370,8 @@ class Context:
     def head_quantize(self, weight: torch.Tensor):
         """A weight matrix [n_tok, dim] (f32, bf16 or f16) in 8 bits with one
         scale per 128 x 128 block: (w8 float8_e4m3fn [n_tok, dim], its rows
-        starting on 16 bytes, ws f32 [ceil(n_tok / 128), ceil(dim / 128)])."""
+        starting on 16 bytes, ws f32 [ceil(n_tok / 128), ceil(dim / 128)]).
+        Not differentiable."""
         weight, stride = _head_matrix(weight, "weight", self.device, _HEAD_TYPES)
         n_tok, dim = weight.shape
         w8 = torch.empty(n_tok, -(-dim // 16) * 16, dtype=_E4M3, device=self.device)[:, :dim]
@@ -386,8 +389,9 @@ class Context:
         xs [rows, ceil(dim / 128)]) and weights w8 [n_tok, dim] (scales ws
         [ceil(n_tok / 128), ceil(dim / 128)]), accumulated in 32 bits and
         rounded once to ``dtype`` (f32, bf16 or f16; ``out``'s when it is
-        given).  Scales may have any strides.  Asynchronous on the current
-        stream."""
+        given).  Scales may have any strides.  Matrices whose rows do not start
+        on 16 bytes are copied at each call, to memory that stays with the
+        context.  Asynchronous on the current stream.  Not differentiable."""
         dev = self.device
         x8, x_stride = _head_matrix(x8, "x8", dev, (_E4M3,))
         w8, w_stride = _head_matrix(w8, "w8", dev, (_E4M3,))

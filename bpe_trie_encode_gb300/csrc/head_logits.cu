@@ -45,10 +45,13 @@ struct LogitsParams {
 // tensor memory, and is loaded again when its sums have been read: the warp
 // that multiplies, whose loop of about 300 cycles a block must stay below the
 // 700 that 16 KB take to arrive, waits on one barrier and signals one (with two
-// of each, 520 cycles, it was the bound).  Measured: 1 x 65,536 x 8,192 in 86 us,
-// 6.2 TB/s; 1 x 32,256 x 4,096 in 24.8 us, 5.3 TB/s with the launch; 64 x 65,536
-// x 4,096 in 56 us, 5.1 TB/s: its stages hold 24 KB for 16 KB of weights, so
-// less is on the way.
+// of each, 520 cycles, it was the bound).  Measured: 1 x 65,536 x 8,192 in 87 us,
+// 6.1 TB/s; 1 x 32,256 x 4,096 in 25 to 26 us, 5.1 TB/s with the launch; 64 x
+// 65,536 x 4,096 in 57 us, 5.0 TB/s.  That last one is not short of loads on the
+// way (128-row tiles, below, have 96 KB of weights under way on an SM, not 128,
+// and took 53): its adding warps take 8 instructions a sum, a shuffle and a
+// product of scales among them, and 60% of the issue slots; a stage takes nine
+// loads where a 128-row tile's takes two.
 constexpr int kStep = 16;          // tokens per load
 
 template <int kN> struct Few {
@@ -224,10 +227,11 @@ k_logits_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
 // its factor is one number per block.  16 such warps, 4 per scheduler, cover
 // the latency of reading tensor memory.  The tile leaves through shared memory
 // by TMA while the next one is under way.  Measured: 4,096 x 32,256 x 4,096 in
-// 364 us (2.97 PFLOP/s) in a burst, 410 us when run on end; a block takes 800
+// 374 us (2.9 PFLOP/s) after a pause, 417 us when run on end; a block takes 800
 // cycles of a CTA's tensor core where products alone, without scales, took
 // 750; the rest is 2,000 cycles at each tile's end.  333 x 250,000 x 1,040, 9
-// blocks a tile, 134 us: those ends are a fifth of it.
+// blocks a tile, 135 us: those ends are a fifth of it, waits for weights have
+// not been measured apart.
 constexpr int kManyThreads = 576;   // 16 warps scale and add, 1 loads, 1 multiplies
 constexpr int kManyToks = 256;
 constexpr int kOutBytes = 128 * 128;   // of one group of 4 warps: 128 rows of 128 bytes
@@ -635,7 +639,9 @@ int launch(bpe_ctx *ctx, const uint8_t *x8, uint64_t x_stride, const uint8_t *w8
     const uint64_t singles = (row_tiles * tok_tiles + sms - 1) / sms, pairs = ((row_tiles + 1) / 2 * tok_tiles + sms / 2 - 1) / (sms / 2);
     // Pairs or single CTAs, by the rounds that each needs and what a round of pairs takes of one of single CTAs: 0.91 to
     // 0.94 measured over several rounds, more than all of it where there are few (2,000 x 4,352 x 1,024 f32: 19.1 us
-    // against 17.3), 0.75 to 0.83 where rows start between lines of 128 bytes: loads cost more, and pairs load less.
+    // against 17.3), 0.73 to 0.83 where rows start between lines of 128 bytes: loads cost more, and pairs load less.
+    // 0.8 is the middle of eleven sizes of 300 to 1,100 rows, 60,000 to 250,000 tokens and 528 to 4,176 columns; at 272
+    // columns it was 0.93 (640 x 100,000: 50 / 44 us).
     // In us, pairs / single CTAs: 512 x 250,000 x 1,024 120 / 129, x 1,040 147 / 175; 779 x 142,608 x 2,896 318 / 368;
     // 640 x 65,536 x 4,096 156 / 138; 384 x 65,536 x 4,096 103 / 98; 128 x 65,536 x 4,096 74 / 58.  An output that TMA
     // cannot write makes a tile's end longer than its loads (1,547 x 53,514 x 433: 120 / 108).  Up to 64 rows the few-row

@@ -19,9 +19,11 @@
 // for an exponential and an exact weight, 26 more with two shared-memory
 // atomics for the first histogram; a small top-k needs neither (2 instructions)
 // and is bound by the latency of its steps.  Measured: 4,096 rows of 4,352 bf16
-// without filters 25 us (1.4 TB/s); 256 x 65,536 bf16 with
-// all filters 25 us (1.4 TB/s); 61 x 250,000 f32, top-p over flat rows, 110 us;
-// 1 x 32,256 f32, top-p, 14 us.
+// without filters 25 us (1.4 TB/s; 34 instructions a logit, 70% of the issue
+// slots); 256 x 65,536 bf16 with all filters 26 us (1.3 TB/s); 61 x 250,000 f32,
+// top-p over flat rows, 111 to 119 us by where its clusters land (100
+// instructions a logit, 41% of the issue slots, barriers the first of its
+// stalls); 1 x 32,256 f32, top-p, 14 to 16 us.
 #include "head.cuh"
 
 #include "device.cuh"
@@ -675,7 +677,8 @@ struct Sampler {
             if (x < (float)kNear) atomicAdd(&S.near_n[(int)x], 1u);
         };
         if (kThreads >= 512) {
-            for (uint32_t g = g0; g < g1; g++) file(most(data[g]));   // over 600 groups
+            // a k above the number of groups (512 tokens of 16 bits have 64) finds no bound here and goes on to select
+            for (uint32_t g = g0; g < g1; g++) file(most(data[g]));
         } else {
             each([&](uint32_t, float v) { file(v); });
         }

@@ -460,8 +460,9 @@ int head_quantize(bpe_ctx *ctx, const void *d_w, uint64_t w_stride, int type, ui
  * b at r * xs_row_stride + b * xs_block_stride.  d_w8: n_tok x dim e4m3, rows
  * w8_stride apart; d_ws: block (t, b) at t * ws_row_stride + b *
  * ws_block_stride.  d_out: n_rows x n_tok of out_type, rows out_stride apart.
- * Matrices whose rows do not all start on 16 bytes are first copied to
- * stream-ordered scratch.  The kernels' waits are bounded: if one gives up, the
+ * Matrices whose rows do not all start on 16 bytes are first copied, at each
+ * call, to stream-ordered scratch, which stays with the context like its other
+ * scratch (a captured graph has its own).  The kernels' waits are bounded: if one gives up, the
  * logits that it was for are NaN, and head_check or the next head_logits or
  * head_sample on the context, on any stream, returns TIMEOUT (once) and does
  * nothing else.  1 <= dim <= BPE_HEAD_MAX_DIM, 1 <= n_tok <=
