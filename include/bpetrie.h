@@ -418,7 +418,8 @@ void unigram_free(bpe_unigram *model);
  * The pages have no counterpart.  The calls are asynchronous on the context's
  * stream, may be captured in a CUDA graph, and share nothing between calls but
  * the report of a wait that gave up (head_check), so that streams may take turns
- * freely, and a captured graph may outlive its context; strides count elements; n_rows == 0 is a no-op. */
+ * freely, and a captured graph may outlive its context; strides count elements;
+ * n_rows == 0 is a no-op. */
 enum { BPE_F32 = 0, BPE_BF16 = 1, BPE_F16 = 2 };
 #define BPE_HEAD_BLOCK 128u            /* columns (and vocabulary rows) that share a scale */
 #define BPE_HEAD_MAX_DIM 32768u
@@ -427,8 +428,9 @@ enum { BPE_F32 = 0, BPE_BF16 = 1, BPE_F16 = 2 };
 /* Root-mean-square norm of x + residual, in 8 bits.  Per row, in 32 bits:
  *   s = x + residual (s = x when d_residual is NULL)
  *   y = s * rsqrt(mean(s^2) + eps) * weight
- *   per block b of 128 columns: scale[b] = max(max|y| / 448, 2^-126) and
- *   y8 = e4m3(y * (1 / scale[b])), rounded to nearest even.
+ *   per block b of 128 columns: scale[b] = max(max|y| * (1 / 448), 2^-126), the
+ *   product with the 32-bit number next to 1 / 448, and y8 = e4m3(y / scale[b]),
+ *   quotient and 8-bit value rounded to nearest even.
  * A block that holds an infinity or a NaN gets that as its scale, so its
  * values stand for NaN.
  *
@@ -445,7 +447,7 @@ int head_norm(bpe_ctx *ctx, const void *d_x, uint64_t x_stride, int type, const 
               float *d_scales, uint64_t scale_row_stride, uint64_t scale_block_stride);
 
 /* A weight matrix in 8 bits, once, for head_logits: per block of 128 rows and
- * 128 columns scale = max(max|w| / 448, 2^-126), w8 = e4m3(w * (1 / scale)).
+ * 128 columns scale = max(max|w| * (1 / 448), 2^-126), w8 = e4m3(w / scale).
  * d_w: n_tok x dim of `type`, rows w_stride apart; d_w8: n_tok x dim, rows
  * w8_stride apart; d_ws: ceil(n_tok/128) x ceil(dim/128), rows ws_stride
  * apart.  Infinities and NaN as in head_norm.  Errors: INVALID_ARG, CUDA. */

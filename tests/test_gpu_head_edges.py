@@ -12,6 +12,7 @@ pytestmark = pytest.mark.gpu
 F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
 E4M3 = torch.float8_e4m3fn
 INF, NAN = float("inf"), float("nan")
+C448 = np.float32(1) / np.float32(448)
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -37,16 +38,15 @@ def blocks_exactly(v):
     q, scales = torch.empty(rows, dim), []
     for c in range(0, dim, 128):
         part = v[:, c:c + 128].numpy()
-        scale = np.maximum(np.abs(part).max(1) / np.float32(448), np.float32(2.0 ** -126))
-        back = np.float32(1) / scale
-        q[:, c:c + 128] = torch.from_numpy(part * back[:, None]).clamp(-448, 448).to(E4M3).float()
+        scale = np.maximum(np.abs(part).max(1) * C448, np.float32(2.0 ** -126))
+        q[:, c:c + 128] = torch.from_numpy(part / scale[:, None]).clamp(-448, 448).to(E4M3).float()
         scales.append(torch.from_numpy(scale))
     return q, torch.stack(scales, 1)
 
 
 @pytest.mark.parametrize("dim,off", [(4096, 0), (1024, 3), (128, 0)])
 def test_norm_scales_and_values_are_the_formulas(ctx, dim, off):
-    """A state of +-1 has the root mean square 1, so that y is the weight: max|y| / 448 and e4m3(y * (1 / scale)) bit for bit."""
+    """A state of +-1 has the root mean square 1, so that y is the weight: scales and e4m3(y / scale) bit for bit."""
     sign = randn(64, dim, seed=1).sign()
     for seed in range(8):
         w = randn(dim, seed=10 + seed) * 10.0 ** (seed - 4)
@@ -63,10 +63,9 @@ def test_quantize_scales_and_values_are_the_formulas(ctx):
         w = randn(128 * 40, 128, seed=20 + seed)
         w8, ws = ctx.head_quantize(w.cuda())
         part = w.view(40, -1).numpy()
-        scale = np.abs(part).max(1) / np.float32(448)
+        scale = np.abs(part).max(1) * C448
         assert np.array_equal(ws.cpu().numpy()[:, 0], scale)
-        back = (np.float32(1) / scale)[:, None]
-        assert torch.equal(w8.cpu().float().view(40, -1), torch.from_numpy(part * back).to(E4M3).float())
+        assert torch.equal(w8.cpu().float().view(40, -1), torch.from_numpy(part / scale[:, None]).to(E4M3).float())
 
 
 # --------------------------------------------------- waits that give up ---
@@ -410,7 +409,6 @@ def test_quantize_scales_over_the_whole_range(ctx):
     w = (torch.rand(blocks, 128, generator=g) * 2 - 1) * size
     w8, ws = ctx.head_quantize(w.view(-1, 1).cuda())
     part = w.numpy()
-    scale = np.maximum(np.abs(part).max(1) / np.float32(448), np.float32(2.0 ** -126))
+    scale = np.maximum(np.abs(part).max(1) * C448, np.float32(2.0 ** -126))
     assert np.array_equal(ws.cpu().numpy()[:, 0], scale)
-    back = (np.float32(1) / scale)[:, None]
-    assert torch.equal(w8.cpu().float().view(blocks, 128), torch.from_numpy(part * back).to(E4M3).float())
+    assert torch.equal(w8.cpu().float().view(blocks, 128), torch.from_numpy(part / scale[:, None]).to(E4M3).float())
