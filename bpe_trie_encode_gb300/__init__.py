@@ -117,6 +117,27 @@ def _head_vector(t: torch.Tensor, name: str, device: torch.device, dtype: torch.
     return t
 
 
+def _head_table(t, name: str, device: torch.device, dtypes, rows: int, columns=None, out: bool = False) -> torch.Tensor:
+    """A contiguous [rows, columns] tensor; an input that is none is copied."""
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype not in dtypes:
+        _head_place(t, name, device, dtypes)
+    if t.dim() != 2 or t.shape[0] != rows or (columns is not None and t.shape[1] != columns):
+        raise ValueError(f"{name} must be ({rows}, {'any' if columns is None else columns}), got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        if out:
+            raise ValueError(f"{name}: an output must be contiguous")
+        t = t.contiguous()
+    return t
+
+
+def _head_number(v, name: str, device: torch.device, rows: int):
+    """A number, or one for each row: (number, tensor or None, its pointer or None)."""
+    if not isinstance(v, torch.Tensor):
+        return v, None, None
+    v = _head_vector(v, name, device, torch.float32, rows)
+    return 1.0, v, v.data_ptr()
+
+
 def _head_count(k):
     """A number of tokens as the library's 32 bits hold it: none of its vocabularies has as many as the largest."""
     return max(-1, min(k, _HEAD_MOST))
@@ -459,11 +480,143 @@ class Context:
             _capi.check(self._h, rc)
         return ids, logprob
 
+    def head_logprobs(self, logits: torch.Tensor, ids: torch.Tensor | None = None, temperature=1.0, top: int = 0,
+                      logprob: torch.Tensor | None = None, entropy: torch.Tensor | None = None,
+                      top_ids: torch.Tensor | None = None, top_logprob: torch.Tensor | None = None,
+                      norm: torch.Tensor | None = None):
+        """Of each row of logits [rows, n_tok] (f32, bf16 or f16), divided by
+        temperature (a number or an f32 [rows] tensor): the log-probability of
+        the given id (ids int32 [rows]; 0 where an id is outside 0 .. n_tok -
+        1), the entropy, and the ``top`` (up to 128) largest logits' ids,
+        equal ones by lowest id, with their log-probabilities (-1 and
+        -infinity after the last logit above -infinity).  Returns (logprob
+        f32 [rows] or None without ids, entropy f32 [rows], top_ids int32
+        [rows, top], top_logprob f32 [rows, top], both None without ``top``,
+        and norm f32 [rows, 2] for ``head_logprobs_backward``).  Asynchronous
+        on the current stream.  What it returns has no gradient of its own:
+        ``logits.backward(ctx.head_logprobs_backward(...))`` gives one."""
+        dev = self.device
+        logits, stride = _head_matrix(logits, "logits", dev, _HEAD_TYPES)
+        rows, n_tok = logits.shape
+        if not 0 <= top <= _capi.BPE_HEAD_MAX_TOP:
+            raise ValueError(f"top must be 0 to {_capi.BPE_HEAD_MAX_TOP}, got {top}")
+        if ids is not None:
+            ids = _head_vector(ids, "ids", dev, torch.int32, rows)
+            logprob = torch.empty(rows, dtype=torch.float32, device=dev) if logprob is None else \
+                _head_vector(logprob, "logprob", dev, torch.float32, rows, out=True)
+        elif logprob is not None:
+            raise ValueError("logprob needs ids")
+        entropy = torch.empty(rows, dtype=torch.float32, device=dev) if entropy is None else \
+            _head_vector(entropy, "entropy", dev, torch.float32, rows, out=True)
+        if top:
+            top_ids = torch.empty(rows, top, dtype=torch.int32, device=dev) if top_ids is None else \
+                _head_table(top_ids, "top_ids", dev, (torch.int32,), rows, top, out=True)
+            top_logprob = torch.empty(rows, top, dtype=torch.float32, device=dev) if top_logprob is None else \
+                _head_table(top_logprob, "top_logprob", dev, (torch.float32,), rows, top, out=True)
+        elif top_ids is not None or top_logprob is not None:
+            raise ValueError("top_ids and top_logprob need top")
+        norm = torch.empty(rows, 2, dtype=torch.float32, device=dev) if norm is None else \
+            _head_table(norm, "norm", dev, (torch.float32,), rows, 2, out=True)
+        t, d_t, t_ptr = _head_number(temperature, "temperature", dev, rows)
+        self._sync_stream()
+        rc = self.lib.head_logprobs(self._h, logits.data_ptr(), stride, _HEAD_TYPES[logits.dtype], rows, n_tok,
+                                    ids.data_ptr() if ids is not None else None, t, t_ptr, top,
+                                    logprob.data_ptr() if ids is not None else None, entropy.data_ptr(),
+                                    top_ids.data_ptr() if top else None, top_logprob.data_ptr() if top else None,
+                                    norm.data_ptr())
+        if rc:
+            _capi.check(self._h, rc)
+        return logprob, entropy, top_ids, top_logprob, norm
+
+    def head_logprobs_backward(self, logits: torch.Tensor, ids: torch.Tensor | None, norm: torch.Tensor,
+                               grad_logprob: torch.Tensor | None = None, entropy: torch.Tensor | None = None,
+                               grad_entropy: torch.Tensor | None = None, temperature=1.0,
+                               out: torch.Tensor | None = None) -> torch.Tensor:
+        """The gradient, in the logits' type [rows, n_tok], of the sum of
+        grad_logprob * logprob + grad_entropy * entropy (each f32 [rows], None:
+        0) that ``head_logprobs`` gave for the same logits, ids and
+        temperature, from its norm and, with grad_entropy, its entropy.  A row
+        whose id is outside 0 .. n_tok - 1 has no part of grad_logprob.
+        ``out`` may be the logits themselves.  Asynchronous on the current
+        stream."""
+        dev = self.device
+        logits, stride = _head_matrix(logits, "logits", dev, _HEAD_TYPES)
+        size, dtype = logits.shape, logits.dtype
+        rows, n_tok = size
+        norm = _head_table(norm, "norm", dev, (torch.float32,), rows, 2)
+        i_ptr = a_ptr = h_ptr = b_ptr = None
+        if grad_logprob is not None:
+            if ids is None:
+                raise ValueError("grad_logprob needs ids")
+            ids = _head_vector(ids, "ids", dev, torch.int32, rows)
+            grad_logprob = _head_vector(grad_logprob, "grad_logprob", dev, torch.float32, rows)
+            i_ptr, a_ptr = ids.data_ptr(), grad_logprob.data_ptr()
+        if grad_entropy is not None:
+            if entropy is None:
+                raise ValueError("grad_entropy needs the entropy")
+            entropy = _head_vector(entropy, "entropy", dev, torch.float32, rows)
+            grad_entropy = _head_vector(grad_entropy, "grad_entropy", dev, torch.float32, rows)
+            h_ptr, b_ptr = entropy.data_ptr(), grad_entropy.data_ptr()
+        if out is None:
+            out = torch.empty(rows, n_tok, dtype=dtype, device=dev)
+        out, out_stride = _head_matrix(out, "out", dev, (dtype,), size, out=True)
+        t, d_t, t_ptr = _head_number(temperature, "temperature", dev, rows)
+        self._sync_stream()
+        rc = self.lib.head_logprobs_backward(self._h, logits.data_ptr(), stride, _HEAD_TYPES[dtype], rows, n_tok, i_ptr,
+                                             t, t_ptr, norm.data_ptr(), a_ptr, h_ptr, b_ptr, out.data_ptr(), out_stride)
+        if rc:
+            _capi.check(self._h, rc)
+        return out
+
+    def head_distill(self, logits: torch.Tensor, top_ids: torch.Tensor, top_logprob: torch.Tensor, temperature=1.0,
+                     rest: bool = False, grad=None, loss: torch.Tensor | None = None, out: torch.Tensor | None = None):
+        """(loss f32 [rows], gradient [rows, n_tok] or None): the divergence
+        KL(teacher || softmax(logits / temperature)) of each row from a
+        teacher's top alternatives, top_ids int32 and top_logprob (f32, bf16 or
+        f16) [rows, listed], listed 1 to 128, as ``head_logprobs`` gives them;
+        ids outside 0 .. n_tok - 1 are no entries.  rest=False: the teacher is
+        the softmax of the listed values, which may be logits.  rest=True: the
+        values are log-probabilities, and what they leave of 1 belongs to the
+        unlisted tokens as one class.  temperature (a number or f32 [rows])
+        divides the logits alone.  With ``grad`` (the gradient of each row's
+        loss: a number or f32 [rows], 1 / rows for a mean) the same call gives
+        the gradient of the logits in their type, for ``logits.backward``;
+        ``out`` may be the logits themselves.  One entry a row is cross
+        entropy.  Asynchronous on the current stream."""
+        dev = self.device
+        logits, stride = _head_matrix(logits, "logits", dev, _HEAD_TYPES)
+        size, dtype = logits.shape, logits.dtype
+        rows, n_tok = size
+        top_ids = _head_table(top_ids, "top_ids", dev, (torch.int32,), rows)
+        listed = top_ids.shape[1]
+        top_logprob = _head_table(top_logprob, "top_logprob", dev, _HEAD_TYPES, rows, listed)
+        if not 1 <= listed <= _capi.BPE_HEAD_MAX_TOP:
+            raise ValueError(f"top_ids must list 1 to {_capi.BPE_HEAD_MAX_TOP} tokens, got {listed}")
+        loss = torch.empty(rows, dtype=torch.float32, device=dev) if loss is None else \
+            _head_vector(loss, "loss", dev, torch.float32, rows, out=True)
+        g, d_g, g_ptr, o_ptr, o_stride = 0.0, None, None, None, 0
+        if grad is not None:
+            g, d_g, g_ptr = _head_number(grad, "grad", dev, rows)
+            if out is None:
+                out = torch.empty(rows, n_tok, dtype=dtype, device=dev)
+            out, o_stride = _head_matrix(out, "out", dev, (dtype,), size, out=True)
+            o_ptr = out.data_ptr()
+        elif out is not None:
+            raise ValueError("out needs grad")
+        t, d_t, t_ptr = _head_number(temperature, "temperature", dev, rows)
+        self._sync_stream()
+        rc = self.lib.head_distill(self._h, logits.data_ptr(), stride, _HEAD_TYPES[dtype], rows, n_tok, top_ids.data_ptr(),
+                                   top_logprob.data_ptr(), _HEAD_TYPES[top_logprob.dtype], listed, int(rest), t, t_ptr,
+                                   loss.data_ptr(), g, g_ptr, o_ptr, o_stride)
+        if rc:
+            _capi.check(self._h, rc)
+        return loss, out
+
     def head_check(self) -> None:
         """Raises BpeError (TIMEOUT), once, when a head_logits of this context
-        has given up a wait: some of its logits are NaN.  head_logits and
-        head_sample ask the same before they start; a replayed CUDA graph does
-        not.  Does not wait: call it after a synchronization."""
+        has given up a wait: some of its logits are NaN.  The other head_ calls
+        on logits ask the same before they start (head_logprobs_backward does
+        not); a replayed CUDA graph does not.  Does not wait: call it after a synchronization."""
         rc = self.lib.head_check(self._h)
         if rc:
             _capi.check(self._h, rc)

@@ -27,7 +27,7 @@ BPE_OPT_TEST_STALL_HEAD = 14
 BPE_TRIE_DOUBLE_ARRAY, BPE_TRIE_BITMAP = 0, 1
 BPE_MERGE_TWO_PASS, BPE_MERGE_LOOKBACK, BPE_MERGE_TILES, BPE_MERGE_LISTS = 0, 1, 2, 3
 BPE_F32, BPE_BF16, BPE_F16 = 0, 1, 2
-BPE_HEAD_BLOCK, BPE_HEAD_MAX_DIM, BPE_HEAD_MAX_TOKENS = 128, 32768, 1 << 22
+BPE_HEAD_BLOCK, BPE_HEAD_MAX_DIM, BPE_HEAD_MAX_TOKENS, BPE_HEAD_MAX_TOP = 128, 32768, 1 << 22, 128
 
 # every symbol the header declares (checked by the tests)
 EXPORTS = [
@@ -38,6 +38,7 @@ EXPORTS = [
     "trie_encode_host", "unigram_create", "unigram_encode", "unigram_free",
     "bpe_vocab_from_merges", "bpe_decode",
     "head_norm", "head_quantize", "head_logits", "head_sample", "head_check",
+    "head_logprobs", "head_logprobs_backward", "head_distill",
 ]
 
 
@@ -82,7 +83,7 @@ def load() -> ctypes.CDLL:
             raise ImportError(f"{LIB_PATH} is not built; run "
                               "`python -c 'import __graft_entry__ as g; g.build()'`")
         lib = ctypes.CDLL(LIB_PATH)
-        vp, i32, u32, u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint32, ctypes.c_uint64
+        vp, i32, u32, u64, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_float
         P = ctypes.POINTER
         sig = {
             "bpe_ctx_create": (i32, [P(vp), i32, vp]),
@@ -113,6 +114,9 @@ def load() -> ctypes.CDLL:
             "head_quantize": (i32, [vp, vp, u64, i32, u32, u32, vp, u64, vp, u64]),
             "head_logits": (i32, [vp, vp, u64, vp, u64, u64, vp, u64, vp, u64, u64, u32, u32, u32, vp, u64, i32]),
             "head_check": (i32, [vp]),
+            "head_logprobs": (i32, [vp, vp, u64, i32, u32, u32, vp, f32, vp, u32, vp, vp, vp, vp, vp]),
+            "head_logprobs_backward": (i32, [vp, vp, u64, i32, u32, u32, vp, f32, vp, vp, vp, vp, vp, vp, u64]),
+            "head_distill": (i32, [vp, vp, u64, i32, u32, u32, vp, vp, i32, u32, i32, f32, vp, vp, f32, vp, vp, u64]),
             "head_sample": (i32, [vp, vp, u64, i32, u32, u32, vp, P(head_filters), vp, vp]),
         }
         for name, (res, args) in sig.items():

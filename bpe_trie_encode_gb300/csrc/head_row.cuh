@@ -1,0 +1,230 @@
+// head_row.cuh -- a row of logits as the scoring and training kernels of the
+// output head see it (head_score.cu, head_distill.cu): its vectors of 16 bytes,
+// its softmax, and the sums over its threads and CTAs.
+#pragma once
+
+#include "device.cuh"
+#include "head.cuh"
+#include "internal.h"
+
+namespace bpe {
+
+typedef unsigned long long u64;
+
+constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
+constexpr int kMaxTeam = 8;                // CTAs of a row: a cluster
+
+struct RowParams {
+    const void *logits;
+    uint64_t stride;
+    uint32_t n_tok;
+    float temperature;
+    const float *d_temperature;
+
+    // c = 1 / temperature, or infinity for the limit
+    __device__ __forceinline__ float inverse(uint32_t row) const {
+        const float t = d_temperature ? d_temperature[row] : temperature;
+        return t >= kMinScale ? 1.0f / t : INFINITY;
+    }
+};
+
+// ------------------------------------------------------------ elements ---
+template <typename T> struct Bits;
+template <> struct Bits<float> { static constexpr uint32_t kNegInf = 0xFF800000u, kShift = 0; };
+template <> struct Bits<__nv_bfloat16> { static constexpr uint32_t kNegInf = 0xFF80FF80u, kShift = 16; };
+template <> struct Bits<__half> { static constexpr uint32_t kNegInf = 0xFC00FC00u, kShift = 13; };   // of 32 bits, the low ones that carry nothing
+
+// Logits as whole numbers of the same order (a NaN as -infinity, -0 as 0).
+constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
+__device__ __forceinline__ uint32_t key_of(float v) {
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    const uint32_t k = b & 0x80000000u ? ~b : b | 0x80000000u;
+    return v != v ? kKeyNegInf : k;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+
+__device__ __forceinline__ void unpack(const uint4 &q, float (&v)[4], float) {
+    v[0] = __uint_as_float(q.x), v[1] = __uint_as_float(q.y), v[2] = __uint_as_float(q.z), v[3] = __uint_as_float(q.w);
+}
+__device__ __forceinline__ void unpack(const uint4 &q, float (&v)[8], __nv_bfloat16) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+}
+__device__ __forceinline__ void unpack(const uint4 &q, float (&v)[8], __half) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float2 f = __half22float2(*(const __half2 *)&w[i]);
+        v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
+}
+
+// A row that starts anywhere, as the aligned vectors of 16 bytes that hold it.  Element e of vector i is token
+// i * kVec + e - shift; the first and the last vector may reach beyond the row, which is neither read nor written there.
+template <typename T> struct RowView {
+    static constexpr uint32_t kVec = 16 / sizeof(T);
+    T *at;              // the vector in which the row starts
+    uint32_t shift;     // elements of it before the row
+    uint32_t end;       // shift + tokens
+
+    __device__ __forceinline__ RowView(const void *base, uint64_t stride, uint32_t row, uint32_t n) {
+        const uintptr_t a = (uintptr_t)((const T *)base + row * stride);
+        at = (T *)(a & ~(uintptr_t)15);
+        shift = (uint32_t)(a & 15) / sizeof(T);
+        end = shift + n;
+    }
+    __device__ __forceinline__ uint32_t vecs() const { return (end + kVec - 1) / kVec; }
+    __device__ __forceinline__ bool whole(uint32_t i) const { return i * kVec >= shift && (i + 1) * kVec <= end; }
+    // vector i, -infinity where it reaches beyond the row
+    __device__ __forceinline__ uint4 load(uint32_t i) const {
+        if (whole(i)) return *((const uint4 *)at + i);
+        uint4 q = make_uint4(Bits<T>::kNegInf, Bits<T>::kNegInf, Bits<T>::kNegInf, Bits<T>::kNegInf);
+#pragma unroll
+        for (uint32_t e = 0; e < kVec; e++) {
+            const uint32_t p = i * kVec + e;
+            if (p >= shift && p < end) put(q, e, at[p]);
+        }
+        return q;
+    }
+    __device__ __forceinline__ void store(uint32_t i, const float (&v)[kVec]) const {
+        if (whole(i)) {
+            *((uint4 *)at + i) = pack16(v, T());
+            return;
+        }
+#pragma unroll
+        for (uint32_t e = 0; e < kVec; e++) {
+            const uint32_t p = i * kVec + e;
+            if (p >= shift && p < end) at[p] = from_f32<T>(v[e]);
+        }
+    }
+
+    static __device__ __forceinline__ void put(uint4 &q, uint32_t e, T v) {
+        uint32_t *w = (uint32_t *)&q;
+        if (sizeof(T) == 4) {
+            w[e] = *(const uint32_t *)&v;
+        } else {
+            const uint32_t b = *(const unsigned short *)&v;
+            w[e / 2] = e & 1 ? (w[e / 2] & 0xFFFFu) | b << 16 : (w[e / 2] & 0xFFFF0000u) | b;
+        }
+    }
+};
+
+// ------------------------------------------------------------ softmax ---
+// z of a logit, for every m and c (NaN counts as -infinity).
+__device__ __forceinline__ float z_any(float v, float m, float c) {
+    const float d = v - m;
+    return v == m ? 0.0f : d > -INFINITY ? d * c : -INFINITY;   // a NaN compares false
+}
+
+// ------------------------------------------------- sums over a row's CTAs ---
+__device__ __forceinline__ uint32_t far_addr(const void *p, uint32_t rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void far_store(float4 *p, uint32_t rank, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(far_addr(p, rank)), "f"(v.x), "f"(v.y), "f"(v.z),
+                 "f"(v.w) : "memory");
+}
+__device__ __forceinline__ u64 far_load(const u64 *p, uint32_t rank) {
+    u64 v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(far_addr(p, rank)) : "memory");
+    return v;
+}
+
+struct TeamShared {
+    float4 red[kRowWarps];
+    float4 slot[2][kMaxTeam];
+};
+
+// The threads of a row: one CTA, or the CTAs of a cluster.
+template <bool kTeam> struct Team {
+    TeamShared &S;
+    uint32_t rank, size;
+    int lane, warp, turn;
+
+    __device__ __forceinline__ Team(TeamShared &s, uint32_t team)
+        : S(s), rank(kTeam ? blockIdx.x % team : 0), size(kTeam ? team : 1), lane(threadIdx.x & 31),
+          warp(threadIdx.x >> 5), turn(0) {}
+
+    __device__ __forceinline__ void sync() const {
+        __syncwarp();
+        if (!kTeam)
+            __syncthreads();
+        else
+            asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+    // Before the first exchange: a CTA's shared memory is there for the others once it runs.
+    __device__ __forceinline__ void begin() const {
+        if (kTeam) sync();
+    }
+    // One value of each CTA to all: S.slot[turn][r] is CTA r's.  The slots of one exchange are written again two exchanges
+    // later, when a barrier has shown that all have read them.
+    __device__ __forceinline__ void exchange(float4 v) {
+        turn ^= 1;
+        if (threadIdx.x < size) far_store(&S.slot[turn][rank], threadIdx.x, v);
+        sync();
+    }
+    // The warps' values combined in the order of warps and CTAs; every thread gets the result.
+    template <typename F> __device__ __forceinline__ float4 across(float4 v, F f) {
+        __syncthreads();
+        if (lane == 0) S.red[warp] = v;
+        __syncthreads();
+        v = S.red[0];
+#pragma unroll
+        for (int i = 1; i < kRowWarps; i++) v = f(v, S.red[i]);
+        if (!kTeam) return v;
+        exchange(v);
+        v = S.slot[turn][0];
+        for (uint32_t r = 1; r < size; r++) v = f(v, S.slot[turn][r]);
+        return v;
+    }
+    __device__ __forceinline__ float max(float v) {   // of values that are not NaN
+        v = key_value(__reduce_max_sync(kFull, key_of(v)));
+        return across(make_float4(v, 0, 0, 0), [](float4 a, float4 b) { return make_float4(fmaxf(a.x, b.x), 0, 0, 0); }).x;
+    }
+    __device__ __forceinline__ float4 sum(float4 v) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            v.x += __shfl_xor_sync(kFull, v.x, d), v.y += __shfl_xor_sync(kFull, v.y, d);
+            v.z += __shfl_xor_sync(kFull, v.z, d), v.w += __shfl_xor_sync(kFull, v.w, d);
+        }
+        return across(v, [](float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); });
+    }
+};
+
+// The largest logit, the sum of exp(z) and that of exp(z) z.
+struct Softmax { float m, s, sz; };
+
+// Both in their general form: any logits and any c, two passes.  `load(i)` gives vector i.
+template <typename T, bool kTeam, typename L>
+__device__ __noinline__ Softmax softmax_any(Team<kTeam> &team, uint32_t lo, uint32_t hi, float c, L load) {
+    constexpr int kVec = RowView<T>::kVec;
+    float m = -INFINITY;
+    for (uint32_t i = lo + threadIdx.x; i < hi; i += kRowThreads) {
+        float v[kVec];
+        unpack(load(i), v, T());
+#pragma unroll
+        for (int e = 0; e < kVec; e++) m = fmaxf(m, v[e]);   // the other one where one is NaN
+    }
+    m = team.max(m);
+    if (m == -INFINITY) return {m, 0.0f, 0.0f};
+    float s = 0, sz = 0;
+    for (uint32_t i = lo + threadIdx.x; i < hi; i += kRowThreads) {
+        float v[kVec];
+        unpack(load(i), v, T());
+#pragma unroll
+        for (int e = 0; e < kVec; e++) {
+            const float z = z_any(v[e], m, c), x = expf(z);
+            s += x;
+            sz += x > 0.0f ? x * z : 0.0f;
+        }
+    }
+    const float4 all = team.sum(make_float4(s, sz, 0, 0));
+    return {m, all.x, all.y};
+}
+
+}  // namespace bpe

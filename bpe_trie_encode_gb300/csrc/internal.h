@@ -123,6 +123,13 @@ int head_report(bpe_ctx *ctx);
 int head_scratch(bpe_ctx *ctx, size_t bytes, void **out);
 int head_scratch_free(bpe_ctx *ctx, void *p);
 
+// The checks that the calls on rows of logits share: the logits, and a gradient
+// beside them, which is the logits themselves or overlaps them nowhere.
+int head_row_check(bpe_ctx *ctx, const char *name, const void *d_logits, uint64_t stride, int type, uint32_t n_rows,
+                   uint32_t n_tok);
+int head_grad_check(bpe_ctx *ctx, const char *name, const void *d_logits, uint64_t stride, int type, uint32_t n_rows,
+                    uint32_t n_tok, const void *d_grad, uint64_t grad_stride);
+
 // Stats helpers.
 void stats_reset(bpe_ctx *ctx);
 int stats_slot(bpe_ctx *ctx, const char *name);

@@ -1,7 +1,7 @@
 /*
  * bpetrie.h -- byte-level BPE training, greedy trie encoding, Unigram
- * (Viterbi) encoding, and the 8-bit output head that draws token ids, on one
- * GPU.
+ * (Viterbi) encoding, and the output head that draws, scores and learns token
+ * ids, on one GPU.
  *
  * C ABI of libbpetrie.so (sm_103a).  Plain pointers and sizes only.
  *
@@ -414,8 +414,9 @@ void unigram_free(bpe_unigram *model);
 
 /* The last step of a language model over a vocabulary of this library: from
  * the hidden state of each position (a row) to the id that follows it.
- * head_norm -> head_logits -> head_sample, then bpe_decode for the bytes.
- * The pages have no counterpart.  The calls are asynchronous on the context's
+ * head_norm -> head_logits -> head_sample, then bpe_decode for the bytes; from
+ * the same logits head_logprobs scores given ids, and head_distill learns from
+ * a teacher's.  The pages have no counterpart.  The calls are asynchronous on the context's
  * stream, may be captured in a CUDA graph, and share nothing between calls but
  * the report of a wait that gave up (head_check), so that streams may take turns
  * freely, and a captured graph may outlive its context; strides count elements;
@@ -465,9 +466,9 @@ int head_quantize(bpe_ctx *ctx, const void *d_w, uint64_t w_stride, int type, ui
  * Matrices whose rows do not all start on 16 bytes are first copied, at each
  * call, to stream-ordered scratch, which stays with the context like its other
  * scratch (a captured graph has its own).  The kernels' waits are bounded: if one gives up, the
- * logits that it was for are NaN, and head_check or the next head_logits or
- * head_sample on the context, on any stream, returns TIMEOUT (once) and does
- * nothing else.  1 <= dim <= BPE_HEAD_MAX_DIM, 1 <= n_tok <=
+ * logits that it was for are NaN, and head_check or the next head_logits,
+ * head_sample, head_logprobs or head_distill on the context, on any stream,
+ * returns TIMEOUT (once) and does nothing else.  1 <= dim <= BPE_HEAD_MAX_DIM, 1 <= n_tok <=
  * BPE_HEAD_MAX_TOKENS.  Errors: INVALID_ARG, OOM, TIMEOUT, CUDA. */
 int head_logits(bpe_ctx *ctx, const uint8_t *d_x8, uint64_t x8_stride, const float *d_xs, uint64_t xs_row_stride,
                 uint64_t xs_block_stride, const uint8_t *d_w8, uint64_t w8_stride, const float *d_ws,
@@ -512,6 +513,86 @@ typedef struct {
  * earlier head_logits), CUDA. */
 int head_sample(bpe_ctx *ctx, const void *d_logits, uint64_t stride, int type, uint32_t n_rows, uint32_t n_tok,
                 const float *d_u, const head_filters *filters, int32_t *d_ids_out, float *d_logprob_out);
+
+/* The softmax that the calls below work on.  With m the row's largest logit (a
+ * NaN counts as -infinity) and c = 1 / temperature: z = (logit - m) * c in 32
+ * bits (0 where logit == m, -infinity where logit - m is), s = the sum of exp(z),
+ * p = exp(z) / s.  A temperature below 2^-126 (0, negative, NaN) is the limit:
+ * the largest logits share the row evenly; an infinite one shares it among all
+ * above -infinity.  Sums are in 32 bits, in an order that n_rows, n_tok, the
+ * type and the device alone decide, so that equal calls give equal results.
+ * temperature is replaced by d_temperature (nullable, n_rows values). */
+#define BPE_HEAD_MAX_TOP 128u          /* alternatives of a row */
+
+/* Log-probabilities of given ids, the entropy, and the top alternatives.  Per row:
+ *   logprob = z[id] - log s; 0 where the id is outside 0 .. n_tok - 1, so that
+ *     rows that pad a batch add nothing to a sum
+ *   entropy = log s - (sum of p * z)
+ *   alternatives: the n_top largest logits, equal ones by lowest id, and their
+ *     z - log s; ids of -1 and -infinity after the last logit above -infinity
+ *   norm = (m, log s), for head_logprobs_backward
+ * A row with no logit above -infinity gives a logprob of -infinity, an entropy
+ * of 0 and a norm of (-infinity, 0).
+ *
+ * d_logits: n_rows x n_tok of `type`, rows `stride` apart; d_ids (nullable, with
+ * d_logprob_out): n_rows int32; d_logprob_out, d_entropy_out: n_rows f32;
+ * d_top_ids_out, d_top_logprob_out: n_rows x n_top int32 and f32, rows n_top
+ * apart; d_norm_out: n_rows x 2 f32.  Each output is nullable.  n_top <=
+ * BPE_HEAD_MAX_TOP, 1 <= n_tok <= BPE_HEAD_MAX_TOKENS.  Errors: INVALID_ARG,
+ * TIMEOUT (of an earlier head_logits), CUDA. */
+int head_logprobs(bpe_ctx *ctx, const void *d_logits, uint64_t stride, int type, uint32_t n_rows, uint32_t n_tok,
+                  const int32_t *d_ids, float temperature, const float *d_temperature, uint32_t n_top,
+                  float *d_logprob_out, float *d_entropy_out, int32_t *d_top_ids_out, float *d_top_logprob_out,
+                  float *d_norm_out);
+
+/* The gradient of the sum over rows of a * logprob + b * entropy:
+ *   d[j] = c * (a * ((j == id) - p[j]) - b * p[j] * (log p[j] + entropy))
+ * in 32 bits, rounded once to `type`; a counts as 0 where the id is outside 0 ..
+ * n_tok - 1, b * p * (log p + entropy) as 0 where p is; rows without a logit
+ * above -infinity, and temperatures below 2^-126, give zeros.
+ *
+ * d_norm: head_logprobs' norm of the same logits and temperatures.  d_grad_logprob
+ * (nullable, needs d_ids): a, n_rows f32.  d_grad_entropy (nullable, needs
+ * d_entropy, head_logprobs' entropy): b, n_rows f32.  d_grad_out: n_rows x n_tok
+ * of `type`, rows grad_stride apart; it may be d_logits itself, with the same
+ * stride, and overlaps it in no other way.  Errors: INVALID_ARG, CUDA. */
+int head_logprobs_backward(bpe_ctx *ctx, const void *d_logits, uint64_t stride, int type, uint32_t n_rows,
+                           uint32_t n_tok, const int32_t *d_ids, float temperature, const float *d_temperature,
+                           const float *d_norm, const float *d_grad_logprob, const float *d_entropy,
+                           const float *d_grad_entropy, void *d_grad_out, uint64_t grad_stride);
+
+/* Divergence of rows of logits from a teacher's top alternatives, and its
+ * gradient.  Row by row the teacher lists n_listed ids and values; an entry whose
+ * id is outside 0 .. n_tok - 1, or whose value is -infinity or NaN, is none.
+ *   rest == 0: q = softmax of the listed values (logits or log-probabilities)
+ *   rest != 0: q = exp(value), values being log-probabilities, and what is left
+ *     of 1, q_R = max(0, 1 - sum of q), belongs to the unlisted tokens as one class
+ *     (0 where no unlisted token is above -infinity: the class is empty, and
+ *     what is left is mostly rounding)
+ *   loss = sum over entries of q * (log q - log p[id])
+ *          + q_R * (log q_R - log p_R), p_R the sum of p over the unlisted tokens
+ *   d loss / d logit[j] = c * (Q * p[j] - q[j]) for listed tokens,
+ *     c * (Q - q_R / p_R) * p[j] for the others, Q = sum of q + q_R
+ * temperature divides this row's logits alone: the teacher's values are given at
+ * theirs.  An id that is listed more than once is one token: its entries' q add up
+ * in q[j], each with its own term in the loss.  Terms with q == 0 are 0; a q above
+ * 0 where p is 0 makes the loss infinite, the gradient stays finite.  A row of
+ * which nothing is listed has a loss and a gradient of 0 (rest == 0); a row
+ * without a logit above -infinity has an infinite loss, unless Q is 0, and a
+ * gradient of 0, and so have temperatures below 2^-126 (the gradient).  One entry a
+ * row with rest == 0 is cross entropy.
+ *
+ * d_top_ids: n_rows x n_listed int32; d_top_logprob: n_rows x n_listed of
+ * top_type; rows n_listed apart.  d_loss_out: n_rows f32.  d_grad_out (nullable):
+ * n_rows x n_tok of `type`, rows grad_stride apart, receives the gradient times
+ * grad (d_grad's value of the row, nullable), in 32 bits and rounded once; it may
+ * be d_logits itself, with the same stride, and overlaps it in no other way.
+ * 1 <= n_listed <= BPE_HEAD_MAX_TOP.  Errors: INVALID_ARG, TIMEOUT (of an earlier
+ * head_logits), CUDA. */
+int head_distill(bpe_ctx *ctx, const void *d_logits, uint64_t stride, int type, uint32_t n_rows, uint32_t n_tok,
+                 const int32_t *d_top_ids, const void *d_top_logprob, int top_type, uint32_t n_listed, int rest,
+                 float temperature, const float *d_temperature, float *d_loss_out, float grad, const float *d_grad,
+                 void *d_grad_out, uint64_t grad_stride);
 
 /* TIMEOUT, once, when a head_logits of this context, one in a replayed graph
  * included, has given up a wait.  Reads a word of host memory and does not
