@@ -119,6 +119,156 @@ __device__ __forceinline__ float z_any(float v, float m, float c) {
     return v == m ? 0.0f : d > -INFINITY ? d * c : -INFINITY;   // a NaN compares false
 }
 
+// ------------------------------------------------------- the usual row ---
+// Sums over rows are taken in one pass: every thread keeps the largest logit that it has met, and its sums relative to
+// that one, which are scaled when a larger one comes.  In powers of two, z = v (c log2 e) - R with R = m (c log2 e) rounded
+// once, so that a logit costs one fused step and one exponential.
+//
+// That needs numbers that stay finite: logits below `kLow` count as it, and what comes out holds where they have no weight:
+// where the row is `usual`.  Others (masked by the type's lowest value throughout, infinite, at far temperatures) take the
+// general form, softmax_any.
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+template <typename T> struct Usual {
+    static constexpr float kLow = -0x1p60f, kLeast = -0x1p50f, kMost = 0x1p50f, kMinC = 0x1p-40f, kMaxC = 0x1p20f;
+};
+template <> struct Usual<__half> {   // its lowest number is -65,504; from -16,384 down by 2^-6 a unit e^-768 is left of it
+    static constexpr float kLow = -65504.0f, kLeast = -16384.0f, kMost = 65504.0f, kMinC = 0x1p-6f, kMaxC = 0x1p20f;
+};
+template <typename T> __device__ __forceinline__ bool usual(float m, float c) {
+    return m >= Usual<T>::kLeast && m <= Usual<T>::kMost && c >= Usual<T>::kMinC && c <= Usual<T>::kMaxC;
+}
+// What the sums run with in its place until that is known (a far c would make them NaN; they are not used then).
+template <typename T> __device__ __forceinline__ float usual_c(float c) {
+    return c >= Usual<T>::kMinC && c <= Usual<T>::kMaxC ? c : 1.0f;
+}
+
+__device__ __forceinline__ float exp2_of(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Two numbers of 32 bits in one register pair.
+struct Pair {
+    u64 b;
+    Pair() = default;
+    __device__ __forceinline__ Pair(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(x), "f"(y)); }
+    __device__ __forceinline__ float2 both() const {
+        float2 f;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(b));
+        return f;
+    }
+};
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.b) : "l"(a.b), "l"(b.b), "l"(c.b));
+    return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
+    return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
+    return r;
+}
+
+// Raises a vector's logits to kLow (a NaN too), and gives the largest; an element beyond the row does not matter.
+__device__ __forceinline__ float raise(uint4 &q, float) {
+    float *v = (float *)&q;
+#pragma unroll
+    for (int e = 0; e < 4; e++) v[e] = fmaxf(v[e], Usual<float>::kLow);
+    return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+}
+__device__ __forceinline__ float raise(uint4 &q, __nv_bfloat16) {
+    __nv_bfloat162 *h = (__nv_bfloat162 *)&q;
+    const __nv_bfloat162 low = __float2bfloat162_rn(Usual<__nv_bfloat16>::kLow);
+#pragma unroll
+    for (int e = 0; e < 4; e++) h[e] = __hmax2(h[e], low);
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float raise(uint4 &q, __half) {
+    __half2 *h = (__half2 *)&q;
+    const __half2 low = __float2half2_rn(Usual<__half>::kLow);
+#pragma unroll
+    for (int e = 0; e < 4; e++) h[e] = __hmax2(h[e], low);
+    const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+// The largest of a raised vector.
+template <typename T> __device__ __forceinline__ float most_of(uint4 q) { return raise(q, T()); }
+
+// kSize vectors a thread, of the CTA's share of a row.
+template <typename T, int kSize> struct Tile {
+    static constexpr uint32_t kVecs = kSize * kRowThreads;
+    uint4 q[kSize];
+
+    __device__ __forceinline__ static uint32_t place(uint32_t i0, int u) { return i0 + u * kRowThreads + threadIdx.x; }
+    // the vectors from i0, -infinity from `hi` on; the loads of all are under way at once
+    __device__ __forceinline__ void load(const RowView<T> &row, uint32_t i0, uint32_t hi) {
+        const uint32_t whole = row.end / RowView<T>::kVec;   // vectors before this one end within the row
+        if ((i0 > 0 || row.shift == 0) && i0 + kVecs <= min(hi, whole)) {
+#pragma unroll
+            for (int u = 0; u < kSize; u++) q[u] = *((const uint4 *)row.at + place(i0, u));
+            return;
+        }
+#pragma unroll
+        for (int u = 0; u < kSize; u++) {
+            const uint32_t i = place(i0, u);
+            q[u] = make_uint4(Bits<T>::kNegInf, Bits<T>::kNegInf, Bits<T>::kNegInf, Bits<T>::kNegInf);
+            if (i < hi && row.whole(i)) q[u] = *((const uint4 *)row.at + i);
+        }
+        // the row's first and last vectors
+        if (i0 == 0 && row.shift && threadIdx.x == 0 && hi > 0) q[0] = row.load(0);
+        if (whole >= i0 && whole < i0 + kVecs && whole < hi && (whole - i0) % kRowThreads == threadIdx.x) {
+#pragma unroll
+            for (int u = 0; u < kSize; u++)
+                if (place(i0, u) == whole) q[u] = row.load(whole);
+        }
+    }
+};
+
+template <typename T, bool kEntropy> struct Running {
+    float most, r;      // the largest logit, and it times c log2 e
+    Pair s, sz;
+
+    __device__ __forceinline__ explicit Running(float c2) : most(Usual<T>::kLow), r(__fmul_rn(Usual<T>::kLow, c2)), s(0, 0), sz(0, 0) {}
+    // Relative to `m` instead, which is no less.
+    __device__ __forceinline__ void move(float m, float c2) {
+        const float to = __fmul_rn(m, c2), d = r - to, f = exp2_of(d);
+        if (kEntropy) sz = mul2(fma2(s, Pair(d, d), sz), Pair(f, f));
+        s = mul2(s, Pair(f, f));
+        most = m, r = to;
+    }
+    // Raises the tile and adds it; gives its largest logit.
+    template <int kSize> __device__ __forceinline__ float add(Tile<T, kSize> &t, float c2) {
+        constexpr int kVec = RowView<T>::kVec;
+        float m = raise(t.q[0], T());
+#pragma unroll
+        for (int u = 1; u < kSize; u++) m = fmaxf(m, raise(t.q[u], T()));
+        if (m > most) move(m, c2);
+        const Pair k(c2, c2), off(-r, -r);
+#pragma unroll
+        for (int u = 0; u < kSize; u++) {
+            float v[kVec];
+            unpack(t.q[u], v, T());
+#pragma unroll
+            for (int e = 0; e < kVec; e += 2) {
+                const Pair z = fma2(Pair(v[e], v[e + 1]), k, off);
+                const float2 x = z.both();
+                const Pair w(exp2_of(x.x), exp2_of(x.y));
+                s = add2(s, w);
+                if (kEntropy) sz = fma2(w, z, sz);
+            }
+        }
+        return m;
+    }
+};
+
 // ------------------------------------------------- sums over a row's CTAs ---
 __device__ __forceinline__ uint32_t far_addr(const void *p, uint32_t rank) {
     uint32_t a;
@@ -199,6 +349,36 @@ template <bool kTeam> struct Team {
 // The largest logit, the sum of exp(z) and that of exp(z) z.
 struct Softmax { float m, s, sz; };
 
+// Sums relative to `m` out of those relative to a.x.
+__device__ __forceinline__ float4 moved(float4 a, float m, float c2) {
+    const float d = __fmul_rn(a.x, c2) - __fmul_rn(m, c2), f = exp2_of(d);
+    return make_float4(m, a.y * f, (a.z + a.y * d) * f, a.w);
+}
+__device__ __forceinline__ float4 joined(float4 a, float4 b, float c2) {
+    const float m = fmaxf(a.x, b.x);
+    a = moved(a, m, c2), b = moved(b, m, c2);
+    return make_float4(m, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
+// The threads' sums to the row's.  m is exact; s and sz count where the row is usual.  `count` is added up beside them.
+template <typename T, bool kEntropy, bool kTeam>
+__device__ __forceinline__ Softmax softmax_join(Team<kTeam> &team, Running<T, kEntropy> a, float c2, float &count) {
+    const float m = key_value(__reduce_max_sync(kFull, key_of(a.most)));
+    a.move(m, c2);
+    const float2 s = a.s.both(), sz = a.sz.both();
+    float4 v = make_float4(m, s.x + s.y, sz.x + sz.y, count);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        v.y += __shfl_xor_sync(kFull, v.y, d);
+        if (kEntropy) v.z += __shfl_xor_sync(kFull, v.z, d);
+    }
+    v = team.across(v, [&](float4 x, float4 y) { return joined(x, y, c2); });
+    count = v.w;
+    // relative to m itself rather than to m c2 rounded
+    const float d = fmaf(v.x, c2, -__fmul_rn(v.x, c2)), f = exp2_of(-d);
+    return {v.x, v.y * f, (v.z - d * v.y) * f * kLn2};
+}
+
 // Both in their general form: any logits and any c, two passes.  `load(i)` gives vector i.
 template <typename T, bool kTeam, typename L>
 __device__ __noinline__ Softmax softmax_any(Team<kTeam> &team, uint32_t lo, uint32_t hi, float c, L load) {
@@ -225,6 +405,13 @@ __device__ __noinline__ Softmax softmax_any(Team<kTeam> &team, uint32_t lo, uint
     }
     const float4 all = team.sum(make_float4(s, sz, 0, 0));
     return {m, all.x, all.y};
+}
+
+// CTAs of a row: as many as keep every SM at work with some to spare, of 16 KB at least.
+inline uint32_t row_team(uint32_t n_rows, uint32_t bytes, uint32_t sms) {
+    uint32_t team = 1;
+    while (team < (uint32_t)kMaxTeam && (uint64_t)n_rows * team * 2 <= 6ull * sms && bytes >= team * 2 * 16384u) team *= 2;
+    return team;
 }
 
 }  // namespace bpe

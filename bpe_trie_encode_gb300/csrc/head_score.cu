@@ -23,7 +23,9 @@ struct ScoreShared {
     uint32_t list_n, scan[kRowWarps];
     u64 list[kList];                       // key of the logit, then the id from above, so that the larger comes first
     u64 best[kTop];                        // in order
+    float bound[kRowWarps];
 };
+static_assert(kTop <= kRowThreads && kMaxTeam * kTop <= kList, "one thread for each alternative, room for a team's");
 
 __device__ __forceinline__ u64 entry_of(uint32_t key, uint32_t id) { return (u64)key << 32 | (uint32_t)~id; }
 
@@ -125,39 +127,174 @@ __device__ __forceinline__ uint32_t rank_list(ScoreShared &S, uint32_t k) {
     return min(n, k);
 }
 
-template <typename T, bool kTeam>
+// ------------------------------------------- alternatives, on the way ---
+// A bound from below on the k-th largest logit of the CTA's share.  Every thread is a group; with the j-th largest of each
+// warp's 32 largest logits in S.bound, and w j >= k of them, the least of w warps' bounds has k logits at or above it.  A
+// bound only rises, so that reading one early does no harm.
+struct Bound {
+    uint32_t warps, j;                     // 0 warps: the share is too short for one
+
+    __device__ __forceinline__ Bound(uint32_t vecs, uint32_t k) : warps(min((uint32_t)kRowWarps, vecs / 32)), j(0) {
+        if (warps) j = (k + warps - 1) / warps;
+        if (j > 32) warps = 0;
+    }
+    __device__ __forceinline__ float read(const ScoreShared &S, float low) const {
+        if (!warps) return low;
+        float b = INFINITY;
+        for (uint32_t w = 0; w < warps; w++) b = fminf(b, *(const volatile float *)&S.bound[w]);
+        return b;
+    }
+    // this warp's, from its lanes' largest logits
+    __device__ __forceinline__ void write(ScoreShared &S, float v, int lane, int warp) const {
+        if (warp >= (int)warps) return;
+#pragma unroll
+        for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+            for (int d = size >> 1; d > 0; d >>= 1) {
+                const float o = __shfl_xor_sync(kFull, v, d);
+                const bool first = (lane & d) == 0, down = (lane & size) == 0 || size == 32;   // largest first
+                v = first == down ? fmaxf(v, o) : fminf(v, o);
+            }
+        if (lane == (int)j - 1) *(volatile float *)&S.bound[warp] = v;
+    }
+};
+
+// The tile's logits that may be among the alternatives.
+template <typename T, int kSize>
+__device__ __forceinline__ void list_tile(ScoreShared &S, const Tile<T, kSize> &t, const RowView<T> &row, uint32_t i0, float bound) {
+    constexpr int kVec = RowView<T>::kVec;
+#pragma unroll
+    for (int u = 0; u < kSize; u++) {
+        if (most_of<T>(t.q[u]) < bound) continue;
+        float v[kVec];
+        unpack(t.q[u], v, T());
+#pragma unroll
+        for (int e = 0; e < kVec; e++)
+            if (v[e] >= bound && v[e] > Usual<T>::kLow) {
+                const uint32_t at = atomicAdd(&S.list_n, 1);
+                if (at < kList) S.list[at] = entry_of(key_of(v[e]), t.place(i0, u) * kVec + e - row.shift);
+            }
+    }
+}
+
+// What of the list is at or above the bound, moved to its front.
+__device__ __forceinline__ void trim_list(ScoreShared &S, float bound) {
+    const uint32_t n = min(S.list_n, (uint32_t)kList);
+    u64 mine[kList / kRowThreads];
+#pragma unroll
+    for (int i = 0; i < kList / kRowThreads; i++) {
+        const uint32_t at = i * kRowThreads + threadIdx.x;
+        mine[i] = at < n ? S.list[at] : 0;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) S.list_n = 0;
+    __syncthreads();
+    const u64 least = (u64)key_of(bound) << 32;
+#pragma unroll
+    for (int i = 0; i < kList / kRowThreads; i++)
+        if (mine[i] && mine[i] >= least) S.list[atomicAdd(&S.list_n, 1)] = mine[i];
+    __syncthreads();
+}
+
+template <typename T, bool kTeam, bool kTops>
 __global__ void __launch_bounds__(kRowThreads) k_logprobs(ScoreParams P, uint32_t n_team) {
+    constexpr int kSize = 4;
+    using Tiles = Tile<T, kSize>;
     __shared__ ScoreShared S;
     Team<kTeam> team(S.team, n_team);
+    team.begin();
     const uint32_t r = kTeam ? blockIdx.x / n_team : blockIdx.x;
     const RowView<T> row(P.row.logits, P.row.stride, r, P.row.n_tok);
     const uint32_t vecs = row.vecs(), share = (vecs + team.size - 1) / team.size;
     const uint32_t lo = min(vecs, team.rank * share), hi = min(vecs, lo + share);
-    const float c = P.row.inverse(r);
-    const uint32_t k = P.top_ids || P.top_logprob ? P.n_top : 0;
+    const float c = P.row.inverse(r), c2 = usual_c<T>(c) * kLog2e;
+    const uint32_t k = kTops ? P.n_top : 0;
+    int32_t id = -1;
+    float given = 0.0f;
+    if (threadIdx.x == 0 && team.rank == 0 && P.logprob) {
+        id = P.ids[r];
+        if (id >= 0 && (uint32_t)id < P.row.n_tok) given = to_f32(row.at[row.shift + id]);
+    }
 
-    const Softmax all = softmax_any<T, kTeam>(team, lo, hi, c, [&](uint32_t i) { return row.load(i); });
-    if (k) list_any<T, kTeam>(S, team, row, lo, hi, k);
+    Running<T, true> sums(c2);
+    const Bound tops(hi - lo, k);
+    if (kTops) {
+        if (threadIdx.x == 0) S.list_n = 0;
+        float bound = Usual<T>::kLow;
+        uint32_t n = 0;
+        for (uint32_t i0 = lo; i0 < hi || n == 0; i0 += Tiles::kVecs, n++) {
+            Tiles t;
+            t.load(row, i0, hi);
+            const float m = sums.add(t, c2);
+            if ((n & (n + 1)) == 0) tops.write(S, sums.most, team.lane, team.warp);   // after 1, 2, 4... tiles
+            if (n == 0) __syncthreads();
+            bound = tops.read(S, Usual<T>::kLow);
+            if (m >= bound && m > Usual<T>::kLow) list_tile(S, t, row, i0, bound);
+        }
+        tops.write(S, sums.most, team.lane, team.warp);
+        __syncthreads();
+    } else {
+        for (uint32_t i0 = lo; i0 < hi; i0 += Tiles::kVecs) {
+            Tiles t;
+            t.load(row, i0, hi);
+            sums.add(t, c2);
+        }
+    }
+    float count = 0.0f;
+    if (kTops) {
+        const bool over = S.list_n > kList;
+        trim_list(S, tops.read(S, Usual<T>::kLow));
+        if (team.warp == 0) count = over ? -0x1p24f : fminf((float)S.list_n, (float)k);
+    }
+    Softmax all = softmax_join(team, sums, c2, count);
+    if (!usual<T>(all.m, c)) all = softmax_any<T, kTeam>(team, lo, hi, c, [&](uint32_t i) { return row.load(i); });
+    // more equal or masked logits than the list holds, or fewer others than were asked for
+    if (kTops && count < (float)min(k, P.row.n_tok)) list_any<T, kTeam>(S, team, row, lo, hi, k);
 
     const bool none = all.m == -INFINITY;
     const float log_s = none ? 0.0f : logf(all.s);
     if (threadIdx.x == 0 && team.rank == 0) {
         if (P.norm) P.norm[2 * (uint64_t)r] = all.m, P.norm[2 * (uint64_t)r + 1] = log_s;
         if (P.entropy) P.entropy[r] = none ? 0.0f : log_s - all.sz / all.s;
-        if (P.logprob) {
-            const int32_t id = P.ids ? P.ids[r] : -1;
-            float lp = 0.0f;
-            if (id >= 0 && (uint32_t)id < P.row.n_tok) lp = none ? -INFINITY : z_any(to_f32(row.at[row.shift + id]), all.m, c) - log_s;
-            P.logprob[r] = lp;
+        if (P.logprob) P.logprob[r] = id < 0 || (uint32_t)id >= P.row.n_tok ? 0.0f : none ? -INFINITY : z_any(given, all.m, c) - log_s;
+    }
+    if (!kTops) return;
+    uint32_t n = rank_list(S, k), total = n;
+    const u64 one = S.best[min(threadIdx.x, k - 1)];   // this thread's, of the n
+    uint32_t place = threadIdx.x;
+    if (kTeam) {
+        team.exchange(make_float4((float)n, 0, 0, 0));
+        total = 0;
+        for (uint32_t o = 0; o < team.size; o++) total += (uint32_t)team.S.slot[team.turn][o].x;
+        // every CTA's list, then each of its own finds its place by those that are larger
+        for (uint32_t i = threadIdx.x; i < team.size * k; i += kRowThreads) {
+            const uint32_t o = i / k;
+            if (o != team.rank && i % k < (uint32_t)team.S.slot[team.turn][o].x) S.list[i] = far_load(&S.best[i % k], o);
         }
+        __syncthreads();
+        if (threadIdx.x < n)
+            for (uint32_t o = 0; o < team.size; o++) {
+                if (o == team.rank) continue;
+                uint32_t x = 0, y = (uint32_t)team.S.slot[team.turn][o].x;
+                while (x < y) {
+                    const uint32_t mid = (x + y) / 2;
+                    if (S.list[o * k + mid] > one) x = mid + 1;
+                    else y = mid;
+                }
+                place += x;
+            }
     }
-    if (!k) return;
-    const uint32_t n = rank_list(S, k);
-    for (uint32_t i = threadIdx.x; i < k; i += kRowThreads) {
-        const u64 one = S.best[min(i, n)];
-        if (P.top_ids) P.top_ids[(uint64_t)r * k + i] = i < n ? (int32_t)~(uint32_t)one : -1;
-        if (P.top_logprob) P.top_logprob[(uint64_t)r * k + i] = i < n ? z_any(key_value((uint32_t)(one >> 32)), all.m, c) - log_s : -INFINITY;
+    if (threadIdx.x < n && place < k) {
+        const uint64_t at = (uint64_t)r * k + place;
+        if (P.top_ids) P.top_ids[at] = (int32_t)~(uint32_t)one;
+        if (P.top_logprob) P.top_logprob[at] = z_any(key_value((uint32_t)(one >> 32)), all.m, c) - log_s;
     }
+    if (team.rank == 0 && threadIdx.x >= total && threadIdx.x < k) {
+        const uint64_t at = (uint64_t)r * k + threadIdx.x;
+        if (P.top_ids) P.top_ids[at] = -1;
+        if (P.top_logprob) P.top_logprob[at] = -INFINITY;
+    }
+    if (kTeam) team.sync();   // until the others have read this CTA's list
 }
 
 // ----------------------------------------------------------- gradient ---
@@ -169,34 +306,93 @@ struct ScoreGradParams {
     uint64_t out_stride;
 };
 
+// A CTA takes one tile of a row: no sums, so that rows are cut where it suits.
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) k_logprobs_backward(ScoreGradParams P) {
-    constexpr int kVec = RowView<T>::kVec;
-    const uint32_t r = blockIdx.x;
+__global__ void __launch_bounds__(kRowThreads) k_logprobs_backward(ScoreGradParams P, uint32_t cuts) {
+    constexpr int kVec = RowView<T>::kVec, kSize = 4;
+    const uint32_t r = blockIdx.x / cuts, cut = blockIdx.x % cuts;
     const RowView<T> row(P.row.logits, P.row.stride, r, P.row.n_tok), out(P.out, P.out_stride, r, P.row.n_tok);
+    const uint32_t vecs = row.vecs(), share = (vecs + cuts - 1) / cuts;
+    const uint32_t lo = min(vecs, cut * share), hi = min(vecs, lo + share);
+    Tile<T, kSize> t;
+    t.load(row, lo, hi);
     const float c = P.row.inverse(r);
-    const float2 norm = make_float2(P.norm[2 * (uint64_t)r], P.norm[2 * (uint64_t)r + 1]);
+    const float m = P.norm[2 * (uint64_t)r], log_s = P.norm[2 * (uint64_t)r + 1];
     const int32_t id = P.ids ? P.ids[r] : -1;
     const bool given = id >= 0 && (uint32_t)id < P.row.n_tok;
     const float a = given && P.grad_logprob ? P.grad_logprob[r] : 0.0f, b = P.grad_entropy ? P.grad_entropy[r] : 0.0f;
     const float h = P.grad_entropy ? P.entropy[r] : 0.0f;
-    const bool zero = norm.x == -INFINITY || c == INFINITY;
-    for (uint32_t j = threadIdx.x; j < P.row.n_tok; j += kRowThreads) {
-        const float z = z_any(to_f32(row.at[row.shift + j]), norm.x, c), lp = z - norm.y, p = expf(lp);
-        float d = (given && (uint32_t)id == j ? a : 0.0f) - a * p;
-        if (p > 0.0f) d -= b * p * (lp + h);
-        out.at[out.shift + j] = from_f32<T>(zero ? 0.0f : c * d);
+    const bool zero = m == -INFINITY || c == INFINITY, fast = usual<T>(m, c);
+    // x = exp2(z) of the logits relative to R, m c log2 e rounded; d = x (f + g z), and c a more for the id itself.  The
+    // factor 1 / s, and what R was rounded by, are part of f and g.
+    const float c2 = c * kLog2e, off = __fmul_rn(m, c2), d0 = fmaf(m, c2, -off);
+    const float w = c * exp2_of(-fmaf(log_s, kLog2e, d0));
+    const float f = -w * (a + b * (h - log_s - d0 * kLn2)), g = -w * b * kLn2;
+    const uint32_t hot = given ? row.shift + (uint32_t)id : ~0u;
+#pragma unroll
+    for (int u = 0; u < kSize; u++) {
+        const uint32_t i = t.place(lo, u);
+        if (i >= hi) break;
+        float v[kVec];
+        if (fast) {
+            raise(t.q[u], T());
+            unpack(t.q[u], v, T());
+#pragma unroll
+            for (int e = 0; e < kVec; e++) {
+                const float z = fmaf(v[e], c2, -off);
+                v[e] = exp2_of(z) * fmaf(g, z, f);
+            }
+        } else {
+            unpack(t.q[u], v, T());
+#pragma unroll
+            for (int e = 0; e < kVec; e++) {
+                const float lp = z_any(v[e], m, c) - log_s, p = expf(lp), one = i * kVec + e == hot ? a : 0.0f;
+                v[e] = zero ? 0.0f : c * (one - a * p - (p > 0.0f ? b * p * (lp + h) : 0.0f));
+            }
+        }
+        if (fast && i == hot / kVec) {
+#pragma unroll
+            for (int e = 0; e < kVec; e++)
+                if (e == hot % kVec) v[e] = fmaf(c, a, v[e]);
+        }
+        if (out.shift == row.shift) {
+            out.store(i, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; e++) {
+                const uint32_t at = i * kVec + e;
+                if (at >= row.shift && at < row.end) out.at[out.shift + at - row.shift] = from_f32<T>(v[e]);
+            }
+        }
     }
 }
 
-template <typename T> int launch_logprobs(bpe_ctx *ctx, const ScoreParams &P, uint32_t n_rows) {
-    k_logprobs<T, false><<<n_rows, kRowThreads, 0, ctx->stream>>>(P, 1);
-    BPE_CUDA(ctx, cudaGetLastError(), "head_logprobs launch");
+template <typename T, bool kTeam, bool kTops> int launch_team(bpe_ctx *ctx, const ScoreParams &P, uint32_t n_rows, uint32_t team) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n_rows * team);
+    cfg.blockDim = dim3(kRowThreads);
+    cfg.stream = ctx->stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {team, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = kTeam ? 1 : 0;
+    BPE_CUDA(ctx, cudaLaunchKernelEx(&cfg, k_logprobs<T, kTeam, kTops>, P, team), "head_logprobs launch");
     return BPE_OK;
 }
 
+template <typename T> int launch_logprobs(bpe_ctx *ctx, const ScoreParams &P, uint32_t n_rows) {
+    const uint32_t team = row_team(n_rows, P.row.n_tok * (uint32_t)sizeof(T), (uint32_t)ctx->sm_count);
+    if (P.n_top && (P.top_ids || P.top_logprob))
+        return team > 1 ? launch_team<T, true, true>(ctx, P, n_rows, team) : launch_team<T, false, true>(ctx, P, n_rows, 1);
+    return team > 1 ? launch_team<T, true, false>(ctx, P, n_rows, team) : launch_team<T, false, false>(ctx, P, n_rows, 1);
+}
+
 template <typename T> int launch_backward(bpe_ctx *ctx, const ScoreGradParams &P, uint32_t n_rows) {
-    k_logprobs_backward<T><<<n_rows, kRowThreads, 0, ctx->stream>>>(P);
+    const uint32_t vecs = (P.row.n_tok + RowView<T>::kVec - 1) / RowView<T>::kVec + 1;   // of a row that starts anywhere
+    const uint32_t cuts = (vecs + Tile<T, 4>::kVecs - 1) / Tile<T, 4>::kVecs;
+    if ((uint64_t)n_rows * cuts > 0x7FFFFFFFu) return fail(ctx, BPE_ERR_INVALID_ARG, "head_logprobs_backward: %u rows", n_rows);
+    k_logprobs_backward<T><<<n_rows * cuts, kRowThreads, 0, ctx->stream>>>(P, cuts);
     BPE_CUDA(ctx, cudaGetLastError(), "head_logprobs_backward launch");
     return BPE_OK;
 }

@@ -16,6 +16,7 @@ pytestmark = pytest.mark.gpu
 F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
 INF, NAN = float("inf"), float("nan")
 U = 2.0 ** -24
+TINY = 2.0 ** -126
 LEAST = {F32: 2.0 ** -126, BF16: 2.0 ** -126, F16: 2.0 ** -25}   # numbers below may be lost: half the smallest, or flushed
 
 
@@ -134,6 +135,8 @@ def grad64(logits, ids, a, b, t=1.0):
     ez = mean_of(p, z.abs())[:, None]
     off = c0 * (p * rel * (a.abs() + b.abs() * (lp0.abs() + h)) + b.abs() * p * U * (r * (2 + ez) + 16 * (lp0.abs() + h) + 8 * ez)
                 + 4 * U * a.abs() * hot)
+    # exponentials relative to the largest are flushed below 2^-126: what they are multiplied by is lost that often
+    off = off + c0 * TINY * (a.abs() + b.abs() * (lp0.abs() + h))
     return d, torch.where(dead, 0.0, off)
 
 
@@ -417,6 +420,7 @@ def distill64(logits, ids, values, t, rest, g=None):
             d[r] = w * (Q * p[r] - qj - ratio)
             zz = torch.where(p[r] > 0, z[r].abs(), 0.0)
             doff[r] = abs(w) * U * (Q * p[r] * (8 * zz + rr + 30) + p[r] * (e_total + e_rest) + e_qj + 4 * qj + e_ratio)
+            doff[r] += abs(w) * TINY * (Q + q_rest)   # flushed exponentials, as above
     return loss, U * off, d, doff
 
 
