@@ -23,134 +23,261 @@ struct DistillParams {
     uint64_t out_stride;
 };
 
+constexpr int kHash = 256;
+
 struct DistillShared {
     TeamShared team;
-    uint32_t id[kMost];        // ~0: none
-    float q[kMost], v[kMost];  // the entry's q, its token's logit
+    uint32_t id[kMost];        // ~0: none, or the same as one before
+    float q[kMost], v[kMost];  // the token's q, of all its entries; its logit
+    uint32_t hash[kHash];
+    float q_sum, q_log_q, m, s;   // of the entries: the sums of q and of q log q; the listed tokens' softmax
     uint32_t bits[1];          // a bit for each place of the CTA's vectors: listed
 };
 
-// What the row's listed entries come to.
-struct Listed { float q_sum, q_log_q; };
-
-// Entries, with their weights and logits, into shared memory.
-template <typename T>
-__device__ __forceinline__ Listed read_entries(DistillShared &S, Team<false> &cta, const DistillParams &P, uint32_t r, const RowView<T> &row) {
-    const uint32_t i = threadIdx.x;
-    uint32_t id = ~0u;
-    float t = -INFINITY, v = -INFINITY;
-    if (i < P.n_listed) {
-        const uint64_t at = (uint64_t)r * P.n_listed + i;
-        id = (uint32_t)P.top_ids[at];
-        t = P.top_type == BPE_F32    ? ((const float *)P.top_logprob)[at]
-            : P.top_type == BPE_BF16 ? to_f32(((const __nv_bfloat16 *)P.top_logprob)[at])
-                                     : to_f32(((const __half *)P.top_logprob)[at]);
-        if (id >= P.row.n_tok || !(t > -INFINITY)) id = ~0u, t = -INFINITY;
-        if (id != ~0u) v = to_f32(row.at[row.shift + id]);
-    }
-    if (!P.rest) {             // the softmax of the listed values
-        const float m = cta.max(t);
-        const float z = m > -INFINITY ? z_any(t, m, 1.0f) : -INFINITY;
-        const float s = cta.sum(make_float4(expf(z), 0, 0, 0)).x;
-        t = z - logf(s);
-    }
-    const float q = t > -INFINITY ? expf(t) : 0.0f;
-    const float4 sum = cta.sum(make_float4(q, q > 0.0f ? q * t : 0.0f, 0, 0));
-    if (i < P.n_listed) S.id[i] = id, S.q[i] = q, S.v[i] = v;
-    __syncthreads();
-    return {sum.x, sum.y};
+__device__ __forceinline__ float warp_max(float v) { return key_value(__reduce_max_sync(kFull, key_of(v))); }
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+    return v;
 }
 
-template <typename T, bool kTeam>
+// The row's entries, four to a lane of the CTA's first warp, which alone deals with them while the others read the row.
+struct Entries {
+    static constexpr int kEach = kMost / 32;
+    uint32_t id[kEach];        // ~0: none
+    float t[kEach], v[kEach];  // value, then log q; the token's logit
+
+    template <typename T> __device__ __forceinline__ void load(const DistillParams &P, uint32_t r, const RowView<T> &row, int lane) {
+#pragma unroll
+        for (int j = 0; j < kEach; j++) {
+            const uint32_t i = j * 32 + lane;
+            id[j] = ~0u, t[j] = -INFINITY, v[j] = -INFINITY;
+            if (i >= P.n_listed) continue;
+            const uint64_t at = (uint64_t)r * P.n_listed + i;
+            id[j] = (uint32_t)P.top_ids[at];
+            t[j] = P.top_type == BPE_F32    ? ((const float *)P.top_logprob)[at]
+                   : P.top_type == BPE_BF16 ? to_f32(((const __nv_bfloat16 *)P.top_logprob)[at])
+                                            : to_f32(((const __half *)P.top_logprob)[at]);
+        }
+#pragma unroll
+        for (int j = 0; j < kEach; j++) {
+            if (id[j] >= P.row.n_tok || !(t[j] > -INFINITY)) id[j] = ~0u, t[j] = -INFINITY;
+            if (id[j] != ~0u) v[j] = to_f32(row.at[row.shift + id[j]]);
+        }
+    }
+    // q and the tokens to shared memory.  An id that comes twice is found by a table of hashes; then (hardly ever) every
+    // entry looks all others through, so that the sums are in the order of entries.
+    __device__ __forceinline__ void weigh(DistillShared &S, const DistillParams &P, float c, int lane) {
+        float m = -INFINITY, sum = 0, log_s = 0;
+        if (!P.rest) {         // the softmax of the listed values
+#pragma unroll
+            for (int j = 0; j < kEach; j++) m = fmaxf(m, t[j]);
+            m = warp_max(m);
+#pragma unroll
+            for (int j = 0; j < kEach; j++) {
+                t[j] = id[j] != ~0u ? z_any(t[j], m, 1.0f) : -INFINITY;
+                sum += expf(t[j]);
+            }
+            log_s = logf(warp_sum(sum));
+        }
+        float q_sum = 0, q_log_q = 0;
+        bool twice = false;
+#pragma unroll
+        for (int j = 0; j < kHash / 32; j++) S.hash[j * 32 + lane] = ~0u;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < kEach; j++) {
+            const uint32_t i = j * 32 + lane;
+            if (t[j] > -INFINITY) t[j] -= log_s;
+            const float q = expf(t[j]);
+            q_sum += q;
+            q_log_q += q > 0.0f ? q * t[j] : 0.0f;
+            S.id[i] = id[j], S.q[i] = q, S.v[i] = v[j];
+            if (id[j] == ~0u) continue;
+            for (uint32_t h = id[j] * 2654435769u >> 24;; h = (h + 1) % kHash) {   // at most 128 of 256 places are taken
+                const uint32_t old = atomicCAS(&S.hash[h], ~0u, id[j]);
+                if (old == ~0u) break;
+                if (old == id[j]) {
+                    twice = true;
+                    break;
+                }
+            }
+        }
+        __syncwarp();
+        if (__any_sync(kFull, twice)) {
+            float q[kEach];
+            bool later[kEach];
+#pragma unroll
+            for (int j = 0; j < kEach; j++) {
+                const uint32_t i = j * 32 + lane;
+                q[j] = 0, later[j] = false;
+                if (id[j] == ~0u) continue;
+                for (uint32_t o = 0; o < P.n_listed; o++)
+                    if (S.id[o] == id[j]) q[j] += S.q[o], later[j] |= o < i;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < kEach; j++) {
+                S.q[j * 32 + lane] = q[j];
+                if (later[j]) S.id[j * 32 + lane] = ~0u;
+            }
+            __syncwarp();
+        }
+        q_sum = warp_sum(q_sum), q_log_q = warp_sum(q_log_q);
+        float top = -INFINITY, s = 0;
+        if (P.rest) {          // the listed tokens' softmax, each once
+#pragma unroll
+            for (int j = 0; j < kEach; j++) top = fmaxf(top, v[j]);   // the other one where one is NaN
+            top = warp_max(top);
+#pragma unroll
+            for (int j = 0; j < kEach; j++)
+                if (top > -INFINITY && S.id[j * 32 + lane] != ~0u) s += expf(z_any(v[j], top, c));
+            s = warp_sum(s);
+        }
+        if (lane == 0) S.q_sum = q_sum, S.q_log_q = q_log_q, S.m = top, S.s = s;
+    }
+    // The sum of q log p, in the entries' own terms.
+    __device__ __forceinline__ float cross(float m, float c, float log_s) const {
+        float sum = 0;
+#pragma unroll
+        for (int j = 0; j < kEach; j++) {
+            const float q = expf(t[j]);
+            if (q > 0.0f) sum += q * (z_any(v[j], m, c) - log_s);
+        }
+        return warp_sum(sum);
+    }
+};
+
+template <typename T, bool kTeam, bool kRest, bool kGrad>
 __global__ void __launch_bounds__(kRowThreads) k_distill(DistillParams P, uint32_t n_team) {
-    constexpr int kVec = RowView<T>::kVec;
+    constexpr int kVec = RowView<T>::kVec, kSize = 4;
+    using Tiles = Tile<T, kSize>;
     extern __shared__ __align__(16) unsigned char smem[];
     DistillShared &S = *(DistillShared *)smem;
     Team<kTeam> team(S.team, n_team);
-    Team<false> cta(S.team, 1);
     team.begin();
     const uint32_t r = kTeam ? blockIdx.x / n_team : blockIdx.x;
     const RowView<T> row(P.row.logits, P.row.stride, r, P.row.n_tok);
     const uint32_t vecs = row.vecs(), share = (vecs + team.size - 1) / team.size;
     const uint32_t lo = min(vecs, team.rank * share), hi = min(vecs, lo + share);
-    const float c = P.row.inverse(r);
-    const uint32_t k = P.n_listed;
+    Tiles t;
+    t.load(row, lo, hi);       // under way while the entries are read
+    const float c = P.row.inverse(r), c2 = usual_c<T>(c) * kLog2e;
+    const float grad = kGrad ? P.d_grad ? P.d_grad[r] : P.grad : 0.0f;
 
-    const Listed listed = read_entries<T>(S, cta, P, r, row);
-    if (P.rest) {
-        for (uint32_t i = threadIdx.x; i < (share * kVec + 31) / 32; i += kRowThreads) S.bits[i] = 0;
+    Entries list;
+    if (team.warp == 0) list.load<T>(P, r, row, team.lane);
+    if (kRest) {
+        for (uint32_t i = threadIdx.x; i < ((hi - lo) * kVec + 31) / 32; i += kRowThreads) S.bits[i] = 0;
         __syncthreads();
-        if (threadIdx.x < k && S.id[threadIdx.x] != ~0u) {
-            const uint32_t at = S.id[threadIdx.x] + row.shift;
-            if (at >= lo * kVec && at < hi * kVec) atomicOr(&S.bits[(at - lo * kVec) / 32], 1u << ((at - lo * kVec) % 32));
-        }
+        if (team.warp == 0)
+#pragma unroll
+            for (int j = 0; j < Entries::kEach; j++) {
+                const uint32_t at = list.id[j] + row.shift - lo * kVec;
+                if (list.id[j] != ~0u && at < (hi - lo) * kVec) atomicOr(&S.bits[at / 32], 1u << at % 32);
+            }
         __syncthreads();
     }
-    // the softmax of the tokens that have no entry of their own: of all, where unlisted tokens are no class
-    auto load = [&](uint32_t i) {
-        uint4 q = row.load(i);
-        if (P.rest) {
-            const uint32_t at = (i - lo) * kVec, bits = S.bits[at / 32] >> (at % 32);
-            for (int e = 0; e < kVec; e++)
-                if (bits >> e & 1) RowView<T>::put(q, e, from_f32<T>(-INFINITY));
+    if (team.warp == 0) list.weigh(S, P, c, team.lane);
+
+    // The softmax of all tokens, or of the unlisted ones, whose share among themselves is exact then however little of the
+    // row they hold.
+    auto unlisted = [&](uint4 q, uint32_t i) {
+        if (kRest) {
+            const uint32_t at = (i - lo) * kVec, bits = (S.bits[at / 32] >> at % 32) & ((1u << kVec) - 1);
+            if (bits) {
+#pragma unroll
+                for (int e = 0; e < kVec; e++)
+                    if (bits >> e & 1) RowView<T>::put(q, e, from_f32<T>(-INFINITY));
+            }
         }
         return q;
     };
-    const Softmax free = softmax_any<T, kTeam>(team, lo, hi, c, load);
-
-    // every entry finds the first of its id, and that one the sum of their q
-    bool first = false;
-    uint32_t id = ~0u;
-    float v = -INFINITY, q_all = 0.0f;
-    if (threadIdx.x < k && (id = S.id[threadIdx.x]) != ~0u) {
-        first = true;
-        v = S.v[threadIdx.x];
-        for (uint32_t j = 0; j < k; j++)
-            if (S.id[j] == id) q_all += S.q[j], first &= j >= threadIdx.x;
+    Running<T, false> sums(c2);
+    uint32_t last = lo;        // the tile that stays in registers
+    for (uint32_t i0 = lo;;) {
+        if (kRest) {
+#pragma unroll
+            for (int u = 0; u < kSize; u++) {
+                const uint32_t i = t.place(i0, u);
+                if (i < hi) t.q[u] = unlisted(t.q[u], i);
+            }
+        }
+        sums.add(t, c2);
+        last = i0;
+        i0 += Tiles::kVecs;
+        if (i0 >= hi) break;
+        t.load(row, i0, hi);
     }
-    // the whole row's softmax: m, s, relative to which the unlisted tokens' is
+    float none_counted = 0.0f;
+    Softmax free = softmax_join(team, sums, c2, none_counted);
+    const bool fast = usual<T>(free.m, c);
+    if (!fast) free = softmax_any<T, kTeam>(team, lo, hi, c, [&](uint32_t i) { return unlisted(row.load(i), i); });
+
+    // the whole row's softmax: m and s, and what exp of an unlisted token's z is to be multiplied by
     float m = free.m, s = free.s, to_all = 1.0f;
-    if (P.rest) {
-        m = fmaxf(cta.max(first ? v == v ? v : -INFINITY : -INFINITY), free.m);
+    if (kRest) {
+        m = fmaxf(S.m, free.m);
         if (m > -INFINITY) {
             to_all = free.m > -INFINITY ? expf(z_any(free.m, m, c)) : 0.0f;
-            s = free.s * to_all + cta.sum(make_float4(first ? expf(z_any(v, m, c)) : 0.0f, 0, 0, 0)).x;
+            s = free.s * to_all + (S.m > -INFINITY ? S.s * expf(z_any(S.m, m, c)) : 0.0f);
         }
     }
     const bool none = m == -INFINITY;
     const float log_s = logf(s);
-    const float z = none ? -INFINITY : z_any(v, m, c);
-    float term = 0.0f;
-    if (threadIdx.x < k && S.q[threadIdx.x] > 0.0f) term = S.q[threadIdx.x] * (z - log_s);
-    const float cross = cta.sum(make_float4(term, 0, 0, 0)).x;
-    const float q_rest = P.rest && free.m > -INFINITY ? fmaxf(0.0f, 1.0f - listed.q_sum) : 0.0f, q_total = listed.q_sum + q_rest;
-    if (threadIdx.x == 0 && team.rank == 0) {
-        float loss = listed.q_log_q - cross;
-        if (q_rest > 0.0f) {
-            loss += q_rest * (logf(q_rest) - (z_any(free.m, m, c) + logf(free.s) - log_s));
-        }
-        P.loss[r] = none ? (q_total > 0.0f ? INFINITY : 0.0f) : loss;
+    const float q_rest = kRest && free.m > -INFINITY ? fmaxf(0.0f, 1.0f - S.q_sum) : 0.0f, q_total = S.q_sum + q_rest;
+    if (team.warp == 0 && team.rank == 0) {
+        float loss = S.q_log_q - list.cross(m, c, log_s);
+        if (q_rest > 0.0f) loss += q_rest * (logf(q_rest) - (z_any(free.m, m, c) + logf(free.s) - log_s));
+        if (team.lane == 0) P.loss[r] = none ? (q_total > 0.0f ? INFINITY : 0.0f) : loss;
     }
-    if (!P.out) return;
+    if (!kGrad) return;
 
     const RowView<T> out(P.out, P.out_stride, r, P.row.n_tok);
     const bool zero = none || c == INFINITY;
-    const float g = zero ? 0.0f : c * (P.d_grad ? P.d_grad[r] : P.grad);
-    const float of_free = q_total / s * to_all - (q_rest > 0.0f ? q_rest / free.s : 0.0f);
-    __syncthreads();
-    const uint32_t t0 = lo * kVec, t1 = hi * kVec;   // places of the CTA's vectors
-    for (uint32_t at = t0 + threadIdx.x; at < t1; at += kRowThreads)
-        if (at >= row.shift && at < row.end) {
-            const float x = zero || free.m == -INFINITY ? 0.0f : expf(z_any(to_f32(row.at[at]), free.m, c));
-            out.at[out.shift + at - row.shift] = from_f32<T>(zero ? 0.0f : g * (x * of_free));
+    const float g = zero ? 0.0f : c * grad;
+    const float of_free = zero || free.m == -INFINITY ? 0.0f : g * (q_total / s * to_all - (q_rest > 0.0f ? q_rest / free.s : 0.0f));
+    const float off = __fmul_rn(free.m, c2), w = of_free * exp2_of(-fmaf(free.m, c2, -off));   // what off was rounded by
+    for (uint32_t i0 = last;; i0 -= Tiles::kVecs) {   // backwards: the last tile is here
+        if (i0 != last || !fast) t.load(row, i0, hi);
+#pragma unroll
+        for (int u = 0; u < kSize; u++) {
+            const uint32_t i = t.place(i0, u);
+            if (i >= hi) break;
+            float v[kVec];
+            if (fast) {
+                raise(t.q[u], T());
+                unpack(t.q[u], v, T());
+#pragma unroll
+                for (int e = 0; e < kVec; e++) v[e] = exp2_of(fmaf(v[e], c2, -off)) * w;
+            } else {
+                unpack(t.q[u], v, T());
+#pragma unroll
+                for (int e = 0; e < kVec; e++) v[e] = of_free == 0.0f ? 0.0f : expf(z_any(v[e], free.m, c)) * of_free;
+            }
+            if (out.shift == row.shift) {
+                out.store(i, v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kVec; e++) {
+                    const uint32_t at = i * kVec + e;
+                    if (at >= row.shift && at < row.end) out.at[out.shift + at - row.shift] = from_f32<T>(v[e]);
+                }
+            }
         }
+        if (i0 == lo) break;
+    }
     __syncthreads();
-    if (first && id + row.shift >= t0 && id + row.shift < t1)
-        out.at[out.shift + id] = from_f32<T>(zero ? 0.0f : g * (q_total * expf(z - log_s) - q_all));
+    if (threadIdx.x < P.n_listed) {
+        const uint32_t id = S.id[threadIdx.x], at = id + row.shift - lo * kVec;
+        if (id != ~0u && at < (hi - lo) * kVec)
+            out.at[out.shift + id] = from_f32<T>(zero ? 0.0f : g * (q_total * expf(z_any(S.v[threadIdx.x], m, c) - log_s) - S.q[threadIdx.x]));
+    }
 }
 
-template <typename T, bool kTeam> int launch_team(bpe_ctx *ctx, const DistillParams &P, uint32_t n_rows, uint32_t team, size_t smem) {
-    auto k = k_distill<T, kTeam>;
+template <typename T, bool kTeam, bool kRest, bool kGrad>
+int launch_team(bpe_ctx *ctx, const DistillParams &P, uint32_t n_rows, uint32_t team, size_t smem) {
+    auto k = k_distill<T, kTeam, kRest, kGrad>;
     static std::atomic<uint64_t> devices{0};
     BPE_CUDA(ctx, allow_shared(k, ctx->device, kMostShared, devices), "head_distill");
     cudaLaunchConfig_t cfg = {};
@@ -167,15 +294,21 @@ template <typename T, bool kTeam> int launch_team(bpe_ctx *ctx, const DistillPar
     return BPE_OK;
 }
 
-template <typename T> int launch(bpe_ctx *ctx, const DistillParams &P, uint32_t n_rows) {
+template <typename T, bool kRest, bool kGrad> int launch(bpe_ctx *ctx, const DistillParams &P, uint32_t n_rows) {
     constexpr uint32_t kVec = RowView<T>::kVec;
     const uint32_t vecs = (P.row.n_tok + kVec - 1) / kVec + 1;   // of a row that starts anywhere
     auto shared = [&](uint32_t team) {
-        return sizeof(DistillShared) + (P.rest ? (size_t)((vecs + team - 1) / team * kVec + 31) / 32 * 4 : 0);
+        return sizeof(DistillShared) + (kRest ? (size_t)((vecs + team - 1) / team * kVec + 31) / 32 * 4 : 0);
     };
-    uint32_t team = 1;
+    uint32_t team = row_team(n_rows, P.row.n_tok * (uint32_t)sizeof(T), (uint32_t)ctx->sm_count);
     while (team < kMaxTeam && shared(team) > kMostShared) team *= 2;
-    return team > 1 ? launch_team<T, true>(ctx, P, n_rows, team, shared(team)) : launch_team<T, false>(ctx, P, n_rows, 1, shared(1));
+    return team > 1 ? launch_team<T, true, kRest, kGrad>(ctx, P, n_rows, team, shared(team))
+                    : launch_team<T, false, kRest, kGrad>(ctx, P, n_rows, 1, shared(1));
+}
+
+template <typename T> int launch(bpe_ctx *ctx, const DistillParams &P, uint32_t n_rows) {
+    if (P.rest) return P.out ? launch<T, true, true>(ctx, P, n_rows) : launch<T, true, false>(ctx, P, n_rows);
+    return P.out ? launch<T, false, true>(ctx, P, n_rows) : launch<T, false, false>(ctx, P, n_rows);
 }
 
 }  // namespace
