@@ -203,7 +203,8 @@ __global__ void __launch_bounds__(kRowThreads) k_distill(DistillParams P, uint32
                 if (i < hi) t.q[u] = unlisted(t.q[u], i);
             }
         }
-        sums.add(t, c2);
+        float each[kSize];
+        sums.add(t, c2, each);
         last = i0;
         i0 += Tiles::kVecs;
         if (i0 >= hi) break;
@@ -255,15 +256,7 @@ __global__ void __launch_bounds__(kRowThreads) k_distill(DistillParams P, uint32
 #pragma unroll
                 for (int e = 0; e < kVec; e++) v[e] = of_free == 0.0f ? 0.0f : expf(z_any(v[e], free.m, c)) * of_free;
             }
-            if (out.shift == row.shift) {
-                out.store(i, v);
-            } else {
-#pragma unroll
-                for (int e = 0; e < kVec; e++) {
-                    const uint32_t at = i * kVec + e;
-                    if (at >= row.shift && at < row.end) out.at[out.shift + at - row.shift] = from_f32<T>(v[e]);
-                }
-            }
+            put_vector(out, row, i, v);
         }
         if (i0 == lo) break;
     }
@@ -280,18 +273,7 @@ int launch_team(bpe_ctx *ctx, const DistillParams &P, uint32_t n_rows, uint32_t 
     auto k = k_distill<T, kTeam, kRest, kGrad>;
     static std::atomic<uint64_t> devices{0};
     BPE_CUDA(ctx, allow_shared(k, ctx->device, kMostShared, devices), "head_distill");
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(n_rows * team);
-    cfg.blockDim = dim3(kRowThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = ctx->stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {team, 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = kTeam ? 1 : 0;
-    BPE_CUDA(ctx, cudaLaunchKernelEx(&cfg, k, P, team), "head_distill launch");
-    return BPE_OK;
+    return launch_rows(ctx, "head_distill launch", k, P, n_rows, team, kTeam, smem);
 }
 
 template <typename T, bool kRest, bool kGrad> int launch(bpe_ctx *ctx, const DistillParams &P, uint32_t n_rows) {

@@ -80,12 +80,14 @@ template <typename T> struct RowView {
     __device__ __forceinline__ bool whole(uint32_t i) const { return i * kVec >= shift && (i + 1) * kVec <= end; }
     // vector i, -infinity where it reaches beyond the row
     __device__ __forceinline__ uint4 load(uint32_t i) const {
-        if (whole(i)) return *((const uint4 *)at + i);
+        return whole(i) ? *((const uint4 *)at + i) : edge(*this, i);
+    }
+    static __device__ __noinline__ uint4 edge(RowView r, uint32_t i) {
         uint4 q = make_uint4(Bits<T>::kNegInf, Bits<T>::kNegInf, Bits<T>::kNegInf, Bits<T>::kNegInf);
 #pragma unroll
         for (uint32_t e = 0; e < kVec; e++) {
             const uint32_t p = i * kVec + e;
-            if (p >= shift && p < end) put(q, e, at[p]);
+            if (p >= r.shift && p < r.end) put(q, e, r.at[p]);
         }
         return q;
     }
@@ -111,6 +113,25 @@ template <typename T> struct RowView {
         }
     }
 };
+
+// Vector i of a gradient, in the place of the row's; where the two start at other bytes of a vector, element by element.
+template <typename T>
+__device__ __forceinline__ void put_vector(const RowView<T> &out, const RowView<T> &row, uint32_t i, const float (&v)[RowView<T>::kVec]) {
+    if (out.shift == row.shift) {
+        out.store(i, v);
+    } else {
+#pragma unroll
+        for (uint32_t e = 0; e < RowView<T>::kVec; e++) {
+            const uint32_t at = i * RowView<T>::kVec + e;
+            if (at >= row.shift && at < row.end) out.at[out.shift + at - row.shift] = from_f32<T>(v[e]);
+        }
+    }
+}
+
+// Whether any row starts inside a vector.
+template <typename T> inline bool row_shifts(const void *base, uint64_t stride, uint32_t n_rows) {
+    return (uintptr_t)base % 16 || (n_rows > 1 && stride * sizeof(T) % 16);
+}
 
 // ------------------------------------------------------------ softmax ---
 // z of a logit, for every m and c (NaN counts as -infinity).
@@ -199,19 +220,22 @@ __device__ __forceinline__ float raise(uint4 &q, __half) {
     const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
     return fmaxf(__low2float(m), __high2float(m));
 }
-// The largest of a raised vector.
-template <typename T> __device__ __forceinline__ float most_of(uint4 q) { return raise(q, T()); }
-
 // kSize vectors a thread, of the CTA's share of a row.
 template <typename T, int kSize> struct Tile {
     static constexpr uint32_t kVecs = kSize * kRowThreads;
     uint4 q[kSize];
 
     __device__ __forceinline__ static uint32_t place(uint32_t i0, int u) { return i0 + u * kRowThreads + threadIdx.x; }
+    // No vector from i0 on ends outside the row or the share.
+    __device__ __forceinline__ static bool inside(const RowView<T> &row, uint32_t i0, uint32_t hi) {
+        return (i0 > 0 || row.shift == 0) && i0 + kVecs <= min(hi, row.end / RowView<T>::kVec);
+    }
+    __device__ __forceinline__ static uint4 fill() {
+        return make_uint4(Bits<T>::kNegInf, Bits<T>::kNegInf, Bits<T>::kNegInf, Bits<T>::kNegInf);
+    }
     // the vectors from i0, -infinity from `hi` on; the loads of all are under way at once
     __device__ __forceinline__ void load(const RowView<T> &row, uint32_t i0, uint32_t hi) {
-        const uint32_t whole = row.end / RowView<T>::kVec;   // vectors before this one end within the row
-        if ((i0 > 0 || row.shift == 0) && i0 + kVecs <= min(hi, whole)) {
+        if (inside(row, i0, hi)) {
 #pragma unroll
             for (int u = 0; u < kSize; u++) q[u] = *((const uint4 *)row.at + place(i0, u));
             return;
@@ -219,16 +243,66 @@ template <typename T, int kSize> struct Tile {
 #pragma unroll
         for (int u = 0; u < kSize; u++) {
             const uint32_t i = place(i0, u);
-            q[u] = make_uint4(Bits<T>::kNegInf, Bits<T>::kNegInf, Bits<T>::kNegInf, Bits<T>::kNegInf);
+            q[u] = fill();
             if (i < hi && row.whole(i)) q[u] = *((const uint4 *)row.at + i);
         }
-        // the row's first and last vectors
-        if (i0 == 0 && row.shift && threadIdx.x == 0 && hi > 0) q[0] = row.load(0);
-        if (whole >= i0 && whole < i0 + kVecs && whole < hi && (whole - i0) % kRowThreads == threadIdx.x) {
+#pragma unroll 1
+        for (int u = 0; u < kSize; u++) {   // the row's first and last vectors
+            const uint32_t i = place(i0, u);
+            if (i < hi && !row.whole(i)) {
+                const uint4 one = row.load(i);
 #pragma unroll
-            for (int u = 0; u < kSize; u++)
-                if (place(i0, u) == whole) q[u] = row.load(whole);
+                for (int o = 0; o < kSize; o++)
+                    if (o == u) q[o] = one;
+            }
         }
+    }
+};
+
+// The CTA's share of a row on its way through shared memory, kAhead tiles ahead of where it is read.  Every thread copies
+// (asynchronously, without registers) what it will read itself, so that no barrier is needed.  With as many slots as tiles
+// all of the share stays for a second look.
+template <typename T, int kSize> struct Feed {
+    using Tiles = Tile<T, kSize>;
+    static constexpr int kAhead = 2;
+    const RowView<T> &row;
+    uint4 *mine;               // this thread's place in the first slot
+    uint32_t lo, hi, slots;
+
+    __device__ __forceinline__ Feed(const RowView<T> &r, void *shared, uint32_t lo_, uint32_t hi_, uint32_t slots_)
+        : row(r), mine((uint4 *)shared + threadIdx.x), lo(lo_), hi(hi_), slots(slots_) {
+#pragma unroll
+        for (int n = 0; n < kAhead; n++) ask(n);
+    }
+    // tile n's copies, as one group (an empty one behind the share, but for its first)
+    __device__ __forceinline__ void ask(uint32_t n) const {
+        const uint32_t i0 = lo + n * Tiles::kVecs;
+        if (i0 < hi || n == 0) {
+            uint4 *const to = mine + n % slots * Tiles::kVecs;
+            const bool inside = Tiles::inside(row, i0, hi);
+#pragma unroll
+            for (int u = 0; u < kSize; u++) {
+                const uint32_t i = Tiles::place(i0, u);
+                if (inside || (i < hi && row.whole(i)))
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to + u * kRowThreads)),
+                                 "l"((const uint4 *)row.at + i) : "memory");
+                else
+                    to[u * kRowThreads] = i < hi ? row.load(i) : Tiles::fill();
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // tile n, in order; then the copies of the one that takes its slot
+    __device__ __forceinline__ void next(Tiles &t, uint32_t n) const {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        again(t, n);
+        ask(n + kAhead);
+    }
+    // a tile that is still there
+    __device__ __forceinline__ void again(Tiles &t, uint32_t n) const {
+        const uint4 *const from = mine + n % slots * Tiles::kVecs;
+#pragma unroll
+        for (int u = 0; u < kSize; u++) t.q[u] = from[u * kRowThreads];
     }
 };
 
@@ -244,12 +318,12 @@ template <typename T, bool kEntropy> struct Running {
         s = mul2(s, Pair(f, f));
         most = m, r = to;
     }
-    // Raises the tile and adds it; gives its largest logit.
-    template <int kSize> __device__ __forceinline__ float add(Tile<T, kSize> &t, float c2) {
+    // Raises the tile and adds it; gives its largest logit, and each vector's.
+    template <int kSize> __device__ __forceinline__ float add(Tile<T, kSize> &t, float c2, float (&each)[kSize]) {
         constexpr int kVec = RowView<T>::kVec;
-        float m = raise(t.q[0], T());
+        float m = each[0] = raise(t.q[0], T());
 #pragma unroll
-        for (int u = 1; u < kSize; u++) m = fmaxf(m, raise(t.q[u], T()));
+        for (int u = 1; u < kSize; u++) m = fmaxf(m, each[u] = raise(t.q[u], T()));
         if (m > most) move(m, c2);
         const Pair k(c2, c2), off(-r, -r);
 #pragma unroll
@@ -349,30 +423,45 @@ template <bool kTeam> struct Team {
 // The largest logit, the sum of exp(z) and that of exp(z) z.
 struct Softmax { float m, s, sz; };
 
-// Sums relative to `m` out of those relative to a.x.
-__device__ __forceinline__ float4 moved(float4 a, float m, float c2) {
-    const float d = __fmul_rn(a.x, c2) - __fmul_rn(m, c2), f = exp2_of(d);
-    return make_float4(m, a.y * f, (a.z + a.y * d) * f, a.w);
-}
-__device__ __forceinline__ float4 joined(float4 a, float4 b, float c2) {
-    const float m = fmaxf(a.x, b.x);
-    a = moved(a, m, c2), b = moved(b, m, c2);
-    return make_float4(m, a.y + b.y, a.z + b.z, a.w + b.w);
+// Sums relative to the largest m of eight lanes' out of each lane's own, added up.
+template <bool kEntropy> __device__ __forceinline__ float4 join_eight(float4 v, float c2) {
+    float m = v.x;
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+    const float d = __fmul_rn(v.x, c2) - __fmul_rn(m, c2), f = exp2_of(d);
+    v = make_float4(m, v.y * f, kEntropy ? fmaf(v.y, d, v.z) * f : 0.0f, v.w);
+#pragma unroll
+    for (int e = 4; e > 0; e >>= 1) {
+        v.y += __shfl_xor_sync(kFull, v.y, e);
+        if (kEntropy) v.z += __shfl_xor_sync(kFull, v.z, e);
+        v.w += __shfl_xor_sync(kFull, v.w, e);
+    }
+    return v;
 }
 
-// The threads' sums to the row's.  m is exact; s and sz count where the row is usual.  `count` is added up beside them.
+// The threads' sums to the row's.  m is exact; s and sz count where the row is usual.  `count`, the first warp's, is added
+// up over CTAs beside them.
 template <typename T, bool kEntropy, bool kTeam>
 __device__ __forceinline__ Softmax softmax_join(Team<kTeam> &team, Running<T, kEntropy> a, float c2, float &count) {
+    static_assert(kRowWarps == 8 && kMaxTeam == 8, "eight lanes for either");
     const float m = key_value(__reduce_max_sync(kFull, key_of(a.most)));
     a.move(m, c2);
     const float2 s = a.s.both(), sz = a.sz.both();
-    float4 v = make_float4(m, s.x + s.y, sz.x + sz.y, count);
+    float4 v = make_float4(m, s.x + s.y, sz.x + sz.y, team.warp == 0 ? count : 0.0f);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
         v.y += __shfl_xor_sync(kFull, v.y, d);
         if (kEntropy) v.z += __shfl_xor_sync(kFull, v.z, d);
     }
-    v = team.across(v, [&](float4 x, float4 y) { return joined(x, y, c2); });
+    if (team.lane == 0) team.S.red[team.warp] = v;
+    __syncthreads();
+    v = join_eight<kEntropy>(team.S.red[team.lane & 7], c2);
+    if (kTeam) {
+        team.exchange(v);
+        const uint32_t o = team.lane & 7;
+        v = o < team.size ? team.S.slot[team.turn][o] : make_float4(Usual<T>::kLow, 0, 0, 0);
+        v = join_eight<kEntropy>(v, c2);
+    }
     count = v.w;
     // relative to m itself rather than to m c2 rounded
     const float d = fmaf(v.x, c2, -__fmul_rn(v.x, c2)), f = exp2_of(-d);
@@ -412,6 +501,24 @@ inline uint32_t row_team(uint32_t n_rows, uint32_t bytes, uint32_t sms) {
     uint32_t team = 1;
     while (team < (uint32_t)kMaxTeam && (uint64_t)n_rows * team * 2 <= 6ull * sms && bytes >= team * 2 * 16384u) team *= 2;
     return team;
+}
+
+// A kernel with a CTA, or a cluster of them, for each row.
+template <typename K, typename P>
+inline int launch_rows(bpe_ctx *ctx, const char *what, K kernel, const P &params, uint32_t n_rows, uint32_t team, bool cluster, size_t shared) {
+    if ((uint64_t)n_rows * team > 0x7FFFFFFFu) return fail(ctx, BPE_ERR_INVALID_ARG, "%s: %u rows", what, n_rows);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n_rows * team);
+    cfg.blockDim = dim3(kRowThreads);
+    cfg.dynamicSmemBytes = shared;
+    cfg.stream = ctx->stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {team, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster ? 1 : 0;
+    BPE_CUDA(ctx, cudaLaunchKernelEx(&cfg, kernel, params, team), what);
+    return BPE_OK;
 }
 
 }  // namespace bpe

@@ -159,21 +159,30 @@ struct Bound {
     }
 };
 
-// The tile's logits that may be among the alternatives.
+// The tile's logits that may be among the alternatives, vector by vector that holds one: its elements go to as many lanes,
+// since hardly ever more than one or two lanes of a warp have any.
 template <typename T, int kSize>
-__device__ __forceinline__ void list_tile(ScoreShared &S, const Tile<T, kSize> &t, const RowView<T> &row, uint32_t i0, float bound) {
+__device__ __forceinline__ void list_tile(ScoreShared &S, const Tile<T, kSize> &t, const float (&each)[kSize], const RowView<T> &row,
+                                          uint32_t i0, float bound, int lane) {
     constexpr int kVec = RowView<T>::kVec;
 #pragma unroll
     for (int u = 0; u < kSize; u++) {
-        if (most_of<T>(t.q[u]) < bound) continue;
-        float v[kVec];
-        unpack(t.q[u], v, T());
-#pragma unroll
-        for (int e = 0; e < kVec; e++)
-            if (v[e] >= bound && v[e] > Usual<T>::kLow) {
+        unsigned left = __ballot_sync(kFull, each[u] >= bound && each[u] > Usual<T>::kLow);
+        while (left) {
+            const int from = __ffs(left) - 1;
+            left &= left - 1;
+            const uint32_t word = lane / (4 / sizeof(T)) % 4;
+            const uint32_t x = __shfl_sync(kFull, t.q[u].x, from), y = __shfl_sync(kFull, t.q[u].y, from);
+            const uint32_t z = __shfl_sync(kFull, t.q[u].z, from), w = __shfl_sync(kFull, t.q[u].w, from);
+            const uint4 same = make_uint4(word & 2 ? word & 1 ? w : z : word & 1 ? y : x, 0, 0, 0);
+            float v[kVec];
+            unpack(same, v, T());
+            const float mine = sizeof(T) == 2 && lane & 1 ? v[1] : v[0];
+            if (lane < kVec && mine >= bound && mine > Usual<T>::kLow) {
                 const uint32_t at = atomicAdd(&S.list_n, 1);
-                if (at < kList) S.list[at] = entry_of(key_of(v[e]), t.place(i0, u) * kVec + e - row.shift);
+                if (at < kList) S.list[at] = entry_of(key_of(mine), (t.place(i0, u) - lane + from) * kVec + lane - row.shift);
             }
+        }
     }
 }
 
@@ -196,9 +205,11 @@ __device__ __forceinline__ void trim_list(ScoreShared &S, float bound) {
     __syncthreads();
 }
 
+constexpr int kSize = 4;                   // vectors of a thread at a time
+constexpr size_t kFeedBytes = (size_t)Feed<float, kSize>::kAhead * kSize * kRowThreads * 16;
+
 template <typename T, bool kTeam, bool kTops>
-__global__ void __launch_bounds__(kRowThreads) k_logprobs(ScoreParams P, uint32_t n_team) {
-    constexpr int kSize = 4;
+__global__ void __launch_bounds__(kRowThreads, 4) k_logprobs(ScoreParams P, uint32_t n_team) {
     using Tiles = Tile<T, kSize>;
     __shared__ ScoreShared S;
     Team<kTeam> team(S.team, n_team);
@@ -216,35 +227,37 @@ __global__ void __launch_bounds__(kRowThreads) k_logprobs(ScoreParams P, uint32_
         if (id >= 0 && (uint32_t)id < P.row.n_tok) given = to_f32(row.at[row.shift + id]);
     }
 
+    extern __shared__ __align__(16) unsigned char tiles[];
+    const Feed<T, kSize> feed(row, tiles, lo, hi, Feed<T, kSize>::kAhead);
     Running<T, true> sums(c2);
     const Bound tops(hi - lo, k);
     if (kTops) {
         if (threadIdx.x == 0) S.list_n = 0;
-        float bound = Usual<T>::kLow;
-        uint32_t n = 0;
-        for (uint32_t i0 = lo; i0 < hi || n == 0; i0 += Tiles::kVecs, n++) {
+        for (uint32_t n = 0, i0 = lo; i0 < hi || n == 0; i0 += Tiles::kVecs, n++) {
             Tiles t;
-            t.load(row, i0, hi);
-            const float m = sums.add(t, c2);
+            float each[kSize];
+            feed.next(t, n);
+            const float m = sums.add(t, c2, each);
             if ((n & (n + 1)) == 0) tops.write(S, sums.most, team.lane, team.warp);   // after 1, 2, 4... tiles
             if (n == 0) __syncthreads();
-            bound = tops.read(S, Usual<T>::kLow);
-            if (m >= bound && m > Usual<T>::kLow) list_tile(S, t, row, i0, bound);
+            const float bound = tops.read(S, Usual<T>::kLow);
+            if (__any_sync(kFull, m >= bound)) list_tile(S, t, each, row, i0, bound, team.lane);
         }
         tops.write(S, sums.most, team.lane, team.warp);
         __syncthreads();
     } else {
-        for (uint32_t i0 = lo; i0 < hi; i0 += Tiles::kVecs) {
+        for (uint32_t n = 0, i0 = lo; i0 < hi; i0 += Tiles::kVecs, n++) {
             Tiles t;
-            t.load(row, i0, hi);
-            sums.add(t, c2);
+            float each[kSize];
+            feed.next(t, n);
+            sums.add(t, c2, each);
         }
     }
     float count = 0.0f;
     if (kTops) {
         const bool over = S.list_n > kList;
         trim_list(S, tops.read(S, Usual<T>::kLow));
-        if (team.warp == 0) count = over ? -0x1p24f : fminf((float)S.list_n, (float)k);
+        count = over ? -0x1p24f : fminf((float)S.list_n, (float)k);
     }
     Softmax all = softmax_join(team, sums, c2, count);
     if (!usual<T>(all.m, c)) all = softmax_any<T, kTeam>(team, lo, hi, c, [&](uint32_t i) { return row.load(i); });
@@ -307,30 +320,34 @@ struct ScoreGradParams {
 };
 
 // A CTA takes one tile of a row: no sums, so that rows are cut where it suits.
-template <typename T>
+constexpr int kGradSize = 4;
+
+template <typename T, bool kEntropy>
 __global__ void __launch_bounds__(kRowThreads) k_logprobs_backward(ScoreGradParams P, uint32_t cuts) {
-    constexpr int kVec = RowView<T>::kVec, kSize = 4;
+    constexpr int kVec = RowView<T>::kVec;
+    using Tiles = Tile<T, kGradSize>;
     const uint32_t r = blockIdx.x / cuts, cut = blockIdx.x % cuts;
     const RowView<T> row(P.row.logits, P.row.stride, r, P.row.n_tok), out(P.out, P.out_stride, r, P.row.n_tok);
-    const uint32_t vecs = row.vecs(), share = (vecs + cuts - 1) / cuts;
-    const uint32_t lo = min(vecs, cut * share), hi = min(vecs, lo + share);
-    Tile<T, kSize> t;
+    const uint32_t lo = cut * Tiles::kVecs, hi = min(row.vecs(), lo + Tiles::kVecs);
+    if (lo >= hi) return;
+    Tiles t;
     t.load(row, lo, hi);
     const float c = P.row.inverse(r);
     const float m = P.norm[2 * (uint64_t)r], log_s = P.norm[2 * (uint64_t)r + 1];
     const int32_t id = P.ids ? P.ids[r] : -1;
     const bool given = id >= 0 && (uint32_t)id < P.row.n_tok;
-    const float a = given && P.grad_logprob ? P.grad_logprob[r] : 0.0f, b = P.grad_entropy ? P.grad_entropy[r] : 0.0f;
-    const float h = P.grad_entropy ? P.entropy[r] : 0.0f;
+    const float a = given && P.grad_logprob ? P.grad_logprob[r] : 0.0f;
+    const float b = kEntropy ? P.grad_entropy[r] : 0.0f, h = kEntropy ? P.entropy[r] : 0.0f;
     const bool zero = m == -INFINITY || c == INFINITY, fast = usual<T>(m, c);
     // x = exp2(z) of the logits relative to R, m c log2 e rounded; d = x (f + g z), and c a more for the id itself.  The
     // factor 1 / s, and what R was rounded by, are part of f and g.
     const float c2 = c * kLog2e, off = __fmul_rn(m, c2), d0 = fmaf(m, c2, -off);
     const float w = c * exp2_of(-fmaf(log_s, kLog2e, d0));
     const float f = -w * (a + b * (h - log_s - d0 * kLn2)), g = -w * b * kLn2;
+    const Pair c22(c2, c2), off2(-off, -off), f2(f, f), g2(g, g);
     const uint32_t hot = given ? row.shift + (uint32_t)id : ~0u;
 #pragma unroll
-    for (int u = 0; u < kSize; u++) {
+    for (int u = 0; u < kGradSize; u++) {
         const uint32_t i = t.place(lo, u);
         if (i >= hi) break;
         float v[kVec];
@@ -338,9 +355,11 @@ __global__ void __launch_bounds__(kRowThreads) k_logprobs_backward(ScoreGradPara
             raise(t.q[u], T());
             unpack(t.q[u], v, T());
 #pragma unroll
-            for (int e = 0; e < kVec; e++) {
-                const float z = fmaf(v[e], c2, -off);
-                v[e] = exp2_of(z) * fmaf(g, z, f);
+            for (int e = 0; e < kVec; e += 2) {
+                const Pair z = fma2(Pair(v[e], v[e + 1]), c22, off2);
+                const float2 x = z.both();
+                const float2 d = mul2(Pair(exp2_of(x.x), exp2_of(x.y)), kEntropy ? fma2(g2, z, f2) : f2).both();
+                v[e] = d.x, v[e + 1] = d.y;
             }
         } else {
             unpack(t.q[u], v, T());
@@ -355,30 +374,12 @@ __global__ void __launch_bounds__(kRowThreads) k_logprobs_backward(ScoreGradPara
             for (int e = 0; e < kVec; e++)
                 if (e == hot % kVec) v[e] = fmaf(c, a, v[e]);
         }
-        if (out.shift == row.shift) {
-            out.store(i, v);
-        } else {
-#pragma unroll
-            for (int e = 0; e < kVec; e++) {
-                const uint32_t at = i * kVec + e;
-                if (at >= row.shift && at < row.end) out.at[out.shift + at - row.shift] = from_f32<T>(v[e]);
-            }
-        }
+        put_vector(out, row, i, v);
     }
 }
 
 template <typename T, bool kTeam, bool kTops> int launch_team(bpe_ctx *ctx, const ScoreParams &P, uint32_t n_rows, uint32_t team) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(n_rows * team);
-    cfg.blockDim = dim3(kRowThreads);
-    cfg.stream = ctx->stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {team, 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = kTeam ? 1 : 0;
-    BPE_CUDA(ctx, cudaLaunchKernelEx(&cfg, k_logprobs<T, kTeam, kTops>, P, team), "head_logprobs launch");
-    return BPE_OK;
+    return launch_rows(ctx, "head_logprobs launch", k_logprobs<T, kTeam, kTops>, P, n_rows, team, kTeam, kFeedBytes);
 }
 
 template <typename T> int launch_logprobs(bpe_ctx *ctx, const ScoreParams &P, uint32_t n_rows) {
@@ -389,10 +390,13 @@ template <typename T> int launch_logprobs(bpe_ctx *ctx, const ScoreParams &P, ui
 }
 
 template <typename T> int launch_backward(bpe_ctx *ctx, const ScoreGradParams &P, uint32_t n_rows) {
-    const uint32_t vecs = (P.row.n_tok + RowView<T>::kVec - 1) / RowView<T>::kVec + 1;   // of a row that starts anywhere
-    const uint32_t cuts = (vecs + Tile<T, 4>::kVecs - 1) / Tile<T, 4>::kVecs;
+    const uint32_t vecs = (P.row.n_tok + RowView<T>::kVec - 1) / RowView<T>::kVec + (row_shifts<T>(P.row.logits, P.row.stride, n_rows) ? 1 : 0);
+    const uint32_t cuts = (vecs + Tile<T, kGradSize>::kVecs - 1) / Tile<T, kGradSize>::kVecs;
     if ((uint64_t)n_rows * cuts > 0x7FFFFFFFu) return fail(ctx, BPE_ERR_INVALID_ARG, "head_logprobs_backward: %u rows", n_rows);
-    k_logprobs_backward<T><<<n_rows * cuts, kRowThreads, 0, ctx->stream>>>(P, cuts);
+    if (P.grad_entropy)
+        k_logprobs_backward<T, true><<<n_rows * cuts, kRowThreads, 0, ctx->stream>>>(P, cuts);
+    else
+        k_logprobs_backward<T, false><<<n_rows * cuts, kRowThreads, 0, ctx->stream>>>(P, cuts);
     BPE_CUDA(ctx, cudaGetLastError(), "head_logprobs_backward launch");
     return BPE_OK;
 }
