@@ -6,7 +6,8 @@ namespace bpe {
 namespace {
 
 constexpr int kMost = (int)BPE_HEAD_MAX_TOP;   // alternatives that a teacher lists
-constexpr size_t kMostShared = 72 * 1024;       // of a CTA: the bits of the most tokens over the largest team
+constexpr size_t kMostShared = 200 * 1024;      // of a CTA
+constexpr uint32_t kKeep = 4;                   // tiles of a row that leave room for three CTAs on an SM
 static_assert(kMost <= kRowThreads, "one thread for each");
 
 struct DistillParams {
@@ -148,20 +149,32 @@ struct Entries {
     }
 };
 
+constexpr int kSize = 4;       // vectors of a thread at a time
+
+// A vector with -infinity in the elements that `some` has bits for.
+template <typename T> __device__ __forceinline__ uint4 without(uint4 q, uint32_t some) {
+    constexpr uint32_t k = Bits<T>::kNegInf;
+    auto word = [=](uint32_t w, int i) {
+        const uint32_t mask = sizeof(T) == 4 ? (some >> i & 1 ? ~0u : 0u)
+                                             : (some >> 2 * i & 1 ? 0xFFFFu : 0u) | (some >> 2 * i & 2 ? 0xFFFF0000u : 0u);
+        return (w & ~mask) | (k & mask);
+    };
+    return make_uint4(word(q.x, 0), word(q.y, 1), word(q.z, 2), word(q.w, 3));
+}
+
 template <typename T, bool kTeam, bool kRest, bool kGrad>
-__global__ void __launch_bounds__(kRowThreads) k_distill(DistillParams P, uint32_t n_team) {
-    constexpr int kVec = RowView<T>::kVec, kSize = 4;
+__global__ void __launch_bounds__(kRowThreads, 4) k_distill(DistillParams P, uint32_t n_team, uint32_t slots) {
+    constexpr int kVec = RowView<T>::kVec;
     using Tiles = Tile<T, kSize>;
     extern __shared__ __align__(16) unsigned char smem[];
-    DistillShared &S = *(DistillShared *)smem;
+    DistillShared &S = *(DistillShared *)(smem + slots * (Tiles::kVecs * 16));
     Team<kTeam> team(S.team, n_team);
     team.begin();
     const uint32_t r = kTeam ? blockIdx.x / n_team : blockIdx.x;
     const RowView<T> row(P.row.logits, P.row.stride, r, P.row.n_tok);
     const uint32_t vecs = row.vecs(), share = (vecs + team.size - 1) / team.size;
     const uint32_t lo = min(vecs, team.rank * share), hi = min(vecs, lo + share);
-    Tiles t;
-    t.load(row, lo, hi);       // under way while the entries are read
+    const Feed<T, kSize> feed(row, smem, lo, hi, slots);   // under way while the entries are read
     const float c = P.row.inverse(r), c2 = usual_c<T>(c) * kLog2e;
     const float grad = kGrad ? P.d_grad ? P.d_grad[r] : P.grad : 0.0f;
 
@@ -182,38 +195,33 @@ __global__ void __launch_bounds__(kRowThreads) k_distill(DistillParams P, uint32
 
     // The softmax of all tokens, or of the unlisted ones, whose share among themselves is exact then however little of the
     // row they hold.
-    auto unlisted = [&](uint4 q, uint32_t i) {
+    const uint32_t *const bits = S.bits;
+    auto unlisted = [=](uint4 q, uint32_t i) {
         if (kRest) {
-            const uint32_t at = (i - lo) * kVec, bits = (S.bits[at / 32] >> at % 32) & ((1u << kVec) - 1);
-            if (bits) {
-#pragma unroll
-                for (int e = 0; e < kVec; e++)
-                    if (bits >> e & 1) RowView<T>::put(q, e, from_f32<T>(-INFINITY));
-            }
+            const uint32_t at = (i - lo) * kVec, some = (bits[at / 32] >> at % 32) & ((1u << kVec) - 1);
+            if (some) q = without<T>(q, some);
         }
         return q;
     };
     Running<T, false> sums(c2);
-    uint32_t last = lo;        // the tile that stays in registers
-    for (uint32_t i0 = lo;;) {
+    const uint32_t steps = (hi - lo + Tiles::kVecs - 1) / Tiles::kVecs;
+    for (uint32_t n = 0; n < steps; n++) {
+        Tiles t;
+        feed.next(t, n);
         if (kRest) {
 #pragma unroll
             for (int u = 0; u < kSize; u++) {
-                const uint32_t i = t.place(i0, u);
+                const uint32_t i = t.place(lo + n * Tiles::kVecs, u);
                 if (i < hi) t.q[u] = unlisted(t.q[u], i);
             }
         }
         float each[kSize];
         sums.add(t, c2, each);
-        last = i0;
-        i0 += Tiles::kVecs;
-        if (i0 >= hi) break;
-        t.load(row, i0, hi);
     }
     float none_counted = 0.0f;
     Softmax free = softmax_join(team, sums, c2, none_counted);
     const bool fast = usual<T>(free.m, c);
-    if (!fast) free = softmax_any<T, kTeam>(team, lo, hi, c, [&](uint32_t i) { return unlisted(row.load(i), i); });
+    if (!fast) free = softmax_any<T, kTeam>(team, lo, hi, c, [=](uint32_t i) { return unlisted(row.load(i), i); });
 
     // the whole row's softmax: m and s, and what exp of an unlisted token's z is to be multiplied by
     float m = free.m, s = free.s, to_all = 1.0f;
@@ -239,8 +247,11 @@ __global__ void __launch_bounds__(kRowThreads) k_distill(DistillParams P, uint32
     const float g = zero ? 0.0f : c * grad;
     const float of_free = zero || free.m == -INFINITY ? 0.0f : g * (q_total / s * to_all - (q_rest > 0.0f ? q_rest / free.s : 0.0f));
     const float off = __fmul_rn(free.m, c2), w = of_free * exp2_of(-fmaf(free.m, c2, -off));   // what off was rounded by
-    for (uint32_t i0 = last;; i0 -= Tiles::kVecs) {   // backwards: the last tile is here
-        if (i0 != last || !fast) t.load(row, i0, hi);
+    for (uint32_t n = 0; n < steps; n++) {
+        const uint32_t i0 = lo + n * Tiles::kVecs;
+        Tiles t;
+        if (slots >= steps) feed.again(t, n);
+        else t.load(row, i0, hi);
 #pragma unroll
         for (int u = 0; u < kSize; u++) {
             const uint32_t i = t.place(i0, u);
@@ -250,7 +261,11 @@ __global__ void __launch_bounds__(kRowThreads) k_distill(DistillParams P, uint32
                 raise(t.q[u], T());
                 unpack(t.q[u], v, T());
 #pragma unroll
-                for (int e = 0; e < kVec; e++) v[e] = exp2_of(fmaf(v[e], c2, -off)) * w;
+                for (int e = 0; e < kVec; e += 2) {
+                    const float2 x = fma2(Pair(v[e], v[e + 1]), Pair(c2, c2), Pair(-off, -off)).both();
+                    const float2 d = mul2(Pair(exp2_of(x.x), exp2_of(x.y)), Pair(w, w)).both();
+                    v[e] = d.x, v[e + 1] = d.y;
+                }
             } else {
                 unpack(t.q[u], v, T());
 #pragma unroll
@@ -258,7 +273,6 @@ __global__ void __launch_bounds__(kRowThreads) k_distill(DistillParams P, uint32
             }
             put_vector(out, row, i, v);
         }
-        if (i0 == lo) break;
     }
     __syncthreads();
     if (threadIdx.x < P.n_listed) {
@@ -269,23 +283,31 @@ __global__ void __launch_bounds__(kRowThreads) k_distill(DistillParams P, uint32
 }
 
 template <typename T, bool kTeam, bool kRest, bool kGrad>
-int launch_team(bpe_ctx *ctx, const DistillParams &P, uint32_t n_rows, uint32_t team, size_t smem) {
+int launch_team(bpe_ctx *ctx, const DistillParams &P, uint32_t n_rows, uint32_t team, uint32_t slots, size_t smem) {
     auto k = k_distill<T, kTeam, kRest, kGrad>;
     static std::atomic<uint64_t> devices{0};
     BPE_CUDA(ctx, allow_shared(k, ctx->device, kMostShared, devices), "head_distill");
-    return launch_rows(ctx, "head_distill launch", k, P, n_rows, team, kTeam, smem);
+    return launch_rows(ctx, "head_distill launch", k, P, n_rows, team, kTeam, smem, slots);
 }
 
 template <typename T, bool kRest, bool kGrad> int launch(bpe_ctx *ctx, const DistillParams &P, uint32_t n_rows) {
-    constexpr uint32_t kVec = RowView<T>::kVec;
-    const uint32_t vecs = (P.row.n_tok + kVec - 1) / kVec + 1;   // of a row that starts anywhere
+    constexpr uint32_t kVec = RowView<T>::kVec, kTileBytes = Tile<T, kSize>::kVecs * 16, kAhead = Feed<T, kSize>::kAhead;
+    const uint32_t vecs = (P.row.n_tok + kVec - 1) / kVec + (row_shifts<T>(P.row.logits, P.row.stride, n_rows) ? 1 : 0);
+    uint32_t slots = kAhead;
     auto shared = [&](uint32_t team) {
-        return sizeof(DistillShared) + (kRest ? (size_t)((vecs + team - 1) / team * kVec + 31) / 32 * 4 : 0);
+        return (size_t)slots * kTileBytes + sizeof(DistillShared) + (kRest ? (size_t)((vecs + team - 1) / team * kVec + 31) / 32 * 4 : 0);
     };
+    auto tiles = [&](uint32_t team) { return ((vecs + team - 1) / team + Tile<T, kSize>::kVecs - 1) / Tile<T, kSize>::kVecs; };
     uint32_t team = row_team(n_rows, P.row.n_tok * (uint32_t)sizeof(T), (uint32_t)ctx->sm_count);
+    if (kGrad) {
+        // A row that stays in shared memory is read once.
+        while (team < kMaxTeam && tiles(team) > kKeep) team *= 2;
+        if (tiles(team) > kAhead) slots = tiles(team);
+        if (shared(team) > kMostShared) slots = kAhead;
+    }
     while (team < kMaxTeam && shared(team) > kMostShared) team *= 2;
-    return team > 1 ? launch_team<T, true, kRest, kGrad>(ctx, P, n_rows, team, shared(team))
-                    : launch_team<T, false, kRest, kGrad>(ctx, P, n_rows, 1, shared(1));
+    return team > 1 ? launch_team<T, true, kRest, kGrad>(ctx, P, n_rows, team, slots, shared(team))
+                    : launch_team<T, false, kRest, kGrad>(ctx, P, n_rows, 1, slots, shared(1));
 }
 
 template <typename T> int launch(bpe_ctx *ctx, const DistillParams &P, uint32_t n_rows) {

@@ -71,9 +71,9 @@ template <typename T> struct RowView {
     uint32_t end;       // shift + tokens
 
     __device__ __forceinline__ RowView(const void *base, uint64_t stride, uint32_t row, uint32_t n) {
-        const uintptr_t a = (uintptr_t)((const T *)base + row * stride);
-        at = (T *)(a & ~(uintptr_t)15);
-        shift = (uint32_t)(a & 15) / sizeof(T);
+        T *const p = (T *)base + row * stride;
+        shift = (uint32_t)((uintptr_t)p & 15) / sizeof(T);
+        at = p - shift;     // a pointer rounded as a number would be one to any memory, whose stores are slower
         end = shift + n;
     }
     __device__ __forceinline__ uint32_t vecs() const { return (end + kVec - 1) / kVec; }
@@ -91,18 +91,6 @@ template <typename T> struct RowView {
         }
         return q;
     }
-    __device__ __forceinline__ void store(uint32_t i, const float (&v)[kVec]) const {
-        if (whole(i)) {
-            *((uint4 *)at + i) = pack16(v, T());
-            return;
-        }
-#pragma unroll
-        for (uint32_t e = 0; e < kVec; e++) {
-            const uint32_t p = i * kVec + e;
-            if (p >= shift && p < end) at[p] = from_f32<T>(v[e]);
-        }
-    }
-
     static __device__ __forceinline__ void put(uint4 &q, uint32_t e, T v) {
         uint32_t *w = (uint32_t *)&q;
         if (sizeof(T) == 4) {
@@ -114,18 +102,22 @@ template <typename T> struct RowView {
     }
 };
 
-// Vector i of a gradient, in the place of the row's; where the two start at other bytes of a vector, element by element.
+// Vector i of a gradient, in the place of the row's.  What is not a whole vector, or starts elsewhere in one than the row
+// does, goes element by element, in a function of its own: written out here, its stores take issue slots when they do not run.
+template <typename T> __device__ __noinline__ void put_elements(RowView<T> out, RowView<T> row, uint32_t i, uint4 q) {
+    const T *const v = (const T *)&q;
+    constexpr uint32_t kVec = RowView<T>::kVec;
+#pragma unroll
+    for (uint32_t e = 0; e < kVec; e++) {
+        const uint32_t at = i * kVec + e;
+        if (at >= row.shift && at < row.end) out.at[out.shift + at - row.shift] = v[e];
+    }
+}
 template <typename T>
 __device__ __forceinline__ void put_vector(const RowView<T> &out, const RowView<T> &row, uint32_t i, const float (&v)[RowView<T>::kVec]) {
-    if (out.shift == row.shift) {
-        out.store(i, v);
-    } else {
-#pragma unroll
-        for (uint32_t e = 0; e < RowView<T>::kVec; e++) {
-            const uint32_t at = i * RowView<T>::kVec + e;
-            if (at >= row.shift && at < row.end) out.at[out.shift + at - row.shift] = from_f32<T>(v[e]);
-        }
-    }
+    const uint4 q = pack16(v, T());
+    if (out.shift == row.shift && row.whole(i)) *((uint4 *)out.at + i) = q;
+    else put_elements(out, row, i, q);
 }
 
 // Whether any row starts inside a vector.
@@ -422,6 +414,7 @@ template <bool kTeam> struct Team {
 
 // The largest logit, the sum of exp(z) and that of exp(z) z.
 struct Softmax { float m, s, sz; };
+struct SoftmaxAny { Softmax all; int turn; };
 
 // Sums relative to the largest m of eight lanes' out of each lane's own, added up.
 template <bool kEntropy> __device__ __forceinline__ float4 join_eight(float4 v, float c2) {
@@ -468,9 +461,10 @@ __device__ __forceinline__ Softmax softmax_join(Team<kTeam> &team, Running<T, kE
     return {v.x, v.y * f, (v.z - d * v.y) * f * kLn2};
 }
 
-// Both in their general form: any logits and any c, two passes.  `load(i)` gives vector i.
+// Both in their general form: any logits and any c, two passes.  `load(i)` gives vector i.  (By value, and the team's turn
+// given back: what a function that is called takes by reference lives in memory, in the usual rows' loops too.)
 template <typename T, bool kTeam, typename L>
-__device__ __noinline__ Softmax softmax_any(Team<kTeam> &team, uint32_t lo, uint32_t hi, float c, L load) {
+__device__ __noinline__ SoftmaxAny softmax_sums(Team<kTeam> team, uint32_t lo, uint32_t hi, float c, L load) {
     constexpr int kVec = RowView<T>::kVec;
     float m = -INFINITY;
     for (uint32_t i = lo + threadIdx.x; i < hi; i += kRowThreads) {
@@ -480,7 +474,7 @@ __device__ __noinline__ Softmax softmax_any(Team<kTeam> &team, uint32_t lo, uint
         for (int e = 0; e < kVec; e++) m = fmaxf(m, v[e]);   // the other one where one is NaN
     }
     m = team.max(m);
-    if (m == -INFINITY) return {m, 0.0f, 0.0f};
+    if (m == -INFINITY) return {{m, 0.0f, 0.0f}, team.turn};
     float s = 0, sz = 0;
     for (uint32_t i = lo + threadIdx.x; i < hi; i += kRowThreads) {
         float v[kVec];
@@ -493,7 +487,13 @@ __device__ __noinline__ Softmax softmax_any(Team<kTeam> &team, uint32_t lo, uint
         }
     }
     const float4 all = team.sum(make_float4(s, sz, 0, 0));
-    return {m, all.x, all.y};
+    return {{m, all.x, all.y}, team.turn};
+}
+template <typename T, bool kTeam, typename L>
+__device__ __forceinline__ Softmax softmax_any(Team<kTeam> &team, uint32_t lo, uint32_t hi, float c, L load) {
+    const SoftmaxAny any = softmax_sums<T, kTeam>(team, lo, hi, c, load);
+    team.turn = any.turn;
+    return any.all;
 }
 
 // CTAs of a row: as many as keep every SM at work with some to spare, of 16 KB at least.
@@ -504,8 +504,9 @@ inline uint32_t row_team(uint32_t n_rows, uint32_t bytes, uint32_t sms) {
 }
 
 // A kernel with a CTA, or a cluster of them, for each row.
-template <typename K, typename P>
-inline int launch_rows(bpe_ctx *ctx, const char *what, K kernel, const P &params, uint32_t n_rows, uint32_t team, bool cluster, size_t shared) {
+template <typename K, typename P, typename... More>
+inline int launch_rows(bpe_ctx *ctx, const char *what, K kernel, const P &params, uint32_t n_rows, uint32_t team, bool cluster,
+                       size_t shared, More... more) {
     if ((uint64_t)n_rows * team > 0x7FFFFFFFu) return fail(ctx, BPE_ERR_INVALID_ARG, "%s: %u rows", what, n_rows);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(n_rows * team);
@@ -517,7 +518,7 @@ inline int launch_rows(bpe_ctx *ctx, const char *what, K kernel, const P &params
     attr[0].val.clusterDim = {team, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = cluster ? 1 : 0;
-    BPE_CUDA(ctx, cudaLaunchKernelEx(&cfg, kernel, params, team), what);
+    BPE_CUDA(ctx, cudaLaunchKernelEx(&cfg, kernel, params, team, more...), what);
     return BPE_OK;
 }
 

@@ -8,6 +8,10 @@ namespace {
 constexpr int kTop = (int)BPE_HEAD_MAX_TOP;
 constexpr int kList = 1024;                // tokens that may be among the alternatives
 
+constexpr int kSize = 4;                   // vectors of a thread at a time
+constexpr size_t kFeedBytes = (size_t)Feed<float, kSize>::kAhead * kSize * kRowThreads * 16;
+constexpr uint32_t kGradTiles = 8;         // of a CTA of the gradient, at most
+
 struct ScoreParams {
     RowParams row;
     const int32_t *ids;
@@ -30,9 +34,9 @@ static_assert(kTop <= kRowThreads && kMaxTeam * kTop <= kList, "one thread for e
 __device__ __forceinline__ u64 entry_of(uint32_t key, uint32_t id) { return (u64)key << 32 | (uint32_t)~id; }
 
 // The alternatives in S.list, at most k of this CTA's, for any logits: the key of the k-th largest is found by bits, two
-// a pass; those above it are listed, and as many of its equals, in order of ids, as there is room for.
+// a pass; those above it are listed, and as many of its equals, in order of ids, as there is room for.  Gives the team's turn.
 template <typename T, bool kTeam>
-__device__ __noinline__ void list_any(ScoreShared &S, Team<kTeam> &team, const RowView<T> &row, uint32_t lo, uint32_t hi, uint32_t k) {
+__device__ __noinline__ int list_any(ScoreShared &S, Team<kTeam> team, RowView<T> row, uint32_t lo, uint32_t hi, uint32_t k) {
     constexpr int kVec = RowView<T>::kVec, kShift = Bits<T>::kShift, kBits = (32 - kShift + 1) & ~1;
     uint32_t some = 0;
     for (uint32_t i = lo + threadIdx.x; i < hi; i += kRowThreads) {
@@ -45,7 +49,7 @@ __device__ __noinline__ void list_any(ScoreShared &S, Team<kTeam> &team, const R
     const float want = fminf((float)k, valid);
     if (threadIdx.x == 0) S.list_n = 0;
     __syncthreads();
-    if (want == 0.0f) return;
+    if (want == 0.0f) return team.turn;
     uint32_t cut = 0;
     for (int bit = kBits - 2; bit >= 0; bit -= 2) {
         uint32_t n1 = 0, n2 = 0, n3 = 0;
@@ -109,6 +113,7 @@ __device__ __noinline__ void list_any(ScoreShared &S, Team<kTeam> &team, const R
         }
     }
     __syncthreads();
+    return team.turn;
 }
 
 // The list's k largest in order, in S.best: each entry's place is the number of larger ones, counted by four threads.
@@ -205,9 +210,6 @@ __device__ __forceinline__ void trim_list(ScoreShared &S, float bound) {
     __syncthreads();
 }
 
-constexpr int kSize = 4;                   // vectors of a thread at a time
-constexpr size_t kFeedBytes = (size_t)Feed<float, kSize>::kAhead * kSize * kRowThreads * 16;
-
 template <typename T, bool kTeam, bool kTops>
 __global__ void __launch_bounds__(kRowThreads, 4) k_logprobs(ScoreParams P, uint32_t n_team) {
     using Tiles = Tile<T, kSize>;
@@ -260,9 +262,9 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_logprobs(ScoreParams P, uint
         count = over ? -0x1p24f : fminf((float)S.list_n, (float)k);
     }
     Softmax all = softmax_join(team, sums, c2, count);
-    if (!usual<T>(all.m, c)) all = softmax_any<T, kTeam>(team, lo, hi, c, [&](uint32_t i) { return row.load(i); });
+    if (!usual<T>(all.m, c)) all = softmax_any<T, kTeam>(team, lo, hi, c, [=](uint32_t i) { return row.load(i); });
     // more equal or masked logits than the list holds, or fewer others than were asked for
-    if (kTops && count < (float)min(k, P.row.n_tok)) list_any<T, kTeam>(S, team, row, lo, hi, k);
+    if (kTops && count < (float)min(k, P.row.n_tok)) team.turn = list_any<T, kTeam>(S, team, row, lo, hi, k);
 
     const bool none = all.m == -INFINITY;
     const float log_s = none ? 0.0f : logf(all.s);
@@ -319,19 +321,17 @@ struct ScoreGradParams {
     uint64_t out_stride;
 };
 
-// A CTA takes one tile of a row: no sums, so that rows are cut where it suits.
-constexpr int kGradSize = 4;
-
+// No sums, so that a row is cut where it suits: a CTA takes `each` tiles of it.
 template <typename T, bool kEntropy>
-__global__ void __launch_bounds__(kRowThreads) k_logprobs_backward(ScoreGradParams P, uint32_t cuts) {
+__global__ void __launch_bounds__(kRowThreads) k_logprobs_backward(ScoreGradParams P, uint32_t cuts, uint32_t each) {
     constexpr int kVec = RowView<T>::kVec;
-    using Tiles = Tile<T, kGradSize>;
+    using Tiles = Tile<T, kSize>;
+    extern __shared__ __align__(16) unsigned char tiles[];
     const uint32_t r = blockIdx.x / cuts, cut = blockIdx.x % cuts;
     const RowView<T> row(P.row.logits, P.row.stride, r, P.row.n_tok), out(P.out, P.out_stride, r, P.row.n_tok);
-    const uint32_t lo = cut * Tiles::kVecs, hi = min(row.vecs(), lo + Tiles::kVecs);
+    const uint32_t lo = cut * each * Tiles::kVecs, hi = min(row.vecs(), lo + each * Tiles::kVecs);
     if (lo >= hi) return;
-    Tiles t;
-    t.load(row, lo, hi);
+    const Feed<T, kSize> feed(row, tiles, lo, hi, Feed<T, kSize>::kAhead);
     const float c = P.row.inverse(r);
     const float m = P.norm[2 * (uint64_t)r], log_s = P.norm[2 * (uint64_t)r + 1];
     const int32_t id = P.ids ? P.ids[r] : -1;
@@ -346,35 +346,38 @@ __global__ void __launch_bounds__(kRowThreads) k_logprobs_backward(ScoreGradPara
     const float f = -w * (a + b * (h - log_s - d0 * kLn2)), g = -w * b * kLn2;
     const Pair c22(c2, c2), off2(-off, -off), f2(f, f), g2(g, g);
     const uint32_t hot = given ? row.shift + (uint32_t)id : ~0u;
+    for (uint32_t n = 0; n * Tiles::kVecs < hi - lo; n++) {
+        Tiles t;
+        feed.next(t, n);
 #pragma unroll
-    for (int u = 0; u < kGradSize; u++) {
-        const uint32_t i = t.place(lo, u);
-        if (i >= hi) break;
-        float v[kVec];
-        if (fast) {
-            raise(t.q[u], T());
-            unpack(t.q[u], v, T());
+        for (int u = 0; u < kSize; u++) {
+            const uint32_t i = t.place(lo + n * Tiles::kVecs, u);
+            if (i >= hi) break;
+            float v[kVec];
+            if (fast) {
+                raise(t.q[u], T());
+                unpack(t.q[u], v, T());
 #pragma unroll
-            for (int e = 0; e < kVec; e += 2) {
-                const Pair z = fma2(Pair(v[e], v[e + 1]), c22, off2);
-                const float2 x = z.both();
-                const float2 d = mul2(Pair(exp2_of(x.x), exp2_of(x.y)), kEntropy ? fma2(g2, z, f2) : f2).both();
-                v[e] = d.x, v[e + 1] = d.y;
+                for (int e = 0; e < kVec; e += 2) {
+                    const Pair z = fma2(Pair(v[e], v[e + 1]), c22, off2);
+                    const float2 x = z.both();
+                    const float2 d = mul2(Pair(exp2_of(x.x), exp2_of(x.y)), kEntropy ? fma2(g2, z, f2) : f2).both();
+                    v[e] = d.x, v[e + 1] = d.y;
+                }
+            } else {
+                unpack(t.q[u], v, T());
+#pragma unroll
+                for (int e = 0; e < kVec; e++) {
+                    const float lp = z_any(v[e], m, c) - log_s, p = expf(lp), one = i * kVec + e == hot ? a : 0.0f;
+                    v[e] = zero ? 0.0f : c * (one - a * p - (p > 0.0f ? b * p * (lp + h) : 0.0f));
+                }
             }
-        } else {
-            unpack(t.q[u], v, T());
+            if (fast && i == hot / kVec) {
 #pragma unroll
-            for (int e = 0; e < kVec; e++) {
-                const float lp = z_any(v[e], m, c) - log_s, p = expf(lp), one = i * kVec + e == hot ? a : 0.0f;
-                v[e] = zero ? 0.0f : c * (one - a * p - (p > 0.0f ? b * p * (lp + h) : 0.0f));
+                for (int e = 0; e < kVec; e++) v[e] = fmaf(c, e == hot % kVec ? a : 0.0f, v[e]);
             }
+            put_vector(out, row, i, v);
         }
-        if (fast && i == hot / kVec) {
-#pragma unroll
-            for (int e = 0; e < kVec; e++)
-                if (e == hot % kVec) v[e] = fmaf(c, a, v[e]);
-        }
-        put_vector(out, row, i, v);
     }
 }
 
@@ -391,12 +394,13 @@ template <typename T> int launch_logprobs(bpe_ctx *ctx, const ScoreParams &P, ui
 
 template <typename T> int launch_backward(bpe_ctx *ctx, const ScoreGradParams &P, uint32_t n_rows) {
     const uint32_t vecs = (P.row.n_tok + RowView<T>::kVec - 1) / RowView<T>::kVec + (row_shifts<T>(P.row.logits, P.row.stride, n_rows) ? 1 : 0);
-    const uint32_t cuts = (vecs + Tile<T, kGradSize>::kVecs - 1) / Tile<T, kGradSize>::kVecs;
+    const uint32_t tiles = (vecs + Tile<T, kSize>::kVecs - 1) / Tile<T, kSize>::kVecs;
+    uint32_t each = 1;
+    while (each < kGradTiles && each < tiles && (uint64_t)n_rows * ((tiles + each) / (each + 1)) >= 16ull * ctx->sm_count) each++;
+    const uint32_t cuts = (tiles + each - 1) / each;
     if ((uint64_t)n_rows * cuts > 0x7FFFFFFFu) return fail(ctx, BPE_ERR_INVALID_ARG, "head_logprobs_backward: %u rows", n_rows);
-    if (P.grad_entropy)
-        k_logprobs_backward<T, true><<<n_rows * cuts, kRowThreads, 0, ctx->stream>>>(P, cuts);
-    else
-        k_logprobs_backward<T, false><<<n_rows * cuts, kRowThreads, 0, ctx->stream>>>(P, cuts);
+    auto k = P.grad_entropy ? k_logprobs_backward<T, true> : k_logprobs_backward<T, false>;
+    k<<<n_rows * cuts, kRowThreads, kFeedBytes, ctx->stream>>>(P, cuts, each);
     BPE_CUDA(ctx, cudaGetLastError(), "head_logprobs_backward launch");
     return BPE_OK;
 }
