@@ -8,7 +8,7 @@ namespace {
 constexpr int kMost = (int)BPE_HEAD_MAX_TOP;   // alternatives that a teacher lists
 constexpr size_t kMostShared = 200 * 1024;      // of a CTA
 constexpr uint32_t kKeep = 4;                   // tiles of a row that leave room for three CTAs on an SM
-static_assert(kMost <= kRowThreads, "one thread for each");
+static_assert(kMost <= (int)kRowThreads, "one thread for each");
 
 struct DistillParams {
     RowParams row;
@@ -25,6 +25,8 @@ struct DistillParams {
 };
 
 constexpr int kHash = 256;
+constexpr int kThreads = kRowThreads + 32;      // the row's, and a warp for the entries
+constexpr int kLister = kRowWarps;
 
 struct DistillShared {
     TeamShared team;
@@ -42,7 +44,7 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// The row's entries, four to a lane of the CTA's first warp, which alone deals with them while the others read the row.
+// The row's entries, four to a lane of the CTA's last warp, which deals with them while the others read the row.
 struct Entries {
     static constexpr int kEach = kMost / 32;
     uint32_t id[kEach];        // ~0: none
@@ -151,6 +153,12 @@ struct Entries {
 
 constexpr int kSize = 4;       // vectors of a thread at a time
 
+// The bits of vector i of the share.
+template <typename T> __device__ __forceinline__ uint32_t vector_bits(const uint32_t *bits, uint32_t i) {
+    const uint8_t *const bytes = (const uint8_t *)bits;
+    return sizeof(T) == 2 ? bytes[i] : bytes[i / 2] >> i % 2 * 4 & 15;
+}
+
 // A vector with -infinity in the elements that `some` has bits for.
 template <typename T> __device__ __forceinline__ uint4 without(uint4 q, uint32_t some) {
     constexpr uint32_t k = Bits<T>::kNegInf;
@@ -163,27 +171,28 @@ template <typename T> __device__ __forceinline__ uint4 without(uint4 q, uint32_t
 }
 
 template <typename T, bool kTeam, bool kRest, bool kGrad>
-__global__ void __launch_bounds__(kRowThreads, 4) k_distill(DistillParams P, uint32_t n_team, uint32_t slots) {
+__global__ void __launch_bounds__(kThreads, 3) k_distill(DistillParams P, uint32_t n_team, uint32_t slots, bool kept) {
     constexpr int kVec = RowView<T>::kVec;
     using Tiles = Tile<T, kSize>;
     extern __shared__ __align__(16) unsigned char smem[];
     DistillShared &S = *(DistillShared *)(smem + slots * (Tiles::kVecs * 16));
     Team<kTeam> team(S.team, n_team);
-    team.begin();
+    team.arrive();
     const uint32_t r = kTeam ? blockIdx.x / n_team : blockIdx.x;
     const RowView<T> row(P.row.logits, P.row.stride, r, P.row.n_tok);
     const uint32_t vecs = row.vecs(), share = (vecs + team.size - 1) / team.size;
     const uint32_t lo = min(vecs, team.rank * share), hi = min(vecs, lo + share);
-    const Feed<T, kSize> feed(row, smem, lo, hi, slots);   // under way while the entries are read
+    const bool reads = team.warp != kLister;
+    const Feed<T, kSize> feed(row, smem, lo, reads ? hi : lo, kept, reads);   // under way while the entries are read
     const float c = P.row.inverse(r), c2 = usual_c<T>(c) * kLog2e;
     const float grad = kGrad ? P.d_grad ? P.d_grad[r] : P.grad : 0.0f;
 
     Entries list;
-    if (team.warp == 0) list.load<T>(P, r, row, team.lane);
+    if (team.warp == kLister) list.load<T>(P, r, row, team.lane);
     if (kRest) {
-        for (uint32_t i = threadIdx.x; i < ((hi - lo) * kVec + 31) / 32; i += kRowThreads) S.bits[i] = 0;
+        for (uint32_t i = threadIdx.x; i < ((hi - lo) * kVec + 31) / 32; i += kThreads) S.bits[i] = 0;
         __syncthreads();
-        if (team.warp == 0)
+        if (team.warp == kLister)
 #pragma unroll
             for (int j = 0; j < Entries::kEach; j++) {
                 const uint32_t at = list.id[j] + row.shift - lo * kVec;
@@ -191,32 +200,33 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_distill(DistillParams P, uin
             }
         __syncthreads();
     }
-    if (team.warp == 0) list.weigh(S, P, c, team.lane);
+    if (team.warp == kLister) list.weigh(S, P, c, team.lane);
 
     // The softmax of all tokens, or of the unlisted ones, whose share among themselves is exact then however little of the
     // row they hold.
     const uint32_t *const bits = S.bits;
     auto unlisted = [=](uint4 q, uint32_t i) {
         if (kRest) {
-            const uint32_t at = (i - lo) * kVec, some = (bits[at / 32] >> at % 32) & ((1u << kVec) - 1);
+            const uint32_t some = vector_bits<T>(bits, i - lo);
             if (some) q = without<T>(q, some);
         }
         return q;
     };
     Running<T, false> sums(c2);
-    const uint32_t steps = (hi - lo + Tiles::kVecs - 1) / Tiles::kVecs;
+    const uint32_t steps = reads ? (hi - lo + Tiles::kVecs - 1) / Tiles::kVecs : 0;
     for (uint32_t n = 0; n < steps; n++) {
         Tiles t;
         feed.next(t, n);
-        if (kRest) {
+        if (kRest) {           // what lies behind the share is -infinity whatever its bits
+            uint32_t some[kSize], any = 0;
 #pragma unroll
-            for (int u = 0; u < kSize; u++) {
-                const uint32_t i = t.place(lo + n * Tiles::kVecs, u);
-                if (i < hi) t.q[u] = unlisted(t.q[u], i);
+            for (int u = 0; u < kSize; u++) any |= some[u] = vector_bits<T>(S.bits, t.place(n * Tiles::kVecs, u));
+            if (any) {
+#pragma unroll
+                for (int u = 0; u < kSize; u++) t.q[u] = without<T>(t.q[u], some[u]);
             }
         }
-        float each[kSize];
-        sums.add(t, c2, each);
+        sums.add(t, t.raise_all(), c2);
     }
     float none_counted = 0.0f;
     Softmax free = softmax_join(team, sums, c2, none_counted);
@@ -235,7 +245,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_distill(DistillParams P, uin
     const bool none = m == -INFINITY;
     const float log_s = logf(s);
     const float q_rest = kRest && free.m > -INFINITY ? fmaxf(0.0f, 1.0f - S.q_sum) : 0.0f, q_total = S.q_sum + q_rest;
-    if (team.warp == 0 && team.rank == 0) {
+    if (team.warp == kLister && team.rank == 0) {
         float loss = S.q_log_q - list.cross(m, c, log_s);
         if (q_rest > 0.0f) loss += q_rest * (logf(q_rest) - (z_any(free.m, m, c) + logf(free.s) - log_s));
         if (team.lane == 0) P.loss[r] = none ? (q_total > 0.0f ? INFINITY : 0.0f) : loss;
@@ -250,7 +260,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_distill(DistillParams P, uin
     for (uint32_t n = 0; n < steps; n++) {
         const uint32_t i0 = lo + n * Tiles::kVecs;
         Tiles t;
-        if (slots >= steps) feed.again(t, n);
+        if (kept) feed.again(t, n);
         else t.load(row, i0, hi);
 #pragma unroll
         for (int u = 0; u < kSize; u++) {
@@ -258,7 +268,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_distill(DistillParams P, uin
             if (i >= hi) break;
             float v[kVec];
             if (fast) {
-                raise(t.q[u], T());
+                raise<T>(t.q[u]);
                 unpack(t.q[u], v, T());
 #pragma unroll
                 for (int e = 0; e < kVec; e += 2) {
@@ -283,31 +293,31 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_distill(DistillParams P, uin
 }
 
 template <typename T, bool kTeam, bool kRest, bool kGrad>
-int launch_team(bpe_ctx *ctx, const DistillParams &P, uint32_t n_rows, uint32_t team, uint32_t slots, size_t smem) {
+int launch_team(bpe_ctx *ctx, const DistillParams &P, uint32_t n_rows, uint32_t team, uint32_t slots, bool kept, size_t smem) {
     auto k = k_distill<T, kTeam, kRest, kGrad>;
     static std::atomic<uint64_t> devices{0};
     BPE_CUDA(ctx, allow_shared(k, ctx->device, kMostShared, devices), "head_distill");
-    return launch_rows(ctx, "head_distill launch", k, P, n_rows, team, kTeam, smem, slots);
+    return launch_rows(ctx, "head_distill launch", k, P, n_rows, team, kThreads, kTeam, smem, slots, kept);
 }
 
 template <typename T, bool kRest, bool kGrad> int launch(bpe_ctx *ctx, const DistillParams &P, uint32_t n_rows) {
     constexpr uint32_t kVec = RowView<T>::kVec, kTileBytes = Tile<T, kSize>::kVecs * 16, kAhead = Feed<T, kSize>::kAhead;
     const uint32_t vecs = (P.row.n_tok + kVec - 1) / kVec + (row_shifts<T>(P.row.logits, P.row.stride, n_rows) ? 1 : 0);
-    uint32_t slots = kAhead;
-    auto shared = [&](uint32_t team) {
-        return (size_t)slots * kTileBytes + sizeof(DistillShared) + (kRest ? (size_t)((vecs + team - 1) / team * kVec + 31) / 32 * 4 : 0);
+    uint32_t team = row_team(n_rows, P.row.n_tok * (uint32_t)sizeof(T), (uint32_t)ctx->sm_count), slots = kAhead;
+    auto tiles = [&](uint32_t t) { return ((vecs + t - 1) / t + Tile<T, kSize>::kVecs - 1) / Tile<T, kSize>::kVecs; };
+    auto shared = [&]() {   // of the entries, the tiles, and bits for tiles that are whole
+        return sizeof(DistillShared) + (size_t)slots * kTileBytes + (kRest ? (size_t)tiles(team) * Tile<T, kSize>::kVecs * kVec / 8 : 0);
     };
-    auto tiles = [&](uint32_t team) { return ((vecs + team - 1) / team + Tile<T, kSize>::kVecs - 1) / Tile<T, kSize>::kVecs; };
-    uint32_t team = row_team(n_rows, P.row.n_tok * (uint32_t)sizeof(T), (uint32_t)ctx->sm_count);
-    if (kGrad) {
-        // A row that stays in shared memory is read once.
+    bool kept = false;
+    if (kGrad) {   // a row that stays in shared memory is read once
         while (team < kMaxTeam && tiles(team) > kKeep) team *= 2;
-        if (tiles(team) > kAhead) slots = tiles(team);
-        if (shared(team) > kMostShared) slots = kAhead;
+        slots = tiles(team);
+        kept = shared() <= kMostShared;
+        if (!kept) slots = kAhead;
     }
-    while (team < kMaxTeam && shared(team) > kMostShared) team *= 2;
-    return team > 1 ? launch_team<T, true, kRest, kGrad>(ctx, P, n_rows, team, slots, shared(team))
-                    : launch_team<T, false, kRest, kGrad>(ctx, P, n_rows, 1, slots, shared(1));
+    while (team < kMaxTeam && shared() > kMostShared) team *= 2;
+    return team > 1 ? launch_team<T, true, kRest, kGrad>(ctx, P, n_rows, team, slots, kept, shared())
+                    : launch_team<T, false, kRest, kGrad>(ctx, P, n_rows, 1, slots, kept, shared());
 }
 
 template <typename T> int launch(bpe_ctx *ctx, const DistillParams &P, uint32_t n_rows) {

@@ -189,34 +189,51 @@ __device__ __forceinline__ Pair mul2(Pair a, Pair b) {
     return r;
 }
 
-// Raises a vector's logits to kLow (a NaN too), and gives the largest; an element beyond the row does not matter.
-__device__ __forceinline__ float raise(uint4 &q, float) {
-    float *v = (float *)&q;
+// Logits by words of 32 bits: raised to kLow (a NaN too), the larger of two, the largest of a word.
+template <typename T> struct Words;
+template <> struct Words<float> {
+    using W = float;
+    static __device__ __forceinline__ W low() { return Usual<float>::kLow; }
+    static __device__ __forceinline__ W larger(W a, W b) { return fmaxf(a, b); }
+    static __device__ __forceinline__ float largest(W a) { return a; }
+};
+template <> struct Words<__nv_bfloat16> {
+    using W = __nv_bfloat162;
+    static __device__ __forceinline__ W low() { return __float2bfloat162_rn(Usual<__nv_bfloat16>::kLow); }
+    static __device__ __forceinline__ W larger(W a, W b) { return __hmax2(a, b); }
+    static __device__ __forceinline__ float largest(W a) { return fmaxf(__low2float(a), __high2float(a)); }
+};
+template <> struct Words<__half> {
+    using W = __half2;
+    static __device__ __forceinline__ W low() { return __float2half2_rn(Usual<__half>::kLow); }
+    static __device__ __forceinline__ W larger(W a, W b) { return __hmax2(a, b); }
+    static __device__ __forceinline__ float largest(W a) { return fmaxf(__low2float(a), __high2float(a)); }
+};
+// Raises a vector, and gives the word of its largest logits.
+template <typename T> __device__ __forceinline__ typename Words<T>::W raise(uint4 &q) {
+    using F = Words<T>;
+    typename F::W *w = (typename F::W *)&q;
 #pragma unroll
-    for (int e = 0; e < 4; e++) v[e] = fmaxf(v[e], Usual<float>::kLow);
-    return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+    for (int e = 0; e < 4; e++) w[e] = F::larger(w[e], F::low());
+    return F::larger(F::larger(w[0], w[1]), F::larger(w[2], w[3]));
 }
-__device__ __forceinline__ float raise(uint4 &q, __nv_bfloat16) {
-    __nv_bfloat162 *h = (__nv_bfloat162 *)&q;
-    const __nv_bfloat162 low = __float2bfloat162_rn(Usual<__nv_bfloat16>::kLow);
-#pragma unroll
-    for (int e = 0; e < 4; e++) h[e] = __hmax2(h[e], low);
-    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-    return fmaxf(__low2float(m), __high2float(m));
-}
-__device__ __forceinline__ float raise(uint4 &q, __half) {
-    __half2 *h = (__half2 *)&q;
-    const __half2 low = __float2half2_rn(Usual<__half>::kLow);
-#pragma unroll
-    for (int e = 0; e < 4; e++) h[e] = __hmax2(h[e], low);
-    const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-    return fmaxf(__low2float(m), __high2float(m));
-}
+
 // kSize vectors a thread, of the CTA's share of a row.
 template <typename T, int kSize> struct Tile {
     static constexpr uint32_t kVecs = kSize * kRowThreads;
     uint4 q[kSize];
 
+    // Raises the tile; gives its largest logit, and each vector's largest word.
+    __device__ __forceinline__ float raise_all(typename Words<T>::W (&each)[kSize]) {
+        typename Words<T>::W m = each[0] = raise<T>(q[0]);
+#pragma unroll
+        for (int u = 1; u < kSize; u++) m = Words<T>::larger(m, each[u] = raise<T>(q[u]));
+        return Words<T>::largest(m);
+    }
+    __device__ __forceinline__ float raise_all() {
+        typename Words<T>::W each[kSize];
+        return raise_all(each);
+    }
     __device__ __forceinline__ static uint32_t place(uint32_t i0, int u) { return i0 + u * kRowThreads + threadIdx.x; }
     // No vector from i0 on ends outside the row or the share.
     __device__ __forceinline__ static bool inside(const RowView<T> &row, uint32_t i0, uint32_t hi) {
@@ -252,25 +269,29 @@ template <typename T, int kSize> struct Tile {
 };
 
 // The CTA's share of a row on its way through shared memory, kAhead tiles ahead of where it is read.  Every thread copies
-// (asynchronously, without registers) what it will read itself, so that no barrier is needed.  With as many slots as tiles
-// all of the share stays for a second look.
+// (asynchronously, without registers) what it will read itself, so that no barrier is needed.  A share that is kept has a
+// slot for every tile, and stays for a second look.
 template <typename T, int kSize> struct Feed {
     using Tiles = Tile<T, kSize>;
     static constexpr int kAhead = 2;
     const RowView<T> &row;
     uint4 *mine;               // this thread's place in the first slot
-    uint32_t lo, hi, slots;
+    uint32_t lo, hi;
+    bool kept;
 
-    __device__ __forceinline__ Feed(const RowView<T> &r, void *shared, uint32_t lo_, uint32_t hi_, uint32_t slots_)
-        : row(r), mine((uint4 *)shared + threadIdx.x), lo(lo_), hi(hi_), slots(slots_) {
+    __device__ __forceinline__ Feed(const RowView<T> &r, void *shared, uint32_t lo_, uint32_t hi_, bool kept_ = false, bool reads = true)
+        : row(r), mine((uint4 *)shared + threadIdx.x), lo(lo_), hi(hi_), kept(kept_) {
+        if (reads) {
 #pragma unroll
-        for (int n = 0; n < kAhead; n++) ask(n);
+            for (int n = 0; n < kAhead; n++) ask(n);
+        }
     }
+    __device__ __forceinline__ uint4 *slot(uint32_t n) const { return mine + (kept ? n : n % kAhead) * Tiles::kVecs; }
     // tile n's copies, as one group (an empty one behind the share, but for its first)
     __device__ __forceinline__ void ask(uint32_t n) const {
         const uint32_t i0 = lo + n * Tiles::kVecs;
         if (i0 < hi || n == 0) {
-            uint4 *const to = mine + n % slots * Tiles::kVecs;
+            uint4 *const to = slot(n);
             const bool inside = Tiles::inside(row, i0, hi);
 #pragma unroll
             for (int u = 0; u < kSize; u++) {
@@ -292,31 +313,31 @@ template <typename T, int kSize> struct Feed {
     }
     // a tile that is still there
     __device__ __forceinline__ void again(Tiles &t, uint32_t n) const {
-        const uint4 *const from = mine + n % slots * Tiles::kVecs;
+        const uint4 *const from = slot(n);
 #pragma unroll
         for (int u = 0; u < kSize; u++) t.q[u] = from[u * kRowThreads];
     }
 };
 
+// A thread's sums, relative to 2^r.  r follows the largest logit only where that is 2^kSlack above it: larger numbers lose
+// nothing, and a row's first tile is hardly ever so far below its others.
 template <typename T, bool kEntropy> struct Running {
-    float most, r;      // the largest logit, and it times c log2 e
+    static constexpr float kSlack = 64.0f;
+    float most, r;      // the largest logit; what the sums are relative to
     Pair s, sz;
 
     __device__ __forceinline__ explicit Running(float c2) : most(Usual<T>::kLow), r(__fmul_rn(Usual<T>::kLow, c2)), s(0, 0), sz(0, 0) {}
-    // Relative to `m` instead, which is no less.
-    __device__ __forceinline__ void move(float m, float c2) {
-        const float to = __fmul_rn(m, c2), d = r - to, f = exp2_of(d);
+    __device__ __forceinline__ void move(float to) {   // no less than r
+        const float d = r - to, f = exp2_of(d);
         if (kEntropy) sz = mul2(fma2(s, Pair(d, d), sz), Pair(f, f));
         s = mul2(s, Pair(f, f));
-        most = m, r = to;
+        r = to;
     }
-    // Raises the tile and adds it; gives its largest logit, and each vector's.
-    template <int kSize> __device__ __forceinline__ float add(Tile<T, kSize> &t, float c2, float (&each)[kSize]) {
+    // Adds a raised tile whose largest logit is m.
+    template <int kSize> __device__ __forceinline__ void add(const Tile<T, kSize> &t, float m, float c2) {
         constexpr int kVec = RowView<T>::kVec;
-        float m = each[0] = raise(t.q[0], T());
-#pragma unroll
-        for (int u = 1; u < kSize; u++) m = fmaxf(m, each[u] = raise(t.q[u], T()));
-        if (m > most) move(m, c2);
+        most = fmaxf(most, m);
+        if (fmaf(m, c2, -r) > kSlack) move(__fmul_rn(m, c2));
         const Pair k(c2, c2), off(-r, -r);
 #pragma unroll
         for (int u = 0; u < kSize; u++) {
@@ -331,7 +352,6 @@ template <typename T, bool kEntropy> struct Running {
                 if (kEntropy) sz = fma2(w, z, sz);
             }
         }
-        return m;
     }
 };
 
@@ -373,9 +393,19 @@ template <bool kTeam> struct Team {
         else
             asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
-    // Before the first exchange: a CTA's shared memory is there for the others once it runs.
-    __device__ __forceinline__ void begin() const {
-        if (kTeam) sync();
+    // A CTA's shared memory is there for the others once it runs, and until it ends: the first exchange comes after the one
+    // barrier's wait, the end after the other's.  Neither orders memory.
+    __device__ __forceinline__ void arrive() const {
+        if (kTeam) {
+            __syncwarp();
+            asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+        }
+    }
+    __device__ __forceinline__ void wait() const {
+        if (kTeam) {
+            __syncwarp();
+            asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        }
     }
     // One value of each CTA to all: S.slot[turn][r] is CTA r's.  The slots of one exchange are written again two exchanges
     // later, when a barrier has shown that all have read them.
@@ -387,7 +417,7 @@ template <bool kTeam> struct Team {
     // The warps' values combined in the order of warps and CTAs; every thread gets the result.
     template <typename F> __device__ __forceinline__ float4 across(float4 v, F f) {
         __syncthreads();
-        if (lane == 0) S.red[warp] = v;
+        if (lane == 0 && warp < kRowWarps) S.red[warp] = v;
         __syncthreads();
         v = S.red[0];
 #pragma unroll
@@ -416,7 +446,7 @@ template <bool kTeam> struct Team {
 struct Softmax { float m, s, sz; };
 struct SoftmaxAny { Softmax all; int turn; };
 
-// Sums relative to the largest m of eight lanes' out of each lane's own, added up.
+// Sums relative to the largest m c2 of eight lanes' out of each lane's own, added up.
 template <bool kEntropy> __device__ __forceinline__ float4 join_eight(float4 v, float c2) {
     float m = v.x;
 #pragma unroll
@@ -438,7 +468,7 @@ template <typename T, bool kEntropy, bool kTeam>
 __device__ __forceinline__ Softmax softmax_join(Team<kTeam> &team, Running<T, kEntropy> a, float c2, float &count) {
     static_assert(kRowWarps == 8 && kMaxTeam == 8, "eight lanes for either");
     const float m = key_value(__reduce_max_sync(kFull, key_of(a.most)));
-    a.move(m, c2);
+    a.move(__fmul_rn(m, c2));
     const float2 s = a.s.both(), sz = a.sz.both();
     float4 v = make_float4(m, s.x + s.y, sz.x + sz.y, team.warp == 0 ? count : 0.0f);
 #pragma unroll
@@ -446,10 +476,11 @@ __device__ __forceinline__ Softmax softmax_join(Team<kTeam> &team, Running<T, kE
         v.y += __shfl_xor_sync(kFull, v.y, d);
         if (kEntropy) v.z += __shfl_xor_sync(kFull, v.z, d);
     }
-    if (team.lane == 0) team.S.red[team.warp] = v;
+    if (team.lane == 0 && team.warp < kRowWarps) team.S.red[team.warp] = v;
     __syncthreads();
     v = join_eight<kEntropy>(team.S.red[team.lane & 7], c2);
     if (kTeam) {
+        team.wait();   // the others run
         team.exchange(v);
         const uint32_t o = team.lane & 7;
         v = o < team.size ? team.S.slot[team.turn][o] : make_float4(Usual<T>::kLow, 0, 0, 0);
@@ -461,11 +492,13 @@ __device__ __forceinline__ Softmax softmax_join(Team<kTeam> &team, Running<T, kE
     return {v.x, v.y * f, (v.z - d * v.y) * f * kLn2};
 }
 
-// Both in their general form: any logits and any c, two passes.  `load(i)` gives vector i.  (By value, and the team's turn
+// Both in their general form: any logits and any c, two passes.  `load(i)` gives vector i; threads beyond the row's own add
+// nothing.  (By value, and the team's turn
 // given back: what a function that is called takes by reference lives in memory, in the usual rows' loops too.)
 template <typename T, bool kTeam, typename L>
 __device__ __noinline__ SoftmaxAny softmax_sums(Team<kTeam> team, uint32_t lo, uint32_t hi, float c, L load) {
     constexpr int kVec = RowView<T>::kVec;
+    if (threadIdx.x >= kRowThreads) lo = hi;
     float m = -INFINITY;
     for (uint32_t i = lo + threadIdx.x; i < hi; i += kRowThreads) {
         float v[kVec];
@@ -505,12 +538,12 @@ inline uint32_t row_team(uint32_t n_rows, uint32_t bytes, uint32_t sms) {
 
 // A kernel with a CTA, or a cluster of them, for each row.
 template <typename K, typename P, typename... More>
-inline int launch_rows(bpe_ctx *ctx, const char *what, K kernel, const P &params, uint32_t n_rows, uint32_t team, bool cluster,
-                       size_t shared, More... more) {
+inline int launch_rows(bpe_ctx *ctx, const char *what, K kernel, const P &params, uint32_t n_rows, uint32_t team, int threads,
+                       bool cluster, size_t shared, More... more) {
     if ((uint64_t)n_rows * team > 0x7FFFFFFFu) return fail(ctx, BPE_ERR_INVALID_ARG, "%s: %u rows", what, n_rows);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(n_rows * team);
-    cfg.blockDim = dim3(kRowThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = shared;
     cfg.stream = ctx->stream;
     cudaLaunchAttribute attr[1];

@@ -6,7 +6,8 @@ namespace bpe {
 namespace {
 
 constexpr int kTop = (int)BPE_HEAD_MAX_TOP;
-constexpr int kList = 1024;                // tokens that may be among the alternatives
+constexpr int kFound = 512;                // vectors that may hold alternatives
+constexpr int kList = 1024;                // tokens that may be among them
 
 constexpr int kSize = 4;                   // vectors of a thread at a time
 constexpr size_t kFeedBytes = (size_t)Feed<float, kSize>::kAhead * kSize * kRowThreads * 16;
@@ -24,19 +25,22 @@ struct ScoreParams {
 
 struct ScoreShared {
     TeamShared team;
-    uint32_t list_n, scan[kRowWarps];
-    u64 list[kList];                       // key of the logit, then the id from above, so that the larger comes first
+    uint32_t list_n, early_n, found_n[2], scan[kRowWarps];
     u64 best[kTop];                        // in order
     float bound[kRowWarps];
+    uint4 found[kFound];                   // vectors that may hold alternatives,
+    uint32_t found_at[kFound];             // and their places
+    u64 early[kList];                      // tokens out of earlier ones
 };
-static_assert(kTop <= kRowThreads && kMaxTeam * kTop <= kList, "one thread for each alternative, room for a team's");
+static_assert(kTop <= kRowThreads && kMaxTeam * kTop <= kList && kList * sizeof(u64) <= kFeedBytes,
+              "one thread for each alternative, room for a team's");
 
 __device__ __forceinline__ u64 entry_of(uint32_t key, uint32_t id) { return (u64)key << 32 | (uint32_t)~id; }
 
-// The alternatives in S.list, at most k of this CTA's, for any logits: the key of the k-th largest is found by bits, two
+// The alternatives in `list`, at most k of this CTA's, for any logits: the key of the k-th largest is found by bits, two
 // a pass; those above it are listed, and as many of its equals, in order of ids, as there is room for.  Gives the team's turn.
 template <typename T, bool kTeam>
-__device__ __noinline__ int list_any(ScoreShared &S, Team<kTeam> team, RowView<T> row, uint32_t lo, uint32_t hi, uint32_t k) {
+__device__ __noinline__ int list_any(ScoreShared &S, u64 *list, Team<kTeam> team, RowView<T> row, uint32_t lo, uint32_t hi, uint32_t k) {
     constexpr int kVec = RowView<T>::kVec, kShift = Bits<T>::kShift, kBits = (32 - kShift + 1) & ~1;
     uint32_t some = 0;
     for (uint32_t i = lo + threadIdx.x; i < hi; i += kRowThreads) {
@@ -72,7 +76,7 @@ __device__ __noinline__ int list_any(ScoreShared &S, Team<kTeam> team, RowView<T
 #pragma unroll
         for (int e = 0; e < kVec; e++) {
             const uint32_t key = key_of(v[e]);
-            if (key >> kShift > cut) S.list[atomicAdd(&S.list_n, 1)] = entry_of(key, i * kVec + e - row.shift), above++;   // fewer than k
+            if (key >> kShift > cut) list[atomicAdd(&S.list_n, 1)] = entry_of(key, i * kVec + e - row.shift), above++;   // fewer than k
             equal += key >> kShift == cut;
         }
     }
@@ -109,7 +113,7 @@ __device__ __noinline__ int list_any(ScoreShared &S, Team<kTeam> team, RowView<T
 #pragma unroll
             for (int e = 0; e < kVec; e++)
                 if (key_of(v[e]) >> kShift == cut && at++ < quota)
-                    S.list[atomicAdd(&S.list_n, 1)] = entry_of(key_of(v[e]), i * kVec + e - row.shift);
+                    list[atomicAdd(&S.list_n, 1)] = entry_of(key_of(v[e]), i * kVec + e - row.shift);
         }
     }
     __syncthreads();
@@ -117,13 +121,13 @@ __device__ __noinline__ int list_any(ScoreShared &S, Team<kTeam> team, RowView<T
 }
 
 // The list's k largest in order, in S.best: each entry's place is the number of larger ones, counted by four threads.
-__device__ __forceinline__ uint32_t rank_list(ScoreShared &S, uint32_t k) {
+__device__ __forceinline__ uint32_t rank_list(ScoreShared &S, const u64 *list, uint32_t k) {
     const uint32_t n = S.list_n, part = threadIdx.x & 3;
     for (uint32_t i0 = 0; i0 < n; i0 += kRowThreads / 4) {
         const uint32_t i = i0 + threadIdx.x / 4;
-        const u64 one = S.list[min(i, n - 1)];
+        const u64 one = list[min(i, n - 1)];
         uint32_t place = 0;
-        for (uint32_t j = part; j < n; j += 4) place += S.list[j] > one;
+        for (uint32_t j = part; j < n; j += 4) place += list[j] > one;
         place += __shfl_xor_sync(kFull, place, 1);
         place += __shfl_xor_sync(kFull, place, 2);
         if (i < n && part == 0 && place < k) S.best[place] = one;
@@ -143,15 +147,24 @@ struct Bound {
         if (warps) j = (k + warps - 1) / warps;
         if (j > 32) warps = 0;
     }
-    __device__ __forceinline__ float read(const ScoreShared &S, float low) const {
+    __device__ __forceinline__ float least(const ScoreShared &S, float low) const {
         if (!warps) return low;
         float b = INFINITY;
         for (uint32_t w = 0; w < warps; w++) b = fminf(b, *(const volatile float *)&S.bound[w]);
         return b;
     }
-    // this warp's, from its lanes' largest logits
+    // this warp's, from its lanes' largest logits: by taking out the largest where few are asked for, by sorting else
     __device__ __forceinline__ void write(ScoreShared &S, float v, int lane, int warp) const {
         if (warp >= (int)warps) return;
+        if (j <= 8) {
+            uint32_t key = key_of(v), top = 0;
+            for (uint32_t i = 0; i < j; i++) {
+                top = __reduce_max_sync(kFull, key);
+                if (lane == __ffs(__ballot_sync(kFull, key == top)) - 1) key = 0;
+            }
+            if (lane == 0) *(volatile float *)&S.bound[warp] = key_value(top);
+            return;
+        }
 #pragma unroll
         for (int size = 2; size <= 32; size <<= 1)
 #pragma unroll
@@ -164,58 +177,44 @@ struct Bound {
     }
 };
 
-// The tile's logits that may be among the alternatives, vector by vector that holds one: its elements go to as many lanes,
-// since hardly ever more than one or two lanes of a warp have any.
+// The tile's vectors that hold a logit at or above the bound: as they are, since few of them turn out to matter.
 template <typename T, int kSize>
-__device__ __forceinline__ void list_tile(ScoreShared &S, const Tile<T, kSize> &t, const float (&each)[kSize], const RowView<T> &row,
-                                          uint32_t i0, float bound, int lane) {
-    constexpr int kVec = RowView<T>::kVec;
+__device__ __forceinline__ void find(ScoreShared &S, uint32_t &found_n, const Tile<T, kSize> &t, const typename Words<T>::W (&each)[kSize],
+                                     uint32_t i0, float bound) {
 #pragma unroll
     for (int u = 0; u < kSize; u++) {
-        unsigned left = __ballot_sync(kFull, each[u] >= bound && each[u] > Usual<T>::kLow);
-        while (left) {
-            const int from = __ffs(left) - 1;
-            left &= left - 1;
-            const uint32_t word = lane / (4 / sizeof(T)) % 4;
-            const uint32_t x = __shfl_sync(kFull, t.q[u].x, from), y = __shfl_sync(kFull, t.q[u].y, from);
-            const uint32_t z = __shfl_sync(kFull, t.q[u].z, from), w = __shfl_sync(kFull, t.q[u].w, from);
-            const uint4 same = make_uint4(word & 2 ? word & 1 ? w : z : word & 1 ? y : x, 0, 0, 0);
-            float v[kVec];
-            unpack(same, v, T());
-            const float mine = sizeof(T) == 2 && lane & 1 ? v[1] : v[0];
-            if (lane < kVec && mine >= bound && mine > Usual<T>::kLow) {
-                const uint32_t at = atomicAdd(&S.list_n, 1);
-                if (at < kList) S.list[at] = entry_of(key_of(mine), (t.place(i0, u) - lane + from) * kVec + lane - row.shift);
-            }
+        const float m = Words<T>::largest(each[u]);
+        if (m >= bound && m > Usual<T>::kLow) {
+            const uint32_t at = atomicAdd(&found_n, 1);
+            if (at < kFound) S.found[at] = t.q[u], S.found_at[at] = t.place(i0, u);
         }
     }
 }
 
-// What of the list is at or above the bound, moved to its front.
-__device__ __forceinline__ void trim_list(ScoreShared &S, float bound) {
-    const uint32_t n = min(S.list_n, (uint32_t)kList);
-    u64 mine[kList / kRowThreads];
+// Their logits at or above the bound, which has risen since, to a list.
+template <typename T>
+__device__ __forceinline__ void list_found(const ScoreShared &S, uint32_t found_n, u64 *list, uint32_t &list_n, const RowView<T> &row, float bound) {
+    constexpr int kVec = RowView<T>::kVec;
+    for (uint32_t i = threadIdx.x; i < min(found_n, (uint32_t)kFound); i += kRowThreads) {
+        float v[kVec];
+        unpack(S.found[i], v, T());
+        const uint32_t id = S.found_at[i] * kVec - row.shift;
 #pragma unroll
-    for (int i = 0; i < kList / kRowThreads; i++) {
-        const uint32_t at = i * kRowThreads + threadIdx.x;
-        mine[i] = at < n ? S.list[at] : 0;
+        for (int e = 0; e < kVec; e++)
+            if (v[e] >= bound && v[e] > Usual<T>::kLow) {
+                const uint32_t at = atomicAdd(&list_n, 1);
+                if (at < kList) list[at] = entry_of(key_of(v[e]), id + e);
+            }
     }
-    __syncthreads();
-    if (threadIdx.x == 0) S.list_n = 0;
-    __syncthreads();
-    const u64 least = (u64)key_of(bound) << 32;
-#pragma unroll
-    for (int i = 0; i < kList / kRowThreads; i++)
-        if (mine[i] && mine[i] >= least) S.list[atomicAdd(&S.list_n, 1)] = mine[i];
-    __syncthreads();
 }
 
 template <typename T, bool kTeam, bool kTops>
 __global__ void __launch_bounds__(kRowThreads, 4) k_logprobs(ScoreParams P, uint32_t n_team) {
     using Tiles = Tile<T, kSize>;
-    __shared__ ScoreShared S;
+    extern __shared__ __align__(16) unsigned char tiles[];
+    ScoreShared &S = *(ScoreShared *)(tiles + kFeedBytes);   // without alternatives the team's part alone
     Team<kTeam> team(S.team, n_team);
-    team.begin();
+    team.arrive();
     const uint32_t r = kTeam ? blockIdx.x / n_team : blockIdx.x;
     const RowView<T> row(P.row.logits, P.row.stride, r, P.row.n_tok);
     const uint32_t vecs = row.vecs(), share = (vecs + team.size - 1) / team.size;
@@ -229,42 +228,64 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_logprobs(ScoreParams P, uint
         if (id >= 0 && (uint32_t)id < P.row.n_tok) given = to_f32(row.at[row.shift + id]);
     }
 
-    extern __shared__ __align__(16) unsigned char tiles[];
-    const Feed<T, kSize> feed(row, tiles, lo, hi, Feed<T, kSize>::kAhead);
+    const Feed<T, kSize> feed(row, tiles, lo, hi);
     Running<T, true> sums(c2);
     const Bound tops(hi - lo, k);
+    float count = 0.0f;
+    u64 *const list = (u64 *)tiles;        // once the tiles are through
     if (kTops) {
-        if (threadIdx.x == 0) S.list_n = 0;
-        for (uint32_t n = 0, i0 = lo; i0 < hi || n == 0; i0 += Tiles::kVecs, n++) {
+        if (threadIdx.x == 0) S.list_n = S.early_n = S.found_n[0] = 0;
+        uint32_t n = 0, phase = 0;
+        bool stale = true, over = false;
+        float bound = Usual<T>::kLow;
+        const uint32_t flush = k > 32 ? 3 : 7;
+        for (uint32_t i0 = lo; i0 < hi || n == 0; i0 += Tiles::kVecs, n++) {
             Tiles t;
-            float each[kSize];
+            typename Words<T>::W each[kSize];
             feed.next(t, n);
-            const float m = sums.add(t, c2, each);
-            if ((n & (n + 1)) == 0) tops.write(S, sums.most, team.lane, team.warp);   // after 1, 2, 4... tiles
+            const float m = t.raise_all(each);
+            sums.add(t, m, c2);
+            stale = (n & (n + 1)) != 0;    // after 1, 2, 4... tiles
+            if (!stale) tops.write(S, sums.most, team.lane, team.warp);
             if (n == 0) __syncthreads();
-            const float bound = tops.read(S, Usual<T>::kLow);
-            if (__any_sync(kFull, m >= bound)) list_tile(S, t, each, row, i0, bound, team.lane);
+            if (!stale) bound = tops.least(S, Usual<T>::kLow);
+            if (m >= bound && m > Usual<T>::kLow) find(S, S.found_n[phase], t, each, i0, bound);
+            // Room for the next tiles' vectors: some hundred have come by then, of which the bound by now leaves few.
+            if ((n & flush) == flush || (n == 1 && flush == 3)) {
+                __syncthreads();
+                over |= S.found_n[phase] > kFound;
+                bound = tops.least(S, Usual<T>::kLow);
+                list_found(S, S.found_n[phase], S.early, S.early_n, row, bound);
+                phase ^= 1;
+                if (threadIdx.x == 0) S.found_n[phase] = 0;
+                __syncthreads();
+            }
         }
-        tops.write(S, sums.most, team.lane, team.warp);
+        if (stale) tops.write(S, sums.most, team.lane, team.warp);
         __syncthreads();
+        bound = tops.least(S, Usual<T>::kLow);
+        list_found(S, S.found_n[phase], list, S.list_n, row, bound);
+        const u64 least = (u64)key_of(bound) << 32;
+        for (uint32_t i = threadIdx.x; i < min(S.early_n, (uint32_t)kList); i += kRowThreads)
+            if (S.early[i] >= least) {
+                const uint32_t at = atomicAdd(&S.list_n, 1);
+                if (at < kList) list[at] = S.early[i];
+            }
+        __syncthreads();
+        over |= S.found_n[phase] > kFound || S.early_n > kList || S.list_n > kList;
+        count = over ? -0x1p24f : fminf((float)S.list_n, (float)k);
     } else {
         for (uint32_t n = 0, i0 = lo; i0 < hi; i0 += Tiles::kVecs, n++) {
             Tiles t;
-            float each[kSize];
             feed.next(t, n);
-            sums.add(t, c2, each);
+            sums.add(t, t.raise_all(), c2);
         }
     }
-    float count = 0.0f;
-    if (kTops) {
-        const bool over = S.list_n > kList;
-        trim_list(S, tops.read(S, Usual<T>::kLow));
-        count = over ? -0x1p24f : fminf((float)S.list_n, (float)k);
-    }
     Softmax all = softmax_join(team, sums, c2, count);
+    if (!kTeam && !kTops && team.warp > 0 && usual<T>(all.m, c)) return;
     if (!usual<T>(all.m, c)) all = softmax_any<T, kTeam>(team, lo, hi, c, [=](uint32_t i) { return row.load(i); });
     // more equal or masked logits than the list holds, or fewer others than were asked for
-    if (kTops && count < (float)min(k, P.row.n_tok)) team.turn = list_any<T, kTeam>(S, team, row, lo, hi, k);
+    if (kTops && count < (float)min(k, P.row.n_tok)) team.turn = list_any<T, kTeam>(S, list, team, row, lo, hi, k);
 
     const bool none = all.m == -INFINITY;
     const float log_s = none ? 0.0f : logf(all.s);
@@ -274,7 +295,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_logprobs(ScoreParams P, uint
         if (P.logprob) P.logprob[r] = id < 0 || (uint32_t)id >= P.row.n_tok ? 0.0f : none ? -INFINITY : z_any(given, all.m, c) - log_s;
     }
     if (!kTops) return;
-    uint32_t n = rank_list(S, k), total = n;
+    uint32_t n = rank_list(S, list, k), total = n;
     const u64 one = S.best[min(threadIdx.x, k - 1)];   // this thread's, of the n
     uint32_t place = threadIdx.x;
     if (kTeam) {
@@ -282,10 +303,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_logprobs(ScoreParams P, uint
         total = 0;
         for (uint32_t o = 0; o < team.size; o++) total += (uint32_t)team.S.slot[team.turn][o].x;
         // every CTA's list, then each of its own finds its place by those that are larger
-        for (uint32_t i = threadIdx.x; i < team.size * k; i += kRowThreads) {
-            const uint32_t o = i / k;
-            if (o != team.rank && i % k < (uint32_t)team.S.slot[team.turn][o].x) S.list[i] = far_load(&S.best[i % k], o);
-        }
+        for (uint32_t o = 0; o < team.size; o++)
+            if (o != team.rank && threadIdx.x < (uint32_t)team.S.slot[team.turn][o].x) list[o * k + threadIdx.x] = far_load(&S.best[threadIdx.x], o);
         __syncthreads();
         if (threadIdx.x < n)
             for (uint32_t o = 0; o < team.size; o++) {
@@ -293,7 +312,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_logprobs(ScoreParams P, uint
                 uint32_t x = 0, y = (uint32_t)team.S.slot[team.turn][o].x;
                 while (x < y) {
                     const uint32_t mid = (x + y) / 2;
-                    if (S.list[o * k + mid] > one) x = mid + 1;
+                    if (list[o * k + mid] > one) x = mid + 1;
                     else y = mid;
                 }
                 place += x;
@@ -309,7 +328,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_logprobs(ScoreParams P, uint
         if (P.top_ids) P.top_ids[at] = -1;
         if (P.top_logprob) P.top_logprob[at] = -INFINITY;
     }
-    if (kTeam) team.sync();   // until the others have read this CTA's list
+    team.arrive();
+    team.wait();   // the others have read this CTA's list
 }
 
 // ----------------------------------------------------------- gradient ---
@@ -331,7 +351,7 @@ __global__ void __launch_bounds__(kRowThreads) k_logprobs_backward(ScoreGradPara
     const RowView<T> row(P.row.logits, P.row.stride, r, P.row.n_tok), out(P.out, P.out_stride, r, P.row.n_tok);
     const uint32_t lo = cut * each * Tiles::kVecs, hi = min(row.vecs(), lo + each * Tiles::kVecs);
     if (lo >= hi) return;
-    const Feed<T, kSize> feed(row, tiles, lo, hi, Feed<T, kSize>::kAhead);
+    const Feed<T, kSize> feed(row, tiles, lo, hi);
     const float c = P.row.inverse(r);
     const float m = P.norm[2 * (uint64_t)r], log_s = P.norm[2 * (uint64_t)r + 1];
     const int32_t id = P.ids ? P.ids[r] : -1;
@@ -355,7 +375,7 @@ __global__ void __launch_bounds__(kRowThreads) k_logprobs_backward(ScoreGradPara
             if (i >= hi) break;
             float v[kVec];
             if (fast) {
-                raise(t.q[u], T());
+                raise<T>(t.q[u]);
                 unpack(t.q[u], v, T());
 #pragma unroll
                 for (int e = 0; e < kVec; e += 2) {
@@ -382,7 +402,11 @@ __global__ void __launch_bounds__(kRowThreads) k_logprobs_backward(ScoreGradPara
 }
 
 template <typename T, bool kTeam, bool kTops> int launch_team(bpe_ctx *ctx, const ScoreParams &P, uint32_t n_rows, uint32_t team) {
-    return launch_rows(ctx, "head_logprobs launch", k_logprobs<T, kTeam, kTops>, P, n_rows, team, kTeam, kFeedBytes);
+    auto k = k_logprobs<T, kTeam, kTops>;
+    constexpr size_t kShared = kFeedBytes + (kTops ? sizeof(ScoreShared) : sizeof(TeamShared));
+    static std::atomic<uint64_t> devices{0};
+    BPE_CUDA(ctx, allow_shared(k, ctx->device, kShared, devices), "head_logprobs");
+    return launch_rows(ctx, "head_logprobs launch", k, P, n_rows, team, kRowThreads, kTeam, kShared);
 }
 
 template <typename T> int launch_logprobs(bpe_ctx *ctx, const ScoreParams &P, uint32_t n_rows) {
