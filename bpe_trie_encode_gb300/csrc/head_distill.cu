@@ -162,9 +162,12 @@ template <typename T> __device__ __forceinline__ uint32_t vector_bits(const uint
 // A vector with -infinity in the elements that `some` has bits for.
 template <typename T> __device__ __forceinline__ uint4 without(uint4 q, uint32_t some) {
     constexpr uint32_t k = Bits<T>::kNegInf;
+    // 16 bits: this has bit 0 at 7 and bit 1 at 15, of which prmt makes bytes (8 and 9: the sign of byte 0 or 1), and shifted
+    // right by 2 the next two
+    const uint32_t spread = some << 7 | some << 14;
     auto word = [=](uint32_t w, int i) {
-        const uint32_t mask = sizeof(T) == 4 ? (some >> i & 1 ? ~0u : 0u)
-                                             : (some >> 2 * i & 1 ? 0xFFFFu : 0u) | (some >> 2 * i & 2 ? 0xFFFF0000u : 0u);
+        uint32_t mask = (uint32_t)((int32_t)(some << (31 - i)) >> 31);
+        if (sizeof(T) == 2) asm("prmt.b32 %0, %1, 0, 0x9988;" : "=r"(mask) : "r"(spread >> 2 * i));
         return (w & ~mask) | (k & mask);
     };
     return make_uint4(word(q.x, 0), word(q.y, 1), word(q.z, 2), word(q.w, 3));
@@ -262,10 +265,11 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill(DistillParams P, uint32
         Tiles t;
         if (kept) feed.again(t, n);
         else t.load(row, i0, hi);
+        const bool direct = out.shift == row.shift && Tiles::inside(row, i0, hi);
 #pragma unroll
         for (int u = 0; u < kSize; u++) {
             const uint32_t i = t.place(i0, u);
-            if (i >= hi) break;
+            if (!direct && i >= hi) break;
             float v[kVec];
             if (fast) {
                 raise<T>(t.q[u]);
@@ -281,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill(DistillParams P, uint32
 #pragma unroll
                 for (int e = 0; e < kVec; e++) v[e] = of_free == 0.0f ? 0.0f : expf(z_any(v[e], free.m, c)) * of_free;
             }
-            put_vector(out, row, i, v);
+            put_vector(out, row, i, v, direct);
         }
     }
     __syncthreads();

@@ -103,7 +103,8 @@ template <typename T> struct RowView {
 };
 
 // Vector i of a gradient, in the place of the row's.  What is not a whole vector, or starts elsewhere in one than the row
-// does, goes element by element, in a function of its own: written out here, its stores take issue slots when they do not run.
+// does, goes element by element, in a function of its own: written out here, its stores take issue slots when they do not
+// run.  `direct`: known to be neither.
 template <typename T> __device__ __noinline__ void put_elements(RowView<T> out, RowView<T> row, uint32_t i, uint4 q) {
     const T *const v = (const T *)&q;
     constexpr uint32_t kVec = RowView<T>::kVec;
@@ -114,9 +115,9 @@ template <typename T> __device__ __noinline__ void put_elements(RowView<T> out, 
     }
 }
 template <typename T>
-__device__ __forceinline__ void put_vector(const RowView<T> &out, const RowView<T> &row, uint32_t i, const float (&v)[RowView<T>::kVec]) {
+__device__ __forceinline__ void put_vector(const RowView<T> &out, const RowView<T> &row, uint32_t i, const float (&v)[RowView<T>::kVec], bool direct) {
     const uint4 q = pack16(v, T());
-    if (out.shift == row.shift && row.whole(i)) *((uint4 *)out.at + i) = q;
+    if (direct || (out.shift == row.shift && row.whole(i))) *((uint4 *)out.at + i) = q;
     else put_elements(out, row, i, q);
 }
 
@@ -274,36 +275,48 @@ template <typename T, int kSize> struct Tile {
 template <typename T, int kSize> struct Feed {
     using Tiles = Tile<T, kSize>;
     static constexpr int kAhead = 2;
-    const RowView<T> &row;
-    uint4 *mine;               // this thread's place in the first slot
+    static constexpr uint32_t kBytes = Tiles::kVecs * 16, kStep = kRowThreads * 16;   // of a tile, from a thread's vector to its next
+    RowView<T> row;
+    const char *from;          // this thread's first vector
+    uint32_t mine;             // its place in the first slot, an address of 32 bits
     uint32_t lo, hi;
     bool kept;
 
     __device__ __forceinline__ Feed(const RowView<T> &r, void *shared, uint32_t lo_, uint32_t hi_, bool kept_ = false, bool reads = true)
-        : row(r), mine((uint4 *)shared + threadIdx.x), lo(lo_), hi(hi_), kept(kept_) {
+        : row(r), from((const char *)r.at + (uint64_t)(lo_ + threadIdx.x) * 16),
+          mine((uint32_t)__cvta_generic_to_shared(shared) + threadIdx.x * 16), lo(lo_), hi(hi_), kept(kept_) {
         if (reads) {
 #pragma unroll
             for (int n = 0; n < kAhead; n++) ask(n);
         }
     }
-    __device__ __forceinline__ uint4 *slot(uint32_t n) const { return mine + (kept ? n : n % kAhead) * Tiles::kVecs; }
+    __device__ __forceinline__ uint32_t slot(uint32_t n) const { return mine + (kept ? n : n % kAhead) * kBytes; }
+    static __device__ __forceinline__ void copy(uint32_t to, const void *from) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    }
     // tile n's copies, as one group (an empty one behind the share, but for its first)
     __device__ __forceinline__ void ask(uint32_t n) const {
         const uint32_t i0 = lo + n * Tiles::kVecs;
-        if (i0 < hi || n == 0) {
-            uint4 *const to = slot(n);
-            const bool inside = Tiles::inside(row, i0, hi);
+        if (Tiles::inside(row, i0, hi)) {
+            const uint32_t to = slot(n);
+            const char *const f = from + (uint64_t)n * kBytes;
 #pragma unroll
-            for (int u = 0; u < kSize; u++) {
-                const uint32_t i = Tiles::place(i0, u);
-                if (inside || (i < hi && row.whole(i)))
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to + u * kRowThreads)),
-                                 "l"((const uint4 *)row.at + i) : "memory");
-                else
-                    to[u * kRowThreads] = i < hi ? row.load(i) : Tiles::fill();
-            }
+            for (int u = 0; u < kSize; u++) copy(to + u * kStep, f + u * kStep);
+        } else if (i0 < hi || n == 0) {
+            ask_edge(i0, slot(n));
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    __device__ __forceinline__ void ask_edge(uint32_t i0, uint32_t to) const {
+#pragma unroll 1
+        for (uint32_t i = i0 + threadIdx.x; i < i0 + Tiles::kVecs; i += kRowThreads, to += kStep) {
+            if (i < hi && row.whole(i)) {
+                copy(to, (const uint4 *)row.at + i);
+                continue;
+            }
+            const uint4 q = i < hi ? row.load(i) : Tiles::fill();
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w) : "memory");
+        }
     }
     // tile n, in order; then the copies of the one that takes its slot
     __device__ __forceinline__ void next(Tiles &t, uint32_t n) const {
@@ -313,9 +326,11 @@ template <typename T, int kSize> struct Feed {
     }
     // a tile that is still there
     __device__ __forceinline__ void again(Tiles &t, uint32_t n) const {
-        const uint4 *const from = slot(n);
+        const uint32_t at = slot(n);
 #pragma unroll
-        for (int u = 0; u < kSize; u++) t.q[u] = from[u * kRowThreads];
+        for (int u = 0; u < kSize; u++)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(t.q[u].x), "=r"(t.q[u].y), "=r"(t.q[u].z), "=r"(t.q[u].w)
+                         : "r"(at + u * kStep) : "memory");
     }
 };
 

@@ -6,7 +6,7 @@ namespace bpe {
 namespace {
 
 constexpr int kTop = (int)BPE_HEAD_MAX_TOP;
-constexpr int kFound = 512;                // vectors that may hold alternatives
+constexpr int kFound = 2048;               // vectors that may hold alternatives
 constexpr int kList = 1024;                // tokens that may be among them
 
 constexpr int kSize = 4;                   // vectors of a thread at a time
@@ -25,12 +25,10 @@ struct ScoreParams {
 
 struct ScoreShared {
     TeamShared team;
-    uint32_t list_n, early_n, found_n[2], scan[kRowWarps];
+    uint32_t list_n, found_n, scan[kRowWarps];
     u64 best[kTop];                        // in order
     float bound[kRowWarps];
-    uint4 found[kFound];                   // vectors that may hold alternatives,
-    uint32_t found_at[kFound];             // and their places
-    u64 early[kList];                      // tokens out of earlier ones
+    uint32_t found[kFound];                // vectors that may hold alternatives
 };
 static_assert(kTop <= kRowThreads && kMaxTeam * kTop <= kList && kList * sizeof(u64) <= kFeedBytes,
               "one thread for each alternative, room for a team's");
@@ -123,7 +121,7 @@ __device__ __noinline__ int list_any(ScoreShared &S, u64 *list, Team<kTeam> team
 // The list's k largest in order, in S.best: each entry's place is the number of larger ones, counted by four threads.
 __device__ __forceinline__ uint32_t rank_list(ScoreShared &S, const u64 *list, uint32_t k) {
     const uint32_t n = S.list_n, part = threadIdx.x & 3;
-    for (uint32_t i0 = 0; i0 < n; i0 += kRowThreads / 4) {
+    for (uint32_t i0 = 0; i0 + (threadIdx.x & ~31u) / 4 < n; i0 += kRowThreads / 4) {
         const uint32_t i = i0 + threadIdx.x / 4;
         const u64 one = list[min(i, n - 1)];
         uint32_t place = 0;
@@ -177,33 +175,36 @@ struct Bound {
     }
 };
 
-// The tile's vectors that hold a logit at or above the bound: as they are, since few of them turn out to matter.
+// The tile's vectors that hold a logit at or above the bound: their places, since few of them turn out to matter.
 template <typename T, int kSize>
-__device__ __forceinline__ void find(ScoreShared &S, uint32_t &found_n, const Tile<T, kSize> &t, const typename Words<T>::W (&each)[kSize],
-                                     uint32_t i0, float bound) {
+__device__ __forceinline__ void find(ScoreShared &S, const typename Words<T>::W (&each)[kSize], uint32_t i0, float bound) {
 #pragma unroll
     for (int u = 0; u < kSize; u++) {
         const float m = Words<T>::largest(each[u]);
         if (m >= bound && m > Usual<T>::kLow) {
-            const uint32_t at = atomicAdd(&found_n, 1);
-            if (at < kFound) S.found[at] = t.q[u], S.found_at[at] = t.place(i0, u);
+            const uint32_t at = atomicAdd(&S.found_n, 1);
+            if (at < kFound) S.found[at] = Tile<T, kSize>::place(i0, u);
         }
     }
 }
 
-// Their logits at or above the bound, which has risen since, to a list.
+// Their logits at or above the bound, which has risen since, to the list.  (Read once more: 32 bytes for each of them.)
 template <typename T>
-__device__ __forceinline__ void list_found(const ScoreShared &S, uint32_t found_n, u64 *list, uint32_t &list_n, const RowView<T> &row, float bound) {
+__device__ __forceinline__ void list_found(ScoreShared &S, u64 *list, const RowView<T> &row, float bound) {
     constexpr int kVec = RowView<T>::kVec;
-    for (uint32_t i = threadIdx.x; i < min(found_n, (uint32_t)kFound); i += kRowThreads) {
+    for (uint32_t i = threadIdx.x; i < min(S.found_n, (uint32_t)kFound); i += kRowThreads) {
+        const uint32_t place = S.found[i];
         float v[kVec];
-        unpack(S.found[i], v, T());
-        const uint32_t id = S.found_at[i] * kVec - row.shift;
+        unpack(row.load(place), v, T());
+        uint32_t some = 0;
+#pragma unroll
+        for (int e = 0; e < kVec; e++) some |= v[e] >= bound && v[e] > Usual<T>::kLow ? 1u << e : 0u;
+        uint32_t at = atomicAdd(&S.list_n, __popc(some));
 #pragma unroll
         for (int e = 0; e < kVec; e++)
-            if (v[e] >= bound && v[e] > Usual<T>::kLow) {
-                const uint32_t at = atomicAdd(&list_n, 1);
-                if (at < kList) list[at] = entry_of(key_of(v[e]), id + e);
+            if (some >> e & 1) {
+                if (at < kList) list[at] = entry_of(key_of(v[e]), place * kVec - row.shift + e);
+                at++;
             }
     }
 }
@@ -234,45 +235,28 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_logprobs(ScoreParams P, uint
     float count = 0.0f;
     u64 *const list = (u64 *)tiles;        // once the tiles are through
     if (kTops) {
-        if (threadIdx.x == 0) S.list_n = S.early_n = S.found_n[0] = 0;
-        uint32_t n = 0, phase = 0;
-        bool stale = true, over = false;
+        if (threadIdx.x == 0) S.list_n = S.found_n = 0;
+        bool stale = true;
         float bound = Usual<T>::kLow;
-        const uint32_t flush = k > 32 ? 3 : 7;
-        for (uint32_t i0 = lo; i0 < hi || n == 0; i0 += Tiles::kVecs, n++) {
+        for (uint32_t n = 0, i0 = lo; i0 < hi || n == 0; i0 += Tiles::kVecs, n++) {
             Tiles t;
             typename Words<T>::W each[kSize];
             feed.next(t, n);
             const float m = t.raise_all(each);
             sums.add(t, m, c2);
             stale = (n & (n + 1)) != 0;    // after 1, 2, 4... tiles
-            if (!stale) tops.write(S, sums.most, team.lane, team.warp);
-            if (n == 0) __syncthreads();
-            if (!stale) bound = tops.least(S, Usual<T>::kLow);
-            if (m >= bound && m > Usual<T>::kLow) find(S, S.found_n[phase], t, each, i0, bound);
-            // Room for the next tiles' vectors: some hundred have come by then, of which the bound by now leaves few.
-            if ((n & flush) == flush || (n == 1 && flush == 3)) {
-                __syncthreads();
-                over |= S.found_n[phase] > kFound;
+            if (!stale) {
+                tops.write(S, sums.most, team.lane, team.warp);
+                if (n == 0) __syncthreads();
                 bound = tops.least(S, Usual<T>::kLow);
-                list_found(S, S.found_n[phase], S.early, S.early_n, row, bound);
-                phase ^= 1;
-                if (threadIdx.x == 0) S.found_n[phase] = 0;
-                __syncthreads();
             }
+            if (m >= bound && m > Usual<T>::kLow) find<T, kSize>(S, each, i0, bound);
         }
         if (stale) tops.write(S, sums.most, team.lane, team.warp);
         __syncthreads();
-        bound = tops.least(S, Usual<T>::kLow);
-        list_found(S, S.found_n[phase], list, S.list_n, row, bound);
-        const u64 least = (u64)key_of(bound) << 32;
-        for (uint32_t i = threadIdx.x; i < min(S.early_n, (uint32_t)kList); i += kRowThreads)
-            if (S.early[i] >= least) {
-                const uint32_t at = atomicAdd(&S.list_n, 1);
-                if (at < kList) list[at] = S.early[i];
-            }
+        list_found(S, list, row, tops.least(S, Usual<T>::kLow));
         __syncthreads();
-        over |= S.found_n[phase] > kFound || S.early_n > kList || S.list_n > kList;
+        const bool over = S.found_n > kFound || S.list_n > kList;
         count = over ? -0x1p24f : fminf((float)S.list_n, (float)k);
     } else {
         for (uint32_t n = 0, i0 = lo; i0 < hi; i0 += Tiles::kVecs, n++) {
@@ -369,10 +353,11 @@ __global__ void __launch_bounds__(kRowThreads) k_logprobs_backward(ScoreGradPara
     for (uint32_t n = 0; n * Tiles::kVecs < hi - lo; n++) {
         Tiles t;
         feed.next(t, n);
+        const bool direct = out.shift == row.shift && Tiles::inside(row, lo + n * Tiles::kVecs, hi);
 #pragma unroll
         for (int u = 0; u < kSize; u++) {
             const uint32_t i = t.place(lo + n * Tiles::kVecs, u);
-            if (i >= hi) break;
+            if (!direct && i >= hi) break;
             float v[kVec];
             if (fast) {
                 raise<T>(t.q[u]);
@@ -396,7 +381,7 @@ __global__ void __launch_bounds__(kRowThreads) k_logprobs_backward(ScoreGradPara
 #pragma unroll
                 for (int e = 0; e < kVec; e++) v[e] = fmaf(c, e == hot % kVec ? a : 0.0f, v[e]);
             }
-            put_vector(out, row, i, v);
+            put_vector(out, row, i, v, direct);
         }
     }
 }
