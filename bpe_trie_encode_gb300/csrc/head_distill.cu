@@ -1,338 +1,8 @@
-// head_distill.cu -- divergence of rows of logits from a teacher's top
-// alternatives, and its gradient in the same call.
-#include "head_row.cuh"
-
-namespace bpe {
-namespace {
-
-constexpr int kMost = (int)BPE_HEAD_MAX_TOP;   // alternatives that a teacher lists
-constexpr size_t kMostShared = 200 * 1024;      // of a CTA
-constexpr uint32_t kKeep = 4;                   // tiles of a row that leave room for three CTAs on an SM
-static_assert(kMost <= (int)kRowThreads, "one thread for each");
-
-struct DistillParams {
-    RowParams row;
-    const int32_t *top_ids;
-    const void *top_logprob;
-    int top_type;
-    uint32_t n_listed;
-    int rest;
-    float *loss;
-    float grad;
-    const float *d_grad;
-    void *out;
-    uint64_t out_stride;
-};
-
-constexpr int kHash = 256;
-constexpr int kThreads = kRowThreads + 32;      // the row's, and a warp for the entries
-constexpr int kLister = kRowWarps;
-
-struct DistillShared {
-    TeamShared team;
-    uint32_t id[kMost];        // ~0: none, or the same as one before
-    float q[kMost], v[kMost];  // the token's q, of all its entries; its logit
-    uint32_t hash[kHash];
-    float q_sum, q_log_q, m, s;   // of the entries: the sums of q and of q log q; the listed tokens' softmax
-    uint32_t bits[1];          // a bit for each place of the CTA's vectors: listed
-};
-
-__device__ __forceinline__ float warp_max(float v) { return key_value(__reduce_max_sync(kFull, key_of(v))); }
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
-    return v;
-}
-
-// The row's entries, four to a lane of the CTA's last warp, which deals with them while the others read the row.
-struct Entries {
-    static constexpr int kEach = kMost / 32;
-    uint32_t id[kEach];        // ~0: none
-    float t[kEach], v[kEach];  // value, then log q; the token's logit
-
-    template <typename T> __device__ __forceinline__ void load(const DistillParams &P, uint32_t r, const RowView<T> &row, int lane) {
-#pragma unroll
-        for (int j = 0; j < kEach; j++) {
-            const uint32_t i = j * 32 + lane;
-            id[j] = ~0u, t[j] = -INFINITY, v[j] = -INFINITY;
-            if (i >= P.n_listed) continue;
-            const uint64_t at = (uint64_t)r * P.n_listed + i;
-            id[j] = (uint32_t)P.top_ids[at];
-            t[j] = P.top_type == BPE_F32    ? ((const float *)P.top_logprob)[at]
-                   : P.top_type == BPE_BF16 ? to_f32(((const __nv_bfloat16 *)P.top_logprob)[at])
-                                            : to_f32(((const __half *)P.top_logprob)[at]);
-        }
-#pragma unroll
-        for (int j = 0; j < kEach; j++) {
-            if (id[j] >= P.row.n_tok || !(t[j] > -INFINITY)) id[j] = ~0u, t[j] = -INFINITY;
-            if (id[j] != ~0u) v[j] = to_f32(row.at[row.shift + id[j]]);
-        }
-    }
-    // q and the tokens to shared memory.  An id that comes twice is found by a table of hashes; then (hardly ever) every
-    // entry looks all others through, so that the sums are in the order of entries.
-    __device__ __forceinline__ void weigh(DistillShared &S, const DistillParams &P, float c, int lane) {
-        float m = -INFINITY, sum = 0, log_s = 0;
-        if (!P.rest) {         // the softmax of the listed values
-#pragma unroll
-            for (int j = 0; j < kEach; j++) m = fmaxf(m, t[j]);
-            m = warp_max(m);
-#pragma unroll
-            for (int j = 0; j < kEach; j++) {
-                t[j] = id[j] != ~0u ? z_any(t[j], m, 1.0f) : -INFINITY;
-                sum += expf(t[j]);
-            }
-            log_s = logf(warp_sum(sum));
-        }
-        float q_sum = 0, q_log_q = 0;
-        bool twice = false;
-#pragma unroll
-        for (int j = 0; j < kHash / 32; j++) S.hash[j * 32 + lane] = ~0u;
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < kEach; j++) {
-            const uint32_t i = j * 32 + lane;
-            if (t[j] > -INFINITY) t[j] -= log_s;
-            const float q = expf(t[j]);
-            q_sum += q;
-            q_log_q += q > 0.0f ? q * t[j] : 0.0f;
-            S.id[i] = id[j], S.q[i] = q, S.v[i] = v[j];
-            if (id[j] == ~0u) continue;
-            for (uint32_t h = id[j] * 2654435769u >> 24;; h = (h + 1) % kHash) {   // at most 128 of 256 places are taken
-                const uint32_t old = atomicCAS(&S.hash[h], ~0u, id[j]);
-                if (old == ~0u) break;
-                if (old == id[j]) {
-                    twice = true;
-                    break;
-                }
-            }
-        }
-        __syncwarp();
-        if (__any_sync(kFull, twice)) {
-            float q[kEach];
-            bool later[kEach];
-#pragma unroll
-            for (int j = 0; j < kEach; j++) {
-                const uint32_t i = j * 32 + lane;
-                q[j] = 0, later[j] = false;
-                if (id[j] == ~0u) continue;
-                for (uint32_t o = 0; o < P.n_listed; o++)
-                    if (S.id[o] == id[j]) q[j] += S.q[o], later[j] |= o < i;
-            }
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < kEach; j++) {
-                S.q[j * 32 + lane] = q[j];
-                if (later[j]) S.id[j * 32 + lane] = ~0u;
-            }
-            __syncwarp();
-        }
-        q_sum = warp_sum(q_sum), q_log_q = warp_sum(q_log_q);
-        float top = -INFINITY, s = 0;
-        if (P.rest) {          // the listed tokens' softmax, each once
-#pragma unroll
-            for (int j = 0; j < kEach; j++) top = fmaxf(top, v[j]);   // the other one where one is NaN
-            top = warp_max(top);
-#pragma unroll
-            for (int j = 0; j < kEach; j++)
-                if (top > -INFINITY && S.id[j * 32 + lane] != ~0u) s += expf(z_any(v[j], top, c));
-            s = warp_sum(s);
-        }
-        if (lane == 0) S.q_sum = q_sum, S.q_log_q = q_log_q, S.m = top, S.s = s;
-    }
-    // The sum of q log p, in the entries' own terms.
-    __device__ __forceinline__ float cross(float m, float c, float log_s) const {
-        float sum = 0;
-#pragma unroll
-        for (int j = 0; j < kEach; j++) {
-            const float q = expf(t[j]);
-            if (q > 0.0f) sum += q * (z_any(v[j], m, c) - log_s);
-        }
-        return warp_sum(sum);
-    }
-};
-
-constexpr int kSize = 4;       // vectors of a thread at a time
-
-// The bits of vector i of the share.
-template <typename T> __device__ __forceinline__ uint32_t vector_bits(const uint32_t *bits, uint32_t i) {
-    const uint8_t *const bytes = (const uint8_t *)bits;
-    return sizeof(T) == 2 ? bytes[i] : bytes[i / 2] >> i % 2 * 4 & 15;
-}
-
-// A vector with -infinity in the elements that `some` has bits for.
-template <typename T> __device__ __forceinline__ uint4 without(uint4 q, uint32_t some) {
-    constexpr uint32_t k = Bits<T>::kNegInf;
-    // 16 bits: this has bit 0 at 7 and bit 1 at 15, of which prmt makes bytes (8 and 9: the sign of byte 0 or 1), and shifted
-    // right by 2 the next two
-    const uint32_t spread = some << 7 | some << 14;
-    auto word = [=](uint32_t w, int i) {
-        uint32_t mask = (uint32_t)((int32_t)(some << (31 - i)) >> 31);
-        if (sizeof(T) == 2) asm("prmt.b32 %0, %1, 0, 0x9988;" : "=r"(mask) : "r"(spread >> 2 * i));
-        return (w & ~mask) | (k & mask);
-    };
-    return make_uint4(word(q.x, 0), word(q.y, 1), word(q.z, 2), word(q.w, 3));
-}
-
-template <typename T, bool kTeam, bool kRest, bool kGrad>
-__global__ void __launch_bounds__(kThreads, 3) k_distill(DistillParams P, uint32_t n_team, uint32_t slots, bool kept) {
-    constexpr int kVec = RowView<T>::kVec;
-    using Tiles = Tile<T, kSize>;
-    extern __shared__ __align__(16) unsigned char smem[];
-    DistillShared &S = *(DistillShared *)(smem + slots * (Tiles::kVecs * 16));
-    Team<kTeam> team(S.team, n_team);
-    team.arrive();
-    const uint32_t r = kTeam ? blockIdx.x / n_team : blockIdx.x;
-    const RowView<T> row(P.row.logits, P.row.stride, r, P.row.n_tok);
-    const uint32_t vecs = row.vecs(), share = (vecs + team.size - 1) / team.size;
-    const uint32_t lo = min(vecs, team.rank * share), hi = min(vecs, lo + share);
-    const bool reads = team.warp != kLister;
-    const Feed<T, kSize> feed(row, smem, lo, reads ? hi : lo, kept, reads);   // under way while the entries are read
-    const float c = P.row.inverse(r), c2 = usual_c<T>(c) * kLog2e;
-    const float grad = kGrad ? P.d_grad ? P.d_grad[r] : P.grad : 0.0f;
-
-    Entries list;
-    if (team.warp == kLister) list.load<T>(P, r, row, team.lane);
-    if (kRest) {
-        for (uint32_t i = threadIdx.x; i < ((hi - lo) * kVec + 31) / 32; i += kThreads) S.bits[i] = 0;
-        __syncthreads();
-        if (team.warp == kLister)
-#pragma unroll
-            for (int j = 0; j < Entries::kEach; j++) {
-                const uint32_t at = list.id[j] + row.shift - lo * kVec;
-                if (list.id[j] != ~0u && at < (hi - lo) * kVec) atomicOr(&S.bits[at / 32], 1u << at % 32);
-            }
-        __syncthreads();
-    }
-    if (team.warp == kLister) list.weigh(S, P, c, team.lane);
-
-    // The softmax of all tokens, or of the unlisted ones, whose share among themselves is exact then however little of the
-    // row they hold.
-    const uint32_t *const bits = S.bits;
-    auto unlisted = [=](uint4 q, uint32_t i) {
-        if (kRest) {
-            const uint32_t some = vector_bits<T>(bits, i - lo);
-            if (some) q = without<T>(q, some);
-        }
-        return q;
-    };
-    Running<T, false> sums(c2);
-    const uint32_t steps = reads ? (hi - lo + Tiles::kVecs - 1) / Tiles::kVecs : 0;
-    for (uint32_t n = 0; n < steps; n++) {
-        Tiles t;
-        feed.next(t, n);
-        if (kRest) {           // what lies behind the share is -infinity whatever its bits
-            uint32_t some[kSize], any = 0;
-#pragma unroll
-            for (int u = 0; u < kSize; u++) any |= some[u] = vector_bits<T>(S.bits, t.place(n * Tiles::kVecs, u));
-            if (any) {
-#pragma unroll
-                for (int u = 0; u < kSize; u++) t.q[u] = without<T>(t.q[u], some[u]);
-            }
-        }
-        sums.add(t, t.raise_all(), c2);
-    }
-    float none_counted = 0.0f;
-    Softmax free = softmax_join(team, sums, c2, none_counted);
-    const bool fast = usual<T>(free.m, c);
-    if (!fast) free = softmax_any<T, kTeam>(team, lo, hi, c, [=](uint32_t i) { return unlisted(row.load(i), i); });
-
-    // the whole row's softmax: m and s, and what exp of an unlisted token's z is to be multiplied by
-    float m = free.m, s = free.s, to_all = 1.0f;
-    if (kRest) {
-        m = fmaxf(S.m, free.m);
-        if (m > -INFINITY) {
-            to_all = free.m > -INFINITY ? expf(z_any(free.m, m, c)) : 0.0f;
-            s = free.s * to_all + (S.m > -INFINITY ? S.s * expf(z_any(S.m, m, c)) : 0.0f);
-        }
-    }
-    const bool none = m == -INFINITY;
-    const float log_s = logf(s);
-    const float q_rest = kRest && free.m > -INFINITY ? fmaxf(0.0f, 1.0f - S.q_sum) : 0.0f, q_total = S.q_sum + q_rest;
-    if (team.warp == kLister && team.rank == 0) {
-        float loss = S.q_log_q - list.cross(m, c, log_s);
-        if (q_rest > 0.0f) loss += q_rest * (logf(q_rest) - (z_any(free.m, m, c) + logf(free.s) - log_s));
-        if (team.lane == 0) P.loss[r] = none ? (q_total > 0.0f ? INFINITY : 0.0f) : loss;
-    }
-    if (!kGrad) return;
-
-    const RowView<T> out(P.out, P.out_stride, r, P.row.n_tok);
-    const bool zero = none || c == INFINITY;
-    const float g = zero ? 0.0f : c * grad;
-    const float of_free = zero || free.m == -INFINITY ? 0.0f : g * (q_total / s * to_all - (q_rest > 0.0f ? q_rest / free.s : 0.0f));
-    const float off = __fmul_rn(free.m, c2), w = of_free * exp2_of(-fmaf(free.m, c2, -off));   // what off was rounded by
-    for (uint32_t n = 0; n < steps; n++) {
-        const uint32_t i0 = lo + n * Tiles::kVecs;
-        Tiles t;
-        if (kept) feed.again(t, n);
-        else t.load(row, i0, hi);
-        const bool direct = out.shift == row.shift && Tiles::inside(row, i0, hi);
-#pragma unroll
-        for (int u = 0; u < kSize; u++) {
-            const uint32_t i = t.place(i0, u);
-            if (!direct && i >= hi) break;
-            float v[kVec];
-            if (fast) {
-                raise<T>(t.q[u]);
-                unpack(t.q[u], v, T());
-#pragma unroll
-                for (int e = 0; e < kVec; e += 2) {
-                    const float2 x = fma2(Pair(v[e], v[e + 1]), Pair(c2, c2), Pair(-off, -off)).both();
-                    const float2 d = mul2(Pair(exp2_of(x.x), exp2_of(x.y)), Pair(w, w)).both();
-                    v[e] = d.x, v[e + 1] = d.y;
-                }
-            } else {
-                unpack(t.q[u], v, T());
-#pragma unroll
-                for (int e = 0; e < kVec; e++) v[e] = of_free == 0.0f ? 0.0f : expf(z_any(v[e], free.m, c)) * of_free;
-            }
-            put_vector(out, row, i, v, direct);
-        }
-    }
-    __syncthreads();
-    if (threadIdx.x < P.n_listed) {
-        const uint32_t id = S.id[threadIdx.x], at = id + row.shift - lo * kVec;
-        if (id != ~0u && at < (hi - lo) * kVec)
-            out.at[out.shift + id] = from_f32<T>(zero ? 0.0f : g * (q_total * expf(z_any(S.v[threadIdx.x], m, c) - log_s) - S.q[threadIdx.x]));
-    }
-}
-
-template <typename T, bool kTeam, bool kRest, bool kGrad>
-int launch_team(bpe_ctx *ctx, const DistillParams &P, uint32_t n_rows, uint32_t team, uint32_t slots, bool kept, size_t smem) {
-    auto k = k_distill<T, kTeam, kRest, kGrad>;
-    static std::atomic<uint64_t> devices{0};
-    BPE_CUDA(ctx, allow_shared(k, ctx->device, kMostShared, devices), "head_distill");
-    return launch_rows(ctx, "head_distill launch", k, P, n_rows, team, kThreads, kTeam, smem, slots, kept);
-}
-
-template <typename T, bool kRest, bool kGrad> int launch(bpe_ctx *ctx, const DistillParams &P, uint32_t n_rows) {
-    constexpr uint32_t kVec = RowView<T>::kVec, kTileBytes = Tile<T, kSize>::kVecs * 16, kAhead = Feed<T, kSize>::kAhead;
-    const uint32_t vecs = (P.row.n_tok + kVec - 1) / kVec + (row_shifts<T>(P.row.logits, P.row.stride, n_rows) ? 1 : 0);
-    uint32_t team = row_team(n_rows, P.row.n_tok * (uint32_t)sizeof(T), (uint32_t)ctx->sm_count), slots = kAhead;
-    auto tiles = [&](uint32_t t) { return ((vecs + t - 1) / t + Tile<T, kSize>::kVecs - 1) / Tile<T, kSize>::kVecs; };
-    auto shared = [&]() {   // of the entries, the tiles, and bits for tiles that are whole
-        return sizeof(DistillShared) + (size_t)slots * kTileBytes + (kRest ? (size_t)tiles(team) * Tile<T, kSize>::kVecs * kVec / 8 : 0);
-    };
-    bool kept = false;
-    if (kGrad) {   // a row that stays in shared memory is read once
-        while (team < kMaxTeam && tiles(team) > kKeep) team *= 2;
-        slots = tiles(team);
-        kept = shared() <= kMostShared;
-        if (!kept) slots = kAhead;
-    }
-    while (team < kMaxTeam && shared() > kMostShared) team *= 2;
-    return team > 1 ? launch_team<T, true, kRest, kGrad>(ctx, P, n_rows, team, slots, kept, shared())
-                    : launch_team<T, false, kRest, kGrad>(ctx, P, n_rows, 1, slots, kept, shared());
-}
-
-template <typename T> int launch(bpe_ctx *ctx, const DistillParams &P, uint32_t n_rows) {
-    if (P.rest) return P.out ? launch<T, true, true>(ctx, P, n_rows) : launch<T, true, false>(ctx, P, n_rows);
-    return P.out ? launch<T, false, true>(ctx, P, n_rows) : launch<T, false, false>(ctx, P, n_rows);
-}
-
-}  // namespace
-}  // namespace bpe
+// head_distill.cu -- the entry point of head_distill (head_distill.cuh).
+#include "head_distill.cuh"
 
 using namespace bpe;
+
 
 extern "C" int head_distill(bpe_ctx *ctx, const void *d_logits, uint64_t stride, int type, uint32_t n_rows, uint32_t n_tok,
                             const int32_t *d_top_ids, const void *d_top_logprob, int top_type, uint32_t n_listed, int rest,
@@ -352,7 +22,7 @@ extern "C" int head_distill(bpe_ctx *ctx, const void *d_logits, uint64_t stride,
     BPE_CUDA(ctx, cudaSetDevice(ctx->device), "cudaSetDevice");
     const DistillParams P{{d_logits, stride, n_tok, temperature, d_temperature}, d_top_ids, d_top_logprob, top_type, n_listed,
                           rest, d_loss_out, grad, d_grad, d_grad_out, grad_stride};
-    return type == BPE_F32    ? launch<float>(ctx, P, n_rows)
-           : type == BPE_BF16 ? launch<__nv_bfloat16>(ctx, P, n_rows)
-                              : launch<__half>(ctx, P, n_rows);
+    return type == BPE_F32    ? distill_f32(ctx, P, n_rows)
+           : type == BPE_BF16 ? distill_bf16(ctx, P, n_rows)
+                              : distill_f16(ctx, P, n_rows);
 }

@@ -1,0 +1,6 @@
+// head_distill_f32.cu -- head_distill's kernels for logits of this type.
+#include "head_distill.cuh"
+
+namespace bpe {
+int distill_f32(bpe_ctx *ctx, const DistillParams &P, uint32_t n_rows) { return launch<float>(ctx, P, n_rows); }
+}  // namespace bpe

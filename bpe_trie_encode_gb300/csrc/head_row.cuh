@@ -11,8 +11,10 @@ namespace bpe {
 
 typedef unsigned long long u64;
 
-constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
 constexpr int kMaxTeam = 8;                // CTAs of a row: a cluster
+constexpr int kMost = 256, kMostWarps = kMost / 32;   // threads of a row in a CTA
+// A row's threads, kLanes: a warp of a CTA that takes eight rows, or a CTA of 64, 128 or 256.
+constexpr int kWarpRows = 8;
 
 struct RowParams {
     const void *logits;
@@ -219,9 +221,11 @@ template <typename T> __device__ __forceinline__ typename Words<T>::W raise(uint
     return F::larger(F::larger(w[0], w[1]), F::larger(w[2], w[3]));
 }
 
+template <int kLanes> __device__ __forceinline__ uint32_t row_thread() { return kLanes == 32 ? threadIdx.x & 31 : threadIdx.x; }
+
 // kSize vectors a thread, of the CTA's share of a row.
-template <typename T, int kSize> struct Tile {
-    static constexpr uint32_t kVecs = kSize * kRowThreads;
+template <typename T, int kSize, int kLanes> struct Tile {
+    static constexpr uint32_t kVecs = kSize * kLanes;
     uint4 q[kSize];
 
     // Raises the tile; gives its largest logit, and each vector's largest word.
@@ -235,7 +239,7 @@ template <typename T, int kSize> struct Tile {
         typename Words<T>::W each[kSize];
         return raise_all(each);
     }
-    __device__ __forceinline__ static uint32_t place(uint32_t i0, int u) { return i0 + u * kRowThreads + threadIdx.x; }
+    __device__ __forceinline__ static uint32_t place(uint32_t i0, int u) { return i0 + u * kLanes + row_thread<kLanes>(); }
     // No vector from i0 on ends outside the row or the share.
     __device__ __forceinline__ static bool inside(const RowView<T> &row, uint32_t i0, uint32_t hi) {
         return (i0 > 0 || row.shift == 0) && i0 + kVecs <= min(hi, row.end / RowView<T>::kVec);
@@ -272,10 +276,10 @@ template <typename T, int kSize> struct Tile {
 // The CTA's share of a row on its way through shared memory, kAhead tiles ahead of where it is read.  Every thread copies
 // (asynchronously, without registers) what it will read itself, so that no barrier is needed.  A share that is kept has a
 // slot for every tile, and stays for a second look.
-template <typename T, int kSize> struct Feed {
-    using Tiles = Tile<T, kSize>;
+template <typename T, int kSize, int kLanes> struct Feed {
+    using Tiles = Tile<T, kSize, kLanes>;
     static constexpr int kAhead = 2;
-    static constexpr uint32_t kBytes = Tiles::kVecs * 16, kStep = kRowThreads * 16;   // of a tile, from a thread's vector to its next
+    static constexpr uint32_t kBytes = Tiles::kVecs * 16, kStep = kLanes * 16;   // of a tile, from a thread's vector to its next
     RowView<T> row;
     const char *from;          // this thread's first vector
     uint32_t mine;             // its place in the first slot, an address of 32 bits
@@ -283,8 +287,8 @@ template <typename T, int kSize> struct Feed {
     bool kept;
 
     __device__ __forceinline__ Feed(const RowView<T> &r, void *shared, uint32_t lo_, uint32_t hi_, bool kept_ = false, bool reads = true)
-        : row(r), from((const char *)r.at + (uint64_t)(lo_ + threadIdx.x) * 16),
-          mine((uint32_t)__cvta_generic_to_shared(shared) + threadIdx.x * 16), lo(lo_), hi(hi_), kept(kept_) {
+        : row(r), from((const char *)r.at + (uint64_t)(lo_ + row_thread<kLanes>()) * 16),
+          mine((uint32_t)__cvta_generic_to_shared(shared) + row_thread<kLanes>() * 16), lo(lo_), hi(hi_), kept(kept_) {
         if (reads) {
 #pragma unroll
             for (int n = 0; n < kAhead; n++) ask(n);
@@ -309,7 +313,7 @@ template <typename T, int kSize> struct Feed {
     }
     __device__ __forceinline__ void ask_edge(uint32_t i0, uint32_t to) const {
 #pragma unroll 1
-        for (uint32_t i = i0 + threadIdx.x; i < i0 + Tiles::kVecs; i += kRowThreads, to += kStep) {
+        for (uint32_t i = i0 + row_thread<kLanes>(); i < i0 + Tiles::kVecs; i += kLanes, to += kStep) {
             if (i < hi && row.whole(i)) {
                 copy(to, (const uint4 *)row.at + i);
                 continue;
@@ -349,7 +353,7 @@ template <typename T, bool kEntropy> struct Running {
         r = to;
     }
     // Adds a raised tile whose largest logit is m.
-    template <int kSize> __device__ __forceinline__ void add(const Tile<T, kSize> &t, float m, float c2) {
+    template <int kSize, int kLanes> __device__ __forceinline__ void add(const Tile<T, kSize, kLanes> &t, float m, float c2) {
         constexpr int kVec = RowView<T>::kVec;
         most = fmaxf(most, m);
         if (fmaf(m, c2, -r) > kSlack) move(__fmul_rn(m, c2));
@@ -387,26 +391,26 @@ __device__ __forceinline__ u64 far_load(const u64 *p, uint32_t rank) {
 }
 
 struct TeamShared {
-    float4 red[kRowWarps];
+    float4 red[kMostWarps];
     float4 slot[2][kMaxTeam];
 };
 
-// The threads of a row: one CTA, or the CTAs of a cluster.
-template <bool kTeam> struct Team {
-    TeamShared &S;
-    uint32_t rank, size;
-    int lane, warp, turn;
+// The threads of a row: a warp, a CTA, or the CTAs of a cluster.
+template <int kLanes, bool kTeam> struct Team {
+    static_assert(kLanes <= kMost && (!kTeam || kLanes == kMost), "clusters are of full CTAs");
+    static constexpr bool kWarp = kLanes == 32;
+    static constexpr int kWarps = kLanes / 32;
+    TeamShared &S;         // not there for a warp
+    uint32_t rank, size, thread;
+    int lane, warp, turn;  // a thread beyond kLanes is of a warp that helps
 
     __device__ __forceinline__ Team(TeamShared &s, uint32_t team)
-        : S(s), rank(kTeam ? blockIdx.x % team : 0), size(kTeam ? team : 1), lane(threadIdx.x & 31),
-          warp(threadIdx.x >> 5), turn(0) {}
+        : S(s), rank(kTeam ? blockIdx.x % team : 0), size(kTeam ? team : 1), thread(row_thread<kLanes>()), lane(threadIdx.x & 31),
+          warp(kWarp ? 0 : threadIdx.x >> 5), turn(0) {}
 
-    __device__ __forceinline__ void sync() const {
-        __syncwarp();
-        if (!kTeam)
-            __syncthreads();
-        else
-            asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    __device__ __forceinline__ void sync_cta() const {   // or the warp
+        if (kWarp) __syncwarp();
+        else __syncthreads();
     }
     // A CTA's shared memory is there for the others once it runs, and until it ends: the first exchange comes after the one
     // barrier's wait, the end after the other's.  Neither orders memory.
@@ -427,16 +431,18 @@ template <bool kTeam> struct Team {
     __device__ __forceinline__ void exchange(float4 v) {
         turn ^= 1;
         if (threadIdx.x < size) far_store(&S.slot[turn][rank], threadIdx.x, v);
-        sync();
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
     // The warps' values combined in the order of warps and CTAs; every thread gets the result.
     template <typename F> __device__ __forceinline__ float4 across(float4 v, F f) {
+        if (kWarp) return v;
         __syncthreads();
-        if (lane == 0 && warp < kRowWarps) S.red[warp] = v;
+        if (lane == 0 && warp < kWarps) S.red[warp] = v;
         __syncthreads();
         v = S.red[0];
 #pragma unroll
-        for (int i = 1; i < kRowWarps; i++) v = f(v, S.red[i]);
+        for (int i = 1; i < kWarps; i++) v = f(v, S.red[i]);
         if (!kTeam) return v;
         exchange(v);
         v = S.slot[turn][0];
@@ -461,15 +467,15 @@ template <bool kTeam> struct Team {
 struct Softmax { float m, s, sz; };
 struct SoftmaxAny { Softmax all; int turn; };
 
-// Sums relative to the largest m c2 of eight lanes' out of each lane's own, added up.
-template <bool kEntropy> __device__ __forceinline__ float4 join_eight(float4 v, float c2) {
+// Sums relative to the largest m c2 of kN lanes' out of each lane's own, added up.
+template <bool kEntropy, int kN> __device__ __forceinline__ float4 join_lanes(float4 v, float c2) {
     float m = v.x;
 #pragma unroll
-    for (int d = 4; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+    for (int d = kN / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
     const float d = __fmul_rn(v.x, c2) - __fmul_rn(m, c2), f = exp2_of(d);
     v = make_float4(m, v.y * f, kEntropy ? fmaf(v.y, d, v.z) * f : 0.0f, v.w);
 #pragma unroll
-    for (int e = 4; e > 0; e >>= 1) {
+    for (int e = kN / 2; e > 0; e >>= 1) {
         v.y += __shfl_xor_sync(kFull, v.y, e);
         if (kEntropy) v.z += __shfl_xor_sync(kFull, v.z, e);
         v.w += __shfl_xor_sync(kFull, v.w, e);
@@ -479,9 +485,9 @@ template <bool kEntropy> __device__ __forceinline__ float4 join_eight(float4 v, 
 
 // The threads' sums to the row's.  m is exact; s and sz count where the row is usual.  `count`, the first warp's, is added
 // up over CTAs beside them.
-template <typename T, bool kEntropy, bool kTeam>
-__device__ __forceinline__ Softmax softmax_join(Team<kTeam> &team, Running<T, kEntropy> a, float c2, float &count) {
-    static_assert(kRowWarps == 8 && kMaxTeam == 8, "eight lanes for either");
+template <typename T, bool kEntropy, int kLanes, bool kTeam>
+__device__ __forceinline__ Softmax softmax_join(Team<kLanes, kTeam> &team, Running<T, kEntropy> a, float c2, float &count) {
+    constexpr int kWarps = kLanes / 32;
     const float m = key_value(__reduce_max_sync(kFull, key_of(a.most)));
     a.move(__fmul_rn(m, c2));
     const float2 s = a.s.both(), sz = a.sz.both();
@@ -491,15 +497,17 @@ __device__ __forceinline__ Softmax softmax_join(Team<kTeam> &team, Running<T, kE
         v.y += __shfl_xor_sync(kFull, v.y, d);
         if (kEntropy) v.z += __shfl_xor_sync(kFull, v.z, d);
     }
-    if (team.lane == 0 && team.warp < kRowWarps) team.S.red[team.warp] = v;
-    __syncthreads();
-    v = join_eight<kEntropy>(team.S.red[team.lane & 7], c2);
+    if (kLanes > 32) {
+        if (team.lane == 0 && team.warp < kWarps) team.S.red[team.warp] = v;
+        __syncthreads();
+        v = join_lanes<kEntropy, kWarps>(team.S.red[team.lane % kWarps], c2);
+    }
     if (kTeam) {
         team.wait();   // the others run
         team.exchange(v);
-        const uint32_t o = team.lane & 7;
+        const uint32_t o = team.lane % kMaxTeam;
         v = o < team.size ? team.S.slot[team.turn][o] : make_float4(Usual<T>::kLow, 0, 0, 0);
-        v = join_eight<kEntropy>(v, c2);
+        v = join_lanes<kEntropy, kMaxTeam>(v, c2);
     }
     count = v.w;
     // relative to m itself rather than to m c2 rounded
@@ -508,14 +516,14 @@ __device__ __forceinline__ Softmax softmax_join(Team<kTeam> &team, Running<T, kE
 }
 
 // Both in their general form: any logits and any c, two passes.  `load(i)` gives vector i; threads beyond the row's own add
-// nothing.  (By value, and the team's turn
-// given back: what a function that is called takes by reference lives in memory, in the usual rows' loops too.)
-template <typename T, bool kTeam, typename L>
-__device__ __noinline__ SoftmaxAny softmax_sums(Team<kTeam> team, uint32_t lo, uint32_t hi, float c, L load) {
+// nothing.  (By value, and the team's turn given back: what a function that is called takes by reference lives in memory, in
+// the usual rows' loops too.)
+template <typename T, int kLanes, bool kTeam, typename L>
+__device__ __noinline__ SoftmaxAny softmax_sums(Team<kLanes, kTeam> team, uint32_t lo, uint32_t hi, float c, L load) {
     constexpr int kVec = RowView<T>::kVec;
-    if (threadIdx.x >= kRowThreads) lo = hi;
+    if (team.thread >= (uint32_t)kLanes) lo = hi;
     float m = -INFINITY;
-    for (uint32_t i = lo + threadIdx.x; i < hi; i += kRowThreads) {
+    for (uint32_t i = lo + team.thread; i < hi; i += kLanes) {
         float v[kVec];
         unpack(load(i), v, T());
 #pragma unroll
@@ -524,7 +532,7 @@ __device__ __noinline__ SoftmaxAny softmax_sums(Team<kTeam> team, uint32_t lo, u
     m = team.max(m);
     if (m == -INFINITY) return {{m, 0.0f, 0.0f}, team.turn};
     float s = 0, sz = 0;
-    for (uint32_t i = lo + threadIdx.x; i < hi; i += kRowThreads) {
+    for (uint32_t i = lo + team.thread; i < hi; i += kLanes) {
         float v[kVec];
         unpack(load(i), v, T());
 #pragma unroll
@@ -537,11 +545,24 @@ __device__ __noinline__ SoftmaxAny softmax_sums(Team<kTeam> team, uint32_t lo, u
     const float4 all = team.sum(make_float4(s, sz, 0, 0));
     return {{m, all.x, all.y}, team.turn};
 }
-template <typename T, bool kTeam, typename L>
-__device__ __forceinline__ Softmax softmax_any(Team<kTeam> &team, uint32_t lo, uint32_t hi, float c, L load) {
-    const SoftmaxAny any = softmax_sums<T, kTeam>(team, lo, hi, c, load);
+template <typename T, int kLanes, bool kTeam, typename L>
+__device__ __forceinline__ Softmax softmax_any(Team<kLanes, kTeam> &team, uint32_t lo, uint32_t hi, float c, L load) {
+    const SoftmaxAny any = softmax_sums<T, kLanes, kTeam>(team, lo, hi, c, load);
     team.turn = any.turn;
     return any.all;
+}
+
+// Threads of a row, at least `least` of them.  A row of few threads takes longer, but loses less to what is done once for each
+// thread and to barriers.  So it is for many rows, where the time of the last ones hardly counts: with `each` bytes of a warp's
+// share for every warp beyond two an SM.  In us with 32 / 64 / 128 / 256 threads, bf16, 20 alternatives (each = 4): 8,192 rows
+// of 1,000 17 / 25 / 40 / 70, 1,024 of 8,192 14 / 11 / 9.5 / 12.5, 256 of 8,192 14 / 9 / 6.8 / 6.5; without alternatives
+// (each = 40), 32 / 256: 8,192 of 1,000 7 / 32, of 32,256 81 / 85, 1,024 of 8,192 5.1 / 5.9, 512 of 8,192 5.0 / 3.8.
+inline int row_lanes(uint32_t n_rows, uint32_t bytes, uint32_t sms, int least, uint32_t each) {
+    for (int lanes = least; lanes < kMost; lanes *= 2) {
+        const uint64_t warps = (uint64_t)n_rows * (lanes / 32);
+        if (warps > 2 * sms && (uint64_t)bytes * 32 / lanes <= each * (warps - 2 * sms)) return lanes;
+    }
+    return kMost;
 }
 
 // CTAs of a row: as many as keep every SM at work with some to spare, of 16 KB at least.
@@ -551,13 +572,13 @@ inline uint32_t row_team(uint32_t n_rows, uint32_t bytes, uint32_t sms) {
     return team;
 }
 
-// A kernel with a CTA, or a cluster of them, for each row.
+// A kernel with `ctas` CTAs, or clusters of `team` of them.
 template <typename K, typename P, typename... More>
-inline int launch_rows(bpe_ctx *ctx, const char *what, K kernel, const P &params, uint32_t n_rows, uint32_t team, int threads,
+inline int launch_rows(bpe_ctx *ctx, const char *what, K kernel, const P &params, uint32_t ctas, uint32_t team, int threads,
                        bool cluster, size_t shared, More... more) {
-    if ((uint64_t)n_rows * team > 0x7FFFFFFFu) return fail(ctx, BPE_ERR_INVALID_ARG, "%s: %u rows", what, n_rows);
+    if ((uint64_t)ctas * team > 0x7FFFFFFFu) return fail(ctx, BPE_ERR_INVALID_ARG, "%s: too many rows", what);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(n_rows * team);
+    cfg.gridDim = dim3(ctas * team);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = shared;
     cfg.stream = ctx->stream;

@@ -5,12 +5,7 @@
 namespace bpe {
 namespace {
 
-constexpr int kTop = (int)BPE_HEAD_MAX_TOP;
-constexpr int kFound = 2048;               // vectors that may hold alternatives
-constexpr int kList = 1024;                // tokens that may be among them
-
 constexpr int kSize = 4;                   // vectors of a thread at a time
-constexpr size_t kFeedBytes = (size_t)Feed<float, kSize>::kAhead * kSize * kRowThreads * 16;
 constexpr uint32_t kGradTiles = 8;         // of a CTA of the gradient, at most
 
 struct ScoreParams {
@@ -23,25 +18,33 @@ struct ScoreParams {
     float *norm;
 };
 
-struct ScoreShared {
+// Of a row's threads, which take up to as many alternatives.
+template <int kLanes> struct ScoreShared {
+    static constexpr int kTop = kLanes < (int)BPE_HEAD_MAX_TOP ? kLanes : (int)BPE_HEAD_MAX_TOP;
+    static constexpr int kFound = 8 * kLanes;                       // vectors that may hold alternatives
+    static constexpr int kList = kLanes < 128 ? 8 * kLanes : 1024;  // tokens that may be among them, in the tiles' place
+    static constexpr uint32_t kFeedBytes = Feed<float, kSize, kLanes>::kAhead * kSize * kLanes * 16;
+    static_assert(kTop <= kLanes && (kLanes < kMost || kMaxTeam * kTop <= kList) && kList * sizeof(u64) <= kFeedBytes,
+                  "one thread for each alternative, room for a team's");
     TeamShared team;
-    uint32_t list_n, found_n, scan[kRowWarps];
+    uint32_t list_n, found_n, scan[kMostWarps];
+    float bound[kMostWarps];
     u64 best[kTop];                        // in order
-    float bound[kRowWarps];
-    uint32_t found[kFound];                // vectors that may hold alternatives
+    uint32_t found[kFound];
 };
-static_assert(kTop <= kRowThreads && kMaxTeam * kTop <= kList && kList * sizeof(u64) <= kFeedBytes,
-              "one thread for each alternative, room for a team's");
+// Shared memory of a row: its tiles, and without alternatives the team's part alone.
+template <int kLanes, bool kTops>
+constexpr uint32_t kScoreBytes = ScoreShared<kLanes>::kFeedBytes + (uint32_t)(kTops ? sizeof(ScoreShared<kLanes>) : sizeof(TeamShared));
 
 __device__ __forceinline__ u64 entry_of(uint32_t key, uint32_t id) { return (u64)key << 32 | (uint32_t)~id; }
 
 // The alternatives in `list`, at most k of this CTA's, for any logits: the key of the k-th largest is found by bits, two
 // a pass; those above it are listed, and as many of its equals, in order of ids, as there is room for.  Gives the team's turn.
-template <typename T, bool kTeam>
-__device__ __noinline__ int list_any(ScoreShared &S, u64 *list, Team<kTeam> team, RowView<T> row, uint32_t lo, uint32_t hi, uint32_t k) {
+template <typename T, int kLanes, bool kTeam>
+__device__ __noinline__ int list_any(ScoreShared<kLanes> &S, u64 *list, Team<kLanes, kTeam> team, RowView<T> row, uint32_t lo, uint32_t hi, uint32_t k) {
     constexpr int kVec = RowView<T>::kVec, kShift = Bits<T>::kShift, kBits = (32 - kShift + 1) & ~1;
     uint32_t some = 0;
-    for (uint32_t i = lo + threadIdx.x; i < hi; i += kRowThreads) {
+    for (uint32_t i = lo + team.thread; i < hi; i += kLanes) {
         float v[kVec];
         unpack(row.load(i), v, T());
 #pragma unroll
@@ -49,13 +52,13 @@ __device__ __noinline__ int list_any(ScoreShared &S, u64 *list, Team<kTeam> team
     }
     const float valid = team.sum(make_float4(some, 0, 0, 0)).x;   // counts up to 2^22 are exact in 32 bits
     const float want = fminf((float)k, valid);
-    if (threadIdx.x == 0) S.list_n = 0;
-    __syncthreads();
+    if (team.thread == 0) S.list_n = 0;
+    team.sync_cta();
     if (want == 0.0f) return team.turn;
     uint32_t cut = 0;
     for (int bit = kBits - 2; bit >= 0; bit -= 2) {
         uint32_t n1 = 0, n2 = 0, n3 = 0;
-        for (uint32_t i = lo + threadIdx.x; i < hi; i += kRowThreads) {
+        for (uint32_t i = lo + team.thread; i < hi; i += kLanes) {
             float v[kVec];
             unpack(row.load(i), v, T());
 #pragma unroll
@@ -68,7 +71,7 @@ __device__ __noinline__ int list_any(ScoreShared &S, u64 *list, Team<kTeam> team
         cut |= (n.z >= want ? 3u : n.y >= want ? 2u : n.x >= want ? 1u : 0u) << bit;
     }
     uint32_t above = 0, equal = 0;
-    for (uint32_t i = lo + threadIdx.x; i < hi; i += kRowThreads) {
+    for (uint32_t i = lo + team.thread; i < hi; i += kLanes) {
         float v[kVec];
         unpack(row.load(i), v, T());
 #pragma unroll
@@ -89,8 +92,8 @@ __device__ __noinline__ int list_any(ScoreShared &S, u64 *list, Team<kTeam> team
     const uint32_t need = (uint32_t)(want - n.x);
     const uint32_t quota = min(mine, need > before ? need - before : 0u);
     uint32_t seen = 0;
-    for (uint32_t i0 = lo; i0 < hi && seen < quota; i0 += kRowThreads) {
-        const uint32_t i = i0 + threadIdx.x;
+    for (uint32_t i0 = lo; i0 < hi && seen < quota; i0 += kLanes) {
+        const uint32_t i = i0 + team.thread;
         float v[kVec];
         uint32_t own = 0;
         if (i < hi) {
@@ -99,13 +102,17 @@ __device__ __noinline__ int list_any(ScoreShared &S, u64 *list, Team<kTeam> team
             for (int e = 0; e < kVec; e++) own += key_of(v[e]) >> kShift == cut;
         }
         const uint32_t upto = warp_incl_sum(own, team.lane);
-        __syncthreads();
-        if (team.lane == 31) S.scan[team.warp] = upto;
-        __syncthreads();
         uint32_t at = seen + upto - own;
-        for (int w = 0; w < kRowWarps; w++) {
-            if (w < team.warp) at += S.scan[w];
-            seen += S.scan[w];
+        if (kLanes == 32) {
+            seen += __shfl_sync(kFull, upto, 31);
+        } else {
+            __syncthreads();
+            if (team.lane == 31) S.scan[team.warp] = upto;
+            __syncthreads();
+            for (int w = 0; w < kLanes / 32; w++) {
+                if (w < team.warp) at += S.scan[w];
+                seen += S.scan[w];
+            }
         }
         if (own) {
 #pragma unroll
@@ -114,15 +121,16 @@ __device__ __noinline__ int list_any(ScoreShared &S, u64 *list, Team<kTeam> team
                     list[atomicAdd(&S.list_n, 1)] = entry_of(key_of(v[e]), i * kVec + e - row.shift);
         }
     }
-    __syncthreads();
+    team.sync_cta();
     return team.turn;
 }
 
 // The list's k largest in order, in S.best: each entry's place is the number of larger ones, counted by four threads.
-__device__ __forceinline__ uint32_t rank_list(ScoreShared &S, const u64 *list, uint32_t k) {
-    const uint32_t n = S.list_n, part = threadIdx.x & 3;
-    for (uint32_t i0 = 0; i0 + (threadIdx.x & ~31u) / 4 < n; i0 += kRowThreads / 4) {
-        const uint32_t i = i0 + threadIdx.x / 4;
+template <int kLanes, bool kTeam>
+__device__ __forceinline__ uint32_t rank_list(ScoreShared<kLanes> &S, const Team<kLanes, kTeam> &team, const u64 *list, uint32_t k) {
+    const uint32_t n = S.list_n, part = team.thread & 3;
+    for (uint32_t i0 = 0; i0 + (team.thread & ~31u) / 4 < n; i0 += kLanes / 4) {
+        const uint32_t i = i0 + team.thread / 4;
         const u64 one = list[min(i, n - 1)];
         uint32_t place = 0;
         for (uint32_t j = part; j < n; j += 4) place += list[j] > one;
@@ -130,7 +138,7 @@ __device__ __forceinline__ uint32_t rank_list(ScoreShared &S, const u64 *list, u
         place += __shfl_xor_sync(kFull, place, 2);
         if (i < n && part == 0 && place < k) S.best[place] = one;
     }
-    __syncthreads();
+    team.sync_cta();
     return min(n, k);
 }
 
@@ -138,21 +146,21 @@ __device__ __forceinline__ uint32_t rank_list(ScoreShared &S, const u64 *list, u
 // A bound from below on the k-th largest logit of the CTA's share.  Every thread is a group; with the j-th largest of each
 // warp's 32 largest logits in S.bound, and w j >= k of them, the least of w warps' bounds has k logits at or above it.  A
 // bound only rises, so that reading one early does no harm.
-struct Bound {
+template <int kLanes> struct Bound {
     uint32_t warps, j;                     // 0 warps: the share is too short for one
 
-    __device__ __forceinline__ Bound(uint32_t vecs, uint32_t k) : warps(min((uint32_t)kRowWarps, vecs / 32)), j(0) {
+    __device__ __forceinline__ Bound(uint32_t vecs, uint32_t k) : warps(min((uint32_t)kLanes / 32, vecs / 32)), j(0) {
         if (warps) j = (k + warps - 1) / warps;
         if (j > 32) warps = 0;
     }
-    __device__ __forceinline__ float least(const ScoreShared &S, float low) const {
+    __device__ __forceinline__ float least(const ScoreShared<kLanes> &S, float low) const {
         if (!warps) return low;
         float b = INFINITY;
         for (uint32_t w = 0; w < warps; w++) b = fminf(b, *(const volatile float *)&S.bound[w]);
         return b;
     }
     // this warp's, from its lanes' largest logits: by taking out the largest where few are asked for, by sorting else
-    __device__ __forceinline__ void write(ScoreShared &S, float v, int lane, int warp) const {
+    __device__ __forceinline__ void write(ScoreShared<kLanes> &S, float v, int lane, int warp) const {
         if (warp >= (int)warps) return;
         if (j <= 8) {
             uint32_t key = key_of(v), top = 0;
@@ -176,23 +184,23 @@ struct Bound {
 };
 
 // The tile's vectors that hold a logit at or above the bound: their places, since few of them turn out to matter.
-template <typename T, int kSize>
-__device__ __forceinline__ void find(ScoreShared &S, const typename Words<T>::W (&each)[kSize], uint32_t i0, float bound) {
+template <typename T, int kLanes>
+__device__ __forceinline__ void find(ScoreShared<kLanes> &S, const typename Words<T>::W (&each)[kSize], uint32_t i0, float bound) {
 #pragma unroll
     for (int u = 0; u < kSize; u++) {
         const float m = Words<T>::largest(each[u]);
         if (m >= bound && m > Usual<T>::kLow) {
             const uint32_t at = atomicAdd(&S.found_n, 1);
-            if (at < kFound) S.found[at] = Tile<T, kSize>::place(i0, u);
+            if (at < S.kFound) S.found[at] = Tile<T, kSize, kLanes>::place(i0, u);
         }
     }
 }
 
 // Their logits at or above the bound, which has risen since, to the list.  (Read once more: 32 bytes for each of them.)
-template <typename T>
-__device__ __forceinline__ void list_found(ScoreShared &S, u64 *list, const RowView<T> &row, float bound) {
+template <typename T, int kLanes>
+__device__ __forceinline__ void list_found(ScoreShared<kLanes> &S, u64 *list, const RowView<T> &row, float bound) {
     constexpr int kVec = RowView<T>::kVec;
-    for (uint32_t i = threadIdx.x; i < min(S.found_n, (uint32_t)kFound); i += kRowThreads) {
+    for (uint32_t i = row_thread<kLanes>(); i < min(S.found_n, (uint32_t)S.kFound); i += kLanes) {
         const uint32_t place = S.found[i];
         float v[kVec];
         unpack(row.load(place), v, T());
@@ -203,20 +211,23 @@ __device__ __forceinline__ void list_found(ScoreShared &S, u64 *list, const RowV
 #pragma unroll
         for (int e = 0; e < kVec; e++)
             if (some >> e & 1) {
-                if (at < kList) list[at] = entry_of(key_of(v[e]), place * kVec - row.shift + e);
+                if (at < S.kList) list[at] = entry_of(key_of(v[e]), place * kVec - row.shift + e);
                 at++;
             }
     }
 }
 
-template <typename T, bool kTeam, bool kTops>
-__global__ void __launch_bounds__(kRowThreads, 4) k_logprobs(ScoreParams P, uint32_t n_team) {
-    using Tiles = Tile<T, kSize>;
-    extern __shared__ __align__(16) unsigned char tiles[];
-    ScoreShared &S = *(ScoreShared *)(tiles + kFeedBytes);   // without alternatives the team's part alone
-    Team<kTeam> team(S.team, n_team);
+template <typename T, int kLanes, bool kTeam, bool kTops>
+__global__ void __launch_bounds__(kLanes == 32 ? kWarpRows * 32 : kLanes, kLanes == 32 ? 4 : 1024 / kLanes) k_logprobs(ScoreParams P, uint32_t n_team, uint32_t n_rows) {
+    using Tiles = Tile<T, kSize, kLanes>;
+    using Shared = ScoreShared<kLanes>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const uint32_t r = kLanes == 32 ? blockIdx.x * kWarpRows + threadIdx.x / 32 : kTeam ? blockIdx.x / n_team : blockIdx.x;
+    if (kLanes == 32 && r >= n_rows) return;
+    unsigned char *const tiles = smem + (kLanes == 32 ? threadIdx.x / 32 * kScoreBytes<kLanes, kTops> : 0);
+    Shared &S = *(Shared *)(tiles + Shared::kFeedBytes);
+    Team<kLanes, kTeam> team(S.team, n_team);
     team.arrive();
-    const uint32_t r = kTeam ? blockIdx.x / n_team : blockIdx.x;
     const RowView<T> row(P.row.logits, P.row.stride, r, P.row.n_tok);
     const uint32_t vecs = row.vecs(), share = (vecs + team.size - 1) / team.size;
     const uint32_t lo = min(vecs, team.rank * share), hi = min(vecs, lo + share);
@@ -224,18 +235,18 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_logprobs(ScoreParams P, uint
     const uint32_t k = kTops ? P.n_top : 0;
     int32_t id = -1;
     float given = 0.0f;
-    if (threadIdx.x == 0 && team.rank == 0 && P.logprob) {
+    if (team.thread == 0 && team.rank == 0 && P.logprob) {
         id = P.ids[r];
         if (id >= 0 && (uint32_t)id < P.row.n_tok) given = to_f32(row.at[row.shift + id]);
     }
 
-    const Feed<T, kSize> feed(row, tiles, lo, hi);
+    const Feed<T, kSize, kLanes> feed(row, tiles, lo, hi);
     Running<T, true> sums(c2);
-    const Bound tops(hi - lo, k);
+    const Bound<kLanes> tops(hi - lo, k);
     float count = 0.0f;
     u64 *const list = (u64 *)tiles;        // once the tiles are through
     if (kTops) {
-        if (threadIdx.x == 0) S.list_n = S.found_n = 0;
+        if (team.thread == 0) S.list_n = S.found_n = 0;
         bool stale = true;
         float bound = Usual<T>::kLow;
         for (uint32_t n = 0, i0 = lo; i0 < hi || n == 0; i0 += Tiles::kVecs, n++) {
@@ -247,16 +258,16 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_logprobs(ScoreParams P, uint
             stale = (n & (n + 1)) != 0;    // after 1, 2, 4... tiles
             if (!stale) {
                 tops.write(S, sums.most, team.lane, team.warp);
-                if (n == 0) __syncthreads();
+                if (kLanes == 32 || n == 0) team.sync_cta();
                 bound = tops.least(S, Usual<T>::kLow);
             }
-            if (m >= bound && m > Usual<T>::kLow) find<T, kSize>(S, each, i0, bound);
+            if (m >= bound && m > Usual<T>::kLow) find<T, kLanes>(S, each, i0, bound);
         }
         if (stale) tops.write(S, sums.most, team.lane, team.warp);
-        __syncthreads();
-        list_found(S, list, row, tops.least(S, Usual<T>::kLow));
-        __syncthreads();
-        const bool over = S.found_n > kFound || S.list_n > kList;
+        team.sync_cta();
+        list_found<T, kLanes>(S, list, row, tops.least(S, Usual<T>::kLow));
+        team.sync_cta();
+        const bool over = S.found_n > S.kFound || S.list_n > S.kList;
         count = over ? -0x1p24f : fminf((float)S.list_n, (float)k);
     } else {
         for (uint32_t n = 0, i0 = lo; i0 < hi; i0 += Tiles::kVecs, n++) {
@@ -266,31 +277,31 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_logprobs(ScoreParams P, uint
         }
     }
     Softmax all = softmax_join(team, sums, c2, count);
-    if (!kTeam && !kTops && team.warp > 0 && usual<T>(all.m, c)) return;
-    if (!usual<T>(all.m, c)) all = softmax_any<T, kTeam>(team, lo, hi, c, [=](uint32_t i) { return row.load(i); });
+    if (kLanes > 32 && !kTeam && !kTops && team.warp > 0 && usual<T>(all.m, c)) return;
+    if (!usual<T>(all.m, c)) all = softmax_any<T, kLanes, kTeam>(team, lo, hi, c, [=](uint32_t i) { return row.load(i); });
     // more equal or masked logits than the list holds, or fewer others than were asked for
-    if (kTops && count < (float)min(k, P.row.n_tok)) team.turn = list_any<T, kTeam>(S, list, team, row, lo, hi, k);
+    if (kTops && count < (float)min(k, P.row.n_tok)) team.turn = list_any<T, kLanes, kTeam>(S, list, team, row, lo, hi, k);
 
     const bool none = all.m == -INFINITY;
     const float log_s = none ? 0.0f : logf(all.s);
-    if (threadIdx.x == 0 && team.rank == 0) {
+    if (team.thread == 0 && team.rank == 0) {
         if (P.norm) P.norm[2 * (uint64_t)r] = all.m, P.norm[2 * (uint64_t)r + 1] = log_s;
         if (P.entropy) P.entropy[r] = none ? 0.0f : log_s - all.sz / all.s;
         if (P.logprob) P.logprob[r] = id < 0 || (uint32_t)id >= P.row.n_tok ? 0.0f : none ? -INFINITY : z_any(given, all.m, c) - log_s;
     }
     if (!kTops) return;
-    uint32_t n = rank_list(S, list, k), total = n;
-    const u64 one = S.best[min(threadIdx.x, k - 1)];   // this thread's, of the n
-    uint32_t place = threadIdx.x;
+    uint32_t n = rank_list(S, team, list, k), total = n;
+    const u64 one = S.best[min(team.thread, k - 1)];   // this thread's, of the n
+    uint32_t place = team.thread;
     if (kTeam) {
         team.exchange(make_float4((float)n, 0, 0, 0));
         total = 0;
         for (uint32_t o = 0; o < team.size; o++) total += (uint32_t)team.S.slot[team.turn][o].x;
         // every CTA's list, then each of its own finds its place by those that are larger
         for (uint32_t o = 0; o < team.size; o++)
-            if (o != team.rank && threadIdx.x < (uint32_t)team.S.slot[team.turn][o].x) list[o * k + threadIdx.x] = far_load(&S.best[threadIdx.x], o);
+            if (o != team.rank && team.thread < (uint32_t)team.S.slot[team.turn][o].x) list[o * k + team.thread] = far_load(&S.best[team.thread], o);
         __syncthreads();
-        if (threadIdx.x < n)
+        if (team.thread < n)
             for (uint32_t o = 0; o < team.size; o++) {
                 if (o == team.rank) continue;
                 uint32_t x = 0, y = (uint32_t)team.S.slot[team.turn][o].x;
@@ -302,13 +313,13 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_logprobs(ScoreParams P, uint
                 place += x;
             }
     }
-    if (threadIdx.x < n && place < k) {
+    if (team.thread < n && place < k) {
         const uint64_t at = (uint64_t)r * k + place;
         if (P.top_ids) P.top_ids[at] = (int32_t)~(uint32_t)one;
         if (P.top_logprob) P.top_logprob[at] = z_any(key_value((uint32_t)(one >> 32)), all.m, c) - log_s;
     }
-    if (team.rank == 0 && threadIdx.x >= total && threadIdx.x < k) {
-        const uint64_t at = (uint64_t)r * k + threadIdx.x;
+    if (team.rank == 0 && team.thread >= total && team.thread < k) {
+        const uint64_t at = (uint64_t)r * k + team.thread;
         if (P.top_ids) P.top_ids[at] = -1;
         if (P.top_logprob) P.top_logprob[at] = -INFINITY;
     }
@@ -326,16 +337,18 @@ struct ScoreGradParams {
 };
 
 // No sums, so that a row is cut where it suits: a CTA takes `each` tiles of it.
-template <typename T, bool kEntropy>
-__global__ void __launch_bounds__(kRowThreads) k_logprobs_backward(ScoreGradParams P, uint32_t cuts, uint32_t each) {
+template <typename T, int kLanes, bool kEntropy>
+__global__ void __launch_bounds__(256) k_logprobs_backward(ScoreGradParams P, uint32_t cuts, uint32_t each, uint32_t n_rows) {
     constexpr int kVec = RowView<T>::kVec;
-    using Tiles = Tile<T, kSize>;
+    using Tiles = Tile<T, kSize, kLanes>;
     extern __shared__ __align__(16) unsigned char tiles[];
-    const uint32_t r = blockIdx.x / cuts, cut = blockIdx.x % cuts;
+    const uint32_t unit = kLanes == 32 ? blockIdx.x * kWarpRows + threadIdx.x / 32 : blockIdx.x, r = unit / cuts, cut = unit % cuts;
+    if (r >= n_rows) return;
     const RowView<T> row(P.row.logits, P.row.stride, r, P.row.n_tok), out(P.out, P.out_stride, r, P.row.n_tok);
     const uint32_t lo = cut * each * Tiles::kVecs, hi = min(row.vecs(), lo + each * Tiles::kVecs);
     if (lo >= hi) return;
-    const Feed<T, kSize> feed(row, tiles, lo, hi);
+    using F = Feed<T, kSize, kLanes>;
+    const F feed(row, tiles + (kLanes == 32 ? threadIdx.x / 32 * (F::kAhead * F::kBytes) : 0), lo, hi);
     const float c = P.row.inverse(r);
     const float m = P.norm[2 * (uint64_t)r], log_s = P.norm[2 * (uint64_t)r + 1];
     const int32_t id = P.ids ? P.ids[r] : -1;
@@ -386,32 +399,48 @@ __global__ void __launch_bounds__(kRowThreads) k_logprobs_backward(ScoreGradPara
     }
 }
 
-template <typename T, bool kTeam, bool kTops> int launch_team(bpe_ctx *ctx, const ScoreParams &P, uint32_t n_rows, uint32_t team) {
-    auto k = k_logprobs<T, kTeam, kTops>;
-    constexpr size_t kShared = kFeedBytes + (kTops ? sizeof(ScoreShared) : sizeof(TeamShared));
+template <typename T, int kLanes, bool kTeam, bool kTops>
+int launch_team(bpe_ctx *ctx, const ScoreParams &P, uint32_t n_rows, uint32_t team) {
+    auto k = k_logprobs<T, kLanes, kTeam, kTops>;
+    constexpr uint32_t kRows = kLanes == 32 ? kWarpRows : 1, kShared = kScoreBytes<kLanes, kTops> * kRows;
     static std::atomic<uint64_t> devices{0};
     BPE_CUDA(ctx, allow_shared(k, ctx->device, kShared, devices), "head_logprobs");
-    return launch_rows(ctx, "head_logprobs launch", k, P, n_rows, team, kRowThreads, kTeam, kShared);
+    return launch_rows(ctx, "head_logprobs launch", k, P, (n_rows + kRows - 1) / kRows, team, kLanes * kRows, kTeam, kShared, n_rows);
 }
-
 template <typename T> int launch_logprobs(bpe_ctx *ctx, const ScoreParams &P, uint32_t n_rows) {
-    const uint32_t team = row_team(n_rows, P.row.n_tok * (uint32_t)sizeof(T), (uint32_t)ctx->sm_count);
-    if (P.n_top && (P.top_ids || P.top_logprob))
-        return team > 1 ? launch_team<T, true, true>(ctx, P, n_rows, team) : launch_team<T, false, true>(ctx, P, n_rows, 1);
-    return team > 1 ? launch_team<T, true, false>(ctx, P, n_rows, team) : launch_team<T, false, false>(ctx, P, n_rows, 1);
+    const uint32_t bytes = P.row.n_tok * (uint32_t)sizeof(T), sms = (uint32_t)ctx->sm_count, team = row_team(n_rows, bytes, sms);
+    if (!P.n_top || !(P.top_ids || P.top_logprob)) {
+        if (row_lanes(n_rows, bytes, sms, 32, 40) == 32) return launch_team<T, 32, false, false>(ctx, P, n_rows, 1);
+        return team > 1 ? launch_team<T, kMost, true, false>(ctx, P, n_rows, team) : launch_team<T, kMost, false, false>(ctx, P, n_rows, 1);
+    }
+    // The threads are the groups of Bound: with fewer than 1.5 for each alternative the bound leaves more than the list holds.
+    int least = 32;
+    while (least < kMost && (uint32_t)least * 2 < P.n_top * 3) least *= 2;
+    switch (row_lanes(n_rows, bytes, sms, least, 4)) {
+    case 32: return launch_team<T, 32, false, true>(ctx, P, n_rows, 1);
+    case 64: return launch_team<T, 64, false, true>(ctx, P, n_rows, 1);
+    case 128: return launch_team<T, 128, false, true>(ctx, P, n_rows, 1);
+    default: return team > 1 ? launch_team<T, kMost, true, true>(ctx, P, n_rows, team) : launch_team<T, kMost, false, true>(ctx, P, n_rows, 1);
+    }
 }
 
-template <typename T> int launch_backward(bpe_ctx *ctx, const ScoreGradParams &P, uint32_t n_rows) {
-    const uint32_t vecs = (P.row.n_tok + RowView<T>::kVec - 1) / RowView<T>::kVec + (row_shifts<T>(P.row.logits, P.row.stride, n_rows) ? 1 : 0);
-    const uint32_t tiles = (vecs + Tile<T, kSize>::kVecs - 1) / Tile<T, kSize>::kVecs;
+template <typename T, int kLanes> int launch_backward(bpe_ctx *ctx, const ScoreGradParams &P, uint32_t n_rows) {
+    using F = Feed<T, kSize, kLanes>;
+    constexpr uint32_t kRows = 256 / kLanes, kVec = RowView<T>::kVec;
+    const uint32_t vecs = (P.row.n_tok + kVec - 1) / kVec + (row_shifts<T>(P.row.logits, P.row.stride, n_rows) ? 1 : 0);
+    const uint32_t tiles = (vecs + F::Tiles::kVecs - 1) / F::Tiles::kVecs;
     uint32_t each = 1;
-    while (each < kGradTiles && each < tiles && (uint64_t)n_rows * ((tiles + each) / (each + 1)) >= 16ull * ctx->sm_count) each++;
+    while (each < kGradTiles && each < tiles && (uint64_t)n_rows * ((tiles + each) / (each + 1)) >= 16ull * kRows * ctx->sm_count) each++;
     const uint32_t cuts = (tiles + each - 1) / each;
-    if ((uint64_t)n_rows * cuts > 0x7FFFFFFFu) return fail(ctx, BPE_ERR_INVALID_ARG, "head_logprobs_backward: %u rows", n_rows);
-    auto k = P.grad_entropy ? k_logprobs_backward<T, true> : k_logprobs_backward<T, false>;
-    k<<<n_rows * cuts, kRowThreads, kFeedBytes, ctx->stream>>>(P, cuts, each);
+    const uint64_t ctas = ((uint64_t)n_rows * cuts + kRows - 1) / kRows;
+    if (ctas > 0x7FFFFFFFu) return fail(ctx, BPE_ERR_INVALID_ARG, "head_logprobs_backward: too many rows");
+    auto k = P.grad_entropy ? k_logprobs_backward<T, kLanes, true> : k_logprobs_backward<T, kLanes, false>;
+    k<<<(uint32_t)ctas, 256, F::kAhead * F::kBytes * kRows, ctx->stream>>>(P, cuts, each, n_rows);
     BPE_CUDA(ctx, cudaGetLastError(), "head_logprobs_backward launch");
     return BPE_OK;
+}
+template <typename T> int launch_backward(bpe_ctx *ctx, const ScoreGradParams &P, uint32_t n_rows) {
+    return n_rows >= 256 && P.row.n_tok * sizeof(T) <= 10240 ? launch_backward<T, 32>(ctx, P, n_rows) : launch_backward<T, kMost>(ctx, P, n_rows);
 }
 
 }  // namespace

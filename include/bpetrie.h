@@ -519,8 +519,8 @@ int head_sample(bpe_ctx *ctx, const void *d_logits, uint64_t stride, int type, u
  * bits (0 where logit == m, -infinity where logit - m is), s = the sum of exp(z),
  * p = exp(z) / s.  A temperature below 2^-126 (0, negative, NaN) is the limit:
  * the largest logits share the row evenly; an infinite one shares it among all
- * above -infinity.  Sums are in 32 bits, in an order that n_rows, n_tok, the
- * type and the device alone decide, so that equal calls give equal results.
+ * above -infinity.  Sums are in 32 bits, in an order that the call's sizes,
+ * types, alignment and outputs decide, so that equal calls give equal results.
  * temperature is replaced by d_temperature (nullable, n_rows values). */
 #define BPE_HEAD_MAX_TOP 128u          /* alternatives of a row */
 
