@@ -242,6 +242,8 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kCtas<kLanes>) k_distill(Dis
         }
         sums.add(t, t.raise_all(), c2);
     }
+    // A row that was not kept is read again, from L2 as a rule; its first tiles come while the sums are joined.
+    if (kGrad && !kept && reads) feed.start();
     float none_counted = 0.0f;
     Softmax free = softmax_join(team, sums, c2, none_counted);
     const bool fast = usual<T>(free.m, c);
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kCtas<kLanes>) k_distill(Dis
         const uint32_t i0 = lo + n * Tiles::kVecs;
         Tiles t;
         if (kept) feed.again(t, n);
-        else t.load(row, i0, hi);
+        else feed.next(t, n);
         const bool direct = out.shift == row.shift && Tiles::inside(row, i0, hi);
 #pragma unroll
         for (int u = 0; u < kSize; u++) {

@@ -247,30 +247,6 @@ template <typename T, int kSize, int kLanes> struct Tile {
     __device__ __forceinline__ static uint4 fill() {
         return make_uint4(Bits<T>::kNegInf, Bits<T>::kNegInf, Bits<T>::kNegInf, Bits<T>::kNegInf);
     }
-    // the vectors from i0, -infinity from `hi` on; the loads of all are under way at once
-    __device__ __forceinline__ void load(const RowView<T> &row, uint32_t i0, uint32_t hi) {
-        if (inside(row, i0, hi)) {
-#pragma unroll
-            for (int u = 0; u < kSize; u++) q[u] = *((const uint4 *)row.at + place(i0, u));
-            return;
-        }
-#pragma unroll
-        for (int u = 0; u < kSize; u++) {
-            const uint32_t i = place(i0, u);
-            q[u] = fill();
-            if (i < hi && row.whole(i)) q[u] = *((const uint4 *)row.at + i);
-        }
-#pragma unroll 1
-        for (int u = 0; u < kSize; u++) {   // the row's first and last vectors
-            const uint32_t i = place(i0, u);
-            if (i < hi && !row.whole(i)) {
-                const uint4 one = row.load(i);
-#pragma unroll
-                for (int o = 0; o < kSize; o++)
-                    if (o == u) q[o] = one;
-            }
-        }
-    }
 };
 
 // The CTA's share of a row on its way through shared memory, kAhead tiles ahead of where it is read.  Every thread copies
@@ -289,10 +265,11 @@ template <typename T, int kSize, int kLanes> struct Feed {
     __device__ __forceinline__ Feed(const RowView<T> &r, void *shared, uint32_t lo_, uint32_t hi_, bool kept_ = false, bool reads = true)
         : row(r), from((const char *)r.at + (uint64_t)(lo_ + row_thread<kLanes>()) * 16),
           mine((uint32_t)__cvta_generic_to_shared(shared) + row_thread<kLanes>() * 16), lo(lo_), hi(hi_), kept(kept_) {
-        if (reads) {
+        if (reads) start();
+    }
+    __device__ __forceinline__ void start() const {
 #pragma unroll
-            for (int n = 0; n < kAhead; n++) ask(n);
-        }
+        for (int n = 0; n < kAhead; n++) ask(n);
     }
     __device__ __forceinline__ uint32_t slot(uint32_t n) const { return mine + (kept ? n : n % kAhead) * kBytes; }
     static __device__ __forceinline__ void copy(uint32_t to, const void *from) {
@@ -565,10 +542,10 @@ inline int row_lanes(uint32_t n_rows, uint32_t bytes, uint32_t sms, int least, u
     return kMost;
 }
 
-// CTAs of a row: as many as keep every SM at work with some to spare, of 16 KB at least.
+// CTAs of a row: more than one where there are too few rows for the SMs, of 32 KB at least.
 inline uint32_t row_team(uint32_t n_rows, uint32_t bytes, uint32_t sms) {
     uint32_t team = 1;
-    while (team < (uint32_t)kMaxTeam && (uint64_t)n_rows * team * 2 <= 6ull * sms && bytes >= team * 2 * 16384u) team *= 2;
+    while (team < (uint32_t)kMaxTeam && (uint64_t)n_rows * team * 2 <= 2ull * sms && bytes >= team * 2 * 32768u) team *= 2;
     return team;
 }
 
