@@ -29,7 +29,7 @@ int distill_f16(bpe_ctx *ctx, const DistillParams &P, uint32_t n_rows);
 namespace {
 
 constexpr int kEntries = (int)BPE_HEAD_MAX_TOP;   // alternatives that a teacher lists
-constexpr uint32_t kMostShared = 200 * 1024;      // of a CTA
+constexpr uint32_t kMostShared = 200 * 1024, kSmShared = 228 * 1024;   // of a CTA, of an SM
 constexpr uint32_t kKeep = 4;                     // tiles of a row that leave room for three CTAs on an SM
 
 constexpr int kHash = 256;
@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kCtas<kLanes>) k_distill(Dis
         team.sync_cta();
     }
     if (lists) list.weigh(S, P, c, team.lane);
+    if (kLanes == 32) __syncwarp();
 
     // The softmax of all tokens, or of the unlisted ones, whose share among themselves is exact then however little of the
     // row they hold.
@@ -342,12 +343,21 @@ template <typename T, bool kRest, bool kGrad> int launch(bpe_ctx *ctx, const Dis
     };
     tile = kSize * lanes;
     if (lanes == 32 && place(false).row_bytes * kWarpRows > kMostShared / 2) lanes = kMost, tile = kSize * lanes;   // the bits
-    if (lanes == kMost) {
-        team = row_team(n_rows, bytes, sms);
-        while (kGrad && team < kMaxTeam && tiles() > kKeep) team *= 2;
-    }
     const uint32_t rows = lanes == 32 ? kWarpRows : 1;
-    const bool kept = kGrad && place(true).row_bytes * rows <= kMostShared;
+    bool kept = kGrad;
+    if (lanes == kMost) {
+        team = row_team(n_rows, bytes, sms, kGrad ? 4 : 2);
+        if (kGrad && tiles() > kKeep) {
+            // Longer rows stay where all CTAs run at once.  Else they are read again while L2 holds them: 64 MB of it for the
+            // rows at hand.  (In us, read again from L2 / kept in 64 KB of more CTAs / of one CTA: 1,000 x 65,536 bf16 55 / 56 /
+            // 74, with the rest 57 / 61 / 82; 1,000 x 250,000 in 4 CTAs 206 / in 8 226 with the rest, in 1 252 from DRAM.)
+            const uint32_t fit = kSmShared / (place(true).row_bytes + 1024);
+            kept = (uint64_t)n_rows * team <= (uint64_t)sms * (fit < 3 ? fit : 3);
+            auto in_flight = [&] { const uint32_t n = 3 * sms / team; return (uint64_t)(n_rows < n ? n_rows : n) * bytes; };
+            while (!kept && team < kMaxTeam && in_flight() > 64u << 20) team *= 2;
+        }
+    }
+    kept = kept && place(true).row_bytes * rows <= kMostShared;
     while (lanes == kMost && team < kMaxTeam && place(kept).row_bytes > kMostShared) team *= 2;
     const Place at = place(kept);
     if constexpr (kGrad) {

@@ -408,7 +408,7 @@ int launch_team(bpe_ctx *ctx, const ScoreParams &P, uint32_t n_rows, uint32_t te
     return launch_rows(ctx, "head_logprobs launch", k, P, (n_rows + kRows - 1) / kRows, team, kLanes * kRows, kTeam, kShared, n_rows);
 }
 template <typename T> int launch_logprobs(bpe_ctx *ctx, const ScoreParams &P, uint32_t n_rows) {
-    const uint32_t bytes = P.row.n_tok * (uint32_t)sizeof(T), sms = (uint32_t)ctx->sm_count, team = row_team(n_rows, bytes, sms);
+    const uint32_t bytes = P.row.n_tok * (uint32_t)sizeof(T), sms = (uint32_t)ctx->sm_count, team = row_team(n_rows, bytes, sms, 2);
     if (!P.n_top || !(P.top_ids || P.top_logprob)) {
         if (row_lanes(n_rows, bytes, sms, 32, 40) == 32) return launch_team<T, 32, false, false>(ctx, P, n_rows, 1);
         return team > 1 ? launch_team<T, kMost, true, false>(ctx, P, n_rows, team) : launch_team<T, kMost, false, false>(ctx, P, n_rows, 1);
