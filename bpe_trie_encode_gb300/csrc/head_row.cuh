@@ -12,8 +12,9 @@ namespace bpe {
 typedef unsigned long long u64;
 
 constexpr int kMaxTeam = 8;                // CTAs of a row: a cluster
-constexpr int kMost = 256, kMostWarps = kMost / 32;   // threads of a row in a CTA
-// A row's threads, kLanes: a warp of a CTA that takes eight rows, or a CTA of 64, 128 or 256.
+constexpr int kMost = 256;                 // threads of a row in a CTA of a cluster
+constexpr int kMostWarps = 16;             // of any CTA
+// A row's threads, kLanes: a warp of a CTA that takes eight rows, or a CTA of 64, 128, 256 or 512.
 constexpr int kWarpRows = 8;
 
 struct RowParams {
@@ -228,16 +229,12 @@ template <typename T, int kSize, int kLanes> struct Tile {
     static constexpr uint32_t kVecs = kSize * kLanes;
     uint4 q[kSize];
 
-    // Raises the tile; gives its largest logit, and each vector's largest word.
-    __device__ __forceinline__ float raise_all(typename Words<T>::W (&each)[kSize]) {
-        typename Words<T>::W m = each[0] = raise<T>(q[0]);
-#pragma unroll
-        for (int u = 1; u < kSize; u++) m = Words<T>::larger(m, each[u] = raise<T>(q[u]));
-        return Words<T>::largest(m);
-    }
+    // Raises the tile; gives its largest logit.
     __device__ __forceinline__ float raise_all() {
-        typename Words<T>::W each[kSize];
-        return raise_all(each);
+        typename Words<T>::W m = raise<T>(q[0]);
+#pragma unroll
+        for (int u = 1; u < kSize; u++) m = Words<T>::larger(m, raise<T>(q[u]));
+        return Words<T>::largest(m);
     }
     __device__ __forceinline__ static uint32_t place(uint32_t i0, int u) { return i0 + u * kLanes + row_thread<kLanes>(); }
     // No vector from i0 on ends outside the row or the share.
@@ -275,7 +272,8 @@ template <typename T, int kSize, int kLanes> struct Feed {
     static __device__ __forceinline__ void copy(uint32_t to, const void *from) {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
     }
-    // tile n's copies, as one group (an empty one behind the share, but for its first)
+    __device__ __forceinline__ uint32_t steps() const { return (hi - lo + Tiles::kVecs - 1) / Tiles::kVecs; }
+    // tile n's copies, as one group (an empty one behind the share)
     __device__ __forceinline__ void ask(uint32_t n) const {
         const uint32_t i0 = lo + n * Tiles::kVecs;
         if (Tiles::inside(row, i0, hi)) {
@@ -283,7 +281,7 @@ template <typename T, int kSize, int kLanes> struct Feed {
             const char *const f = from + (uint64_t)n * kBytes;
 #pragma unroll
             for (int u = 0; u < kSize; u++) copy(to + u * kStep, f + u * kStep);
-        } else if (i0 < hi || n == 0) {
+        } else if (i0 < hi) {
             ask_edge(i0, slot(n));
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -374,7 +372,7 @@ struct TeamShared {
 
 // The threads of a row: a warp, a CTA, or the CTAs of a cluster.
 template <int kLanes, bool kTeam> struct Team {
-    static_assert(kLanes <= kMost && (!kTeam || kLanes == kMost), "clusters are of full CTAs");
+    static_assert(kLanes <= 32 * kMostWarps && (!kTeam || kLanes == kMost), "clusters are of CTAs of kMost");
     static constexpr bool kWarp = kLanes == 32;
     static constexpr int kWarps = kLanes / 32;
     TeamShared &S;         // not there for a warp

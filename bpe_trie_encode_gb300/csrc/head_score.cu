@@ -21,16 +21,18 @@ struct ScoreParams {
 // Of a row's threads, which take up to as many alternatives.
 template <int kLanes> struct ScoreShared {
     static constexpr int kTop = kLanes < (int)BPE_HEAD_MAX_TOP ? kLanes : (int)BPE_HEAD_MAX_TOP;
-    static constexpr int kFound = 8 * kLanes;                       // vectors that may hold alternatives
+    static constexpr int kGroups = kLanes < 256 ? 16 : 32;          // of a thread's tiles
+    static constexpr int kFound = 4 * kLanes;                       // threads' groups that may hold alternatives
     static constexpr int kList = kLanes < 128 ? 8 * kLanes : 1024;  // tokens that may be among them, in the tiles' place
     static constexpr uint32_t kFeedBytes = Feed<float, kSize, kLanes>::kAhead * kSize * kLanes * 16;
-    static_assert(kTop <= kLanes && (kLanes < kMost || kMaxTeam * kTop <= kList) && kList * sizeof(u64) <= kFeedBytes,
+    static_assert(kTop <= kLanes && (kLanes != kMost || kMaxTeam * kTop <= kList) && kList * sizeof(u64) <= kFeedBytes,
                   "one thread for each alternative, room for a team's");
     TeamShared team;
     uint32_t list_n, found_n, scan[kMostWarps];
     float bound[kMostWarps];
     u64 best[kTop];                        // in order
     uint32_t found[kFound];
+    uint16_t most[kGroups][kLanes];        // the largest logit of each
 };
 // Shared memory of a row: its tiles, and without alternatives the team's part alone.
 template <int kLanes, bool kTops>
@@ -143,9 +145,11 @@ __device__ __forceinline__ uint32_t rank_list(ScoreShared<kLanes> &S, const Team
 }
 
 // ------------------------------------------- alternatives, on the way ---
-// A bound from below on the k-th largest logit of the CTA's share.  Every thread is a group; with the j-th largest of each
-// warp's 32 largest logits in S.bound, and w j >= k of them, the least of w warps' bounds has k logits at or above it.  A
-// bound only rises, so that reading one early does no harm.
+// While a row goes by, every thread notes the largest logit of each of its tiles (or of up to kGroups groups of them).  Then
+// comes a bound from below on the k-th largest logit of the CTA's share: with the j-th largest of each warp's 32 largest logits
+// in S.bound, and w j >= k of them, the least of w warps' bounds has k logits at or above it.  The groups that reach it, some
+// 1.5 k, are read once more, and what reaches it of them is ranked.  (Listing on the way, with a bound that rises, cost 80 to
+// 280 instructions a tile of 193: 256 x 65,536 bf16, 20 alternatives, 13.7 us.)
 template <int kLanes> struct Bound {
     uint32_t warps, j;                     // 0 warps: the share is too short for one
 
@@ -156,7 +160,7 @@ template <int kLanes> struct Bound {
     __device__ __forceinline__ float least(const ScoreShared<kLanes> &S, float low) const {
         if (!warps) return low;
         float b = INFINITY;
-        for (uint32_t w = 0; w < warps; w++) b = fminf(b, *(const volatile float *)&S.bound[w]);
+        for (uint32_t w = 0; w < warps; w++) b = fminf(b, S.bound[w]);
         return b;
     }
     // this warp's, from its lanes' largest logits: by taking out the largest where few are asked for, by sorting else
@@ -168,7 +172,7 @@ template <int kLanes> struct Bound {
                 top = __reduce_max_sync(kFull, key);
                 if (lane == __ffs(__ballot_sync(kFull, key == top)) - 1) key = 0;
             }
-            if (lane == 0) *(volatile float *)&S.bound[warp] = key_value(top);
+            if (lane == 0) S.bound[warp] = key_value(top);
             return;
         }
 #pragma unroll
@@ -179,34 +183,47 @@ template <int kLanes> struct Bound {
                 const bool first = (lane & d) == 0, down = (lane & size) == 0 || size == 32;   // largest first
                 v = first == down ? fmaxf(v, o) : fminf(v, o);
             }
-        if (lane == (int)j - 1) *(volatile float *)&S.bound[warp] = v;
+        if (lane == (int)j - 1) S.bound[warp] = v;
     }
 };
 
-// The tile's vectors that hold a logit at or above the bound: their places, since few of them turn out to matter.
+// A group's largest logit in 16 bits, no less than it is.
+__device__ __forceinline__ uint16_t note(float v, float) { return __bfloat16_as_ushort(__float2bfloat16_ru(v)); }
+__device__ __forceinline__ uint16_t note(float v, __nv_bfloat16) { return (uint16_t)(__float_as_uint(v) >> 16); }
+__device__ __forceinline__ uint16_t note(float v, __half) { return __half_as_ushort(__float2half_rn(v)); }
+__device__ __forceinline__ float noted(uint16_t b, float) { return __uint_as_float((uint32_t)b << 16); }
+__device__ __forceinline__ float noted(uint16_t b, __nv_bfloat16) { return __uint_as_float((uint32_t)b << 16); }
+__device__ __forceinline__ float noted(uint16_t b, __half) { return __half2float(__ushort_as_half(b)); }
+
+// This thread's groups that reach the bound.
 template <typename T, int kLanes>
-__device__ __forceinline__ void find(ScoreShared<kLanes> &S, const typename Words<T>::W (&each)[kSize], uint32_t i0, float bound) {
-#pragma unroll
-    for (int u = 0; u < kSize; u++) {
-        const float m = Words<T>::largest(each[u]);
+__device__ __forceinline__ void find(ScoreShared<kLanes> &S, uint32_t groups, float bound) {
+    const uint32_t t = row_thread<kLanes>();
+    for (uint32_t g = 0; g < groups; g++) {
+        const float m = noted(S.most[g][t], T());
         if (m >= bound && m > Usual<T>::kLow) {
             const uint32_t at = atomicAdd(&S.found_n, 1);
-            if (at < S.kFound) S.found[at] = Tile<T, kSize, kLanes>::place(i0, u);
+            if (at < S.kFound) S.found[at] = g << 16 | t;
         }
     }
 }
 
-// Their logits at or above the bound, which has risen since, to the list.  (Read once more: 32 bytes for each of them.)
+// Their logits that reach it, to the list: a thread takes a vector.
 template <typename T, int kLanes>
-__device__ __forceinline__ void list_found(ScoreShared<kLanes> &S, u64 *list, const RowView<T> &row, float bound) {
+__device__ __forceinline__ void list_found(ScoreShared<kLanes> &S, u64 *list, const RowView<T> &row, uint32_t lo, uint32_t hi, uint32_t tiles,
+                                           float bound) {
     constexpr int kVec = RowView<T>::kVec;
-    for (uint32_t i = row_thread<kLanes>(); i < min(S.found_n, (uint32_t)S.kFound); i += kLanes) {
-        const uint32_t place = S.found[i];
+    const uint32_t each = tiles * kSize, n = min(S.found_n, (uint32_t)S.kFound) * each;   // vectors of a group, of all
+    for (uint32_t i = row_thread<kLanes>(); i < n; i += kLanes) {
+        const uint32_t f = S.found[i / each], v0 = (f >> 16) * each + i % each;
+        const uint32_t place = lo + v0 * kLanes + (f & 0xFFFFu);
+        if (place >= hi) continue;
         float v[kVec];
         unpack(row.load(place), v, T());
         uint32_t some = 0;
 #pragma unroll
         for (int e = 0; e < kVec; e++) some |= v[e] >= bound && v[e] > Usual<T>::kLow ? 1u << e : 0u;
+        if (!some) continue;
         uint32_t at = atomicAdd(&S.list_n, __popc(some));
 #pragma unroll
         for (int e = 0; e < kVec; e++)
@@ -247,25 +264,26 @@ __global__ void __launch_bounds__(kLanes == 32 ? kWarpRows * 32 : kLanes, kLanes
     u64 *const list = (u64 *)tiles;        // once the tiles are through
     if (kTops) {
         if (team.thread == 0) S.list_n = S.found_n = 0;
-        bool stale = true;
-        float bound = Usual<T>::kLow;
-        for (uint32_t n = 0, i0 = lo; i0 < hi || n == 0; i0 += Tiles::kVecs, n++) {
+        const uint32_t steps = feed.steps(), per = (steps + S.kGroups - 1) / S.kGroups;   // tiles of a group
+        uint32_t group = 0, left = per;
+        float most = Usual<T>::kLow;
+        for (uint32_t n = 0; n < steps; n++) {
             Tiles t;
-            typename Words<T>::W each[kSize];
             feed.next(t, n);
-            const float m = t.raise_all(each);
+            const float m = t.raise_all();
             sums.add(t, m, c2);
-            stale = (n & (n + 1)) != 0;    // after 1, 2, 4... tiles
-            if (!stale) {
-                tops.write(S, sums.most, team.lane, team.warp);
-                if (kLanes == 32 || n == 0) team.sync_cta();
-                bound = tops.least(S, Usual<T>::kLow);
+            most = fmaxf(most, m);
+            if (--left == 0 || n + 1 == steps) {
+                S.most[group++][team.thread] = note(most, T());
+                left = per, most = Usual<T>::kLow;
             }
-            if (m >= bound && m > Usual<T>::kLow) find<T, kLanes>(S, each, i0, bound);
         }
-        if (stale) tops.write(S, sums.most, team.lane, team.warp);
+        tops.write(S, sums.most, team.lane, team.warp);
         team.sync_cta();
-        list_found<T, kLanes>(S, list, row, tops.least(S, Usual<T>::kLow));
+        const float bound = tops.least(S, Usual<T>::kLow);
+        find<T, kLanes>(S, group, bound);
+        team.sync_cta();
+        list_found<T, kLanes>(S, list, row, lo, hi, per, bound);
         team.sync_cta();
         const bool over = S.found_n > S.kFound || S.list_n > S.kList;
         count = over ? -0x1p24f : fminf((float)S.list_n, (float)k);
@@ -407,10 +425,15 @@ int launch_team(bpe_ctx *ctx, const ScoreParams &P, uint32_t n_rows, uint32_t te
     BPE_CUDA(ctx, allow_shared(k, ctx->device, kShared, devices), "head_logprobs");
     return launch_rows(ctx, "head_logprobs launch", k, P, (n_rows + kRows - 1) / kRows, team, kLanes * kRows, kTeam, kShared, n_rows);
 }
+// Whether a row has a CTA of 512 threads: where no SM has more than two rows, and they are long.
+static bool row_wide(uint32_t n_rows, uint32_t bytes, uint32_t sms) { return n_rows <= sms && n_rows > sms / 2 && bytes >= 65536; }
+
 template <typename T> int launch_logprobs(bpe_ctx *ctx, const ScoreParams &P, uint32_t n_rows) {
     const uint32_t bytes = P.row.n_tok * (uint32_t)sizeof(T), sms = (uint32_t)ctx->sm_count, team = row_team(n_rows, bytes, sms, 2);
+    const bool wide = row_wide(n_rows, bytes, sms);
     if (!P.n_top || !(P.top_ids || P.top_logprob)) {
         if (row_lanes(n_rows, bytes, sms, 32, 40) == 32) return launch_team<T, 32, false, false>(ctx, P, n_rows, 1);
+        if (wide) return launch_team<T, 512, false, false>(ctx, P, n_rows, 1);
         return team > 1 ? launch_team<T, kMost, true, false>(ctx, P, n_rows, team) : launch_team<T, kMost, false, false>(ctx, P, n_rows, 1);
     }
     // The threads are the groups of Bound: with fewer than 1.5 for each alternative the bound leaves more than the list holds.
@@ -420,7 +443,9 @@ template <typename T> int launch_logprobs(bpe_ctx *ctx, const ScoreParams &P, ui
     case 32: return launch_team<T, 32, false, true>(ctx, P, n_rows, 1);
     case 64: return launch_team<T, 64, false, true>(ctx, P, n_rows, 1);
     case 128: return launch_team<T, 128, false, true>(ctx, P, n_rows, 1);
-    default: return team > 1 ? launch_team<T, kMost, true, true>(ctx, P, n_rows, team) : launch_team<T, kMost, false, true>(ctx, P, n_rows, 1);
+    default:
+        if (wide) return launch_team<T, 512, false, true>(ctx, P, n_rows, 1);
+        return team > 1 ? launch_team<T, kMost, true, true>(ctx, P, n_rows, team) : launch_team<T, kMost, false, true>(ctx, P, n_rows, 1);
     }
 }
 
