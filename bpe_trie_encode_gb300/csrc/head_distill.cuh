@@ -42,7 +42,7 @@ struct DistillShared {
     uint32_t id[kEntries];            // ~0: none, or the same as one before
     float q[kEntries], v[kEntries];   // the token's q, of all its entries; its logit
     uint32_t hash[kHash];
-    float q_sum, q_log_q, m, s;   // of the entries: the sums of q and of q log q; the listed tokens' softmax
+    float q_sum, m, s;         // the sum of the entries' q; the listed tokens' softmax
     uint32_t bits[1];          // a bit for each place of the CTA's vectors: listed
 };
 
@@ -92,7 +92,7 @@ struct Entries {
             }
             log_s = logf(warp_sum(sum));
         }
-        float q_sum = 0, q_log_q = 0;
+        float q_sum = 0;
         bool twice = false;
 #pragma unroll
         for (int j = 0; j < kHash / 32; j++) S.hash[j * 32 + lane] = ~0u;
@@ -103,7 +103,6 @@ struct Entries {
             if (t[j] > -INFINITY) t[j] -= log_s;
             const float q = expf(t[j]);
             q_sum += q;
-            q_log_q += q > 0.0f ? q * t[j] : 0.0f;
             S.id[i] = id[j], S.q[i] = q, S.v[i] = v[j];
             if (id[j] == ~0u) continue;
             for (uint32_t h = id[j] * 2654435769u >> 24;; h = (h + 1) % kHash) {   // at most 128 of 256 places are taken
@@ -135,7 +134,7 @@ struct Entries {
             }
             __syncwarp();
         }
-        q_sum = warp_sum(q_sum), q_log_q = warp_sum(q_log_q);
+        q_sum = warp_sum(q_sum);
         float top = -INFINITY, s = 0;
         if (P.rest) {          // the listed tokens' softmax, each once
 #pragma unroll
@@ -146,15 +145,15 @@ struct Entries {
                 if (top > -INFINITY && S.id[j * 32 + lane] != ~0u) s += expf(z_any(v[j], top, c));
             s = warp_sum(s);
         }
-        if (lane == 0) S.q_sum = q_sum, S.q_log_q = q_log_q, S.m = top, S.s = s;
+        if (lane == 0) S.q_sum = q_sum, S.m = top, S.s = s;
     }
-    // The sum of q log p, in the entries' own terms.
-    __device__ __forceinline__ float cross(float m, float c, float log_s) const {
+    // The sum of q (log q - log p).
+    __device__ __forceinline__ float loss(float m, float c, float log_s) const {
         float sum = 0;
 #pragma unroll
         for (int j = 0; j < kEach; j++) {
             const float q = expf(t[j]);
-            if (q > 0.0f) sum += q * (z_any(v[j], m, c) - log_s);
+            if (q > 0.0f) sum += q * (t[j] - (z_any(v[j], m, c) - log_s));
         }
         return warp_sum(sum);
     }
@@ -241,7 +240,9 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kCtas<kLanes>) k_distill(Dis
                 for (int u = 0; u < kSize; u++) t.q[u] = without<T>(t.q[u], some[u]);
             }
         }
-        sums.add(t, t.raise_all(), c2);
+        const float m = t.raise_all();
+        if (n == 0) sums.begin(m, c2);
+        sums.add(t, m, c2);
     }
     // A row that was not kept is read again, from L2 as a rule; its first tiles come while the sums are joined.
     if (kGrad && !kept && reads) feed.start();
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kCtas<kLanes>) k_distill(Dis
     const float log_s = logf(s);
     const float q_rest = kRest && free.m > -INFINITY ? fmaxf(0.0f, 1.0f - S.q_sum) : 0.0f, q_total = S.q_sum + q_rest;
     if (lists && team.rank == 0) {
-        float loss = S.q_log_q - list.cross(m, c, log_s);
+        float loss = list.loss(m, c, log_s);
         if (q_rest > 0.0f) loss += q_rest * (logf(q_rest) - (z_any(free.m, m, c) + logf(free.s) - log_s));
         if (team.lane == 0) P.loss[r] = none ? (q_total > 0.0f ? INFINITY : 0.0f) : loss;
     }

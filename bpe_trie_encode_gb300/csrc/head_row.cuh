@@ -313,10 +313,11 @@ template <typename T, int kSize, int kLanes> struct Feed {
     }
 };
 
-// A thread's sums, relative to 2^r.  r follows the largest logit only where that is 2^kSlack above it: larger numbers lose
-// nothing, and a row's first tile is hardly ever so far below its others.
+// A thread's sums, relative to 2^r: the largest logit of the warp's first tile, and a larger one only where that is 2^kSlack
+// above it, which is rare.  Larger numbers lose nothing; but z counts from r too, and a sum of z that has a far larger one
+// taken off its terms at the end would lose as much, so that entropies allow little.
 template <typename T, bool kEntropy> struct Running {
-    static constexpr float kSlack = 64.0f;
+    static constexpr float kSlack = kEntropy ? 4.0f : 64.0f;
     float most, r;      // the largest logit; what the sums are relative to
     Pair s, sz;
 
@@ -326,6 +327,10 @@ template <typename T, bool kEntropy> struct Running {
         if (kEntropy) sz = mul2(fma2(s, Pair(d, d), sz), Pair(f, f));
         s = mul2(s, Pair(f, f));
         r = to;
+    }
+    // Before the first tile, whose largest logit is m.
+    __device__ __forceinline__ void begin(float m, float c2) {
+        r = __fmul_rn(key_value(__reduce_max_sync(kFull, key_of(m))), c2);
     }
     // Adds a raised tile whose largest logit is m.
     template <int kSize, int kLanes> __device__ __forceinline__ void add(const Tile<T, kSize, kLanes> &t, float m, float c2) {

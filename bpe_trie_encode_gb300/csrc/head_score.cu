@@ -271,6 +271,7 @@ __global__ void __launch_bounds__(kLanes == 32 ? kWarpRows * 32 : kLanes, kLanes
             Tiles t;
             feed.next(t, n);
             const float m = t.raise_all();
+            if (n == 0) sums.begin(m, c2);
             sums.add(t, m, c2);
             most = fmaxf(most, m);
             if (--left == 0 || n + 1 == steps) {
@@ -291,7 +292,9 @@ __global__ void __launch_bounds__(kLanes == 32 ? kWarpRows * 32 : kLanes, kLanes
         for (uint32_t n = 0, i0 = lo; i0 < hi; i0 += Tiles::kVecs, n++) {
             Tiles t;
             feed.next(t, n);
-            sums.add(t, t.raise_all(), c2);
+            const float m = t.raise_all();
+            if (n == 0) sums.begin(m, c2);
+            sums.add(t, m, c2);
         }
     }
     Softmax all = softmax_join(team, sums, c2, count);
