@@ -577,6 +577,86 @@ def test_the_largest_vocabularies(ctx, n):
         check_distill(ctx, logits, tids, values, rest=rest)
 
 
+# ------------------------------------------------------- every kind of launch ---
+# A row has a warp, 64 to 512 threads or a cluster, and a gradient's row stays in shared memory or is read again, by numbers
+# of rows and sizes: a few rows of each are checked, and all of them by a second call on the rows in another order, which no
+# row's result may depend on (where rows start anywhere, in the same order: a row's sums go by its first byte's place).
+
+LAUNCHES = [(1300, 7), (1300, 264), (1300, 1001), (1301, 4352), (800, 9000), (2500, 9001), (400, 17000), (1100, 33000), (100, 70001),
+            (310, 66000), (160, 131080), (20, 250000)]
+
+
+def another_order(rows, n):
+    return (torch.randperm(rows, generator=torch.Generator().manual_seed(0)) if n % 8 == 0 else torch.arange(rows)).cuda()
+
+
+def launch_logits(rows, n, dtype):
+    g = torch.Generator(device="cuda").manual_seed(rows + n)
+    x = 2 * torch.randn(rows, n, generator=g, device="cuda")
+    at = torch.randint(0, n, (rows, 25), generator=g, device="cuda")
+    x.scatter_(1, at, 8 + 3 * torch.randn(rows, 25, generator=g, device="cuda"))
+    x[3] = -INF                       # rows for the general forms among the others
+    x[5, : n // 2] = torch.finfo(dtype).min
+    x[6] = 0.5
+    x[7, 0] = INF
+    x[8, 1:] = NAN
+    return x.to(dtype), torch.tensor(sorted({0, 1, 3, 5, 6, 7, 8, rows // 2, rows - 2, rows - 1}))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("rows,n", LAUNCHES)
+def test_logprobs_of_every_launch(ctx, dtype, rows, n):
+    x, some = launch_logits(rows, n, dtype)
+    ids = some_ids(rows, n)
+    a, order = randn(rows, seed=1).float().cuda(), another_order(rows, n)
+    for top in (0, 5, 21, 40, 64, 128):
+        out = ctx.head_logprobs(x, ids, temperature=0.8, top=top)
+
+        class Some:   # the rows to be checked, as check_logprobs asks for them
+            @staticmethod
+            def head_logprobs(*_, **__):
+                return tuple(o if o is None else o[some.cuda()] for o in out)
+
+        check_logprobs(Some, x[some.cuda()], ids[some.cuda()], t=0.8, top=top)
+        again = ctx.head_logprobs(x[order], ids[order], temperature=0.8, top=top)
+        for one, two in zip(out, again):
+            assert (one is None and two is None) or torch.equal(one[order], two)
+    _, h, _, _, norm = out
+    for b in (None, a):
+        d = ctx.head_logprobs_backward(x, ids, norm, a, h if b is not None else None, b, temperature=0.8)
+        at = some.cuda()
+        want, off = grad64(x[at], ids[at], a[at], a[at] if b is not None else None, 0.8)
+        rounded(d[at], want, off, dtype)
+        args = (norm[order], a[order], h[order] if b is not None else None, b[order] if b is not None else None)
+        assert torch.equal(d[order], ctx.head_logprobs_backward(x[order], ids[order], *args, temperature=0.8))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("rows,n", LAUNCHES)
+@pytest.mark.parametrize("rest", [False, True])
+def test_distill_of_every_launch(ctx, dtype, rows, n, rest):
+    x, some = launch_logits(rows, n, dtype)
+    k = min(n, 50)
+    t = x.float().nan_to_num(-1e4, 1e4, -1e4) + torch.randn(rows, n, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda")
+    top = torch.log_softmax(t.clamp_min(-1e4), 1).topk(k, dim=1)
+    ids, values = top.indices.to(torch.int32), top.values
+    ids[0, : k // 2] = -1
+    if k > 2:
+        ids[rows - 1, 2] = ids[rows - 1, 0]
+    g, order = (0.5 + torch.rand(rows, generator=torch.Generator().manual_seed(3))).cuda(), another_order(rows, n)
+    at = some.cuda()
+    loss, _ = ctx.head_distill(x, ids, values, temperature=0.8, rest=rest)
+    loss2, d = ctx.head_distill(x, ids, values, temperature=0.8, rest=rest, grad=g)
+    want, off, dwant, doff = distill64(x[at], ids[at], values[at], 0.8, rest, g[at])
+    near(loss[at], want, off)
+    near(loss2[at], want, off)
+    rounded(d[at], dwant, doff, dtype)
+    again, e = ctx.head_distill(x[order], ids[order], values[order], temperature=0.8, rest=rest, grad=g[order])
+    assert torch.equal(loss2[order], again) and torch.equal(d[order], e)
+    assert torch.equal(loss[order], ctx.head_distill(x[order], ids[order], values[order], temperature=0.8, rest=rest)[0])
+    assert torch.equal(ctx.head_distill(x, ids, values, temperature=0.8, rest=rest, grad=g, out=x)[1], d) and torch.equal(x, d)
+
+
 # ------------------------------------------------------- streams and graphs ---
 
 def test_other_streams_and_captured_graphs(ctx):
