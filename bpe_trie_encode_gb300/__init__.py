@@ -21,6 +21,13 @@ The output head of a model over the same vocabulary (``examples/generate.py``):
     logits = ctx.head_logits(x8, xs, w8, ws)
     ids, logprob = ctx.head_sample(logits, u, temperature=0.8, top_p=0.95)
     text = ctx.decode(merges, ids)
+
+Scoring given ids, and learning from a teacher, with logits [rows, n_tok]:
+
+    logprob, entropy, top_ids, top_logprob, norm = ctx.head_logprobs(logits, ids, top=64)
+    grad = ctx.head_logprobs_backward(logits, ids, norm, grad_logprob)
+    loss, grad = ctx.head_distill(student, top_ids, top_logprob, rest=True, grad=1 / rows)
+    student.backward(grad)
 """
 from __future__ import annotations
 

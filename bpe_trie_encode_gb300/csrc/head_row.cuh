@@ -1,6 +1,14 @@
 // head_row.cuh -- a row of logits as the scoring and training kernels of the
-// output head see it (head_score.cu, head_distill.cu): its vectors of 16 bytes,
+// output head see it (head_score.cu, head_distill.cuh): its vectors of 16 bytes,
 // its softmax, and the sums over its threads and CTAs.
+//
+// A row of V logits is read once, by a warp, a CTA or a cluster.  Its bytes, V x 2
+// or 4, are the floor; what competes with them is issue slots.  A logit of 16 bits
+// takes about six instructions (a share of two copies, raise, largest, unpack, half
+// a fused step, an exponential, one or two half additions), and 130 to 190 a thread
+// for each row come on top, so that many rows have few threads each.  With the
+// loads two tiles ahead, 8,192 x 32,256 bf16 are summed in 83 us (6.4 TB/s, 94% of
+// the copy rate), 8,192 x 1,000 in 7 (2.3 TB/s).
 #pragma once
 
 #include "device.cuh"

@@ -1,5 +1,17 @@
 // head_score.cu -- log-probabilities of given ids, with the entropy and the top
 // alternatives of each row of logits, and the gradient of both.
+//
+// With z = (v - m) c: log s - sum(exp(z) z) / s is the entropy, so that one pass
+// with two sums gives all but the alternatives; those come from the largest logit
+// of each thread's tiles, noted on the way, and a second look at the few tiles that
+// reach a bound.  Bound by HBM where there are many rows (8,192 x 32,256 bf16: 83 us,
+// 94% of the copy rate; with 20 alternatives 107), by the latency of the steps after
+// a row's last logit where there are few (256 x 65,536 bf16: 6.8 us without
+// alternatives, 12.8 with 20; 1 x 32,256 f32: 3.7 and 6).
+//
+// The gradient needs no sums: with the norm of the forward pass every logit's is an
+// exponential and a product (with the entropy's, a fused step more).  8,192 x 32,156
+// bf16: 157 us, 6.7 TB/s of reading and writing, 99% of the copy rate.
 #include "head_row.cuh"
 
 namespace bpe {
@@ -428,7 +440,8 @@ int launch_team(bpe_ctx *ctx, const ScoreParams &P, uint32_t n_rows, uint32_t te
     BPE_CUDA(ctx, allow_shared(k, ctx->device, kShared, devices), "head_logprobs");
     return launch_rows(ctx, "head_logprobs launch", k, P, (n_rows + kRows - 1) / kRows, team, kLanes * kRows, kTeam, kShared, n_rows);
 }
-// Whether a row has a CTA of 512 threads: where no SM has more than two rows, and they are long.
+// Whether a row has a CTA of 512 threads: where no SM has more than one row, and they are long.  In us, 512 threads / clusters
+// of two CTAs of 256, 20 alternatives: 120 x 65,536 bf16 9.4 / 11.0, 152 x 250,000 bf16 17.8 / 19.7; 120 x 32,256 8.4 / 7.5.
 static bool row_wide(uint32_t n_rows, uint32_t bytes, uint32_t sms) { return n_rows <= sms && n_rows > sms / 2 && bytes >= 65536; }
 
 template <typename T> int launch_logprobs(bpe_ctx *ctx, const ScoreParams &P, uint32_t n_rows) {
