@@ -139,10 +139,56 @@ __device__ __noinline__ int list_any(ScoreShared<kLanes> &S, u64 *list, Team<kLa
     return team.turn;
 }
 
-// The list's k largest in order, in S.best: each entry's place is the number of larger ones, counted by four threads.
-template <int kLanes, bool kTeam>
-__device__ __forceinline__ uint32_t rank_list(ScoreShared<kLanes> &S, const Team<kLanes, kTeam> &team, const u64 *list, uint32_t k) {
-    const uint32_t n = S.list_n, part = team.thread & 3;
+// Rows are many where they have few threads each (row_lanes): instructions count, not a row's latency.
+template <int kLanes> constexpr bool kManyRows = kLanes < 256;
+
+// 32 kEach entries in order, largest first, by a bitonic network: entry e of a lane is number 32 e + lane.
+template <int kEach> __device__ __forceinline__ void sort_warp(u64 (&v)[kEach], int lane) {
+#pragma unroll
+    for (int size = 2; size <= 32 * kEach; size <<= 1)
+#pragma unroll
+        for (int d = size >> 1; d > 0; d >>= 1)
+#pragma unroll
+            for (int e = 0; e < kEach; e++) {
+                if (d >= 32) {
+                    const int o = e ^ d / 32;
+                    if (o < e) continue;
+                    const bool down = (32 * e & size) == 0;
+                    const u64 a = v[e], b = v[o];
+                    const bool swap = (a < b) == down;
+                    v[e] = swap ? b : a, v[o] = swap ? a : b;
+                } else {
+                    const u64 o = __shfl_xor_sync(kFull, v[e], d);
+                    const bool first = (lane & d) == 0, down = ((32 * e + lane) & size) == 0;
+                    v[e] = (first == down) == (v[e] < o) ? o : v[e];
+                }
+            }
+}
+// f(place, entry) for the list's k largest, by one warp.
+template <int kEach, typename F> __device__ __forceinline__ void sort_list(const u64 *list, uint32_t n, uint32_t k, int lane, F f) {
+    u64 v[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; e++) v[e] = 32 * e + lane < n ? list[32 * e + lane] : 0;
+    sort_warp(v, lane);
+#pragma unroll
+    for (int e = 0; e < kEach; e++)
+        if (32 * e + lane < min(n, k)) f(32 * e + lane, v[e]);
+}
+// The same for any list, by all of a row's threads: a place is the number of larger entries, counted by four threads for each.
+// Where rows are many, up to 128 entries are sorted by one warp: fewer instructions, but one after the other (64 alternatives,
+// sorted / ranked: 8,192 x 32,256 bf16 by 128 threads 123 / 137 us; 256 x 65,536 by 256 14.7 / 13.4).
+template <int kLanes, bool kTeam, typename F>
+__device__ __forceinline__ uint32_t rank_list(const ScoreShared<kLanes> &S, const Team<kLanes, kTeam> &team, const u64 *list, uint32_t k, F f) {
+    const uint32_t n = S.list_n;
+    if (kManyRows<kLanes> && n <= 128) {
+        if (team.warp == 0) {
+            if (n <= 32) sort_list<1>(list, n, k, team.lane, f);
+            else if (n <= 64) sort_list<2>(list, n, k, team.lane, f);
+            else sort_list<4>(list, n, k, team.lane, f);
+        }
+        return min(n, k);
+    }
+    const uint32_t part = team.thread & 3;
     for (uint32_t i0 = 0; i0 + (team.thread & ~31u) / 4 < n; i0 += kLanes / 4) {
         const uint32_t i = i0 + team.thread / 4;
         const u64 one = list[min(i, n - 1)];
@@ -150,9 +196,8 @@ __device__ __forceinline__ uint32_t rank_list(ScoreShared<kLanes> &S, const Team
         for (uint32_t j = part; j < n; j += 4) place += list[j] > one;
         place += __shfl_xor_sync(kFull, place, 1);
         place += __shfl_xor_sync(kFull, place, 2);
-        if (i < n && part == 0 && place < k) S.best[place] = one;
+        if (i < n && part == 0 && place < k) f(place, one);
     }
-    team.sync_cta();
     return min(n, k);
 }
 
@@ -220,29 +265,60 @@ __device__ __forceinline__ void find(ScoreShared<kLanes> &S, uint32_t groups, fl
     }
 }
 
-// Their logits that reach it, to the list: a thread takes a vector.
+// The logits of a vector that reach it, to the list.
+template <typename T, int kLanes>
+__device__ __forceinline__ void list_vector(ScoreShared<kLanes> &S, u64 *list, const RowView<T> &row, uint4 q, uint32_t place, float bound) {
+    constexpr int kVec = RowView<T>::kVec;
+    float v[kVec];
+    unpack(q, v, T());
+    uint32_t some = 0;
+#pragma unroll
+    for (int e = 0; e < kVec; e++) some |= v[e] >= bound && v[e] > Usual<T>::kLow ? 1u << e : 0u;
+    if (!some) return;
+    uint32_t at = atomicAdd(&S.list_n, __popc(some));
+#pragma unroll
+    for (int e = 0; e < kVec; e++)
+        if (some >> e & 1) {
+            if (at < S.kList) list[at] = entry_of(key_of(v[e]), place * kVec - row.shift + e);
+            at++;
+        }
+}
+// Those of the groups that were found.  A thread takes a vector, or where rows are many a group, tile by tile, of which it looks
+// closer at the vectors that have any (one, as a rule).
 template <typename T, int kLanes>
 __device__ __forceinline__ void list_found(ScoreShared<kLanes> &S, u64 *list, const RowView<T> &row, uint32_t lo, uint32_t hi, uint32_t tiles,
                                            float bound) {
-    constexpr int kVec = RowView<T>::kVec;
-    const uint32_t each = tiles * kSize, n = min(S.found_n, (uint32_t)S.kFound) * each;   // vectors of a group, of all
+    const uint32_t n = min(S.found_n, (uint32_t)S.kFound), each = tiles * kSize;
+    if (!kManyRows<kLanes>) {
+        for (uint32_t i = row_thread<kLanes>(); i < n * each; i += kLanes) {
+            const uint32_t f = S.found[i / each], place = lo + ((f >> 16) * each + i % each) * kLanes + (f & 0xFFFFu);
+            if (place < hi) list_vector<T, kLanes>(S, list, row, row.load(place), place, bound);
+        }
+        return;
+    }
     for (uint32_t i = row_thread<kLanes>(); i < n; i += kLanes) {
-        const uint32_t f = S.found[i / each], v0 = (f >> 16) * each + i % each;
-        const uint32_t place = lo + v0 * kLanes + (f & 0xFFFFu);
-        if (place >= hi) continue;
-        float v[kVec];
-        unpack(row.load(place), v, T());
-        uint32_t some = 0;
+        const uint32_t f = S.found[i];
+        for (uint32_t t = 0; t < tiles; t++) {
+            const uint32_t first = lo + ((f >> 16) * each + t * kSize) * kLanes + (f & 0xFFFFu);
+            uint4 q[kSize];
 #pragma unroll
-        for (int e = 0; e < kVec; e++) some |= v[e] >= bound && v[e] > Usual<T>::kLow ? 1u << e : 0u;
-        if (!some) continue;
-        uint32_t at = atomicAdd(&S.list_n, __popc(some));
+            for (int u = 0; u < kSize; u++) q[u] = first + u * kLanes < hi ? row.load(first + u * kLanes) : Tile<T, kSize, kLanes>::fill();
+            uint32_t some = 0;
 #pragma unroll
-        for (int e = 0; e < kVec; e++)
-            if (some >> e & 1) {
-                if (at < S.kList) list[at] = entry_of(key_of(v[e]), place * kVec - row.shift + e);
-                at++;
+            for (int u = 0; u < kSize; u++) {
+                const float m = Words<T>::largest(raise<T>(q[u]));
+                some |= m >= bound && m > Usual<T>::kLow ? 1u << u : 0u;
             }
+            while (some) {
+                const int u = __ffs(some) - 1;
+                some &= some - 1;
+                uint4 one = q[0];
+#pragma unroll
+                for (int o = 1; o < kSize; o++)
+                    if (u == o) one = q[o];
+                list_vector<T, kLanes>(S, list, row, one, first + u * kLanes, bound);
+            }
+        }
     }
 }
 
@@ -323,10 +399,18 @@ __global__ void __launch_bounds__(kLanes == 32 ? kWarpRows * 32 : kLanes, kLanes
         if (P.logprob) P.logprob[r] = id < 0 || (uint32_t)id >= P.row.n_tok ? 0.0f : none ? -INFINITY : z_any(given, all.m, c) - log_s;
     }
     if (!kTops) return;
-    uint32_t n = rank_list(S, team, list, k), total = n;
-    const u64 one = S.best[min(team.thread, k - 1)];   // this thread's, of the n
-    uint32_t place = team.thread;
-    if (kTeam) {
+    auto put = [=](uint32_t place, u64 one) {
+        const uint64_t at = (uint64_t)r * k + place;
+        if (P.top_ids) P.top_ids[at] = (int32_t)~(uint32_t)one;
+        if (P.top_logprob) P.top_logprob[at] = z_any(key_value((uint32_t)(one >> 32)), all.m, c) - log_s;
+    };
+    uint32_t total;
+    if (!kTeam) {
+        total = rank_list(S, team, list, k, put);
+    } else {
+        const uint32_t n = rank_list(S, team, list, k, [&](uint32_t place, u64 one) { S.best[place] = one; });
+        __syncthreads();
+        const u64 one = S.best[min(team.thread, k - 1)];   // this thread's, of the n
         team.exchange(make_float4((float)n, 0, 0, 0));
         total = 0;
         for (uint32_t o = 0; o < team.size; o++) total += (uint32_t)team.S.slot[team.turn][o].x;
@@ -334,6 +418,7 @@ __global__ void __launch_bounds__(kLanes == 32 ? kWarpRows * 32 : kLanes, kLanes
         for (uint32_t o = 0; o < team.size; o++)
             if (o != team.rank && team.thread < (uint32_t)team.S.slot[team.turn][o].x) list[o * k + team.thread] = far_load(&S.best[team.thread], o);
         __syncthreads();
+        uint32_t place = team.thread;
         if (team.thread < n)
             for (uint32_t o = 0; o < team.size; o++) {
                 if (o == team.rank) continue;
@@ -345,11 +430,7 @@ __global__ void __launch_bounds__(kLanes == 32 ? kWarpRows * 32 : kLanes, kLanes
                 }
                 place += x;
             }
-    }
-    if (team.thread < n && place < k) {
-        const uint64_t at = (uint64_t)r * k + place;
-        if (P.top_ids) P.top_ids[at] = (int32_t)~(uint32_t)one;
-        if (P.top_logprob) P.top_logprob[at] = z_any(key_value((uint32_t)(one >> 32)), all.m, c) - log_s;
+        if (team.thread < n && place < k) put(place, one);
     }
     if (team.rank == 0 && team.thread >= total && team.thread < k) {
         const uint64_t at = (uint64_t)r * k + team.thread;
