@@ -117,19 +117,27 @@ def _head_vector(t: torch.Tensor, name: str, device: torch.device, dtype: torch.
         _head_place(t, name, device, (dtype,))
     if t.shape != (rows,):
         raise ValueError(f"{name} must be ({rows},), got {tuple(t.shape)}")
-    if rows > 1 and t.stride(0) != 1:
+    if not t.is_contiguous():
         if out:
             raise ValueError(f"{name}: an output must be contiguous")
         t = t.contiguous()
     return t
 
 
+def _head_rows(t, name: str, device: torch.device):
+    """(matrix, distance of its rows, rows, columns, type) of logits, as _head_matrix takes them."""
+    t, stride = _head_matrix(t, name, device, _HEAD_TYPES)
+    rows, columns = t.shape
+    return t, stride, rows, columns, t.dtype
+
+
 def _head_table(t, name: str, device: torch.device, dtypes, rows: int, columns=None, out: bool = False) -> torch.Tensor:
     """A contiguous [rows, columns] tensor; an input that is none is copied."""
     if not isinstance(t, torch.Tensor) or t.device != device or t.dtype not in dtypes:
         _head_place(t, name, device, dtypes)
-    if t.dim() != 2 or t.shape[0] != rows or (columns is not None and t.shape[1] != columns):
-        raise ValueError(f"{name} must be ({rows}, {'any' if columns is None else columns}), got {tuple(t.shape)}")
+    size = t.shape
+    if len(size) != 2 or size != (rows, size[1] if columns is None else columns):
+        raise ValueError(f"{name} must be ({rows}, {'any' if columns is None else columns}), got {tuple(size)}")
     if not t.is_contiguous():
         if out:
             raise ValueError(f"{name}: an output must be contiguous")
@@ -187,14 +195,18 @@ class Context:
         self.device = torch.device("cuda", torch.cuda.current_device() if device is None
                                    else torch.device(device).index or 0)
         h = ctypes.c_void_p()
-        rc = self.lib.bpe_ctx_create(ctypes.byref(h), self.device.index, ctypes.c_void_p(_stream_ptr(self.device)))
+        self._stream = _stream_ptr(self.device)
+        rc = self.lib.bpe_ctx_create(ctypes.byref(h), self.device.index, ctypes.c_void_p(self._stream))
         if rc != 0:
             raise BpeError(rc, "bpe_ctx_create failed")
         self._h = h
 
     # -- plumbing -----------------------------------------------------------
     def _sync_stream(self):
-        self.lib.bpe_ctx_set_stream(self._h, ctypes.c_void_p(_stream_ptr(self.device)))
+        stream = _stream_ptr(self.device)
+        if stream != self._stream:
+            self.lib.bpe_ctx_set_stream(self._h, ctypes.c_void_p(stream))
+            self._stream = stream
 
     def close(self):
         if getattr(self, "_h", None):
@@ -503,8 +515,7 @@ class Context:
         on the current stream.  What it returns has no gradient of its own:
         ``logits.backward(ctx.head_logprobs_backward(...))`` gives one."""
         dev = self.device
-        logits, stride = _head_matrix(logits, "logits", dev, _HEAD_TYPES)
-        rows, n_tok = logits.shape
+        logits, stride, rows, n_tok, dtype = _head_rows(logits, "logits", dev)
         if not 0 <= top <= _capi.BPE_HEAD_MAX_TOP:
             raise ValueError(f"top must be 0 to {_capi.BPE_HEAD_MAX_TOP}, got {top}")
         if ids is not None:
@@ -526,7 +537,7 @@ class Context:
             _head_table(norm, "norm", dev, (torch.float32,), rows, 2, out=True)
         t, d_t, t_ptr = _head_number(temperature, "temperature", dev, rows)
         self._sync_stream()
-        rc = self.lib.head_logprobs(self._h, logits.data_ptr(), stride, _HEAD_TYPES[logits.dtype], rows, n_tok,
+        rc = self.lib.head_logprobs(self._h, logits.data_ptr(), stride, _HEAD_TYPES[dtype], rows, n_tok,
                                     ids.data_ptr() if ids is not None else None, t, t_ptr, top,
                                     logprob.data_ptr() if ids is not None else None, entropy.data_ptr(),
                                     top_ids.data_ptr() if top else None, top_logprob.data_ptr() if top else None,
@@ -547,9 +558,7 @@ class Context:
         ``out`` may be the logits themselves.  Asynchronous on the current
         stream."""
         dev = self.device
-        logits, stride = _head_matrix(logits, "logits", dev, _HEAD_TYPES)
-        size, dtype = logits.shape, logits.dtype
-        rows, n_tok = size
+        logits, stride, rows, n_tok, dtype = _head_rows(logits, "logits", dev)
         norm = _head_table(norm, "norm", dev, (torch.float32,), rows, 2)
         i_ptr = a_ptr = h_ptr = b_ptr = None
         if grad_logprob is not None:
@@ -566,7 +575,7 @@ class Context:
             h_ptr, b_ptr = entropy.data_ptr(), grad_entropy.data_ptr()
         if out is None:
             out = torch.empty(rows, n_tok, dtype=dtype, device=dev)
-        out, out_stride = _head_matrix(out, "out", dev, (dtype,), size, out=True)
+        out, out_stride = _head_matrix(out, "out", dev, (dtype,), (rows, n_tok), out=True)
         t, d_t, t_ptr = _head_number(temperature, "temperature", dev, rows)
         self._sync_stream()
         rc = self.lib.head_logprobs_backward(self._h, logits.data_ptr(), stride, _HEAD_TYPES[dtype], rows, n_tok, i_ptr,
@@ -591,9 +600,7 @@ class Context:
         ``out`` may be the logits themselves.  One entry a row is cross
         entropy.  Asynchronous on the current stream."""
         dev = self.device
-        logits, stride = _head_matrix(logits, "logits", dev, _HEAD_TYPES)
-        size, dtype = logits.shape, logits.dtype
-        rows, n_tok = size
+        logits, stride, rows, n_tok, dtype = _head_rows(logits, "logits", dev)
         top_ids = _head_table(top_ids, "top_ids", dev, (torch.int32,), rows)
         listed = top_ids.shape[1]
         top_logprob = _head_table(top_logprob, "top_logprob", dev, _HEAD_TYPES, rows, listed)
@@ -606,7 +613,7 @@ class Context:
             g, d_g, g_ptr = _head_number(grad, "grad", dev, rows)
             if out is None:
                 out = torch.empty(rows, n_tok, dtype=dtype, device=dev)
-            out, o_stride = _head_matrix(out, "out", dev, (dtype,), size, out=True)
+            out, o_stride = _head_matrix(out, "out", dev, (dtype,), (rows, n_tok), out=True)
             o_ptr = out.data_ptr()
         elif out is not None:
             raise ValueError("out needs grad")
