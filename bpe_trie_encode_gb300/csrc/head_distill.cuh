@@ -62,6 +62,7 @@ struct DistillShared {
     float q[kEntries], v[kEntries];   // the token's q, of all its entries; its logit
     uint32_t hash[kHash];
     float q_sum, m, s;         // the sum of the entries' q; the listed tokens' softmax
+    uint32_t twice;            // whether an id is listed twice
     uint32_t bits[1];          // a bit for each place of the CTA's vectors: listed
 };
 
@@ -70,6 +71,18 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
     return v;
+}
+
+// q (log q - log p) - q + p = q (e^d - 1 - d), d = log p - log q, which is never below 0.  Where all q and all p add up to 1 the
+// sum of these terms is the divergence, and one that is small, since teacher and student agree, is not the difference of far
+// larger ones.
+__device__ __forceinline__ float divergence(float q, float log_q, float log_p) {
+    const float d = log_p - log_q;
+    if (!(fabsf(d) < 1.0f)) return expf(log_p) - q - q * d;
+    float r = 1.0f / 39916800;             // the exponential's series: e^d - 1 - d = d^2 (1/2! + d/3! + d^2/4! ...)
+    r = fmaf(r, d, 1.0f / 3628800), r = fmaf(r, d, 1.0f / 362880), r = fmaf(r, d, 1.0f / 40320), r = fmaf(r, d, 1.0f / 5040);
+    r = fmaf(r, d, 1.0f / 720), r = fmaf(r, d, 1.0f / 120), r = fmaf(r, d, 1.0f / 24), r = fmaf(r, d, 1.0f / 6), r = fmaf(r, d, 0.5f);
+    return q * (d * d * r);
 }
 
 // The row's entries, four to a lane of the CTA's last warp, which deals with them while the others read the row.
@@ -134,7 +147,8 @@ struct Entries {
             }
         }
         __syncwarp();
-        if (__any_sync(kFull, twice)) {
+        twice = __any_sync(kFull, twice);
+        if (twice) {
             float q[kEach];
             bool later[kEach];
 #pragma unroll
@@ -164,15 +178,16 @@ struct Entries {
                 if (top > -INFINITY && S.id[j * 32 + lane] != ~0u) s += expf(z_any(v[j], top, c));
             s = warp_sum(s);
         }
-        if (lane == 0) S.q_sum = q_sum, S.m = top, S.s = s;
+        if (lane == 0) S.q_sum = q_sum, S.twice = twice, S.m = top, S.s = s;
     }
-    // The sum of q (log q - log p).
-    __device__ __forceinline__ float loss(float m, float c, float log_s) const {
+    // The sum of q (log q - log p); with `whole`, of q (log q - log p) - q + p.
+    __device__ __forceinline__ float loss(float m, float c, float log_s, bool whole) const {
         float sum = 0;
 #pragma unroll
         for (int j = 0; j < kEach; j++) {
-            const float q = expf(t[j]);
-            if (q > 0.0f) sum += q * (t[j] - (z_any(v[j], m, c) - log_s));
+            const float q = expf(t[j]), lp = z_any(v[j], m, c) - log_s;
+            if (whole) sum += id[j] == ~0u ? 0.0f : q > 0.0f ? divergence(q, t[j], lp) : expf(lp);
+            else if (q > 0.0f) sum += q * (t[j] - lp);
         }
         return warp_sum(sum);
     }
@@ -283,8 +298,12 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kCtas<kLanes>) k_distill(Dis
     const float log_s = logf(s);
     const float q_rest = kRest && free.m > -INFINITY ? fmaxf(0.0f, 1.0f - S.q_sum) : 0.0f, q_total = S.q_sum + q_rest;
     if (lists && team.rank == 0) {
-        float loss = list.loss(m, c, log_s);
-        if (q_rest > 0.0f) loss += q_rest * (logf(q_rest) - (z_any(free.m, m, c) + logf(free.s) - log_s));
+        const bool whole = q_rest > 0.0f && !S.twice;   // an id listed twice has its p in two terms
+        float loss = list.loss(m, c, log_s, whole);
+        if (q_rest > 0.0f) {
+            const float log_q = logf(q_rest), log_p = z_any(free.m, m, c) + logf(free.s) - log_s;
+            loss += whole ? divergence(q_rest, log_q, log_p) : q_rest * (log_q - log_p);
+        }
         if (team.lane == 0) P.loss[r] = none ? (q_total > 0.0f ? INFINITY : 0.0f) : loss;
     }
     if (!kGrad) return;

@@ -516,6 +516,32 @@ def test_distill_of_far_masses(ctx):
         check_distill(ctx, logits.to(dtype).cuda(), ids, values, rest=True)
 
 
+@pytest.mark.parametrize("n,k", [(300, 1), (5000, 3), (70000, 40)])
+def test_a_small_divergence_keeps_its_digits(ctx, n, k):
+    """Teacher and student that differ by a hundredth: the divergence is some 10^-5, far less than its terms."""
+    logits = some_logits(40, n, F32, seed=55)
+    t = logits.cpu().double() + 0.01 * randn(40, n, seed=56)
+    top = torch.log_softmax(t, 1).topk(k, dim=1)
+    ids, values = top.indices, top.values.float()
+    loss, _ = ctx.head_distill(logits, ids.to(torch.int32).cuda(), values.cuda(), rest=True)
+    _, z, p, log_s, _ = softmax64(logits)
+    lp, lq = (z - log_s[:, None]).gather(1, ids), values.double()
+    q, pk = lq.exp(), lp.exp()
+    q_rest, left = 1 - q.sum(1), torch.ones(40, n, dtype=torch.bool).scatter_(1, ids, False)
+    p_rest = torch.where(left, p, 0.0).sum(1)
+
+    def term(q, p):
+        return q * (q / p).log() - q + p
+
+    want = term(q, pk).sum(1) + term(q_rest, p_rest)
+    # q h(d) changes by (p - q) for a change of d, of which the roundings of log p are room's and a few of its own; q_rest is off
+    # by the roundings of the q and their sum, and h by a few of its own
+    e = U * (room(z, p, log_s) + 8 * z.gather(1, ids).abs().amax(1) + 4 * p_rest.log().abs() + 4 * lq.abs().amax(1) + n / 256 + 60)
+    off = ((pk - q).abs().sum(1) + (p_rest - q_rest).abs()) * e + U * (2 * lq.abs().amax(1) + 30) * (p_rest / q_rest - 1).abs() + 32 * U * want + e * e
+    near(loss, want, off)
+    assert ((off < 0.1 * want).float().mean() > 0.8).item(), (off / want).quantile(0.8)   # the bound says something
+
+
 @pytest.mark.parametrize("rest", [False, True])
 def test_distill_against_differences(ctx, rest):
     n, rows, k = 31, 3, 4
