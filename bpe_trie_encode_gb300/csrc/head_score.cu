@@ -5,9 +5,9 @@
 // with two sums gives all but the alternatives; those come from the largest logit
 // of each thread's tiles, noted on the way, and a second look at the few tiles that
 // reach a bound.  Bound by HBM where there are many rows (8,192 x 32,256 bf16: 83 us,
-// 94% of the copy rate; with 20 alternatives 107), by the latency of the steps after
-// a row's last logit where there are few (256 x 65,536 bf16: 6.8 us without
-// alternatives, 12.8 with 20; 1 x 32,256 f32: 3.7 and 6).
+// 94% of the copy rate; with 20 alternatives 102), by the latency of the steps after
+// a row's last logit where there are few (256 x 65,536 bf16: 6.7 us without
+// alternatives, 11.3 with 20; 1 x 32,256 bf16: 3.5 and 5.9).
 //
 // The gradient needs no sums: with the norm of the forward pass every logit's is an
 // exponential and a product (with the entropy's, a fused step more).  8,192 x 32,156
