@@ -1,5 +1,6 @@
 // head.cuh -- element types and small helpers shared by the output head's
-// kernels (head_norm.cu, head_logits.cu, head_sample.cu).
+// kernels (head_norm.cu, head_logits.cu, head_sample.cu, head_score.cu,
+// head_distill.cuh).
 #pragma once
 
 #include <cuda_bf16.h>

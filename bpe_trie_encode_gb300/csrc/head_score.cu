@@ -53,49 +53,72 @@ constexpr uint32_t kScoreBytes = ScoreShared<kLanes>::kFeedBytes + (uint32_t)(kT
 __device__ __forceinline__ u64 entry_of(uint32_t key, uint32_t id) { return (u64)key << 32 | (uint32_t)~id; }
 
 // The alternatives in `list`, at most k of this CTA's, for any logits: the key of the k-th largest is found by bits, two
-// a pass; those above it are listed, and as many of its equals, in order of ids, as there is room for.  Gives the team's turn.
+// a pass; those above it are listed, and as many of its equals, in order of ids, as there is room for.  `have` >= 0: the lists
+// hold all logits above kLow, so many, and fewer than k; then there may be no more, or those that a mask has set to one value,
+// the largest of the others (256 x 32,256 bf16 with 5 others, 20 alternatives: 78 us by bits).  Gives the team's turn.
 template <typename T, int kLanes, bool kTeam>
-__device__ __noinline__ int list_any(ScoreShared<kLanes> &S, u64 *list, Team<kLanes, kTeam> team, RowView<T> row, uint32_t lo, uint32_t hi, uint32_t k) {
+__device__ __noinline__ int list_any(ScoreShared<kLanes> &S, u64 *list, Team<kLanes, kTeam> team, RowView<T> row, uint32_t lo, uint32_t hi,
+                                     uint32_t k, float have) {
     constexpr int kVec = RowView<T>::kVec, kShift = Bits<T>::kShift, kBits = (32 - kShift + 1) & ~1;
     uint32_t some = 0;
+    float low = -INFINITY;                 // the largest at or below kLow
     for (uint32_t i = lo + team.thread; i < hi; i += kLanes) {
         float v[kVec];
         unpack(row.load(i), v, T());
 #pragma unroll
-        for (int e = 0; e < kVec; e++) some += v[e] > -INFINITY;
+        for (int e = 0; e < kVec; e++) some += v[e] > -INFINITY, low = v[e] <= Usual<T>::kLow ? fmaxf(low, v[e]) : low;
     }
     const float valid = team.sum(make_float4(some, 0, 0, 0)).x;   // counts up to 2^22 are exact in 32 bits
     const float want = fminf((float)k, valid);
-    if (team.thread == 0) S.list_n = 0;
-    team.sync_cta();
-    if (want == 0.0f) return team.turn;
+    if (want == have) return team.turn;
     uint32_t cut = 0;
-    for (int bit = kBits - 2; bit >= 0; bit -= 2) {
-        uint32_t n1 = 0, n2 = 0, n3 = 0;
+    float4 n;
+    float above_all = -1.0f;
+    if (have >= 0.0f && (low = team.max(low)) > -INFINITY) {
+        cut = key_of(low) >> kShift;
+        uint32_t equal = 0;
+        for (uint32_t i = lo + team.thread; i < hi; i += kLanes) {
+            float v[kVec];
+            unpack(row.load(i), v, T());
+#pragma unroll
+            for (int e = 0; e < kVec; e++) equal += key_of(v[e]) >> kShift == cut;
+        }
+        n = team.sum(make_float4(0, equal, 0, 0));
+        if (have + n.y >= want) above_all = have;
+    }
+    if (above_all < 0.0f) {
+        if (team.thread == 0) S.list_n = 0;
+        team.sync_cta();
+        if (want == 0.0f) return team.turn;
+        cut = 0;
+        for (int bit = kBits - 2; bit >= 0; bit -= 2) {
+            uint32_t n1 = 0, n2 = 0, n3 = 0;
+            for (uint32_t i = lo + team.thread; i < hi; i += kLanes) {
+                float v[kVec];
+                unpack(row.load(i), v, T());
+#pragma unroll
+                for (int e = 0; e < kVec; e++) {
+                    const uint32_t key = key_of(v[e]) >> kShift;
+                    n1 += key >= (cut | 1u << bit), n2 += key >= (cut | 2u << bit), n3 += key >= (cut | 3u << bit);
+                }
+            }
+            const float4 c = team.sum(make_float4(n1, n2, n3, 0));
+            cut |= (c.z >= want ? 3u : c.y >= want ? 2u : c.x >= want ? 1u : 0u) << bit;
+        }
+        uint32_t above = 0, equal = 0;
         for (uint32_t i = lo + team.thread; i < hi; i += kLanes) {
             float v[kVec];
             unpack(row.load(i), v, T());
 #pragma unroll
             for (int e = 0; e < kVec; e++) {
-                const uint32_t key = key_of(v[e]) >> kShift;
-                n1 += key >= (cut | 1u << bit), n2 += key >= (cut | 2u << bit), n3 += key >= (cut | 3u << bit);
+                const uint32_t key = key_of(v[e]);
+                if (key >> kShift > cut) list[atomicAdd(&S.list_n, 1)] = entry_of(key, i * kVec + e - row.shift), above++;   // fewer than k
+                equal += key >> kShift == cut;
             }
         }
-        const float4 n = team.sum(make_float4(n1, n2, n3, 0));
-        cut |= (n.z >= want ? 3u : n.y >= want ? 2u : n.x >= want ? 1u : 0u) << bit;
+        n = team.sum(make_float4(above, equal, 0, 0));
+        above_all = n.x;
     }
-    uint32_t above = 0, equal = 0;
-    for (uint32_t i = lo + team.thread; i < hi; i += kLanes) {
-        float v[kVec];
-        unpack(row.load(i), v, T());
-#pragma unroll
-        for (int e = 0; e < kVec; e++) {
-            const uint32_t key = key_of(v[e]);
-            if (key >> kShift > cut) list[atomicAdd(&S.list_n, 1)] = entry_of(key, i * kVec + e - row.shift), above++;   // fewer than k
-            equal += key >> kShift == cut;
-        }
-    }
-    const float4 n = team.sum(make_float4(above, equal, 0, 0));
     uint32_t mine = 0, before = 0;         // equals of this CTA, and of those before it
     if (kTeam) {
         for (uint32_t r = 0; r < team.rank; r++) before += (uint32_t)team.S.slot[team.turn][r].y;
@@ -103,7 +126,7 @@ __device__ __noinline__ int list_any(ScoreShared<kLanes> &S, u64 *list, Team<kLa
     } else {
         mine = (uint32_t)n.y;
     }
-    const uint32_t need = (uint32_t)(want - n.x);
+    const uint32_t need = (uint32_t)(want - above_all);
     const uint32_t quota = min(mine, need > before ? need - before : 0u);
     uint32_t seen = 0;
     for (uint32_t i0 = lo; i0 < hi && seen < quota; i0 += kLanes) {
@@ -405,7 +428,7 @@ __global__ void __launch_bounds__(kLanes == 32 ? kWarpRows * 32 : kLanes, kLanes
     if (kLanes > 32 && !kTeam && !kTops && team.warp > 0 && usual<T>(all.m, c)) return;
     if (!usual<T>(all.m, c)) all = softmax_any<T, kLanes, kTeam>(team, lo, hi, c, [=](uint32_t i) { return row.load(i); });
     // more equal or masked logits than the list holds, or fewer others than were asked for
-    if (kTops && count < (float)min(k, P.row.n_tok)) team.turn = list_any<T, kLanes, kTeam>(S, list, team, row, lo, hi, k);
+    if (kTops && count < (float)min(k, P.row.n_tok)) team.turn = list_any<T, kLanes, kTeam>(S, list, team, row, lo, hi, k, count);
 
     const bool none = all.m == -INFINITY;
     const float log_s = none ? 0.0f : logf(all.s);

@@ -213,6 +213,37 @@ def test_logprobs_of_hard_rows(ctx, dtype, n, top):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("rows,n", [(7, 50), (7, 5000), (7, 300_000), (900, 2000)])
+def test_alternatives_of_masked_rows(ctx, dtype, rows, n):
+    """Fewer tokens than alternatives, the others at -infinity, at the type's lowest value, or at several low values."""
+    low = torch.finfo(dtype).min
+    x = 2 * randn(rows, n, seed=91)
+    keep = torch.zeros(rows, n, dtype=torch.bool)
+    keep.scatter_(1, torch.randint(0, n, (rows, 6), generator=torch.Generator().manual_seed(4)), True)
+    x[0::7] = torch.where(keep, x, -INF)[0::7]
+    x[1::7] = torch.where(keep, x, low)[1::7]
+    x[2::7] = torch.where(keep, x, NAN)[2::7]
+    x[3::7] = torch.where(keep, x, -INF)[3::7]
+    x[3::7, n - 3:] = low                          # three masked ones at the end, and nothing else
+    x[4::7] = torch.where(keep, x, low)[4::7]
+    x[4::7, n // 2:n // 2 + 2] = low / 2           # two values below every other
+    x[5::7] = torch.where(keep, x, low / 2)[5::7]
+    x[5::7, n // 3] = low
+    x = x.to(dtype).cuda()
+    some = torch.arange(min(rows, 14))
+    for top in (1, 5, 6, 7, 20, 128):
+        for t in (1.0, 0.7):
+            out = ctx.head_logprobs(x, None, temperature=t, top=top)
+
+            class Some:
+                @staticmethod
+                def head_logprobs(*_, **__):
+                    return tuple(o if o is None else o[:len(some)] for o in out)
+
+            check_logprobs(Some, x[:len(some)], None, t=t, top=top)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
 @pytest.mark.parametrize("n", [40, 4351])
 def test_logprobs_at_any_temperature(ctx, dtype, n):
     ts = [1.0, 0.01, 100.0, 0.0, -1.0, NAN, INF, 2.0 ** -126, 2.0 ** -127, 1e-30, 1e30, 3e38, 1e-4, 1e5]
