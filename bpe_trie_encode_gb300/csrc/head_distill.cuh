@@ -137,7 +137,8 @@ struct Entries {
             q_sum += q;
             S.id[i] = id[j], S.q[i] = q, S.v[i] = v[j];
             if (id[j] == ~0u) continue;
-            for (uint32_t h = id[j] * 2654435769u >> 24;; h = (h + 1) % kHash) {   // at most 128 of 256 places are taken
+            // at most 128 of 256 places are taken; ids at equal distances are spread as others are
+            for (uint32_t h = fmix32(id[j]) % kHash;; h = (h + 1) % kHash) {
                 const uint32_t old = atomicCAS(&S.hash[h], ~0u, id[j]);
                 if (old == ~0u) break;
                 if (old == id[j]) {
