@@ -174,6 +174,11 @@ __device__ __forceinline__ float exp2_of(float x) {
     return r;
 }
 
+// R of a largest logit m, but no less than -2^25.  Far from 0 the rounding of m c2 is more than a step of the exponent, from 2^31
+// on more than all of its range, so that what a tile, a warp or a CTA of masked logits alone weighs relative to its own largest
+// may come out infinite.  Relative to -2^25 it is 0, as it is beside the largest of a usual row.
+__device__ __forceinline__ float base_of(float m, float c2) { return fmaxf(__fmul_rn(m, c2), -0x1p25f); }
+
 // Two numbers of 32 bits in one register pair.
 struct Pair {
     u64 b;
@@ -338,7 +343,7 @@ template <typename T, bool kEntropy> struct Running {
     }
     // Before the first tile, whose largest logit is m.
     __device__ __forceinline__ void begin(float m, float c2) {
-        r = __fmul_rn(key_value(__reduce_max_sync(kFull, key_of(m))), c2);
+        r = base_of(key_value(__reduce_max_sync(kFull, key_of(m))), c2);
     }
     // Adds a raised tile whose largest logit is m.
     template <int kSize, int kLanes> __device__ __forceinline__ void add(const Tile<T, kSize, kLanes> &t, float m, float c2) {
@@ -460,7 +465,7 @@ template <bool kEntropy, int kN> __device__ __forceinline__ float4 join_lanes(fl
     float m = v.x;
 #pragma unroll
     for (int d = kN / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-    const float d = __fmul_rn(v.x, c2) - __fmul_rn(m, c2), f = exp2_of(d);
+    const float d = base_of(v.x, c2) - base_of(m, c2), f = exp2_of(d);
     v = make_float4(m, v.y * f, kEntropy ? fmaf(v.y, d, v.z) * f : 0.0f, v.w);
 #pragma unroll
     for (int e = kN / 2; e > 0; e >>= 1) {
@@ -477,7 +482,7 @@ template <typename T, bool kEntropy, int kLanes, bool kTeam>
 __device__ __forceinline__ Softmax softmax_join(Team<kLanes, kTeam> &team, Running<T, kEntropy> a, float c2, float &count) {
     constexpr int kWarps = kLanes / 32;
     const float m = key_value(__reduce_max_sync(kFull, key_of(a.most)));
-    a.move(__fmul_rn(m, c2));
+    a.move(base_of(m, c2));
     const float2 s = a.s.both(), sz = a.sz.both();
     float4 v = make_float4(m, s.x + s.y, sz.x + sz.y, team.warp == 0 ? count : 0.0f);
 #pragma unroll
