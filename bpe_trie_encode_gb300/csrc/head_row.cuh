@@ -149,10 +149,13 @@ __device__ __forceinline__ float z_any(float v, float m, float c) {
 // that one, which are scaled when a larger one comes.  In powers of two, z = v (c log2 e) - R with R = m (c log2 e) rounded
 // once, so that a logit costs one fused step and one exponential.
 //
-// That needs numbers that stay finite: logits below `kLow` count as it, and what comes out holds where they have no weight:
-// where the row is `usual`.  Others (masked by the type's lowest value throughout, infinite, at far temperatures) take the
-// general form, softmax_any.
+// That needs numbers that stay finite: logits below `kLow` count as it, and what comes out holds where they have no weight,
+// and where the largest logit's own z, what R was rounded by, is at most one step of the exponent: where the row is `usual`.
+// Others (masked by the type's lowest value or another far from 0 throughout, infinite, at far temperatures, |m| / T above
+// 2^24) take the general form, softmax_any.
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+constexpr float kMostMc = 0x1p24f;         // m c log2 e below 2^24.6: numbers are 2 apart there
 
 template <typename T> struct Usual {
     static constexpr float kLow = -0x1p60f, kLeast = -0x1p50f, kMost = 0x1p50f, kMinC = 0x1p-40f, kMaxC = 0x1p20f;
@@ -161,7 +164,7 @@ template <> struct Usual<__half> {   // its lowest number is -65,504; from -16,3
     static constexpr float kLow = -65504.0f, kLeast = -16384.0f, kMost = 65504.0f, kMinC = 0x1p-6f, kMaxC = 0x1p20f;
 };
 template <typename T> __device__ __forceinline__ bool usual(float m, float c) {
-    return m >= Usual<T>::kLeast && m <= Usual<T>::kMost && c >= Usual<T>::kMinC && c <= Usual<T>::kMaxC;
+    return m >= Usual<T>::kLeast && m <= Usual<T>::kMost && c >= Usual<T>::kMinC && c <= Usual<T>::kMaxC && fabsf(m) * c <= kMostMc;
 }
 // What the sums run with in its place until that is known (a far c would make them NaN; they are not used then).
 template <typename T> __device__ __forceinline__ float usual_c(float c) {
@@ -174,9 +177,9 @@ __device__ __forceinline__ float exp2_of(float x) {
     return r;
 }
 
-// R of a largest logit m, but no less than -2^25.  Far from 0 the rounding of m c2 is more than a step of the exponent, from 2^31
-// on more than all of its range, so that what a tile, a warp or a CTA of masked logits alone weighs relative to its own largest
-// may come out infinite.  Relative to -2^25 it is 0, as it is beside the largest of a usual row.
+// R of a largest logit m, but no less than -2^25, which is below any usual row's.  Far from 0 the rounding of m c2 is more than a
+// step of the exponent, from 2^31 on more than all of its range, so that what a tile, a warp or a CTA of masked logits alone
+// weighs relative to its own largest may come out infinite.  Relative to -2^25 it is 0, as it is beside the row's largest.
 __device__ __forceinline__ float base_of(float m, float c2) { return fmaxf(__fmul_rn(m, c2), -0x1p25f); }
 
 // Two numbers of 32 bits in one register pair.

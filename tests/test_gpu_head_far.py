@@ -111,3 +111,81 @@ def test_many_rows_with_parts_masked_far(ctx, dtype, rows, n):
     x = torch.where(kept == INF, far[torch.arange(rows) % 5][:, None].cuda(), x).to(dtype)
     t = torch.tensor([1.0, 0.1, 0.01] if dtype != F16 else [1.0, 1e-5, 2e-6])[torch.arange(rows) // 35 % 3].cuda()
     check_all(ctx, x, t, tops=(0, 5, 21, 64), check=torch.arange(0, rows, 1)[:105])
+
+
+# ------------------------------------------------------------ rows that are far ---
+
+def far_rows(n, dtype):
+    """Rows of which all logits are far from 0, or all but one or two."""
+    v = [-1e9, -1e10, -3e11, -1e12, -1e15, 1e10, 1e12, 2.0 ** 49, -2.0 ** 49] if dtype != F16 else [-16000.0, -65504.0, 65504.0, 3e4]
+    x = torch.empty(2 * len(v) + 4, n, dtype=torch.float64)
+    for i, one in enumerate(v):
+        x[2 * i] = one
+        x[2 * i + 1] = one * (1 + 2.0 ** -6 * randn(n, seed=i).abs())   # far apart, all but some
+    x[-4] = 1.0
+    x[-4, 0] = v[5] if dtype != F16 else 65504.0
+    x[-3] = v[1]
+    x[-3, n - 1] = 0.5
+    x[-2] = v[3]
+    x[-2, : n // 2] = v[1]
+    x[-1] = 2 * randn(n, seed=99)
+    big = torch.finfo(dtype).max
+    return x.clamp(-big, big).to(dtype).cuda()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("n", [2, 300, 5000, 70001])
+@pytest.mark.parametrize("t", [1.0, 0.1, 1e-5, 2e-6])
+def test_rows_far_from_0(ctx, dtype, n, t):
+    logits = far_rows(n, dtype)
+    check_all(ctx, logits, torch.full((len(logits),), t).cuda())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,n", [(20, 400), (20, 40000), (1300, 900)])
+def test_unlisted_tokens_far_below_the_listed(ctx, dtype, rows, n):
+    """Listed tokens as usual and the unlisted ones masked: the far ones among themselves decide the rest's shares."""
+    value = torch.tensor([-1e9, -1e10, -1e12, -1e15])[torch.arange(rows) % 4][:, None].double()
+    x = value * (1 + 2.0 ** -20 * randn(rows, n, seed=7).abs() * (torch.arange(rows) % 2)[:, None])
+    listed = (torch.arange(6) * 31 + 5)[None].expand(rows, 6) % n
+    x = x.scatter(1, listed, 3 * randn(rows, 6, seed=8)).to(dtype).cuda()
+    t = torch.tensor([1.0, 0.5])[torch.arange(rows) // 8 % 2].cuda()
+    check_all(ctx, x, t, tops=(0, 5), teacher=listed.cuda(), check=torch.arange(min(rows, 40)))
+
+
+# On both sides of each number that decides between the usual form and the general one: the inverse of the temperature, the largest
+# logit, and their product.
+def limits(dtype):
+    """(what lies at 0, how far logits spread, temperature)"""
+    for e in (1 - 2.0 ** -9, 1 + 2.0 ** -9):
+        yield 0.0, 2.0 ** -19, 2.0 ** -20 * e
+        yield 4.0, 2.0 ** -19, 2.0 ** -20 * e
+        for s in (1.0, -1.0):
+            yield s * 2.0 ** 24 * e * 2.0 ** -12, 2.0 ** -4, 2.0 ** -12
+            yield s * 2.0 ** 24 * e * 2.0 ** -20, 2.0 ** -18, 2.0 ** -20
+            yield s * 2.0 ** 14 * e, 4.0, 1.0
+        if dtype == F16:
+            yield 0.0, 100.0, 64.0 * e
+            yield -16384.0 * e, 30.0, 10.0
+            yield 65000.0 * min(e, 1), 30.0, 60.0
+        else:
+            yield 0.0, 2.0 ** 41, 2.0 ** 40 * e
+            for s in (1.0, -1.0):
+                yield s * 2.0 ** 24 * e, 4.0, 1.0
+                yield s * 2.0 ** 25 * e, 4.0, 1.0
+                yield s * 2.0 ** 50 * e, 2.0 ** 33, 2.0 ** 32
+                yield s * 2.0 ** 50 * e, 2.0 ** 28, 2.0 ** 26
+                yield s * 2.0 ** 60 * e, 2.0 ** 41, 2.0 ** 39
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("n", [9, 1000, 20000])
+def test_both_sides_of_the_usual_form(ctx, dtype, n):
+    every = list(limits(dtype))
+    rows = 2 * len(every)
+    x, t = torch.empty(rows, n, dtype=torch.float64), torch.empty(rows)
+    for i, (at, spread, temperature) in enumerate(every):
+        x[2 * i:2 * i + 2], t[2 * i:2 * i + 2] = at + spread * randn(2, n, seed=i), temperature
+        if n > 4:   # half of the second one masked at the type's lowest number
+            x[2 * i + 1, n // 2:] = torch.finfo(dtype).min
+    check_all(ctx, x.to(dtype).cuda(), t.cuda(), tops=(0, 3))
