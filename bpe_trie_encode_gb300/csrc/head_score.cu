@@ -510,12 +510,14 @@ __global__ void __launch_bounds__(256) k_logprobs_backward(ScoreGradParams P, ui
     const bool given = id >= 0 && (uint32_t)id < P.row.n_tok;
     const float a = given && P.grad_logprob ? P.grad_logprob[r] : 0.0f;
     const float b = kEntropy ? P.grad_entropy[r] : 0.0f, h = kEntropy ? P.entropy[r] : 0.0f;
-    const bool zero = m == -INFINITY || c == INFINITY, fast = usual<T>(m, c);
+    const bool zero = m == -INFINITY || c == INFINITY;
     // x = exp2(z) of the logits relative to R, m c log2 e rounded; d = x (f + g z), and c a more for the id itself.  The
     // factor 1 / s, and what R was rounded by, are part of f and g.
     const float c2 = c * kLog2e, off = __fmul_rn(m, c2), d0 = fmaf(m, c2, -off);
     const float w = c * exp2_of(-fmaf(log_s, kLog2e, d0));
     const float f = -w * (a + b * (h - log_s - d0 * kLn2)), g = -w * b * kLn2;
+    // A masked logit's x is 0, and its z kLow c2 - R: f + g z is to be finite, or 0 times it is NaN.
+    const bool fast = usual<T>(m, c) && fabsf(f) + fabsf(g) * fmaf(-Usual<T>::kLow, c2, fabsf(off)) <= 0x1p126f;
     const Pair c22(c2, c2), off2(-off, -off), f2(f, f), g2(g, g);
     const uint32_t hot = given ? row.shift + (uint32_t)id : ~0u;
     for (uint32_t n = 0; n * Tiles::kVecs < hi - lo; n++) {

@@ -189,3 +189,27 @@ def test_both_sides_of_the_usual_form(ctx, dtype, n):
         if n > 4:   # half of the second one masked at the type's lowest number
             x[2 * i + 1, n // 2:] = torch.finfo(dtype).min
     check_all(ctx, x.to(dtype).cuda(), t.cuda(), tops=(0, 3))
+
+
+# ------------------------------------------------------- gradients of any size ---
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("rows,n", [(6, 300), (6, 6000), (400, 900)])
+def test_masked_logits_have_no_gradient_however_large_its_weight(ctx, dtype, rows, n):
+    """What is multiplied by a probability of 0 may be beyond 32 bits: the product is 0."""
+    x = masked_parts(rows, n, -INF, dtype)
+    x[:, 1] = torch.finfo(dtype).min
+    x[:, 5] = 1.0
+    gone = torch.isinf(x)
+    gone[:, 1] = True
+    if dtype == F16:
+        gone = x < -60000
+    ids = some_ids(x)
+    for t, weights in ((1.0, (1.0, 2.0 ** 66, 2.0 ** 70, 2.0 ** 120, -3e38)), (2.0 ** -19, (1e-6, 2.0 ** 28, 2.0 ** 31, 2.0 ** 60, -3e38))):
+        _, h, _, _, norm = ctx.head_logprobs(x, ids, temperature=t)
+        for w in weights:
+            w = torch.full((rows,), w).cuda()
+            for a, b in ((w, None), (None, w), (w, w)):
+                d = ctx.head_logprobs_backward(x, ids if a is not None else None, norm, a, None if b is None else h, b, temperature=t)
+                listed = torch.zeros_like(gone).scatter_(1, ids.long().clamp_min(0)[:, None], a is not None and (ids >= 0)[:, None])
+                assert (d[gone & ~listed] == 0).all(), (t, w[0])
