@@ -73,6 +73,9 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// x y, and 0 where x is 0 whatever y is.
+__device__ __forceinline__ float product(float x, float y) { return x == 0.0f ? 0.0f : x * y; }
+
 // q (log q - log p) - q + p = q (e^d - 1 - d), d = log p - log q, which is never below 0.  Where all q and all p add up to 1 the
 // sum of these terms is the divergence, and one that is small, since teacher and student agree, is not the difference of far
 // larger ones.
@@ -311,8 +314,10 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kCtas<kLanes>) k_distill(Dis
 
     const RowView<T> out(P.out, P.out_stride, r, P.row.n_tok);
     const bool zero = none || c == INFINITY;
+    // c and grad together may be beyond 32 bits: what they are multiplied by is 0 where no token has a share, and the product too
     const float g = zero ? 0.0f : c * grad;
-    const float of_free = zero || free.m == -INFINITY ? 0.0f : g * (q_total / s * to_all - (q_rest > 0.0f ? q_rest / free.s : 0.0f));
+    const float of_free = zero || free.m == -INFINITY ? 0.0f : product(q_total / s * to_all - (q_rest > 0.0f ? q_rest / free.s : 0.0f), g);
+    const bool finite = fast && fabsf(of_free) <= 0x1p126f;
     const float off = __fmul_rn(free.m, c2), w = of_free * exp2_of(-fmaf(free.m, c2, -off));   // what off was rounded by
     for (uint32_t n = 0; n < steps; n++) {
         const uint32_t i0 = lo + n * Tiles::kVecs;
@@ -325,7 +330,7 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kCtas<kLanes>) k_distill(Dis
             const uint32_t i = t.place(i0, u);
             if (!direct && i >= hi) break;
             float v[kVec];
-            if (fast) {
+            if (finite) {
                 raise<T>(t.q[u]);
                 unpack(t.q[u], v, T());
 #pragma unroll
@@ -337,7 +342,7 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kCtas<kLanes>) k_distill(Dis
             } else {
                 unpack(t.q[u], v, T());
 #pragma unroll
-                for (int e = 0; e < kVec; e++) v[e] = of_free == 0.0f ? 0.0f : expf(z_any(v[e], free.m, c)) * of_free;
+                for (int e = 0; e < kVec; e++) v[e] = of_free == 0.0f ? 0.0f : product(expf(z_any(v[e], free.m, c)), of_free);
             }
             put_vector(out, row, i, v, direct);
         }
@@ -346,7 +351,7 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kCtas<kLanes>) k_distill(Dis
     for (uint32_t i = reads ? team.thread : P.n_listed; i < P.n_listed; i += kLanes) {
         const uint32_t id = S.id[i], at = id + row.shift - lo * kVec;
         if (id != ~0u && at < (hi - lo) * kVec)
-            out.at[out.shift + id] = from_f32<T>(zero ? 0.0f : g * (q_total * expf(z_any(S.v[i], m, c) - log_s) - S.q[i]));
+            out.at[out.shift + id] = from_f32<T>(zero ? 0.0f : product(q_total * expf(z_any(S.v[i], m, c) - log_s) - S.q[i], g));
     }
 }
 

@@ -213,3 +213,20 @@ def test_masked_logits_have_no_gradient_however_large_its_weight(ctx, dtype, row
                 d = ctx.head_logprobs_backward(x, ids if a is not None else None, norm, a, None if b is None else h, b, temperature=t)
                 listed = torch.zeros_like(gone).scatter_(1, ids.long().clamp_min(0)[:, None], a is not None and (ids >= 0)[:, None])
                 assert (d[gone & ~listed] == 0).all(), (t, w[0])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("rows,n", [(6, 300), (6, 6000), (400, 900)])
+@pytest.mark.parametrize("rest", [False, True])
+def test_masked_logits_have_no_distilled_gradient_however_large_its_weight(ctx, dtype, rows, n, rest):
+    x = masked_parts(rows, n, -INF, dtype)
+    x[:, 5] = 1.0
+    x[:, 7] = -INF
+    gone = torch.isinf(x)
+    tids = torch.tensor([[5, 7, 9]], dtype=torch.int32).expand(rows, 3).contiguous().cuda()
+    values = torch.tensor([[-0.5, -300.0, -2.0]]).expand(rows, 3).contiguous().cuda()   # no q is left of the masked one
+    listed = torch.zeros_like(gone).scatter_(1, tids[:, ::2].long(), True)
+    for t in (1.0, 2.0 ** -19, 1e-30):
+        for w in (1.0, 2.0 ** 100, 2.0 ** 120, -3e38):
+            d = ctx.head_distill(x, tids, values, temperature=t, rest=rest, grad=w)[1]
+            assert (d[gone & ~listed] == 0).all(), (t, w)
