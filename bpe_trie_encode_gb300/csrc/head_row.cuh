@@ -164,7 +164,9 @@ template <> struct Usual<__half> {   // its lowest number is -65,504; from -16,3
     static constexpr float kLow = -65504.0f, kLeast = -16384.0f, kMost = 65504.0f, kMinC = 0x1p-6f, kMaxC = 0x1p20f;
 };
 template <typename T> __device__ __forceinline__ bool usual(float m, float c) {
-    return m >= Usual<T>::kLeast && m <= Usual<T>::kMost && c >= Usual<T>::kMinC && c <= Usual<T>::kMaxC && fabsf(m) * c <= kMostMc;
+    float mc;   // written out: as an expression among the others it gives distillation with gradient another order of instructions
+    asm("mul.rn.f32 %0, %1, %2;" : "=f"(mc) : "f"(fabsf(m)), "f"(c));   // (8,192 x 32,256 bf16: 173.9 us, 171.4 so)
+    return m >= Usual<T>::kLeast && m <= Usual<T>::kMost && c >= Usual<T>::kMinC && c <= Usual<T>::kMaxC && mc <= kMostMc;
 }
 // What the sums run with in its place until that is known (a far c would make them NaN; they are not used then).
 template <typename T> __device__ __forceinline__ float usual_c(float c) {
