@@ -32,6 +32,7 @@ Scoring given ids, and learning from a teacher, with logits [rows, n_tok]:
 from __future__ import annotations
 
 import ctypes
+import threading
 
 import numpy as np
 import torch
@@ -47,13 +48,7 @@ __all__ = ["Context", "Trie", "Unigram", "BpeError", "vocab_from_merges", "BPE_W
 
 
 # the current stream's handle without a Stream object around it, where torch has that (2 us of a call's 10)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream_ptr(device: torch.device) -> int:
-    if _raw_stream is not None:
-        return _raw_stream(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _need_cuda(t: torch.Tensor, dtype: torch.dtype, name: str, device: torch.device) -> torch.Tensor:
@@ -186,7 +181,8 @@ class Trie:
 
 class Context:
     """A library context on one CUDA device.  Calls are ordered on the torch
-    current stream of that device at the time of each call."""
+    current stream of that device at the time of each call.  Threads may share
+    a context for the head_ calls: each runs on its own thread's stream."""
 
     def __init__(self, device=None):
         if not torch.cuda.is_available():
@@ -195,21 +191,23 @@ class Context:
         self.device = torch.device("cuda", torch.cuda.current_device() if device is None
                                    else torch.device(device).index or 0)
         h = ctypes.c_void_p()
-        self._stream = _stream_ptr(self.device)
-        rc = self.lib.bpe_ctx_create(ctypes.byref(h), self.device.index, ctypes.c_void_p(self._stream))
+        self._lock = threading.Lock()   # a stream is handed over and used in one turn
+        rc = self.lib.bpe_ctx_create(ctypes.byref(h), self.device.index, ctypes.c_void_p(_raw_stream(self.device.index)))
         if rc != 0:
             raise BpeError(rc, "bpe_ctx_create failed")
         self._h = h
+        self._at = ctypes.c_size_t.from_address(self.lib.bpe_ctx_stream(h))   # the library's own word of it
 
     # -- plumbing -----------------------------------------------------------
     def _sync_stream(self):
-        stream = _stream_ptr(self.device)
-        if stream != self._stream:
-            self.lib.bpe_ctx_set_stream(self._h, ctypes.c_void_p(stream))
-            self._stream = stream
+        """Orders the call that follows, in the same hold of ``_lock``, on the current stream."""
+        stream = _raw_stream(self.device.index)
+        if self._at.value != stream:   # a look costs 0.04 us, handing over 0.25, and 1.5 where the GPU has been waited for
+            self.lib.bpe_ctx_set_stream(self._h, stream)
 
     def close(self):
         if getattr(self, "_h", None):
+            self._at = ctypes.c_size_t()   # the library's is gone
             self.lib.bpe_ctx_destroy(self._h)
             self._h = None
 
@@ -241,9 +239,10 @@ class Context:
         out = _need_cuda(out, torch.int32, "out", self.device)
         if out.numel() < n:
             raise ValueError("out too small")
-        self._sync_stream()
-        _capi.check(self._h, self.lib.bpe_pretokenize(self._h, ctypes.c_void_p(data.data_ptr()), n,
-                                                      ctypes.c_void_p(out.data_ptr())))
+        with self._lock:
+            self._sync_stream()
+            _capi.check(self._h, self.lib.bpe_pretokenize(self._h, ctypes.c_void_p(data.data_ptr()), n,
+                                                          ctypes.c_void_p(out.data_ptr())))
         return out[:n]
 
     def train(self, symbols: torch.Tensor, n_merges: int, final: bool = True):
@@ -255,12 +254,13 @@ class Context:
         n_done = ctypes.c_uint32(0)
         n_final = ctypes.c_uint64(0)
         fin = torch.empty(max(n, 1), dtype=torch.int32, device=self.device) if final else None
-        self._sync_stream()
-        rc = self.lib.bpe_train(self._h, ctypes.c_void_p(symbols.data_ptr() if n else 0), n, n_merges,
-                                merges, ctypes.byref(n_done),
-                                ctypes.c_void_p(fin.data_ptr()) if fin is not None else None,
-                                ctypes.byref(n_final))
-        _capi.check(self._h, rc)
+        with self._lock:
+            self._sync_stream()
+            rc = self.lib.bpe_train(self._h, ctypes.c_void_p(symbols.data_ptr() if n else 0), n, n_merges,
+                                    merges, ctypes.byref(n_done),
+                                    ctypes.c_void_p(fin.data_ptr()) if fin is not None else None,
+                                    ctypes.byref(n_final))
+            _capi.check(self._h, rc)
         m = np.frombuffer(merges, dtype=np.uint32).reshape(-1, 4)[: n_done.value].copy()
         return m, (fin[: n_final.value] if fin is not None else None)
 
@@ -296,14 +296,15 @@ class Context:
         n_ids = ctypes.c_uint64(0)
         if data.numel() == 0:   # keep a valid device pointer for empty input
             data = torch.empty(16, dtype=torch.uint8, device=self.device)
-        self._sync_stream()
-        rc = self.lib.trie_encode(self._h, trie._h, ctypes.c_void_p(data.data_ptr()),
-                                  ctypes.c_void_p(doc_off.data_ptr()), max(n_docs, 0),
-                                  ctypes.c_void_p(ids_out.data_ptr()), cap,
-                                  ctypes.c_void_p(id_off.data_ptr()), ctypes.byref(n_ids))
-        if rc == -6:
-            raise BpeError(rc, f"{n_ids.value} ids needed, capacity {cap}")
-        _capi.check(self._h, rc)
+        with self._lock:
+            self._sync_stream()
+            rc = self.lib.trie_encode(self._h, trie._h, ctypes.c_void_p(data.data_ptr()),
+                                      ctypes.c_void_p(doc_off.data_ptr()), max(n_docs, 0),
+                                      ctypes.c_void_p(ids_out.data_ptr()), cap,
+                                      ctypes.c_void_p(id_off.data_ptr()), ctypes.byref(n_ids))
+            if rc == -6:
+                raise BpeError(rc, f"{n_ids.value} ids needed, capacity {cap}")
+            _capi.check(self._h, rc)
         return ids_out[: n_ids.value], id_off[: n_docs + 1]
 
     def decode(self, merges, ids: torch.Tensor) -> torch.Tensor:
@@ -313,15 +314,16 @@ class Context:
         arr, n = _merge_array(merges)
         n_bytes = ctypes.c_uint64(0)
         ptr = ctypes.c_void_p(ids.data_ptr() if ids.numel() else 0)
-        self._sync_stream()
-        rc = self.lib.bpe_decode(self._h, arr, n, ptr, ids.numel(), None, 0, ctypes.byref(n_bytes))
-        if rc not in (0, -6):
-            _capi.check(self._h, rc)
-        out = torch.empty(max(n_bytes.value, 1), dtype=torch.uint8, device=self.device)
-        if ids.numel():
-            _capi.check(self._h, self.lib.bpe_decode(self._h, arr, n, ptr, ids.numel(),
-                                                     ctypes.c_void_p(out.data_ptr()), out.numel(),
-                                                     ctypes.byref(n_bytes)))
+        with self._lock:
+            self._sync_stream()
+            rc = self.lib.bpe_decode(self._h, arr, n, ptr, ids.numel(), None, 0, ctypes.byref(n_bytes))
+            if rc not in (0, -6):
+                _capi.check(self._h, rc)
+            out = torch.empty(max(n_bytes.value, 1), dtype=torch.uint8, device=self.device)
+            if ids.numel():
+                _capi.check(self._h, self.lib.bpe_decode(self._h, arr, n, ptr, ids.numel(),
+                                                         ctypes.c_void_p(out.data_ptr()), out.numel(),
+                                                         ctypes.byref(n_bytes)))
         return out[: n_bytes.value]
 
 
@@ -354,14 +356,15 @@ class Context:
         n_ids = ctypes.c_uint64(0)
         if data.numel() == 0:
             data = torch.empty(16, dtype=torch.uint8, device=self.device)
-        self._sync_stream()
-        rc = self.lib.unigram_encode(self._h, model._h, ctypes.c_void_p(data.data_ptr()),
-                                     ctypes.c_void_p(doc_off.data_ptr()), max(n_docs, 0),
-                                     ctypes.c_void_p(ids_out.data_ptr()), cap,
-                                     ctypes.c_void_p(id_off.data_ptr()), ctypes.byref(n_ids))
-        if rc == -6:
-            raise BpeError(rc, f"{n_ids.value} ids needed, capacity {cap}")
-        _capi.check(self._h, rc)
+        with self._lock:
+            self._sync_stream()
+            rc = self.lib.unigram_encode(self._h, model._h, ctypes.c_void_p(data.data_ptr()),
+                                         ctypes.c_void_p(doc_off.data_ptr()), max(n_docs, 0),
+                                         ctypes.c_void_p(ids_out.data_ptr()), cap,
+                                         ctypes.c_void_p(id_off.data_ptr()), ctypes.byref(n_ids))
+            if rc == -6:
+                raise BpeError(rc, f"{n_ids.value} ids needed, capacity {cap}")
+            _capi.check(self._h, rc)
         return ids_out[: n_ids.value], id_off[: n_docs + 1]
 
     # -- the output head ------------------------------------------------------
@@ -399,12 +402,13 @@ class Context:
         if scales is None:
             scales = torch.empty(blocks, rows, dtype=torch.float32, device=dev).t()
         s_row, s_block = _head_scales(scales, "scales", dev, rows, blocks, out=True)
-        self._sync_stream()
-        rc = self.lib.head_norm(self._h, x.data_ptr(), x_stride, _HEAD_TYPES[dtype], weight.data_ptr(),
-                                _HEAD_TYPES[weight.dtype], r_ptr, r_stride, rows, dim, eps, ro_ptr, ro_stride,
-                                out.data_ptr(), y_stride, scales.data_ptr(), s_row, s_block)
-        if rc:
-            _capi.check(self._h, rc)
+        with self._lock:
+            self._sync_stream()
+            rc = self.lib.head_norm(self._h, x.data_ptr(), x_stride, _HEAD_TYPES[dtype], weight.data_ptr(),
+                                    _HEAD_TYPES[weight.dtype], r_ptr, r_stride, rows, dim, eps, ro_ptr, ro_stride,
+                                    out.data_ptr(), y_stride, scales.data_ptr(), s_row, s_block)
+            if rc:
+                _capi.check(self._h, rc)
         return out, scales, residual_out
 
     def head_quantize(self, weight: torch.Tensor):
@@ -417,10 +421,11 @@ class Context:
         w8 = torch.empty(n_tok, -(-dim // 16) * 16, dtype=_E4M3, device=self.device)[:, :dim]
         ws = torch.empty(-(-n_tok // _capi.BPE_HEAD_BLOCK), -(-dim // _capi.BPE_HEAD_BLOCK), dtype=torch.float32,
                          device=self.device)
-        self._sync_stream()
-        _capi.check(self._h, self.lib.head_quantize(self._h, weight.data_ptr(), stride,
-                                                    _HEAD_TYPES[weight.dtype], n_tok, dim, w8.data_ptr(),
-                                                    w8.stride(0), ws.data_ptr(), ws.stride(0)))
+        with self._lock:
+            self._sync_stream()
+            _capi.check(self._h, self.lib.head_quantize(self._h, weight.data_ptr(), stride,
+                                                        _HEAD_TYPES[weight.dtype], n_tok, dim, w8.data_ptr(),
+                                                        w8.stride(0), ws.data_ptr(), ws.stride(0)))
         return w8, ws
 
     def head_logits(self, x8: torch.Tensor, xs: torch.Tensor, w8: torch.Tensor, ws: torch.Tensor,
@@ -447,12 +452,13 @@ class Context:
                 raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
             out = torch.empty(rows, n_tok, dtype=dtype, device=dev)
         out, out_stride = _head_matrix(out, "out", dev, _HEAD_TYPES, (rows, n_tok), out=True)
-        self._sync_stream()
-        rc = self.lib.head_logits(self._h, x8.data_ptr(), x_stride, xs.data_ptr(), xs_row, xs_block, w8.data_ptr(),
-                                  w_stride, ws.data_ptr(), ws_row, ws_block, rows, n_tok, dim, out.data_ptr(),
-                                  out_stride, _HEAD_TYPES[out.dtype])
-        if rc:
-            _capi.check(self._h, rc)
+        with self._lock:
+            self._sync_stream()
+            rc = self.lib.head_logits(self._h, x8.data_ptr(), x_stride, xs.data_ptr(), xs_row, xs_block, w8.data_ptr(),
+                                      w_stride, ws.data_ptr(), ws_row, ws_block, rows, n_tok, dim, out.data_ptr(),
+                                      out_stride, _HEAD_TYPES[out.dtype])
+            if rc:
+                _capi.check(self._h, rc)
         return out
 
     def head_sample(self, logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=None, top_p=None, min_p=None,
@@ -492,11 +498,12 @@ class Context:
         p, d_p = one(top_p, "top_p", torch.float32, 1.0)
         q, d_q = one(min_p, "min_p", torch.float32, 0.0)
         filters = _capi.head_filters(t, k, p, q, d_t, d_k, d_p, d_q)
-        self._sync_stream()
-        rc = self.lib.head_sample(self._h, logits.data_ptr(), stride, _HEAD_TYPES[logits.dtype], rows, n_tok,
-                                  u.data_ptr(), ctypes.byref(filters), ids.data_ptr(), logprob.data_ptr())
-        if rc:
-            _capi.check(self._h, rc)
+        with self._lock:
+            self._sync_stream()
+            rc = self.lib.head_sample(self._h, logits.data_ptr(), stride, _HEAD_TYPES[logits.dtype], rows, n_tok,
+                                      u.data_ptr(), ctypes.byref(filters), ids.data_ptr(), logprob.data_ptr())
+            if rc:
+                _capi.check(self._h, rc)
         return ids, logprob
 
     def head_logprobs(self, logits: torch.Tensor, ids: torch.Tensor | None = None, temperature=1.0, top: int = 0,
@@ -536,14 +543,15 @@ class Context:
         norm = torch.empty(rows, 2, dtype=torch.float32, device=dev) if norm is None else \
             _head_table(norm, "norm", dev, (torch.float32,), rows, 2, out=True)
         t, d_t, t_ptr = _head_number(temperature, "temperature", dev, rows)
-        self._sync_stream()
-        rc = self.lib.head_logprobs(self._h, logits.data_ptr(), stride, _HEAD_TYPES[dtype], rows, n_tok,
-                                    ids.data_ptr() if ids is not None else None, t, t_ptr, top,
-                                    logprob.data_ptr() if ids is not None else None, entropy.data_ptr(),
-                                    top_ids.data_ptr() if top else None, top_logprob.data_ptr() if top else None,
-                                    norm.data_ptr())
-        if rc:
-            _capi.check(self._h, rc)
+        with self._lock:
+            self._sync_stream()
+            rc = self.lib.head_logprobs(self._h, logits.data_ptr(), stride, _HEAD_TYPES[dtype], rows, n_tok,
+                                        ids.data_ptr() if ids is not None else None, t, t_ptr, top,
+                                        logprob.data_ptr() if ids is not None else None, entropy.data_ptr(),
+                                        top_ids.data_ptr() if top else None, top_logprob.data_ptr() if top else None,
+                                        norm.data_ptr())
+            if rc:
+                _capi.check(self._h, rc)
         return logprob, entropy, top_ids, top_logprob, norm
 
     def head_logprobs_backward(self, logits: torch.Tensor, ids: torch.Tensor | None, norm: torch.Tensor,
@@ -577,11 +585,12 @@ class Context:
             out = torch.empty(rows, n_tok, dtype=dtype, device=dev)
         out, out_stride = _head_matrix(out, "out", dev, (dtype,), (rows, n_tok), out=True)
         t, d_t, t_ptr = _head_number(temperature, "temperature", dev, rows)
-        self._sync_stream()
-        rc = self.lib.head_logprobs_backward(self._h, logits.data_ptr(), stride, _HEAD_TYPES[dtype], rows, n_tok, i_ptr,
-                                             t, t_ptr, norm.data_ptr(), a_ptr, h_ptr, b_ptr, out.data_ptr(), out_stride)
-        if rc:
-            _capi.check(self._h, rc)
+        with self._lock:
+            self._sync_stream()
+            rc = self.lib.head_logprobs_backward(self._h, logits.data_ptr(), stride, _HEAD_TYPES[dtype], rows, n_tok, i_ptr,
+                                                 t, t_ptr, norm.data_ptr(), a_ptr, h_ptr, b_ptr, out.data_ptr(), out_stride)
+            if rc:
+                _capi.check(self._h, rc)
         return out
 
     def head_distill(self, logits: torch.Tensor, top_ids: torch.Tensor, top_logprob: torch.Tensor, temperature=1.0,
@@ -618,12 +627,13 @@ class Context:
         elif out is not None:
             raise ValueError("out needs grad")
         t, d_t, t_ptr = _head_number(temperature, "temperature", dev, rows)
-        self._sync_stream()
-        rc = self.lib.head_distill(self._h, logits.data_ptr(), stride, _HEAD_TYPES[dtype], rows, n_tok, top_ids.data_ptr(),
-                                   top_logprob.data_ptr(), _HEAD_TYPES[top_logprob.dtype], listed, int(rest), t, t_ptr,
-                                   loss.data_ptr(), g, g_ptr, o_ptr, o_stride)
-        if rc:
-            _capi.check(self._h, rc)
+        with self._lock:
+            self._sync_stream()
+            rc = self.lib.head_distill(self._h, logits.data_ptr(), stride, _HEAD_TYPES[dtype], rows, n_tok, top_ids.data_ptr(),
+                                       top_logprob.data_ptr(), _HEAD_TYPES[top_logprob.dtype], listed, int(rest), t, t_ptr,
+                                       loss.data_ptr(), g, g_ptr, o_ptr, o_stride)
+            if rc:
+                _capi.check(self._h, rc)
         return loss, out
 
     def head_check(self) -> None:
@@ -631,9 +641,10 @@ class Context:
         has given up a wait: some of its logits are NaN.  The other head_ calls
         on logits ask the same before they start (head_logprobs_backward does
         not); a replayed CUDA graph does not.  Does not wait: call it after a synchronization."""
-        rc = self.lib.head_check(self._h)
-        if rc:
-            _capi.check(self._h, rc)
+        with self._lock:
+            rc = self.lib.head_check(self._h)
+            if rc:
+                _capi.check(self._h, rc)
 
 
 class Unigram:
@@ -673,14 +684,15 @@ def encode_host(ctx: "Context", trie: "Trie", data, doc_off=None, ids_out=None, 
     if id_off_out is None:
         id_off_out = torch.empty(max(n_docs + 1, 1), dtype=torch.int64)
     n = ctypes.c_uint64(0)
-    ctx._sync_stream()
-    rc = ctx.lib.trie_encode_host(ctx._h, trie._h, ctypes.c_void_p(data.data_ptr() if data.numel() else 0),
-                                  ctypes.c_void_p(doc_off.data_ptr()), max(n_docs, 0),
-                                  ctypes.c_void_p(ids_out.data_ptr()), ids_out.numel(),
-                                  ctypes.c_void_p(id_off_out.data_ptr()), ctypes.byref(n), slice_bytes)
-    if rc == -6:
-        raise BpeError(rc, f"{n.value} ids needed, capacity {ids_out.numel()}")
-    _capi.check(ctx._h, rc)
+    with ctx._lock:
+        ctx._sync_stream()
+        rc = ctx.lib.trie_encode_host(ctx._h, trie._h, ctypes.c_void_p(data.data_ptr() if data.numel() else 0),
+                                      ctypes.c_void_p(doc_off.data_ptr()), max(n_docs, 0),
+                                      ctypes.c_void_p(ids_out.data_ptr()), ids_out.numel(),
+                                      ctypes.c_void_p(id_off_out.data_ptr()), ctypes.byref(n), slice_bytes)
+        if rc == -6:
+            raise BpeError(rc, f"{n.value} ids needed, capacity {ids_out.numel()}")
+        _capi.check(ctx._h, rc)
     return ids_out[: n.value], id_off_out[: n_docs + 1]
 
 
@@ -704,12 +716,13 @@ class Stream:
             ids_out = _need_cuda(ids_out, torch.int32, "ids_out", self.ctx.device)
         n_ids = ctypes.c_uint64(0)
         ptr = data.data_ptr() if data.numel() else 0
-        self.ctx._sync_stream()
-        rc = self.ctx.lib.trie_stream_push(self._h, ctypes.c_void_p(ptr), data.numel(), 1 if last else 0,
-                                           ctypes.c_void_p(ids_out.data_ptr()), ids_out.numel(), ctypes.byref(n_ids))
-        if rc == -6:
-            raise BpeError(rc, f"{n_ids.value} ids needed, capacity {ids_out.numel()}")
-        _capi.check(self.ctx._h, rc)
+        with self.ctx._lock:
+            self.ctx._sync_stream()
+            rc = self.ctx.lib.trie_stream_push(self._h, ctypes.c_void_p(ptr), data.numel(), 1 if last else 0,
+                                               ctypes.c_void_p(ids_out.data_ptr()), ids_out.numel(), ctypes.byref(n_ids))
+            if rc == -6:
+                raise BpeError(rc, f"{n_ids.value} ids needed, capacity {ids_out.numel()}")
+            _capi.check(self.ctx._h, rc)
         return ids_out[: n_ids.value]
 
     def close(self):

@@ -31,7 +31,7 @@ BPE_HEAD_BLOCK, BPE_HEAD_MAX_DIM, BPE_HEAD_MAX_TOKENS, BPE_HEAD_MAX_TOP = 128, 3
 
 # every symbol the header declares (checked by the tests)
 EXPORTS = [
-    "bpe_ctx_create", "bpe_ctx_set_stream", "bpe_ctx_destroy", "bpe_last_error",
+    "bpe_ctx_create", "bpe_ctx_set_stream", "bpe_ctx_stream", "bpe_ctx_destroy", "bpe_last_error",
     "bpe_ctx_set_option", "bpe_last_stats", "bpe_pretokenize", "bpe_train",
     "trie_build", "trie_layout", "trie_info", "trie_free", "trie_encode",
     "trie_encode_noalloc", "trie_stream_open", "trie_stream_push", "trie_stream_close",
@@ -88,6 +88,7 @@ def load() -> ctypes.CDLL:
         sig = {
             "bpe_ctx_create": (i32, [P(vp), i32, vp]),
             "bpe_ctx_set_stream": (i32, [vp, vp]),
+            "bpe_ctx_stream": (vp, [vp]),
             "bpe_ctx_destroy": (None, [vp]),
             "bpe_last_error": (ctypes.c_char_p, [vp]),
             "bpe_ctx_set_option": (i32, [vp, i32, ctypes.c_int64]),

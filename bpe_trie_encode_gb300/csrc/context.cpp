@@ -191,6 +191,8 @@ extern "C" int bpe_ctx_set_stream(bpe_ctx *ctx, void *cuda_stream) {
     return BPE_OK;
 }
 
+extern "C" const uintptr_t *bpe_ctx_stream(const bpe_ctx *ctx) { return ctx ? (const uintptr_t *)&ctx->stream : nullptr; }
+
 extern "C" void bpe_ctx_destroy(bpe_ctx *ctx) {
     if (!ctx) return;
     cudaSetDevice(ctx->device);

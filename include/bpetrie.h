@@ -67,8 +67,15 @@ typedef struct {
  * Errors: INVALID_ARG (out NULL, bad device), CUDA. */
 int bpe_ctx_create(bpe_ctx **out, int device, void *cuda_stream);
 
-/* Change the stream later calls are ordered on. */
+/* Change the stream later calls are ordered on, whichever thread makes them:
+ * threads that share a context, each with a stream of its own, set it and call
+ * in one turn. */
 int bpe_ctx_set_stream(bpe_ctx *ctx, void *cuda_stream);
+
+/* Where the context keeps that stream, as a number, so that a caller may look
+ * before it hands one over.  Valid until bpe_ctx_destroy.  NULL for a null
+ * context. */
+const uintptr_t *bpe_ctx_stream(const bpe_ctx *ctx);
 
 /* Release the context and its scratch (waits for its stream first). */
 void bpe_ctx_destroy(bpe_ctx *ctx);
