@@ -47,6 +47,9 @@ from ._capi import (BPE_MAX_MERGES, BPE_MERGE_LISTS, BPE_MERGE_LOOKBACK, BPE_MER
 __all__ = ["Context", "Trie", "Unigram", "BpeError", "vocab_from_merges", "BPE_WORD_START", "BPE_MAX_MERGES"]
 
 
+# notes for autograd that a tensor was written to, as torch's own calls do
+_overwritten = torch.autograd.graph.increment_version
+
 # the current stream's handle without a Stream object around it, where torch has that (2 us of a call's 10)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -563,8 +566,9 @@ class Context:
         0) that ``head_logprobs`` gave for the same logits, ids and
         temperature, from its norm and, with grad_entropy, its entropy.  A row
         whose id is outside 0 .. n_tok - 1 has no part of grad_logprob.
-        ``out`` may be the logits themselves.  Asynchronous on the current
-        stream."""
+        ``out`` may be the logits themselves (where autograd has kept them for
+        the backward pass of what made them, that raises an error, as after any
+        call that overwrites).  Asynchronous on the current stream."""
         dev = self.device
         logits, stride, rows, n_tok, dtype = _head_rows(logits, "logits", dev)
         norm = _head_table(norm, "norm", dev, (torch.float32,), rows, 2)
@@ -591,6 +595,8 @@ class Context:
                                                  t, t_ptr, norm.data_ptr(), a_ptr, h_ptr, b_ptr, out.data_ptr(), out_stride)
             if rc:
                 _capi.check(self._h, rc)
+        if out.data_ptr() == logits.data_ptr():
+            _overwritten(out)
         return out
 
     def head_distill(self, logits: torch.Tensor, top_ids: torch.Tensor, top_logprob: torch.Tensor, temperature=1.0,
@@ -606,8 +612,8 @@ class Context:
         divides the logits alone.  With ``grad`` (the gradient of each row's
         loss: a number or f32 [rows], 1 / rows for a mean) the same call gives
         the gradient of the logits in their type, for ``logits.backward``;
-        ``out`` may be the logits themselves.  One entry a row is cross
-        entropy.  Asynchronous on the current stream."""
+        ``out`` may be the logits themselves, as in ``head_logprobs_backward``.
+        One entry a row is cross entropy.  Asynchronous on the current stream."""
         dev = self.device
         logits, stride, rows, n_tok, dtype = _head_rows(logits, "logits", dev)
         top_ids = _head_table(top_ids, "top_ids", dev, (torch.int32,), rows)
@@ -634,6 +640,8 @@ class Context:
                                        loss.data_ptr(), g, g_ptr, o_ptr, o_stride)
             if rc:
                 _capi.check(self._h, rc)
+        if o_ptr == logits.data_ptr():
+            _overwritten(out)
         return loss, out
 
     def head_check(self) -> None:
