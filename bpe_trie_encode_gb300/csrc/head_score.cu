@@ -4,14 +4,15 @@
 // With z = (v - m) c: log s - sum(exp(z) z) / s is the entropy, so that one pass
 // with two sums gives all but the alternatives; those come from the largest logit
 // of each thread's tiles, noted on the way, and a second look at the few tiles that
-// reach a bound.  Bound by HBM where there are many rows (8,192 x 32,256 bf16: 83 us,
-// 94% of the copy rate; with 20 alternatives 102), by the latency of the steps after
-// a row's last logit where there are few (256 x 65,536 bf16: 6.7 us without
-// alternatives, 11.3 with 20; 1 x 32,256 bf16: 3.5 and 5.9).
+// reach a bound.  Bound by HBM where there are many rows (8,192 x 32,256 bf16: 81 us,
+// 97% of the copy rate; with 20 alternatives 98), by the latency of the steps after
+// a row's last logit where there are few (256 x 65,536 bf16: 7.0 us without
+// alternatives, 11.6 with 20; 1 x 32,256 bf16: 4.0 and 6.4; by graphs of calls on end).
 //
 // The gradient needs no sums: with the norm of the forward pass every logit's is an
 // exponential and a product (with the entropy's, a fused step more).  8,192 x 32,156
-// bf16: 157 us, 6.7 TB/s of reading and writing, 99% of the copy rate.
+// bf16: 157 us, 6.7 TB/s of reading and writing, 99% of the copy rate; 8,192 x 32,256
+// 154 us, with the entropy's too.
 #include "head_row.cuh"
 
 namespace bpe {
@@ -53,9 +54,11 @@ constexpr uint32_t kScoreBytes = ScoreShared<kLanes>::kFeedBytes + (uint32_t)(kT
 __device__ __forceinline__ u64 entry_of(uint32_t key, uint32_t id) { return (u64)key << 32 | (uint32_t)~id; }
 
 // The alternatives in `list`, at most k of this CTA's, for any logits: the key of the k-th largest is found by bits, two
-// a pass; those above it are listed, and as many of its equals, in order of ids, as there is room for.  `have` >= 0: the lists
+// a pass (of bf16 8 passes, f16 10, f32 16, and three more reads of the row: 256 x 32,256, all equal, 20 alternatives, 93 / 109 /
+// 168 us); those above it are listed, and as many of its equals, in order of ids, as there is room for.  `have` >= 0: the lists
 // hold all logits above kLow, so many, and fewer than k; then there may be no more, or those that a mask has set to one value,
-// the largest of the others (256 x 32,256 bf16 with 5 others, 20 alternatives: 78 us by bits).  Gives the team's turn.
+// the largest of the others (256 x 32,256 bf16 with 5 others, 20 alternatives: 93 us by bits, 20 so; masks above kLow, -1e4 and
+// -1e9, go by bits).  Gives the team's turn.
 template <typename T, int kLanes, bool kTeam>
 __device__ __noinline__ int list_any(ScoreShared<kLanes> &S, u64 *list, Team<kLanes, kTeam> team, RowView<T> row, uint32_t lo, uint32_t hi,
                                      uint32_t k, float have) {
@@ -227,8 +230,11 @@ __device__ __forceinline__ uint32_t rank_list(const Team<kLanes, kTeam> &team, c
 // While a row goes by, every thread notes the largest logit of each of its tiles (or of up to kGroups groups of them).  Then
 // comes a bound from below on the k-th largest logit of the CTA's share: with the j-th largest of each warp's 32 largest logits
 // in S.bound, and w j >= k of them, the least of w warps' bounds has k logits at or above it.  The groups that reach it, some
-// 1.5 k, are read once more, and what reaches it of them is ranked.  (Listing on the way, with a bound that rises, cost 80 to
-// 280 instructions a tile of 193: 256 x 65,536 bf16, 20 alternatives, 13.7 us.)
+// 1.5 k where likely tokens lie anywhere in the row, are read once more, and what reaches it of them is ranked.  Where all lie
+// near each other at its start the warp that has none of them sets the bound, and more reach it (256 x 65,536 bf16, 20
+// alternatives, logits of -log(1 + id) and normal noise of 1 / 0.7 / 0.3: 14.7 / 15.7 / 151 us, the last by bits, where those
+// spread take 12.5).  (Listing on the way, with a bound that rises, cost 80 to 280 instructions a tile of 193: 256 x 65,536
+// bf16, 20 alternatives, 13.7 us.)
 template <int kLanes> struct Bound {
     uint32_t warps, j;                     // 0 warps: the share is too short for one
 
@@ -589,6 +595,10 @@ template <typename T> int launch_logprobs(bpe_ctx *ctx, const ScoreParams &P, ui
     }
 }
 
+// A CTA takes up to eight tiles of a row, as long as 16 CTAs an SM are left: what a row costs once is shared by its tiles, and many
+// CTAs leave a short last wave.  (Us where 1 / 4 / 16 / 64 are to be left, and with one tile each: 8,192 x 32,156 bf16 155 / 155 / 155 / 154 /
+// 165; 8,192 x 4,352 22.9 / 22.7 / 25.9 / 29.0 / 29.2; 500 x 65,536 20.5 / 19.9 / 22.6 / 22.5 / 22.5; 300 x 32,256 5.7 / 7.0 /
+// 6.7 / 6.7 / 6.8; 1,024 x 250,000 f16 153 / 153 / 153 / 148 / 147.)
 template <typename T, int kLanes> int launch_backward(bpe_ctx *ctx, const ScoreGradParams &P, uint32_t n_rows) {
     using F = Feed<T, kSize, kLanes>;
     constexpr uint32_t kRows = 256 / kLanes, kVec = RowView<T>::kVec;
@@ -604,6 +614,9 @@ template <typename T, int kLanes> int launch_backward(bpe_ctx *ctx, const ScoreG
     BPE_CUDA(ctx, cudaGetLastError(), "head_logprobs_backward launch");
     return BPE_OK;
 }
+// A warp a row where rows are many and no more than five of a warp's tiles; a CTA's tile is 16 KB, of which a short row leaves
+// most threads idle, and few rows leave SMs idle if they are warps.  (Us by warps / CTAs, bf16: 64 x 1,000 2.9 / 2.4, 512 x 1,000
+// 3.1 / 3.4, 4,096 x 1,000 4.7 / 12.4, 4,096 x 5,000 13.1 / 17.0, 256 x 5,000 3.1 / 3.1, 4,096 x 8,000 25.4 / 25.2.)
 template <typename T> int launch_backward(bpe_ctx *ctx, const ScoreGradParams &P, uint32_t n_rows) {
     return n_rows >= 256 && P.row.n_tok * sizeof(T) <= 10240 ? launch_backward<T, 32>(ctx, P, n_rows) : launch_backward<T, kMost>(ctx, P, n_rows);
 }
