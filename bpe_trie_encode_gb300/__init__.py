@@ -194,7 +194,7 @@ class Context:
         self.device = torch.device("cuda", torch.cuda.current_device() if device is None
                                    else torch.device(device).index or 0)
         h = ctypes.c_void_p()
-        self._lock = threading.Lock()   # a stream is handed over and used in one turn
+        self._lock = threading.RLock()   # a stream is handed over and used in one turn (a signal handler may call too)
         rc = self.lib.bpe_ctx_create(ctypes.byref(h), self.device.index, ctypes.c_void_p(_raw_stream(self.device.index)))
         if rc != 0:
             raise BpeError(rc, "bpe_ctx_create failed")

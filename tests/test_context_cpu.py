@@ -107,3 +107,26 @@ def test_an_error_leaves_the_context_usable(ctx):
 def test_where_the_stream_is_kept():
     lib = bt._capi.load()
     assert lib.bpe_ctx_stream(None) is None
+
+
+def test_a_call_within_a_call_of_the_same_thread(ctx):
+    """As a signal handler makes one."""
+    def handled(handle, stream):
+        ctx.lib.word.value = stream
+        del ctx.lib.bpe_ctx_set_stream
+        ctx.head_sample(torch.zeros(2, 16), torch.zeros(2))
+        return 0
+
+    ctx.lib.bpe_ctx_set_stream = handled
+    HERE.stream = 8
+    done = []
+
+    def work():
+        HERE.stream = 8
+        ctx.head_logprobs(torch.zeros(2, 16))
+        done.append(ctx.lib.ran)
+
+    t = threading.Thread(target=work, daemon=True)
+    t.start()
+    t.join(10)
+    assert done == [[("head_sample", 8, 8), ("head_logprobs", 8, 8)]]
